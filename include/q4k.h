@@ -364,6 +364,173 @@ q4k_status q4k_gemv_grouped(const q4k_gemv_group *groups, int ngroups, const flo
  */
 q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Rotary positions, the paged cache and attention over it: what stands between
+ * a layer's q/k/v products and its output product.
+ * ---------------------------------------------------------------------------
+ * Tokens are rows of a [tokens][heads][dim] tensor of type Q4K_F32, Q4K_F16 or
+ * Q4K_BF16; token and head strides are free (in elements), dim is contiguous.
+ *
+ * A paged cache holds keys and values in pages of page_size slots each, element
+ * (page, slot, head, d) at page*page_stride + slot*slot_stride + head*head_stride
+ * + d, for the keys and for the values with strides of their own: page-by-page
+ * [slot][head] and [head][slot] orders and keys and values in one buffer are all
+ * strides.  Cached position j of sequence b is slot j % page_size of page
+ * page_table[b*page_table_stride + j / page_size].  Sequence b of `batch` owns
+ * the token rows seq_start[b] .. seq_start[b+1]-1 of the call (none is fine) and
+ * kv_len[b] cached positions, these new tokens included: its token i is at
+ * position kv_len[b] - (seq_start[b+1] - seq_start[b]) + i.
+ *
+ * page_table, seq_start, kv_len and the other index arrays are device memory and
+ * are read only by the kernels, so a call needs no host copy of them and can be
+ * captured in a graph.  The kernels check them: a position, page, row range or
+ * length outside the buffers is not followed (nothing is read or written through
+ * it), sets bit 2 of q4k_device_error_flags(), and leaves the outputs that
+ * depend on it invalid.  Token rows that belong to no sequence are left as they
+ * are.
+ */
+#define Q4K_F32 0
+#define Q4K_F16 1
+#define Q4K_BF16 2
+
+/* Frequency scaling of q4k_rope_table. */
+#define Q4K_ROPE_PLAIN 0  /* f_i = base^(-2i/rot)                                        */
+#define Q4K_ROPE_LINEAR 1 /* f_i / factor (positions interpolated)                       */
+#define Q4K_ROPE_BASE 2   /* base * factor^(rot/(rot-2)) in place of base                */
+#define Q4K_ROPE_RAMP 3   /* f_i / factor for slow pairs, f_i for fast ones, a linear ramp
+                             between the pairs that turn `low` and `high` times over
+                             orig_len positions (Peng et al., YaRN, 2023)               */
+#define Q4K_ROPE_BANDS 4  /* by wavelength w_i = 2 pi / f_i: f_i where w_i < orig_len/high,
+                             f_i / factor where w_i > orig_len/low, between them
+                             (1-s) f_i / factor + s f_i, s = (orig_len/w_i - low)/(high - low) */
+
+typedef struct {
+    double base;      /* > 0, usually 10000 or more */
+    double factor;    /* > 0; 1 leaves the frequencies as they are */
+    double orig_len;  /* RAMP and BANDS: the context length the model was trained on */
+    double low, high; /* RAMP: turns (usually 1 and 32); BANDS: usually 1 and 4; high > low > 0 */
+    double magnitude; /* factor on every cosine and sine (RAMP models use 0.1 ln(factor) + 1), usually 1 */
+    int32_t scaling;  /* Q4K_ROPE_* */
+    int32_t reserved;
+} q4k_rope_scaling;
+
+/*
+ * table[p][i] = magnitude * cos(p f_i), table[p][rot/2 + i] = magnitude * sin(p f_i)
+ * for p < rows, i < rot/2: fp32 [rows][rot], angles and functions formed in fp64
+ * (an fp32 angle would be off by 2^-24 p).  Made once, kept by the caller.
+ * rows >= 0 (0: no-op), rot even, 2 <= rot <= 512.  Errors: INVALID_ARG,
+ * UNSUPPORTED_DEVICE, CUDA.
+ */
+q4k_status q4k_rope_table(float *table, int64_t rows, int64_t rot, const q4k_rope_scaling *s, void *stream);
+
+/*
+ * y = x with each head turned by its token's table row: for i < rot/2 the pair
+ * (a, b) = (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) with `interleaved`, becomes
+ * (a c - b s, a s + b c); elements rot .. dim-1 are copied.  Arithmetic in fp32,
+ * one rounding to y's type.  Token t uses row pos[t].  y may be x itself (same
+ * type and strides); they must not overlap otherwise.
+ *   tokens >= 0 (0: no-op), heads >= 1, dim >= 1, rot even, 0 <= rot <= dim and
+ *   <= 512 (rot = 0 copies; pos and table may then be NULL); any alignment of
+ *   the element type (16-byte aligned rows take wide loads).
+ * Errors: INVALID_ARG, MISALIGNED (a pointer not aligned to its element),
+ * UNSUPPORTED_DEVICE, CUDA.
+ */
+typedef struct {
+    const void *x;
+    void *y;
+    const int32_t *pos; /* [tokens] */
+    const float *table; /* [table_rows][rot] */
+    int64_t tokens, heads, dim, rot, table_rows;
+    int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+    int32_t x_type, y_type, interleaved, reserved;
+} q4k_rope_args;
+
+q4k_status q4k_rope(const q4k_rope_args *a, void *stream);
+
+typedef struct {
+    void *k, *v;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    int64_t pages, page_size, heads, dim;
+    const int32_t *page_table; /* [batch][page_table_stride], max_pages of each row used */
+    int64_t page_table_stride, max_pages;
+    const int32_t *seq_start; /* [batch + 1] */
+    const int32_t *kv_len;    /* [batch] */
+    int64_t batch, tokens;
+    int32_t type;             /* Q4K_F16 or Q4K_BF16 */
+    int32_t reserved;
+} q4k_paged_cache;
+
+/*
+ * Stores the new tokens' keys and values in the cache, the keys turned as
+ * q4k_rope turns them (row pos[t], or the token's cache position where pos is
+ * NULL), and turns the queries into q_out in the same launch where q is given.
+ * Rounding: fp32 arithmetic, then once to the cache's (q_out's) type.
+ *   k, v [tokens][cache heads][dim] of type kv_type; q, q_out
+ *   [tokens][q_heads][dim] (NULL: none); rot = 0: nothing is turned (table NULL).
+ *   The slots written must be distinct over the call; q_out may be q itself.
+ * Only the new tokens' slots of the cache are written.
+ * Errors: as q4k_rope.
+ */
+typedef struct {
+    const void *k, *v, *q;
+    void *q_out;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    const int32_t *pos;
+    const float *table;
+    int64_t table_rows, rot, q_heads;
+    int32_t kv_type, q_type, q_out_type, interleaved;
+} q4k_append_args;
+
+q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, void *stream);
+
+/*
+ * Attention of the new tokens (one or many per sequence) over the paged cache.
+ * Query head h reads cache head h / (q_heads / cache heads).  Token t at
+ * position p of sequence b sees the positions lo <= j < hi with
+ *   hi = kv_len[b] without `causal`, else min(kv_len[b], max(p + 1, prefix_len[b])),
+ *   lo = max(0, kv_start[t], p + 1 - window)
+ * (prefix_len, kv_start NULL and window 0: not applied) and gets
+ *   s_j = scale q.k_j,  s_j = softcap tanh(s_j / softcap) (softcap > 0),
+ *   s_j = s_j - slopes[h] |p - j| (slopes not NULL),
+ *   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + ln sum_j exp(s_j - m).
+ * A row that sees nothing, or only scores of -inf, gives out = 0, lse = -inf.
+ * Slots that no token of a sequence's query tile sees may hold anything,
+ * infinities and NaN included; an infinite or NaN value that some token sees may
+ * also reach nearby tokens that do not see it (an infinite one as NaN).
+ *
+ * Precision: softmax statistics, sums and outputs accumulate in fp32.  With q of
+ * the cache's type and a 16-bit out, the weights exp(s_j - m) are rounded once to
+ * the cache's type before they meet the values on the tensor cores (each by
+ * at most 2^-8 of itself in bf16, 2^-11 in fp16, beside the output's own rounding).  With fp32 q or out, q and the weights enter as 2 (fp16) or 3
+ * (bf16) parts, 22 and 24 bits.
+ *
+ *   q, out [tokens][q_heads][dim]: any type each; lse fp32 [tokens][q_heads] or NULL
+ *   q_heads a positive multiple of the cache's heads, dim a multiple of 8,
+ *   8 <= dim <= 256; 16-byte aligned k, v, q, out and strides that keep every
+ *   row 16-byte aligned; tokens * q_heads < 2^31.
+ *   causal 0 or 1; window >= 0; softcap >= 0 and finite.
+ * Scratch comes from cudaMallocAsync on `stream` and is freed on it.  Partial
+ * results of split rows are added in a fixed order: the same inputs give the same
+ * bits.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
+ */
+typedef struct {
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    int64_t q_heads, window;
+    const float *slopes;       /* [q_heads] or NULL */
+    const int32_t *prefix_len; /* [batch] or NULL */
+    const int32_t *kv_start;   /* [tokens] or NULL */
+    float scale, softcap;
+    int32_t q_type, out_type, causal, reserved;
+} q4k_attention_args;
+
+q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
+
 /* Launch plan the automatic heuristics pick for a shape (for tests and
  * reports): out[0] = split_k, out[1] = number of CTAs, out[2] = rows per CTA
  * tile, out[3] = K blocks per x chunk held in shared memory. */
@@ -372,7 +539,9 @@ q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4]);
 /* Sticky device-side error bits of the library's kernels, read synchronously
  * from the current device: bit 0 = a bounded wait inside a GEMV/argmax
  * kernel (Q4_K or Q6_K) or the streaming probe timed out, bit 1 = the same in the prefill
- * kernel; the kernel then wound down early and its outputs are invalid.
+ * kernel; the kernel then wound down early and its outputs are invalid;
+ * bit 2 = an index array of q4k_rope, q4k_kv_append or q4k_paged_attention
+ * points outside its buffers; bit 3 = a bounded wait in q4k_paged_attention.
  * 0 = no error.  The bits stay set until q4k_device_error_clear(). */
 unsigned int q4k_device_error_flags(void);
 

@@ -48,7 +48,8 @@ EXPORTS = ("q4k_status_string", "q4k_abi_version", "q4k_gemv", "q4k_gemv_argmax"
            "q4k_gemv_argmax_noalloc", "q4k_gemm_prefill", "q4k_gemm_prefill_exact", "q4k_gemv_ex",
            "q4k_gemv_grouped", "q4k_gemv_plan",
            "q4k_device_error_flags", "q4k_device_error_clear", "q4k_stream_read", "q6k_gemv",
-           "q6k_planar_bytes", "q6k_repack_planar", "q6k_gemv_planar")
+           "q6k_planar_bytes", "q6k_repack_planar", "q6k_gemv_planar",
+           "q4k_rope_table", "q4k_rope", "q4k_kv_append", "q4k_paged_attention")
 
 
 def lib():
@@ -94,6 +95,13 @@ def lib():
         L.q4k_device_error_clear.restype = I
         L.q4k_stream_read.argtypes = [P, I64, ctypes.POINTER(ctypes.c_int64), P]
         L.q4k_stream_read.restype = I
+        # the structures of these four are passed as packed bytes
+        L.q4k_rope_table.argtypes = [P, I64, I64, ctypes.c_char_p, P]
+        L.q4k_rope.argtypes = [ctypes.c_char_p, P]
+        L.q4k_kv_append.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
+        L.q4k_paged_attention.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
+        for f in (L.q4k_rope_table, L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention):
+            f.restype = I
         _lib = L
         return L
 
@@ -316,6 +324,15 @@ def stream_read(buf, *, stream=None) -> int:
     _check("q4k_stream_read", lib().q4k_stream_read(buf.data_ptr(), buf.numel() * buf.element_size(), ctypes.byref(n),
                                                     _stream_ptr(stream)))
     return int(n.value)
+
+
+def __getattr__(name):
+    # The attention module needs torch at import; the rest of the binding does not.
+    if name in ("rope_table", "rope", "kv_append", "paged_attention"):
+        from . import _attention
+        globals()[name] = f = getattr(_attention, name)
+        return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def device_error_flags() -> int:

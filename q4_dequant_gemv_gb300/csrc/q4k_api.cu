@@ -90,23 +90,41 @@ q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, 
     return q4k::stream_read_impl(buf, bytes, bytes_read, stream);
 }
 
+q4k_status q4k_rope_table(float *table, int64_t rows, int64_t rot, const q4k_rope_scaling *s, void *stream)
+{
+    return q4k::rope_table_impl(table, rows, rot, s, stream);
+}
+
+q4k_status q4k_rope(const q4k_rope_args *a, void *stream) { return q4k::rope_impl(a, stream); }
+
+q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, void *stream)
+{
+    return q4k::kv_append_impl(c, a, stream);
+}
+
+q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)
+{
+    return q4k::paged_attention_impl(c, a, stream);
+}
+
 q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4])
 {
     return q4k::gemv_plan_impl(N, K, batch, out);
 }
 
-/* Sticky device-side error bits (bit 0: a bounded wait inside a kernel timed
- * out and the kernel wound down early).  Synchronous; 0 means no error. */
+/* Sticky device-side error bits (what each means: q4k.h).  Synchronous; 0 means
+ * no error. */
 unsigned int q4k_device_error_flags(void)
 {
     return q4k::read_device_error() | q4k::read_prefill_error() | q4k::read_q6k_error() | q4k::read_q6p_error() |
-           q4k::read_probe_error();
+           q4k::read_probe_error() | q4k::read_rope_error() | q4k::read_attn_error();
 }
 
 q4k_status q4k_device_error_clear(void)
 {
     const bool ok = q4k::clear_device_error() & q4k::clear_prefill_error() & q4k::clear_q6k_error() &
-                    q4k::clear_q6p_error() & q4k::clear_probe_error();
+                    q4k::clear_q6p_error() & q4k::clear_probe_error() & q4k::clear_rope_error() &
+                    q4k::clear_attn_error();
     return ok ? Q4K_OK : Q4K_ERR_CUDA;
 }
 

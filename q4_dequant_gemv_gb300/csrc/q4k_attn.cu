@@ -1,0 +1,96 @@
+// q4k_attn.cu -- q4k_paged_attention: argument checks and the choice of kernel.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/q4k.h"
+#include "q4k_attn_rows.cuh"
+#include "q4k_internal.h"
+
+namespace q4k {
+
+__device__ unsigned int g_attn_error = 0;   // bit 2: an index outside its buffer, bit 3: a bounded wait timed out
+
+unsigned int read_attn_error()
+{
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+    return v;
+}
+
+bool clear_attn_error()
+{
+    const unsigned int z = 0;
+    return cudaMemcpyToSymbol(g_attn_error, &z, sizeof(z)) == cudaSuccess;
+}
+
+// Device address of the error word on the current device (looked up once per device).
+static unsigned int *error_word()
+{
+    constexpr int kDevices = 64;
+    static unsigned int *at[kDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return nullptr;
+    unsigned int *p = __atomic_load_n(&at[dev], __ATOMIC_ACQUIRE);
+    if (p) return p;
+    void *v = nullptr;
+    if (cudaGetSymbolAddress(&v, g_attn_error) != cudaSuccess) return nullptr;
+    __atomic_store_n(&at[dev], static_cast<unsigned int *>(v), __ATOMIC_RELEASE);
+    return static_cast<unsigned int *>(v);
+}
+
+q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)
+{
+    q4k_status st = check_cache(c);
+    if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
+    auto type_ok = [](int t) { return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16; };
+    if (c->dim % 8 || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
+        !type_ok(a->q_type) || !type_ok(a->out_type) || (a->causal & ~1) || a->window < 0 ||
+        !std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.0f ||
+        c->tokens * a->q_heads > 0x7FFFFFFF)
+        return Q4K_ERR_INVALID_ARG;
+    const bool some = c->tokens > 0 && c->batch > 0;
+    if (some && (!a->q || !a->out)) return Q4K_ERR_INVALID_ARG;
+    if (st != Q4K_OK) return st;
+    auto off16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; };
+    auto off4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+    const int64_t qn = a->q_type == Q4K_F32 ? 4 : 8, on = a->out_type == Q4K_F32 ? 4 : 8;
+    if (off16(c->k) || off16(c->v) || off16(a->q) || off16(a->out) || off4(a->lse) || off4(a->slopes) ||
+        off4(a->prefix_len) || off4(a->kv_start) || c->k_page_stride % 8 || c->k_slot_stride % 8 ||
+        c->k_head_stride % 8 || c->v_page_stride % 8 || c->v_slot_stride % 8 || c->v_head_stride % 8 ||
+        a->q_token_stride % qn || a->q_head_stride % qn || a->out_token_stride % on || a->out_head_stride % on)
+        return Q4K_ERR_MISALIGNED;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != Q4K_OK || !some) return st;
+
+    attn::RowsLaunch l{};
+    attn::Args &p = l.args;
+    p.q = a->q, p.k = c->k, p.v = c->v, p.out = a->out, p.lse = a->lse;
+    p.q_token = a->q_token_stride, p.q_head = a->q_head_stride;
+    p.out_token = a->out_token_stride, p.out_head = a->out_head_stride;
+    p.k_page = c->k_page_stride, p.k_slot = c->k_slot_stride, p.k_head = c->k_head_stride;
+    p.v_page = c->v_page_stride, p.v_slot = c->v_slot_stride, p.v_head = c->v_head_stride;
+    p.table_stride = c->page_table_stride, p.page_size = c->page_size;
+    p.page_table = c->page_table, p.seq_start = c->seq_start, p.kv_len = c->kv_len;
+    p.prefix_len = a->prefix_len, p.kv_start = a->kv_start, p.slopes = a->slopes;
+    // positions are 32-bit in the kernels, with room for the last unit's end
+    const int64_t most = 0x7FFFFFFF - 4096;
+    const int64_t per = c->pages > 0 ? c->max_pages : 0;
+    p.capacity = per > most / c->page_size ? most : per * c->page_size;
+    p.window = a->window, p.scale = a->scale, p.softcap = a->softcap;
+    p.pages = static_cast<int>(c->pages), p.batch = static_cast<int>(c->batch);
+    p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
+    p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
+    p.dim = static_cast<int>(c->dim), p.q_type = a->q_type, p.out_type = a->out_type, p.causal = a->causal;
+    p.error = error_word();
+    if (!p.error) return Q4K_ERR_CUDA;
+    l.sms = sms;
+    l.stream = static_cast<cudaStream_t>(stream);
+    l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
+    const cudaError_t e = c->type == Q4K_F16 ? attn::launch_rows_f16(l) : attn::launch_rows_bf16(l);
+    return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+}
+
+}  // namespace q4k

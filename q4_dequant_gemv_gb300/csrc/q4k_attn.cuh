@@ -1,0 +1,262 @@
+// q4k_attn.cuh -- what the attention kernels share: the arguments, the split of
+// a call's work over the CTAs, and the join of split rows.
+//
+// A sequence's query rows for one cache head are its (token, head of the group)
+// pairs, row r = token r / G, head r % G of the group (G = query heads per cache
+// head).  A tile is R consecutive rows of one sequence and one cache head; its
+// work is counted in units of U keys over the keys that any of its rows sees.
+// Lengths live on the device, so every CTA works the split out by itself: it
+// sums the units of all tiles (a prefix over the call, identical in every CTA)
+// and takes an equal, contiguous share of them, wherever that begins or ends
+// inside a tile.  The load is therefore even for ragged lengths, causal tiles
+// and one long sequence alike, with no host knowledge of lengths.  Rows of a
+// tile that several CTAs hold meet in scratch memory: the last of them to
+// arrive (one atomic ticket per split tile) adds the partial results in the
+// order of the keys, so the same inputs give the same bits.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "../../include/q4k.h"
+
+namespace q4k {
+namespace attn {
+
+// Packed pairs of a 16-bit type (Q4K_F16 or Q4K_BF16), low half first.
+__device__ __forceinline__ float2 unpack2(uint32_t v, int type)
+{
+    if (type == Q4K_F16) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&v);
+        return __half22float2(h);
+    }
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type)
+{
+    uint32_t r;
+    if (type == Q4K_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+struct Args {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    int64_t q_token, q_head, out_token, out_head;        // strides in elements
+    int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+    int64_t table_stride, page_size;
+    const int32_t *page_table, *seq_start, *kv_len, *prefix_len, *kv_start;
+    const float *slopes;
+    int64_t capacity;      // cached positions a page table row can hold
+    int64_t window;        // 0: none
+    float scale, softcap;
+    int pages, batch, tokens, heads, kv_heads, group, dim;
+    int q_type, out_type, causal;
+    int slots;             // upper bound of the tiles per cache head
+    float *part;           // partial results: two slots per CTA
+    unsigned int *ticket;  // one per CTA, zero at launch
+    unsigned int *error;   // the sticky error word
+};
+
+// One tile: the rows, their token range and the keys that any of them sees.
+struct Tile {
+    int seq, first, rows;      // first row in the sequence, number of rows (0: nothing to do)
+    int tok0, ntok;            // first token row of the sequence in the call, its tokens
+    int64_t pos0;              // position of the sequence's first new token
+    int len;                   // cached positions (clamped to the page table)
+    int from, hi;              // keys [from, hi) that some row sees
+    int lo;                    // `from` rounded down to a multiple of 16: where unit 0 starts
+    int units;
+};
+
+struct Range {
+    int64_t lo, hi;
+};
+
+// Keys that the new token i of the tile's sequence sees.
+__device__ __forceinline__ Range token_range(const Args &a, int seq, int64_t pos, int tok, int len)
+{
+    Range r{0, len};
+    if (a.causal) {
+        int64_t h = pos + 1;
+        if (a.prefix_len) h = max(h, static_cast<int64_t>(a.prefix_len[seq]));
+        r.hi = min(h, static_cast<int64_t>(len));
+    }
+    if (a.window) r.lo = max(r.lo, pos + 1 - a.window);
+    if (a.kv_start) r.lo = max(r.lo, static_cast<int64_t>(a.kv_start[tok]));
+    r.hi = max(r.hi, static_cast<int64_t>(0));
+    r.lo = min(r.lo, r.hi);
+    return r;
+}
+
+// The split of the call's work, one copy per CTA in shared memory.
+template <int R, int U, int THREADS>
+struct Split {
+    static constexpr int kStripes = 1024;     // prefix entries; each covers `stripe` tile slots
+    static constexpr int kSeqs = 1024;        // sequence starts held in shared memory
+    struct Shared {
+        uint32_t prefix[kStripes];
+        int start[kSeqs + 1];
+        uint32_t warp[THREADS / 32];
+    };
+
+    const Args &a;
+    Shared &sh;
+    int stripe;
+    uint32_t per_head;      // units of one cache head
+
+    __device__ __forceinline__ int start_of(int b) const
+    {
+        const int s = a.batch <= kSeqs ? sh.start[b] : a.seq_start[b];
+        return min(max(s, 0), a.tokens);
+    }
+    // First tile slot of sequence b: no smaller than the tiles before it need.
+    __device__ __forceinline__ int slot_of(int b) const
+    {
+        return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / R) + b;
+    }
+
+    __device__ __forceinline__ Tile tile(int slot, bool report) const
+    {
+        Tile t{};
+        int b = 0, e = a.batch - 1;
+        while (b < e) {   // the last sequence whose first slot is <= slot
+            const int m = (b + e + 1) >> 1;
+            if (slot_of(m) <= slot) b = m; else e = m - 1;
+        }
+        const int s0 = start_of(b), n = start_of(b + 1) - s0;
+        const int raw = a.kv_len[b];
+        t.seq = b, t.tok0 = s0, t.ntok = n;
+        t.first = (slot - slot_of(b)) * R;
+        if (n <= 0 || t.first < 0 || t.first >= n * a.group) return t;
+        t.rows = min(R, n * a.group - t.first);
+        t.len = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), a.capacity));
+        if (report && (raw < 0 || raw > a.capacity)) atomicOr(a.error, 4u);
+        t.pos0 = static_cast<int64_t>(raw) - n;
+        const int i0 = t.first / a.group, i1 = (t.first + t.rows - 1) / a.group;
+        const Range last = token_range(a, b, t.pos0 + i1, s0 + i1, t.len);
+        int64_t lo = last.hi;
+        if (a.kv_start) {
+            for (int i = i0; i <= i1; ++i) {
+                const Range r = token_range(a, b, t.pos0 + i, s0 + i, t.len);
+                if (r.hi > r.lo) lo = min(lo, r.lo);
+            }
+        } else {
+            lo = min(lo, token_range(a, b, t.pos0 + i0, s0 + i0, t.len).lo);
+        }
+        t.hi = static_cast<int>(last.hi);
+        t.from = static_cast<int>(lo);
+        t.lo = t.from & ~15;
+        t.units = t.hi > t.lo ? (t.hi - t.lo + U - 1) / U : 1;   // a tile that sees nothing still writes its zeros
+        return t;
+    }
+
+    // All threads of the CTA.
+    __device__ __forceinline__ Split(const Args &args, Shared &shared) : a(args), sh(shared)
+    {
+        const int tid = threadIdx.x;
+        for (int i = tid; i <= a.batch; i += THREADS) {
+            const int s = a.seq_start[i];
+            if (s < 0 || s > a.tokens || (i > 0 && s < a.seq_start[i - 1])) atomicOr(a.error, 4u);
+            if (a.batch <= kSeqs) sh.start[i] = s;
+        }
+        __syncthreads();
+        stripe = (a.slots + kStripes - 1) / kStripes;
+        constexpr int PER = kStripes / THREADS;   // consecutive prefix entries of a thread
+        static_assert(PER * THREADS == kStripes, "whole entries per thread");
+        uint32_t sum[PER], run = 0;
+        const int e0 = tid * PER;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            for (int s = (e0 + j) * stripe; s < min((e0 + j + 1) * stripe, a.slots); ++s) run += tile(s, false).units;
+            sum[j] = run;
+        }
+        uint32_t incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((tid & 31) >= o) incl += v;
+        }
+        if ((tid & 31) == 31) sh.warp[tid >> 5] = incl;
+        __syncthreads();
+        uint32_t before = 0, total = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < (tid >> 5)) before += sh.warp[w];
+            total += sh.warp[w];
+        }
+        before += incl - run;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sh.prefix[e0 + j] = before + sum[j];
+        per_head = total;
+        __syncthreads();
+    }
+
+    // The tile that holds unit r (< per_head) of a cache head, and r's place in it.
+    __device__ __forceinline__ Tile locate(uint32_t r, int &offset) const
+    {
+        int lo = 0, hi = kStripes - 1;
+        while (lo < hi) {
+            const int m = (lo + hi) >> 1;
+            if (sh.prefix[m] > r) hi = m; else lo = m + 1;
+        }
+        uint32_t at = lo ? sh.prefix[lo - 1] : 0;
+        for (int s = lo * stripe;; ++s) {
+            const Tile t = tile(s, true);
+            if (at + t.units > r || s + 1 >= a.slots) {
+                offset = static_cast<int>(r - at);
+                return t;
+            }
+            at += t.units;
+        }
+    }
+};
+
+// A CTA's share [begin, end) of `total` units over n CTAs, and the CTA that
+// holds a unit.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int share_owner(int64_t total, int n, int64_t unit)
+{
+    return static_cast<int>(((unit + 1) * n - 1) / total);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Weight of a partial result with maximum m in a sum with maximum mx.  One that
+// saw nothing (m = -inf) holds zeros, or a NaN to pass on (fmaxf drops NaN from
+// the maxima, the sums carry it).
+__device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 1.0f : ex2(m - mx); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Four consecutive outputs of a row.
+__device__ __forceinline__ void store4(void *out, int type, int64_t i, float4 v)
+{
+    if (type == Q4K_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + i) = v;
+    } else {
+        uint2 w;
+        w.x = pack2(v.x, v.y, type);
+        w.y = pack2(v.z, v.w, type);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + i) = w;
+    }
+}
+
+}  // namespace attn
+}  // namespace q4k

@@ -28,6 +28,16 @@ q4k_status q6k_gemv_planar_impl(const void *Wp, const float *x, float *y, int64_
                                 void *stream);
 q4k_status prefill_impl(const void *W, const void *X, float *Y, int64_t N, int64_t K, int64_t T, void *stream,
                         bool exact);
+q4k_status rope_table_impl(float *table, int64_t rows, int64_t rot, const q4k_rope_scaling *s, void *stream);
+q4k_status rope_impl(const q4k_rope_args *a, void *stream);
+q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, void *stream);
+q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
+// Sizes, types and index pointers of a cache (no device call).
+q4k_status check_cache(const q4k_paged_cache *c);
+unsigned int read_rope_error();
+unsigned int read_attn_error();
+bool clear_rope_error();
+bool clear_attn_error();
 unsigned int read_device_error();
 unsigned int read_prefill_error();
 unsigned int read_q6k_error();
