@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "../../include/q4k.h"
+#include "q4k_attn_chunk.cuh"
 #include "q4k_attn_rows.cuh"
 #include "q4k_internal.h"
 
@@ -89,7 +90,20 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     l.sms = sms;
     l.stream = static_cast<cudaStream_t>(stream);
     l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
-    const cudaError_t e = c->type == Q4K_F16 ? attn::launch_rows_f16(l) : attn::launch_rows_bf16(l);
+    // The tcgen05 kernel takes calls with more query rows per sequence and cache
+    // head than the mma.sync kernel holds at once (16), in one 16-bit type, over
+    // pages that split into boxes of 16 slots or more.
+    auto stride_ok = [](int64_t s) { return s > 0 && s < (int64_t{1} << 39); };
+    const bool boxes = c->page_size % 16 == 0 && stride_ok(c->k_slot_stride) && stride_ok(c->v_slot_stride) &&
+                       (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
+                       (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
+    cudaError_t e;
+    if (!l.parts_many && c->dim <= 128 && boxes && p.capacity > 0 && c->tokens * p.group > 16 * c->batch) {
+        const attn::ChunkLaunch ch{p, sms, l.stream};
+        e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
+    } else {
+        e = c->type == Q4K_F16 ? attn::launch_rows_f16(l) : attn::launch_rows_bf16(l);
+    }
     return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 

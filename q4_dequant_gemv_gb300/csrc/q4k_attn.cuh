@@ -69,7 +69,7 @@ struct Tile {
     int64_t pos0;              // position of the sequence's first new token
     int len;                   // cached positions (clamped to the page table)
     int from, hi;              // keys [from, hi) that some row sees
-    int lo;                    // `from` rounded down to a multiple of 16: where unit 0 starts
+    int lo;                    // `from` rounded down to a multiple of ALIGN: where unit 0 starts
     int units;
 };
 
@@ -94,7 +94,8 @@ __device__ __forceinline__ Range token_range(const Args &a, int seq, int64_t pos
 }
 
 // The split of the call's work, one copy per CTA in shared memory.
-template <int R, int U, int THREADS>
+// ALIGN: where units start (a power of two).
+template <int R, int U, int THREADS, int ALIGN>
 struct Split {
     static constexpr int kStripes = 1024;     // prefix entries; each covers `stripe` tile slots
     static constexpr int kSeqs = 1024;        // sequence starts held in shared memory
@@ -150,7 +151,7 @@ struct Split {
         }
         t.hi = static_cast<int>(last.hi);
         t.from = static_cast<int>(lo);
-        t.lo = t.from & ~15;
+        t.lo = t.from & ~(ALIGN - 1);
         t.units = t.hi > t.lo ? (t.hi - t.lo + U - 1) / U : 1;   // a tile that sees nothing still writes its zeros
         return t;
     }
@@ -166,8 +167,7 @@ struct Split {
         }
         __syncthreads();
         stripe = (a.slots + kStripes - 1) / kStripes;
-        constexpr int PER = kStripes / THREADS;   // consecutive prefix entries of a thread
-        static_assert(PER * THREADS == kStripes, "whole entries per thread");
+        constexpr int PER = (kStripes + THREADS - 1) / THREADS;   // consecutive prefix entries of a thread
         uint32_t sum[PER], run = 0;
         const int e0 = tid * PER;
 #pragma unroll
@@ -190,7 +190,8 @@ struct Split {
         }
         before += incl - run;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) sh.prefix[e0 + j] = before + sum[j];
+        for (int j = 0; j < PER; ++j)
+            if (e0 + j < kStripes) sh.prefix[e0 + j] = before + sum[j];
         per_head = total;
         __syncthreads();
     }

@@ -1,0 +1,585 @@
+// q4k_attn_chunk.cuh -- attention of many query rows per cache head (prompt
+// chunks) on the tcgen05 tensor cores, keys and values by TMA from their pages.
+//
+// 4 dim flops per (row, key) against 4 dim bytes per key and 256-row tile: the
+// tensor cores bound it (two 128 x 128 x 128 products a step and half tile, 512
+// cycles each), with one exponential per (row, key) beside them.
+//
+// CTA: one tile of 256 query rows as two halves of 128 (the MMA's M), one CTA
+// per SM, persistent over its share of the call's units (128 keys each).
+//   * warps 0-3 and 4-7: softmax of a half, a thread per row: S from tensor
+//     memory (128 values), mask, maximum, exponentials, P as 16-bit pairs back
+//     into the columns of S; at the end of a tile O out of tensor memory.
+//   * warp 8 issues the MMAs: S = Q K^T (both from shared memory, K-major) and
+//     O += P V (P from tensor memory, V from shared memory as it lies, rows of
+//     keys: MN-major).  The halves alternate, so one half's softmax runs
+//     under the other's products.
+//   * warp 9 loads K and V tiles (128 keys) through a ring of four stages: a
+//     lane per page piece looks the page up and issues its TMA boxes.
+// Tensor memory, all 512 columns: S (and P) of the halves, O of the halves.
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the
+// one in use (exponents relative to an older maximum stay exact in fp32 and
+// within the range of 16 bits), which after the first tiles is rare.  When S of
+// step i is complete, so is the O of step i - 1 (MMAs complete in order), so
+// the rescaling waits for nothing.
+//
+// Slots that nothing of the tile sees may hold NaN: scores are replaced, not
+// added to, and the rows of V outside the tile's keys are zeroed in shared
+// memory before they meet P = 0.  Every wait is bounded in time: on a timeout the
+// CTA sets bit 3 of the error word, stops, waits (bounded) for its copies in
+// flight, frees its tensor memory and returns.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "q4k_attn.cuh"
+#include "ptx.cuh"
+
+namespace q4k {
+namespace attn {
+
+constexpr int kChunkRows = 256;              // query rows of a tile
+constexpr int kChunkKeys = 128;              // keys of a unit
+constexpr int kChunkThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kStages = 4;
+constexpr uint64_t kChunkWaitNs = 2000000000ull;
+
+template <int DP>
+struct ChunkShared {
+    using Plan = Split<kChunkRows, kChunkKeys, kChunkThreads, kChunkKeys>;
+    static constexpr int kHalf = 128 * 128;                    // bytes: 128 rows of 64 elements
+    static constexpr int kTile = kHalf * (DP / 64);            // 128 rows of DP elements
+    uint8_t q[2 * kTile];                                      // two halves of query rows
+    uint8_t kv[kStages * kTile];
+    typename Plan::Shared plan;
+    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2], o_done, q_ready, edge, joined;
+    uint32_t tmem;
+    unsigned int arrived;
+    int abort;
+};
+
+__device__ __forceinline__ void tm_ld32(uint32_t addr, float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *u)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
+        "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
+        "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Issued by one elected lane of a converged warp (the loop's arithmetic stays
+// warp-uniform that way).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle, rows of 128 bytes in atoms
+// of 8 rows (1024 bytes).  K-major: `lead` is not used.  MN-major (V): `lead` is
+// the distance of the next 64 elements of a row, the atoms follow along K.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+// Instruction descriptor, kind::f16, fp32 accumulators, M = 128.
+template <int CT>
+constexpr uint32_t chunk_idesc(int n, bool b_mn_major)
+{
+    return (1u << 4) | (CT == Q4K_BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// The keys of one cache head of a page: box of `rows` slots by 64 elements.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int d, int slot, int head, int page,
+                                         uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+struct ChunkMaps {
+    CUtensorMap k, v;
+};
+
+// MODE bit 0: capped scores, bit 1: distance bias.
+template <int CT, int DP, int MODE>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkMaps maps, const Args a, const int box)
+{
+    using Sh = ChunkShared<DP>;
+    constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
+    // fp16 weights are kept at 2^6 and below 2^14, bf16 has range to spare
+    constexpr float kShift = CT == Q4K_F16 ? 6.0f : 0.0f;
+    constexpr float kLazy = 8.0f;
+    extern __shared__ uint8_t smem_raw[];
+    Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+
+    if (w == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.s_full[i]), 1), mbar_init(smem_u32(&sh.p_ready[i]), 128);
+        mbar_init(smem_u32(&sh.o_done), 1);
+        mbar_init(smem_u32(&sh.q_ready), 256);
+        mbar_init(smem_u32(&sh.edge), 1);
+        mbar_init(smem_u32(&sh.joined), 256);
+        fence_barrier_init();
+        sh.abort = 0;
+    }
+    tm_fence_before();
+    typename Sh::Plan plan(a, sh.plan);   // synchronises the CTA
+    tm_fence_after();
+    const uint32_t tm = sh.tmem;
+
+    // Waits for a phase, whole warps together; false: the CTA winds down.
+    volatile int *abort = &sh.abort;
+    auto wait_lane = [&](uint32_t b, uint32_t parity) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = 1;; ++i) {
+            if (mbar_try_wait_sleep(b, parity, 20000u)) return true;
+            if ((i & 15u) == 0u) {
+                if (*abort) return false;
+                if (globaltimer_ns() - t0 > kChunkWaitNs) {
+                    *abort = 1;
+                    atomicOr(a.error, 8u);
+                    return false;
+                }
+            }
+        }
+    };
+    auto wait = [&](unsigned long long &bar, uint32_t parity) -> bool {
+        const uint32_t b = smem_u32(&bar);
+        const bool done = mbar_try_wait(b, parity) || wait_lane(b, parity);
+        return __all_sync(0xffffffffu, done);
+    };
+
+    const int64_t total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
+    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int cta = blockIdx.x;
+    int64_t u = 0, u_end = 0;
+    if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+
+    if (w == kLoadWarp) {
+        // ------------------------------------------------------------ loads
+        int stage = 0, edges = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        unsigned int pending = 0;   // stages whose copies may still be in flight at a wind-down
+        const int per = kChunkKeys / box;
+        while (u < u_end && ok) {
+            const int head = static_cast<int>(u / plan.per_head);
+            int off;
+            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+            const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
+            const int psize = static_cast<int>(a.page_size);
+            for (int i = 0; i < todo && ok; ++i) {
+                const int kb = t.lo + (off + i) * kChunkKeys;
+                // lane j: piece j of the tile
+                const int key = kb + lane * box;
+                bool live = lane < per && key + box > t.from && key < t.hi;
+                int page = 0, slot = 0;
+                if (live) {
+                    const int e = key / psize;
+                    slot = key - e * psize;
+                    page = pages[e];
+                    if (page < 0 || page >= a.pages) {
+                        atomicOr(a.error, 4u);
+                        live = false;
+                    }
+                }
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * static_cast<uint32_t>(box) * 128u * ND;
+                const bool edge = kb < t.from || kb + kChunkKeys > t.hi;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (round > 0 && !wait(sh.empty[stage], (round - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = sh.kv + stage * kTile;
+                    const bool clean = kv == 1 && edge;
+                    unsigned long long &bar = clean ? sh.edge : sh.full[stage];
+                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes);
+                    __syncwarp();
+                    if (live) {
+#pragma unroll
+                        for (int h = 0; h < ND; ++h)
+                            load_box(smem_u32(dst + h * kHalf + lane * box * 128), kv ? &maps.v : &maps.k, 64 * h, slot,
+                                     head, page, smem_u32(&bar));
+                    }
+                    if (clean) {
+                        // zero the rows that nothing of the tile sees, then hand the stage on
+                        if (!wait(sh.edge, edges & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        ++edges;
+                        const int r0 = max(0, t.from - kb), r1 = min(kChunkKeys, t.hi - kb);
+                        for (int r = 0; r < kChunkKeys; ++r) {
+                            if (r >= r0 && r < r1) continue;
+                            if (lane < 8 * ND)
+                                *reinterpret_cast<uint4 *>(dst + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.full[stage]));
+                    }
+                    pending |= 1u << stage;
+                    if (++stage == kStages) stage = 0, ++round;
+                }
+            }
+            u += todo;
+        }
+        // every copy issued lands before the CTA exits
+        if (!ok) {
+            for (int s = 0; s < kStages; ++s)
+                if (pending >> s & 1) {
+                    const uint32_t r = s < stage ? round : round - 1;
+                    (void)mbar_wait_bounded(smem_u32(&sh.full[s]), r & 1, kChunkWaitNs);
+                }
+        }
+    } else if (w == kMmaWarp) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t id_s = chunk_idesc<CT>(kChunkKeys, false), id_o = chunk_idesc<CT>(DP, true);
+        const uint32_t q0 = smem_u32(sh.q), kv0 = smem_u32(sh.kv);
+        int stage = 0, items = 0;
+        uint32_t round = 0, steps[2] = {0, 0};
+        bool ok = true;
+        auto take = [&](uint32_t &addr) -> bool {   // next stage of the ring
+            if (!wait(sh.full[stage], round & 1)) return false;
+            addr = kv0 + stage * kTile;
+            return true;
+        };
+        auto next = [&]() {
+            mma_commit(smem_u32(&sh.empty[stage]));
+            if (++stage == kStages) stage = 0, ++round;
+        };
+        auto scores = [&](int h, uint32_t k) {
+#pragma unroll
+            for (int j = 0; j < DP / 16; ++j) {
+                const uint32_t o = (j >> 2) * kHalf + (j & 3) * 32;
+                mma_ss(tm + 128 * h, tile_desc(q0 + h * kTile + o, 16), tile_desc(k + o, 16), id_s, j > 0);
+            }
+            mma_commit(smem_u32(&sh.s_full[h]));
+        };
+        auto values = [&](int h, uint32_t v, bool more) {
+#pragma unroll
+            for (int j = 0; j < kChunkKeys / 16; ++j)
+                mma_ts(tm + 256 + 128 * h, tm + 128 * h + 8 * j, tile_desc(v + j * 2048, kHalf), id_o, more || j > 0);
+        };
+        while (u < u_end && ok) {
+            const int head = static_cast<int>(u / plan.per_head);
+            int off;
+            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+            const int halves = t.rows > 128 ? 2 : 1;
+            uint32_t kt = 0, vt = 0;
+            ok = wait(sh.q_ready, items & 1) && take(kt);
+            if (!ok) break;
+            tm_fence_after();
+            for (int h = 0; h < halves; ++h) scores(h, kt);
+            next();
+            for (int i = 0; i < todo && ok; ++i) {
+                ok = take(vt);
+                const int vstage = stage;
+                if (++stage == kStages) stage = 0, ++round;
+                const bool more = i + 1 < todo;
+                for (int h = 0; h < halves && ok; ++h) {
+                    ok = wait(sh.p_ready[h], steps[h] & 1);
+                    if (!ok) break;
+                    ++steps[h];
+                    tm_fence_after();
+                    values(h, vt, i > 0);
+                    if (h == halves - 1) mma_commit(smem_u32(&sh.empty[vstage]));
+                    if (more) {
+                        if (h == 0) ok = take(kt);
+                        if (!ok) break;
+                        tm_fence_after();
+                        scores(h, kt);
+                        if (h == halves - 1) next();
+                    }
+                }
+            }
+            if (ok) mma_commit(smem_u32(&sh.o_done));
+            u += todo;
+            ++items;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
+        const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
+        const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
+        uint32_t steps = 0;
+        int items = 0;
+        bool ok = true;
+        const float neg = a.scale < 0.0f ? -1.0f : 1.0f;
+        // masked scores are -inf: keep their product with the scale -inf when the scale is 0
+        const float c = (MODE & 1) ? fabsf(a.scale) / a.softcap : fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        while (u < u_end && ok) {
+            const int head = static_cast<int>(u / plan.per_head);
+            int off;
+            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            const int64_t u0 = u - off;
+            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+            const bool active = t.rows > 128 * h;
+
+            // ---- Q of this half into shared memory (128-byte swizzle)
+            if (active) {
+                const uint16_t *q = static_cast<const uint16_t *>(a.q);
+                const uint32_t flip = neg < 0.0f ? 0x80008000u : 0u;
+                uint8_t *dst = sh.q + h * kTile;
+                for (int i = tid & 127; i < 128 * 8 * ND; i += 128) {
+                    const int r = i / (8 * ND), ch = i % (8 * ND);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (128 * h + r < t.rows && 8 * ch < a.dim) {
+                        const int gr = t.first + 128 * h + r;
+                        v = *reinterpret_cast<const uint4 *>(q + (t.tok0 + gr / a.group) * a.q_token +
+                                                             (head * a.group + gr % a.group) * a.q_head + 8 * ch);
+                        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                    }
+                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+            }
+            // ---- this row's keys
+            const int gr = t.first + row, tok = gr / a.group, hq = head * a.group + gr % a.group;
+            const bool live = row < t.rows;
+            int lo = 0, hi = 0;
+            if (live) {
+                const Range r = token_range(a, t.seq, t.pos0 + tok, t.tok0 + tok, t.len);
+                lo = static_cast<int>(r.lo), hi = static_cast<int>(r.hi);
+            }
+            // keys that every live row of the warp sees need no mask
+            int in_lo = live ? lo : 0, in_hi = live ? hi : 0x7FFFFFFF;
+            in_lo = __reduce_max_sync(0xffffffffu, in_lo);
+            in_hi = __reduce_min_sync(0xffffffffu, in_hi);
+            mbar_arrive(smem_u32(&sh.q_ready));
+            const float slope = (MODE & 2) && live ? a.slopes[hq] * kLog2e : 0.0f;
+            const int rel = live ? static_cast<int>(t.pos0 + tok) : 0;   // position, for the distance
+
+            float m = -INFINITY, l = 0.0f;   // maximum in use (of c s, log2) and sum
+            for (int i = 0; i < todo && active; ++i) {
+                const int kb = t.lo + (off + i) * kChunkKeys;
+                ok = wait(sh.s_full[h], steps & 1);
+                if (!ok) break;
+                ++steps;
+                tm_fence_after();
+                float s[kChunkKeys];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tm_ld32(ts + 32 * j, s + 32 * j);
+                tm_wait_ld();
+                float mul = c;
+                if (MODE & 1) {
+#pragma unroll
+                    for (int j = 0; j < kChunkKeys; ++j)
+                        s[j] = a.softcap * kLog2e * (1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * (s[j] * c)) + 1.0f));
+                    mul = 1.0f;
+                }
+                if (MODE & 2) {
+                    const float d0 = static_cast<float>(rel - kb);
+#pragma unroll
+                    for (int j = 0; j < kChunkKeys; ++j)
+                        s[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), s[j] * mul);
+                    mul = 1.0f;
+                }
+                if (kb < in_lo || kb + kChunkKeys > in_hi) {
+                    const int a0 = lo - kb, a1 = hi - kb;
+#pragma unroll
+                    for (int j = 0; j < kChunkKeys; ++j) s[j] = j >= a0 && j < a1 ? s[j] : -INFINITY;
+                }
+                float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int j = 4; j < kChunkKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
+                const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
+                float f = 1.0f;
+                if (mx > m + kLazy || m == -INFINITY) {
+                    // (m = mx = -inf: everything masked so far, l and O are zero)
+                    f = mx == m ? 1.0f : ex2(m - mx);
+                    m = mx;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                    l *= f;
+#pragma unroll
+                    for (int j = 0; j < DP / 32; ++j) {
+                        float o[32];
+                        tm_ld32(to + 32 * j, o);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= f;
+                        tm_st32(to + 32 * j, reinterpret_cast<const uint32_t *>(o));
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m - kShift;
+                float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float e0 = ex2(fmaf(s[64 * j + 2 * k], mul, -base));
+                        const float e1 = ex2(fmaf(s[64 * j + 2 * k + 1], mul, -base));
+                        sum[k & 1] += e0, sum[2 + (k & 1)] += e1;
+                        p[k] = pack2(e0, e1, CT);
+                    }
+                    tm_st32(ts + 32 * j, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tm_wait_st();
+                tm_fence_before();
+                mbar_arrive(smem_u32(&sh.p_ready[h]));
+            }
+            if (!ok) break;
+
+            // ---- O: divide and store, or leave a partial result
+            ok = wait(sh.o_done, items & 1);
+            if (!ok) break;
+            ++items;
+            tm_fence_after();
+            const bool split = todo < t.units;
+            float *part = a.part + (2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0)) * (kChunkRows * (DP + 2));
+            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            if (active) {
+                const int64_t at = (t.tok0 + tok) * a.out_token + hq * a.out_head;
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    float o[32];
+                    tm_ld32(to + 32 * j, o);
+                    tm_wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 v = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+                            if (split) *reinterpret_cast<float4 *>(part + row * DP + 32 * j + k) = v;
+                            else if (32 * j + k < a.dim) store4(a.out, a.out_type, at + 32 * j + k, v);
+                        }
+                    }
+                }
+                if (live) {
+                    if (split) part[kChunkRows * DP + row] = m, part[kChunkRows * (DP + 1) + row] = l;
+                    else if (a.lse)
+                        a.lse[static_cast<int64_t>(t.tok0 + tok) * a.heads + hq] =
+                            l == 0.0f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+                }
+                tm_fence_before();
+            }
+            if (split) {
+                // the last CTA to arrive adds the parts in key order
+                const int c0 = share_owner(total, n, u0), c1 = share_owner(total, n, u0 + t.units - 1);
+                __threadfence();
+                mbar_arrive(smem_u32(&sh.joined));
+                ok = wait(sh.joined, 0);
+                if (!ok) break;
+                if (tid == 0) sh.arrived = atomicAdd(a.ticket + c0, 1u);
+                mbar_arrive(smem_u32(&sh.joined));
+                ok = wait(sh.joined, 1);
+                if (!ok) break;
+                if (sh.arrived == static_cast<unsigned int>(c1 - c0)) {
+                    __threadfence();
+                    auto slot_of = [&](int q) {
+                        return a.part + (2 * static_cast<int64_t>(q) + (q == c0 ? 1 : 0)) * (kChunkRows * (DP + 2));
+                    };
+                    for (int i = tid; i < t.rows * (DP / 4); i += 256) {
+                        const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+                        if (d >= a.dim) continue;
+                        float mx = -INFINITY;
+                        for (int q = c0; q <= c1; ++q) mx = fmaxf(mx, __ldcg(slot_of(q) + kChunkRows * DP + r));
+                        float4 v = make_float4(0, 0, 0, 0);
+                        float ls = 0.0f;
+                        for (int q = c0; q <= c1; ++q) {
+                            const float *p = slot_of(q);
+                            const float f = weight(__ldcg(p + kChunkRows * DP + r), mx);
+                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p + r * DP + d));
+                            ls += f * __ldcg(p + kChunkRows * (DP + 1) + r);
+                            v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
+                        }
+                        const float iv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                        const int g2 = t.first + r;
+                        const int64_t tk = t.tok0 + g2 / a.group;
+                        const int h2 = head * a.group + g2 % a.group;
+                        store4(a.out, a.out_type, tk * a.out_token + h2 * a.out_head + d,
+                               make_float4(v.x * iv, v.y * iv, v.z * iv, v.w * iv));
+                        if (a.lse && d == 0)
+                            a.lse[tk * a.heads + h2] = ls == 0.0f ? -INFINITY : (mx + log2f(ls) - kShift) * kLn2;
+                    }
+                }
+            }
+            u += todo;
+        }
+    }
+    __syncwarp();
+    tm_fence_before();
+    __syncthreads();
+    if (w == kMmaWarp) {
+        tm_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u) : "memory");
+    }
+}
+
+struct ChunkLaunch {
+    Args args;
+    int sms;
+    cudaStream_t stream;
+};
+cudaError_t launch_chunk_f16(const ChunkLaunch &l);
+cudaError_t launch_chunk_bf16(const ChunkLaunch &l);
+
+}  // namespace attn
+}  // namespace q4k

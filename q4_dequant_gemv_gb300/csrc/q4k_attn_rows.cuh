@@ -81,7 +81,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS])
 template <int CT, int PARTS, int NT, int DP>
 struct RowsShared {
     static constexpr int R = 8 * NT;
-    using Plan = Split<R, kRowsUnit, kRowsThreads>;
+    using Plan = Split<R, kRowsUnit, kRowsThreads, 16>;
     typename Plan::Shared plan;
     uint4 q[PARTS][NT][DP / 32][32];       // B fragments of Q, lane-major
     float red[kRowsWarps][8][DP];          // O of the warps, one n8 tile at a time
