@@ -41,6 +41,32 @@ static unsigned int *error_word()
     return static_cast<unsigned int *>(v);
 }
 
+namespace attn {
+
+bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    auto one = [&](CUtensorMap *map, const void *base, int64_t page, int64_t slot, int64_t head) {
+        // a stride that no index uses may be anything; the encoder wants a legal one
+        const int64_t row = (a.dim + 7) / 8 * 8;
+        if (a.kv_heads == 1) head = row;
+        if (a.pages == 1) page = row;
+        cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.page_size),
+                              static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.pages)};
+        cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot) * 2, static_cast<cuuint64_t>(head) * 2,
+                                 static_cast<cuuint64_t>(page) * 2};
+        cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+        return enc(map, type == Q4K_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return one(&maps->k, a.k, a.k_page, a.k_slot, a.k_head) && one(&maps->v, a.v, a.v_page, a.v_slot, a.v_head);
+}
+
+}  // namespace attn
+
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)
 {
     q4k_status st = check_cache(c);
@@ -97,6 +123,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     const bool boxes = c->page_size % 16 == 0 && stride_ok(c->k_slot_stride) && stride_ok(c->v_slot_stride) &&
                        (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
+    l.boxes = boxes && p.capacity > 0;
     cudaError_t e;
     if (!l.parts_many && c->dim <= 128 && boxes && p.capacity > 0 && c->tokens * p.group > 16 * c->batch) {
         const attn::ChunkLaunch ch{p, sms, l.stream};

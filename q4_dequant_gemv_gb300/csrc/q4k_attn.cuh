@@ -14,6 +14,7 @@
 // arrive (one atomic ticket per split tile) adds the partial results in the
 // order of the keys, so the same inputs give the same bits.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -97,8 +98,8 @@ __device__ __forceinline__ Range token_range(const Args &a, int seq, int64_t pos
 // ALIGN: where units start (a power of two).
 template <int R, int U, int THREADS, int ALIGN>
 struct Split {
-    static constexpr int kStripes = 1024;     // prefix entries; each covers `stripe` tile slots
-    static constexpr int kSeqs = 1024;        // sequence starts held in shared memory
+    static constexpr int kStripes = 512;     // prefix entries; each covers `stripe` tile slots
+    static constexpr int kSeqs = 512;        // sequence starts held in shared memory
     struct Shared {
         uint32_t prefix[kStripes];
         int start[kSeqs + 1];
@@ -258,6 +259,38 @@ __device__ __forceinline__ void store4(void *out, int type, int64_t i, float4 v)
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + i) = w;
     }
 }
+
+// Four outputs of a tile's row r from d on: v / ls; and the row's lse with d = 0.
+// m and ls as the kernels keep them: log2 domain, ls carrying 2^shift.
+__device__ __forceinline__ void finish_row(const Args &a, const Tile &t, int head, int r, int d, float4 v, float m, float ls,
+                                           float shift)
+{
+    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+    const int row = t.first + r, hq = head * a.group + row % a.group;
+    const int64_t tok = t.tok0 + row / a.group;
+    store4(a.out, a.out_type, tok * a.out_token + hq * a.out_head + d,
+           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (a.lse && d == 0) a.lse[tok * a.heads + hq] = ls == 0.0f ? -INFINITY : (m + log2f(ls) - shift) * kLn2;
+}
+
+// The cache as two 4-D tensors [page][head][slot][d], and a box of one cache
+// head of a page: some slots by 64 elements, 128-byte swizzle.
+struct CacheMaps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int d, int slot, int head, int page,
+                                         uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+// Host: the maps of a call's cache with boxes of `box` slots.
+bool encode_cache(CacheMaps *maps, const Args &a, int type, int box);
 
 }  // namespace attn
 }  // namespace q4k

@@ -138,25 +138,10 @@ constexpr uint32_t chunk_idesc(int n, bool b_mn_major)
            (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
-// The keys of one cache head of a page: box of `rows` slots by 64 elements.
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int d, int slot, int head, int page,
-                                         uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(bar)
-        : "memory");
-}
-
-struct ChunkMaps {
-    CUtensorMap k, v;
-};
-
 // MODE bit 0: capped scores, bit 1: distance bias.
 template <int CT, int DP, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    chunk_kernel(const __grid_constant__ ChunkMaps maps, const Args a, const int box)
+    chunk_kernel(const __grid_constant__ CacheMaps maps, const Args a, const int box)
 {
     using Sh = ChunkShared<DP>;
     constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
@@ -550,14 +535,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             ls += f * __ldcg(p + kChunkRows * (DP + 1) + r);
                             v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
                         }
-                        const float iv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                        const int g2 = t.first + r;
-                        const int64_t tk = t.tok0 + g2 / a.group;
-                        const int h2 = head * a.group + g2 % a.group;
-                        store4(a.out, a.out_type, tk * a.out_token + h2 * a.out_head + d,
-                               make_float4(v.x * iv, v.y * iv, v.z * iv, v.w * iv));
-                        if (a.lse && d == 0)
-                            a.lse[tk * a.heads + h2] = ls == 0.0f ? -INFINITY : (mx + log2f(ls) - kShift) * kLn2;
+                        finish_row(a, t, head, r, d, v, mx, ls, kShift);
                     }
                 }
             }

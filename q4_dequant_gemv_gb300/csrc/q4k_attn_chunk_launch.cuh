@@ -1,34 +1,12 @@
 // q4k_attn_chunk_launch.cuh -- host side of the many-rows attention kernel: the
-// tensor maps of the cache, the variant, the grid and its scratch.
+// variant by sizes, its grid and its scratch.
 #pragma once
 #include <algorithm>
 
 #include "q4k_attn_chunk.cuh"
-#include "q4k_internal.h"
 
 namespace q4k {
 namespace attn {
-
-// A cache as [page][head][slot][d]: boxes of `box` slots by 64 elements, 128-byte swizzle.
-static bool encode_cache(CUtensorMap *map, const void *base, const Args &a, int64_t page, int64_t slot, int64_t head,
-                         int type, int box)
-{
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    // a stride that no index uses may be anything; the encoder wants a legal one
-    const int64_t row = (a.dim + 7) / 8 * 8;
-    if (a.kv_heads == 1) head = row;
-    if (a.pages == 1) page = row;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.page_size),
-                          static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.pages)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot) * 2, static_cast<cuuint64_t>(head) * 2,
-                             static_cast<cuuint64_t>(page) * 2};
-    cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
-    return enc(map, type == Q4K_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-               const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int CT, int DP, int MODE>
 static cudaError_t launch_chunk_one(const ChunkLaunch &l)
@@ -41,10 +19,8 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     int box = 128;
     while (a.page_size % box) box /= 2;
-    ChunkMaps maps;
-    if (!encode_cache(&maps.k, a.k, a, a.k_page, a.k_slot, a.k_head, CT, box) ||
-        !encode_cache(&maps.v, a.v, a, a.v_page, a.v_slot, a.v_head, CT, box))
-        return cudaErrorInvalidValue;
+    CacheMaps maps;
+    if (!encode_cache(&maps, a, CT, box)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;

@@ -1,27 +1,31 @@
 // q4k_attn_rows.cuh -- attention of a few query rows per cache head (decode and
-// verification) on mma.sync, keys and values straight from global memory into
-// registers.
+// verification) on mma.sync.
 //
-// Such a call reads every visible key and value once for 1 to 16 query rows: at
+// Such a call reads every visible key and value once for 1 to 32 query rows: at
 // 7 rows 7 flops a byte, far below what any tensor path offers, so the kernel is
-// bound by memory and by how many loads are in flight.  A warp takes 16 keys at
-// a time and needs no barrier and no shared memory for them:
-//   S^T = K Q^T: A fragment = 16 keys x 16 d.  The order of d inside the
-//     contraction is free, so a thread's fragment registers for two MMAs are one
-//     16-byte load of 8 consecutive d of its key; Q is laid out to match.
-//   O^T = V^T P^T: A fragment = 16 d x 16 keys.  The order of d in the rows is
-//     free too: a thread loads 8 consecutive d of four keys (16 bytes each) and
-//     pairs the keys with byte permutes, which gives the fragments of four MMAs.
-//     P^T comes from the S^T accumulators by an 8x8 transpose (movmatrix).
+// bound by memory and by how many bytes are in flight.  A warp owns blocks of 16
+// keys and a ring of its own in shared memory, fills a slot ahead of time and
+// refills it when it has read it: no barrier between warps until they join at
+// the end of a tile, and 150 to 200 KB in flight per SM.
+//   S^T = K Q^T: A = 16 keys x 16 d (ldmatrix), B = Q^T from shared memory;
+//   O^T = V^T P^T: A = 16 d x 16 keys (ldmatrix.trans), B = P^T from the S^T
+//   accumulators by an 8x8 transpose (movmatrix).
 // The queries are the 8-wide N side, so 7 or 8 heads of a group fill it.
 // Softmax runs per warp over its own keys (running maximum, sum and O rescaled
-// when the maximum grows); the warps of a CTA join once per tile.
+// when the maximum grows).
+//
+// Slots are filled by TMA boxes of 16 keys x 64 d (128-byte swizzle) where pages
+// hold a multiple of 16 keys, else by 16-byte asynchronous copies row by row in
+// the same layout.  Rows of V that no row of the tile sees are zero (they may
+// hold NaN in memory, and P = 0 would not remove it); such keys' scores are
+// replaced.
 //
 // Parts: with fp32 queries or outputs, Q and P enter as PARTS 16-bit parts (3
 // bf16 or 2 fp16: 24 and 22 bits), each an MMA of its own; the products are
 // exact in fp32.  fp16: a power of two per query row brings max|q| to 2^14, and
 // P carries 2^14, so the low parts stay above fp16's subnormals.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "q4k_attn.cuh"
@@ -30,9 +34,18 @@
 namespace q4k {
 namespace attn {
 
-constexpr int kRowsWarps = 8;
-constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kRowsUnit = 16 * kRowsWarps;   // keys per unit
+constexpr int kBlock = 16;                   // keys of a ring slot
+constexpr uint64_t kRowsWaitNs = 2000000000ull;
+
+// Warps of a CTA and slots of a warp's ring, by head size: 160 to 192 KB of ring.
+template <int DP>
+struct RowsShape {
+    static constexpr int kWarps = DP == 256 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kUnit = kBlock * kWarps;          // keys per unit
+    static constexpr int kSide = kBlock * DP * 2;          // bytes of K (or V) in a slot
+    static constexpr int kSlots = DP == 64 ? 5 : 3;
+};
 
 template <int CT>
 __device__ __forceinline__ void mma_t(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -55,13 +68,26 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
-__device__ __forceinline__ uint4 load_stream(const void *p)
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 16 bytes global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 // x as PARTS packed pairs; each part takes what the earlier ones left.
@@ -80,29 +106,43 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS])
 
 template <int CT, int PARTS, int NT, int DP>
 struct RowsShared {
+    using Sp = RowsShape<DP>;
     static constexpr int R = 8 * NT;
-    using Plan = Split<R, kRowsUnit, kRowsThreads, 16>;
+    using Plan = Split<R, Sp::kUnit, Sp::kThreads, kBlock>;
+    static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
+    // a warp's ring; when the warps join it holds the warp's O instead
+    static constexpr int kRing = Sp::kSlots * 2 * Sp::kSide;
+    static_assert(R * kRed * 4 <= kRing, "O of a warp fits in its ring");
+    uint8_t ring[Sp::kWarps][kRing];
     typename Plan::Shared plan;
     uint4 q[PARTS][NT][DP / 32][32];       // B fragments of Q, lane-major
-    float red[kRowsWarps][8][DP];          // O of the warps, one n8 tile at a time
-    float m[kRowsWarps][R], l[kRowsWarps][R];
+    float m[Sp::kWarps][R], l[Sp::kWarps][R];
     float scale[R], slope[R];
-    int lo[R], hi[R], pos[R];              // visible keys and position of each row (position relative to `pos0`)
+    int lo[R], hi[R], pos[R];              // visible keys of each row, its token
     float wm[R], wl[R];                    // joined statistics
+    unsigned long long full[Sp::kWarps][Sp::kSlots];
     unsigned int arrived;
 };
 
-template <int CT, int PARTS, int NT, int DP>
-__global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) rows_kernel(const Args a)
+// TMA: slots filled by tensor copies (maps), else by cp.async.
+template <int CT, int PARTS, int NT, int DP, bool TMA>
+__global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
 {
     using Sh = RowsShared<CT, PARTS, NT, DP>;
-    constexpr int R = Sh::R, CH = DP / 32, VH = DP / 64;
+    using Sp = RowsShape<DP>;
+    constexpr int R = Sh::R, ND = DP / 64, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
+    constexpr int kHalf = kBlock * 128;      // bytes of 16 rows of 64 elements
     constexpr float kShift = CT == Q4K_F16 ? 14.0f : 0.0f;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Sh &sh = *reinterpret_cast<Sh *>(smem_raw);
+    extern __shared__ uint8_t smem_raw[];
+    Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
 
-    typename Sh::Plan plan(a, sh.plan);
+    if (TMA && tid == 0) {
+        for (int i = 0; i < WARPS; ++i)
+            for (int j = 0; j < SLOTS; ++j) mbar_init(smem_u32(&sh.full[i][j]), 1);
+        fence_barrier_init();
+    }
+    typename Sh::Plan plan(a, sh.plan);      // synchronises the CTA
     const int64_t total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
     if (total == 0) return;
     const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
@@ -111,8 +151,13 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
     int64_t u = share_begin(total, n, cta);
     const int64_t u_end = share_begin(total, n, cta + 1);
 
-    const uint16_t *kbase = static_cast<const uint16_t *>(a.k), *vbase = static_cast<const uint16_t *>(a.v);
     const int psize = static_cast<int>(a.page_size);
+    const uint32_t ring = smem_u32(sh.ring[w]);
+    // ldmatrix addresses within a slot: row of the lane, chunk before the swizzle
+    const int krow = (lane & 7) + 8 * ((lane >> 3) & 1), kch = lane >> 4;
+    const int vrow = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
+    uint32_t fills = 0;                      // slots filled so far by this warp (TMA: phases)
+    bool good = true;                        // no wait has timed out
 
     while (u < u_end) {
         const int head = static_cast<int>(u / plan.per_head);
@@ -121,9 +166,80 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
         const int64_t u0 = u - off;
         const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
 
+        // ---- this warp's blocks: key kb0 + i * kUnit, i < count
+        const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
+        const int kb0 = t.lo + off * Sp::kUnit + kBlock * w;
+        const int count = good && kb0 < t.hi ? min(todo, (t.hi - kb0 + Sp::kUnit - 1) / Sp::kUnit) : 0;
+        // pages of the next 32 blocks, a lane each (TMA)
+        int ids = 0;
+        auto look = [&](int first) {
+            const int i = first + lane;
+            ids = 0;
+            if (i < count) {
+                ids = pages[(kb0 + i * Sp::kUnit) / psize];
+                if (ids < 0 || ids >= a.pages) {
+                    atomicOr(a.error, 4u);
+                    ids = 0;
+                }
+            }
+        };
+        auto fill = [&](int i) {
+            const int s = static_cast<int>(fills % SLOTS);
+            const int kb = kb0 + i * Sp::kUnit;
+            const uint32_t dst = ring + s * 2 * Sp::kSide;
+            if constexpr (TMA) {
+                if ((i & 31) == 0) look(i);
+                const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sh.full[w][s]);
+                    const int slot = kb % psize;
+                    mbar_arrive_expect_tx(bar, 2 * Sp::kSide);
+#pragma unroll
+                    for (int h = 0; h < ND; ++h) {
+                        load_box(dst + h * kHalf, &maps.k, 64 * h, slot, head, page, bar);
+                        load_box(dst + Sp::kSide + h * kHalf, &maps.v, 64 * h, slot, head, page, bar);
+                    }
+                }
+            } else {
+                // lane r < 16 finds row r
+                const int key = kb + (lane & 15);
+                const bool seen = key >= t.from && key < t.hi;
+                int page = 0, slot = 0;
+                if (seen) {
+                    const int e = key / psize;
+                    slot = key - e * psize;
+                    page = pages[e];
+                    if (page < 0 || page >= a.pages) {
+                        atomicOr(a.error, 4u);
+                        page = 0;
+                    }
+                }
+                const uint32_t some = __ballot_sync(0xffffffffu, seen);
+                constexpr int CPR = DP / 8;      // chunks of a row
+#pragma unroll
+                for (int j = 0; j < kBlock * CPR / 32; ++j) {
+                    const int c = (lane + 32 * j) % CPR, r = (lane + 32 * j) / CPR;
+                    const int64_t p = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
+                    const bool live = (some >> r & 1) && 8 * c < a.dim;
+                    const uint32_t o = (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    // (a dead copy reads nothing; its address stays inside the cache)
+                    const int64_t d = live ? 8 * c : 0;
+                    copy16(dst + o, static_cast<const uint16_t *>(a.k) + p * a.k_page + sl * a.k_slot + head * a.k_head + d, live);
+                    copy16(dst + Sp::kSide + o,
+                           static_cast<const uint16_t *>(a.v) + p * a.v_page + sl * a.v_slot + head * a.v_head + d, live);
+                }
+            }
+            ++fills;
+        };
+        const uint32_t first_fill = fills;
+        if constexpr (TMA) fence_proxy_async_smem();   // (the ring may have held the previous tile's O)
+        for (int i = 0; i < SLOTS; ++i) {
+            if (i < count) fill(i);
+            if constexpr (!TMA) asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+
         // ---- the tile's rows: scale, visible range, fragments of Q
-        __syncthreads();   // the previous tile's shared data is done with
-        for (int r = w; r < R; r += kRowsWarps) {   // a warp per row
+        for (int r = w; r < R; r += WARPS) {   // a warp per row
             const bool live = r < t.rows;
             const int row = t.first + r, tok = row / a.group, hq = head * a.group + row % a.group;
             float x[DP / 32];
@@ -151,13 +267,13 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
             const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
-                // element d = 32c + 8j + i of the row: half i & 1 of word i >> 1 of lane 4 (r % 8) + j
+                // d = 32 c + 16 i + 8 j + 2 t + b: half b of word 2 i + j of lane 4 (r % 8) + t
                 float v = x[c] * up;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
                     const uint32_t h = pack2(v, 0.0f, CT);
-                    reinterpret_cast<uint16_t *>(&sh.q[p][r >> 3][c][4 * (r & 7) + (lane >> 3)])[lane & 7] =
-                        static_cast<uint16_t>(h & 0xFFFFu);
+                    reinterpret_cast<uint16_t *>(&sh.q[p][r >> 3][c][4 * (r & 7) + ((lane >> 1) & 3)])
+                        [2 * (lane >> 3) + (lane & 1)] = static_cast<uint16_t>(h & 0xFFFFu);
                     v -= unpack2(h, CT).x;
                 }
             }
@@ -173,154 +289,121 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
         }
         __syncthreads();
 
-        float scl[NT][2], slope[NT][2];
-        int lo[NT][2], hi[NT][2], ptok[NT][2];
         int in_lo = 0, in_hi = 0x7FFFFFFF;   // keys that every live row sees
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 8 * nt + 2 * t4 + j;
-                scl[nt][j] = sh.scale[r], slope[nt][j] = sh.slope[r];
-                lo[nt][j] = sh.lo[r], hi[nt][j] = sh.hi[r], ptok[nt][j] = sh.pos[r];
-            }
         for (int r = 0; r < t.rows; ++r) in_lo = max(in_lo, sh.lo[r]), in_hi = min(in_hi, sh.hi[r]);
 
-        float m[NT][2], l[NT][2], o[NT][2 * CH][4];   // o[..][4 h + i]: d = 64 h + 8 g + 2 i (+1)
+        float m[NT][2], l[NT][2], o[NT][KS][4];   // o[..][i]: d = 16 i + g (+8), queries 2 t4 (+1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, l[nt][j] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2 * CH; ++i)
+            for (int i = 0; i < KS; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
         }
 
-        // ---- the keys: 16 per warp and step
-        const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
-        const int kb0 = t.lo + off * kRowsUnit + 16 * w;
-        uint4 kf[2][CH], vf[4][VH];
-        // page and slot of this lane's key (key kb + lane % 16)
-        auto place = [&](int kb, int &pg, int &slot) {
-            const int key = kb + (lane & 15);
-            pg = 0, slot = 0;
-            if (key < t.from || key >= t.hi) return;
-            const int e = key / psize;
-            slot = key - e * psize;
-            pg = pages[e];
-            if (pg < 0 || pg >= a.pages) {
-                atomicOr(a.error, 4u);
-                pg = 0;
+        for (int i = 0; i < count; ++i) {
+            const int kb = kb0 + i * Sp::kUnit;
+            const uint32_t f = first_fill + i;
+            const int slot = static_cast<int>(f % SLOTS);
+            const uint32_t kt = ring + slot * 2 * Sp::kSide, vt = kt + Sp::kSide;
+            if constexpr (TMA) {
+                const bool here = mbar_wait_bounded(smem_u32(&sh.full[w][slot]), (f / SLOTS) & 1, kRowsWaitNs);
+                good = __all_sync(0xffffffffu, here);
+                if (!good) {
+                    // wind down: the copies in flight land (or time out) before the ring is used again
+                    if (lane == 0) atomicOr(a.error, 8u);
+                    for (uint32_t k = f; k != fills; ++k)
+                        (void)mbar_wait_bounded(smem_u32(&sh.full[w][k % SLOTS]), (k / SLOTS) & 1, kRowsWaitNs);
+                    break;
+                }
+                if (kb < t.from || kb + kBlock > t.hi) {
+                    // rows of V that nothing sees: zero
+                    for (int r = 0; r < kBlock; ++r)
+                        if ((kb + r < t.from || kb + r >= t.hi) && lane < 8 * ND)
+                            *reinterpret_cast<uint4 *>(sh.ring[w] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf +
+                                                       r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();   // before a later copy into the slot
+                    __syncwarp();
+                }
+            } else {
+                asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+                __syncwarp();
             }
-        };
-        auto load_k = [&](int kb, int pg, int slot) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r;
-                const int p = __shfl_sync(0xffffffffu, pg, row), sl = __shfl_sync(0xffffffffu, slot, row);
-                const uint16_t *s = kbase + p * a.k_page + sl * a.k_slot + head * a.k_head + 8 * t4;
-                const bool live = kb + row >= t.from && kb + row < t.hi;
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    kf[r][c] = live && 32 * c + 8 * t4 < a.dim ? load_stream(s + 32 * c) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto load_v = [&](int kb, int pg, int slot) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 2 * t4 + (r & 1) + 8 * (r >> 1);
-                const int p = __shfl_sync(0xffffffffu, pg, row), sl = __shfl_sync(0xffffffffu, slot, row);
-                const uint16_t *s = vbase + p * a.v_page + sl * a.v_slot + head * a.v_head + 8 * g;
-                const bool live = kb + row >= t.from && kb + row < t.hi;
-#pragma unroll
-                for (int h = 0; h < VH; ++h)
-                    vf[r][h] = live && 64 * h + 8 * g < a.dim ? load_stream(s + 64 * h) : make_uint4(0, 0, 0, 0);
-            }
-        };
 
-        int pg, slot;
-        place(kb0, pg, slot);
-        if (kb0 < t.hi) load_k(kb0, pg, slot), load_v(kb0, pg, slot);
-        for (int i = 0; i < todo; ++i) {
-            const int kb = kb0 + i * kRowsUnit;
-            if (kb >= t.hi) break;
-            const int kn = kb + kRowsUnit;
-            const bool more = i + 1 < todo && kn < t.hi;
-            if (more) place(kn, pg, slot);
-
-            float s[NT][4];
+            // ---- S^T
+            // chains of their own: even and odd k-steps (one part), or the parts
+            constexpr int CHAINS = PARTS > 1 ? PARTS : 2;
+            float acc[NT][CHAINS][4] = {};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // chains of their own: the two k-steps of a load (one part), or the parts
-                constexpr int CHAINS = PARTS > 1 ? PARTS : 2;
-                float acc[CHAINS][4] = {};
+            for (int j = 0; j < KS; ++j) {
+                const int c = 2 * j + kch;
+                uint32_t kf[4];
+                ldmatrix4(kt + (c >> 3) * kHalf + krow * 128 + (((c & 7) ^ (krow & 7)) << 4), kf);
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {
-                        const uint4 b = sh.q[p][nt][c][lane];
-                        mma_t<CT>(acc[p], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, b.x, b.y);
-                        mma_t<CT>(acc[PARTS > 1 ? p : 1], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, b.z, b.w);
+                        const uint2 b = reinterpret_cast<const uint2 *>(&sh.q[p][nt][j >> 1][lane])[j & 1];
+                        mma_t<CT>(acc[nt][PARTS > 1 ? p : j & 1], kf[0], kf[1], kf[2], kf[3], b.x, b.y);
                     }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (PARTS > 1) {
-                        // an infinite key: the first part has its sign, the others may be 0 or of the other sign
-                        float rest = acc[PARTS - 1][j];
-#pragma unroll
-                        for (int p = PARTS - 2; p > 0; --p) rest += acc[p][j];
-                        const bool finite = fabsf(acc[0][j]) < INFINITY;
-                        s[nt][j] = finite ? acc[0][j] + rest : acc[0][j];
-                    } else {
-                        s[nt][j] = acc[0][j] + acc[1][j];
-                    }
-                }
             }
-            if (more) load_k(kn, pg, slot);
 
-            const bool all = kb >= in_lo && kb + 16 <= in_hi;
+            const bool all = kb >= in_lo && kb + kBlock <= in_hi;
             uint32_t pb[NT][PARTS][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                const int r0 = 8 * nt + 2 * t4;
+                const float2 scl = *reinterpret_cast<const float2 *>(&sh.scale[r0]);
+                float s[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float x = s[nt][j] * scl[nt][j & 1];
+                    float x;
+                    if constexpr (PARTS > 1) {
+                        // an infinite key: the first part has its sign, the others may be 0 or of the other sign
+                        float rest = acc[nt][PARTS - 1][j];
+#pragma unroll
+                        for (int p = PARTS - 2; p > 0; --p) rest += acc[nt][p][j];
+                        x = fabsf(acc[nt][0][j]) < INFINITY ? acc[nt][0][j] + rest : acc[nt][0][j];
+                    } else {
+                        x = acc[nt][0][j] + acc[nt][1][j];
+                    }
+                    x *= j & 1 ? scl.y : scl.x;
                     if (a.softcap > 0.0f) {
                         const float th = PARTS > 1 ? tanhf(x) : 1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * x) + 1.0f);
                         x = a.softcap * kLog2e * th;
                     }
                     const int key = kb + g + 8 * (j >> 1);
                     if (a.slopes)
-                        x -= slope[nt][j & 1] *
-                             fabsf(static_cast<float>(t.pos0 + ptok[nt][j & 1] - key));
-                    if (!all && (key < lo[nt][j & 1] || key >= hi[nt][j & 1])) x = -INFINITY;
-                    s[nt][j] = x;
+                        x -= sh.slope[r0 + (j & 1)] * fabsf(static_cast<float>(t.pos0 + sh.pos[r0 + (j & 1)] - key));
+                    if (!all && (key < sh.lo[r0 + (j & 1)] || key >= sh.hi[r0 + (j & 1)])) x = -INFINITY;
+                    s[j] = x;
                 }
-                float mx[2], f[2];
+                float mx[2], fa[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float v = fmaxf(s[nt][j], s[nt][j + 2]);
+                    float v = fmaxf(s[j], s[j + 2]);
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                     mx[j] = fmaxf(m[nt][j], v);
-                    f[j] = mx[j] == -INFINITY ? 1.0f : ex2(m[nt][j] - mx[j]);
+                    fa[j] = mx[j] == -INFINITY ? 1.0f : ex2(m[nt][j] - mx[j]);
                     m[nt][j] = mx[j];
-                    l[nt][j] *= f[j];
+                    l[nt][j] *= fa[j];
                 }
-                if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
+                if (__any_sync(0xffffffffu, fa[0] != 1.0f || fa[1] != 1.0f)) {
 #pragma unroll
-                    for (int q = 0; q < 2 * CH; ++q) {
-                        o[nt][q][0] *= f[0], o[nt][q][1] *= f[1];
-                        o[nt][q][2] *= f[0], o[nt][q][3] *= f[1];
+                    for (int q = 0; q < KS; ++q) {
+                        o[nt][q][0] *= fa[0], o[nt][q][1] *= fa[1];
+                        o[nt][q][2] *= fa[0], o[nt][q][3] *= fa[1];
                     }
                 }
                 float e[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float base = mx[j & 1] == -INFINITY ? 0.0f : mx[j & 1] - kShift;
-                    e[j] = ex2(s[nt][j] - base);
+                    e[j] = ex2(s[j] - base);
                     l[nt][j & 1] += e[j];
                 }
                 uint32_t p0[PARTS], p1[PARTS];
@@ -329,24 +412,26 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) pb[nt][p][0] = transpose8(p0[p]), pb[nt][p][1] = transpose8(p1[p]);
             }
+
+            // ---- O^T
 #pragma unroll
-            for (int h = 0; h < VH; ++h) {
-                const uint32_t *v0 = &vf[0][h].x, *v1 = &vf[1][h].x, *v2 = &vf[2][h].x, *v3 = &vf[3][h].x;
+            for (int j = 0; j < KS; ++j) {
+                const int c = 2 * j + vch;
+                uint32_t vf[4];
+                ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t a0 = __byte_perm(v0[q], v1[q], 0x5410), a1 = __byte_perm(v0[q], v1[q], 0x7632);
-                    const uint32_t a2 = __byte_perm(v2[q], v3[q], 0x5410), a3 = __byte_perm(v2[q], v3[q], 0x7632);
+                for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int p = PARTS - 1; p >= 0; --p)
-                            mma_t<CT>(o[nt][4 * h + q], a0, a1, a2, a3, pb[nt][p][0], pb[nt][p][1]);
-                }
+                        mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
             }
-            if (more) load_v(kn, pg, slot);
+            __syncwarp();   // the slot has been read by every lane
+            if (i + SLOTS < count) fill(i + SLOTS);
+            if constexpr (!TMA) asm volatile("cp.async.commit_group;" ::: "memory");
         }
 
-        // ---- join the warps
+        // ---- join the warps: each leaves O in its own ring
+        float *red = reinterpret_cast<float *>(sh.ring[w]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -354,67 +439,36 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
-                if (g == 0) sh.m[w][8 * nt + 2 * t4 + j] = m[nt][j], sh.l[w][8 * nt + 2 * t4 + j] = l[nt][j];
+                const int q = 8 * nt + 2 * t4 + j;
+                if (g == 0) sh.m[w][q] = m[nt][j], sh.l[w][q] = l[nt][j];
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    red[q * Sh::kRed + 16 * i + g] = o[nt][i][j];
+                    red[q * Sh::kRed + 16 * i + 8 + g] = o[nt][i][j + 2];
+                }
             }
         __syncthreads();
-        if (tid < R) {
-            float mx = -INFINITY, ls = 0.0f;
-            for (int i = 0; i < kRowsWarps; ++i) mx = fmaxf(mx, sh.m[i][tid]);
-            for (int i = 0; i < kRowsWarps; ++i)
-                ls += sh.l[i][tid] * weight(sh.m[i][tid], mx);
-            sh.wm[tid] = mx, sh.wl[tid] = ls;
-        }
         const bool split = todo < t.units;
-        const int64_t pslot = 2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0);
-        float *part = a.part + pslot * (R * (DP + 2));
-        __syncthreads();
+        float *part = a.part + (2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0)) * (R * (DP + 2));
+        for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
+            const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+            float mx = -INFINITY, ls = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int k = 0; k < WARPS; ++k) mx = fmaxf(mx, sh.m[k][r]);
+            float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int q = 2 * t4 + j;
-                const float mx = sh.wm[8 * nt + q];
-                const float f = weight(m[nt][j], mx);
-#pragma unroll
-                for (int h = 0; h < VH; ++h) {
-                    float4 *dst = reinterpret_cast<float4 *>(&sh.red[w][q][64 * h + 8 * g]);
-                    dst[0] = make_float4(o[nt][4 * h][j] * f, o[nt][4 * h][j + 2] * f, o[nt][4 * h + 1][j] * f,
-                                         o[nt][4 * h + 1][j + 2] * f);
-                    dst[1] = make_float4(o[nt][4 * h + 2][j] * f, o[nt][4 * h + 2][j + 2] * f,
-                                         o[nt][4 * h + 3][j] * f, o[nt][4 * h + 3][j + 2] * f);
-                }
+            for (int k = 0; k < WARPS; ++k) {
+                const float f = weight(sh.m[k][r], mx);
+                const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sh.ring[k]) + r * Sh::kRed + d);
+                ls += f * sh.l[k][r];
+                v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
             }
-            __syncthreads();
-            for (int i = tid; i < 8 * DP / 4; i += kRowsThreads) {
-                const int q = i / (DP / 4), d = 4 * (i % (DP / 4)), r = 8 * nt + q;
-                float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int k = 0; k < kRowsWarps; ++k) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sh.red[k][q][d]);
-                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-                }
-                if (r < t.rows && d < a.dim) {
-                    if (split) {
-                        *reinterpret_cast<float4 *>(part + r * DP + d) = v;
-                    } else {
-                        const float ls = sh.wl[r], inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                        const int row = t.first + r;
-                        const int64_t at = (t.tok0 + row / a.group) * a.out_token +
-                                           (head * a.group + row % a.group) * a.out_head + d;
-                        store4(a.out, a.out_type, at, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        if (tid < t.rows) {
+            if (d >= a.dim) continue;
             if (split) {
-                part[R * DP + tid] = sh.wm[tid], part[R * DP + R + tid] = sh.wl[tid];
-            } else if (a.lse) {
-                const int row = t.first + tid;
-                const float ls = sh.wl[tid];
-                a.lse[static_cast<int64_t>(t.tok0 + row / a.group) * a.heads + head * a.group + row % a.group] =
-                    ls == 0.0f ? -INFINITY : (sh.wm[tid] + log2f(ls) - kShift) * kLn2;
+                *reinterpret_cast<float4 *>(part + r * DP + d) = v;
+                if (d == 0) part[R * DP + r] = mx, part[R * DP + R + r] = ls;
+            } else {
+                finish_row(a, t, head, r, d, v, mx, ls, kShift);
             }
         }
 
@@ -428,41 +482,36 @@ __global__ void __launch_bounds__(kRowsThreads, (NT == 1 && DP <= 128) ? 2 : 1) 
             if (sh.arrived == static_cast<unsigned int>(c1 - c0)) {
                 __threadfence();
                 auto slot_of = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * (R * (DP + 2)); };
-                for (int i = tid; i < R * DP / 4; i += kRowsThreads) {
+                for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
                     const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-                    if (r >= t.rows || d >= a.dim) continue;
+                    if (d >= a.dim) continue;
                     float mx = -INFINITY;
+#pragma unroll 8
                     for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + R * DP + r));
                     float4 v = make_float4(0, 0, 0, 0);
                     float ls = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = c0; c <= c1; ++c) {
                         const float *p = slot_of(c);
-                        const float pm = __ldcg(p + R * DP + r);
-                        const float f = weight(pm, mx);
+                        const float f = weight(__ldcg(p + R * DP + r), mx);
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + r * DP + d));
                         ls += f * __ldcg(p + R * DP + R + r);
                         v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
                     }
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                    const int row = t.first + r;
-                    const int64_t tok = t.tok0 + row / a.group;
-                    const int hq = head * a.group + row % a.group;
-                    store4(a.out, a.out_type, tok * a.out_token + hq * a.out_head + d,
-                           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    if (a.lse && d == 0)
-                        a.lse[tok * a.heads + hq] = ls == 0.0f ? -INFINITY : (mx + log2f(ls) - kShift) * kLn2;
+                    finish_row(a, t, head, r, d, v, mx, ls, kShift);
                 }
             }
         }
         u += todo;
+        __syncthreads();   // the tile's shared data is done with
     }
 }
 
 // Launches the kernel of one cache type (in a translation unit of its own).
 struct RowsLaunch {
     Args args;
-    int sms, parts_many;   // parts_many: fp32 queries or outputs
+    int sms, parts_many;   // parts_many: fp32 queries or outputs, or a 16-bit type that is not the cache's
+    bool boxes;            // pages and strides that TMA boxes of 16 slots can take
     cudaStream_t stream;
 };
 cudaError_t launch_rows_f16(const RowsLaunch &l);

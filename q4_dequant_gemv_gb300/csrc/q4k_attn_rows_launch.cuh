@@ -8,20 +8,23 @@
 namespace q4k {
 namespace attn {
 
-template <int CT, int PARTS, int NT, int DP>
-static cudaError_t launch_rows_one(const RowsLaunch &l)
+template <int CT, int PARTS, int NT, int DP, bool TMA>
+static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
     using Sh = RowsShared<CT, PARTS, NT, DP>;
-    auto kern = rows_kernel<CT, PARTS, NT, DP>;
-    constexpr int per_sm = (NT == 1 && DP <= 128) ? 2 : 1;
+    using Sp = RowsShape<DP>;
+    auto kern = rows_kernel<CT, PARTS, NT, DP, TMA>;
     Args a = l.args;
     constexpr int R = Sh::R;
+    constexpr int kSmem = static_cast<int>(sizeof(Sh)) + 1024;   // room to align the rings to 1024 bytes
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+    CacheMaps maps;
+    if (TMA && !encode_cache(&maps, a, CT, kBlock)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
-    const int64_t units = (a.capacity + 15) / kRowsUnit + 1;   // of one tile at most
+    const int64_t units = (a.capacity + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
-    const int grid = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(l.sms) * per_sm));
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Sh)));
+    const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
+    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
     const size_t head = (grid * sizeof(unsigned int) + 255) / 256 * 256;
     void *scratch = nullptr;
@@ -37,7 +40,7 @@ static cudaError_t launch_rows_one(const RowsLaunch &l)
         a.ticket = static_cast<unsigned int *>(scratch);
         a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
     }
-    kern<<<grid, kRowsThreads, sizeof(Sh), l.stream>>>(a);
+    kern<<<grid, Sp::kThreads, kSmem, l.stream>>>(maps, a);
     cudaError_t e = cudaGetLastError();
     if (scratch) {
         const cudaError_t f = cudaFreeAsync(scratch, l.stream);
@@ -46,21 +49,34 @@ static cudaError_t launch_rows_one(const RowsLaunch &l)
     return e;
 }
 
+template <int CT, int PARTS, int NT, int DP>
+static cudaError_t launch_rows_one(const RowsLaunch &l)
+{
+    return l.boxes ? launch_rows_fill<CT, PARTS, NT, DP, true>(l) : launch_rows_fill<CT, PARTS, NT, DP, false>(l);
+}
+
+template <int CT, int PARTS, int DP>
+static cudaError_t launch_rows_tiles(const RowsLaunch &l)
+{
+    // the smallest tile that holds the rows an average sequence brings (fewer
+    // reads of the cache), 8 to 32; dim > 128 leaves registers for 16
+    const int64_t rows = static_cast<int64_t>(l.args.tokens) * l.args.group, batch = l.args.batch;
+    if (rows <= 8 * batch) return launch_rows_one<CT, PARTS, 1, DP>(l);
+    if constexpr (DP <= 128)
+        if (rows > 16 * batch) return launch_rows_one<CT, PARTS, 4, DP>(l);
+    return launch_rows_one<CT, PARTS, 2, DP>(l);
+}
+
 template <int CT, int MANY>
 static cudaError_t launch_rows_type(const RowsLaunch &l)
 {
-    // 16 query rows where sequences bring more than 8 per cache head: half the
-    // reads of the cache
-    const bool two = static_cast<int64_t>(l.args.tokens) * l.args.group > 8 * static_cast<int64_t>(l.args.batch);
     const int dim = l.args.dim;
     if (l.parts_many) {
-        if (dim > 128) return launch_rows_one<CT, MANY, 1, 256>(l);
-        if (dim > 64) return two ? launch_rows_one<CT, MANY, 2, 128>(l) : launch_rows_one<CT, MANY, 1, 128>(l);
-        return two ? launch_rows_one<CT, MANY, 2, 64>(l) : launch_rows_one<CT, MANY, 1, 64>(l);
+        if (dim > 128) return launch_rows_tiles<CT, MANY, 256>(l);
+        return dim > 64 ? launch_rows_tiles<CT, MANY, 128>(l) : launch_rows_tiles<CT, MANY, 64>(l);
     }
-    if (dim > 128) return launch_rows_one<CT, 1, 1, 256>(l);
-    if (dim > 64) return two ? launch_rows_one<CT, 1, 2, 128>(l) : launch_rows_one<CT, 1, 1, 128>(l);
-    return two ? launch_rows_one<CT, 1, 2, 64>(l) : launch_rows_one<CT, 1, 1, 64>(l);
+    if (dim > 128) return launch_rows_tiles<CT, 1, 256>(l);
+    return dim > 64 ? launch_rows_tiles<CT, 1, 128>(l) : launch_rows_tiles<CT, 1, 64>(l);
 }
 
 }  // namespace attn
