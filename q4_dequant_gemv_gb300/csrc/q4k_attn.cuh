@@ -58,6 +58,7 @@ struct Args {
     int pages, batch, tokens, heads, kv_heads, group, dim;
     int q_type, out_type, causal;
     int slots;             // upper bound of the tiles per cache head
+    int cluster;           // few-rows kernel: CTAs of a cluster that share a tile; 0: the split over all CTAs
     float *part;           // partial results: two slots per CTA
     unsigned int *ticket;  // one per CTA, zero at launch
     unsigned int *error;   // the sticky error word
@@ -102,7 +103,7 @@ struct Split {
     static constexpr int kSeqs = 512;        // sequence starts held in shared memory
     struct Shared {
         uint32_t prefix[kStripes];
-        int start[kSeqs + 1];
+        int start[kSeqs + 1], len[kSeqs];
         uint32_t warp[THREADS / 32];
     };
 
@@ -116,25 +117,32 @@ struct Split {
         const int s = a.batch <= kSeqs ? sh.start[b] : a.seq_start[b];
         return min(max(s, 0), a.tokens);
     }
-    // First tile slot of sequence b: no smaller than the tiles before it need.
-    __device__ __forceinline__ int slot_of(int b) const
+    // Tile slots: slot b < batch is sequence b's first tile; its others take the
+    // slots from batch + extra(b) on, which has room for them whatever the lengths.
+    __device__ __forceinline__ int extra(int b) const
     {
-        return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / R) + b;
+        return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / R);
     }
 
     __device__ __forceinline__ Tile tile(int slot, bool report) const
     {
         Tile t{};
-        int b = 0, e = a.batch - 1;
-        while (b < e) {   // the last sequence whose first slot is <= slot
-            const int m = (b + e + 1) >> 1;
-            if (slot_of(m) <= slot) b = m; else e = m - 1;
+        int b = slot, j = 0;
+        if (slot >= a.batch) {
+            const int x = slot - a.batch;
+            int e = a.batch - 1;
+            b = 0;
+            while (b < e) {   // the last sequence with extra(b) <= x
+                const int m = (b + e + 1) >> 1;
+                if (extra(m) <= x) b = m; else e = m - 1;
+            }
+            j = x - extra(b) + 1;
         }
         const int s0 = start_of(b), n = start_of(b + 1) - s0;
-        const int raw = a.kv_len[b];
+        const int raw = a.batch <= kSeqs ? sh.len[b] : a.kv_len[b];
         t.seq = b, t.tok0 = s0, t.ntok = n;
-        t.first = (slot - slot_of(b)) * R;
-        if (n <= 0 || t.first < 0 || t.first >= n * a.group) return t;
+        if (n <= 0 || j < 0 || j > (n * a.group - 1) / R) return t;
+        t.first = j * R;
         t.rows = min(R, n * a.group - t.first);
         t.len = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), a.capacity));
         if (report && (raw < 0 || raw > a.capacity)) atomicOr(a.error, 4u);
@@ -157,16 +165,25 @@ struct Split {
         return t;
     }
 
-    // All threads of the CTA.
+    // Sequence starts and lengths; all threads of the CTA.
     __device__ __forceinline__ Split(const Args &args, Shared &shared) : a(args), sh(shared)
     {
         const int tid = threadIdx.x;
         for (int i = tid; i <= a.batch; i += THREADS) {
             const int s = a.seq_start[i];
             if (s < 0 || s > a.tokens || (i > 0 && s < a.seq_start[i - 1])) atomicOr(a.error, 4u);
-            if (a.batch <= kSeqs) sh.start[i] = s;
+            if (a.batch <= kSeqs) {
+                sh.start[i] = s;
+                if (i < a.batch) sh.len[i] = a.kv_len[i];
+            }
         }
         __syncthreads();
+    }
+
+    // The prefix over all tiles; all threads of the CTA.
+    __device__ __forceinline__ void scan()
+    {
+        const int tid = threadIdx.x;
         stripe = (a.slots + kStripes - 1) / kStripes;
         constexpr int PER = (kStripes + THREADS - 1) / THREADS;   // consecutive prefix entries of a thread
         uint32_t sum[PER], run = 0;

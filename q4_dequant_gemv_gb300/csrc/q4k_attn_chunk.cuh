@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     tm_fence_before();
     typename Sh::Plan plan(a, sh.plan);   // synchronises the CTA
+    plan.scan();
     tm_fence_after();
     const uint32_t tm = sh.tmem;
 

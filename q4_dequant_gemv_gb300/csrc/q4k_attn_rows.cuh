@@ -34,6 +34,7 @@
 namespace q4k {
 namespace attn {
 
+constexpr int kMaxCluster = 8;               // portable cluster size
 constexpr int kBlock = 16;                   // keys of a ring slot
 constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
@@ -84,6 +85,16 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // 16 bytes global -> shared, or 16 zero bytes.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live)
 {
@@ -112,7 +123,7 @@ struct RowsShared {
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
     // a warp's ring; when the warps join it holds the warp's O instead
     static constexpr int kRing = Sp::kSlots * 2 * Sp::kSide;
-    static_assert(R * kRed * 4 <= kRing, "O of a warp fits in its ring");
+    static_assert((R + R / Sp::kWarps) * kRed * 4 <= kRing, "O of a warp and the sums of its rows fit in its ring");
     uint8_t ring[Sp::kWarps][kRing];
     typename Plan::Shared plan;
     uint4 q[PARTS][NT][DP / 32][32];       // B fragments of Q, lane-major
@@ -143,13 +154,16 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         fence_barrier_init();
     }
     typename Sh::Plan plan(a, sh.plan);      // synchronises the CTA
-    const int64_t total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
-    if (total == 0) return;
-    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
     const int cta = blockIdx.x;
-    if (cta >= n) return;
-    int64_t u = share_begin(total, n, cta);
-    const int64_t u_end = share_begin(total, n, cta + 1);
+    int64_t total = 0, u = 0, u_end = 1;
+    int n = 0;
+    if (!a.cluster) {
+        plan.scan();
+        total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
+        n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+        if (cta >= n) return;
+        u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+    }
 
     const int psize = static_cast<int>(a.page_size);
     const uint32_t ring = smem_u32(sh.ring[w]);
@@ -160,11 +174,23 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
     bool good = true;                        // no wait has timed out
 
     while (u < u_end) {
-        const int head = static_cast<int>(u / plan.per_head);
-        int off;
-        const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
-        const int64_t u0 = u - off;
-        const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+        int head, off, todo;
+        int64_t u0 = 0;
+        Tile t;
+        if (a.cluster) {
+            // a cluster per tile and cache head, equal shares of its units
+            const int item = cta / a.cluster, rank = cta - item * a.cluster;
+            t = plan.tile(item / a.kv_heads, true);
+            if (!t.rows) return;
+            head = item % a.kv_heads;
+            off = t.units * rank / a.cluster;
+            todo = t.units * (rank + 1) / a.cluster - off;
+        } else {
+            head = static_cast<int>(u / plan.per_head);
+            t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            u0 = u - off;
+            todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+        }
 
         // ---- this warp's blocks: key kb0 + i * kUnit, i < count
         const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
@@ -448,7 +474,12 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 }
             }
         __syncthreads();
-        const bool split = todo < t.units;
+        const bool split = a.cluster ? a.cluster > 1 : todo < t.units;
+        // the CTA's own sum of row r, where a cluster joins: behind the O of a warp
+        auto sum_row = [&](int r) {
+            constexpr int PER = R / WARPS;
+            return reinterpret_cast<float *>(sh.ring[r / PER]) + (R + r % PER) * Sh::kRed;
+        };
         float *part = a.part + (2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0)) * (R * (DP + 2));
         for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
             const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
@@ -464,7 +495,10 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
             }
             if (d >= a.dim) continue;
-            if (split) {
+            if (split && a.cluster) {
+                *reinterpret_cast<float4 *>(sum_row(r) + d) = v;
+                if (d == 0) sh.wm[r] = mx, sh.wl[r] = ls;
+            } else if (split) {
                 *reinterpret_cast<float4 *>(part + r * DP + d) = v;
                 if (d == 0) part[R * DP + r] = mx, part[R * DP + R + r] = ls;
             } else {
@@ -472,8 +506,38 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             }
         }
 
-        // ---- a split tile: the last CTA to arrive adds the parts in key order
-        if (split) {
+        if (split && a.cluster) {
+            // ---- a cluster: each CTA adds its share of the outputs over the ranks, in key order
+            __syncthreads();
+            cluster_sync_all();
+            const int rank = cta % a.cluster, outs = t.rows * (DP / 4);
+            for (int i = outs * rank / a.cluster + tid; i < outs * (rank + 1) / a.cluster; i += THREADS) {
+                const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+                if (d >= a.dim) continue;
+                const uint32_t am = smem_u32(&sh.wm[r]), al = smem_u32(&sh.wl[r]), av = smem_u32(sum_row(r) + d);
+                float pm[kMaxCluster], mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < a.cluster) {
+                        pm[c] = ld_shared_cluster_f32(map_shared_rank(am, c));
+                        mx = fmaxf(mx, pm[c]);
+                    }
+                float4 v = make_float4(0, 0, 0, 0);
+                float ls = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < a.cluster) {
+                        const float f = weight(pm[c], mx);
+                        const float4 x = ld_shared_cluster_v4(map_shared_rank(av, c));
+                        ls += f * ld_shared_cluster_f32(map_shared_rank(al, c));
+                        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+                    }
+                finish_row(a, t, head, r, d, v, mx, ls, kShift);
+            }
+            __syncthreads();
+            cluster_sync_all();   // nobody leaves while its memory is read
+        } else if (split) {
+            // ---- a split tile: the last CTA to arrive adds the parts in key order
             const int c0 = share_owner(total, n, u0), c1 = share_owner(total, n, u0 + t.units - 1);
             __threadfence();
             __syncthreads();
@@ -502,6 +566,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 }
             }
         }
+        if (a.cluster) break;   // one tile per cluster (a rank's share of it may be empty)
         u += todo;
         __syncthreads();   // the tile's shared data is done with
     }

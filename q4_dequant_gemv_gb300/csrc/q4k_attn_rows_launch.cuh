@@ -8,6 +8,8 @@
 namespace q4k {
 namespace attn {
 
+constexpr double kSplitCost = 12.0;
+
 template <int CT, int PARTS, int NT, int DP, bool TMA>
 static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
@@ -22,31 +24,48 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     if (TMA && !encode_cache(&maps, a, CT, kBlock)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
     const int64_t units = (a.capacity + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
-    const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
-    const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
+
+    // A cluster of S CTAs per tile and cache head joins through its shared
+    // memory: one launch, no scratch.  The split over all CTAs balances ragged
+    // lengths and a few long sequences, but its scratch, its tickets and the join
+    // through memory cost about kSplitCost units of one CTA's time.
+    const int64_t items = a.kv_heads * std::max<int64_t>(a.batch, (static_cast<int64_t>(a.tokens) * a.group + R - 1) / R);
+    int S = kMaxCluster;
+    while (S > 1 && (S > units || items * S > l.sms)) S /= 2;
+    const int64_t waves = (items * S + l.sms - 1) / l.sms;
+    const double by_cluster = static_cast<double>(waves) * ((units + S - 1) / S);
+    const double by_split = static_cast<double>(items) * units / l.sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = Sp::kThreads;
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = l.stream;
+    if (by_cluster <= by_split + kSplitCost && static_cast<int64_t>(a.slots) * a.kv_heads * S < (1 << 24)) {
+        a.cluster = S;
+        cfg.gridDim = static_cast<unsigned>(a.slots * a.kv_heads * S);
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = S, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, maps, a);
+    }
+    const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
+    const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
     const size_t head = (grid * sizeof(unsigned int) + 255) / 256 * 256;
     void *scratch = nullptr;
-    if (units > 1) {
-        const size_t bytes = head + static_cast<size_t>(grid) * 2 * R * (DP + 2) * sizeof(float);
-        cudaError_t e = cudaMallocAsync(&scratch, bytes, l.stream);
-        if (e != cudaSuccess) return e;
-        e = cudaMemsetAsync(scratch, 0, grid * sizeof(unsigned int), l.stream);
-        if (e != cudaSuccess) {
-            (void)cudaFreeAsync(scratch, l.stream);
-            return e;
-        }
+    cudaError_t e = cudaMallocAsync(&scratch, head + static_cast<size_t>(grid) * 2 * R * (DP + 2) * sizeof(float), l.stream);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(scratch, 0, grid * sizeof(unsigned int), l.stream);
+    if (e == cudaSuccess) {
         a.ticket = static_cast<unsigned int *>(scratch);
         a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
+        cfg.gridDim = static_cast<unsigned>(grid);
+        e = cudaLaunchKernelEx(&cfg, kern, maps, a);
     }
-    kern<<<grid, Sp::kThreads, kSmem, l.stream>>>(maps, a);
-    cudaError_t e = cudaGetLastError();
-    if (scratch) {
-        const cudaError_t f = cudaFreeAsync(scratch, l.stream);
-        if (e == cudaSuccess) e = f;
-    }
-    return e;
+    const cudaError_t f = cudaFreeAsync(scratch, l.stream);
+    return e == cudaSuccess ? f : e;
 }
 
 template <int CT, int PARTS, int NT, int DP>
