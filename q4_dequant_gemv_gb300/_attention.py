@@ -20,8 +20,25 @@ _APPEND = struct.Struct("@4P 8q 2P 3q 4i")
 _ATTENTION = struct.Struct("@3P 4q 2q 3P 2f 4i")
 
 
-def _stream(stream):
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
+_lib = None
+# The handle of a device's current stream, without building a Stream object around it (3 us a call).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _load():
+    global _lib
+    from . import lib
+    _lib = lib()
+    return _lib
+
+
+def _raise(fn, status):
+    from . import _check
+    _check(fn, status)
+
+
+def _stream(stream, t):
+    return _current(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _rows(t, name, heads=None, dim=None, tokens=None):
@@ -124,7 +141,6 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, *, scaling=None, fact
     scaling: None, "linear" (positions divided by factor), "base" (the base grows with factor), "ramp" (slow pairs
     interpolated, fast ones kept, a ramp between the pairs that turn `low` and `high` times over orig_len positions:
     1 and 32 unless given; magnitude 0.1 ln(factor) + 1 unless given) or "bands" (the same by wavelength: 1 and 4)."""
-    from . import _check, lib
     if scaling not in _SCALING:
         raise ValueError(f"scaling must be one of {list(_SCALING)}")
     low = 1.0 if low is None else low
@@ -136,10 +152,11 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, *, scaling=None, fact
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
-        s = _stream(stream)
         table = torch.empty((rows, rot), dtype=torch.float32, device=device)
         args = _SCALE.pack(base, factor, orig_len, low, high, magnitude, _SCALING[scaling], 0)
-        _check("q4k_rope_table", lib().q4k_rope_table(table.data_ptr(), rows, rot, args, s))
+        st = (_lib or _load()).q4k_rope_table(table.data_ptr(), rows, rot, args, _stream(stream, table))
+        if st:
+            _raise("q4k_rope_table", st)
         if stream is not None:
             table.record_stream(stream)
     return table
@@ -159,7 +176,6 @@ def _out(out, name, shape, dtype, device, stream):
 def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, stream=None):
     """y [tokens, heads, dim] = x with the first table.shape[1] elements of each head turned by row pos[token] of the
     table; pairs (i, i + rot/2), or (2i, 2i+1) if interleaved.  y may be x."""
-    from . import _check, lib
     xp, xc, n, h, d, xt, xh = _rows(x, "x")
     tp, rows, rot = _turn(table, d)
     pp = _array(pos, "pos", torch.int32, n)
@@ -168,9 +184,9 @@ def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, st
     y = _out(y, "y", (n, h, d), out_dtype or (x.dtype if y is None else None), x.device, stream)
     yp, yc, _, _, _, yt, yh = _rows(y, "y", h, d, n)
     args = _ROPE.pack(xp, yp, pp, tp, n, h, d, rot, rows, xt, xh, yt, yh, xc, yc, 1 if interleaved else 0, 0)
-    st = lib().q4k_rope(args, _stream(stream))
+    st = (_lib or _load()).q4k_rope(args, _stream(stream, x))
     if st:
-        _check("q4k_rope", st)
+        _raise("q4k_rope", st)
     return y
 
 
@@ -180,7 +196,6 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
     [pages, page size, heads, dim] (any strides).  Rows seq_start[b] .. seq_start[b+1]-1 are the last new tokens of
     sequence b, whose cache holds kv_len[b] positions with them.  q [tokens, q heads, dim], where given, is turned too:
     returns q_out (of q_dtype, or q's type), else None."""
-    from . import _check, lib
     kp, kc, n, h, d, kt, kh = _rows(k, "k")
     vp, vc, _, _, _, vt, vh = _rows(v, "v", h, d, n)
     if vc != kc:
@@ -199,9 +214,9 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
         raise ValueError("q_out without q")
     args = _APPEND.pack(kp, vp, qp, op, kt, kh, vt, vh, qts, qhs, ots, ohs, pp, tp, rows, rot, qh, kc, qc, oc,
                         1 if interleaved else 0)
-    st = lib().q4k_kv_append(cache, args, _stream(stream))
+    st = (_lib or _load()).q4k_kv_append(cache, args, _stream(stream, k))
     if st:
-        _check("q4k_kv_append", st)
+        _raise("q4k_kv_append", st)
     return q_out
 
 
@@ -213,7 +228,6 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None
     max(0, kv_start[t], p + 1 - window) <= j < max(p + 1, prefix_len[b]), or < kv_len[b] if not causal.
     scale: 1/sqrt(dim) unless given; softcap > 0: scores softcap * tanh(s / softcap); slopes fp32 [q heads]: minus
     slopes[h] * |p - j|; lse: fp32 [tokens, q heads], filled with the rows' log-sum-exp."""
-    from . import _check, lib
     qp, qc, n, h, d, qt, qh = _rows(q, "q")
     cache, ch, cd, _ = _cache(k_cache, v_cache, page_table, seq_start, kv_len, n)
     if cd != d or ch < 1 or h % ch:
@@ -232,7 +246,7 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None
                            _array(prefix_len, "prefix_len", torch.int32, batch),
                            _array(kv_start, "kv_start", torch.int32, n),
                            1.0 / math.sqrt(d) if scale is None else scale, softcap, qc, oc, 1 if causal else 0, 0)
-    st = lib().q4k_paged_attention(cache, args, _stream(stream))
+    st = (_lib or _load()).q4k_paged_attention(cache, args, _stream(stream, q))
     if st:
-        _check("q4k_paged_attention", st)
+        _raise("q4k_paged_attention", st)
     return out

@@ -7,10 +7,14 @@
 // value against 4 to 8 bytes moved: bound by memory (or, for a few tokens, by
 // the chain of dependent index loads).
 //
-// One CTA per token.  A thread owns one unit of a head (8 pairs, or 16 copied
-// elements) and walks the heads, so a table row is loaded once per thread and
-// not once per head; all data moves in 16-byte accesses where rows are 16-byte
-// aligned and the sizes are multiples of 16, element by element otherwise.
+// A token's heads (of q, k and v alike) are cut into units of 8 pairs or 16
+// copied elements, a unit per thread, in as many warps as that takes; small
+// tokens share a CTA.  The data's loads are issued before the chain of index
+// loads (sequence, length, page and table row) that the stores wait for, so a
+// call needs three dependent trips to memory; warps find their sequence by
+// themselves, and nothing synchronises a CTA.  All data moves in 16-byte
+// accesses where rows are 16-byte aligned and the sizes are multiples of 16,
+// element by element otherwise.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,7 +47,7 @@ bool clear_rope_error()
 namespace rope {
 
 constexpr int kMaxRot = 512;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 struct Freqs {
     double f[kMaxRot / 2];
@@ -64,12 +68,13 @@ __global__ void __launch_bounds__(kThreads) table_kernel(float *table, int64_t r
     }
 }
 
-// A [heads][dim] row per token, source and destination.
-struct Rows {
+// Heads of one tensor: source and destination of a token.
+struct Part {
     const void *x;
     void *y;
-    int64_t xt, xh, yt, yh;   // strides in elements (yt unused for the cache)
+    int64_t xt, xh, yt, yh;   // strides in elements (yt: of a token, or unused for the cache)
     int heads, xtype, ytype;
+    int rot;                  // turned elements of a head (0: copied)
 };
 
 __device__ __forceinline__ void load8(const void *p, int type, int64_t i, float (&f)[8])
@@ -116,137 +121,184 @@ __device__ __forceinline__ void store1(void *p, int type, int64_t i, float v)
     else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// One token's heads of one tensor, by the calling CTA.  x and y already point
-// at the token's row.  rot = 0 copies.  Wide path: units of 16 elements, unit u
-// < rot/16 turns pairs 8u..8u+7, the others copy elements 16u..16u+15.
-template <bool WIDE>
-__device__ __forceinline__ void turn_rows(const Rows &r, int64_t x0, int64_t y0, int dim, int rot, int inter,
-                                          const float *trow)
-{
-    const int half = rot >> 1;
-    if (WIDE) {
-        const int units = (dim + 15) >> 4, turned = rot >> 4;
-        const int lanes = kThreads / units;   // heads in flight (units <= 64 on this path)
-        const int u = threadIdx.x % units;
-        int h = threadIdx.x / units;
-        if (h >= lanes) return;
-        if (u < turned) {
-            float c[8], s[8];
-            load8(trow, Q4K_F32, 8 * u, c);
-            load8(trow, Q4K_F32, half + 8 * u, s);
-            const int ia = inter ? 16 * u : 8 * u, ib = inter ? ia + 8 : ia + half;
-            for (; h < r.heads; h += lanes) {
-                float a[8], b[8], p[8], q[8];
-                load8(r.x, r.xtype, x0 + h * r.xh + ia, a);
-                load8(r.x, r.xtype, x0 + h * r.xh + ib, b);
-                if (inter) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[2 * j] = a[2 * j] * c[j] - a[2 * j + 1] * s[j];
-                        p[2 * j + 1] = a[2 * j] * s[j] + a[2 * j + 1] * c[j];
-                        q[2 * j] = b[2 * j] * c[4 + j] - b[2 * j + 1] * s[4 + j];
-                        q[2 * j + 1] = b[2 * j] * s[4 + j] + b[2 * j + 1] * c[4 + j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        p[j] = a[j] * c[j] - b[j] * s[j];
-                        q[j] = a[j] * s[j] + b[j] * c[j];
-                    }
-                }
-                store8(r.y, r.ytype, y0 + h * r.yh + ia, p);
-                store8(r.y, r.ytype, y0 + h * r.yh + ib, q);
-            }
-        } else {
-            const bool two = 16 * u + 16 <= dim;
-            for (; h < r.heads; h += lanes) {
-                float a[8], b[8];
-                load8(r.x, r.xtype, x0 + h * r.xh + 16 * u, a);
-                if (two) load8(r.x, r.xtype, x0 + h * r.xh + 16 * u + 8, b);
-                store8(r.y, r.ytype, y0 + h * r.yh + 16 * u, a);
-                if (two) store8(r.y, r.ytype, y0 + h * r.yh + 16 * u + 8, b);
-            }
-        }
-    } else {
-        const int per = half + (dim - rot);   // pairs, then copied elements
-        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(per) * r.heads; i += kThreads) {
-            const int h = static_cast<int>(i / per), u = static_cast<int>(i - static_cast<int64_t>(h) * per);
-            const int64_t x = x0 + h * r.xh, y = y0 + h * r.yh;
-            if (u < half) {
-                const int ia = inter ? 2 * u : u, ib = inter ? ia + 1 : u + half;
-                const float c = trow[u], s = trow[half + u];
-                const float a = load1(r.x, r.xtype, x + ia), b = load1(r.x, r.xtype, x + ib);
-                store1(r.y, r.ytype, y + ia, a * c - b * s);
-                store1(r.y, r.ytype, y + ib, a * s + b * c);
-            } else {
-                const int d = rot + (u - half);
-                store1(r.y, r.ytype, y + d, load1(r.x, r.xtype, x + d));
-            }
-        }
-    }
-}
-
-template <bool WIDE>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Rows r, const int32_t *pos, const float *table,
-                                                        int64_t table_rows, int dim, int rot, int inter)
-{
-    const int64_t t = blockIdx.x;
-    const float *trow = nullptr;
-    if (rot) {
-        const int p = pos[t];
-        if (p < 0 || p >= table_rows) {
-            if (threadIdx.x == 0) atomicOr(&g_rope_error, 4u);
-            return;
-        }
-        trow = table + static_cast<int64_t>(p) * rot;
-    }
-    turn_rows<WIDE>(r, t * r.xt, t * r.yt, dim, rot, inter, trow);
-}
-
-struct AppendArgs {
-    Rows q, k, v;
+struct TokenArgs {
+    Part part[3];             // rope: one; append: keys, values, queries (heads = 0: absent)
     int64_t k_page, k_slot, v_page, v_slot;
     int64_t pages, page_size, table_stride, max_pages, table_rows;
     const int32_t *page_table, *seq_start, *kv_len, *pos;
     const float *table;
     int batch, tokens, dim, rot, inter;
+    int units, items;         // per head, per token
+    int warps;                // of a token
 };
 
-// blockIdx.x = token.  The CTA finds its sequence (one comparison per thread and
-// 256 sequences), then its slot, and writes q_out, the key and the value.
-template <bool WIDE>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a)
+// The last sequence that starts at or before token t (-1: none), by a whole warp
+// in steps of 32-way division.
+__device__ __forceinline__ int find_sequence(const int32_t *start, int batch, int t)
 {
-    __shared__ int s_seq, s_first, s_end;
-    const int t = blockIdx.x;
-    if (threadIdx.x == 0) s_seq = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-        const int lo = a.seq_start[b], hi = a.seq_start[b + 1];
-        if (t >= lo && t < hi) s_seq = b, s_first = lo, s_end = hi;
+    int lo = 0, n = batch;    // the answer is lo - 1 or one of [lo, lo + n)
+    const int lane = threadIdx.x & 31;
+    while (true) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const bool below = i < n && start[lo + i] <= t;
+        const int k = __popc(__ballot_sync(0xffffffffu, below));
+        if (k == 0) return lo - 1;
+        const int skip = (k - 1) * step;
+        lo += skip;
+        if (step == 1) return lo;
+        n = min(step, n - skip);
     }
-    __syncthreads();
-    const int b = s_seq;
-    if (b < 0) return;
-    // a token of a sequence outside the call's rows, or before position 0
-    const int64_t p = static_cast<int64_t>(a.kv_len[b]) - (s_end - s_first) + (t - s_first);
-    bool ok = s_first >= 0 && s_end <= a.tokens && p >= 0 && p / a.page_size < a.max_pages;
-    const int64_t row = a.rot ? (a.pos ? static_cast<int64_t>(a.pos[t]) : p) : 0;
-    if (a.rot && (row < 0 || row >= a.table_rows)) ok = false;
-    int64_t page = 0;
-    if (ok) {
-        page = a.page_table[b * a.table_stride + p / a.page_size];
-        ok = page >= 0 && page < a.pages;
+}
+
+struct Unit {
+    int part, head, ia, ib;   // tensor, head, first elements of its two halves
+    bool turned, two;         // two: the second half exists
+};
+
+__device__ __forceinline__ Unit unit_of(const TokenArgs &a, int i)
+{
+    Unit u;
+    int h = i / a.units;
+    const int j = i - h * a.units;
+    u.part = 0;
+    while (h >= a.part[u.part].heads) h -= a.part[u.part].heads, ++u.part;
+    u.head = h;
+    const int rot = a.part[u.part].rot;
+    u.turned = 16 * j < rot;
+    u.ia = u.turned && !a.inter ? 8 * j : 16 * j;
+    u.ib = u.turned && !a.inter ? u.ia + (rot >> 1) : u.ia + 8;
+    u.two = u.ib < a.dim;
+    return u;
+}
+
+__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8], int inter)
+{
+    float p[8], q[8];
+    if (inter) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            p[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
+            p[2 * j + 1] = x[2 * j] * s[j] + x[2 * j + 1] * c[j];
+            q[2 * j] = y[2 * j] * c[4 + j] - y[2 * j + 1] * s[4 + j];
+            q[2 * j + 1] = y[2 * j] * s[4 + j] + y[2 * j + 1] * c[4 + j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            p[j] = x[j] * c[j] - y[j] * s[j];
+            q[j] = x[j] * s[j] + y[j] * c[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = p[j], y[j] = q[j];
+}
+
+template <bool WIDE, bool APPEND>
+__global__ void __launch_bounds__(kThreads) token_kernel(const TokenArgs a)
+{
+    const int w = threadIdx.x >> 5;
+    const int per = static_cast<int>(blockDim.x >> 5) / a.warps;   // tokens of a CTA
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + w / a.warps;
+    if (t >= a.tokens) return;
+    const int first = (w % a.warps) * 32 + (threadIdx.x & 31), step = a.warps * 32;
+
+    float x[8], y[8];
+    Unit u{};
+    if (WIDE && first < a.items) {
+        u = unit_of(a, first);
+        const Part &p = a.part[u.part];
+        load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ia, x);
+        if (u.two) load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ib, y);
+    }
+
+    // ---- where the token goes and which table row turns it
+    int64_t row = 0, at_k = 0, at_v = 0;
+    bool ok = true;
+    if (APPEND) {
+        const int b = find_sequence(a.seq_start, a.batch, static_cast<int>(t));
+        if (b < 0) return;
+        const int s0 = a.seq_start[b], s1 = a.seq_start[b + 1];
+        if (t >= s1) return;   // a token of no sequence
+        const int64_t p = static_cast<int64_t>(a.kv_len[b]) - s1 + t;
+        row = a.rot ? (a.pos ? static_cast<int64_t>(a.pos[t]) : p) : 0;
+        ok = s0 >= 0 && s1 <= a.tokens && p >= 0 && p / a.page_size < a.max_pages && (!a.rot || (row >= 0 && row < a.table_rows));
+        if (ok) {
+            const int64_t e = p / a.page_size, slot = p - e * a.page_size;
+            const int64_t page = a.page_table[b * a.table_stride + e];
+            ok = page >= 0 && page < a.pages;
+            at_k = page * a.k_page + slot * a.k_slot, at_v = page * a.v_page + slot * a.v_slot;
+        }
+    } else if (a.rot) {
+        row = a.pos[t];
+        ok = row >= 0 && row < a.table_rows;
     }
     if (!ok) {
-        if (threadIdx.x == 0) atomicOr(&g_rope_error, 4u);
+        if (first == 0) atomicOr(&g_rope_error, 4u);
         return;
     }
-    const int64_t slot = p % a.page_size;
-    const float *trow = a.rot ? a.table + row * a.rot : nullptr;
-    turn_rows<WIDE>(a.k, t * a.k.xt, page * a.k_page + slot * a.k_slot, a.dim, a.rot, a.inter, trow);
-    turn_rows<WIDE>(a.v, t * a.v.xt, page * a.v_page + slot * a.v_slot, a.dim, 0, 0, nullptr);
-    if (a.q.x) turn_rows<WIDE>(a.q, t * a.q.xt, t * a.q.yt, a.dim, a.rot, a.inter, trow);
+    const float *trow = a.table + row * a.rot;
+    auto dest = [&](int part) { return APPEND ? (part == 0 ? at_k : part == 1 ? at_v : t * a.part[2].yt) : t * a.part[0].yt; };
+
+    if (WIDE) {
+        for (int i = first; i < a.items; i += step) {
+            if (i != first) {
+                u = unit_of(a, i);
+                const Part &p = a.part[u.part];
+                load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ia, x);
+                if (u.two) load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ib, y);
+            }
+            const Part &p = a.part[u.part];
+            if (u.turned) {
+                const int j = a.inter ? u.ia >> 1 : u.ia;   // first pair
+                float c[8], s[8];
+                load8(trow, Q4K_F32, j, c);
+                load8(trow, Q4K_F32, (a.rot >> 1) + j, s);
+                turn(x, y, c, s, a.inter);
+            }
+            const int64_t o = dest(u.part) + u.head * p.yh;
+            store8(p.y, p.ytype, o + u.ia, x);
+            if (u.two) store8(p.y, p.ytype, o + u.ib, y);
+        }
+    } else {
+        // element by element: a head is its pairs, then its copied elements
+        for (int q = 0; q < (APPEND ? 3 : 1); ++q) {
+            const Part &p = a.part[q];
+            const int half = p.rot >> 1, each = half + (a.dim - p.rot);
+            for (int64_t i = first; i < static_cast<int64_t>(each) * p.heads; i += step) {
+                const int h = static_cast<int>(i / each), j = static_cast<int>(i - static_cast<int64_t>(h) * each);
+                const int64_t from = t * p.xt + h * p.xh, to = dest(q) + h * p.yh;
+                if (j < half) {
+                    const int ia = a.inter ? 2 * j : j, ib = a.inter ? ia + 1 : j + half;
+                    const float c = trow[j], s = trow[half + j];
+                    const float v = load1(p.x, p.xtype, from + ia), z = load1(p.x, p.xtype, from + ib);
+                    store1(p.y, p.ytype, to + ia, v * c - z * s);
+                    store1(p.y, p.ytype, to + ib, v * s + z * c);
+                } else {
+                    const int d = p.rot + (j - half);
+                    store1(p.y, p.ytype, to + d, load1(p.x, p.xtype, from + d));
+                }
+            }
+        }
+    }
+}
+
+// Warps per token and tokens per CTA, then the launch.
+template <bool APPEND>
+static q4k_status launch_tokens(TokenArgs &a, bool wide, void *stream)
+{
+    int64_t heads = 0;
+    for (const Part &p : a.part) heads += p.heads;
+    a.units = (a.dim + 15) / 16;
+    const int64_t items = heads * (wide ? a.units : a.dim);
+    if (items > 0x7FFFFFFF) return Q4K_ERR_INVALID_ARG;
+    a.items = static_cast<int>(items);
+    const int64_t need = (items + 31) / 32, rounds = (need + kThreads / 32 - 1) / (kThreads / 32);
+    a.warps = static_cast<int>((need + rounds - 1) / rounds);
+    const int per = a.warps >= 4 ? 1 : 4 / a.warps;   // tokens of a CTA: four warps or more
+    const int64_t grid = (static_cast<int64_t>(a.tokens) + per - 1) / per;
+    auto kern = wide ? token_kernel<true, APPEND> : token_kernel<false, APPEND>;
+    kern<<<static_cast<unsigned>(grid), a.warps * per * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
 static bool good_type(int t) { return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16; }
@@ -326,14 +378,16 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
         return Q4K_ERR_MISALIGNED;
     q4k_status st = check_device(nullptr);
     if (st != Q4K_OK || a->tokens == 0) return st;
-    const Rows r{a->x, a->y, a->x_token_stride, a->x_head_stride, a->y_token_stride, a->y_head_stride,
-                 static_cast<int>(a->heads), a->x_type, a->y_type};
-    const bool wide = a->dim % 8 == 0 && a->dim <= 1024 && a->rot % 16 == 0 && !off(a->table, 16) &&
+    TokenArgs p{};
+    p.part[0] = Part{a->x, a->y, a->x_token_stride, a->x_head_stride, a->y_token_stride, a->y_head_stride,
+                     static_cast<int>(a->heads), a->x_type, a->y_type, static_cast<int>(a->rot)};
+    p.pos = a->pos, p.table = a->table, p.table_rows = a->table_rows;
+    p.tokens = static_cast<int>(a->tokens), p.dim = static_cast<int>(a->dim), p.rot = static_cast<int>(a->rot);
+    p.inter = a->interleaved;
+    const Part &r = p.part[0];
+    const bool wide = a->dim % 8 == 0 && a->rot % 16 == 0 && !off(a->table, 16) &&
                       wide_rows(a->x, a->x_type, r.xt, r.xh) && wide_rows(a->y, a->y_type, r.yt, r.yh);
-    auto kern = wide ? rope_kernel<true> : rope_kernel<false>;
-    kern<<<static_cast<unsigned>(a->tokens), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        r, a->pos, a->table, a->table_rows, static_cast<int>(a->dim), static_cast<int>(a->rot), a->interleaved);
-    return cudaGetLastError() == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+    return launch_tokens<false>(p, wide, stream);
 }
 
 q4k_status check_cache(const q4k_paged_cache *c)
@@ -369,28 +423,25 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
         return Q4K_ERR_MISALIGNED;
     st = check_device(nullptr);
     if (st != Q4K_OK || !some) return st;
-    AppendArgs p{};
-    const int heads = static_cast<int>(c->heads);
-    p.k = Rows{a->k, c->k, a->k_token_stride, a->k_head_stride, 0, c->k_head_stride, heads, a->kv_type, c->type};
-    p.v = Rows{a->v, c->v, a->v_token_stride, a->v_head_stride, 0, c->v_head_stride, heads, a->kv_type, c->type};
+    TokenArgs p{};
+    const int heads = static_cast<int>(c->heads), rot = static_cast<int>(a->rot);
+    p.part[0] = Part{a->k, c->k, a->k_token_stride, a->k_head_stride, 0, c->k_head_stride, heads, a->kv_type, c->type, rot};
+    p.part[1] = Part{a->v, c->v, a->v_token_stride, a->v_head_stride, 0, c->v_head_stride, heads, a->kv_type, c->type, 0};
     if (a->q)
-        p.q = Rows{a->q, a->q_out, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride,
-                   static_cast<int>(a->q_heads), a->q_type, a->q_out_type};
+        p.part[2] = Part{a->q, a->q_out, a->q_token_stride, a->q_head_stride, a->q_out_token_stride,
+                         a->q_out_head_stride, static_cast<int>(a->q_heads), a->q_type, a->q_out_type, rot};
     p.k_page = c->k_page_stride, p.k_slot = c->k_slot_stride, p.v_page = c->v_page_stride, p.v_slot = c->v_slot_stride;
     p.pages = c->pages, p.page_size = c->page_size, p.table_stride = c->page_table_stride, p.max_pages = c->max_pages;
     p.page_table = c->page_table, p.seq_start = c->seq_start, p.kv_len = c->kv_len, p.pos = a->pos;
     p.table = a->table, p.table_rows = a->table_rows;
     p.batch = static_cast<int>(c->batch), p.tokens = static_cast<int>(c->tokens), p.dim = static_cast<int>(c->dim);
-    p.rot = static_cast<int>(a->rot), p.inter = a->interleaved;
-    bool wide = c->dim % 8 == 0 && c->dim <= 1024 && a->rot % 16 == 0 && !off(a->table, 16) &&
-                wide_rows(a->k, a->kv_type, p.k.xt, p.k.xh) && wide_rows(a->v, a->kv_type, p.v.xt, p.v.xh) &&
-                wide_rows(c->k, c->type, p.k_page, p.k_slot) && wide_rows(c->v, c->type, p.v_page, p.v_slot) &&
-                p.k.yh % 8 == 0 && p.v.yh % 8 == 0;
-    if (a->q)
-        wide = wide && wide_rows(a->q, a->q_type, p.q.xt, p.q.xh) && wide_rows(a->q_out, a->q_out_type, p.q.yt, p.q.yh);
-    auto kern = wide ? append_kernel<true> : append_kernel<false>;
-    kern<<<static_cast<unsigned>(c->tokens), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+    p.rot = rot, p.inter = a->interleaved;
+    const Part &k = p.part[0], &v = p.part[1], &q = p.part[2];
+    bool wide = c->dim % 8 == 0 && rot % 16 == 0 && !off(a->table, 16) && wide_rows(a->k, a->kv_type, k.xt, k.xh) &&
+                wide_rows(a->v, a->kv_type, v.xt, v.xh) && wide_rows(c->k, c->type, p.k_page, p.k_slot) &&
+                wide_rows(c->v, c->type, p.v_page, p.v_slot) && k.yh % 8 == 0 && v.yh % 8 == 0;
+    if (a->q) wide = wide && wide_rows(a->q, a->q_type, q.xt, q.xh) && wide_rows(a->q_out, a->q_out_type, q.yt, q.yh);
+    return launch_tokens<true>(p, wide, stream);
 }
 
 }  // namespace q4k
