@@ -7,13 +7,13 @@
 // value against 4 to 8 bytes moved: bound by memory (or, for a few tokens, by
 // the chain of dependent index loads).
 //
-// A token's heads (of q, k and v alike) are cut into units of 8 pairs or 16
+// A token's heads (of q, k and v alike) are cut into units of 4 pairs or 8
 // copied elements, a unit per thread, in as many warps as that takes; small
-// tokens share a CTA.  The data's loads are issued before the chain of index
-// loads (sequence, length, page and table row) that the stores wait for, so a
-// call needs three dependent trips to memory; warps find their sequence by
-// themselves, and nothing synchronises a CTA.  All data moves in 16-byte
-// accesses where rows are 16-byte aligned and the sizes are multiples of 16,
+// tokens share a CTA.  With many tokens a thread takes the same unit of four of
+// them: all their data is on its way before the chain of index loads (sequence,
+// length, page, table row) begins, and four lanes of each warp follow the four
+// chains at once.  Nothing synchronises a CTA.  Data moves in accesses of four
+// elements where rows are 16-byte aligned and the sizes are multiples of 8,
 // element by element otherwise.
 
 #include <cuda_bf16.h>
@@ -47,7 +47,8 @@ bool clear_rope_error()
 namespace rope {
 
 constexpr int kMaxRot = 512;
-constexpr int kThreads = 512;
+constexpr int kThreads = 128;   // of a CTA at most
+constexpr int kTok = 4;         // tokens of a thread in large calls
 
 struct Freqs {
     double f[kMaxRot / 2];
@@ -77,33 +78,58 @@ struct Part {
     int rot;                  // turned elements of a head (0: copied)
 };
 
-__device__ __forceinline__ void load8(const void *p, int type, int64_t i, float (&f)[8])
+template <int TYPE>
+__device__ __forceinline__ void convert4(const uint4 &r, float (&f)[4])
 {
-    if (type == Q4K_F32) {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 a = s[0], b = s[1];
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    if constexpr (TYPE == Q4K_F32) {
+        f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
     } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 t = attn::unpack2(w[j], type);
-            f[2 * j] = t.x, f[2 * j + 1] = t.y;
-        }
+        const float2 a = attn::unpack2(r.x, TYPE), b = attn::unpack2(r.y, TYPE);
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
     }
 }
 
-__device__ __forceinline__ void store8(void *p, int type, int64_t i, const float (&f)[8])
+template <int TYPE>
+__device__ __forceinline__ void store4(uint8_t *p, const float (&f)[4])
 {
-    if (type == Q4K_F32) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        d[0] = make_float4(f[0], f[1], f[2], f[3]);
-        d[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-            make_uint4(attn::pack2(f[0], f[1], type), attn::pack2(f[2], f[3], type), attn::pack2(f[4], f[5], type),
-                       attn::pack2(f[6], f[7], type));
+    if constexpr (TYPE == Q4K_F32) *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(attn::pack2(f[0], f[1], TYPE), attn::pack2(f[2], f[3], TYPE));
+}
+
+// TOK tokens' unit: converted, turned by their c and s (kind 1: halves apart,
+// kind 2: neighbours, 0: copied) and stored where `to` is not null.
+template <int XT, int YT, int TOK>
+__device__ __forceinline__ void finish(const uint4 (&ra)[TOK], const uint4 (&rb)[TOK], const float4 (&c)[TOK],
+                                       const float4 (&s)[TOK], uint8_t *const (&to)[TOK], int apart, int kind)
+{
+#pragma unroll
+    for (int k = 0; k < TOK; ++k) {
+        float x[4], y[4], p[4], q[4];
+        convert4<XT>(ra[k], x);
+        convert4<XT>(rb[k], y);
+        const float cc[4] = {c[k].x, c[k].y, c[k].z, c[k].w}, ss[4] = {s[k].x, s[k].y, s[k].z, s[k].w};
+        if (kind == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p[j] = x[j] * cc[j] - y[j] * ss[j];
+                q[j] = x[j] * ss[j] + y[j] * cc[j];
+            }
+        } else if (kind == 2) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                p[j] = x[j] * cc[j / 2] - x[j + 1] * ss[j / 2];
+                p[j + 1] = x[j] * ss[j / 2] + x[j + 1] * cc[j / 2];
+                q[j] = y[j] * cc[2 + j / 2] - y[j + 1] * ss[2 + j / 2];
+                q[j + 1] = y[j] * ss[2 + j / 2] + y[j + 1] * cc[2 + j / 2];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = x[j], q[j] = y[j];
+        }
+        if (to[k]) {
+            store4<YT>(to[k], p);
+            store4<YT>(to[k] + apart * (YT == Q4K_F32 ? 4 : 2), q);
+        }
     }
 }
 
@@ -132,172 +158,195 @@ struct TokenArgs {
     int warps;                // of a token
 };
 
-// The last sequence that starts at or before token t (-1: none), by a whole warp
-// in steps of 32-way division.
-__device__ __forceinline__ int find_sequence(const int32_t *start, int batch, int t)
-{
-    int lo = 0, n = batch;    // the answer is lo - 1 or one of [lo, lo + n)
-    const int lane = threadIdx.x & 31;
-    while (true) {
-        const int step = (n + 31) / 32, i = lane * step;
-        const bool below = i < n && start[lo + i] <= t;
-        const int k = __popc(__ballot_sync(0xffffffffu, below));
-        if (k == 0) return lo - 1;
-        const int skip = (k - 1) * step;
-        lo += skip;
-        if (step == 1) return lo;
-        n = min(step, n - skip);
-    }
-}
-
-struct Unit {
-    int part, head, ia, ib;   // tensor, head, first elements of its two halves
-    bool turned, two;         // two: the second half exists
+// Where a token goes and which table row turns it.
+struct Place {
+    int row, page, slot;
+    int state;   // 0: belongs to no sequence, 1: every index is inside its buffer, 2: not so
 };
 
-__device__ __forceinline__ Unit unit_of(const TokenArgs &a, int i)
+template <bool APPEND>
+__device__ __forceinline__ Place place_of(const TokenArgs &a, int t)
 {
-    Unit u;
-    int h = i / a.units;
-    const int j = i - h * a.units;
-    u.part = 0;
-    while (h >= a.part[u.part].heads) h -= a.part[u.part].heads, ++u.part;
-    u.head = h;
-    const int rot = a.part[u.part].rot;
-    u.turned = 16 * j < rot;
-    u.ia = u.turned && !a.inter ? 8 * j : 16 * j;
-    u.ib = u.turned && !a.inter ? u.ia + (rot >> 1) : u.ia + 8;
-    u.two = u.ib < a.dim;
-    return u;
+    Place w{0, 0, 0, 1};
+    if (APPEND) {
+        int b = 0, e = a.batch;   // the last sequence that starts at or before t is b - 1 or in [b, e)
+        while (b < e) {
+            const int m = (b + e) >> 1;
+            if (a.seq_start[m] <= t) b = m + 1; else e = m;
+        }
+        --b;
+        const int s0 = b < 0 ? 0 : a.seq_start[b], s1 = b < 0 ? 0 : a.seq_start[b + 1];
+        if (t >= s1) {
+            w.state = 0;
+            return w;
+        }
+        const int64_t p = static_cast<int64_t>(a.kv_len[b]) - s1 + t;
+        const int64_t row = a.rot ? (a.pos ? static_cast<int64_t>(a.pos[t]) : p) : 0;
+        w.state = 2;
+        if (s0 < 0 || s1 > a.tokens || p < 0 || (a.rot && (row < 0 || row >= a.table_rows))) return w;
+        // (positions fit 32 bits, kv_len does)
+        const uint32_t n = static_cast<uint32_t>(p) / static_cast<uint32_t>(a.page_size);
+        if (n >= a.max_pages) return w;
+        w.row = static_cast<int>(row);
+        w.slot = static_cast<int>(static_cast<uint32_t>(p) - n * static_cast<uint32_t>(a.page_size));
+        w.page = a.page_table[b * a.table_stride + n];
+        if (w.page >= 0 && w.page < a.pages) w.state = 1;
+    } else if (a.rot) {
+        w.row = a.pos[t];
+        w.state = w.row >= 0 && w.row < a.table_rows ? 1 : 2;
+    }
+    return w;
 }
 
-__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8], int inter)
+// TOK consecutive tokens per thread: their data is loaded first; then lane j of
+// each warp places token j; then they are turned and stored.  Bound by memory
+// latency: one token a thread leaves too little in flight, eight spill, and
+// small CTAs even out the tail.  4097 tokens x 32 heads x 128 in bf16, half of
+// each head turned (68 MB): 16.2 us, 4.2 TB/s (a copy of the same size takes
+// 11.7); 2048 tokens of q, k and v from fp32 (58 MB): 14.9 us, 3.9 TB/s.  The
+// same with 512 threads of one token: 25 and 17 us; 256 of four: 17.4 and 14.9.
+template <bool APPEND, int TOK>
+__global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
 {
-    float p[8], q[8];
-    if (inter) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = w / a.warps;   // of TOK tokens, within the CTA
+    const int i = (blockIdx.y * a.warps + (w - group * a.warps)) * 32 + lane;
+    const int per = static_cast<int>(blockDim.x >> 5) / a.warps;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * per + group) * TOK;
+    if (t0 >= a.tokens) return;
+    const bool live = i < a.items;
+
+    // this thread's unit: tensor, head, its two halves of four elements
+    int h = (live ? i : 0) / a.units;
+    const int j = (live ? i : 0) - h * a.units;
+    int part = 0;
+    while (h >= a.part[part].heads) h -= a.part[part].heads, ++part;
+    const Part &p = a.part[part];
+    const bool turned = 8 * j < p.rot, split = turned && !a.inter;
+    const int ia = split ? 4 * j : 8 * j, apart = split ? p.rot >> 1 : 4;
+    const int xs = p.xtype == Q4K_F32 ? 4 : 2, ys = p.ytype == Q4K_F32 ? 4 : 2;
+
+    uint4 ra[TOK], rb[TOK];
+    const uint8_t *src = static_cast<const uint8_t *>(p.x) + (t0 * p.xt + h * p.xh + ia) * xs;
+    const int64_t next = p.xt * xs;   // bytes to the next token
+    // (as they lie in memory: a conversion next to its load would wait for it)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            p[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
-            p[2 * j + 1] = x[2 * j] * s[j] + x[2 * j + 1] * c[j];
-            q[2 * j] = y[2 * j] * c[4 + j] - y[2 * j + 1] * s[4 + j];
-            q[2 * j + 1] = y[2 * j] * s[4 + j] + y[2 * j + 1] * c[4 + j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            p[j] = x[j] * c[j] - y[j] * s[j];
-            q[j] = x[j] * s[j] + y[j] * c[j];
+    for (int k = 0; k < TOK; ++k) {
+        ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
+        if (live && t0 + k < a.tokens) {
+            const uint8_t *q = src + k * next;
+            if (xs == 4) {
+                ra[k] = *reinterpret_cast<const uint4 *>(q);
+                rb[k] = *reinterpret_cast<const uint4 *>(q + 4 * apart);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(q), v = *reinterpret_cast<const uint2 *>(q + 2 * apart);
+                ra[k] = make_uint4(u.x, u.y, 0, 0), rb[k] = make_uint4(v.x, v.y, 0, 0);
+            }
         }
     }
+
+    Place mine{0, 0, 0, 0};
+    if (lane < TOK && t0 + lane < a.tokens) mine = place_of<APPEND>(a, static_cast<int>(t0) + lane);
+    if (mine.state == 2 && i < TOK) atomicOr(&g_rope_error, 4u);
+
+    uint8_t *dst = static_cast<uint8_t *>(p.y) + (h * p.yh + ia) * ys;
+    const float *trow = a.table + (a.inter ? ia >> 1 : ia);
+    const int64_t per_page = (part ? a.v_page : a.k_page) * ys, per_slot = (part ? a.v_slot : a.k_slot) * ys;
+    float4 c[TOK], s[TOK];
+    uint8_t *to[TOK];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = p[j], y[j] = q[j];
+    for (int k = 0; k < TOK; ++k) {
+        const int row = __shfl_sync(0xffffffffu, mine.row, k);
+        const bool good = __shfl_sync(0xffffffffu, mine.state, k) == 1 && live;
+        c[k] = s[k] = make_float4(0, 0, 0, 0);
+        if (good && turned) {
+            const float *r = trow + static_cast<int64_t>(row) * a.rot;
+            c[k] = *reinterpret_cast<const float4 *>(r);
+            s[k] = *reinterpret_cast<const float4 *>(r + (a.rot >> 1));
+        }
+        int64_t o = (t0 + k) * p.yt * ys;
+        if (APPEND) {
+            const int page = __shfl_sync(0xffffffffu, mine.page, k), slot = __shfl_sync(0xffffffffu, mine.slot, k);
+            if (part < 2) o = page * per_page + slot * per_slot;
+        }
+        to[k] = good ? dst + o : nullptr;
+    }
+    const int kind = !turned ? 0 : split ? 1 : 2;
+    switch (3 * p.xtype + p.ytype) {
+        case 3 * Q4K_F32 + Q4K_F32: finish<Q4K_F32, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_F32 + Q4K_F16: finish<Q4K_F32, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_F32 + Q4K_BF16: finish<Q4K_F32, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_F16 + Q4K_F32: finish<Q4K_F16, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_F16 + Q4K_F16: finish<Q4K_F16, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_F16 + Q4K_BF16: finish<Q4K_F16, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_BF16 + Q4K_F32: finish<Q4K_BF16, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
+        case 3 * Q4K_BF16 + Q4K_F16: finish<Q4K_BF16, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        default: finish<Q4K_BF16, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind);
+    }
 }
 
-template <bool WIDE, bool APPEND>
-__global__ void __launch_bounds__(kThreads) token_kernel(const TokenArgs a)
+// Element by element, for rows and sizes that the wide accesses do not fit: a
+// head is its pairs, then its copied elements.
+template <bool APPEND>
+__global__ void __launch_bounds__(kThreads) narrow_kernel(const TokenArgs a)
 {
     const int w = threadIdx.x >> 5;
-    const int per = static_cast<int>(blockDim.x >> 5) / a.warps;   // tokens of a CTA
+    const int per = static_cast<int>(blockDim.x >> 5) / a.warps;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * per + w / a.warps;
     if (t >= a.tokens) return;
     const int first = (w % a.warps) * 32 + (threadIdx.x & 31), step = a.warps * 32;
-
-    float x[8], y[8];
-    Unit u{};
-    if (WIDE && first < a.items) {
-        u = unit_of(a, first);
-        const Part &p = a.part[u.part];
-        load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ia, x);
-        if (u.two) load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ib, y);
-    }
-
-    // ---- where the token goes and which table row turns it
-    int64_t row = 0, at_k = 0, at_v = 0;
-    bool ok = true;
-    if (APPEND) {
-        const int b = find_sequence(a.seq_start, a.batch, static_cast<int>(t));
-        if (b < 0) return;
-        const int s0 = a.seq_start[b], s1 = a.seq_start[b + 1];
-        if (t >= s1) return;   // a token of no sequence
-        const int64_t p = static_cast<int64_t>(a.kv_len[b]) - s1 + t;
-        row = a.rot ? (a.pos ? static_cast<int64_t>(a.pos[t]) : p) : 0;
-        ok = s0 >= 0 && s1 <= a.tokens && p >= 0 && p / a.page_size < a.max_pages && (!a.rot || (row >= 0 && row < a.table_rows));
-        if (ok) {
-            const int64_t e = p / a.page_size, slot = p - e * a.page_size;
-            const int64_t page = a.page_table[b * a.table_stride + e];
-            ok = page >= 0 && page < a.pages;
-            at_k = page * a.k_page + slot * a.k_slot, at_v = page * a.v_page + slot * a.v_slot;
-        }
-    } else if (a.rot) {
-        row = a.pos[t];
-        ok = row >= 0 && row < a.table_rows;
-    }
-    if (!ok) {
-        if (first == 0) atomicOr(&g_rope_error, 4u);
+    const Place at = place_of<APPEND>(a, static_cast<int>(t));
+    if (at.state != 1) {
+        if (at.state == 2 && first == 0) atomicOr(&g_rope_error, 4u);
         return;
     }
-    const float *trow = a.table + row * a.rot;
-    auto dest = [&](int part) { return APPEND ? (part == 0 ? at_k : part == 1 ? at_v : t * a.part[2].yt) : t * a.part[0].yt; };
-
-    if (WIDE) {
-        for (int i = first; i < a.items; i += step) {
-            if (i != first) {
-                u = unit_of(a, i);
-                const Part &p = a.part[u.part];
-                load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ia, x);
-                if (u.two) load8(p.x, p.xtype, t * p.xt + u.head * p.xh + u.ib, y);
-            }
-            const Part &p = a.part[u.part];
-            if (u.turned) {
-                const int j = a.inter ? u.ia >> 1 : u.ia;   // first pair
-                float c[8], s[8];
-                load8(trow, Q4K_F32, j, c);
-                load8(trow, Q4K_F32, (a.rot >> 1) + j, s);
-                turn(x, y, c, s, a.inter);
-            }
-            const int64_t o = dest(u.part) + u.head * p.yh;
-            store8(p.y, p.ytype, o + u.ia, x);
-            if (u.two) store8(p.y, p.ytype, o + u.ib, y);
-        }
-    } else {
-        // element by element: a head is its pairs, then its copied elements
-        for (int q = 0; q < (APPEND ? 3 : 1); ++q) {
-            const Part &p = a.part[q];
-            const int half = p.rot >> 1, each = half + (a.dim - p.rot);
-            for (int64_t i = first; i < static_cast<int64_t>(each) * p.heads; i += step) {
-                const int h = static_cast<int>(i / each), j = static_cast<int>(i - static_cast<int64_t>(h) * each);
-                const int64_t from = t * p.xt + h * p.xh, to = dest(q) + h * p.yh;
-                if (j < half) {
-                    const int ia = a.inter ? 2 * j : j, ib = a.inter ? ia + 1 : j + half;
-                    const float c = trow[j], s = trow[half + j];
-                    const float v = load1(p.x, p.xtype, from + ia), z = load1(p.x, p.xtype, from + ib);
-                    store1(p.y, p.ytype, to + ia, v * c - z * s);
-                    store1(p.y, p.ytype, to + ib, v * s + z * c);
-                } else {
-                    const int d = p.rot + (j - half);
-                    store1(p.y, p.ytype, to + d, load1(p.x, p.xtype, from + d));
-                }
+    const float *trow = a.table + static_cast<int64_t>(at.row) * a.rot;
+    for (int q = 0; q < (APPEND ? 3 : 1); ++q) {
+        const Part &p = a.part[q];
+        const int half = p.rot >> 1, each = half + (a.dim - p.rot);
+        const int64_t base = !APPEND || q == 2 ? t * p.yt
+                                               : at.page * (q ? a.v_page : a.k_page) + at.slot * (q ? a.v_slot : a.k_slot);
+        for (int64_t i = first; i < static_cast<int64_t>(each) * p.heads; i += step) {
+            const int h = static_cast<int>(i / each), j = static_cast<int>(i - static_cast<int64_t>(h) * each);
+            const int64_t from = t * p.xt + h * p.xh, to = base + h * p.yh;
+            if (j < half) {
+                const int ia = a.inter ? 2 * j : j, ib = a.inter ? ia + 1 : j + half;
+                const float c = trow[j], s = trow[half + j];
+                const float v = load1(p.x, p.xtype, from + ia), z = load1(p.x, p.xtype, from + ib);
+                store1(p.y, p.ytype, to + ia, v * c - z * s);
+                store1(p.y, p.ytype, to + ib, v * s + z * c);
+            } else {
+                const int d = p.rot + (j - half);
+                store1(p.y, p.ytype, to + d, load1(p.x, p.xtype, from + d));
             }
         }
     }
 }
 
-// Warps per token and tokens per CTA, then the launch.
+// Warps per token, tokens per thread and CTA, then the launch.
 template <bool APPEND>
-static q4k_status launch_tokens(TokenArgs &a, bool wide, void *stream)
+static q4k_status launch_tokens(TokenArgs &a, bool wide, int sms, void *stream)
 {
     int64_t heads = 0;
     for (const Part &p : a.part) heads += p.heads;
-    a.units = (a.dim + 15) / 16;
+    a.units = a.dim / 8;
     const int64_t items = heads * (wide ? a.units : a.dim);
     if (items > 0x7FFFFFFF) return Q4K_ERR_INVALID_ARG;
     a.items = static_cast<int>(items);
     const int64_t need = (items + 31) / 32, rounds = (need + kThreads / 32 - 1) / (kThreads / 32);
+    if (rounds > 65535) return Q4K_ERR_INVALID_ARG;
     a.warps = static_cast<int>((need + rounds - 1) / rounds);
-    const int per = a.warps >= 4 ? 1 : 4 / a.warps;   // tokens of a CTA: four warps or more
-    const int64_t grid = (static_cast<int64_t>(a.tokens) + per - 1) / per;
-    auto kern = wide ? token_kernel<true, APPEND> : token_kernel<false, APPEND>;
-    kern<<<static_cast<unsigned>(grid), a.warps * per * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const int per = a.warps >= 4 ? 1 : 4 / a.warps;   // token groups of a CTA: four warps or more
+    const int threads = a.warps * per * 32;
+    auto grid = [&](int tok) {
+        const int64_t each = static_cast<int64_t>(per) * tok;
+        return dim3(static_cast<unsigned>((a.tokens + each - 1) / each), static_cast<unsigned>(wide ? rounds : 1));
+    };
+    auto s = static_cast<cudaStream_t>(stream);
+    // several tokens a thread once that still fills the GPU (1024 threads an SM)
+    if (!wide) narrow_kernel<APPEND><<<grid(1), threads, 0, s>>>(a);
+    else if (static_cast<int64_t>(a.tokens) * need * 32 >= 1024LL * kTok * sms) wide_kernel<APPEND, kTok><<<grid(kTok), threads, 0, s>>>(a);
+    else wide_kernel<APPEND, 1><<<grid(1), threads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
@@ -376,7 +425,8 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
     if (a->tokens > 0 && (!a->x || !a->y || (a->rot && (!a->pos || !a->table)))) return Q4K_ERR_INVALID_ARG;
     if (off(a->x, size_of(a->x_type)) || off(a->y, size_of(a->y_type)) || off(a->pos, 4) || off(a->table, 4))
         return Q4K_ERR_MISALIGNED;
-    q4k_status st = check_device(nullptr);
+    int sms = 0;
+    q4k_status st = check_device(&sms);
     if (st != Q4K_OK || a->tokens == 0) return st;
     TokenArgs p{};
     p.part[0] = Part{a->x, a->y, a->x_token_stride, a->x_head_stride, a->y_token_stride, a->y_head_stride,
@@ -385,9 +435,9 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
     p.tokens = static_cast<int>(a->tokens), p.dim = static_cast<int>(a->dim), p.rot = static_cast<int>(a->rot);
     p.inter = a->interleaved;
     const Part &r = p.part[0];
-    const bool wide = a->dim % 8 == 0 && a->rot % 16 == 0 && !off(a->table, 16) &&
+    const bool wide = a->dim % 8 == 0 && a->rot % 8 == 0 && !off(a->table, 16) &&
                       wide_rows(a->x, a->x_type, r.xt, r.xh) && wide_rows(a->y, a->y_type, r.yt, r.yh);
-    return launch_tokens<false>(p, wide, stream);
+    return launch_tokens<false>(p, wide, sms, stream);
 }
 
 q4k_status check_cache(const q4k_paged_cache *c)
@@ -421,7 +471,8 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
     if (off(a->k, size_of(a->kv_type)) || off(a->v, size_of(a->kv_type)) || off(a->pos, 4) || off(a->table, 4) ||
         (a->q && (off(a->q, size_of(a->q_type)) || off(a->q_out, size_of(a->q_out_type)))))
         return Q4K_ERR_MISALIGNED;
-    st = check_device(nullptr);
+    int sms = 0;
+    st = check_device(&sms);
     if (st != Q4K_OK || !some) return st;
     TokenArgs p{};
     const int heads = static_cast<int>(c->heads), rot = static_cast<int>(a->rot);
@@ -437,11 +488,11 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
     p.batch = static_cast<int>(c->batch), p.tokens = static_cast<int>(c->tokens), p.dim = static_cast<int>(c->dim);
     p.rot = rot, p.inter = a->interleaved;
     const Part &k = p.part[0], &v = p.part[1], &q = p.part[2];
-    bool wide = c->dim % 8 == 0 && rot % 16 == 0 && !off(a->table, 16) && wide_rows(a->k, a->kv_type, k.xt, k.xh) &&
+    bool wide = c->dim % 8 == 0 && rot % 8 == 0 && !off(a->table, 16) && wide_rows(a->k, a->kv_type, k.xt, k.xh) &&
                 wide_rows(a->v, a->kv_type, v.xt, v.xh) && wide_rows(c->k, c->type, p.k_page, p.k_slot) &&
                 wide_rows(c->v, c->type, p.v_page, p.v_slot) && k.yh % 8 == 0 && v.yh % 8 == 0;
     if (a->q) wide = wide && wide_rows(a->q, a->q_type, q.xt, q.xh) && wide_rows(a->q_out, a->q_out_type, q.yt, q.yh);
-    return launch_tokens<true>(p, wide, stream);
+    return launch_tokens<true>(p, wide, sms, stream);
 }
 
 }  // namespace q4k
