@@ -85,10 +85,60 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *u)
         : "memory");
 }
 
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
+        : "memory");
+}
+
+// Waits for the loads issued so far; the registers of the one that is about to be
+// used are operands, so that nothing that reads them moves ahead of the wait.
+__device__ __forceinline__ void tm_wait_ld32(float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]),
+                   "+r"(u[15]), "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]),
+                   "+r"(u[22]), "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]),
+                   "+r"(u[29]), "+r"(u[30]), "+r"(u[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// The largest of three (NaN only if all are).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // Issued by one elected lane of a converged warp (the loop's arithmetic stays
 // warp-uniform that way).
@@ -408,33 +458,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!ok) break;
                 ++steps;
                 tm_fence_after();
-                float s[kChunkKeys];
+                // First pass over S, 32 columns at a time: the row's maximum.  Capped,
+                // biased or masked scores are written back for the second pass.
+                const bool edge = kb < in_lo || kb + kChunkKeys > in_hi;
+                const bool back = MODE != 0 || edge;
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float s[2][32];
+                tm_ld32(ts, s[0]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tm_ld32(ts + 32 * j, s + 32 * j);
-                tm_wait_ld();
-                float mul = c;
-                if (MODE & 1) {
+                for (int q = 0; q < 4; ++q) {
+                    float *v = s[q & 1];
+                    tm_wait_ld32(v);
+                    if (q < 3) tm_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+                    if (MODE & 1) {
 #pragma unroll
-                    for (int j = 0; j < kChunkKeys; ++j)
-                        s[j] = a.softcap * kLog2e * (1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * (s[j] * c)) + 1.0f));
-                    mul = 1.0f;
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = a.softcap * kLog2e * (1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * (v[j] * c)) + 1.0f));
+                    }
+                    if (MODE & 2) {
+                        const float d0 = static_cast<float>(rel - kb - 32 * q);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), (MODE & 1) ? v[j] : v[j] * c);
+                    }
+                    if (edge) {
+                        const int a0 = lo - kb - 32 * q, a1 = hi - kb - 32 * q;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = j >= a0 && j < a1 ? v[j] : -INFINITY;
+                    }
+                    if (back) tm_st32(ts + 32 * q, reinterpret_cast<const uint32_t *>(v));
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = max3(x[k], v[j + 2 * k], v[j + 2 * k + 1]);
+                    }
                 }
-                if (MODE & 2) {
-                    const float d0 = static_cast<float>(rel - kb);
-#pragma unroll
-                    for (int j = 0; j < kChunkKeys; ++j)
-                        s[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), s[j] * mul);
-                    mul = 1.0f;
-                }
-                if (kb < in_lo || kb + kChunkKeys > in_hi) {
-                    const int a0 = lo - kb, a1 = hi - kb;
-#pragma unroll
-                    for (int j = 0; j < kChunkKeys; ++j) s[j] = j >= a0 && j < a1 ? s[j] : -INFINITY;
-                }
-                float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int j = 4; j < kChunkKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
-                const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
+                if (back) tm_wait_st();
+                tm_ld32(ts, s[0]);   // second pass, on its way
+                const float mul = MODE ? 1.0f : c;
+                const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * mul;
                 float f = 1.0f;
                 if (mx > m + kLazy || m == -INFINITY) {
                     // (m = mx = -inf: everything masked so far, l and O are zero)
@@ -447,27 +509,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     for (int j = 0; j < DP / 32; ++j) {
                         float o[32];
                         tm_ld32(to + 32 * j, o);
-                        tm_wait_ld();
+                        tm_wait_ld32(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] *= f;
                         tm_st32(to + 32 * j, reinterpret_cast<const uint32_t *>(o));
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : m - kShift;
-                float sum[4] = {0, 0, 0, 0};
+                // Second pass: exponentials, their sum, and P over the columns already read
+                const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t p[32];
+                for (int q = 0; q < 4; ++q) {
+                    float *v = s[q & 1];
+                    tm_wait_ld32(v);
+                    if (q < 3) tm_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+                    uint32_t p[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float e0 = ex2(fmaf(s[64 * j + 2 * k], mul, -base));
-                        const float e1 = ex2(fmaf(s[64 * j + 2 * k + 1], mul, -base));
-                        sum[k & 1] += e0, sum[2 + (k & 1)] += e1;
+                    for (int k = 0; k < 16; ++k) {
+                        float e0, e1;
+                        unpair(fma2(pair(v[2 * k], v[2 * k + 1]), mul2, base2), e0, e1);
+                        e0 = ex2(e0), e1 = ex2(e1);
+                        sum[k & 1] = add2(sum[k & 1], pair(e0, e1));
                         p[k] = pack2(e0, e1, CT);
                     }
-                    tm_st32(ts + 32 * j, p);
+                    tm_st16(ts + 16 * q, p);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float l0, l1;
+                unpair(add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
                 tm_wait_st();
                 tm_fence_before();
                 mbar_arrive(smem_u32(&sh.p_ready[h]));
@@ -488,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int j = 0; j < DP / 32; ++j) {
                     float o[32];
                     tm_ld32(to + 32 * j, o);
-                    tm_wait_ld();
+                    tm_wait_ld32(o);
                     if (live) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
