@@ -403,9 +403,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
         const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
         const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
-        uint32_t steps = 0;
+        uint32_t steps = 0, joins = 0;
         int items = 0;
         bool ok = true;
+        // the 256 softmax threads meet (bounded, like every wait)
+        auto join_sync = [&]() -> bool {
+            mbar_arrive(smem_u32(&sh.joined));
+            return wait(sh.joined, joins++ & 1);
+        };
         const float neg = a.scale < 0.0f ? -1.0f : 1.0f;
         // masked scores are -inf: keep their product with the scale -inf when the scale is 0
         const float c = (MODE & 1) ? fabsf(a.scale) / a.softcap : fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
@@ -544,15 +549,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             if (!ok) break;
 
-            // ---- O: divide and store, or leave a partial result
+            // ---- O: divide and store, or leave a partial result ([dim / 4][row] quads, maxima, sums)
             ok = wait(sh.o_done, items & 1);
             if (!ok) break;
             ++items;
             tm_fence_after();
             const bool split = todo < t.units;
-            float *part = a.part + (2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0)) * (kChunkRows * (DP + 2));
-            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            auto slot_of = [&](int q, bool first) {
+                return a.part + (2 * static_cast<int64_t>(q) + (first ? 1 : 0)) * (kChunkRows * (DP + 2));
+            };
             if (active) {
+                float *part = slot_of(cta, off == 0);
+                const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
                 const int64_t at = (t.tok0 + tok) * a.out_token + hq * a.out_head;
 #pragma unroll
                 for (int j = 0; j < DP / 32; ++j) {
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             const float4 v = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
-                            if (split) *reinterpret_cast<float4 *>(part + row * DP + 32 * j + k) = v;
+                            if (split) reinterpret_cast<float4 *>(part)[(8 * j + k / 4) * kChunkRows + row] = v;
                             else if (32 * j + k < a.dim) store4(a.out, a.out_type, at + 32 * j + k, v);
                         }
                     }
@@ -579,35 +587,81 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (split) {
                 // the last CTA to arrive adds the parts in key order
                 const int c0 = share_owner(total, n, u0), c1 = share_owner(total, n, u0 + t.units - 1);
+                const int parts = c1 - c0 + 1;
                 __threadfence();
-                mbar_arrive(smem_u32(&sh.joined));
-                ok = wait(sh.joined, 0);
-                if (!ok) break;
+                if (!(ok = join_sync())) break;
                 if (tid == 0) sh.arrived = atomicAdd(a.ticket + c0, 1u);
-                mbar_arrive(smem_u32(&sh.joined));
-                ok = wait(sh.joined, 1);
-                if (!ok) break;
-                if (sh.arrived == static_cast<unsigned int>(c1 - c0)) {
+                if (!(ok = join_sync())) break;
+                if (sh.arrived == static_cast<unsigned int>(parts - 1)) {
                     __threadfence();
-                    auto slot_of = [&](int q) {
-                        return a.part + (2 * static_cast<int64_t>(q) + (q == c0 ? 1 : 0)) * (kChunkRows * (DP + 2));
-                    };
-                    for (int i = tid; i < t.rows * (DP / 4); i += 256) {
-                        const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-                        if (d >= a.dim) continue;
-                        float mx = -INFINITY;
-                        for (int q = c0; q <= c1; ++q) mx = fmaxf(mx, __ldcg(slot_of(q) + kChunkRows * DP + r));
-                        float4 v = make_float4(0, 0, 0, 0);
-                        float ls = 0.0f;
-                        for (int q = c0; q <= c1; ++q) {
-                            const float *p = slot_of(q);
-                            const float f = weight(__ldcg(p + kChunkRows * DP + r), mx);
-                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p + r * DP + d));
-                            ls += f * __ldcg(p + kChunkRows * (DP + 1) + r);
-                            v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
+                    // Some rows at a time: first their weights, in the shared memory of the queries (done with)
+                    float *wt = reinterpret_cast<float *>(sh.q);
+                    constexpr int kRoom = 2 * kTile / 4 - kChunkRows;
+                    const int some = parts * t.rows <= kRoom ? t.rows : max(1, kRoom / parts);
+                    float *sums = wt + kRoom;
+                    for (int r0 = 0; r0 < t.rows && ok; r0 += some) {
+                        const int rows = min(some, t.rows - r0);
+                        if (tid < rows) {
+                            const int r = r0 + tid;
+                            float mx = -INFINITY, ls = 0.0f;
+#pragma unroll 8
+                            for (int q = 0; q < parts; ++q) {
+                                const float v = __ldcg(slot_of(c0 + q, q == 0) + kChunkRows * DP + r);
+                                wt[q * rows + tid] = v;
+                                mx = fmaxf(mx, v);
+                            }
+#pragma unroll 8
+                            for (int q = 0; q < parts; ++q) {
+                                const float f = weight(wt[q * rows + tid], mx);
+                                wt[q * rows + tid] = f;
+                                ls += f * __ldcg(slot_of(c0 + q, q == 0) + kChunkRows * (DP + 1) + r);
+                            }
+                            sums[tid] = ls;
+                            if (a.lse) {
+                                const int gr2 = t.first + r;
+                                a.lse[static_cast<int64_t>(t.tok0 + gr2 / a.group) * a.heads + head * a.group + gr2 % a.group] =
+                                    ls == 0.0f ? -INFINITY : (mx + log2f(ls) - kShift) * kLn2;
+                            }
                         }
-                        finish_row(a, t, head, r, d, v, mx, ls, kShift);
+                        if (!(ok = join_sync())) break;
+                        // then four outputs quads a thread at a time, neighbouring threads on neighbouring rows
+                        const int quads = rows * (a.dim / 4);
+                        for (int i0 = tid; i0 < quads; i0 += 4 * 256) {
+                            float4 v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+                            for (int q = 0; q < parts; ++q) {
+                                const float4 *p = reinterpret_cast<const float4 *>(slot_of(c0 + q, q == 0));
+                                float4 x[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int i = i0 + 256 * k;
+                                    if (i < quads) x[k] = __ldcg(p + (i / rows) * kChunkRows + r0 + i % rows);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int i = i0 + 256 * k;
+                                    if (i >= quads) continue;
+                                    const float f = wt[q * rows + i % rows];
+                                    v[k].x += f * x[k].x, v[k].y += f * x[k].y, v[k].z += f * x[k].z, v[k].w += f * x[k].w;
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int i = i0 + 256 * k;
+                                if (i >= quads) continue;
+                                const float ls = sums[i % rows], iv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                                const int gr2 = t.first + r0 + i % rows;
+                                store4(a.out, a.out_type,
+                                       (t.tok0 + gr2 / a.group) * a.out_token +
+                                           (head * a.group + gr2 % a.group) * a.out_head + 4 * (i / rows),
+                                       make_float4(v[k].x * iv, v[k].y * iv, v[k].z * iv, v[k].w * iv));
+                            }
+                        }
+                        if (!(ok = join_sync())) break;
                     }
+                    if (!ok) break;
                 }
             }
             u += todo;
