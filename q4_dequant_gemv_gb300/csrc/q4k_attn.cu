@@ -65,6 +65,65 @@ bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
     return one(&maps->k, a.k, a.k_page, a.k_slot, a.k_head) && one(&maps->v, a.v, a.v_page, a.v_slot, a.v_head);
 }
 
+// Adds the parts of split tiles: blockIdx.x = the CTA in whose share the tile
+// begins, blockIdx.y = 32 of its rows; a thread per row and column quad, loads of
+// several parts in flight.  Launched as the first kernel's programmatic dependent.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R, int width, float shift)
+{
+    pdl_wait();
+    const int4 t0 = __ldcg(reinterpret_cast<const int4 *>(a.joint + blockIdx.x));
+    const int2 t1 = __ldcg(reinterpret_cast<const int2 *>(a.joint + blockIdx.x) + 2);
+    const Joint t{t0.x, t0.y, t0.z, t0.w, t1.x, t1.y};
+    const int span = min(R, kJoinRows), r = blockIdx.y * kJoinRows + static_cast<int>(threadIdx.x) % span;
+    if (r >= t.rows) return;
+    const int64_t size = static_cast<int64_t>(R) * (width + 2);
+    const int lanes = kJoinThreads / span, parts = t.c1 - t.c0 + 1;
+    const float *first = a.part + part_slot(t.c0, true) * size, *rest = a.part + part_slot(t.c0, false) * size;
+    auto slot = [&](int q) { return q == 0 ? first : rest + 2 * q * size; };
+    float mx = -INFINITY, ls = 0.0f;
+#pragma unroll 8
+    for (int q = 0; q < parts; ++q) mx = fmaxf(mx, __ldcg(slot(q) + R * width + r));
+    constexpr int PER = 4;   // quads of a thread at a time
+    for (int c = static_cast<int>(threadIdx.x) / span; 4 * c < a.dim; c += PER * lanes) {
+        float4 v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = make_float4(0, 0, 0, 0);
+        ls = 0.0f;
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q) {
+            const float *p = slot(q);
+            const float f = weight(__ldcg(p + R * width + r), mx);
+            ls += f * __ldcg(p + R * width + R + r);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int x = c + k * lanes;
+                if (4 * x >= a.dim) continue;
+                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p) + x * R + r);
+                v[k].x += f * o.x, v[k].y += f * o.y, v[k].z += f * o.z, v[k].w += f * o.w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int x = c + k * lanes;
+            if (4 * x < a.dim) finish_row(a, t.tok0, t.first + r, t.head, 4 * x, v[k], mx, ls, shift);
+        }
+    }
+}
+
+cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, (R + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = kJoinThreads;
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel, a, R, width, shift);
+}
+
 }  // namespace attn
 
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)

@@ -10,13 +10,14 @@
 // and takes an equal, contiguous share of them, wherever that begins or ends
 // inside a tile.  The load is therefore even for ragged lengths, causal tiles
 // and one long sequence alike, with no host knowledge of lengths.  Rows of a
-// tile that several CTAs hold meet in scratch memory: the last of them to
-// arrive (one atomic ticket per split tile) adds the partial results in the
-// order of the keys, so the same inputs give the same bits.
+// tile that several CTAs hold meet in scratch memory, where a second kernel, its
+// launch hidden under the first, adds the partial results in the order of the
+// keys, so the same inputs give the same bits.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 
@@ -60,9 +61,18 @@ struct Args {
     int slots;             // upper bound of the tiles per cache head
     int cluster;           // few-rows kernel: CTAs of a cluster that share a tile; 0: the split over all CTAs
     float *part;           // partial results: two slots per CTA
-    unsigned int *ticket;  // one per CTA, zero at launch
+    struct Joint *joint;   // the split tile that starts in each CTA's share
     unsigned int *error;   // the sticky error word
 };
+
+// A split tile: its rows, and the CTAs c0 .. c1 that hold its parts.  The first of
+// them has its part in its second slot (the tile begins in its share), the others
+// in their first slots.  A slot is [dim / 4][R] quads of O, R maxima (log2), R sums.
+struct alignas(32) Joint {
+    int tok0, first, rows, head, c0, c1;
+};
+
+__device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * static_cast<int64_t>(cta) + (begins ? 1 : 0); }
 
 // One tile: the rows, their token range and the keys that any of them sees.
 struct Tile {
@@ -277,14 +287,15 @@ __device__ __forceinline__ void store4(void *out, int type, int64_t i, float4 v)
     }
 }
 
-// Four outputs of a tile's row r from d on: v / ls; and the row's lse with d = 0.
-// m and ls as the kernels keep them: log2 domain, ls carrying 2^shift.
-__device__ __forceinline__ void finish_row(const Args &a, const Tile &t, int head, int r, int d, float4 v, float m, float ls,
+// Four outputs from d on of a sequence's row (its first token in row tok0 of the
+// call): v / ls; and the row's lse with d = 0.  m and ls as the kernels keep them:
+// log2 domain, ls carrying 2^shift.
+__device__ __forceinline__ void finish_row(const Args &a, int tok0, int row, int head, int d, float4 v, float m, float ls,
                                            float shift)
 {
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const int row = t.first + r, hq = head * a.group + row % a.group;
-    const int64_t tok = t.tok0 + row / a.group;
+    const int hq = head * a.group + row % a.group;
+    const int64_t tok = tok0 + row / a.group;
     store4(a.out, a.out_type, tok * a.out_token + hq * a.out_head + d,
            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
     if (a.lse && d == 0) a.lse[tok * a.heads + hq] = ls == 0.0f ? -INFINITY : (m + log2f(ls) - shift) * kLn2;
@@ -304,6 +315,26 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
         "[%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(bar)
         : "memory");
+}
+
+// Host: scratch of `grid` CTAs, the first kernel by `launch(args)`, the join of the
+// tiles that it left split; R rows and `width` columns a slot.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
+
+template <class Launch>
+cudaError_t launch_split(Args &a, int grid, int R, int width, float shift, cudaStream_t stream, Launch launch)
+{
+    const size_t head = (grid * sizeof(Joint) + 255) / 256 * 256;
+    void *scratch = nullptr;
+    cudaError_t e = cudaMallocAsync(&scratch, head + static_cast<size_t>(grid) * 2 * R * (width + 2) * sizeof(float), stream);
+    if (e != cudaSuccess) return e;
+    a.joint = static_cast<Joint *>(scratch);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
+    e = launch(a);
+    if (e == cudaSuccess) e = launch_join(a, grid, R, width, shift, stream);
+    const cudaError_t f = cudaFreeAsync(scratch, stream);
+    return e == cudaSuccess ? f : e;
 }
 
 // Host: the maps of a call's cache with boxes of `box` slots.

@@ -54,9 +54,8 @@ struct ChunkShared {
     uint8_t q[2 * kTile];                                      // two halves of query rows
     uint8_t kv[kStages * kTile];
     typename Plan::Shared plan;
-    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2], o_done, q_ready, edge, joined;
+    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2], o_done, q_ready, edge;
     uint32_t tmem;
-    unsigned int arrived;
     int abort;
 };
 
@@ -188,6 +187,13 @@ constexpr uint32_t chunk_idesc(int n, bool b_mn_major)
            (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
+// fp16 weights are kept at 2^6 and below 2^14; bf16 has range to spare.
+template <int CT>
+constexpr float chunk_shift()
+{
+    return CT == Q4K_F16 ? 6.0f : 0.0f;
+}
+
 // MODE bit 0: capped scores, bit 1: distance bias.
 template <int CT, int DP, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -195,8 +201,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 {
     using Sh = ChunkShared<DP>;
     constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
-    // fp16 weights are kept at 2^6 and below 2^14, bf16 has range to spare
-    constexpr float kShift = CT == Q4K_F16 ? 6.0f : 0.0f;
+    constexpr float kShift = chunk_shift<CT>();
     constexpr float kLazy = 8.0f;
     extern __shared__ uint8_t smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -214,7 +219,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(smem_u32(&sh.o_done), 1);
         mbar_init(smem_u32(&sh.q_ready), 256);
         mbar_init(smem_u32(&sh.edge), 1);
-        mbar_init(smem_u32(&sh.joined), 256);
         fence_barrier_init();
         sh.abort = 0;
     }
@@ -251,6 +255,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int cta = blockIdx.x;
     int64_t u = 0, u_end = 0;
     if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+    if (tid == 0) a.joint[cta].rows = 0;
+    pdl_launch_dependents();   // the join waits for this grid's end
 
     if (w == kLoadWarp) {
         // ------------------------------------------------------------ loads
@@ -403,14 +409,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
         const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
         const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
-        uint32_t steps = 0, joins = 0;
+        uint32_t steps = 0;
         int items = 0;
         bool ok = true;
-        // the 256 softmax threads meet (bounded, like every wait)
-        auto join_sync = [&]() -> bool {
-            mbar_arrive(smem_u32(&sh.joined));
-            return wait(sh.joined, joins++ & 1);
-        };
         const float neg = a.scale < 0.0f ? -1.0f : 1.0f;
         // masked scores are -inf: keep their product with the scale -inf when the scale is 0
         const float c = (MODE & 1) ? fabsf(a.scale) / a.softcap : fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
@@ -427,16 +428,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const uint16_t *q = static_cast<const uint16_t *>(a.q);
                 const uint32_t flip = neg < 0.0f ? 0x80008000u : 0u;
                 uint8_t *dst = sh.q + h * kTile;
-                for (int i = tid & 127; i < 128 * 8 * ND; i += 128) {
-                    const int r = i / (8 * ND), ch = i % (8 * ND);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (128 * h + r < t.rows && 8 * ch < a.dim) {
-                        const int gr = t.first + 128 * h + r;
-                        v = *reinterpret_cast<const uint4 *>(q + (t.tok0 + gr / a.group) * a.q_token +
-                                                             (head * a.group + gr % a.group) * a.q_head + 8 * ch);
-                        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                // a thread takes one 16-byte column of every kStep-th row, eight loads at a time
+                constexpr int kStep = 128 / (8 * ND);
+                const int ch = tid % (8 * ND), r0 = (tid & 127) / (8 * ND);
+                const bool in = 8 * ch < a.dim;
+#pragma unroll
+                for (int b = 0; b < 128 / kStep; b += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = r0 + kStep * (b + k);
+                        const uint32_t gr = t.first + 128 * h + r, tk = gr / static_cast<uint32_t>(a.group);
+                        v[k] = make_uint4(0, 0, 0, 0);
+                        if (in && 128 * h + r < t.rows)
+                            v[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                q + (t.tok0 + tk) * a.q_token + (head * a.group + (gr - tk * a.group)) * a.q_head + 8 * ch));
                     }
-                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = r0 + kStep * (b + k);
+                        *reinterpret_cast<uint4 *>(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
+                    }
                 }
                 fence_proxy_async_smem();
             }
@@ -555,11 +568,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ++items;
             tm_fence_after();
             const bool split = todo < t.units;
-            auto slot_of = [&](int q, bool first) {
-                return a.part + (2 * static_cast<int64_t>(q) + (first ? 1 : 0)) * (kChunkRows * (DP + 2));
-            };
             if (active) {
-                float *part = slot_of(cta, off == 0);
+                float *part = a.part + part_slot(cta, off == 0) * (kChunkRows * (DP + 2));
                 const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
                 const int64_t at = (t.tok0 + tok) * a.out_token + hq * a.out_head;
 #pragma unroll
@@ -584,86 +594,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 tm_fence_before();
             }
-            if (split) {
-                // the last CTA to arrive adds the parts in key order
-                const int c0 = share_owner(total, n, u0), c1 = share_owner(total, n, u0 + t.units - 1);
-                const int parts = c1 - c0 + 1;
-                __threadfence();
-                if (!(ok = join_sync())) break;
-                if (tid == 0) sh.arrived = atomicAdd(a.ticket + c0, 1u);
-                if (!(ok = join_sync())) break;
-                if (sh.arrived == static_cast<unsigned int>(parts - 1)) {
-                    __threadfence();
-                    // Some rows at a time: first their weights, in the shared memory of the queries (done with)
-                    float *wt = reinterpret_cast<float *>(sh.q);
-                    constexpr int kRoom = 2 * kTile / 4 - kChunkRows;
-                    const int some = parts * t.rows <= kRoom ? t.rows : max(1, kRoom / parts);
-                    float *sums = wt + kRoom;
-                    for (int r0 = 0; r0 < t.rows && ok; r0 += some) {
-                        const int rows = min(some, t.rows - r0);
-                        if (tid < rows) {
-                            const int r = r0 + tid;
-                            float mx = -INFINITY, ls = 0.0f;
-#pragma unroll 8
-                            for (int q = 0; q < parts; ++q) {
-                                const float v = __ldcg(slot_of(c0 + q, q == 0) + kChunkRows * DP + r);
-                                wt[q * rows + tid] = v;
-                                mx = fmaxf(mx, v);
-                            }
-#pragma unroll 8
-                            for (int q = 0; q < parts; ++q) {
-                                const float f = weight(wt[q * rows + tid], mx);
-                                wt[q * rows + tid] = f;
-                                ls += f * __ldcg(slot_of(c0 + q, q == 0) + kChunkRows * (DP + 1) + r);
-                            }
-                            sums[tid] = ls;
-                            if (a.lse) {
-                                const int gr2 = t.first + r;
-                                a.lse[static_cast<int64_t>(t.tok0 + gr2 / a.group) * a.heads + head * a.group + gr2 % a.group] =
-                                    ls == 0.0f ? -INFINITY : (mx + log2f(ls) - kShift) * kLn2;
-                            }
-                        }
-                        if (!(ok = join_sync())) break;
-                        // then four outputs quads a thread at a time, neighbouring threads on neighbouring rows
-                        const int quads = rows * (a.dim / 4);
-                        for (int i0 = tid; i0 < quads; i0 += 4 * 256) {
-                            float4 v[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-                            for (int q = 0; q < parts; ++q) {
-                                const float4 *p = reinterpret_cast<const float4 *>(slot_of(c0 + q, q == 0));
-                                float4 x[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int i = i0 + 256 * k;
-                                    if (i < quads) x[k] = __ldcg(p + (i / rows) * kChunkRows + r0 + i % rows);
-                                }
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int i = i0 + 256 * k;
-                                    if (i >= quads) continue;
-                                    const float f = wt[q * rows + i % rows];
-                                    v[k].x += f * x[k].x, v[k].y += f * x[k].y, v[k].z += f * x[k].z, v[k].w += f * x[k].w;
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int i = i0 + 256 * k;
-                                if (i >= quads) continue;
-                                const float ls = sums[i % rows], iv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                                const int gr2 = t.first + r0 + i % rows;
-                                store4(a.out, a.out_type,
-                                       (t.tok0 + gr2 / a.group) * a.out_token +
-                                           (head * a.group + gr2 % a.group) * a.out_head + 4 * (i / rows),
-                                       make_float4(v[k].x * iv, v[k].y * iv, v[k].z * iv, v[k].w * iv));
-                            }
-                        }
-                        if (!(ok = join_sync())) break;
-                    }
-                    if (!ok) break;
-                }
-            }
+            if (split && off == 0 && tid == 0)
+                a.joint[cta] = Joint{t.tok0, t.first, t.rows, head, cta, share_owner(total, n, u0 + t.units - 1)};
             u += todo;
         }
     }

@@ -27,19 +27,10 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
-    const size_t head = (grid * sizeof(unsigned int) + 255) / 256 * 256;
-    void *scratch = nullptr;
-    cudaError_t e = cudaMallocAsync(&scratch, head + static_cast<size_t>(grid) * 2 * R * (DP + 2) * sizeof(float), l.stream);
-    if (e != cudaSuccess) return e;
-    e = cudaMemsetAsync(scratch, 0, grid * sizeof(unsigned int), l.stream);
-    if (e == cudaSuccess) {
-        a.ticket = static_cast<unsigned int *>(scratch);
-        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
-        kern<<<grid, kChunkThreads, kSmem, l.stream>>>(maps, a, box);
-        e = cudaGetLastError();
-    }
-    const cudaError_t f = cudaFreeAsync(scratch, l.stream);
-    return e == cudaSuccess ? f : e;
+    return launch_split(a, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
+        kern<<<grid, kChunkThreads, kSmem, l.stream>>>(maps, args, box);
+        return cudaGetLastError();
+    });
 }
 
 template <int CT, int DP>

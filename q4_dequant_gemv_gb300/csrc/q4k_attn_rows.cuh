@@ -115,6 +115,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS])
     }
 }
 
+// P carries 2^shift (see above).
+template <int CT>
+constexpr float rows_shift()
+{
+    return CT == Q4K_F16 ? 14.0f : 0.0f;
+}
+
 template <int CT, int PARTS, int NT, int DP>
 struct RowsShared {
     using Sp = RowsShape<DP>;
@@ -132,7 +139,6 @@ struct RowsShared {
     int lo[R], hi[R], pos[R];              // visible keys of each row, its token
     float wm[R], wl[R];                    // joined statistics
     unsigned long long full[Sp::kWarps][Sp::kSlots];
-    unsigned int arrived;
 };
 
 // TMA: slots filled by tensor copies (maps), else by cp.async.
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
     using Sp = RowsShape<DP>;
     constexpr int R = Sh::R, ND = DP / 64, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
     constexpr int kHalf = kBlock * 128;      // bytes of 16 rows of 64 elements
-    constexpr float kShift = CT == Q4K_F16 ? 14.0f : 0.0f;
+    constexpr float kShift = rows_shift<CT>();
     extern __shared__ uint8_t smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -161,6 +167,8 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         plan.scan();
         total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
         n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+        if (tid == 0) a.joint[cta].rows = 0;
+        pdl_launch_dependents();   // the join waits for this grid's end
         if (cta >= n) return;
         u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
     }
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             constexpr int PER = R / WARPS;
             return reinterpret_cast<float *>(sh.ring[r / PER]) + (R + r % PER) * Sh::kRed;
         };
-        float *part = a.part + (2 * static_cast<int64_t>(cta) + (off == 0 ? 1 : 0)) * (R * (DP + 2));
+        float *part = a.part + part_slot(cta, off == 0) * (R * (DP + 2));
         for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
             const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
             float mx = -INFINITY, ls = 0.0f;
@@ -499,10 +507,10 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 *reinterpret_cast<float4 *>(sum_row(r) + d) = v;
                 if (d == 0) sh.wm[r] = mx, sh.wl[r] = ls;
             } else if (split) {
-                *reinterpret_cast<float4 *>(part + r * DP + d) = v;
+                reinterpret_cast<float4 *>(part)[d / 4 * R + r] = v;
                 if (d == 0) part[R * DP + r] = mx, part[R * DP + R + r] = ls;
             } else {
-                finish_row(a, t, head, r, d, v, mx, ls, kShift);
+                finish_row(a, t.tok0, t.first + r, head, d, v, mx, ls, kShift);
             }
         }
 
@@ -532,39 +540,12 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                         ls += f * ld_shared_cluster_f32(map_shared_rank(al, c));
                         v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
                     }
-                finish_row(a, t, head, r, d, v, mx, ls, kShift);
+                finish_row(a, t.tok0, t.first + r, head, d, v, mx, ls, kShift);
             }
             __syncthreads();
             cluster_sync_all();   // nobody leaves while its memory is read
-        } else if (split) {
-            // ---- a split tile: the last CTA to arrive adds the parts in key order
-            const int c0 = share_owner(total, n, u0), c1 = share_owner(total, n, u0 + t.units - 1);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) sh.arrived = atomicAdd(a.ticket + c0, 1u);
-            __syncthreads();
-            if (sh.arrived == static_cast<unsigned int>(c1 - c0)) {
-                __threadfence();
-                auto slot_of = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * (R * (DP + 2)); };
-                for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
-                    const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-                    if (d >= a.dim) continue;
-                    float mx = -INFINITY;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + R * DP + r));
-                    float4 v = make_float4(0, 0, 0, 0);
-                    float ls = 0.0f;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) {
-                        const float *p = slot_of(c);
-                        const float f = weight(__ldcg(p + R * DP + r), mx);
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + r * DP + d));
-                        ls += f * __ldcg(p + R * DP + R + r);
-                        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
-                    }
-                    finish_row(a, t, head, r, d, v, mx, ls, kShift);
-                }
-            }
+        } else if (split && off == 0 && tid == 0) {
+            a.joint[cta] = Joint{t.tok0, t.first, t.rows, head, cta, share_owner(total, n, u0 + t.units - 1)};
         }
         if (a.cluster) break;   // one tile per cluster (a rank's share of it may be empty)
         u += todo;

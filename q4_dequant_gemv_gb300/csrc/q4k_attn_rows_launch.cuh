@@ -29,8 +29,8 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
 
     // A cluster of S CTAs per tile and cache head joins through its shared
     // memory: one launch, no scratch.  The split over all CTAs balances ragged
-    // lengths and a few long sequences, but its scratch, its tickets and the join
-    // through memory cost about kSplitCost units of one CTA's time.
+    // lengths and a few long sequences, but its scratch and the join through memory
+    // cost about kSplitCost units of one CTA's time.
     const int64_t items = a.kv_heads * std::max<int64_t>(a.batch, (static_cast<int64_t>(a.tokens) * a.group + R - 1) / R);
     int S = kMaxCluster;
     while (S > 1 && (S > units || items * S > l.sms)) S /= 2;
@@ -53,19 +53,9 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     }
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
     const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
-    const size_t head = (grid * sizeof(unsigned int) + 255) / 256 * 256;
-    void *scratch = nullptr;
-    cudaError_t e = cudaMallocAsync(&scratch, head + static_cast<size_t>(grid) * 2 * R * (DP + 2) * sizeof(float), l.stream);
-    if (e != cudaSuccess) return e;
-    e = cudaMemsetAsync(scratch, 0, grid * sizeof(unsigned int), l.stream);
-    if (e == cudaSuccess) {
-        a.ticket = static_cast<unsigned int *>(scratch);
-        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
-        cfg.gridDim = static_cast<unsigned>(grid);
-        e = cudaLaunchKernelEx(&cfg, kern, maps, a);
-    }
-    const cudaError_t f = cudaFreeAsync(scratch, l.stream);
-    return e == cudaSuccess ? f : e;
+    cfg.gridDim = static_cast<unsigned>(grid);
+    return launch_split(a, grid, R, DP, rows_shift<CT>(), l.stream,
+                        [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
 }
 
 template <int CT, int PARTS, int NT, int DP>
