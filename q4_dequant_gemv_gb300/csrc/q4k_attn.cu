@@ -65,6 +65,22 @@ bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
     return one(&maps->k, a.k, a.k_page, a.k_slot, a.k_head) && one(&maps->v, a.v, a.v_page, a.v_slot, a.v_head);
 }
 
+bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int64_t row = (a.dim + 7) / 8 * 8;
+    const int64_t token = a.tokens == 1 ? row : a.q_token, head = a.heads == 1 ? row : a.q_head;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.heads),
+                          static_cast<cuuint64_t>(a.tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2};
+    cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(tokens)}, steps[3] = {1, 1, 1};
+    return enc(map, type == Q4K_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(a.q), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Adds the parts of split tiles: blockIdx.x = the CTA in whose share the tile
 // begins, blockIdx.y = 32 of its rows; a thread per row and column quad, loads of
 // several parts in flight.  Launched as the first kernel's programmatic dependent.
@@ -177,14 +193,18 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
     // The tcgen05 kernel takes calls with more query rows per sequence and cache
     // head than the mma.sync kernel holds at once (16), in one 16-bit type, over
-    // pages that split into boxes of 16 slots or more.
+    // pages that split into boxes of 16 slots or more.  Its TMA boxes also ask for
+    // positive strides and groups of 256 heads at most, its maxima for a scale
+    // that is not negative.
     auto stride_ok = [](int64_t s) { return s > 0 && s < (int64_t{1} << 39); };
     const bool boxes = c->page_size % 16 == 0 && stride_ok(c->k_slot_stride) && stride_ok(c->v_slot_stride) &&
                        (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
     l.boxes = boxes && p.capacity > 0;
+    const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
+                         (c->tokens == 1 || stride_ok(a->q_token_stride)) && (a->q_heads == 1 || stride_ok(a->q_head_stride));
     cudaError_t e;
-    if (!l.parts_many && c->dim <= 128 && boxes && p.capacity > 0 && c->tokens * p.group > 16 * c->batch) {
+    if (!l.parts_many && c->dim <= 128 && l.boxes && queries && c->tokens * p.group > 16 * c->batch) {
         const attn::ChunkLaunch ch{p, sms, l.stream};
         e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {

@@ -106,8 +106,8 @@ __device__ __forceinline__ Range token_range(const Args &a, int seq, int64_t pos
 }
 
 // The split of the call's work, one copy per CTA in shared memory.
-// ALIGN: where units start (a power of two).
-template <int R, int U, int THREADS, int ALIGN>
+// R (rows of a tile) is given at run time; ALIGN: where units start (a power of two).
+template <int U, int THREADS, int ALIGN>
 struct Split {
     static constexpr int kStripes = 512;     // prefix entries; each covers `stripe` tile slots
     static constexpr int kSeqs = 512;        // sequence starts held in shared memory
@@ -119,6 +119,7 @@ struct Split {
 
     const Args &a;
     Shared &sh;
+    const int R;
     int stripe;
     uint32_t per_head;      // units of one cache head
 
@@ -131,7 +132,7 @@ struct Split {
     // slots from batch + extra(b) on, which has room for them whatever the lengths.
     __device__ __forceinline__ int extra(int b) const
     {
-        return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / R);
+        return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / static_cast<uint32_t>(R));
     }
 
     __device__ __forceinline__ Tile tile(int slot, bool report) const
@@ -176,7 +177,7 @@ struct Split {
     }
 
     // Sequence starts and lengths; all threads of the CTA.
-    __device__ __forceinline__ Split(const Args &args, Shared &shared) : a(args), sh(shared)
+    __device__ __forceinline__ Split(const Args &args, Shared &shared, int rows) : a(args), sh(shared), R(rows)
     {
         const int tid = threadIdx.x;
         for (int i = tid; i <= a.batch; i += THREADS) {
@@ -244,12 +245,19 @@ struct Split {
     }
 };
 
+// a / b for non-negative a, b > 0 (a 64-bit division takes ten times a 32-bit one).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // A CTA's share [begin, end) of `total` units over n CTAs, and the CTA that
 // holds a unit.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return quotient(total * c, n); }
 __device__ __forceinline__ int share_owner(int64_t total, int n, int64_t unit)
 {
-    return static_cast<int>(((unit + 1) * n - 1) / total);
+    return static_cast<int>(quotient((unit + 1) * n - 1, total));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -339,6 +347,10 @@ cudaError_t launch_split(Args &a, int grid, int R, int width, float shift, cudaS
 
 // Host: the maps of a call's cache with boxes of `box` slots.
 bool encode_cache(CacheMaps *maps, const Args &a, int type, int box);
+// The queries as [token][head][d]: boxes of `tokens` tokens by a group's heads by 64 elements.
+bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens);
+// The queries as [token][head][d]: boxes of `tokens` tokens by a group's heads by 64 elements.
+bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens);
 
 }  // namespace attn
 }  // namespace q4k

@@ -5,17 +5,22 @@
 // tensor cores bound it (two 128 x 128 x 128 products a step and half tile, 512
 // cycles each), with one exponential per (row, key) beside them.
 //
-// CTA: one tile of 256 query rows as two halves of 128 (the MMA's M), one CTA
-// per SM, persistent over its share of the call's units (128 keys each).
+// CTA: tiles of whole tokens, up to 256 query rows, as two halves of 128 (the
+// MMA's M); one CTA per SM, persistent over its share of the call's units (128
+// keys each).
 //   * warps 0-3 and 4-7: softmax of a half, a thread per row: S from tensor
 //     memory (128 values), mask, maximum, exponentials, P as 16-bit pairs back
 //     into the columns of S; at the end of a tile O out of tensor memory.
 //   * warp 8 issues the MMAs: S = Q K^T (both from shared memory, K-major) and
 //     O += P V (P from tensor memory, V from shared memory as it lies, rows of
 //     keys: MN-major).  The halves alternate, so one half's softmax runs
-//     under the other's products.
-//   * warp 9 loads K and V tiles (128 keys) through a ring of four stages: a
-//     lane per page piece looks the page up and issues its TMA boxes.
+//     under the other's products, and P is taken up in two parts.
+//   * warp 9 walks the tiles and tells the others (a ring of two descriptors),
+//     loads the tile's queries (a TMA box of its tokens and the group's heads) as
+//     soon as the last scores of the tile before are done, and K and V (128
+//     keys) through a ring of four stages: a lane per page piece looks the page
+//     up and issues its boxes.
+// Softmax threads take 200 registers (a row of S and change), the others 96.
 // Tensor memory, all 512 columns: S (and P) of the halves, O of the halves.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the
@@ -39,22 +44,33 @@
 namespace q4k {
 namespace attn {
 
-constexpr int kChunkRows = 256;              // query rows of a tile
+constexpr int kChunkRows = 256;              // query rows of a tile at most
 constexpr int kChunkKeys = 128;              // keys of a unit
-constexpr int kChunkThreads = 320;
+constexpr int kChunkThreads = 384;           // two softmax warpgroups; MMA, load and two idle warps
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kStages = 4;
+// 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 constexpr uint64_t kChunkWaitNs = 2000000000ull;
+
+// A CTA's part of one tile, as the load warp found it.
+struct Work {
+    Tile t;
+    int head, off, todo, last;   // units [off, off + todo) of the tile; the CTA that holds the tile's last unit
+};
 
 template <int DP>
 struct ChunkShared {
-    using Plan = Split<kChunkRows, kChunkKeys, kChunkThreads, kChunkKeys>;
+    using Plan = Split<kChunkKeys, kChunkThreads, kChunkKeys>;
     static constexpr int kHalf = 128 * 128;                    // bytes: 128 rows of 64 elements
     static constexpr int kTile = kHalf * (DP / 64);            // 128 rows of DP elements
-    uint8_t q[2 * kTile];                                      // two halves of query rows
+    uint8_t q[2 * kTile];                                      // [dim / 64][256 rows][64]
     uint8_t kv[kStages * kTile];
+    uint8_t out[8][32 * 64];                                   // a warp's rows on their way out, 32 columns at a time
     typename Plan::Shared plan;
-    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2], o_done, q_ready, edge;
+    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2][2], o_done[2], q_full, q_empty, edge;
+    unsigned long long work_full[2], work_empty[2];
+    Work work[2];
     uint32_t tmem;
     int abort;
 };
@@ -69,6 +85,16 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, float *r)
           "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
           "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
           "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tm_ld16(uint32_t addr, float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(addr));
 }
 
@@ -111,6 +137,39 @@ __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ void tm_wait_ld16(float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_here32(float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(""
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]),
+                   "+r"(u[15]), "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]),
+                   "+r"(u[22]), "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]),
+                   "+r"(u[29]), "+r"(u[30]), "+r"(u[31])
+                 :
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi)
 {
@@ -137,6 +196,16 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Query rows: 64 elements of the group's heads of some tokens.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int d, int head, int token, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(head), "r"(token), "r"(bar)
+        : "memory");
 }
 
 // Issued by one elected lane of a converged warp (the loop's arithmetic stays
@@ -197,7 +266,7 @@ constexpr float chunk_shift()
 // MODE bit 0: capped scores, bit 1: distance bias.
 template <int CT, int DP, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    chunk_kernel(const __grid_constant__ CacheMaps maps, const Args a, const int box)
+    chunk_kernel(const __grid_constant__ CacheMaps maps, const __grid_constant__ CUtensorMap qmap, const Args a, const int box)
 {
     using Sh = ChunkShared<DP>;
     constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
@@ -206,6 +275,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tokens = kChunkRows / a.group;   // of a tile
 
     if (w == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
@@ -215,15 +285,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.s_full[i]), 1), mbar_init(smem_u32(&sh.p_ready[i]), 128);
-        mbar_init(smem_u32(&sh.o_done), 1);
-        mbar_init(smem_u32(&sh.q_ready), 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.p_ready[i][0]), 128);
+            mbar_init(smem_u32(&sh.p_ready[i][1]), 128);
+            mbar_init(smem_u32(&sh.o_done[i]), 1);
+            mbar_init(smem_u32(&sh.work_full[i]), 1);
+            mbar_init(smem_u32(&sh.work_empty[i]), 9);   // the MMA warp and eight softmax warps
+        }
+        mbar_init(smem_u32(&sh.q_full), 1);
+        mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.edge), 1);
         fence_barrier_init();
         sh.abort = 0;
     }
     tm_fence_before();
-    typename Sh::Plan plan(a, sh.plan);   // synchronises the CTA
+    typename Sh::Plan plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
     plan.scan();
     tm_fence_after();
     const uint32_t tm = sh.tmem;
@@ -258,20 +335,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (tid == 0) a.joint[cta].rows = 0;
     pdl_launch_dependents();   // the join waits for this grid's end
 
+    // The k-th part of a tile of this CTA, out of the ring; all lanes of a warp.
+    auto next_work = [&](int k, Work &item) -> bool {
+        if (!wait(sh.work_full[k & 1], (k >> 1) & 1)) return false;
+        item = sh.work[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.work_empty[k & 1]));
+        return true;
+    };
+
     if (w == kLoadWarp) {
         // ------------------------------------------------------------ loads
+        regs_dec<kOtherRegs>();
         int stage = 0, edges = 0;
         uint32_t round = 0;
         bool ok = true;
         unsigned int pending = 0;   // stages whose copies may still be in flight at a wind-down
         const int per = kChunkKeys / box;
-        while (u < u_end && ok) {
-            const int head = static_cast<int>(u / plan.per_head);
+        int k = 0;
+        for (; u < u_end && ok; ++k) {
+            const int head = static_cast<int>(quotient(u, plan.per_head));
             int off;
             const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
             const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
+            if (k > 1 && !(ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1))) break;
+            if (lane == 0) {
+                sh.work[k & 1] = Work{t, head, off, todo, share_owner(total, n, u - off + t.units - 1)};
+                mbar_arrive(smem_u32(&sh.work_full[k & 1]));
+            }
+            __syncwarp();
             const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
-            const int psize = static_cast<int>(a.page_size);
+            const uint32_t psize = static_cast<uint32_t>(a.page_size);
             for (int i = 0; i < todo && ok; ++i) {
                 const int kb = t.lo + (off + i) * kChunkKeys;
                 // lane j: piece j of the tile
@@ -279,7 +373,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 bool live = lane < per && key + box > t.from && key < t.hi;
                 int page = 0, slot = 0;
                 if (live) {
-                    const int e = key / psize;
+                    const uint32_t e = static_cast<uint32_t>(key) / psize;
                     slot = key - e * psize;
                     page = pages[e];
                     if (page < 0 || page >= a.pages) {
@@ -306,6 +400,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             load_box(smem_u32(dst + h * kHalf + lane * box * 128), kv ? &maps.v : &maps.k, 64 * h, slot,
                                      head, page, smem_u32(&bar));
                     }
+                    if (i == 0 && kv == 0) {
+                        // the tile's queries, once the last scores of the tile before are done
+                        if (k > 0 && !wait(sh.q_empty, (k - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(smem_u32(&sh.q_full), tokens * a.group * 128 * ND);
+#pragma unroll
+                            for (int h = 0; h < ND; ++h)
+                                load_rows(smem_u32(sh.q + h * 2 * kHalf), &qmap, 64 * h, head * a.group,
+                                          t.tok0 + t.first / a.group, smem_u32(&sh.q_full));
+                        }
+                        __syncwarp();
+                    }
                     if (clean) {
                         // zero the rows that nothing of the tile sees, then hand the stage on
                         if (!wait(sh.edge, edges & 1)) {
@@ -330,19 +439,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             u += todo;
         }
-        // every copy issued lands before the CTA exits
-        if (!ok) {
+        if (ok) {
+            // no more tiles
+            if (k > 1) ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1);
+            if (ok && lane == 0) {
+                sh.work[k & 1].todo = 0;
+                mbar_arrive(smem_u32(&sh.work_full[k & 1]));
+            }
+        } else {
+            // every copy issued lands before the CTA exits
             for (int s = 0; s < kStages; ++s)
                 if (pending >> s & 1) {
                     const uint32_t r = s < stage ? round : round - 1;
                     (void)mbar_wait_bounded(smem_u32(&sh.full[s]), r & 1, kChunkWaitNs);
                 }
+            (void)mbar_wait_bounded(smem_u32(&sh.q_full), (k - 1) & 1, kChunkWaitNs);
         }
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
+        regs_dec<kOtherRegs>();
         constexpr uint32_t id_s = chunk_idesc<CT>(kChunkKeys, false), id_o = chunk_idesc<CT>(DP, true);
         const uint32_t q0 = smem_u32(sh.q), kv0 = smem_u32(sh.kv);
-        int stage = 0, items = 0;
+        int stage = 0;
         uint32_t round = 0, steps[2] = {0, 0};
         bool ok = true;
         auto take = [&](uint32_t &addr) -> bool {   // next stage of the ring
@@ -351,110 +469,83 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             return true;
         };
         auto next = [&]() {
-            mma_commit(smem_u32(&sh.empty[stage]));
             if (++stage == kStages) stage = 0, ++round;
         };
         auto scores = [&](int h, uint32_t k) {
 #pragma unroll
-            for (int j = 0; j < DP / 16; ++j) {
-                const uint32_t o = (j >> 2) * kHalf + (j & 3) * 32;
-                mma_ss(tm + 128 * h, tile_desc(q0 + h * kTile + o, 16), tile_desc(k + o, 16), id_s, j > 0);
-            }
+            for (int j = 0; j < DP / 16; ++j)
+                mma_ss(tm + 128 * h, tile_desc(q0 + (j >> 2) * 2 * kHalf + h * kHalf + (j & 3) * 32, 16),
+                       tile_desc(k + (j >> 2) * kHalf + (j & 3) * 32, 16), id_s, j > 0);
             mma_commit(smem_u32(&sh.s_full[h]));
         };
-        auto values = [&](int h, uint32_t v, bool more) {
-#pragma unroll
-            for (int j = 0; j < kChunkKeys / 16; ++j)
-                mma_ts(tm + 256 + 128 * h, tm + 128 * h + 8 * j, tile_desc(v + j * 2048, kHalf), id_o, more || j > 0);
-        };
-        while (u < u_end && ok) {
-            const int head = static_cast<int>(u / plan.per_head);
-            int off;
-            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
-            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
-            const int halves = t.rows > 128 ? 2 : 1;
+        for (int k = 0; ok; ++k) {
+            Work item;
+            ok = next_work(k, item);
+            if (!ok || item.todo == 0) break;
+            const int todo = item.todo, halves = item.t.rows > 128 ? 2 : 1;
             uint32_t kt = 0, vt = 0;
-            ok = wait(sh.q_ready, items & 1) && take(kt);
+            ok = wait(sh.q_full, k & 1) && take(kt);
             if (!ok) break;
             tm_fence_after();
             for (int h = 0; h < halves; ++h) scores(h, kt);
+            mma_commit(smem_u32(&sh.empty[stage]));
+            if (todo == 1) mma_commit(smem_u32(&sh.q_empty));
             next();
             for (int i = 0; i < todo && ok; ++i) {
                 ok = take(vt);
                 const int vstage = stage;
-                if (++stage == kStages) stage = 0, ++round;
+                next();
                 const bool more = i + 1 < todo;
                 for (int h = 0; h < halves && ok; ++h) {
-                    ok = wait(sh.p_ready[h], steps[h] & 1);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        ok = ok && wait(sh.p_ready[h][part], steps[h] & 1);
+                        if (!ok) break;
+                        tm_fence_after();
+#pragma unroll
+                        for (int j = 4 * part; j < 4 * part + 4; ++j)
+                            mma_ts(tm + 256 + 128 * h, tm + 128 * h + 8 * j, tile_desc(vt + j * 2048, kHalf), id_o,
+                                   i > 0 || j > 0);
+                    }
                     if (!ok) break;
                     ++steps[h];
-                    tm_fence_after();
-                    values(h, vt, i > 0);
+                    if (!more) mma_commit(smem_u32(&sh.o_done[h]));
                     if (h == halves - 1) mma_commit(smem_u32(&sh.empty[vstage]));
                     if (more) {
                         if (h == 0) ok = take(kt);
                         if (!ok) break;
                         tm_fence_after();
                         scores(h, kt);
-                        if (h == halves - 1) next();
+                        if (h == halves - 1) {
+                            mma_commit(smem_u32(&sh.empty[stage]));
+                            if (i + 2 == todo) mma_commit(smem_u32(&sh.q_empty));
+                            next();
+                        }
                     }
                 }
             }
-            if (ok) mma_commit(smem_u32(&sh.o_done));
-            u += todo;
-            ++items;
         }
-    } else {
+    } else if (w < 8) {
         // ------------------------------------------------------------ softmax
+        regs_inc<kSoftmaxRegs>();
         const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
         const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
         const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
-        uint32_t steps = 0;
-        int items = 0;
+        uint32_t steps = 0, done = 0;
         bool ok = true;
-        const float neg = a.scale < 0.0f ? -1.0f : 1.0f;
         // masked scores are -inf: keep their product with the scale -inf when the scale is 0
-        const float c = (MODE & 1) ? fabsf(a.scale) / a.softcap : fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
-        while (u < u_end && ok) {
-            const int head = static_cast<int>(u / plan.per_head);
-            int off;
-            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
-            const int64_t u0 = u - off;
-            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
-            const bool active = t.rows > 128 * h;
+        const float c = (MODE & 1) ? a.scale / a.softcap : fmaxf(a.scale * kLog2e, 1e-30f);
+        for (int k = 0; ok; ++k) {
+            Work item;
+            ok = next_work(k, item);
+            if (!ok || item.todo == 0) break;
+            const Tile &t = item.t;
+            const int head = item.head, off = item.off, todo = item.todo;
+            if (t.rows <= 128 * h) continue;
 
-            // ---- Q of this half into shared memory (128-byte swizzle)
-            if (active) {
-                const uint16_t *q = static_cast<const uint16_t *>(a.q);
-                const uint32_t flip = neg < 0.0f ? 0x80008000u : 0u;
-                uint8_t *dst = sh.q + h * kTile;
-                // a thread takes one 16-byte column of every kStep-th row, eight loads at a time
-                constexpr int kStep = 128 / (8 * ND);
-                const int ch = tid % (8 * ND), r0 = (tid & 127) / (8 * ND);
-                const bool in = 8 * ch < a.dim;
-#pragma unroll
-                for (int b = 0; b < 128 / kStep; b += 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = r0 + kStep * (b + k);
-                        const uint32_t gr = t.first + 128 * h + r, tk = gr / static_cast<uint32_t>(a.group);
-                        v[k] = make_uint4(0, 0, 0, 0);
-                        if (in && 128 * h + r < t.rows)
-                            v[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                q + (t.tok0 + tk) * a.q_token + (head * a.group + (gr - tk * a.group)) * a.q_head + 8 * ch));
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = r0 + kStep * (b + k);
-                        *reinterpret_cast<uint4 *>(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
-                    }
-                }
-                fence_proxy_async_smem();
-            }
             // ---- this row's keys
-            const int gr = t.first + row, tok = gr / a.group, hq = head * a.group + gr % a.group;
+            const uint32_t gr = t.first + row, tok = gr / static_cast<uint32_t>(a.group);
+            const int hq = head * a.group + static_cast<int>(gr - tok * a.group);
             const bool live = row < t.rows;
             int lo = 0, hi = 0;
             if (live) {
@@ -465,29 +556,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             int in_lo = live ? lo : 0, in_hi = live ? hi : 0x7FFFFFFF;
             in_lo = __reduce_max_sync(0xffffffffu, in_lo);
             in_hi = __reduce_min_sync(0xffffffffu, in_hi);
-            mbar_arrive(smem_u32(&sh.q_ready));
             const float slope = (MODE & 2) && live ? a.slopes[hq] * kLog2e : 0.0f;
             const int rel = live ? static_cast<int>(t.pos0 + tok) : 0;   // position, for the distance
 
             float m = -INFINITY, l = 0.0f;   // maximum in use (of c s, log2) and sum
-            for (int i = 0; i < todo && active; ++i) {
+            for (int i = 0; i < todo; ++i) {
                 const int kb = t.lo + (off + i) * kChunkKeys;
                 ok = wait(sh.s_full[h], steps & 1);
                 if (!ok) break;
                 ++steps;
                 tm_fence_after();
-                // First pass over S, 32 columns at a time: the row's maximum.  Capped,
-                // biased or masked scores are written back for the second pass.
-                const bool edge = kb < in_lo || kb + kChunkKeys > in_hi;
-                const bool back = MODE != 0 || edge;
+                float s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tm_ld32(ts + 32 * q, s[q]);
+                tm_wait_ld32(s[0]);
+#pragma unroll
+                for (int q = 1; q < 4; ++q) tm_here32(s[q]);
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                float s[2][32];
-                tm_ld32(ts, s[0]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float *v = s[q & 1];
-                    tm_wait_ld32(v);
-                    if (q < 3) tm_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+                    float *v = s[q];
                     if (MODE & 1) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -499,20 +587,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             v[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), (MODE & 1) ? v[j] : v[j] * c);
                     }
-                    if (edge) {
+                    if (kb < in_lo || kb + kChunkKeys > in_hi) {
                         const int a0 = lo - kb - 32 * q, a1 = hi - kb - 32 * q;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = j >= a0 && j < a1 ? v[j] : -INFINITY;
                     }
-                    if (back) tm_st32(ts + 32 * q, reinterpret_cast<const uint32_t *>(v));
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = max3(x[k], v[j + 2 * k], v[j + 2 * k + 1]);
+                        for (int z = 0; z < 4; ++z) x[z] = max3(x[z], v[j + 2 * z], v[j + 2 * z + 1]);
                     }
                 }
-                if (back) tm_wait_st();
-                tm_ld32(ts, s[0]);   // second pass, on its way
                 const float mul = MODE ? 1.0f : c;
                 const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * mul;
                 float f = 1.0f;
@@ -524,54 +609,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
                     l *= f;
 #pragma unroll
-                    for (int j = 0; j < DP / 32; ++j) {
-                        float o[32];
-                        tm_ld32(to + 32 * j, o);
-                        tm_wait_ld32(o);
+                    for (int j = 0; j < DP / 16; ++j) {
+                        float o[16];
+                        tm_ld16(to + 16 * j, o);
+                        tm_wait_ld16(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f;
-                        tm_st32(to + 32 * j, reinterpret_cast<const uint32_t *>(o));
+                        for (int z = 0; z < 16; ++z) o[z] *= f;
+                        tm_st16(to + 16 * j, reinterpret_cast<const uint32_t *>(o));
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : m - kShift;
-                // Second pass: exponentials, their sum, and P over the columns already read
                 const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float *v = s[q & 1];
-                    tm_wait_ld32(v);
-                    if (q < 3) tm_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
                     uint32_t p[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    for (int z = 0; z < 16; ++z) {
                         float e0, e1;
-                        unpair(fma2(pair(v[2 * k], v[2 * k + 1]), mul2, base2), e0, e1);
+                        unpair(fma2(pair(s[q][2 * z], s[q][2 * z + 1]), mul2, base2), e0, e1);
                         e0 = ex2(e0), e1 = ex2(e1);
-                        sum[k & 1] = add2(sum[k & 1], pair(e0, e1));
-                        p[k] = pack2(e0, e1, CT);
+                        sum[z & 1] = add2(sum[z & 1], pair(e0, e1));
+                        p[z] = pack2(e0, e1, CT);
                     }
                     tm_st16(ts + 16 * q, p);
+                    if (q & 1) {   // 64 keys of P: the products can start on them
+                        tm_wait_st();
+                        tm_fence_before();
+                        mbar_arrive(smem_u32(&sh.p_ready[h][q >> 1]));
+                    }
                 }
                 float l0, l1;
                 unpair(add2(sum[0], sum[1]), l0, l1);
                 l += l0 + l1;
-                tm_wait_st();
-                tm_fence_before();
-                mbar_arrive(smem_u32(&sh.p_ready[h]));
             }
             if (!ok) break;
 
             // ---- O: divide and store, or leave a partial result ([dim / 4][row] quads, maxima, sums)
-            ok = wait(sh.o_done, items & 1);
+            ok = wait(sh.o_done[h], done & 1);
             if (!ok) break;
-            ++items;
+            ++done;
             tm_fence_after();
-            const bool split = todo < t.units;
-            if (active) {
+            if (todo < t.units) {
                 float *part = a.part + part_slot(cta, off == 0) * (kChunkRows * (DP + 2));
-                const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-                const int64_t at = (t.tok0 + tok) * a.out_token + hq * a.out_head;
 #pragma unroll
                 for (int j = 0; j < DP / 32; ++j) {
                     float o[32];
@@ -579,25 +659,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     tm_wait_ld32(o);
                     if (live) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 v = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
-                            if (split) reinterpret_cast<float4 *>(part)[(8 * j + k / 4) * kChunkRows + row] = v;
-                            else if (32 * j + k < a.dim) store4(a.out, a.out_type, at + 32 * j + k, v);
-                        }
+                        for (int z = 0; z < 8; ++z)
+                            reinterpret_cast<float4 *>(part)[(8 * j + z) * kChunkRows + row] =
+                                make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
                     }
                 }
-                if (live) {
-                    if (split) part[kChunkRows * DP + row] = m, part[kChunkRows * (DP + 1) + row] = l;
-                    else if (a.lse)
-                        a.lse[static_cast<int64_t>(t.tok0 + tok) * a.heads + hq] =
-                            l == 0.0f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+                if (live) part[kChunkRows * DP + row] = m, part[kChunkRows * (DP + 1) + row] = l;
+                if (off == 0 && tid == 0) a.joint[cta] = Joint{t.tok0, t.first, t.rows, head, cta, item.last};
+            } else {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                // through shared memory, so that four lanes write 64 bytes of a row together
+                uint8_t *box_out = sh.out[w];
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    float o[32];
+                    tm_ld32(to + 32 * j, o);
+                    tm_wait_ld32(o);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        *reinterpret_cast<uint4 *>(box_out + lane * 64 + ((z ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(pack2(o[8 * z] * inv, o[8 * z + 1] * inv, a.out_type),
+                                       pack2(o[8 * z + 2] * inv, o[8 * z + 3] * inv, a.out_type),
+                                       pack2(o[8 * z + 4] * inv, o[8 * z + 5] * inv, a.out_type),
+                                       pack2(o[8 * z + 6] * inv, o[8 * z + 7] * inv, a.out_type));
+                    __syncwarp();
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int r = 8 * z + (lane >> 2), ch = lane & 3, d = 32 * j + 8 * ch;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(box_out + r * 64 + ((ch ^ (r >> 1 & 3)) << 4));
+                        const uint32_t g2 = t.first + 32 * w + r, t2 = g2 / static_cast<uint32_t>(a.group);
+                        if (32 * w + r < t.rows && d < a.dim)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (t.tok0 + t2) * a.out_token +
+                                                       (head * a.group + (g2 - t2 * a.group)) * a.out_head + d) = v;
+                    }
+                    __syncwarp();
                 }
-                tm_fence_before();
+                if (live && a.lse)
+                    a.lse[static_cast<int64_t>(t.tok0 + tok) * a.heads + hq] =
+                        l == 0.0f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
             }
-            if (split && off == 0 && tid == 0)
-                a.joint[cta] = Joint{t.tok0, t.first, t.rows, head, cta, share_owner(total, n, u0 + t.units - 1)};
-            u += todo;
+            tm_fence_before();
         }
+    } else {
+        regs_dec<kOtherRegs>();   // (a warpgroup changes its registers together)
     }
     __syncwarp();
     tm_fence_before();

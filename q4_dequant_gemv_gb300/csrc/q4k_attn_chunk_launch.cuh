@@ -20,15 +20,17 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     int box = 128;
     while (a.page_size % box) box /= 2;
     CacheMaps maps;
-    if (!encode_cache(&maps, a, CT, box)) return cudaErrorInvalidValue;
-    a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
+    CUtensorMap qmap;
+    const int tokens = R / a.group;   // of a tile
+    if (!encode_cache(&maps, a, CT, box) || !encode_queries(&qmap, a, CT, tokens)) return cudaErrorInvalidValue;
+    a.slots = a.tokens / tokens + a.batch;
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
     const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
     return launch_split(a, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
-        kern<<<grid, kChunkThreads, kSmem, l.stream>>>(maps, args, box);
+        kern<<<grid, kChunkThreads, kSmem, l.stream>>>(maps, qmap, args, box);
         return cudaGetLastError();
     });
 }

@@ -126,7 +126,7 @@ template <int CT, int PARTS, int NT, int DP>
 struct RowsShared {
     using Sp = RowsShape<DP>;
     static constexpr int R = 8 * NT;
-    using Plan = Split<R, Sp::kUnit, Sp::kThreads, kBlock>;
+    using Plan = Split<Sp::kUnit, Sp::kThreads, kBlock>;
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
     // a warp's ring; when the warps join it holds the warp's O instead
     static constexpr int kRing = Sp::kSlots * 2 * Sp::kSide;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             for (int j = 0; j < SLOTS; ++j) mbar_init(smem_u32(&sh.full[i][j]), 1);
         fence_barrier_init();
     }
-    typename Sh::Plan plan(a, sh.plan);      // synchronises the CTA
+    typename Sh::Plan plan(a, sh.plan, R);   // synchronises the CTA
     const int cta = blockIdx.x;
     int64_t total = 0, u = 0, u_end = 1;
     int n = 0;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             off = t.units * rank / a.cluster;
             todo = t.units * (rank + 1) / a.cluster - off;
         } else {
-            head = static_cast<int>(u / plan.per_head);
+            head = static_cast<int>(quotient(u, plan.per_head));
             t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
             u0 = u - off;
             todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
