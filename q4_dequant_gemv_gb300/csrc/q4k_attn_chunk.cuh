@@ -17,9 +17,9 @@
 //     under the other's products, and P is taken up in two parts.
 //   * warp 9 walks the tiles and tells the others (a ring of two descriptors),
 //     loads the tile's queries (a TMA box of its tokens and the group's heads) as
-//     soon as the last scores of the tile before are done, and K and V (128
-//     keys) through a ring of four stages: a lane per page piece looks the page
-//     up and issues its boxes.
+//     soon as the last scores of the tile before are done, and the keys, two
+//     stages of 128; warp 10 loads the values, two stages: a lane per page piece
+//     looks the page up and issues its boxes.
 // Softmax threads take 200 registers (a row of S and change), the others 96.
 // Tensor memory, all 512 columns: S (and P) of the halves, O of the halves.
 //
@@ -46,14 +46,14 @@ namespace attn {
 
 constexpr int kChunkRows = 256;              // query rows of a tile at most
 constexpr int kChunkKeys = 128;              // keys of a unit
-constexpr int kChunkThreads = 384;           // two softmax warpgroups; MMA, load and two idle warps
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kChunkThreads = 384;           // two softmax warpgroups; MMA, key, value and idle warp
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
 constexpr int kStages = 4;
 // 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
-constexpr uint64_t kChunkWaitNs = 2000000000ull;
+constexpr uint64_t kChunkWaitNs = 2000000000ull, kWindDownNs = 200000000ull;
 
-// A CTA's part of one tile, as the load warp found it.
+// A CTA's part of one tile, as the key warp found it.
 struct Work {
     Tile t;
     int head, off, todo, last;   // units [off, off + todo) of the tile; the CTA that holds the tile's last unit
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(smem_u32(&sh.p_ready[i][1]), 128);
             mbar_init(smem_u32(&sh.o_done[i]), 1);
             mbar_init(smem_u32(&sh.work_full[i]), 1);
-            mbar_init(smem_u32(&sh.work_empty[i]), 9);   // the MMA warp and eight softmax warps
+            mbar_init(smem_u32(&sh.work_empty[i]), 10);   // the MMA, value and eight softmax warps
         }
         mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
@@ -344,30 +344,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         return true;
     };
 
-    if (w == kLoadWarp) {
+    if (w == kKeyWarp || w == kValueWarp) {
         // ------------------------------------------------------------ loads
         regs_dec<kOtherRegs>();
-        int stage = 0, edges = 0;
-        uint32_t round = 0;
-        bool ok = true;
-        unsigned int pending = 0;   // stages whose copies may still be in flight at a wind-down
+        const bool values = w == kValueWarp;
+        const CUtensorMap *map = values ? &maps.v : &maps.k;
+        int unit = 0, edges = 0, k = 0;   // this warp's stage of unit i: 2 (i % 2), + 1 for values
+        bool ok = true, q_sent = false;
         const int per = kChunkKeys / box;
-        int k = 0;
-        for (; u < u_end && ok; ++k) {
-            const int head = static_cast<int>(quotient(u, plan.per_head));
-            int off;
-            const Tile t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
-            const int todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
-            if (k > 1 && !(ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1))) break;
-            if (lane == 0) {
-                sh.work[k & 1] = Work{t, head, off, todo, share_owner(total, n, u - off + t.units - 1)};
-                mbar_arrive(smem_u32(&sh.work_full[k & 1]));
+        for (; ok; ++k) {
+            Work item;
+            if (values) {
+                ok = next_work(k, item);
+                if (!ok || item.todo == 0) break;
+            } else {
+                // the key warp finds the tiles and tells the others (todo = 0: no more)
+                if (k > 1 && !(ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1))) break;
+                item.todo = 0;
+                if (u < u_end) {
+                    item.head = static_cast<int>(quotient(u, plan.per_head));
+                    item.t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(item.head) * plan.per_head), item.off);
+                    item.todo = static_cast<int>(min(static_cast<int64_t>(item.t.units - item.off), u_end - u));
+                    item.last = share_owner(total, n, u - item.off + item.t.units - 1);
+                    u += item.todo;
+                }
+                if (lane == 0) {
+                    sh.work[k & 1] = item;
+                    mbar_arrive(smem_u32(&sh.work_full[k & 1]));
+                }
+                __syncwarp();
+                if (item.todo == 0) break;
             }
-            __syncwarp();
+            const Tile &t = item.t;
             const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
             const uint32_t psize = static_cast<uint32_t>(a.page_size);
-            for (int i = 0; i < todo && ok; ++i) {
-                const int kb = t.lo + (off + i) * kChunkKeys;
+            for (int i = 0; i < item.todo && ok; ++i, ++unit) {
+                const int kb = t.lo + (item.off + i) * kChunkKeys;
+                const int stage = 2 * (unit & 1) + (values ? 1 : 0);
                 // lane j: piece j of the tile
                 const int key = kb + lane * box;
                 bool live = lane < per && key + box > t.from && key < t.hi;
@@ -382,78 +395,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                 }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * static_cast<uint32_t>(box) * 128u * ND;
-                const bool edge = kb < t.from || kb + kChunkKeys > t.hi;
+                if (unit > 1 && !(ok = wait(sh.empty[stage], ((unit >> 1) - 1) & 1))) break;
+                uint8_t *dst = sh.kv + stage * kTile;
+                const bool clean = values && (kb < t.from || kb + kChunkKeys > t.hi);
+                unsigned long long &bar = clean ? sh.edge : sh.full[stage];
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes);
+                __syncwarp();
+                if (live) {
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (round > 0 && !wait(sh.empty[stage], (round - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *dst = sh.kv + stage * kTile;
-                    const bool clean = kv == 1 && edge;
-                    unsigned long long &bar = clean ? sh.edge : sh.full[stage];
-                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes);
-                    __syncwarp();
-                    if (live) {
+                    for (int h = 0; h < ND; ++h)
+                        load_box(smem_u32(dst + h * kHalf + lane * box * 128), map, 64 * h, slot, item.head, page,
+                                 smem_u32(&bar));
+                }
+                if (i == 0 && !values) {
+                    // the tile's queries, once the last scores of the tile before are done
+                    if (k > 0 && !(ok = wait(sh.q_empty, (k - 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(smem_u32(&sh.q_full), tokens * a.group * 128 * ND);
 #pragma unroll
                         for (int h = 0; h < ND; ++h)
-                            load_box(smem_u32(dst + h * kHalf + lane * box * 128), kv ? &maps.v : &maps.k, 64 * h, slot,
-                                     head, page, smem_u32(&bar));
+                            load_rows(smem_u32(sh.q + h * 2 * kHalf), &qmap, 64 * h, item.head * a.group,
+                                      t.tok0 + t.first / a.group, smem_u32(&sh.q_full));
                     }
-                    if (i == 0 && kv == 0) {
-                        // the tile's queries, once the last scores of the tile before are done
-                        if (k > 0 && !wait(sh.q_empty, (k - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(smem_u32(&sh.q_full), tokens * a.group * 128 * ND);
-#pragma unroll
-                            for (int h = 0; h < ND; ++h)
-                                load_rows(smem_u32(sh.q + h * 2 * kHalf), &qmap, 64 * h, head * a.group,
-                                          t.tok0 + t.first / a.group, smem_u32(&sh.q_full));
-                        }
-                        __syncwarp();
+                    q_sent = true;
+                    __syncwarp();
+                }
+                if (clean) {
+                    // zero the rows that nothing of the tile sees, then hand the stage on
+                    if (!(ok = wait(sh.edge, edges & 1))) break;
+                    ++edges;
+                    const int r0 = max(0, t.from - kb), r1 = min(kChunkKeys, t.hi - kb);
+                    for (int r = 0; r < kChunkKeys; ++r) {
+                        if (r >= r0 && r < r1) continue;
+                        if (lane < 8 * ND)
+                            *reinterpret_cast<uint4 *>(dst + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
                     }
-                    if (clean) {
-                        // zero the rows that nothing of the tile sees, then hand the stage on
-                        if (!wait(sh.edge, edges & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        ++edges;
-                        const int r0 = max(0, t.from - kb), r1 = min(kChunkKeys, t.hi - kb);
-                        for (int r = 0; r < kChunkKeys; ++r) {
-                            if (r >= r0 && r < r1) continue;
-                            if (lane < 8 * ND)
-                                *reinterpret_cast<uint4 *>(dst + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sh.full[stage]));
-                    }
-                    pending |= 1u << stage;
-                    if (++stage == kStages) stage = 0, ++round;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[stage]));
                 }
             }
-            u += todo;
         }
-        if (ok) {
-            // no more tiles
-            if (k > 1) ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1);
-            if (ok && lane == 0) {
-                sh.work[k & 1].todo = 0;
-                mbar_arrive(smem_u32(&sh.work_full[k & 1]));
-            }
-        } else {
-            // every copy issued lands before the CTA exits
-            for (int s = 0; s < kStages; ++s)
-                if (pending >> s & 1) {
-                    const uint32_t r = s < stage ? round : round - 1;
-                    (void)mbar_wait_bounded(smem_u32(&sh.full[s]), r & 1, kChunkWaitNs);
-                }
-            (void)mbar_wait_bounded(smem_u32(&sh.q_full), (k - 1) & 1, kChunkWaitNs);
+        if (!ok) {
+            // every copy issued lands before the CTA exits: this warp's last two stages, the queries
+            for (int i = max(0, unit - 1); i <= unit; ++i)
+                (void)mbar_wait_bounded(smem_u32(&sh.full[2 * (i & 1) + (values ? 1 : 0)]), (i >> 1) & 1, kWindDownNs);
+            if (q_sent) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, kWindDownNs);
         }
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
