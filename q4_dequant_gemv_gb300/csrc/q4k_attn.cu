@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R,
     const int lanes = kJoinThreads / span, parts = t.c1 - t.c0 + 1;
     const float *first = a.part + part_slot(t.c0, true) * size, *rest = a.part + part_slot(t.c0, false) * size;
     auto slot = [&](int q) { return q == 0 ? first : rest + 2 * q * size; };
+    const int row = t.first + r;
     float mx = -INFINITY, ls = 0.0f;
 #pragma unroll 8
     for (int q = 0; q < parts; ++q) mx = fmaxf(mx, __ldcg(slot(q) + R * width + r));
@@ -121,7 +122,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R,
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int x = c + k * lanes;
-            if (4 * x < a.dim) finish_row(a, t.tok0, t.first + r, t.head, 4 * x, v[k], mx, ls, shift);
+            if (4 * x < a.dim)
+                finish_row(a, t.tok0 + row / a.group, t.head * a.group + row % a.group, 4 * x, v[k], mx, ls, shift);
         }
     }
 }
@@ -174,14 +176,18 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     p.out_token = a->out_token_stride, p.out_head = a->out_head_stride;
     p.k_page = c->k_page_stride, p.k_slot = c->k_slot_stride, p.k_head = c->k_head_stride;
     p.v_page = c->v_page_stride, p.v_slot = c->v_slot_stride, p.v_head = c->v_head_stride;
-    p.table_stride = c->page_table_stride, p.page_size = c->page_size;
+    p.table_stride = c->page_table_stride, p.page_size = static_cast<int>(c->page_size);
+    p.page_shift = -1;
+    if ((c->page_size & (c->page_size - 1)) == 0)
+        for (p.page_shift = 0; (int64_t{1} << p.page_shift) < c->page_size;) ++p.page_shift;
     p.page_table = c->page_table, p.seq_start = c->seq_start, p.kv_len = c->kv_len;
     p.prefix_len = a->prefix_len, p.kv_start = a->kv_start, p.slopes = a->slopes;
-    // positions are 32-bit in the kernels, with room for the last unit's end
-    const int64_t most = 0x7FFFFFFF - 4096;
+    // positions are 32-bit in the kernels, with room above them
+    const int64_t most = 0x3FFFFFFF;
     const int64_t per = c->pages > 0 ? c->max_pages : 0;
-    p.capacity = per > most / c->page_size ? most : per * c->page_size;
-    p.window = a->window, p.scale = a->scale, p.softcap = a->softcap;
+    p.capacity = static_cast<int>(per > most / c->page_size ? most : per * c->page_size);
+    // a window past every position is none
+    p.window = a->window > most ? 0 : static_cast<int>(a->window), p.scale = a->scale, p.softcap = a->softcap;
     p.pages = static_cast<int>(c->pages), p.batch = static_cast<int>(c->batch);
     p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
     p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);

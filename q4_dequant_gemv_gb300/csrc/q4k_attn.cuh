@@ -50,11 +50,13 @@ struct Args {
     float *lse;
     int64_t q_token, q_head, out_token, out_head;        // strides in elements
     int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
-    int64_t table_stride, page_size;
+    int64_t table_stride;
+    int page_size;
     const int32_t *page_table, *seq_start, *kv_len, *prefix_len, *kv_start;
     const float *slopes;
-    int64_t capacity;      // cached positions a page table row can hold
-    int64_t window;        // 0: none
+    int capacity;          // cached positions a page table row can hold
+    int window;            // 0: none
+    int page_shift;        // page_size = 1 << page_shift, or -1
     float scale, softcap;
     int pages, batch, tokens, heads, kv_heads, group, dim;
     int q_type, out_type, causal;
@@ -78,7 +80,7 @@ __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * 
 struct Tile {
     int seq, first, rows;      // first row in the sequence, number of rows (0: nothing to do)
     int tok0, ntok;            // first token row of the sequence in the call, its tokens
-    int64_t pos0;              // position of the sequence's first new token
+    int pos0;                  // position of the sequence's first new token
     int len;                   // cached positions (clamped to the page table)
     int from, hi;              // keys [from, hi) that some row sees
     int lo;                    // `from` rounded down to a multiple of ALIGN: where unit 0 starts
@@ -86,21 +88,22 @@ struct Tile {
 };
 
 struct Range {
-    int64_t lo, hi;
+    int lo, hi;
 };
 
-// Keys that the new token i of the tile's sequence sees.
-__device__ __forceinline__ Range token_range(const Args &a, int seq, int64_t pos, int tok, int len)
+// Keys that the new token in row `tok` of the call, at position pos, sees.
+// (Lengths leave room above positions, so nothing here overflows.)
+__device__ __forceinline__ Range token_range(const Args &a, int seq, int pos, int tok, int len)
 {
     Range r{0, len};
     if (a.causal) {
-        int64_t h = pos + 1;
-        if (a.prefix_len) h = max(h, static_cast<int64_t>(a.prefix_len[seq]));
-        r.hi = min(h, static_cast<int64_t>(len));
+        int h = pos + 1;
+        if (a.prefix_len) h = max(h, a.prefix_len[seq]);
+        r.hi = min(h, len);
     }
     if (a.window) r.lo = max(r.lo, pos + 1 - a.window);
-    if (a.kv_start) r.lo = max(r.lo, static_cast<int64_t>(a.kv_start[tok]));
-    r.hi = max(r.hi, static_cast<int64_t>(0));
+    if (a.kv_start) r.lo = max(r.lo, a.kv_start[tok]);
+    r.hi = max(r.hi, 0);
     r.lo = min(r.lo, r.hi);
     return r;
 }
@@ -135,7 +138,10 @@ struct Split {
         return static_cast<int>(static_cast<uint32_t>(start_of(b)) * static_cast<uint32_t>(a.group) / static_cast<uint32_t>(R));
     }
 
-    __device__ __forceinline__ Tile tile(int slot, bool report) const
+    // The tile of a slot.  WARP: by a whole warp, reporting lengths that do not fit
+    // the page table; else by one thread, for calls without kv_start.
+    template <bool WARP>
+    __device__ __forceinline__ Tile tile(int slot) const
     {
         Tile t{};
         int b = slot, j = 0;
@@ -149,29 +155,32 @@ struct Split {
             }
             j = x - extra(b) + 1;
         }
-        const int s0 = start_of(b), n = start_of(b + 1) - s0;
+        const int s0 = start_of(b), n = start_of(b + 1) - s0, all = n * a.group;
         const int raw = a.batch <= kSeqs ? sh.len[b] : a.kv_len[b];
         t.seq = b, t.tok0 = s0, t.ntok = n;
-        if (n <= 0 || j < 0 || j > (n * a.group - 1) / R) return t;
+        if (n <= 0 || j < 0 || j > (all - 1) / R) return t;
         t.first = j * R;
-        t.rows = min(R, n * a.group - t.first);
-        t.len = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), a.capacity));
-        if (report && (raw < 0 || raw > a.capacity)) atomicOr(a.error, 4u);
-        t.pos0 = static_cast<int64_t>(raw) - n;
-        const int i0 = t.first / a.group, i1 = (t.first + t.rows - 1) / a.group;
+        t.rows = min(R, all - t.first);
+        t.len = min(max(raw, 0), a.capacity);
+        if (WARP && (raw < 0 || raw > a.capacity)) atomicOr(a.error, 4u);
+        t.pos0 = max(raw, -1) - n;
+        // its tokens (all of them where one tile holds the sequence)
+        int i0 = 0, i1 = n - 1;
+        if (all > R) i0 = t.first / a.group, i1 = (t.first + t.rows - 1) / a.group;
         const Range last = token_range(a, b, t.pos0 + i1, s0 + i1, t.len);
-        int64_t lo = last.hi;
-        if (a.kv_start) {
-            for (int i = i0; i <= i1; ++i) {
+        int lo = last.hi;
+        if (WARP && a.kv_start) {
+            for (int i = i0 + static_cast<int>(threadIdx.x & 31); i <= i1; i += 32) {
                 const Range r = token_range(a, b, t.pos0 + i, s0 + i, t.len);
                 if (r.hi > r.lo) lo = min(lo, r.lo);
             }
+            lo = __reduce_min_sync(0xffffffffu, lo);
         } else {
             lo = min(lo, token_range(a, b, t.pos0 + i0, s0 + i0, t.len).lo);
         }
-        t.hi = static_cast<int>(last.hi);
-        t.from = static_cast<int>(lo);
-        t.lo = t.from & ~(ALIGN - 1);
+        t.hi = last.hi;
+        t.from = lo;
+        t.lo = lo & ~(ALIGN - 1);
         t.units = t.hi > t.lo ? (t.hi - t.lo + U - 1) / U : 1;   // a tile that sees nothing still writes its zeros
         return t;
     }
@@ -199,9 +208,21 @@ struct Split {
         constexpr int PER = (kStripes + THREADS - 1) / THREADS;   // consecutive prefix entries of a thread
         uint32_t sum[PER], run = 0;
         const int e0 = tid * PER;
+        if (a.kv_start) {   // a warp per entry: its lanes share a tile's tokens
+            for (int e = tid >> 5; e < kStripes; e += THREADS / 32) {
+                uint32_t units = 0;
+                for (int s = e * stripe; s < min((e + 1) * stripe, a.slots); ++s) units += tile<true>(s).units;
+                if ((tid & 31) == 0) sh.prefix[e] = units;
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            for (int s = (e0 + j) * stripe; s < min((e0 + j + 1) * stripe, a.slots); ++s) run += tile(s, false).units;
+            if (a.kv_start) {
+                if (e0 + j < kStripes) run += sh.prefix[e0 + j];
+            } else {
+                for (int s = (e0 + j) * stripe; s < min((e0 + j + 1) * stripe, a.slots); ++s) run += tile<false>(s).units;
+            }
             sum[j] = run;
         }
         uint32_t incl = run;
@@ -225,7 +246,7 @@ struct Split {
         __syncthreads();
     }
 
-    // The tile that holds unit r (< per_head) of a cache head, and r's place in it.
+    // The tile that holds unit r (< per_head) of a cache head, and r's place in it; whole warps.
     __device__ __forceinline__ Tile locate(uint32_t r, int &offset) const
     {
         int lo = 0, hi = kStripes - 1;
@@ -235,7 +256,7 @@ struct Split {
         }
         uint32_t at = lo ? sh.prefix[lo - 1] : 0;
         for (int s = lo * stripe;; ++s) {
-            const Tile t = tile(s, true);
+            const Tile t = tile<true>(s);
             if (at + t.units > r || s + 1 >= a.slots) {
                 offset = static_cast<int>(r - at);
                 return t;
@@ -295,18 +316,28 @@ __device__ __forceinline__ void store4(void *out, int type, int64_t i, float4 v)
     }
 }
 
-// Four outputs from d on of a sequence's row (its first token in row tok0 of the
-// call): v / ls; and the row's lse with d = 0.  m and ls as the kernels keep them:
-// log2 domain, ls carrying 2^shift.
-__device__ __forceinline__ void finish_row(const Args &a, int tok0, int row, int head, int d, float4 v, float m, float ls,
-                                           float shift)
+// Four outputs from d on of query head hq in row tok of the call: v / ls; and the
+// row's lse with d = 0.  m and ls as the kernels keep them: log2 domain, ls
+// carrying 2^shift.
+__device__ __forceinline__ void finish_row(const Args &a, int64_t tok, int hq, int d, float4 v, float m, float ls, float shift)
 {
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const int hq = head * a.group + row % a.group;
-    const int64_t tok = tok0 + row / a.group;
     store4(a.out, a.out_type, tok * a.out_token + hq * a.out_head + d,
            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
     if (a.lse && d == 0) a.lse[tok * a.heads + hq] = ls == 0.0f ? -INFINITY : (m + log2f(ls) - shift) * kLn2;
+}
+
+// Page (index into the sequence's table) and slot of a cached position.
+__device__ __forceinline__ void page_of(const Args &a, int key, int &entry, int &slot)
+{
+    entry = a.page_shift >= 0 ? key >> a.page_shift
+                              : static_cast<int>(static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size));
+    slot = key - entry * a.page_size;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // The cache as two 4-D tensors [page][head][slot][d], and a box of one cache

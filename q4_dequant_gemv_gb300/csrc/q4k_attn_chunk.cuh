@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         fence_barrier_init();
         sh.abort = 0;
     }
+    if (tid == 32) prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&qmap);
     tm_fence_before();
     typename Sh::Plan plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
     plan.scan();
@@ -377,7 +378,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             const Tile &t = item.t;
             const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
-            const uint32_t psize = static_cast<uint32_t>(a.page_size);
             for (int i = 0; i < item.todo && ok; ++i, ++unit) {
                 const int kb = t.lo + (item.off + i) * kChunkKeys;
                 const int stage = 2 * (unit & 1) + (values ? 1 : 0);
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 bool live = lane < per && key + box > t.from && key < t.hi;
                 int page = 0, slot = 0;
                 if (live) {
-                    const uint32_t e = static_cast<uint32_t>(key) / psize;
-                    slot = key - e * psize;
+                    int e;
+                    page_of(a, key, e, slot);
                     page = pages[e];
                     if (page < 0 || page >= a.pages) {
                         atomicOr(a.error, 4u);
@@ -538,14 +538,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             int lo = 0, hi = 0;
             if (live) {
                 const Range r = token_range(a, t.seq, t.pos0 + tok, t.tok0 + tok, t.len);
-                lo = static_cast<int>(r.lo), hi = static_cast<int>(r.hi);
+                lo = r.lo, hi = r.hi;
             }
             // keys that every live row of the warp sees need no mask
             int in_lo = live ? lo : 0, in_hi = live ? hi : 0x7FFFFFFF;
             in_lo = __reduce_max_sync(0xffffffffu, in_lo);
             in_hi = __reduce_min_sync(0xffffffffu, in_hi);
             const float slope = (MODE & 2) && live ? a.slopes[hq] * kLog2e : 0.0f;
-            const int rel = live ? static_cast<int>(t.pos0 + tok) : 0;   // position, for the distance
+            const int rel = live ? t.pos0 + static_cast<int>(tok) : 0;   // position, for the distance
 
             float m = -INFINITY, l = 0.0f;   // maximum in use (of c s, log2) and sum
             for (int i = 0; i < todo; ++i) {

@@ -38,14 +38,15 @@ constexpr int kMaxCluster = 8;               // portable cluster size
 constexpr int kBlock = 16;                   // keys of a ring slot
 constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
-// Warps of a CTA and slots of a warp's ring, by head size: 160 to 192 KB of ring.
-template <int DP>
+// Warps of a CTA and slots of a warp's ring, by head size and rows: 128 to 192 KB
+// of ring (what else the larger tiles keep in shared memory leaves two slots).
+template <int NT, int DP>
 struct RowsShape {
     static constexpr int kWarps = DP == 256 ? 4 : 8;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kUnit = kBlock * kWarps;          // keys per unit
     static constexpr int kSide = kBlock * DP * 2;          // bytes of K (or V) in a slot
-    static constexpr int kSlots = DP == 64 ? 5 : 3;
+    static constexpr int kSlots = DP == 64 ? 5 : NT * DP >= 512 ? 2 : 3;
 };
 
 template <int CT>
@@ -85,14 +86,14 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
-__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr)
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, float4 v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_cluster_v2(uint32_t addr, float x, float y)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
 // 16 bytes global -> shared, or 16 zero bytes.
@@ -124,29 +125,32 @@ constexpr float rows_shift()
 
 template <int CT, int PARTS, int NT, int DP>
 struct RowsShared {
-    using Sp = RowsShape<DP>;
+    using Sp = RowsShape<NT, DP>;
     static constexpr int R = 8 * NT;
     using Plan = Split<Sp::kUnit, Sp::kThreads, kBlock>;
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
     // a warp's ring; when the warps join it holds the warp's O instead
-    static constexpr int kRing = Sp::kSlots * 2 * Sp::kSide;
-    static_assert((R + R / Sp::kWarps) * kRed * 4 <= kRing, "O of a warp and the sums of its rows fit in its ring");
+    static constexpr int kSlotBytes = Sp::kSlots * 2 * Sp::kSide, kOBytes = (R * kRed * 4 + 1023) / 1024 * 1024;
+    static constexpr int kRing = kSlotBytes > kOBytes ? kSlotBytes : kOBytes;
     uint8_t ring[Sp::kWarps][kRing];
     typename Plan::Shared plan;
     uint4 q[PARTS][NT][DP / 32][32];       // B fragments of Q, lane-major
     float m[Sp::kWarps][R], l[Sp::kWarps][R];
     float scale[R], slope[R];
     int lo[R], hi[R], pos[R];              // visible keys of each row, its token
-    float wm[R], wl[R];                    // joined statistics
+    // what the ranks of a cluster send: their O for this rank's columns ([rank][row][column
+    // quad], whatever the number of ranks), and their statistics
+    float4 sent[R * (DP / 4)];
+    float2 stat[kMaxCluster][R];
     unsigned long long full[Sp::kWarps][Sp::kSlots];
 };
 
 // TMA: slots filled by tensor copies (maps), else by cp.async.
 template <int CT, int PARTS, int NT, int DP, bool TMA>
-__global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
+__global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
 {
     using Sh = RowsShared<CT, PARTS, NT, DP>;
-    using Sp = RowsShape<DP>;
+    using Sp = RowsShape<NT, DP>;
     constexpr int R = Sh::R, ND = DP / 64, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
     constexpr int kHalf = kBlock * 128;      // bytes of 16 rows of 64 elements
     constexpr float kShift = rows_shift<CT>();
@@ -158,8 +162,10 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         for (int i = 0; i < WARPS; ++i)
             for (int j = 0; j < SLOTS; ++j) mbar_init(smem_u32(&sh.full[i][j]), 1);
         fence_barrier_init();
+        prefetch_map(&maps.k), prefetch_map(&maps.v);
     }
-    typename Sh::Plan plan(a, sh.plan, R);   // synchronises the CTA
+    if (a.cluster > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
+    typename Sh::Plan plan(a, sh.plan, R);         // synchronises the CTA
     const int cta = blockIdx.x;
     int64_t total = 0, u = 0, u_end = 1;
     int n = 0;
@@ -173,7 +179,6 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
     }
 
-    const int psize = static_cast<int>(a.page_size);
     const uint32_t ring = smem_u32(sh.ring[w]);
     // ldmatrix addresses within a slot: row of the lane, chunk before the swizzle
     const int krow = (lane & 7) + 8 * ((lane >> 3) & 1), kch = lane >> 4;
@@ -188,8 +193,11 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         if (a.cluster) {
             // a cluster per tile and cache head, equal shares of its units
             const int item = cta / a.cluster, rank = cta - item * a.cluster;
-            t = plan.tile(item / a.kv_heads, true);
-            if (!t.rows) return;
+            t = plan.template tile<true>(item / a.kv_heads);
+            if (!t.rows) {
+                if (a.cluster > 1) cluster_wait_acquire();
+                return;
+            }
             head = item % a.kv_heads;
             off = t.units * rank / a.cluster;
             todo = t.units * (rank + 1) / a.cluster - off;
@@ -204,13 +212,15 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
         const int kb0 = t.lo + off * Sp::kUnit + kBlock * w;
         const int count = good && kb0 < t.hi ? min(todo, (t.hi - kb0 + Sp::kUnit - 1) / Sp::kUnit) : 0;
-        // pages of the next 32 blocks, a lane each (TMA)
-        int ids = 0;
+        // pages and slots of the next 32 blocks, a lane each (TMA)
+        int ids = 0, slots = 0;
         auto look = [&](int first) {
             const int i = first + lane;
-            ids = 0;
+            ids = slots = 0;
             if (i < count) {
-                ids = pages[(kb0 + i * Sp::kUnit) / psize];
+                int e;
+                page_of(a, kb0 + i * Sp::kUnit, e, slots);
+                ids = pages[e];
                 if (ids < 0 || ids >= a.pages) {
                     atomicOr(a.error, 4u);
                     ids = 0;
@@ -219,14 +229,12 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         };
         auto fill = [&](int i) {
             const int s = static_cast<int>(fills % SLOTS);
-            const int kb = kb0 + i * Sp::kUnit;
             const uint32_t dst = ring + s * 2 * Sp::kSide;
             if constexpr (TMA) {
-                if ((i & 31) == 0) look(i);
-                const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+                if (i > 0 && (i & 31) == 0) look(i);
+                const int page = __shfl_sync(0xffffffffu, ids, i & 31), slot = __shfl_sync(0xffffffffu, slots, i & 31);
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&sh.full[w][s]);
-                    const int slot = kb % psize;
                     mbar_arrive_expect_tx(bar, 2 * Sp::kSide);
 #pragma unroll
                     for (int h = 0; h < ND; ++h) {
@@ -236,12 +244,12 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 }
             } else {
                 // lane r < 16 finds row r
-                const int key = kb + (lane & 15);
+                const int key = kb0 + i * Sp::kUnit + (lane & 15);
                 const bool seen = key >= t.from && key < t.hi;
                 int page = 0, slot = 0;
                 if (seen) {
-                    const int e = key / psize;
-                    slot = key - e * psize;
+                    int e;
+                    page_of(a, key, e, slot);
                     page = pages[e];
                     if (page < 0 || page >= a.pages) {
                         atomicOr(a.error, 4u);
@@ -265,6 +273,37 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             }
             ++fills;
         };
+        // row r of the tile: its token and its query head (divisions of small numbers)
+        const int i0 = t.first ? t.first / a.group : 0, rem = t.first - i0 * a.group;
+        const uint32_t inv = a.group < 32 ? 65536u / a.group + 1u : 0u;   // exact below 64
+        auto token_of = [&](int r, int &hq) {
+            const int x = rem + r, q = a.group < 32 ? static_cast<int>(x * inv >> 16) : (x >= a.group ? 1 : 0);
+            hq = head * a.group + x - q * a.group;
+            return i0 + q;
+        };
+
+        // ---- loads on their way: pages, queries (a warp per row), then the first slots
+        if constexpr (TMA) look(0);
+        constexpr int PER = R / WARPS;   // rows of a warp: w, w + WARPS, ..
+        static_assert(PER * WARPS == R, "whole rows per warp");
+        float x[PER][DP / 32];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int r = w + k * WARPS;
+            int hq;
+            const int tok = token_of(r, hq);
+            const int64_t base = (t.tok0 + tok) * a.q_token + hq * a.q_head;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                const int d = 32 * c + lane;
+                x[k][c] = 0.0f;
+                if (r < t.rows && d < a.dim) {
+                    if (a.q_type == Q4K_F32) x[k][c] = static_cast<const float *>(a.q)[base + d];
+                    else if (a.q_type == Q4K_F16) x[k][c] = __half2float(static_cast<const __half *>(a.q)[base + d]);
+                    else x[k][c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[base + d]);
+                }
+            }
+        }
         const uint32_t first_fill = fills;
         if constexpr (TMA) fence_proxy_async_smem();   // (the ring may have held the previous tile's O)
         for (int i = 0; i < SLOTS; ++i) {
@@ -273,23 +312,15 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
         }
 
         // ---- the tile's rows: scale, visible range, fragments of Q
-        for (int r = w; r < R; r += WARPS) {   // a warp per row
-            const bool live = r < t.rows;
-            const int row = t.first + r, tok = row / a.group, hq = head * a.group + row % a.group;
-            float x[DP / 32];
-            float mx = 0.0f;
-            const int64_t base = (t.tok0 + tok) * a.q_token + hq * a.q_head;
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-                const int d = 32 * c + lane;
-                x[c] = 0.0f;
-                if (live && d < a.dim) {
-                    if (a.q_type == Q4K_F32) x[c] = static_cast<const float *>(a.q)[base + d];
-                    else if (a.q_type == Q4K_F16) x[c] = __half2float(static_cast<const __half *>(a.q)[base + d]);
-                    else x[c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[base + d]);
-                }
-                mx = fmaxf(mx, fabsf(x[c]));
-            }
+        for (int k = 0; k < PER; ++k) {
+            const int r = w + k * WARPS;
+            const bool live = r < t.rows;
+            int hq;
+            const int tok = token_of(r, hq);
+            float mx = 0.0f;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) mx = fmaxf(mx, fabsf(x[k][c]));
             int e = 0;
             if (PARTS > 1 && CT == Q4K_F16) {   // max|q| to [2^14, 2^15)
 #pragma unroll
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 // d = 32 c + 16 i + 8 j + 2 t + b: half b of word 2 i + j of lane 4 (r % 8) + t
-                float v = x[c] * up;
+                float v = x[k][c] * up;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
                     const uint32_t h = pack2(v, 0.0f, CT);
@@ -314,7 +345,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             if (lane == 0) {
                 Range v{0, 0};
                 if (live) v = token_range(a, t.seq, t.pos0 + tok, t.tok0 + tok, t.len);
-                sh.lo[r] = static_cast<int>(v.lo), sh.hi[r] = static_cast<int>(v.hi);
+                sh.lo[r] = v.lo, sh.hi[r] = v.hi;
                 sh.pos[r] = tok;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                 sh.scale[r] = (a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e) * down;
@@ -483,11 +514,23 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
             }
         __syncthreads();
         const bool split = a.cluster ? a.cluster > 1 : todo < t.units;
-        // the CTA's own sum of row r, where a cluster joins: behind the O of a warp
-        auto sum_row = [&](int r) {
-            constexpr int PER = R / WARPS;
-            return reinterpret_cast<float *>(sh.ring[r / PER]) + (R + r % PER) * Sh::kRed;
-        };
+        const bool send = a.cluster > 1;
+        constexpr int DQ = DP / 4;                           // column quads
+        const int share = send ? DQ / a.cluster : DQ;        // of a rank
+        if (send) {
+            cluster_wait_acquire();   // every CTA of the cluster has started
+            // the row statistics of this CTA, to every rank
+            const int rank = cta % a.cluster;
+            for (int i = tid; i < R * a.cluster; i += THREADS) {
+                const int r = i % R;
+                float mx = -INFINITY, ls = 0.0f;
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) mx = fmaxf(mx, sh.m[k][r]);
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) ls += sh.l[k][r] * weight(sh.m[k][r], mx);
+                st_shared_cluster_v2(map_shared_rank(smem_u32(&sh.stat[rank][r]), i / R), mx, ls);
+            }
+        }
         float *part = a.part + part_slot(cta, off == 0) * (R * (DP + 2));
         for (int i = tid; i < t.rows * (DP / 4); i += THREADS) {
             const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
@@ -503,47 +546,40 @@ __global__ void __launch_bounds__(RowsShape<DP>::kThreads, 1) rows_kernel(const 
                 v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
             }
             if (d >= a.dim) continue;
-            if (split && a.cluster) {
-                *reinterpret_cast<float4 *>(sum_row(r) + d) = v;
-                if (d == 0) sh.wm[r] = mx, sh.wl[r] = ls;
+            if (send) {   // to the rank that owns the columns
+                const int q = d / 4, to = q / share;
+                st_shared_cluster_v4(map_shared_rank(smem_u32(&sh.sent[(cta % a.cluster * R + r) * share + q - to * share]), to), v);
             } else if (split) {
                 reinterpret_cast<float4 *>(part)[d / 4 * R + r] = v;
                 if (d == 0) part[R * DP + r] = mx, part[R * DP + R + r] = ls;
             } else {
-                finish_row(a, t.tok0, t.first + r, head, d, v, mx, ls, kShift);
+                int hq;
+                const int tok = token_of(r, hq);
+                finish_row(a, t.tok0 + tok, hq, d, v, mx, ls, kShift);
             }
         }
 
-        if (split && a.cluster) {
-            // ---- a cluster: each CTA adds its share of the outputs over the ranks, in key order
+        if (send) {
+            // ---- a cluster: each CTA adds its columns over the ranks, in key order
             __syncthreads();
             cluster_sync_all();
-            const int rank = cta % a.cluster, outs = t.rows * (DP / 4);
-            for (int i = outs * rank / a.cluster + tid; i < outs * (rank + 1) / a.cluster; i += THREADS) {
-                const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+            const int rank = cta % a.cluster;
+            for (int i = tid; i < t.rows * share; i += THREADS) {
+                const int r = i / share, d = 4 * (rank * share + i - r * share);
                 if (d >= a.dim) continue;
-                const uint32_t am = smem_u32(&sh.wm[r]), al = smem_u32(&sh.wl[r]), av = smem_u32(sum_row(r) + d);
-                float pm[kMaxCluster], mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < a.cluster) {
-                        pm[c] = ld_shared_cluster_f32(map_shared_rank(am, c));
-                        mx = fmaxf(mx, pm[c]);
-                    }
+                float mx = -INFINITY, ls = 0.0f;
+                for (int c = 0; c < a.cluster; ++c) mx = fmaxf(mx, sh.stat[c][r].x);
                 float4 v = make_float4(0, 0, 0, 0);
-                float ls = 0.0f;
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < a.cluster) {
-                        const float f = weight(pm[c], mx);
-                        const float4 x = ld_shared_cluster_v4(map_shared_rank(av, c));
-                        ls += f * ld_shared_cluster_f32(map_shared_rank(al, c));
-                        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
-                    }
-                finish_row(a, t.tok0, t.first + r, head, d, v, mx, ls, kShift);
+                for (int c = 0; c < a.cluster; ++c) {
+                    const float f = weight(sh.stat[c][r].x, mx);
+                    const float4 x = sh.sent[c * R * share + i];
+                    ls += f * sh.stat[c][r].y;
+                    v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+                }
+                int hq;
+                const int tok = token_of(r, hq);
+                finish_row(a, t.tok0 + tok, hq, d, v, mx, ls, kShift);
             }
-            __syncthreads();
-            cluster_sync_all();   // nobody leaves while its memory is read
         } else if (split && off == 0 && tid == 0) {
             a.joint[cta] = Joint{t.tok0, t.first, t.rows, head, cta, share_owner(total, n, u0 + t.units - 1)};
         }

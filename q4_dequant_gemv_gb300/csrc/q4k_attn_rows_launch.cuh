@@ -14,7 +14,7 @@ template <int CT, int PARTS, int NT, int DP, bool TMA>
 static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
     using Sh = RowsShared<CT, PARTS, NT, DP>;
-    using Sp = RowsShape<DP>;
+    using Sp = RowsShape<NT, DP>;
     auto kern = rows_kernel<CT, PARTS, NT, DP, TMA>;
     Args a = l.args;
     constexpr int R = Sh::R;
@@ -23,7 +23,7 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     CacheMaps maps;
     if (TMA && !encode_cache(&maps, a, CT, kBlock)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
-    const int64_t units = (a.capacity + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
+    const int64_t units = (static_cast<int64_t>(a.capacity) + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
 
