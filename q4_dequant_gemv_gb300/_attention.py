@@ -41,39 +41,44 @@ def _stream(stream, t):
     return _current(t.get_device()) if stream is None else stream.cuda_stream
 
 
+# (What follows runs between a decode step's launches: attributes are read once, and
+# tensors made here are not checked again.)
+_Tensor = torch.Tensor
+_i32 = torch.int32
+
+
 def _rows(t, name, heads=None, dim=None, tokens=None):
     """Address, type code, shape and strides of a [tokens, heads, dim] tensor."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(shape)}")
+    n, h, d = shape
     if (heads is not None and h != heads) or (dim is not None and d != dim) or (tokens is not None and n != tokens):
         want = ", ".join("*" if v is None else str(v) for v in (tokens, heads, dim))
-        raise ValueError(f"{name} must be [{want}], got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be [{want}], got {tuple(shape)}")
     st, sh, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return t.data_ptr(), code, n, h, d, st, sh
 
 
-def _array(t, name, dtype, n=None):
-    """Address of a contiguous 1-D device array (0 for None)."""
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor):
+def _array(t, name, dtype, n):
+    """Address of a contiguous device array of n values."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be a contiguous array{'' if n is None else f' of {n}'}, got {tuple(t.shape)}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous array of {n}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -81,31 +86,32 @@ def _turn(table, rot_max):
     """Address, rows and rot of a rotary table (None: no rotation)."""
     if table is None:
         return 0, 0, 0
-    if not isinstance(table, torch.Tensor):
+    if not isinstance(table, _Tensor):
         raise TypeError("table must be a torch.Tensor")
-    if table.dtype != torch.float32:
+    if table.dtype is not torch.float32:
         raise TypeError(f"table must have dtype torch.float32, got {table.dtype}")
     if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor")
-    if table.dim() != 2 or not table.is_contiguous():
+    shape = table.shape
+    if len(shape) != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous [positions, rot] tensor")
-    rows, rot = table.shape
+    rows, rot = shape
     if rot % 2 or rot > rot_max:
         raise ValueError(f"table turns {rot} of {rot_max} elements of a head")
     return table.data_ptr(), rows, rot
 
 
 def _cache(k_cache, v_cache, page_table, seq_start, kv_len, tokens):
-    """The packed q4k_paged_cache, its heads, dim and type."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+    """The packed q4k_paged_cache, its heads, dim and sequences."""
+    if not (isinstance(k_cache, _Tensor) and isinstance(v_cache, _Tensor) and isinstance(page_table, _Tensor)):
+        raise TypeError("k_cache, v_cache and page_table must be torch.Tensors")
+    if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
+        raise ValueError("k_cache, v_cache and page_table must be CUDA tensors")
     dtype, shape = k_cache.dtype, k_cache.shape
-    if dtype != torch.bfloat16 and dtype != torch.float16:
+    code = _CODE.get(dtype)
+    if not code:      # (fp32 is 0)
         raise TypeError(f"k_cache must be bfloat16 or float16, got {dtype}")
-    if v_cache.dtype != dtype:
+    if v_cache.dtype is not dtype:
         raise TypeError(f"v_cache must have dtype {dtype}, got {v_cache.dtype}")
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache and v_cache must be [pages, page size, heads, dim], got {tuple(shape)} and "
@@ -115,24 +121,19 @@ def _cache(k_cache, v_cache, page_table, seq_start, kv_len, tokens):
     vp, vs, vh, vd = v_cache.stride()
     if (kd != 1 or vd != 1) and dim > 1:
         raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
-    if not isinstance(page_table, torch.Tensor):
-        raise TypeError("page_table must be a torch.Tensor")
-    if page_table.dtype != torch.int32:
+    if page_table.dtype is not _i32:
         raise TypeError(f"page_table must have dtype torch.int32, got {page_table.dtype}")
-    if not page_table.is_cuda:
-        raise ValueError("page_table must be a CUDA tensor")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [sequences, pages]")
-    batch, most = page_table.shape
+    table = page_table.shape
+    if len(table) != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(table)}")
+    batch, most = table
     row, step = page_table.stride()
     if step != 1 and most > 1:
         raise ValueError("page_table must be contiguous in its last dimension")
-    if batch <= 1:
-        row = max(row, most)
     packed = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, ks, kh, vp, vs, vh, pages, size, heads, dim,
-                         page_table.data_ptr(), row, most, _array(seq_start, "seq_start", torch.int32, batch + 1),
-                         _array(kv_len, "kv_len", torch.int32, batch), batch, tokens, _CODE[dtype], 0)
-    return packed, heads, dim, dtype
+                         page_table.data_ptr(), row, most, _array(seq_start, "seq_start", _i32, batch + 1),
+                         _array(kv_len, "kv_len", _i32, batch), batch, tokens, code, 0)
+    return packed, heads, dim, batch
 
 
 def rope_table(rows: int, rot: int, base: float = 10000.0, *, scaling=None, factor: float = 1.0, orig_len: float = 0.0,
@@ -162,15 +163,15 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, *, scaling=None, fact
     return table
 
 
-def _out(out, name, shape, dtype, device, stream):
-    """`out`, or a new tensor that the call's stream may use."""
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            out.record_stream(stream)
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {out.dtype}")
-    return out
+def _new(like, dtype, shape, stream):
+    """Address and type code of a new tensor that the call's stream may use."""
+    t = torch.empty_like(like) if dtype is like.dtype and like.is_contiguous() else torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"the output must be float32, float16 or bfloat16, got {dtype}")
+    return t, t.data_ptr(), code
 
 
 def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, stream=None):
@@ -178,11 +179,16 @@ def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, st
     table; pairs (i, i + rot/2), or (2i, 2i+1) if interleaved.  y may be x."""
     xp, xc, n, h, d, xt, xh = _rows(x, "x")
     tp, rows, rot = _turn(table, d)
-    pp = _array(pos, "pos", torch.int32, n)
-    if rot and not pp:
+    if pos is None and rot:
         raise ValueError("pos is needed with a table")
-    y = _out(y, "y", (n, h, d), out_dtype or (x.dtype if y is None else None), x.device, stream)
-    yp, yc, _, _, _, yt, yh = _rows(y, "y", h, d, n)
+    pp = 0 if pos is None else _array(pos, "pos", _i32, n)
+    if y is None:
+        y, yp, yc = _new(x, out_dtype or x.dtype, (n, h, d), stream)
+        yt, yh = h * d, d
+    else:
+        yp, yc, _, _, _, yt, yh = _rows(y, "y", h, d, n)
+        if out_dtype is not None and y.dtype is not out_dtype:
+            raise TypeError(f"y must have dtype {out_dtype}, got {y.dtype}")
     args = _ROPE.pack(xp, yp, pp, tp, n, h, d, rot, rows, xt, xh, yt, yh, xc, yc, 1 if interleaved else 0, 0)
     st = (_lib or _load()).q4k_rope(args, _stream(stream, x))
     if st:
@@ -204,12 +210,17 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
     if ch != h or cd != d:
         raise ValueError(f"the cache holds {ch} heads of {cd}, k and v {h} of {d}")
     tp, rows, rot = _turn(table, d)
-    pp = _array(pos, "pos", torch.int32, n)
+    pp = 0 if pos is None else _array(pos, "pos", _i32, n)
     qp = qc = qh = qts = qhs = op = oc = ots = ohs = 0
     if q is not None:
         qp, qc, _, qh, _, qts, qhs = _rows(q, "q", None, d, n)
-        q_out = _out(q_out, "q_out", q.shape, q_dtype or (q.dtype if q_out is None else None), q.device, stream)
-        op, oc, _, _, _, ots, ohs = _rows(q_out, "q_out", qh, d, n)
+        if q_out is None:
+            q_out, op, oc = _new(q, q_dtype or q.dtype, (n, qh, d), stream)
+            ots, ohs = qh * d, d
+        else:
+            op, oc, _, _, _, ots, ohs = _rows(q_out, "q_out", qh, d, n)
+            if q_dtype is not None and q_out.dtype is not q_dtype:
+                raise TypeError(f"q_out must have dtype {q_dtype}, got {q_out.dtype}")
     elif q_out is not None:
         raise ValueError("q_out without q")
     args = _APPEND.pack(kp, vp, qp, op, kt, kh, vt, vh, qts, qhs, ots, ohs, pp, tp, rows, rot, qh, kc, qc, oc,
@@ -229,11 +240,16 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None
     scale: 1/sqrt(dim) unless given; softcap > 0: scores softcap * tanh(s / softcap); slopes fp32 [q heads]: minus
     slopes[h] * |p - j|; lse: fp32 [tokens, q heads], filled with the rows' log-sum-exp."""
     qp, qc, n, h, d, qt, qh = _rows(q, "q")
-    cache, ch, cd, _ = _cache(k_cache, v_cache, page_table, seq_start, kv_len, n)
+    cache, ch, cd, batch = _cache(k_cache, v_cache, page_table, seq_start, kv_len, n)
     if cd != d or ch < 1 or h % ch:
         raise ValueError(f"the cache holds {ch} heads of {cd}, q {h} of {d}")
-    out = _out(out, "out", (n, h, d), out_dtype or (q.dtype if out is None else None), q.device, stream)
-    op, oc, _, _, _, ot, oh = _rows(out, "out", h, d, n)
+    if out is None:
+        out, op, oc = _new(q, out_dtype or q.dtype, (n, h, d), stream)
+        ot, oh = h * d, d
+    else:
+        op, oc, _, _, _, ot, oh = _rows(out, "out", h, d, n)
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out must have dtype {out_dtype}, got {out.dtype}")
     lp = 0
     if lse is not None:
         if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
@@ -241,10 +257,10 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None
         if not lse.is_cuda or not lse.is_contiguous() or tuple(lse.shape) != (n, h):
             raise ValueError(f"lse must be a contiguous CUDA tensor [{n}, {h}]")
         lp = lse.data_ptr()
-    batch = page_table.shape[0]
-    args = _ATTENTION.pack(qp, op, lp, qt, qh, ot, oh, h, int(window), _array(slopes, "slopes", torch.float32, h),
-                           _array(prefix_len, "prefix_len", torch.int32, batch),
-                           _array(kv_start, "kv_start", torch.int32, n),
+    args = _ATTENTION.pack(qp, op, lp, qt, qh, ot, oh, h, window,
+                           0 if slopes is None else _array(slopes, "slopes", torch.float32, h),
+                           0 if prefix_len is None else _array(prefix_len, "prefix_len", _i32, batch),
+                           0 if kv_start is None else _array(kv_start, "kv_start", _i32, n),
                            1.0 / math.sqrt(d) if scale is None else scale, softcap, qc, oc, 1 if causal else 0, 0)
     st = (_lib or _load()).q4k_paged_attention(cache, args, _stream(stream, q))
     if st:
