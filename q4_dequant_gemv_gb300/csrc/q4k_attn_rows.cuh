@@ -1,12 +1,13 @@
 // q4k_attn_rows.cuh -- attention of a few query rows per cache head (decode and
 // verification) on mma.sync.
 //
-// Such a call reads every visible key and value once for 1 to 32 query rows: at
+// Such a call reads every visible key and value once for 1 to 48 query rows: at
 // 7 rows 7 flops a byte, far below what any tensor path offers, so the kernel is
 // bound by memory and by how many bytes are in flight.  A warp owns blocks of 16
 // keys and a ring of its own in shared memory, fills a slot ahead of time and
 // refills it when it has read it: no barrier between warps until they join at
-// the end of a tile, and 150 to 200 KB in flight per SM.
+// the end of a tile, and 130 to 190 KB in flight per SM.  Tiles of 32 and 48
+// rows give each block to two warps, half of the rows each (registers).
 //   S^T = K Q^T: A = 16 keys x 16 d (ldmatrix), B = Q^T from shared memory;
 //   O^T = V^T P^T: A = 16 d x 16 keys (ldmatrix.trans), B = P^T from the S^T
 //   accumulators by an 8x8 transpose (movmatrix).
@@ -38,15 +39,18 @@ constexpr int kMaxCluster = 8;               // portable cluster size
 constexpr int kBlock = 16;                   // keys of a ring slot
 constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
-// Warps of a CTA and slots of a warp's ring, by head size and rows: 128 to 192 KB
-// of ring (what else the larger tiles keep in shared memory leaves two slots).
-template <int NT, int DP>
+// A tile's shape: NT n8 tiles of query rows per warp, RG warps side by side on a
+// block of keys, KG such groups; slots of a group's ring (128 to 192 KB in all,
+// what the queries and the join leave).
+template <int NT, int RG, int DP>
 struct RowsShape {
+    static constexpr int R = 8 * NT * RG;
     static constexpr int kWarps = DP == 256 ? 4 : 8;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kUnit = kBlock * kWarps;          // keys per unit
+    static constexpr int KG = kWarps / RG;
+    static constexpr int kUnit = kBlock * KG;              // keys per unit
     static constexpr int kSide = kBlock * DP * 2;          // bytes of K (or V) in a slot
-    static constexpr int kSlots = DP == 64 ? 5 : NT * DP >= 512 ? 2 : 3;
+    static constexpr int kSlots = RG == 2 ? (DP == 64 ? 8 : 4) : DP == 64 ? 5 : NT * DP >= 512 ? 2 : 3;
 };
 
 template <int CT>
@@ -102,6 +106,27 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+// One arrival on an mbarrier when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// tanh within a few ulp: its series where |x| < 0.4 (the next term is 6e-8 of the
+// sum there), else 1 - 2 / (e^2|x| + 1).
+__device__ __forceinline__ float tanh_close(float x)
+{
+    const float y = x * x;
+    float p = fmaf(y, -8.8632355e-3f, 2.1869488e-2f);
+    p = fmaf(p, y, -5.3968254e-2f);
+    p = fmaf(p, y, 1.3333333e-1f);
+    p = fmaf(p, y, -3.3333333e-1f);
+    p = fmaf(p * y, x, x);
+    const float e = ex2(2.0f * kLog2e * fabsf(x));
+    const float q = copysignf(fmaf(-2.0f, rcp(e + 1.0f), 1.0f), x);
+    return fabsf(x) < 0.4f ? p : q;
+}
+
 // x as PARTS packed pairs; each part takes what the earlier ones left.
 template <int CT, int PARTS>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS])
@@ -123,46 +148,48 @@ constexpr float rows_shift()
     return CT == Q4K_F16 ? 14.0f : 0.0f;
 }
 
-template <int CT, int PARTS, int NT, int DP>
+template <int CT, int PARTS, int NT, int RG, int DP>
 struct RowsShared {
-    using Sp = RowsShape<NT, DP>;
-    static constexpr int R = 8 * NT;
+    using Sp = RowsShape<NT, RG, DP>;
+    static constexpr int R = Sp::R;
     using Plan = Split<Sp::kUnit, Sp::kThreads, kBlock>;
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
-    // a warp's ring; when the warps join it holds the warp's O instead
+    // a group's ring; when the warps join it holds the group's O instead
     static constexpr int kSlotBytes = Sp::kSlots * 2 * Sp::kSide, kOBytes = (R * kRed * 4 + 1023) / 1024 * 1024;
     static constexpr int kRing = kSlotBytes > kOBytes ? kSlotBytes : kOBytes;
-    uint8_t ring[Sp::kWarps][kRing];
+    uint8_t ring[Sp::KG][kRing];
     typename Plan::Shared plan;
-    uint4 q[PARTS][NT][DP / 32][32];       // B fragments of Q, lane-major
-    float m[Sp::kWarps][R], l[Sp::kWarps][R];
+    uint4 q[PARTS][R / 8][DP / 32][32];    // B fragments of Q, lane-major
+    float m[Sp::KG][R], l[Sp::KG][R];
     float scale[R], slope[R];
     int lo[R], hi[R], pos[R];              // visible keys of each row, its token
     // what the ranks of a cluster send: their O for this rank's columns ([rank][row][column
     // quad], whatever the number of ranks), and their statistics
     float4 sent[R * (DP / 4)];
     float2 stat[kMaxCluster][R];
-    unsigned long long full[Sp::kWarps][Sp::kSlots];
+    unsigned long long full[Sp::KG][Sp::kSlots], empty[Sp::KG][Sp::kSlots];
 };
 
 // TMA: slots filled by tensor copies (maps), else by cp.async.
-template <int CT, int PARTS, int NT, int DP, bool TMA>
-__global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
+template <int CT, int PARTS, int NT, int RG, int DP, bool TMA>
+__global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
 {
-    using Sh = RowsShared<CT, PARTS, NT, DP>;
-    using Sp = RowsShape<NT, DP>;
+    using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
+    using Sp = RowsShape<NT, RG, DP>;
     constexpr int R = Sh::R, ND = DP / 64, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
+    constexpr int KG = Sp::KG;
     constexpr int kHalf = kBlock * 128;      // bytes of 16 rows of 64 elements
     constexpr float kShift = rows_shift<CT>();
     extern __shared__ uint8_t smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int kg = w % KG, rg = w / KG;      // group of keys, half of the rows
 
-    if (TMA && tid == 0) {
-        for (int i = 0; i < WARPS; ++i)
-            for (int j = 0; j < SLOTS; ++j) mbar_init(smem_u32(&sh.full[i][j]), 1);
+    if (tid < KG * SLOTS) {
+        mbar_init(smem_u32(&sh.full[0][0] + tid), TMA ? 1 : 32);
+        mbar_init(smem_u32(&sh.empty[0][0] + tid), RG);
         fence_barrier_init();
-        prefetch_map(&maps.k), prefetch_map(&maps.v);
+        if (TMA && tid == 0) prefetch_map(&maps.k), prefetch_map(&maps.v);
     }
     if (a.cluster > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
     typename Sh::Plan plan(a, sh.plan, R);         // synchronises the CTA
@@ -179,11 +206,12 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
         u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
     }
 
-    const uint32_t ring = smem_u32(sh.ring[w]);
+    const uint32_t ring = smem_u32(sh.ring[kg]);
     // ldmatrix addresses within a slot: row of the lane, chunk before the swizzle
     const int krow = (lane & 7) + 8 * ((lane >> 3) & 1), kch = lane >> 4;
     const int vrow = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
-    uint32_t fills = 0;                      // slots filled so far by this warp (TMA: phases)
+    uint32_t fills = 0;                      // slots filled so far in this group's ring
+    uint32_t reads = 0;                      // phases of the slots' `empty` barriers, a bit each
     bool good = true;                        // no wait has timed out
 
     while (u < u_end) {
@@ -208,9 +236,9 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
             todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
         }
 
-        // ---- this warp's blocks: key kb0 + i * kUnit, i < count
+        // ---- this group's blocks: key kb0 + i * kUnit, i < count
         const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
-        const int kb0 = t.lo + off * Sp::kUnit + kBlock * w;
+        const int kb0 = t.lo + off * Sp::kUnit + kBlock * kg;
         const int count = good && kb0 < t.hi ? min(todo, (t.hi - kb0 + Sp::kUnit - 1) / Sp::kUnit) : 0;
         // pages and slots of the next 32 blocks, a lane each (TMA)
         int ids = 0, slots = 0;
@@ -227,14 +255,14 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
                 }
             }
         };
-        auto fill = [&](int i) {
-            const int s = static_cast<int>(fills % SLOTS);
-            const uint32_t dst = ring + s * 2 * Sp::kSide;
+        // block i into its slot, by the group's first warp
+        auto fill = [&](int i, uint32_t f) {
+            const int s = static_cast<int>(f % SLOTS);
+            const uint32_t dst = ring + s * 2 * Sp::kSide, bar = smem_u32(&sh.full[kg][s]);
             if constexpr (TMA) {
                 if (i > 0 && (i & 31) == 0) look(i);
                 const int page = __shfl_sync(0xffffffffu, ids, i & 31), slot = __shfl_sync(0xffffffffu, slots, i & 31);
                 if (lane == 0) {
-                    const uint32_t bar = smem_u32(&sh.full[w][s]);
                     mbar_arrive_expect_tx(bar, 2 * Sp::kSide);
 #pragma unroll
                     for (int h = 0; h < ND; ++h) {
@@ -270,8 +298,8 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
                     copy16(dst + Sp::kSide + o,
                            static_cast<const uint16_t *>(a.v) + p * a.v_page + sl * a.v_slot + head * a.v_head + d, live);
                 }
+                copies_arrive(bar);
             }
-            ++fills;
         };
         // row r of the tile: its token and its query head (divisions of small numbers)
         const int i0 = t.first ? t.first / a.group : 0, rem = t.first - i0 * a.group;
@@ -305,10 +333,10 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
             }
         }
         const uint32_t first_fill = fills;
-        if constexpr (TMA) fence_proxy_async_smem();   // (the ring may have held the previous tile's O)
-        for (int i = 0; i < SLOTS; ++i) {
-            if (i < count) fill(i);
-            if constexpr (!TMA) asm volatile("cp.async.commit_group;" ::: "memory");
+        fills += count;
+        if (rg == 0) {
+            if constexpr (TMA) fence_proxy_async_smem();   // (the ring may have held the previous tile's O)
+            for (int i = 0; i < min(SLOTS, count); ++i) fill(i, first_fill + i);
         }
 
         // ---- the tile's rows: scale, visible range, fragments of Q
@@ -368,135 +396,185 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
                 for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
         }
 
+        // a wait has timed out: the copies in flight land (or time out) before the ring is used again
+        auto wind_down = [&](int i) {
+            if (lane == 0) atomicOr(a.error, 8u);
+            for (int k = i + 1; k < min(i + SLOTS, count); ++k)
+                (void)mbar_wait_bounded(smem_u32(&sh.full[kg][(first_fill + k) % SLOTS]), ((first_fill + k) / SLOTS) & 1,
+                                        kRowsWaitNs);
+        };
         for (int i = 0; i < count; ++i) {
             const int kb = kb0 + i * Sp::kUnit;
             const uint32_t f = first_fill + i;
             const int slot = static_cast<int>(f % SLOTS);
             const uint32_t kt = ring + slot * 2 * Sp::kSide, vt = kt + Sp::kSide;
-            if constexpr (TMA) {
-                const bool here = mbar_wait_bounded(smem_u32(&sh.full[w][slot]), (f / SLOTS) & 1, kRowsWaitNs);
-                good = __all_sync(0xffffffffu, here);
-                if (!good) {
-                    // wind down: the copies in flight land (or time out) before the ring is used again
-                    if (lane == 0) atomicOr(a.error, 8u);
-                    for (uint32_t k = f; k != fills; ++k)
-                        (void)mbar_wait_bounded(smem_u32(&sh.full[w][k % SLOTS]), (k / SLOTS) & 1, kRowsWaitNs);
-                    break;
-                }
-                if (kb < t.from || kb + kBlock > t.hi) {
-                    // rows of V that nothing sees: zero
-                    for (int r = 0; r < kBlock; ++r)
-                        if ((kb + r < t.from || kb + r >= t.hi) && lane < 8 * ND)
-                            *reinterpret_cast<uint4 *>(sh.ring[w] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf +
-                                                       r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();   // before a later copy into the slot
-                    __syncwarp();
-                }
-            } else {
-                asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+            const bool here = mbar_wait_bounded(smem_u32(&sh.full[kg][slot]), (f / SLOTS) & 1, kRowsWaitNs);
+            good = __all_sync(0xffffffffu, here);
+            if (!good) {
+                wind_down(i);
+                break;
+            }
+            if (TMA && (kb < t.from || kb + kBlock > t.hi)) {
+                // rows of V that nothing sees: zero (by every warp that reads them)
+                for (int r = 0; r < kBlock; ++r)
+                    if ((kb + r < t.from || kb + r >= t.hi) && lane < 8 * ND)
+                        *reinterpret_cast<uint4 *>(sh.ring[kg] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf +
+                                                   r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();   // before a later copy into the slot
                 __syncwarp();
             }
 
-            // ---- S^T
-            // chains of their own: even and odd k-steps (one part), or the parts
-            constexpr int CHAINS = PARTS > 1 ? PARTS : 2;
-            float acc[NT][CHAINS][4] = {};
+            if (8 * rg * NT < t.rows) {   // (this half may hold no rows)
+                // ---- S^T
+                // chains of their own: even and odd k-steps (one part), or the parts
+                constexpr int CHAINS = PARTS > 1 ? PARTS : 2;
+                float acc[NT][CHAINS][4] = {};
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                const int c = 2 * j + kch;
-                uint32_t kf[4];
-                ldmatrix4(kt + (c >> 3) * kHalf + krow * 128 + (((c & 7) ^ (krow & 7)) << 4), kf);
+                for (int j = 0; j < KS; ++j) {
+                    const int c = 2 * j + kch;
+                    uint32_t kf[4];
+                    ldmatrix4(kt + (c >> 3) * kHalf + krow * 128 + (((c & 7) ^ (krow & 7)) << 4), kf);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {
+                            const uint2 b = reinterpret_cast<const uint2 *>(&sh.q[p][rg * NT + nt][j >> 1][lane])[j & 1];
+                            mma_t<CT>(acc[nt][PARTS > 1 ? p : j & 1], kf[0], kf[1], kf[2], kf[3], b.x, b.y);
+                        }
+                }
+
+                // (each step over all n8 tiles before the next: their chains run side by side)
+                float s[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int r0 = 8 * (rg * NT + nt) + 2 * t4;
+                    const float2 scl = *reinterpret_cast<const float2 *>(&sh.scale[r0]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float x;
+                        if constexpr (PARTS > 1) {
+                            // an infinite key: the first part has its sign, the others may be 0 or of the other sign
+                            float rest = acc[nt][PARTS - 1][j];
+#pragma unroll
+                            for (int p = PARTS - 2; p > 0; --p) rest += acc[nt][p][j];
+                            x = fabsf(acc[nt][0][j]) < INFINITY ? acc[nt][0][j] + rest : acc[nt][0][j];
+                        } else {
+                            x = acc[nt][0][j] + acc[nt][1][j];
+                        }
+                        s[nt][j] = x * (j & 1 ? scl.y : scl.x);
+                    }
+                }
+                if (a.softcap > 0.0f) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x = s[nt][j];
+                            const float th = PARTS > 1 ? tanh_close(x) : 1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * x) + 1.0f);
+                            s[nt][j] = a.softcap * kLog2e * th;
+                        }
+                }
+                if (a.slopes) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + g + 8 * (j >> 1);
+                            s[nt][j] -= sh.slope[r] * fabsf(static_cast<float>(t.pos0 + sh.pos[r] - key));
+                        }
+                }
+                if (kb < in_lo || kb + kBlock > in_hi) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + g + 8 * (j >> 1);
+                            if (key < sh.lo[r] || key >= sh.hi[r]) s[nt][j] = -INFINITY;
+                        }
+                }
+                float mx[NT][2], fa[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        const uint2 b = reinterpret_cast<const uint2 *>(&sh.q[p][nt][j >> 1][lane])[j & 1];
-                        mma_t<CT>(acc[nt][PARTS > 1 ? p : j & 1], kf[0], kf[1], kf[2], kf[3], b.x, b.y);
-                    }
-            }
-
-            const bool all = kb >= in_lo && kb + kBlock <= in_hi;
-            uint32_t pb[NT][PARTS][2];
+                    for (int j = 0; j < 2; ++j) mx[nt][j] = fmaxf(s[nt][j], s[nt][j + 2]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r0 = 8 * nt + 2 * t4;
-                const float2 scl = *reinterpret_cast<const float2 *>(&sh.scale[r0]);
-                float s[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float x;
-                    if constexpr (PARTS > 1) {
-                        // an infinite key: the first part has its sign, the others may be 0 or of the other sign
-                        float rest = acc[nt][PARTS - 1][j];
-#pragma unroll
-                        for (int p = PARTS - 2; p > 0; --p) rest += acc[nt][p][j];
-                        x = fabsf(acc[nt][0][j]) < INFINITY ? acc[nt][0][j] + rest : acc[nt][0][j];
-                    } else {
-                        x = acc[nt][0][j] + acc[nt][1][j];
-                    }
-                    x *= j & 1 ? scl.y : scl.x;
-                    if (a.softcap > 0.0f) {
-                        const float th = PARTS > 1 ? tanhf(x) : 1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * x) + 1.0f);
-                        x = a.softcap * kLog2e * th;
-                    }
-                    const int key = kb + g + 8 * (j >> 1);
-                    if (a.slopes)
-                        x -= sh.slope[r0 + (j & 1)] * fabsf(static_cast<float>(t.pos0 + sh.pos[r0 + (j & 1)] - key));
-                    if (!all && (key < sh.lo[r0 + (j & 1)] || key >= sh.hi[r0 + (j & 1)])) x = -INFINITY;
-                    s[j] = x;
-                }
-                float mx[2], fa[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v = fmaxf(s[j], s[j + 2]);
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[j] = fmaxf(m[nt][j], v);
-                    fa[j] = mx[j] == -INFINITY ? 1.0f : ex2(m[nt][j] - mx[j]);
-                    m[nt][j] = mx[j];
-                    l[nt][j] *= fa[j];
-                }
-                if (__any_sync(0xffffffffu, fa[0] != 1.0f || fa[1] != 1.0f)) {
-#pragma unroll
-                    for (int q = 0; q < KS; ++q) {
-                        o[nt][q][0] *= fa[0], o[nt][q][1] *= fa[1];
-                        o[nt][q][2] *= fa[0], o[nt][q][3] *= fa[1];
-                    }
-                }
-                float e[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float base = mx[j & 1] == -INFINITY ? 0.0f : mx[j & 1] - kShift;
-                    e[j] = ex2(s[j] - base);
-                    l[nt][j & 1] += e[j];
-                }
-                uint32_t p0[PARTS], p1[PARTS];
-                split2<CT, PARTS>(e[0], e[1], p0);
-                split2<CT, PARTS>(e[2], e[3], p1);
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) pb[nt][p][0] = transpose8(p0[p]), pb[nt][p][1] = transpose8(p1[p]);
-            }
-
-            // ---- O^T
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                const int c = 2 * j + vch;
-                uint32_t vf[4];
-                ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
-#pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p)
+                for (int hop = 4; hop < 32; hop <<= 1)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) mx[nt][j] = fmaxf(mx[nt][j], __shfl_xor_sync(0xffffffffu, mx[nt][j], hop));
+                bool grown = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        mx[nt][j] = fmaxf(m[nt][j], mx[nt][j]);
+                        grown |= mx[nt][j] != m[nt][j];
+                        fa[nt][j] = mx[nt][j] == -INFINITY ? 1.0f : ex2(m[nt][j] - mx[nt][j]);
+                        m[nt][j] = mx[nt][j];
+                    }
+                if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        l[nt][0] *= fa[nt][0], l[nt][1] *= fa[nt][1];
+#pragma unroll
+                        for (int q = 0; q < KS; ++q) {
+                            o[nt][q][0] *= fa[nt][0], o[nt][q][1] *= fa[nt][1];
+                            o[nt][q][2] *= fa[nt][0], o[nt][q][3] *= fa[nt][1];
+                        }
+                    }
+                }
+                uint32_t pb[NT][PARTS][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float base = mx[nt][j & 1] == -INFINITY ? 0.0f : mx[nt][j & 1] - kShift;
+                        e[j] = ex2(s[nt][j] - base);
+                        l[nt][j & 1] += e[j];
+                    }
+                    uint32_t p0[PARTS], p1[PARTS];
+                    split2<CT, PARTS>(e[0], e[1], p0);
+                    split2<CT, PARTS>(e[2], e[3], p1);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) pb[nt][p][0] = transpose8(p0[p]), pb[nt][p][1] = transpose8(p1[p]);
+                }
+
+                // ---- O^T
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    const int c = 2 * j + vch;
+                    uint32_t vf[4];
+                    ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
+#pragma unroll
+                    for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
+                }
             }
             __syncwarp();   // the slot has been read by every lane
-            if (i + SLOTS < count) fill(i + SLOTS);
-            if constexpr (!TMA) asm volatile("cp.async.commit_group;" ::: "memory");
+            if (i + SLOTS < count) {
+                if constexpr (RG > 1) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[kg][slot]));
+                    if (rg == 0) {   // .. of the group's other warp too
+                        const bool free = mbar_wait_bounded(smem_u32(&sh.empty[kg][slot]), reads >> slot & 1, kRowsWaitNs);
+                        reads ^= 1u << slot;
+                        good = __all_sync(0xffffffffu, free);
+                        if (!good) {
+                            wind_down(i);
+                            break;
+                        }
+                    }
+                }
+                if (rg == 0) fill(i + SLOTS, f + SLOTS);
+            }
         }
 
-        // ---- join the warps: each leaves O in its own ring
-        float *red = reinterpret_cast<float *>(sh.ring[w]);
+        // ---- join the groups: each leaves O in its own ring
+        if constexpr (RG > 1) __syncthreads();   // (its other warp may still be reading)
+        float *red = reinterpret_cast<float *>(sh.ring[kg]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -504,8 +582,8 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
-                const int q = 8 * nt + 2 * t4 + j;
-                if (g == 0) sh.m[w][q] = m[nt][j], sh.l[w][q] = l[nt][j];
+                const int q = 8 * (rg * NT + nt) + 2 * t4 + j;
+                if (g == 0) sh.m[kg][q] = m[nt][j], sh.l[kg][q] = l[nt][j];
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
                     red[q * Sh::kRed + 16 * i + g] = o[nt][i][j];
@@ -525,9 +603,9 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
                 const int r = i % R;
                 float mx = -INFINITY, ls = 0.0f;
 #pragma unroll
-                for (int k = 0; k < WARPS; ++k) mx = fmaxf(mx, sh.m[k][r]);
+                for (int k = 0; k < KG; ++k) mx = fmaxf(mx, sh.m[k][r]);
 #pragma unroll
-                for (int k = 0; k < WARPS; ++k) ls += sh.l[k][r] * weight(sh.m[k][r], mx);
+                for (int k = 0; k < KG; ++k) ls += sh.l[k][r] * weight(sh.m[k][r], mx);
                 st_shared_cluster_v2(map_shared_rank(smem_u32(&sh.stat[rank][r]), i / R), mx, ls);
             }
         }
@@ -536,10 +614,10 @@ __global__ void __launch_bounds__(RowsShape<NT, DP>::kThreads, 1) rows_kernel(co
             const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
             float mx = -INFINITY, ls = 0.0f;
 #pragma unroll
-            for (int k = 0; k < WARPS; ++k) mx = fmaxf(mx, sh.m[k][r]);
+            for (int k = 0; k < KG; ++k) mx = fmaxf(mx, sh.m[k][r]);
             float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < WARPS; ++k) {
+            for (int k = 0; k < KG; ++k) {
                 const float f = weight(sh.m[k][r], mx);
                 const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sh.ring[k]) + r * Sh::kRed + d);
                 ls += f * sh.l[k][r];

@@ -10,12 +10,39 @@ namespace attn {
 
 constexpr double kSplitCost = 12.0;
 
-template <int CT, int PARTS, int NT, int DP, bool TMA>
+// How many clusters of 1, 2, 4 and 8 CTAs of a kernel the GPU holds at once.
+struct Together {
+    int n[4];
+};
+
+template <class Kernel>
+static Together clusters_at_once(Kernel kern, int threads, int smem, int sms)
+{
+    Together t{{sms, 0, 0, 0}};
+    for (int i = 1; i < 4; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = static_cast<unsigned>(sms) << i;
+        cfg.blockDim = threads;
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 1u << i, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&t.n[i], kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            t.n[i] = 0;
+        }
+    }
+    return t;
+}
+
+template <int CT, int PARTS, int NT, int RG, int DP, bool TMA>
 static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
-    using Sh = RowsShared<CT, PARTS, NT, DP>;
-    using Sp = RowsShape<NT, DP>;
-    auto kern = rows_kernel<CT, PARTS, NT, DP, TMA>;
+    using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
+    using Sp = RowsShape<NT, RG, DP>;
+    auto kern = rows_kernel<CT, PARTS, NT, RG, DP, TMA>;
     Args a = l.args;
     constexpr int R = Sh::R;
     constexpr int kSmem = static_cast<int>(sizeof(Sh)) + 1024;   // room to align the rings to 1024 bytes
@@ -32,15 +59,17 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     // lengths and a few long sequences, but its scratch and the join through memory
     // cost about kSplitCost units of one CTA's time.
     const int64_t items = a.kv_heads * std::max<int64_t>(a.batch, (static_cast<int64_t>(a.tokens) * a.group + R - 1) / R);
-    int S = kMaxCluster;
-    while (S > 1 && (S > units || items * S > l.sms)) S /= 2;
-    const int64_t waves = (items * S + l.sms - 1) / l.sms;
-    const double by_cluster = static_cast<double>(waves) * ((units + S - 1) / S);
-    const double by_split = static_cast<double>(items) * units / l.sms;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = Sp::kThreads;
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = l.stream;
+    // clusters of 1, 2, 4, 8 CTAs that run at once
+    static const Together room = clusters_at_once(kern, Sp::kThreads, kSmem, l.sms);
+    int S = kMaxCluster, fit = room.n[3];
+    for (int i = 3; i > 0 && (S > units || items > fit); --i) S /= 2, fit = room.n[i - 1];
+    const int64_t waves = (items + fit - 1) / std::max(fit, 1);
+    const double by_cluster = static_cast<double>(waves) * ((units + S - 1) / S);
+    const double by_split = static_cast<double>(items) * units / l.sms;
     if (by_cluster <= by_split + kSplitCost && static_cast<int64_t>(a.slots) * a.kv_heads * S < (1 << 24)) {
         a.cluster = S;
         cfg.gridDim = static_cast<unsigned>(a.slots * a.kv_heads * S);
@@ -58,22 +87,27 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
                         [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
 }
 
-template <int CT, int PARTS, int NT, int DP>
+template <int CT, int PARTS, int NT, int RG, int DP>
 static cudaError_t launch_rows_one(const RowsLaunch &l)
 {
-    return l.boxes ? launch_rows_fill<CT, PARTS, NT, DP, true>(l) : launch_rows_fill<CT, PARTS, NT, DP, false>(l);
+    return l.boxes ? launch_rows_fill<CT, PARTS, NT, RG, DP, true>(l) : launch_rows_fill<CT, PARTS, NT, RG, DP, false>(l);
 }
 
 template <int CT, int PARTS, int DP>
 static cudaError_t launch_rows_tiles(const RowsLaunch &l)
 {
-    // the smallest tile that holds the rows an average sequence brings (fewer
-    // reads of the cache), 8 to 32; dim > 128 leaves registers for 16
-    const int64_t rows = static_cast<int64_t>(l.args.tokens) * l.args.group, batch = l.args.batch;
-    if (rows <= 8 * batch) return launch_rows_one<CT, PARTS, 1, DP>(l);
-    if constexpr (DP <= 128)
-        if (rows > 16 * batch) return launch_rows_one<CT, PARTS, 4, DP>(l);
-    return launch_rows_one<CT, PARTS, 2, DP>(l);
+    // the smallest tile that holds a sequence's rows (a second tile reads its
+    // keys again): those of one token where there are as many tokens as
+    // sequences, else half as many again as the average.  dim > 128 leaves
+    // registers for 16.
+    const int64_t batch = l.args.batch, group = l.args.group;
+    const int64_t rows = l.args.tokens == batch ? group : (3 * l.args.tokens * group + 2 * batch - 1) / (2 * batch);
+    if (rows <= 8) return launch_rows_one<CT, PARTS, 1, 1, DP>(l);
+    if constexpr (DP <= 128) {
+        if (rows > 32) return launch_rows_one<CT, PARTS, 3, 2, DP>(l);
+        if (rows > 16) return launch_rows_one<CT, PARTS, 2, 2, DP>(l);
+    }
+    return launch_rows_one<CT, PARTS, 2, 1, DP>(l);
 }
 
 template <int CT, int MANY>
