@@ -3,6 +3,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/q4k.h"
 #include "q4k_attn_chunk.cuh"
@@ -82,50 +83,76 @@ bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens)
 }
 
 // Adds the parts of split tiles: blockIdx.x = the CTA in whose share the tile
-// begins, blockIdx.y = 32 of its rows; a thread per row and column quad, loads of
-// several parts in flight.  Launched as the first kernel's programmatic dependent.
+// begins, blockIdx.y = 32 of its rows.  Bound by trips to memory, so there are
+// three: the tile, all parts' statistics (they become weights in shared memory),
+// then a thread's column quads of several parts at once.  Launched as the first
+// kernel's programmatic dependent.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R, int width, float shift)
 {
+    __shared__ float s_m[kMaxParts * kJoinRows], s_l[kMaxParts * kJoinRows];
+    __shared__ float s_max[kJoinRows], s_sum[kJoinRows];
     pdl_wait();
     const int4 t0 = __ldcg(reinterpret_cast<const int4 *>(a.joint + blockIdx.x));
     const int2 t1 = __ldcg(reinterpret_cast<const int2 *>(a.joint + blockIdx.x) + 2);
     const Joint t{t0.x, t0.y, t0.z, t0.w, t1.x, t1.y};
-    const int span = min(R, kJoinRows), r = blockIdx.y * kJoinRows + static_cast<int>(threadIdx.x) % span;
-    if (r >= t.rows) return;
+    const int r0 = blockIdx.y * kJoinRows, rows = min(min(R, kJoinRows), t.rows - r0);
+    if (rows <= 0) return;
+    const int tid = threadIdx.x, parts = t.c1 - t.c0 + 1;
     const int64_t size = static_cast<int64_t>(R) * (width + 2);
-    const int lanes = kJoinThreads / span, parts = t.c1 - t.c0 + 1;
-    const float *first = a.part + part_slot(t.c0, true) * size, *rest = a.part + part_slot(t.c0, false) * size;
+    const float *first = a.part + part_slot(t.c0, true) * size + r0, *rest = a.part + part_slot(t.c0, false) * size + r0;
     auto slot = [&](int q) { return q == 0 ? first : rest + 2 * q * size; };
-    const int row = t.first + r;
-    float mx = -INFINITY, ls = 0.0f;
-#pragma unroll 8
-    for (int q = 0; q < parts; ++q) mx = fmaxf(mx, __ldcg(slot(q) + R * width + r));
-    constexpr int PER = 4;   // quads of a thread at a time
-    for (int c = static_cast<int>(threadIdx.x) / span; 4 * c < a.dim; c += PER * lanes) {
-        float4 v[PER];
-#pragma unroll
-        for (int k = 0; k < PER; ++k) v[k] = make_float4(0, 0, 0, 0);
-        ls = 0.0f;
 #pragma unroll 4
+    for (int i = tid; i < parts * rows; i += kJoinThreads) {
+        const int q = i / rows, r = i - q * rows;
+        const float *p = slot(q) + R * width + r;
+        s_m[i] = __ldcg(p), s_l[i] = __ldcg(p + R);
+    }
+    __syncthreads();
+    if (tid < rows) {
+        float mx = -INFINITY, ls = 0.0f;
+        for (int q = 0; q < parts; ++q) mx = fmaxf(mx, s_m[q * rows + tid]);
         for (int q = 0; q < parts; ++q) {
-            const float *p = slot(q);
-            const float f = weight(__ldcg(p + R * width + r), mx);
-            ls += f * __ldcg(p + R * width + R + r);
+            const float f = weight(s_m[q * rows + tid], mx);
+            s_m[q * rows + tid] = f;
+            ls += f * s_l[q * rows + tid];
+        }
+        s_max[tid] = mx, s_sum[tid] = ls;
+    }
+    __syncthreads();
+    // neighbouring threads on neighbouring rows; a few parts: more quads in flight, many: more parts
+    auto add = [&](auto per_c, auto deep_c) {
+        constexpr int PER = decltype(per_c)::value, DEEP = decltype(deep_c)::value;
+        const int quads = rows * (a.dim / 4);
+        for (int i = tid; i < quads; i += PER * kJoinThreads) {
+            float4 v[PER];
+            int c[PER], r[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {   // (quads past the end are read again, not stored)
+                const int j = i + k * kJoinThreads < quads ? i + k * kJoinThreads : i;
+                c[k] = j / rows, r[k] = j - c[k] * rows;
+                v[k] = make_float4(0, 0, 0, 0);
+            }
+#pragma unroll DEEP
+            for (int q = 0; q < parts; ++q) {
+                const float4 *p = reinterpret_cast<const float4 *>(slot(q) - r0) + r0;
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const float4 x = __ldcg(p + c[k] * R + r[k]);
+                    const float f = s_m[q * rows + r[k]];
+                    v[k].x += f * x.x, v[k].y += f * x.y, v[k].z += f * x.z, v[k].w += f * x.w;
+                }
+            }
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                const int x = c + k * lanes;
-                if (4 * x >= a.dim) continue;
-                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p) + x * R + r);
-                v[k].x += f * o.x, v[k].y += f * o.y, v[k].z += f * o.z, v[k].w += f * o.w;
+                if (i + k * kJoinThreads >= quads) break;
+                const int row = t.first + r0 + r[k], tok = row / a.group;
+                finish_row(a, t.tok0 + tok, t.head * a.group + row - tok * a.group, 4 * c[k], v[k], s_max[r[k]], s_sum[r[k]],
+                           shift);
             }
         }
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int x = c + k * lanes;
-            if (4 * x < a.dim)
-                finish_row(a, t.tok0 + row / a.group, t.head * a.group + row % a.group, 4 * x, v[k], mx, ls, shift);
-        }
-    }
+    };
+    if (parts <= 4) add(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    else add(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
 }
 
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream)

@@ -359,6 +359,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
 // Host: scratch of `grid` CTAs, the first kernel by `launch(args)`, the join of the
 // tiles that it left split; R rows and `width` columns a slot.
 constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr int kMaxParts = 192;   // CTAs of a split call at most
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
 
 template <class Launch>

@@ -26,7 +26,7 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     a.slots = a.tokens / tokens + a.batch;
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
-    const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
+    const int grid = static_cast<int>(std::min<int64_t>({most, l.sms, kMaxParts}));
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
     return launch_split(a, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {

@@ -35,7 +35,7 @@
 namespace q4k {
 namespace attn {
 
-constexpr int kMaxCluster = 8;               // portable cluster size
+constexpr int kMaxCluster = 8;               // (the portable size)
 constexpr int kBlock = 16;                   // keys of a ring slot
 constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
@@ -165,7 +165,7 @@ struct RowsShared {
     int lo[R], hi[R], pos[R];              // visible keys of each row, its token
     // what the ranks of a cluster send: their O for this rank's columns ([rank][row][column
     // quad], whatever the number of ranks), and their statistics
-    float4 sent[R * (DP / 4)];
+    float4 sent[R * (DP / 4 + kMaxCluster)];
     float2 stat[kMaxCluster][R];
     unsigned long long full[Sp::KG][Sp::kSlots], empty[Sp::KG][Sp::kSlots];
 };
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         const bool split = a.cluster ? a.cluster > 1 : todo < t.units;
         const bool send = a.cluster > 1;
         constexpr int DQ = DP / 4;                           // column quads
-        const int share = send ? DQ / a.cluster : DQ;        // of a rank
+        const int share = send ? (DQ + a.cluster - 1) / a.cluster : DQ;   // of a rank
         if (send) {
             cluster_wait_acquire();   // every CTA of the cluster has started
             // the row statistics of this CTA, to every rank
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             const int rank = cta % a.cluster;
             for (int i = tid; i < t.rows * share; i += THREADS) {
                 const int r = i / share, d = 4 * (rank * share + i - r * share);
-                if (d >= a.dim) continue;
+                if (d >= a.dim) continue;   // (the last rank's share may end past the head)
                 float mx = -INFINITY, ls = 0.0f;
                 for (int c = 0; c < a.cluster; ++c) mx = fmaxf(mx, sh.stat[c][r].x);
                 float4 v = make_float4(0, 0, 0, 0);

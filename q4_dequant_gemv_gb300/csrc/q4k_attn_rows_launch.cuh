@@ -10,28 +10,29 @@ namespace attn {
 
 constexpr double kSplitCost = 12.0;
 
-// How many clusters of 1, 2, 4 and 8 CTAs of a kernel the GPU holds at once.
+// How many clusters of S CTAs of a kernel the GPU holds at once.
 struct Together {
-    int n[4];
+    int n[kMaxCluster + 1];
 };
 
 template <class Kernel>
 static Together clusters_at_once(Kernel kern, int threads, int smem, int sms)
 {
-    Together t{{sms, 0, 0, 0}};
-    for (int i = 1; i < 4; ++i) {
+    Together t{};
+    t.n[1] = sms;
+    for (int S = 2; S <= kMaxCluster; ++S) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = static_cast<unsigned>(sms) << i;
+        cfg.gridDim = static_cast<unsigned>(sms * S);
         cfg.blockDim = threads;
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 1u << i, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+        at.val.clusterDim.x = S, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&t.n[i], kern, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&t.n[S], kern, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
-            t.n[i] = 0;
+            t.n[S] = 0;
         }
     }
     return t;
@@ -63,14 +64,17 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     cfg.blockDim = Sp::kThreads;
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = l.stream;
-    // clusters of 1, 2, 4, 8 CTAs that run at once
+    // the cluster size that ends soonest: waves of clusters times units of a rank
     static const Together room = clusters_at_once(kern, Sp::kThreads, kSmem, l.sms);
-    int S = kMaxCluster, fit = room.n[3];
-    for (int i = 3; i > 0 && (S > units || items > fit); --i) S /= 2, fit = room.n[i - 1];
-    const int64_t waves = (items + fit - 1) / std::max(fit, 1);
-    const double by_cluster = static_cast<double>(waves) * ((units + S - 1) / S);
+    int S = 1;
+    int64_t by_cluster = INT64_MAX;
+    for (int c = 1; c <= kMaxCluster && c <= units; ++c) {
+        if (room.n[c] < 1) continue;
+        const int64_t cost = (items + room.n[c] - 1) / room.n[c] * ((units + c - 1) / c);
+        if (cost < by_cluster) by_cluster = cost, S = c;
+    }
     const double by_split = static_cast<double>(items) * units / l.sms;
-    if (by_cluster <= by_split + kSplitCost && static_cast<int64_t>(a.slots) * a.kv_heads * S < (1 << 24)) {
+    if (static_cast<double>(by_cluster) <= by_split + kSplitCost && static_cast<int64_t>(a.slots) * a.kv_heads * S < (1 << 24)) {
         a.cluster = S;
         cfg.gridDim = static_cast<unsigned>(a.slots * a.kv_heads * S);
         cudaLaunchAttribute at;
@@ -81,7 +85,7 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
         return cudaLaunchKernelEx(&cfg, kern, maps, a);
     }
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
-    const int grid = static_cast<int>(std::min<int64_t>(most, l.sms));
+    const int grid = static_cast<int>(std::min<int64_t>({most, l.sms, kMaxParts}));
     cfg.gridDim = static_cast<unsigned>(grid);
     return launch_split(a, grid, R, DP, rows_shift<CT>(), l.stream,
                         [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
