@@ -547,11 +547,23 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                     const int c = 2 * j + vch;
                     uint32_t vf[4];
                     ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
+                    if constexpr (PARTS > 1) {
+                        // a block's sum by itself, added to O by an fp32 add: the MMA's own
+                        // additions truncate, which over thousands of blocks is a bias
+                        float sum[NT][4] = {};
 #pragma unroll
-                    for (int p = PARTS - 1; p >= 0; --p)
+                        for (int p = PARTS - 1; p >= 0; --p)   // small parts first
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_t<CT>(sum[nt], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) o[nt][j][z] += sum[nt][z];
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][0][0], pb[nt][0][1]);
+                    }
                 }
             }
             __syncwarp();   // the slot has been read by every lane
