@@ -389,6 +389,10 @@ q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, 
  * it), sets bit 2 of q4k_device_error_flags(), and leaves the outputs that
  * depend on it invalid.  Token rows that belong to no sequence are left as they
  * are.
+ *
+ * Q4K_FLAG_PDL in a call's flags launches its (first) kernel as a programmatic
+ * dependent of the kernel before it on the stream: it may start while that one
+ * still runs and waits for its end before it reads anything.
  */
 #define Q4K_F32 0
 #define Q4K_F16 1
@@ -443,7 +447,8 @@ typedef struct {
     const float *table; /* [table_rows][rot] */
     int64_t tokens, heads, dim, rot, table_rows;
     int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
-    int32_t x_type, y_type, interleaved, reserved;
+    int32_t x_type, y_type, interleaved;
+    uint32_t flags; /* Q4K_FLAG_PDL or 0 */
 } q4k_rope_args;
 
 q4k_status q4k_rope(const q4k_rope_args *a, void *stream);
@@ -482,6 +487,8 @@ typedef struct {
     const float *table;
     int64_t table_rows, rot, q_heads;
     int32_t kv_type, q_type, q_out_type, interleaved;
+    uint32_t flags; /* Q4K_FLAG_PDL or 0 */
+    int32_t reserved;
 } q4k_append_args;
 
 q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, void *stream);
@@ -512,9 +519,12 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  *   8 <= dim <= 256; 16-byte aligned k, v, q, out and strides that keep every
  *   row 16-byte aligned; tokens * q_heads < 2^31.
  *   causal 0 or 1; window >= 0; softcap >= 0 and finite.
- * Scratch comes from cudaMallocAsync on `stream` and is freed on it.  Partial
- * results of split rows are added in a fixed order: the same inputs give the same
- * bits.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
+ * Calls that split rows over the whole GPU (a few long sequences, prompt chunks)
+ * take scratch from cudaMallocAsync on `stream`, freed on it: two partial results
+ * per SM, 0.4 to 44 MB.  Partial results are added in a fixed order: the same
+ * inputs give the same bits.  Q4K_FLAG_TEST_STALL makes the first copy of each
+ * CTA be awaited for 16 bytes more than it brings; the kernel then winds down as
+ * after any wait that runs out (bit 3 of the error flags, outputs invalid).  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
  */
 typedef struct {
     const void *q;
@@ -526,7 +536,10 @@ typedef struct {
     const int32_t *prefix_len; /* [batch] or NULL */
     const int32_t *kv_start;   /* [tokens] or NULL */
     float scale, softcap;
-    int32_t q_type, out_type, causal, reserved;
+    int32_t q_type, out_type, causal;
+    uint32_t flags;         /* Q4K_FLAG_PDL, Q4K_FLAG_TEST_STALL (failure-path tests only) or 0 */
+    uint32_t wait_limit_us; /* bound of each wait inside the kernel; 0 = 2 s */
+    int32_t reserved;
 } q4k_attention_args;
 
 q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);

@@ -16,8 +16,8 @@ _SCALING = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 _ROPE = struct.Struct("@4P 5q 4q 4i")
 _SCALE = struct.Struct("@6d 2i")
 _CACHE = struct.Struct("@2P 6q 4q P 2q 2P 2q 2i")
-_APPEND = struct.Struct("@4P 8q 2P 3q 4i")
-_ATTENTION = struct.Struct("@3P 4q 2q 3P 2f 4i")
+_APPEND = struct.Struct("@4P 8q 2P 3q 6i")
+_ATTENTION = struct.Struct("@3P 4q 2q 3P 2f 6i")
 
 
 _lib = None
@@ -174,7 +174,8 @@ def _new(like, dtype, shape, stream):
     return t, t.data_ptr(), code
 
 
-def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, stream=None):
+def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, stream=None,
+         pdl: bool = False):
     """y [tokens, heads, dim] = x with the first table.shape[1] elements of each head turned by row pos[token] of the
     table; pairs (i, i + rot/2), or (2i, 2i+1) if interleaved.  y may be x."""
     xp, xc, n, h, d, xt, xh = _rows(x, "x")
@@ -189,7 +190,7 @@ def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, st
         yp, yc, _, _, _, yt, yh = _rows(y, "y", h, d, n)
         if out_dtype is not None and y.dtype is not out_dtype:
             raise TypeError(f"y must have dtype {out_dtype}, got {y.dtype}")
-    args = _ROPE.pack(xp, yp, pp, tp, n, h, d, rot, rows, xt, xh, yt, yh, xc, yc, 1 if interleaved else 0, 0)
+    args = _ROPE.pack(xp, yp, pp, tp, n, h, d, rot, rows, xt, xh, yt, yh, xc, yc, 1 if interleaved else 0, 1 if pdl else 0)
     st = (_lib or _load()).q4k_rope(args, _stream(stream, x))
     if st:
         _raise("q4k_rope", st)
@@ -197,7 +198,7 @@ def rope(x, pos, table, y=None, *, interleaved: bool = False, out_dtype=None, st
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=None, interleaved: bool = False, pos=None,
-              q=None, q_out=None, q_dtype=None, stream=None):
+              q=None, q_out=None, q_dtype=None, stream=None, pdl: bool = False):
     """Stores the new tokens' keys (turned by the table) and values [tokens, heads, dim] in the paged cache
     [pages, page size, heads, dim] (any strides).  Rows seq_start[b] .. seq_start[b+1]-1 are the last new tokens of
     sequence b, whose cache holds kv_len[b] positions with them.  q [tokens, q heads, dim], where given, is turned too:
@@ -224,7 +225,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
     elif q_out is not None:
         raise ValueError("q_out without q")
     args = _APPEND.pack(kp, vp, qp, op, kt, kh, vt, vh, qts, qhs, ots, ohs, pp, tp, rows, rot, qh, kc, qc, oc,
-                        1 if interleaved else 0)
+                        1 if interleaved else 0, 1 if pdl else 0, 0)
     st = (_lib or _load()).q4k_kv_append(cache, args, _stream(stream, k))
     if st:
         _raise("q4k_kv_append", st)
@@ -233,12 +234,14 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
 
 def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None, *, scale=None, out_dtype=None,
                     softcap: float = 0.0, slopes=None, window: int = 0, causal: bool = True, prefix_len=None,
-                    kv_start=None, lse=None, stream=None):
+                    kv_start=None, lse=None, stream=None, pdl: bool = False, wait_limit_us: int = 0,
+                    test_stall: bool = False):
     """out [tokens, q heads, dim] = attention of the new tokens over their sequences' cached positions, the new ones
     included (the cache, seq_start and kv_len as kv_append leaves them).  Token t at position p sees
     max(0, kv_start[t], p + 1 - window) <= j < max(p + 1, prefix_len[b]), or < kv_len[b] if not causal.
     scale: 1/sqrt(dim) unless given; softcap > 0: scores softcap * tanh(s / softcap); slopes fp32 [q heads]: minus
-    slopes[h] * |p - j|; lse: fp32 [tokens, q heads], filled with the rows' log-sum-exp."""
+    slopes[h] * |p - j|; lse: fp32 [tokens, q heads], filled with the rows' log-sum-exp.  wait_limit_us, test_stall:
+    bound of the kernel's waits, and a wait made to run out (failure tests)."""
     qp, qc, n, h, d, qt, qh = _rows(q, "q")
     cache, ch, cd, batch = _cache(k_cache, v_cache, page_table, seq_start, kv_len, n)
     if cd != d or ch < 1 or h % ch:
@@ -261,7 +264,8 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None
                            0 if slopes is None else _array(slopes, "slopes", torch.float32, h),
                            0 if prefix_len is None else _array(prefix_len, "prefix_len", _i32, batch),
                            0 if kv_start is None else _array(kv_start, "kv_start", _i32, n),
-                           1.0 / math.sqrt(d) if scale is None else scale, softcap, qc, oc, 1 if causal else 0, 0)
+                           1.0 / math.sqrt(d) if scale is None else scale, softcap, qc, oc, 1 if causal else 0,
+                           (1 if pdl else 0) | (8 if test_stall else 0), wait_limit_us, 0)
     st = (_lib or _load()).q4k_paged_attention(cache, args, _stream(stream, q))
     if st:
         _raise("q4k_paged_attention", st)

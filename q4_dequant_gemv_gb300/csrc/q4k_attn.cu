@@ -179,7 +179,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     if (c->dim % 8 || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
         !type_ok(a->q_type) || !type_ok(a->out_type) || (a->causal & ~1) || a->window < 0 ||
         !std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.0f ||
-        c->tokens * a->q_heads > 0x7FFFFFFF)
+        c->tokens * a->q_heads > 0x7FFFFFFF || (a->flags & ~(Q4K_FLAG_PDL | Q4K_FLAG_TEST_STALL)))
         return Q4K_ERR_INVALID_ARG;
     const bool some = c->tokens > 0 && c->batch > 0;
     if (some && (!a->q || !a->out)) return Q4K_ERR_INVALID_ARG;
@@ -219,6 +219,9 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
     p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
     p.dim = static_cast<int>(c->dim), p.q_type = a->q_type, p.out_type = a->out_type, p.causal = a->causal;
+    p.wait_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 2000000000ull;
+    p.stall = (a->flags & Q4K_FLAG_TEST_STALL) != 0;
+    p.pdl = (a->flags & Q4K_FLAG_PDL) != 0;
     p.error = error_word();
     if (!p.error) return Q4K_ERR_CUDA;
     l.sms = sms;

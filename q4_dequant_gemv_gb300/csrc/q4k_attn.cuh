@@ -65,6 +65,9 @@ struct Args {
     float *part;           // partial results: two slots per CTA
     struct Joint *joint;   // the split tile that starts in each CTA's share
     unsigned int *error;   // the sticky error word
+    uint64_t wait_ns;      // bound of each wait
+    int stall;             // (tests) the first copy of a CTA is awaited for 16 bytes too many
+    bool pdl;              // launched as a programmatic dependent
 };
 
 // A split tile: its rows, and the CTAs c0 .. c1 that hold its parts.  The first of
@@ -376,6 +379,27 @@ cudaError_t launch_split(Args &a, int grid, int R, int width, float shift, cudaS
     const cudaError_t f = cudaFreeAsync(scratch, stream);
     return e == cudaSuccess ? f : e;
 }
+
+// Host: the launch attributes of a first kernel: clusters of `cluster` CTAs (0:
+// none), a programmatic dependent of the kernel before.
+struct Attributes {
+    cudaLaunchAttribute at[2];
+    Attributes(cudaLaunchConfig_t *cfg, int cluster, bool pdl)
+    {
+        cfg->attrs = at;
+        cfg->numAttrs = 0;
+        if (cluster > 0) {
+            cudaLaunchAttribute &c = at[cfg->numAttrs++];
+            c.id = cudaLaunchAttributeClusterDimension;
+            c.val.clusterDim.x = cluster, c.val.clusterDim.y = 1, c.val.clusterDim.z = 1;
+        }
+        if (pdl) {
+            cudaLaunchAttribute &c = at[cfg->numAttrs++];
+            c.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            c.val.programmaticStreamSerializationAllowed = 1;
+        }
+    }
+};
 
 // Host: the maps of a call's cache with boxes of `box` slots.
 bool encode_cache(CacheMaps *maps, const Args &a, int type, int box);

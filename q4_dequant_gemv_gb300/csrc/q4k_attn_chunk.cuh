@@ -51,7 +51,6 @@ constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
 constexpr int kStages = 4;
 // 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
-constexpr uint64_t kChunkWaitNs = 2000000000ull, kWindDownNs = 200000000ull;
 
 // A CTA's part of one tile, as the key warp found it.
 struct Work {
@@ -301,6 +300,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (tid == 32) prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&qmap);
     tm_fence_before();
+    pdl_launch_dependents();
+    pdl_wait();   // (everything below may come from the kernel before)
     typename Sh::Plan plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
     plan.scan();
     tm_fence_after();
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (mbar_try_wait_sleep(b, parity, 20000u)) return true;
             if ((i & 15u) == 0u) {
                 if (*abort) return false;
-                if (globaltimer_ns() - t0 > kChunkWaitNs) {
+                if (globaltimer_ns() - t0 > a.wait_ns) {
                     *abort = 1;
                     atomicOr(a.error, 8u);
                     return false;
@@ -334,7 +335,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     int64_t u = 0, u_end = 0;
     if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
     if (tid == 0) a.joint[cta].rows = 0;
-    pdl_launch_dependents();   // the join waits for this grid's end
 
     // The k-th part of a tile of this CTA, out of the ring; all lanes of a warp.
     auto next_work = [&](int k, Work &item) -> bool {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 uint8_t *dst = sh.kv + stage * kTile;
                 const bool clean = values && (kb < t.from || kb + kChunkKeys > t.hi);
                 unsigned long long &bar = clean ? sh.edge : sh.full[stage];
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes);
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes + (a.stall && !values && unit == 0 ? 16 : 0));
                 __syncwarp();
                 if (live) {
 #pragma unroll
@@ -437,12 +437,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
             }
         }
-        if (!ok) {
-            // every copy issued lands before the CTA exits: this warp's last two stages, the queries
-            for (int i = max(0, unit - 1); i <= unit; ++i)
-                (void)mbar_wait_bounded(smem_u32(&sh.full[2 * (i & 1) + (values ? 1 : 0)]), (i >> 1) & 1, kWindDownNs);
-            if (q_sent) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, kWindDownNs);
-        }
+        // every copy issued lands before the CTA exits (at a wind-down, or its wait runs out): this
+        // warp's last two stages, the queries
+        for (int i = max(0, unit - 2); i < unit + (ok ? 0 : 1); ++i)
+            (void)mbar_wait_bounded(smem_u32(&sh.full[2 * (i & 1) + (values ? 1 : 0)]), (i >> 1) & 1, a.wait_ns);
+        if (!ok && q_sent) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, a.wait_ns);
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
         regs_dec<kOtherRegs>();

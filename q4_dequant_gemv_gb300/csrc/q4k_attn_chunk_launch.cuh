@@ -30,8 +30,13 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return attr;
     return launch_split(a, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
-        kern<<<grid, kChunkThreads, kSmem, l.stream>>>(maps, qmap, args, box);
-        return cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = kChunkThreads;
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.stream = l.stream;
+        const Attributes at(&cfg, 0, args.pdl);
+        return cudaLaunchKernelEx(&cfg, kern, maps, qmap, args, box);
     });
 }
 

@@ -37,7 +37,6 @@ namespace attn {
 
 constexpr int kMaxCluster = 8;               // (the portable size)
 constexpr int kBlock = 16;                   // keys of a ring slot
-constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
 // A tile's shape: NT n8 tiles of query rows per warp, RG warps side by side on a
 // block of keys, KG such groups; slots of a group's ring (128 to 192 KB in all,
@@ -192,6 +191,8 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         if (TMA && tid == 0) prefetch_map(&maps.k), prefetch_map(&maps.v);
     }
     if (a.cluster > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
+    pdl_launch_dependents();
+    pdl_wait();                                    // (everything below may come from the kernel before)
     typename Sh::Plan plan(a, sh.plan, R);         // synchronises the CTA
     const int cta = blockIdx.x;
     int64_t total = 0, u = 0, u_end = 1;
@@ -201,7 +202,6 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
         n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
         if (tid == 0) a.joint[cta].rows = 0;
-        pdl_launch_dependents();   // the join waits for this grid's end
         if (cta >= n) return;
         u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
     }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 if (i > 0 && (i & 31) == 0) look(i);
                 const int page = __shfl_sync(0xffffffffu, ids, i & 31), slot = __shfl_sync(0xffffffffu, slots, i & 31);
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, 2 * Sp::kSide);
+                    mbar_arrive_expect_tx(bar, 2 * Sp::kSide + (a.stall && f == 0 ? 16 : 0));
 #pragma unroll
                     for (int h = 0; h < ND; ++h) {
                         load_box(dst + h * kHalf, &maps.k, 64 * h, slot, head, page, bar);
@@ -401,14 +401,14 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             if (lane == 0) atomicOr(a.error, 8u);
             for (int k = i + 1; k < min(i + SLOTS, count); ++k)
                 (void)mbar_wait_bounded(smem_u32(&sh.full[kg][(first_fill + k) % SLOTS]), ((first_fill + k) / SLOTS) & 1,
-                                        kRowsWaitNs);
+                                        a.wait_ns);
         };
         for (int i = 0; i < count; ++i) {
             const int kb = kb0 + i * Sp::kUnit;
             const uint32_t f = first_fill + i;
             const int slot = static_cast<int>(f % SLOTS);
             const uint32_t kt = ring + slot * 2 * Sp::kSide, vt = kt + Sp::kSide;
-            const bool here = mbar_wait_bounded(smem_u32(&sh.full[kg][slot]), (f / SLOTS) & 1, kRowsWaitNs);
+            const bool here = mbar_wait_bounded(smem_u32(&sh.full[kg][slot]), (f / SLOTS) & 1, a.wait_ns);
             good = __all_sync(0xffffffffu, here);
             if (!good) {
                 wind_down(i);
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 if constexpr (RG > 1) {
                     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[kg][slot]));
                     if (rg == 0) {   // .. of the group's other warp too
-                        const bool free = mbar_wait_bounded(smem_u32(&sh.empty[kg][slot]), reads >> slot & 1, kRowsWaitNs);
+                        const bool free = mbar_wait_bounded(smem_u32(&sh.empty[kg][slot]), reads >> slot & 1, a.wait_ns);
                         reads ^= 1u << slot;
                         good = __all_sync(0xffffffffu, free);
                         if (!good) {

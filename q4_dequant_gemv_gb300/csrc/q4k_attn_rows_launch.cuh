@@ -77,16 +77,13 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     if (static_cast<double>(by_cluster) <= by_split + kSplitCost && static_cast<int64_t>(a.slots) * a.kv_heads * S < (1 << 24)) {
         a.cluster = S;
         cfg.gridDim = static_cast<unsigned>(a.slots * a.kv_heads * S);
-        cudaLaunchAttribute at;
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = S, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
+        const Attributes at(&cfg, S, a.pdl);
         return cudaLaunchKernelEx(&cfg, kern, maps, a);
     }
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
     const int grid = static_cast<int>(std::min<int64_t>({most, l.sms, kMaxParts}));
     cfg.gridDim = static_cast<unsigned>(grid);
+    const Attributes at(&cfg, 0, a.pdl);
     return launch_split(a, grid, R, DP, rows_shift<CT>(), l.stream,
                         [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
 }

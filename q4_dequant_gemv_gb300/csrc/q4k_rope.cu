@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "../../include/q4k.h"
+#include "ptx.cuh"
 #include "q4k_attn.cuh"
 #include "q4k_internal.h"
 
@@ -155,6 +156,7 @@ struct TokenArgs {
     const float *table;
     int batch, tokens, dim, rot, inter;
     int units, items;         // per head, per token
+    bool pdl;                 // launched as a programmatic dependent
     int warps;                // of a token
 };
 
@@ -208,6 +210,7 @@ __device__ __forceinline__ Place place_of(const TokenArgs &a, int t)
 template <bool APPEND, int TOK>
 __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
 {
+    pdl_launch_dependents();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = w / a.warps;   // of TOK tokens, within the CTA
     const int i = (blockIdx.y * a.warps + (w - group * a.warps)) * 32 + lane;
@@ -226,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
     const int ia = split ? 4 * j : 8 * j, apart = split ? p.rot >> 1 : 4;
     const int xs = p.xtype == Q4K_F32 ? 4 : 2, ys = p.ytype == Q4K_F32 ? 4 : 2;
 
+    pdl_wait();   // (everything below may come from the kernel before)
     uint4 ra[TOK], rb[TOK];
     const uint8_t *src = static_cast<const uint8_t *>(p.x) + (t0 * p.xt + h * p.xh + ia) * xs;
     const int64_t next = p.xt * xs;   // bytes to the next token
@@ -290,6 +294,8 @@ __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
 template <bool APPEND>
 __global__ void __launch_bounds__(kThreads) narrow_kernel(const TokenArgs a)
 {
+    pdl_launch_dependents();
+    pdl_wait();
     const int w = threadIdx.x >> 5;
     const int per = static_cast<int>(blockDim.x >> 5) / a.warps;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * per + w / a.warps;
@@ -344,10 +350,18 @@ static q4k_status launch_tokens(TokenArgs &a, bool wide, int sms, void *stream)
     };
     auto s = static_cast<cudaStream_t>(stream);
     // several tokens a thread once that still fills the GPU (1024 threads an SM)
-    if (!wide) narrow_kernel<APPEND><<<grid(1), threads, 0, s>>>(a);
-    else if (static_cast<int64_t>(a.tokens) * need * 32 >= 1024LL * kTok * sms) wide_kernel<APPEND, kTok><<<grid(kTok), threads, 0, s>>>(a);
-    else wide_kernel<APPEND, 1><<<grid(1), threads, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+    const int tok = wide && static_cast<int64_t>(a.tokens) * need * 32 >= 1024LL * kTok * sms ? kTok : 1;
+    auto kern = !wide ? narrow_kernel<APPEND> : tok > 1 ? wide_kernel<APPEND, kTok> : wide_kernel<APPEND, 1>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid(tok);
+    cfg.blockDim = threads;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = a.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
 static bool good_type(int t) { return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16; }
@@ -420,7 +434,7 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
     using namespace rope;
     if (!a || a->tokens < 0 || a->tokens > 0x7FFFFFFF || a->heads < 1 || a->heads > 65536 || a->dim < 1 ||
         a->dim > 65536 || a->rot < 0 || a->rot % 2 || a->rot > a->dim || a->rot > kMaxRot || a->table_rows < 0 ||
-        !good_type(a->x_type) || !good_type(a->y_type) || (a->interleaved & ~1))
+        !good_type(a->x_type) || !good_type(a->y_type) || (a->interleaved & ~1) || (a->flags & ~Q4K_FLAG_PDL))
         return Q4K_ERR_INVALID_ARG;
     if (a->tokens > 0 && (!a->x || !a->y || (a->rot && (!a->pos || !a->table)))) return Q4K_ERR_INVALID_ARG;
     if (off(a->x, size_of(a->x_type)) || off(a->y, size_of(a->y_type)) || off(a->pos, 4) || off(a->table, 4))
@@ -433,7 +447,7 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
                      static_cast<int>(a->heads), a->x_type, a->y_type, static_cast<int>(a->rot)};
     p.pos = a->pos, p.table = a->table, p.table_rows = a->table_rows;
     p.tokens = static_cast<int>(a->tokens), p.dim = static_cast<int>(a->dim), p.rot = static_cast<int>(a->rot);
-    p.inter = a->interleaved;
+    p.inter = a->interleaved, p.pdl = a->flags & Q4K_FLAG_PDL;
     const Part &r = p.part[0];
     const bool wide = a->dim % 8 == 0 && a->rot % 8 == 0 && !off(a->table, 16) &&
                       wide_rows(a->x, a->x_type, r.xt, r.xh) && wide_rows(a->y, a->y_type, r.yt, r.yh);
@@ -462,7 +476,7 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
     if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
     const bool some = c->tokens > 0 && c->batch > 0;
     if (a->rot < 0 || a->rot % 2 || a->rot > c->dim || a->rot > kMaxRot || a->table_rows < 0 ||
-        !good_type(a->kv_type) || (a->interleaved & ~1) || (a->q == nullptr) != (a->q_out == nullptr))
+        !good_type(a->kv_type) || (a->interleaved & ~1) || (a->flags & ~Q4K_FLAG_PDL) || (a->q == nullptr) != (a->q_out == nullptr))
         return Q4K_ERR_INVALID_ARG;
     if (a->q && (a->q_heads < 1 || a->q_heads > 65536 || !good_type(a->q_type) || !good_type(a->q_out_type)))
         return Q4K_ERR_INVALID_ARG;
@@ -486,7 +500,7 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
     p.page_table = c->page_table, p.seq_start = c->seq_start, p.kv_len = c->kv_len, p.pos = a->pos;
     p.table = a->table, p.table_rows = a->table_rows;
     p.batch = static_cast<int>(c->batch), p.tokens = static_cast<int>(c->tokens), p.dim = static_cast<int>(c->dim);
-    p.rot = rot, p.inter = a->interleaved;
+    p.rot = rot, p.inter = a->interleaved, p.pdl = a->flags & Q4K_FLAG_PDL;
     const Part &k = p.part[0], &v = p.part[1], &q = p.part[2];
     bool wide = c->dim % 8 == 0 && rot % 8 == 0 && !off(a->table, 16) && wide_rows(a->k, a->kv_type, k.xt, k.xh) &&
                 wide_rows(a->v, a->kv_type, v.xt, v.xh) && wide_rows(c->k, c->type, p.k_page, p.k_slot) &&
