@@ -22,6 +22,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/q4k.h"
 #include "ptx.cuh"
@@ -80,6 +81,13 @@ struct Part {
 };
 
 template <int TYPE>
+__device__ __forceinline__ void convert4(const uint2 &r, float (&f)[4])
+{
+    const float2 a = attn::unpack2(r.x, TYPE), b = attn::unpack2(r.y, TYPE);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+
+template <int TYPE>
 __device__ __forceinline__ void convert4(const uint4 &r, float (&f)[4])
 {
     if constexpr (TYPE == Q4K_F32) {
@@ -99,9 +107,9 @@ __device__ __forceinline__ void store4(uint8_t *p, const float (&f)[4])
 
 // TOK tokens' unit: converted, turned by their c and s (kind 1: halves apart,
 // kind 2: neighbours, 0: copied) and stored where `to` is not null.
-template <int XT, int YT, int TOK>
-__device__ __forceinline__ void finish(const uint4 (&ra)[TOK], const uint4 (&rb)[TOK], const float4 (&c)[TOK],
-                                       const float4 (&s)[TOK], uint8_t *const (&to)[TOK], int apart, int kind)
+template <int XT, int YT, int TOK, class Raw>
+__device__ __forceinline__ void finish(const Raw *ra, const Raw *rb, const float4 (&c)[TOK], const float4 (&s)[TOK],
+                                       uint8_t *const (&to)[TOK], int apart, int kind)
 {
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
@@ -201,14 +209,15 @@ __device__ __forceinline__ Place place_of(const TokenArgs &a, int t)
 }
 
 // TOK consecutive tokens per thread: their data is loaded first; then lane j of
-// each warp places token j; then they are turned and stored.  Bound by memory
-// latency: one token a thread leaves too little in flight, eight spill, and
-// small CTAs even out the tail.  4097 tokens x 32 heads x 128 in bf16, half of
-// each head turned (68 MB): 16.2 us, 4.2 TB/s (a copy of the same size takes
-// 11.7); 2048 tokens of q, k and v from fp32 (58 MB): 14.9 us, 3.9 TB/s.  The
-// same with 512 threads of one token: 25 and 17 us; 256 of four: 17.4 and 14.9.
-template <bool APPEND, int TOK>
-__global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
+// each warp places token j; then they are turned and stored.  HALF: all data is
+// 16-bit (fewer registers, more threads).  Bound by memory latency: one token a
+// thread leaves too little in flight, eight take the registers of other threads,
+// and small CTAs even out the tail.  4097 tokens x 32 heads x 128 in bf16, half of
+// each head turned (68 MB): 14.0 us, 4.9 TB/s (a copy of the same size takes 11.7);
+// one token a thread 25 us, eight 15.8.  2048 tokens of q, k and v from fp32 (58
+// MB): 14.9 us, 3.9 TB/s.
+template <bool APPEND, int TOK, bool HALF>
+__global__ void __launch_bounds__(kThreads, HALF ? 7 : 6) wide_kernel(const TokenArgs a)
 {
     pdl_launch_dependents();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,16 +239,19 @@ __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
     const int xs = p.xtype == Q4K_F32 ? 4 : 2, ys = p.ytype == Q4K_F32 ? 4 : 2;
 
     pdl_wait();   // (everything below may come from the kernel before)
-    uint4 ra[TOK], rb[TOK];
+    // (as they lie in memory: a conversion next to its load would wait for it)
+    using Raw = typename std::conditional<HALF, uint2, uint4>::type;
+    Raw ra[TOK], rb[TOK];
     const uint8_t *src = static_cast<const uint8_t *>(p.x) + (t0 * p.xt + h * p.xh + ia) * xs;
     const int64_t next = p.xt * xs;   // bytes to the next token
-    // (as they lie in memory: a conversion next to its load would wait for it)
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-        ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
+        ra[k] = rb[k] = Raw{};
         if (live && t0 + k < a.tokens) {
             const uint8_t *q = src + k * next;
-            if (xs == 4) {
+            if constexpr (HALF) {
+                ra[k] = *reinterpret_cast<const uint2 *>(q), rb[k] = *reinterpret_cast<const uint2 *>(q + 2 * apart);
+            } else if (xs == 4) {
                 ra[k] = *reinterpret_cast<const uint4 *>(q);
                 rb[k] = *reinterpret_cast<const uint4 *>(q + 4 * apart);
             } else {
@@ -256,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
     uint8_t *dst = static_cast<uint8_t *>(p.y) + (h * p.yh + ia) * ys;
     const float *trow = a.table + (a.inter ? ia >> 1 : ia);
     const int64_t per_page = (part ? a.v_page : a.k_page) * ys, per_slot = (part ? a.v_slot : a.k_slot) * ys;
+    const int kind = !turned ? 0 : split ? 1 : 2;
     float4 c[TOK], s[TOK];
     uint8_t *to[TOK];
 #pragma unroll
@@ -275,17 +288,19 @@ __global__ void __launch_bounds__(kThreads, 6) wide_kernel(const TokenArgs a)
         }
         to[k] = good ? dst + o : nullptr;
     }
-    const int kind = !turned ? 0 : split ? 1 : 2;
     switch (3 * p.xtype + p.ytype) {
-        case 3 * Q4K_F32 + Q4K_F32: finish<Q4K_F32, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
-        case 3 * Q4K_F32 + Q4K_F16: finish<Q4K_F32, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
-        case 3 * Q4K_F32 + Q4K_BF16: finish<Q4K_F32, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind); break;
         case 3 * Q4K_F16 + Q4K_F32: finish<Q4K_F16, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
         case 3 * Q4K_F16 + Q4K_F16: finish<Q4K_F16, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
         case 3 * Q4K_F16 + Q4K_BF16: finish<Q4K_F16, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind); break;
         case 3 * Q4K_BF16 + Q4K_F32: finish<Q4K_BF16, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind); break;
         case 3 * Q4K_BF16 + Q4K_F16: finish<Q4K_BF16, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind); break;
-        default: finish<Q4K_BF16, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind);
+        case 3 * Q4K_BF16 + Q4K_BF16: finish<Q4K_BF16, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind); break;
+        default:
+            if constexpr (!HALF) {
+                if (p.ytype == Q4K_F32) finish<Q4K_F32, Q4K_F32, TOK>(ra, rb, c, s, to, apart, kind);
+                else if (p.ytype == Q4K_F16) finish<Q4K_F32, Q4K_F16, TOK>(ra, rb, c, s, to, apart, kind);
+                else finish<Q4K_F32, Q4K_BF16, TOK>(ra, rb, c, s, to, apart, kind);
+            }
     }
 }
 
@@ -350,10 +365,14 @@ static q4k_status launch_tokens(TokenArgs &a, bool wide, int sms, void *stream)
     };
     auto s = static_cast<cudaStream_t>(stream);
     // several tokens a thread once that still fills the GPU (1024 threads an SM)
-    const int tok = wide && static_cast<int64_t>(a.tokens) * need * 32 >= 1024LL * kTok * sms ? kTok : 1;
-    auto kern = !wide ? narrow_kernel<APPEND> : tok > 1 ? wide_kernel<APPEND, kTok> : wide_kernel<APPEND, 1>;
+    const bool many = wide && static_cast<int64_t>(a.tokens) * need * 32 >= 1024LL * kTok * sms;
+    bool half = true;
+    for (const Part &p : a.part) half = half && (!p.heads || p.xtype != Q4K_F32);
+    auto kern = !wide ? narrow_kernel<APPEND>
+                : !many ? wide_kernel<APPEND, 1, false>
+                : half ? wide_kernel<APPEND, kTok, true> : wide_kernel<APPEND, kTok, false>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid(tok);
+    cfg.gridDim = grid(many ? kTok : 1);
     cfg.blockDim = threads;
     cfg.stream = s;
     cudaLaunchAttribute at;
