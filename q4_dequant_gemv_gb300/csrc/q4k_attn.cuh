@@ -276,6 +276,10 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return a / b;
 }
 
+// How many of `grid` CTAs share `total` units: at least two units each (a part
+// costs the join more than a unit saves).
+__device__ __forceinline__ int sharers(int64_t total, int grid) { return static_cast<int>(min(static_cast<int64_t>(grid), (total + 1) / 2)); }
+
 // A CTA's share [begin, end) of `total` units over n CTAs, and the CTA that
 // holds a unit.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return quotient(total * c, n); }

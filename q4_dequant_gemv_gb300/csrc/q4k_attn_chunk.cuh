@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
 
     const int64_t total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
-    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int n = sharers(total, gridDim.x);
     const int cta = blockIdx.x;
     int64_t u = 0, u_end = 0;
     if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
     if (!a.cluster) {
         plan.scan();
         total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
-        n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+        n = sharers(total, gridDim.x);
         if (tid == 0) a.joint[cta].rows = 0;
         if (cta >= n) return;
         u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);

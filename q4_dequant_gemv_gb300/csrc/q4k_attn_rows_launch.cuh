@@ -8,7 +8,7 @@
 namespace q4k {
 namespace attn {
 
-constexpr double kSplitCost = 12.0;
+constexpr double kSplitCost = 18.0;
 
 // How many clusters of S CTAs of a kernel the GPU holds at once.
 struct Together {
@@ -99,10 +99,10 @@ static cudaError_t launch_rows_tiles(const RowsLaunch &l)
 {
     // the smallest tile that holds a sequence's rows (a second tile reads its
     // keys again): those of one token where there are as many tokens as
-    // sequences, else half as many again as the average.  dim > 128 leaves
-    // registers for 16.
-    const int64_t batch = l.args.batch, group = l.args.group;
-    const int64_t rows = l.args.tokens == batch ? group : (3 * l.args.tokens * group + 2 * batch - 1) / (2 * batch);
+    // sequences, all of a single sequence, else half as many again as the average.
+    // dim > 128 leaves registers for 16.
+    const int64_t batch = l.args.batch, all = static_cast<int64_t>(l.args.tokens) * l.args.group;
+    const int64_t rows = l.args.tokens == batch ? l.args.group : batch == 1 ? all : (3 * all + 2 * batch - 1) / (2 * batch);
     if (rows <= 8) return launch_rows_one<CT, PARTS, 1, 1, DP>(l);
     if constexpr (DP <= 128) {
         if (rows > 32) return launch_rows_one<CT, PARTS, 3, 2, DP>(l);
