@@ -520,8 +520,9 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  *   row 16-byte aligned; tokens * q_heads < 2^31.
  *   causal 0 or 1; window >= 0; softcap >= 0 and finite.
  * Calls that split rows over the whole GPU (a few long sequences, prompt chunks)
- * take scratch from cudaMallocAsync on `stream`, freed on it: two partial results
- * per SM, 0.4 to 44 MB.  Partial results are added in a fixed order: the same
+ * take scratch on `stream` from a stream-ordered pool of the library's own, which
+ * keeps it for later calls: two partial results per SM, 0.4 to 44 MB for each call
+ * in flight.  Partial results are added in a fixed order: the same
  * inputs give the same bits.  Q4K_FLAG_TEST_STALL makes the first copy of each
  * CTA be awaited for 16 bytes more than it brings; the kernel then winds down as
  * after any wait that runs out (bit 3 of the error flags, outputs invalid).  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.

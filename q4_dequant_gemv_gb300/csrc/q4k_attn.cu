@@ -3,6 +3,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "../../include/q4k.h"
@@ -43,6 +44,42 @@ static unsigned int *error_word()
 }
 
 namespace attn {
+
+// Scratch comes from a pool of the library's own, one per device, that keeps its
+// memory: the default pool gives it back to the system whenever the program
+// synchronises, and the next call then waits 250 us for it.
+cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream)
+{
+    constexpr int kDevices = 64;
+    static cudaMemPool_t pools[kDevices] = {};
+    static std::mutex lock;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    cudaMemPool_t pool;
+    {
+        const std::lock_guard<std::mutex> hold(lock);
+        if (!pools[dev]) {
+            cudaMemPoolProps props = {};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = dev;
+            cudaMemPool_t made = nullptr;
+            e = cudaMemPoolCreate(&made, &props);
+            if (e != cudaSuccess) return e;
+            cuuint64_t keep = UINT64_MAX;
+            e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (e != cudaSuccess) {
+                (void)cudaMemPoolDestroy(made);
+                return e;
+            }
+            pools[dev] = made;
+        }
+        pool = pools[dev];
+    }
+    return cudaMallocFromPoolAsync(p, bytes, pool, stream);
+}
 
 bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
 {

@@ -367,6 +367,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
 // tiles that it left split; R rows and `width` columns a slot.
 constexpr int kJoinThreads = 256, kJoinRows = 32;
 constexpr int kMaxParts = 192;   // CTAs of a split call at most
+cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream);   // freed with cudaFreeAsync
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
 
 template <class Launch>
@@ -374,7 +375,7 @@ cudaError_t launch_split(Args &a, int grid, int R, int width, float shift, cudaS
 {
     const size_t head = (grid * sizeof(Joint) + 255) / 256 * 256;
     void *scratch = nullptr;
-    cudaError_t e = cudaMallocAsync(&scratch, head + static_cast<size_t>(grid) * 2 * R * (width + 2) * sizeof(float), stream);
+    cudaError_t e = take_scratch(&scratch, head + static_cast<size_t>(grid) * 2 * R * (width + 2) * sizeof(float), stream);
     if (e != cudaSuccess) return e;
     a.joint = static_cast<Joint *>(scratch);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);
