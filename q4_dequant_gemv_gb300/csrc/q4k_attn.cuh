@@ -193,12 +193,13 @@ struct Split {
     {
         const int tid = threadIdx.x;
         for (int i = tid; i <= a.batch; i += THREADS) {
-            const int s = a.seq_start[i];
-            if (s < 0 || s > a.tokens || (i > 0 && s < a.seq_start[i - 1])) atomicOr(a.error, 4u);
+            // (all three on their way before any is looked at)
+            const int s = a.seq_start[i], before = i > 0 ? a.seq_start[i - 1] : 0, len = i < a.batch ? a.kv_len[i] : 0;
             if (a.batch <= kSeqs) {
                 sh.start[i] = s;
-                if (i < a.batch) sh.len[i] = a.kv_len[i];
+                if (i < a.batch) sh.len[i] = len;
             }
+            if (s < before || s < 0 || s > a.tokens) atomicOr(a.error, 4u);
         }
         __syncthreads();
     }

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
         const int kb0 = t.lo + off * Sp::kUnit + kBlock * kg;
         const int count = good && kb0 < t.hi ? min(todo, (t.hi - kb0 + Sp::kUnit - 1) / Sp::kUnit) : 0;
-        // pages and slots of the next 32 blocks, a lane each (TMA)
+        // pages and slots of the next 32 blocks, a lane each (TMA): loaded, then checked
         int ids = 0, slots = 0;
         auto look = [&](int first) {
             const int i = first + lane;
@@ -249,10 +249,12 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 int e;
                 page_of(a, kb0 + i * Sp::kUnit, e, slots);
                 ids = pages[e];
-                if (ids < 0 || ids >= a.pages) {
-                    atomicOr(a.error, 4u);
-                    ids = 0;
-                }
+            }
+        };
+        auto check = [&]() {
+            if (ids < 0 || ids >= a.pages) {
+                atomicOr(a.error, 4u);
+                ids = 0;
             }
         };
         // block i into its slot, by the group's first warp
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             const int s = static_cast<int>(f % SLOTS);
             const uint32_t dst = ring + s * 2 * Sp::kSide, bar = smem_u32(&sh.full[kg][s]);
             if constexpr (TMA) {
-                if (i > 0 && (i & 31) == 0) look(i);
+                if (i > 0 && (i & 31) == 0) look(i), check();
                 const int page = __shfl_sync(0xffffffffu, ids, i & 31), slot = __shfl_sync(0xffffffffu, slots, i & 31);
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, 2 * Sp::kSide + (a.stall && f == 0 ? 16 : 0));
@@ -332,6 +334,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 }
             }
         }
+        if constexpr (TMA) check();
         const uint32_t first_fill = fills;
         fills += count;
         if (rg == 0) {
