@@ -115,18 +115,21 @@ __device__ __forceinline__ Range token_range(const Args &a, int seq, int pos, in
 // R (rows of a tile) is given at run time; ALIGN: where units start (a power of two).
 template <int U, int THREADS, int ALIGN>
 struct Split {
-    static constexpr int kStripes = 512;     // prefix entries; each covers `stripe` tile slots
     static constexpr int kSeqs = 512;        // sequence starts held in shared memory
     struct Shared {
-        uint32_t prefix[kStripes];
+        uint32_t prefix[THREADS];            // units up to the end of each stripe of tile slots
         int start[kSeqs + 1], len[kSeqs];
         uint32_t warp[THREADS / 32];
+        Tile first;                          // the tile of `hand_out`
+        int offset;
     };
 
     const Args &a;
     Shared &sh;
     const int R;
-    int stripe;
+    int stripe;             // slots of a prefix entry
+    Tile mine;              // the slot of this thread where an entry is one slot (without kv_start)
+    uint32_t before;        // units before this thread's entry
     uint32_t per_head;      // units of one cache head
 
     __device__ __forceinline__ int start_of(int b) const
@@ -173,6 +176,7 @@ struct Split {
         const Range last = token_range(a, b, t.pos0 + i1, s0 + i1, t.len);
         int lo = last.hi;
         if (WARP && a.kv_start) {
+#pragma unroll 4
             for (int i = i0 + static_cast<int>(threadIdx.x & 31); i <= i1; i += 32) {
                 const Range r = token_range(a, b, t.pos0 + i, s0 + i, t.len);
                 if (r.hi > r.lo) lo = min(lo, r.lo);
@@ -208,28 +212,24 @@ struct Split {
     __device__ __forceinline__ void scan()
     {
         const int tid = threadIdx.x;
-        stripe = (a.slots + kStripes - 1) / kStripes;
-        constexpr int PER = (kStripes + THREADS - 1) / THREADS;   // consecutive prefix entries of a thread
-        uint32_t sum[PER], run = 0;
-        const int e0 = tid * PER;
+        stripe = (a.slots + THREADS - 1) / THREADS;
+        uint32_t units = 0;
         if (a.kv_start) {   // a warp per entry: its lanes share a tile's tokens
-            for (int e = tid >> 5; e < kStripes; e += THREADS / 32) {
-                uint32_t units = 0;
-                for (int s = e * stripe; s < min((e + 1) * stripe, a.slots); ++s) units += tile<true>(s).units;
-                if ((tid & 31) == 0) sh.prefix[e] = units;
+            const int entries = (a.slots + stripe - 1) / stripe;
+            for (int e = tid >> 5; e < entries; e += THREADS / 32) {
+                uint32_t n = 0;
+                for (int s = e * stripe; s < min((e + 1) * stripe, a.slots); ++s) n += tile<true>(s).units;
+                if ((tid & 31) == 0) sh.prefix[e] = n;
             }
             __syncthreads();
-        }
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if (a.kv_start) {
-                if (e0 + j < kStripes) run += sh.prefix[e0 + j];
-            } else {
-                for (int s = (e0 + j) * stripe; s < min((e0 + j + 1) * stripe, a.slots); ++s) run += tile<false>(s).units;
+            if (tid < entries) units = sh.prefix[tid];
+        } else {
+            for (int s = tid * stripe; s < min((tid + 1) * stripe, a.slots); ++s) {
+                mine = tile<false>(s);
+                units += mine.units;
             }
-            sum[j] = run;
         }
-        uint32_t incl = run;
+        uint32_t incl = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -237,23 +237,35 @@ struct Split {
         }
         if ((tid & 31) == 31) sh.warp[tid >> 5] = incl;
         __syncthreads();
-        uint32_t before = 0, total = 0;
+        uint32_t base = 0, total = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < (tid >> 5)) before += sh.warp[w];
+            if (w < (tid >> 5)) base += sh.warp[w];
             total += sh.warp[w];
         }
-        before += incl - run;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (e0 + j < kStripes) sh.prefix[e0 + j] = before + sum[j];
+        before = base + incl - units;
+        sh.prefix[tid] = base + incl;
         per_head = total;
+    }
+
+    // Where each entry is one slot, the thread that holds unit r leaves its tile in
+    // `first`; all threads of the CTA (it also completes the prefix).  False:
+    // `locate` has to find it.
+    __device__ __forceinline__ bool hand_out(uint32_t r)
+    {
+        const bool known = stripe == 1 && !a.kv_start;
+        if (known && r >= before && r < sh.prefix[threadIdx.x]) {
+            sh.first = mine, sh.offset = static_cast<int>(r - before);
+            const int len = a.batch <= kSeqs ? sh.len[mine.seq] : a.kv_len[mine.seq];
+            if (len < 0 || len > a.capacity) atomicOr(a.error, 4u);
+        }
         __syncthreads();
+        return known;
     }
 
     // The tile that holds unit r (< per_head) of a cache head, and r's place in it; whole warps.
     __device__ __forceinline__ Tile locate(uint32_t r, int &offset) const
     {
-        int lo = 0, hi = kStripes - 1;
+        int lo = 0, hi = THREADS - 1;
         while (lo < hi) {
             const int m = (lo + hi) >> 1;
             if (sh.prefix[m] > r) hi = m; else lo = m + 1;
@@ -275,6 +287,12 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
+}
+
+// A unit's place within its cache head.
+__device__ __forceinline__ uint32_t per_head_rest(int64_t unit, uint32_t per_head)
+{
+    return per_head ? static_cast<uint32_t>(unit - quotient(unit, per_head) * per_head) : 0u;
 }
 
 // How many of `grid` CTAs share `total` units: at least two units each (a part

@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int cta = blockIdx.x;
     int64_t u = 0, u_end = 0;
     if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+    const bool known = plan.hand_out(per_head_rest(u, plan.per_head));   // the first tile
     if (tid == 0) a.joint[cta].rows = 0;
 
     // The k-th part of a tile of this CTA, out of the ring; all lanes of a warp.
@@ -353,6 +354,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int unit = 0, edges = 0, k = 0;   // this warp's stage of unit i: 2 (i % 2), + 1 for values
         bool ok = true, q_sent = false;
         const int per = kChunkKeys / box;
+        auto queries = [&](const Work &item) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(&sh.q_full), tokens * a.group * 128 * ND);
+#pragma unroll
+                for (int h = 0; h < ND; ++h)
+                    load_rows(smem_u32(sh.q + h * 2 * kHalf), &qmap, 64 * h, item.head * a.group,
+                              item.t.tok0 + item.t.first / a.group, smem_u32(&sh.q_full));
+            }
+            q_sent = true;
+            __syncwarp();
+        };
         for (; ok; ++k) {
             Work item;
             if (values) {
@@ -364,7 +376,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 item.todo = 0;
                 if (u < u_end) {
                     item.head = static_cast<int>(quotient(u, plan.per_head));
-                    item.t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(item.head) * plan.per_head), item.off);
+                    if (k == 0 && known) item.t = sh.plan.first, item.off = sh.plan.offset;
+                    else item.t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(item.head) * plan.per_head), item.off);
                     item.todo = static_cast<int>(min(static_cast<int64_t>(item.t.units - item.off), u_end - u));
                     item.last = share_owner(total, n, u - item.off + item.t.units - 1);
                     u += item.todo;
@@ -378,6 +391,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             const Tile &t = item.t;
             const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
+            if (!values && k == 0) queries(item);
             for (int i = 0; i < item.todo && ok; ++i, ++unit) {
                 const int kb = t.lo + (item.off + i) * kChunkKeys;
                 const int stage = 2 * (unit & 1) + (values ? 1 : 0);
@@ -407,18 +421,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         load_box(smem_u32(dst + h * kHalf + lane * box * 128), map, 64 * h, slot, item.head, page,
                                  smem_u32(&bar));
                 }
-                if (i == 0 && !values) {
+                if (i == 0 && k > 0 && !values) {
                     // the tile's queries, once the last scores of the tile before are done
-                    if (k > 0 && !(ok = wait(sh.q_empty, (k - 1) & 1))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(smem_u32(&sh.q_full), tokens * a.group * 128 * ND);
-#pragma unroll
-                        for (int h = 0; h < ND; ++h)
-                            load_rows(smem_u32(sh.q + h * 2 * kHalf), &qmap, 64 * h, item.head * a.group,
-                                      t.tok0 + t.first / a.group, smem_u32(&sh.q_full));
-                    }
-                    q_sent = true;
-                    __syncwarp();
+                    if (!(ok = wait(sh.q_empty, (k - 1) & 1))) break;
+                    queries(item);
                 }
                 if (clean) {
                     // zero the rows that nothing of the tile sees, then hand the stage on

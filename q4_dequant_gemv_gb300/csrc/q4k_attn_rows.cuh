@@ -197,13 +197,16 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
     const int cta = blockIdx.x;
     int64_t total = 0, u = 0, u_end = 1;
     int n = 0;
+    bool known = false;   // the first tile has been handed out
     if (!a.cluster) {
         plan.scan();
         total = static_cast<int64_t>(plan.per_head) * a.kv_heads;
         n = sharers(total, gridDim.x);
         if (tid == 0) a.joint[cta].rows = 0;
-        if (cta >= n) return;
-        u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+        if (cta < n) u = share_begin(total, n, cta), u_end = share_begin(total, n, cta + 1);
+        else u_end = 0;
+        const uint32_t at = per_head_rest(u, plan.per_head);
+        known = plan.hand_out(at) && u < u_end;
     }
 
     const uint32_t ring = smem_u32(sh.ring[kg]);
@@ -231,7 +234,9 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             todo = t.units * (rank + 1) / a.cluster - off;
         } else {
             head = static_cast<int>(quotient(u, plan.per_head));
-            t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            if (known) t = sh.plan.first, off = sh.plan.offset;
+            else t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(head) * plan.per_head), off);
+            known = false;
             u0 = u - off;
             todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
         }
