@@ -327,3 +327,35 @@ def test_refusals(q4k):
         assert e.value.status == 1
     torch.cuda.synchronize()
     assert q4k.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 0.7])
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (F32, F16, F32)])
+def test_scales(q4k, scale, types):
+    """Negative, zero and large scales, masked rows among them."""
+    for new, lens in (([1], [70]), ([90, 3], [200, 40])):
+        _run(q4k, dict(new=new, len=lens, window=33), 4, 2, 64, 16, *types, scale=scale)
+
+
+@pytest.mark.parametrize("H", [130, 260])
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (F32, BF16, F32)])
+def test_large_groups(q4k, H, types):
+    """More query heads per cache head than half a tile of rows holds, and than a whole one."""
+    _run(q4k, dict(new=[3, 1], len=[90, 20]), H, 1, 64, 16, *types)
+
+
+def test_one_page_table_column_and_empty_cache(q4k):
+    """A page table one column wide; no cached position: every row sees nothing; a cache without pages: refused."""
+    _run(q4k, dict(new=[1, 5], len=[13, 16]), 4, 2, 64, 16)
+    kc = torch.zeros(0, 16, 2, 64, dtype=BF16, device="cuda")
+    for dtype, n in ((BF16, 1), (F32, 1), (BF16, 40)):
+        q = torch.ones(n, 4, 64, dtype=dtype, device="cuda")
+        out = torch.full_like(q, 3.0)
+        pt = torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+        with pytest.raises(q4k.Q4KError):      # no cache to point at
+            q4k.paged_attention(q, kc, kc, pt, _dev([0, n]), _dev([0]), out)
+        one = torch.zeros(1, 16, 2, 64, dtype=BF16, device="cuda")
+        q4k.paged_attention(q, one, one, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), _dev([0, n]), _dev([0]), out)
+        torch.cuda.synchronize()
+        assert not out.any()
+    assert q4k.device_error_flags() == 0
