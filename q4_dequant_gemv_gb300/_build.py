@@ -1,7 +1,8 @@
 """Build step for the Q4_K CUDA library: nvcc for sm_103a, in-tree.
 
 Compiles every .cu under csrc/ (in parallel) and links them into libq4k.so next
-to this file.  The library is plain C ABI (include/q4k.h); no torch headers.
+to this file.  The library is plain C ABI (include/q4k.h); no torch headers.  The
+marshalling module beside it (csrc/q4k_marshal.c) is plain C over CPython's API.
 """
 from __future__ import annotations
 
@@ -10,12 +11,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libq4k.so")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,14 +38,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.[ch]")) + \
         [os.path.join(INCLUDE, "q4k.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -63,8 +66,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
+    def compile_marshal():
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
+               sysconfig.get_paths()["include"], os.path.join(CSRC, "q4k_marshal.c"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the marshalling module failed to build:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, MARSHAL)
+
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        marshal = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, srcs))
+        marshal.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:

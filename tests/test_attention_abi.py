@@ -4,12 +4,19 @@ import ctypes
 import math
 import os
 import shutil
+import struct
 import subprocess
 
 import pytest
 
 torch = pytest.importorskip("torch")
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+# The structures of include/q4k.h, field by field (native alignment).
+ROPE = struct.Struct("@4P 5q 4q 4i")
+SCALE = struct.Struct("@6d 2i")
+CACHE = struct.Struct("@2P 6q 4q P 2q 2P 2q 2i")
+APPEND = struct.Struct("@4P 8q 2P 3q 6i")
+ATTENTION = struct.Struct("@3P 4q 2q 3P 2f 6i")
 OK = 0x10000   # an aligned address that is never followed on these paths
 
 
@@ -25,7 +32,6 @@ def test_structures_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if not cc:
         pytest.skip("no C compiler")
-    from q4_dequant_gemv_gb300 import _attention as A
     src = tmp_path / "s.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "q4k.h"\nint main(void) {\n'
                    'printf("%zu %zu %zu %zu %zu ", sizeof(q4k_rope_args), sizeof(q4k_rope_scaling), '
@@ -36,15 +42,14 @@ def test_structures_match_the_header(tmp_path):
     exe = str(tmp_path / "s")
     subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     got = [int(v) for v in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
-    structs = [A._ROPE, A._SCALE, A._CACHE, A._APPEND, A._ATTENTION]
+    structs = [ROPE, SCALE, CACHE, APPEND, ATTENTION]
     assert got[:5] == [s.size for s in structs]
     ints = [4, 2, 2, 6, 6]          # the 4-byte fields at the end (the attention's follow two floats)
     assert got[5:] == [s.size - 4 * n for s, n in zip(structs, ints)]
 
 
 def _scaling(base=10000.0, factor=1.0, orig=0.0, low=1.0, high=32.0, mag=1.0, kind=0):
-    from q4_dequant_gemv_gb300 import _attention as A
-    return A._SCALE.pack(base, factor, orig, low, high, mag, kind, 0)
+    return SCALE.pack(base, factor, orig, low, high, mag, kind, 0)
 
 
 def test_rope_table_arguments(L):
@@ -64,10 +69,9 @@ def test_rope_table_arguments(L):
 
 
 def _rope(**kw):
-    from q4_dequant_gemv_gb300 import _attention as A
     d = dict(x=OK, y=OK, pos=OK, table=OK, tokens=2, heads=3, dim=64, rot=64, rows=8, xt=192, xh=64, yt=192, yh=64, xc=0,
              yc=0, inter=0, flags=0) | kw
-    return A._ROPE.pack(*d.values())
+    return ROPE.pack(*d.values())
 
 
 def test_rope_arguments(L):
@@ -82,17 +86,15 @@ def test_rope_arguments(L):
 
 
 def _cache(**kw):
-    from q4_dequant_gemv_gb300 import _attention as A
     d = dict(k=OK, v=OK, kp=2048, ks=128, kh=64, vp=2048, vs=128, vh=64, pages=4, size=16, heads=2, dim=64, table=OK, row=2,
              most=2, start=OK, len=OK, batch=1, tokens=2, type=2, pad=0) | kw
-    return A._CACHE.pack(*d.values())
+    return CACHE.pack(*d.values())
 
 
 def _append(**kw):
-    from q4_dequant_gemv_gb300 import _attention as A
     d = dict(k=OK, v=OK, q=0, qo=0, kt=128, kh=64, vt=128, vh=64, qt=0, qh=0, ot=0, oh=0, pos=0, table=OK, rows=8, rot=64,
              heads=0, kc=0, qc=0, oc=0, inter=0, flags=0, pad=0) | kw
-    return A._APPEND.pack(*d.values())
+    return APPEND.pack(*d.values())
 
 
 BAD_CACHES = (dict(batch=-1), dict(tokens=-1), dict(pages=-1), dict(size=0), dict(heads=0), dict(dim=0), dict(most=-1),
@@ -114,10 +116,9 @@ def test_append_arguments(L):
 
 
 def _attention(**kw):
-    from q4_dequant_gemv_gb300 import _attention as A
     d = dict(q=OK, out=OK, lse=0, qt=256, qh=64, ot=256, oh=64, heads=4, window=0, slopes=0, prefix=0, start=0, scale=0.125,
              cap=0.0, qc=2, oc=2, causal=1, flags=0, limit=0, pad=0) | kw
-    return A._ATTENTION.pack(*d.values())
+    return ATTENTION.pack(*d.values())
 
 
 def test_attention_arguments(L):
