@@ -525,7 +525,13 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  * in flight.  Partial results are added in a fixed order: the same
  * inputs give the same bits.  Q4K_FLAG_TEST_STALL makes the first copy of each
  * CTA be awaited for 16 bytes more than it brings; the kernel then winds down as
- * after any wait that runs out (bit 3 of the error flags, outputs invalid).  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
+ * after any wait that runs out (bit 3 of the error flags, outputs invalid).
+ * Q4K_FLAG_ATTN_FORM(n) has a call take one form of the kernels, normally chosen
+ * by the library from the sizes: tiles of 8, 16 or 32 query rows, each by a cluster
+ * of CTAs (Q4K_ATTN_CLUSTER8, 16, 32) or with the work split over the GPU
+ * (Q4K_ATTN_SPLIT8, 16, 32; tiles of 32 for dim <= 128), or tiles of 256 rows on
+ * tcgen05 (Q4K_ATTN_MANY: q of the cache's type, a 16-bit out, dim <= 128, pages of
+ * a multiple of 16, scale >= 0); INVALID_ARG where the call cannot take it.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
  */
 typedef struct {
     const void *q;
@@ -538,10 +544,19 @@ typedef struct {
     const int32_t *kv_start;   /* [tokens] or NULL */
     float scale, softcap;
     int32_t q_type, out_type, causal;
-    uint32_t flags;         /* Q4K_FLAG_PDL, Q4K_FLAG_TEST_STALL (failure-path tests only) or 0 */
+    uint32_t flags;         /* Q4K_FLAG_PDL, Q4K_FLAG_TEST_STALL (failure-path tests only), Q4K_FLAG_ATTN_FORM(n) or 0 */
     uint32_t wait_limit_us; /* bound of each wait inside the kernel; 0 = 2 s */
     int32_t reserved;
 } q4k_attention_args;
+
+#define Q4K_FLAG_ATTN_FORM(n) ((uint32_t)(n) << 8)
+#define Q4K_ATTN_CLUSTER8 1
+#define Q4K_ATTN_CLUSTER16 2
+#define Q4K_ATTN_CLUSTER32 3
+#define Q4K_ATTN_SPLIT8 4
+#define Q4K_ATTN_SPLIT16 5
+#define Q4K_ATTN_SPLIT32 6
+#define Q4K_ATTN_MANY 7
 
 q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
 

@@ -10,6 +10,7 @@ import struct
 import torch
 
 _SCALING = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+_FORMS = {None: 0, "cluster8": 1, "cluster16": 2, "cluster32": 3, "split8": 4, "split16": 5, "split32": 6, "many": 7}
 _SCALE = struct.Struct("@6d 2i")      # q4k_rope_scaling
 
 # The handle of a device's current stream, without building a Stream object around it (3 us a call).
@@ -85,13 +86,17 @@ def kv_append(k, v, k_cache, v_cache, page_table, seq_start, kv_len, *, table=No
 def paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out=None, *, scale=None, out_dtype=None,
                     softcap: float = 0.0, slopes=None, window: int = 0, causal: bool = True, prefix_len=None,
                     kv_start=None, lse=None, stream=None, pdl: bool = False, wait_limit_us: int = 0,
-                    test_stall: bool = False):
+                    test_stall: bool = False, form=None):
     """out [tokens, q heads, dim] = attention of the new tokens over their sequences' cached positions, the new ones
     included (the cache, seq_start and kv_len as kv_append leaves them).  Token t at position p sees
     max(0, kv_start[t], p + 1 - window) <= j < max(p + 1, prefix_len[b]), or < kv_len[b] if not causal.
     scale: 1/sqrt(dim) unless given; softcap > 0: scores softcap * tanh(s / softcap); slopes fp32 [q heads]: minus
     slopes[h] * |p - j|; lse: fp32 [tokens, q heads], filled with the rows' log-sum-exp.  wait_limit_us, test_stall:
-    bound of the kernel's waits, and a wait made to run out (failure tests)."""
+    bound of the kernel's waits, and a wait made to run out (failure tests).  form: one form of the kernels, "cluster8"
+    .. "many", instead of the library's choice by sizes."""
+    if form not in _FORMS:
+        raise ValueError(f"form must be one of {list(_FORMS)}")
     return (_calls or _load()).paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out, scale, out_dtype,
                                                softcap, slopes, window, causal, prefix_len, kv_start, lse, stream,
-                                               (1 if pdl else 0) | (8 if test_stall else 0), wait_limit_us)
+                                               (1 if pdl else 0) | (8 if test_stall else 0) | _FORMS[form] << 8,
+                                               wait_limit_us)

@@ -8,6 +8,7 @@
 
 #include "../../include/q4k.h"
 #include "q4k_attn_chunk.cuh"
+#include "q4k_attn_plan.h"
 #include "q4k_attn_rows.cuh"
 #include "q4k_internal.h"
 
@@ -216,7 +217,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     if (c->dim % 8 || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
         !type_ok(a->q_type) || !type_ok(a->out_type) || (a->causal & ~1) || a->window < 0 ||
         !std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.0f ||
-        c->tokens * a->q_heads > 0x7FFFFFFF || (a->flags & ~(Q4K_FLAG_PDL | Q4K_FLAG_TEST_STALL)))
+        c->tokens * a->q_heads > 0x7FFFFFFF || (a->flags & ~(Q4K_FLAG_PDL | Q4K_FLAG_TEST_STALL | Q4K_FLAG_ATTN_FORM(7))))
         return Q4K_ERR_INVALID_ARG;
     const bool some = c->tokens > 0 && c->batch > 0;
     if (some && (!a->q || !a->out)) return Q4K_ERR_INVALID_ARG;
@@ -264,11 +265,9 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     l.sms = sms;
     l.stream = static_cast<cudaStream_t>(stream);
     l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
-    // The tcgen05 kernel takes calls with more query rows per sequence and cache
-    // head than the mma.sync kernel holds at once (16), in one 16-bit type, over
-    // pages that split into boxes of 16 slots or more.  Its TMA boxes also ask for
-    // positive strides and groups of 256 heads at most, its maxima for a scale
-    // that is not negative.
+    // The tcgen05 kernel takes q of the cache's type, a 16-bit out and pages that split into
+    // boxes of 16 slots or more.  Its TMA boxes also ask for positive strides and
+    // groups of 256 heads at most, its maxima for a scale that is not negative.
     auto stride_ok = [](int64_t s) { return s > 0 && s < (int64_t{1} << 39); };
     const bool boxes = c->page_size % 16 == 0 && stride_ok(c->k_slot_stride) && stride_ok(c->v_slot_stride) &&
                        (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
@@ -276,8 +275,15 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     l.boxes = boxes && p.capacity > 0;
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
                          (c->tokens == 1 || stride_ok(a->q_token_stride)) && (a->q_heads == 1 || stride_ok(a->q_head_stride));
+    static int room[attn::kMaxCluster + 1];
+    static cudaError_t e_room = attn::clusters_at_once(room);
+    if (e_room != cudaSuccess) return Q4K_ERR_CUDA;
+    const int parts = !l.parts_many ? 1 : c->type == Q4K_F16 ? 2 : 3;
+    l.choice = attn::choose(p, room, sms, parts, !l.parts_many && c->dim <= 128 && l.boxes && queries,
+                            static_cast<int>(a->flags >> 8 & 7));
+    if (!l.choice.chunk && !l.choice.rows) return Q4K_ERR_INVALID_ARG;
     cudaError_t e;
-    if (!l.parts_many && c->dim <= 128 && l.boxes && queries && c->tokens * p.group > 16 * c->batch) {
+    if (l.choice.chunk) {
         const attn::ChunkLaunch ch{p, sms, l.stream};
         e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {

@@ -82,7 +82,7 @@ __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * 
 // One tile: the rows, their token range and the keys that any of them sees.
 struct Tile {
     int seq, first, rows;      // first row in the sequence, number of rows (0: nothing to do)
-    int tok0, ntok;            // first token row of the sequence in the call, its tokens
+    int tok0;                  // first token row of the sequence in the call
     int pos0;                  // position of the sequence's first new token
     int len;                   // cached positions (clamped to the page table)
     int from, hi;              // keys [from, hi) that some row sees
@@ -163,7 +163,7 @@ struct Split {
         }
         const int s0 = start_of(b), n = start_of(b + 1) - s0, all = n * a.group;
         const int raw = a.batch <= kSeqs ? sh.len[b] : a.kv_len[b];
-        t.seq = b, t.tok0 = s0, t.ntok = n;
+        t.seq = b, t.tok0 = s0;
         if (n <= 0 || j < 0 || j > (all - 1) / R) return t;
         t.first = j * R;
         t.rows = min(R, all - t.first);
@@ -359,11 +359,6 @@ __device__ __forceinline__ void page_of(const Args &a, int key, int &entry, int 
     entry = a.page_shift >= 0 ? key >> a.page_shift
                               : static_cast<int>(static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size));
     slot = key - entry * a.page_size;
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // The cache as two 4-D tensors [page][head][slot][d], and a box of one cache

@@ -97,18 +97,6 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, float *r)
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *u)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(u[0]),
-        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
-        "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
-        "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
-        : "memory");
-}
-
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u)
 {
     asm volatile(
@@ -298,7 +286,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         fence_barrier_init();
         sh.abort = 0;
     }
-    if (tid == 32) prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&qmap);
+    if (tid == 32) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v), prefetch_tensormap(&qmap);
     tm_fence_before();
     pdl_launch_dependents();
     pdl_wait();   // (everything below may come from the kernel before)

@@ -1,12 +1,12 @@
 // q4k_attn_rows.cuh -- attention of a few query rows per cache head (decode and
 // verification) on mma.sync.
 //
-// Such a call reads every visible key and value once for 1 to 48 query rows: at
+// Such a call reads every visible key and value once for 1 to 32 query rows: at
 // 7 rows 7 flops a byte, far below what any tensor path offers, so the kernel is
 // bound by memory and by how many bytes are in flight.  A warp owns blocks of 16
 // keys and a ring of its own in shared memory, fills a slot ahead of time and
 // refills it when it has read it: no barrier between warps until they join at
-// the end of a tile, and 130 to 190 KB in flight per SM.  Tiles of 32 and 48
+// the end of a tile, and 130 to 190 KB in flight per SM.  Tiles of 32
 // rows give each block to two warps, half of the rows each (registers).
 //   S^T = K Q^T: A = 16 keys x 16 d (ldmatrix), B = Q^T from shared memory;
 //   O^T = V^T P^T: A = 16 d x 16 keys (ldmatrix.trans), B = P^T from the S^T
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         mbar_init(smem_u32(&sh.full[0][0] + tid), TMA ? 1 : 32);
         mbar_init(smem_u32(&sh.empty[0][0] + tid), RG);
         fence_barrier_init();
-        if (TMA && tid == 0) prefetch_map(&maps.k), prefetch_map(&maps.v);
+        if (TMA && tid == 0) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
     }
     if (a.cluster > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
     pdl_launch_dependents();
@@ -688,12 +688,21 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
 }
 
 // Launches the kernel of one cache type (in a translation unit of its own).
+// What q4k_attn_plan.h chose for a call.
+struct Choice {
+    bool chunk;    // the many-rows kernel
+    int rows;      // few-rows: query rows of a tile
+    int cluster;   // few-rows: CTAs of a cluster per tile, 0: split over the SMs
+};
+
 struct RowsLaunch {
     Args args;
+    Choice choice;
     int sms, parts_many;   // parts_many: fp32 queries or outputs, or a 16-bit type that is not the cache's
     bool boxes;            // pages and strides that TMA boxes of 16 slots can take
     cudaStream_t stream;
 };
+cudaError_t clusters_at_once(int (&n)[kMaxCluster + 1]);
 cudaError_t launch_rows_f16(const RowsLaunch &l);
 cudaError_t launch_rows_bf16(const RowsLaunch &l);
 
