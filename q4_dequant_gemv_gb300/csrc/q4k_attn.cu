@@ -1,6 +1,7 @@
 // q4k_attn.cu -- q4k_paged_attention: argument checks and the choice of kernel.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -120,20 +121,28 @@ bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens)
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A statistic of `slab` rows of up to `grid` parts, in whole float4.
+__host__ __device__ __forceinline__ int join_floats(int slab, int grid) { return (slab * grid + 3) & ~3; }
+
 // Adds the parts of split tiles: blockIdx.x = the CTA in whose share the tile
-// begins, blockIdx.y = 32 of its rows.  Bound by trips to memory, so there are
-// three: the tile, all parts' statistics (they become weights in shared memory),
-// then a thread's column quads of several parts at once.  Launched as the first
-// kernel's programmatic dependent.
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R, int width, float shift)
+// begins, blockIdx.y = `slab` of its rows.  Bound by trips to memory, so there are
+// three: the tile, all parts' statistics (they become weights in shared memory), then
+// column quads.  A slab of a few rows has fewer quads than the CTA has threads: groups
+// of threads take a range of the parts each, and their sums are added in order.  One
+// CTA a tile of 8 rows, a part after the other, cost 0.4 us a part: 2 heads of 30000
+// positions 28.6 us, now 16.8; 8 heads of 131072 93, now 90.  Launched as the first
+// kernel's programmatic dependent; its shared memory is sized by the call, so that
+// after the few-rows kernel it is already there, beside that kernel's rings.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R, int slab, int width, float shift)
 {
-    __shared__ float s_m[kMaxParts * kJoinRows], s_l[kMaxParts * kJoinRows];
+    extern __shared__ __align__(16) float s_stats[];
+    float *s_m = s_stats, *s_l = s_stats + join_floats(slab, gridDim.x);   // (s_l: later the sums of thread groups)
     __shared__ float s_max[kJoinRows], s_sum[kJoinRows];
     pdl_wait();
     const int4 t0 = __ldcg(reinterpret_cast<const int4 *>(a.joint + blockIdx.x));
     const int2 t1 = __ldcg(reinterpret_cast<const int2 *>(a.joint + blockIdx.x) + 2);
     const Joint t{t0.x, t0.y, t0.z, t0.w, t1.x, t1.y};
-    const int r0 = blockIdx.y * kJoinRows, rows = min(min(R, kJoinRows), t.rows - r0);
+    const int r0 = blockIdx.y * slab, rows = min(min(R - r0, slab), t.rows - r0);
     if (rows <= 0) return;
     const int tid = threadIdx.x, parts = t.c1 - t.c0 + 1;
     const int64_t size = static_cast<int64_t>(R) * (width + 2);
@@ -146,28 +155,81 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R,
         s_m[i] = __ldcg(p), s_l[i] = __ldcg(p + R);
     }
     __syncthreads();
-    if (tid < rows) {
-        float mx = -INFINITY, ls = 0.0f;
-        for (int q = 0; q < parts; ++q) mx = fmaxf(mx, s_m[q * rows + tid]);
-        for (int q = 0; q < parts; ++q) {
-            const float f = weight(s_m[q * rows + tid], mx);
-            s_m[q * rows + tid] = f;
-            ls += f * s_l[q * rows + tid];
+    if (parts <= 8 && rows > kJoinThreads / 32) {
+        if (tid < rows) {
+            float mx = -INFINITY, ls = 0.0f;
+            for (int q = 0; q < parts; ++q) mx = fmaxf(mx, s_m[q * rows + tid]);
+            for (int q = 0; q < parts; ++q) {
+                const float f = weight(s_m[q * rows + tid], mx);
+                s_m[q * rows + tid] = f;
+                ls += f * s_l[q * rows + tid];
+            }
+            s_max[tid] = mx, s_sum[tid] = ls;
         }
-        s_max[tid] = mx, s_sum[tid] = ls;
+    } else {
+        for (int r = tid >> 5; r < rows; r += kJoinThreads / 32) {
+            float mx = -INFINITY, ls = 0.0f;
+            for (int q = tid & 31; q < parts; q += 32) mx = fmaxf(mx, s_m[q * rows + r]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int q = tid & 31; q < parts; q += 32) {
+                const float f = weight(s_m[q * rows + r], mx);
+                s_m[q * rows + r] = f;
+                ls += f * s_l[q * rows + r];
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            if ((tid & 31) == 0) s_max[r] = mx, s_sum[r] = ls;
+        }
     }
     __syncthreads();
-    // neighbouring threads on neighbouring rows; a few parts: more quads in flight, many: more parts
-    auto add = [&](auto per_c, auto deep_c) {
+    const int quads = rows * (a.dim / 4);
+    auto finish = [&](int r, int c, float4 v) {
+        const int row = t.first + r0 + r, tok = row / a.group;
+        finish_row(a, t.tok0 + tok, t.head * a.group + row - tok * a.group, 4 * c, v, s_max[r], s_sum[r], shift);
+    };
+    if (quads <= kJoinThreads) {
+        // groups of threads take a range of the parts each, eight loads on their way at once
+        const int groups = max(1, min(kJoinThreads / quads, (parts + 3) / 4));
+        const int g = tid / quads, i = tid - g * quads, c = i / rows, r = i - c * rows;
+        float4 v = make_float4(0, 0, 0, 0);
+        if (g < groups) {
+            const int q1 = parts * (g + 1) / groups;
+            for (int q = parts * g / groups; q < q1; q += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    x[d] = q + d < q1 ? __ldcg(reinterpret_cast<const float4 *>(slot(q + d) - r0) + r0 + c * R + r)
+                                      : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    const float f = q + d < q1 ? s_m[(q + d) * rows + r] : 0.0f;
+                    v.x += f * x[d].x, v.y += f * x[d].y, v.z += f * x[d].z, v.w += f * x[d].w;
+                }
+            }
+        }
+        float4 *s_v = reinterpret_cast<float4 *>(s_l);
+        s_v[tid] = v;
+        __syncthreads();
+        if (g) return;
+        for (int k = 1; k < groups; ++k) {
+            const float4 x = s_v[k * quads + i];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        finish(r, c, v);
+        return;
+    }
+    // else a thread takes PER quads i, i + kJoinThreads, .. (neighbouring threads on neighbouring
+    // rows): a few parts: more quads in flight, many: more parts
+    auto several = [&](auto per_c, auto deep_c) {
         constexpr int PER = decltype(per_c)::value, DEEP = decltype(deep_c)::value;
-        const int quads = rows * (a.dim / 4);
         for (int i = tid; i < quads; i += PER * kJoinThreads) {
             float4 v[PER];
             int c[PER], r[PER];
 #pragma unroll
             for (int k = 0; k < PER; ++k) {   // (quads past the end are read again, not stored)
-                const int j = i + k * kJoinThreads < quads ? i + k * kJoinThreads : i;
-                c[k] = j / rows, r[k] = j - c[k] * rows;
+                const int n = i + k * kJoinThreads < quads ? i + k * kJoinThreads : i;
+                c[k] = n / rows, r[k] = n - c[k] * rows;
                 v[k] = make_float4(0, 0, 0, 0);
             }
 #pragma unroll DEEP
@@ -181,30 +243,31 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R,
                 }
             }
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                if (i + k * kJoinThreads >= quads) break;
-                const int row = t.first + r0 + r[k], tok = row / a.group;
-                finish_row(a, t.tok0 + tok, t.head * a.group + row - tok * a.group, 4 * c[k], v[k], s_max[r[k]], s_sum[r[k]],
-                           shift);
-            }
+            for (int k = 0; k < PER; ++k)
+                if (i + k * kJoinThreads < quads) finish(r[k], c[k], v[k]);
         }
     };
-    if (parts <= 4) add(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    else add(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
+    if (parts <= 4) several(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    else several(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
 }
 
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream)
 {
+    // Few large tiles have many parts each (16 tokens over 14336: 27.6 us with slabs of 16
+    // rows, 31.9 of 32), many have two or three (three chunks of 512 tokens: 84 and 79).
+    const int slab = R <= 32 ? 2 : static_cast<int64_t>(a.slots) * a.kv_heads * 3 <= grid ? kJoinRows / 2 : kJoinRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, (R + kJoinRows - 1) / kJoinRows);
+    cfg.gridDim = dim3(grid, (R + slab - 1) / slab);
     cfg.blockDim = kJoinThreads;
+    const int floats = join_floats(slab, grid);
+    cfg.dynamicSmemBytes = 4 * floats + std::max<int>(4 * floats, 16 * kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel, a, R, width, shift);
+    return cudaLaunchKernelEx(&cfg, join_kernel, a, R, slab, width, shift);
 }
 
 }  // namespace attn

@@ -379,8 +379,8 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
 
 // Host: scratch of `grid` CTAs, the first kernel by `launch(args)`, the join of the
 // tiles that it left split; R rows and `width` columns a slot.
-constexpr int kJoinThreads = 256, kJoinRows = 32;
-constexpr int kMaxParts = 192;   // CTAs of a split call at most
+constexpr int kJoinThreads = 256, kJoinRows = 32;   // of a CTA of the join at most
+constexpr int kMaxParts = 184;   // CTAs of a split call at most (the join's statistics: 47 KB)
 cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream);   // freed with cudaFreeAsync
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
 
