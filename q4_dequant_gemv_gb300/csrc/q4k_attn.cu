@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int R,
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream)
 {
     // Few large tiles have many parts each (16 tokens over 14336: 27.6 us with slabs of 16
-    // rows, 31.9 of 32), many have two or three (three chunks of 512 tokens: 84 and 79).
+    // rows, 31.9 of 32), many have two or three (three chunks of 512 tokens: 84 and 81).
     const int slab = R <= 32 ? 2 : static_cast<int64_t>(a.slots) * a.kv_heads * 3 <= grid ? kJoinRows / 2 : kJoinRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, (R + slab - 1) / slab);

@@ -8,10 +8,10 @@
 //     second launch to join, then a start per tile and the units;
 //   * many-rows kernel (tcgen05), 256 rows a tile, split the same way.
 // Small tiles fill the GPU and read keys again (from L2), large ones read them
-// once.  The estimate below, in us, was fitted to 495 measured calls (1 to 64
-// sequences of 1 to 16 tokens, 28/4 and 32/8 heads of 128, 16/16 of 64, 200 to
-// 16000 positions, 16-bit and fp32 queries), each in every form: its choice is
-// within 1.4 % of the fastest on the geometric mean (1.37x at worst), where the
+// once.  The estimate below, in us, was fitted to 1317 measured calls (1 to 64
+// sequences of 1 to 8 tokens, 28/4, 32/8 and 16/2 heads of 128, 16/16 of 64, 200 to
+// 30000 positions, 16-bit and fp32 queries), each in every form: its choice is
+// within 1.2 % of the fastest on the geometric mean (1.4x at worst), where the
 // rule before it (the smallest tile that holds a sequence's rows, clusters by units,
 // the tcgen05 kernel above 16 rows) was 16 % off.  Both sides of it, in us:
 //   4 sequences of 5 x 7 rows over 2000: clusters with tiles of 8 rows 15, of 16 22, of 32 24;
@@ -38,6 +38,8 @@ struct Cost {
     double unit, part, wave, tile, split;
 };
 constexpr Cost kCosts[] = {{8, 0.83, 0.11, 5.0, 3.0, 9.5}, {16, 1.05, 0.25, 5.7, 4.0, 11.3}, {32, 1.0, 0.23, 7.5, 5.0, 18.0}};
+// A split: per further CTA of a tile (the join), where shares cut through tiles.
+constexpr double kJoinPart = 0.2, kCut = 4.0;
 constexpr double kChunkCall = 14.0, kChunkTile = 4.5, kChunkUnit = 1.35;
 
 inline int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
@@ -48,10 +50,14 @@ inline Choice choose(const Args &a, const int (&room)[kMaxCluster + 1], int sms,
 {
     Choice best{};
     double least = 1e300;
-    // keys that a tile can see: a causal window's, where no prefix reaches past it
+    // keys that a token can see, about: a window's (a prefix may reach past it)
     int64_t keys = a.capacity;
-    if (a.window > 0 && a.causal && !a.prefix_len) keys = std::min<int64_t>(keys, int64_t{a.window} + up(a.tokens, a.batch));
-    const double small = a.dim <= 64 ? 0.7 : 1.0, small_split = a.dim <= 64 ? 0.9 : 1.0;
+    if (a.window > 0) keys = std::min<int64_t>(keys, int64_t{a.window} + up(a.tokens, a.batch));
+    const double small = a.dim <= 64 ? 0.7 : 1.0, small_split = a.dim <= 64 ? 1.1 : 1.0;
+    auto join = [&](int64_t tiles, int64_t units) {
+        const double ctas = std::min<double>(sms, 0.5 * static_cast<double>(tiles * units));
+        return kJoinPart * std::max(0.0, ctas / static_cast<double>(tiles) - 1.0);
+    };
     // tiles of a sequence of average length; where lengths differ some have one more
     const double slack = a.tokens % a.batch ? 1.15 : 1.0;
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
@@ -69,13 +75,15 @@ inline Choice choose(const Args &a, const int (&room)[kMaxCluster + 1], int sms,
             const double us = 2.0 + static_cast<double>(waves) * (c.wave + each * small * static_cast<double>(up(units, S)));
             if (us < least) least = us, best = {false, c.rows, S};
         }
-        const double us = c.split + static_cast<double>(tiles) / sms * (c.tile + each * small_split * static_cast<double>(units));
+        const double us = c.split + (tiles >= sms || sms % tiles ? kCut : 0.0) + join(tiles, units) +
+                          static_cast<double>(tiles) / sms * (c.tile + each * small_split * static_cast<double>(units));
         if (split && us < least) least = us, best = {false, c.rows, 0};
     }
     if (may_chunk && (!form || form == Q4K_ATTN_MANY)) {
         const int64_t tiles = int64_t{a.kv_heads} * a.batch * up(a.tokens, int64_t{kChunkRows / a.group} * a.batch);
-        const double us = kChunkCall + static_cast<double>(tiles) / sms * (a.dim <= 64 ? 0.8 : 1.0) *
-                                           (kChunkTile + kChunkUnit * static_cast<double>(keys / kChunkKeys + 1));
+        const double us = kChunkCall + join(tiles, keys / kChunkKeys + 1) +
+                          static_cast<double>(tiles) / sms * (a.dim <= 64 ? 0.8 : 1.0) *
+                              (kChunkTile + kChunkUnit * static_cast<double>(keys / kChunkKeys + 1));
         if (us < least) best = {true, 0, 0};
     }
     return best;

@@ -26,8 +26,8 @@
 // exact in fp32.  fp16: a power of two per query row brings max|q| to 2^14, and
 // P carries 2^14, so the low parts stay above fp16's subnormals.
 //
-// Measured (device): one token of 32 / 8 bf16 heads over 131072 positions 92 us,
-// 5.8 TB/s = 87 % of a copy's rate (keys straight into registers 142, rings 97, the
+// Measured (device): one token of 32 / 8 bf16 heads over 131072 positions 90 us,
+// 5.9 TB/s = 89 % of a copy's rate (keys straight into registers 142, rings 97, the
 // join in three trips 94); sixteen fp32 tokens of 28 / 4 heads over 4096 26.4 us (58
 // without rings, 37 without clusters); one over 1000 7.4 us, five dependent trips to
 // memory; four times five tokens over 2000, scores capped, 15.4 us.
