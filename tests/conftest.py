@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -17,3 +18,33 @@ def oracle_mod():
     import oracle
     oracle.build()
     return oracle
+
+
+@pytest.fixture(autouse=True)
+def no_collection_in_captures(request, monkeypatch):
+    """Destroying a CUDA graph invalidates every capture that is under way, and a graph that a test leaves in a cycle (a
+    kept exception reaches its frames) is destroyed whenever the collector runs.  So it does not run inside
+    torch.cuda.graph."""
+    if request.node.get_closest_marker("gpu") is None:
+        yield
+        return
+    import torch
+    enter, leave = torch.cuda.graph.__enter__, torch.cuda.graph.__exit__
+
+    def paused(self):
+        gc.disable()
+        try:
+            return enter(self)
+        except BaseException:
+            gc.enable()
+            raise
+
+    def resumed(self, *exc):
+        try:
+            return leave(self, *exc)
+        finally:
+            gc.enable()
+
+    monkeypatch.setattr(torch.cuda.graph, "__enter__", paused)
+    monkeypatch.setattr(torch.cuda.graph, "__exit__", resumed)
+    yield
