@@ -384,7 +384,7 @@ q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, 
  *
  * page_table, seq_start, kv_len and the other index arrays are device memory and
  * are read only by the kernels, so a call needs no host copy of them and can be
- * captured in a graph.  The kernels check them: a position, page, row range or
+ * captured in a graph, a process's first one too.  The kernels check them: a position, page, row range or
  * length outside the buffers is not followed (nothing is read or written through
  * it), sets bit 2 of q4k_device_error_flags(), and leaves the outputs that
  * depend on it invalid.  Token rows that belong to no sequence are left as they

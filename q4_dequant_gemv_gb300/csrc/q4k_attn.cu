@@ -47,6 +47,15 @@ static unsigned int *error_word()
 
 namespace attn {
 
+// Calls of this thread that a capture under way on another stream, or on the
+// call's own, does not concern: creating a pool is refused during a capture
+// otherwise, and ends it.
+struct BesideCaptures {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    BesideCaptures() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~BesideCaptures() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Scratch comes from a pool of the library's own, one per device, that keeps its
 // memory: the default pool gives it back to the system whenever the program
 // synchronises, and the next call then waits 250 us for it.
@@ -63,6 +72,7 @@ cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream)
     {
         const std::lock_guard<std::mutex> hold(lock);
         if (!pools[dev]) {
+            const BesideCaptures beside;   // (a first call may be a captured one)
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;
