@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 #include <type_traits>
 
 #include "../../include/q4k.h"
@@ -30,19 +29,14 @@ bool clear_attn_error()
     return cudaMemcpyToSymbol(g_attn_error, &z, sizeof(z)) == cudaSuccess;
 }
 
-// Device address of the error word on the current device (looked up once per device).
-static unsigned int *error_word()
+// Address of the error word on a device.
+static cudaError_t error_word(int dev, unsigned int **p)
 {
-    constexpr int kDevices = 64;
-    static unsigned int *at[kDevices] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return nullptr;
-    unsigned int *p = __atomic_load_n(&at[dev], __ATOMIC_ACQUIRE);
-    if (p) return p;
-    void *v = nullptr;
-    if (cudaGetSymbolAddress(&v, g_attn_error) != cudaSuccess) return nullptr;
-    __atomic_store_n(&at[dev], static_cast<unsigned int *>(v), __ATOMIC_RELEASE);
-    return static_cast<unsigned int *>(v);
+    static unsigned int *at[attn::kDevices];
+    static attn::OncePerDevice once;
+    const cudaError_t e = once(dev, [&] { return cudaGetSymbolAddress(reinterpret_cast<void **>(&at[dev]), g_attn_error); });
+    *p = at[dev];
+    return e;
 }
 
 namespace attn {
@@ -59,38 +53,35 @@ struct BesideCaptures {
 // Scratch comes from a pool of the library's own, one per device, that keeps its
 // memory: the default pool gives it back to the system whenever the program
 // synchronises, and the next call then waits 250 us for it.
-cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream)
+cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream)
 {
-    constexpr int kDevices = 64;
-    static cudaMemPool_t pools[kDevices] = {};
-    static std::mutex lock;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= kDevices) return cudaErrorInvalidDevice;
-    cudaMemPool_t pool;
-    {
-        const std::lock_guard<std::mutex> hold(lock);
-        if (!pools[dev]) {
-            const BesideCaptures beside;   // (a first call may be a captured one)
-            cudaMemPoolProps props = {};
-            props.allocType = cudaMemAllocationTypePinned;
-            props.location.type = cudaMemLocationTypeDevice;
-            props.location.id = dev;
-            cudaMemPool_t made = nullptr;
-            e = cudaMemPoolCreate(&made, &props);
-            if (e != cudaSuccess) return e;
-            cuuint64_t keep = UINT64_MAX;
-            e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
-            if (e != cudaSuccess) {
-                (void)cudaMemPoolDestroy(made);
-                return e;
-            }
-            pools[dev] = made;
-        }
-        pool = pools[dev];
-    }
-    return cudaMallocFromPoolAsync(p, bytes, pool, stream);
+    static cudaMemPool_t pools[kDevices];
+    static OncePerDevice once;
+    const cudaError_t e = once(dev, [&] {
+        const BesideCaptures beside;   // (a first call may be a captured one)
+        cudaMemPoolProps props = {};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        cudaMemPool_t made = nullptr;
+        cudaError_t bad = cudaMemPoolCreate(&made, &props);
+        if (bad != cudaSuccess) return bad;
+        cuuint64_t keep = UINT64_MAX;
+        bad = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (bad != cudaSuccess) (void)cudaMemPoolDestroy(made);
+        else pools[dev] = made;
+        return bad;
+    });
+    return e == cudaSuccess ? cudaMallocFromPoolAsync(p, bytes, pools[dev], stream) : e;
+}
+
+// Clusters of each size that a device holds at once.
+static cudaError_t room_of(int dev, const int (**room)[kMaxCluster + 1])
+{
+    static int n[kDevices][kMaxCluster + 1];
+    static OncePerDevice once;
+    *room = &n[dev];
+    return once(dev, [&] { return clusters_at_once(n[dev]); });
 }
 
 bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
@@ -333,8 +324,9 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     p.wait_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 2000000000ull;
     p.stall = (a->flags & Q4K_FLAG_TEST_STALL) != 0;
     p.pdl = (a->flags & Q4K_FLAG_PDL) != 0;
-    p.error = error_word();
-    if (!p.error) return Q4K_ERR_CUDA;
+    if (cudaGetDevice(&l.device) != cudaSuccess || l.device < 0 || l.device >= attn::kDevices ||
+        error_word(l.device, &p.error) != cudaSuccess)
+        return Q4K_ERR_CUDA;
     l.sms = sms;
     l.stream = static_cast<cudaStream_t>(stream);
     l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
@@ -348,16 +340,15 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     l.boxes = boxes && p.capacity > 0;
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
                          (c->tokens == 1 || stride_ok(a->q_token_stride)) && (a->q_heads == 1 || stride_ok(a->q_head_stride));
-    static int room[attn::kMaxCluster + 1];
-    static cudaError_t e_room = attn::clusters_at_once(room);
-    if (e_room != cudaSuccess) return Q4K_ERR_CUDA;
+    const int (*room)[attn::kMaxCluster + 1];
+    if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
     const int parts = !l.parts_many ? 1 : c->type == Q4K_F16 ? 2 : 3;
-    l.choice = attn::choose(p, room, sms, parts, !l.parts_many && c->dim <= 128 && l.boxes && queries,
+    l.choice = attn::choose(p, *room, sms, parts, !l.parts_many && c->dim <= 128 && l.boxes && queries,
                             static_cast<int>(a->flags >> 8 & 7));
     if (!l.choice.chunk && !l.choice.rows) return Q4K_ERR_INVALID_ARG;
     cudaError_t e;
     if (l.choice.chunk) {
-        const attn::ChunkLaunch ch{p, sms, l.stream};
+        const attn::ChunkLaunch ch{p, l.device, sms, l.stream};
         e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {
         e = c->type == Q4K_F16 ? attn::launch_rows_f16(l) : attn::launch_rows_bf16(l);

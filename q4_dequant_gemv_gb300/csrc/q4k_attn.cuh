@@ -19,7 +19,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/q4k.h"
 
@@ -377,19 +379,38 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// Host: what a device needs once (a kernel's limits, a pool): `make` runs under a
+// lock until it has succeeded.  A failure goes to its caller; the next call tries again.
+constexpr int kDevices = 64;
+struct OncePerDevice {
+    std::atomic<uint64_t> made{0};
+    std::mutex lock;
+
+    template <class Make>
+    cudaError_t operator()(int dev, Make make)
+    {
+        if (made.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+        const std::lock_guard<std::mutex> hold(lock);
+        if (made.load(std::memory_order_relaxed) >> dev & 1) return cudaSuccess;
+        const cudaError_t e = make();
+        if (e == cudaSuccess) made.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+        return e;
+    }
+};
+
 // Host: scratch of `grid` CTAs, the first kernel by `launch(args)`, the join of the
 // tiles that it left split; R rows and `width` columns a slot.
 constexpr int kJoinThreads = 256, kJoinRows = 32;   // of a CTA of the join at most
 constexpr int kMaxParts = 184;   // CTAs of a split call at most (the join's statistics: 47 KB)
-cudaError_t take_scratch(void **p, size_t bytes, cudaStream_t stream);   // freed with cudaFreeAsync
+cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream);   // freed with cudaFreeAsync
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
 
 template <class Launch>
-cudaError_t launch_split(Args &a, int grid, int R, int width, float shift, cudaStream_t stream, Launch launch)
+cudaError_t launch_split(Args &a, int dev, int grid, int R, int width, float shift, cudaStream_t stream, Launch launch)
 {
     const size_t head = (grid * sizeof(Joint) + 255) / 256 * 256;
     void *scratch = nullptr;
-    cudaError_t e = take_scratch(&scratch, head + static_cast<size_t>(grid) * 2 * R * (width + 2) * sizeof(float), stream);
+    cudaError_t e = take_scratch(dev, &scratch, head + static_cast<size_t>(grid) * 2 * R * (width + 2) * sizeof(float), stream);
     if (e != cudaSuccess) return e;
     a.joint = static_cast<Joint *>(scratch);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + head);

@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
 struct ChunkLaunch {
     Args args;
-    int sms;
+    int device, sms;
     cudaStream_t stream;
 };
 cudaError_t launch_chunk_f16(const ChunkLaunch &l);

@@ -27,9 +27,11 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
     const int grid = static_cast<int>(std::min<int64_t>({most, l.sms, kMaxParts}));
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static OncePerDevice once;
+    const cudaError_t attr =
+        once(l.device, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
     if (attr != cudaSuccess) return attr;
-    return launch_split(a, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
+    return launch_split(a, l.device, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
         cfg.blockDim = kChunkThreads;

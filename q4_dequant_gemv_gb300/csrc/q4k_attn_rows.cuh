@@ -704,7 +704,7 @@ struct Choice {
 struct RowsLaunch {
     Args args;
     Choice choice;
-    int sms, parts_many;   // parts_many: fp32 queries or outputs, or a 16-bit type that is not the cache's
+    int device, sms, parts_many;   // parts_many: fp32 queries or outputs, or a 16-bit type that is not the cache's
     bool boxes;            // pages and strides that TMA boxes of 16 slots can take
     cudaStream_t stream;
 };

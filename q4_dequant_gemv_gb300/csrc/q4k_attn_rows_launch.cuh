@@ -22,7 +22,9 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     if (TMA && !encode_cache(&maps, a, CT, kBlock)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
     const int64_t units = (static_cast<int64_t>(a.capacity) + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static OncePerDevice once;
+    const cudaError_t attr =
+        once(l.device, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
     if (attr != cudaSuccess) return attr;
 
     // A cluster per tile and cache head joins through its shared memory: one
@@ -42,7 +44,7 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
     const int grid = static_cast<int>(std::min<int64_t>({most, l.sms, kMaxParts}));
     cfg.gridDim = static_cast<unsigned>(grid);
     const Attributes at(&cfg, 0, a.pdl);
-    return launch_split(a, grid, R, DP, rows_shift<CT>(), l.stream,
+    return launch_split(a, l.device, grid, R, DP, rows_shift<CT>(), l.stream,
                         [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
 }
 

@@ -1,0 +1,57 @@
+"""Host side of the attention call over a runtime that runs nothing: several devices, calls that fail."""
+import pytest
+
+from fake_runtime import fake, fake_path   # noqa: F401
+from test_attention_abi import _attention, _cache
+
+FORMS = {"cluster8": 1, "cluster16": 2, "cluster32": 3, "split8": 4, "split16": 5, "split32": 6, "many": 7}
+
+
+def _call(lib, form=0, cache=None, **kw):
+    return lib.L.q4k_paged_attention(_cache(**(cache or {})), _attention(flags=form << 8, **kw), 0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_every_device_gets_what_it_needs(fake, form):   # noqa: F811
+    """A kernel's shared memory limit, the scratch pool and the error word belong to a device."""
+    for d in (0, 1, 0, 3, 1):
+        fake.device(d)
+        assert _call(fake, FORMS[form]) == 0, f"device {d}"
+        assert all(x.device == d for x in fake.launches())
+        assert fake.blocks(d) == 0
+
+
+def test_clusters_that_fit_are_a_devices_own(fake):   # noqa: F811
+    """A device that holds no cluster takes the split, one that does goes on taking clusters."""
+    fake.clusters(1, 0)
+    for d in (0, 1, 0):
+        fake.device(d)
+        assert _call(fake) == 0
+        kernels = fake.launches()
+        if d == 1:
+            assert len(kernels) == 2 and kernels[0].cluster == 0 and b"join" in kernels[1].kernel
+        else:
+            assert len(kernels) == 1 and kernels[0].cluster >= 1
+
+
+@pytest.mark.parametrize("form", ["cluster8", "split8", "many"])
+@pytest.mark.parametrize("name", ["cudaFuncSetAttribute", "cudaOccupancyMaxActiveClusters", "cudaMemPoolCreate",
+                                  "cudaMemPoolSetAttribute", "cudaMallocFromPoolAsync", "cudaGetSymbolAddress",
+                                  "cudaLaunchKernelExC"])
+def test_a_failure_is_not_kept(fake, form, name):   # noqa: F811
+    """The call that meets it says so and leaves nothing behind; the next one works."""
+    fake.fail(name)
+    pool = "MemPool" in name or "FromPool" in name
+    assert _call(fake, FORMS[form]) == (0 if pool and form == "cluster8" else 4)
+    assert fake.blocks(0) == 0
+    fake.fail(name, 0)
+    fake.launches()
+    assert _call(fake, FORMS[form]) == 0
+    assert fake.launches() and fake.blocks(0) == 0
+
+
+@pytest.mark.parametrize("form", ["split8", "many"])
+def test_a_join_that_fails_gives_its_scratch_back(fake, form):   # noqa: F811
+    fake.fail("cudaLaunchKernelExC", skip=1)
+    assert _call(fake, FORMS[form]) == 4
+    assert len(fake.launches()) == 1 and fake.blocks(0) == 0
