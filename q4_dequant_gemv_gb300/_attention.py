@@ -18,6 +18,16 @@ _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: to
 _calls = None
 
 
+def _new_on(stream, shape, dtype, device):
+    """A new tensor that a given stream writes: from that stream's own blocks.  One that the current stream has freed may
+    still be read there, and nothing orders the two.  The current stream, which may go on with the tensor, is recorded."""
+    now = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(now)
+    return t
+
+
 def _raise(fn, status):
     from . import _check
     _check(fn, status)
@@ -33,7 +43,7 @@ def _load():
     except ImportError as e:
         raise RuntimeError("the _marshal module is not built; run __graft_entry__.build()") from e
     _marshal.setup(torch.Tensor, torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.empty, torch.empty_like,
-                   _current, _raise, *(ctypes.cast(f, ctypes.c_void_p).value for f in
+                   _new_on, _current, _raise, *(ctypes.cast(f, ctypes.c_void_p).value for f in
                                        (L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention)))
     _calls = _marshal
     return _marshal
@@ -56,13 +66,12 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, *, scaling=None, fact
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
-        table = torch.empty((rows, rot), dtype=torch.float32, device=device)
+        table = (torch.empty((rows, rot), dtype=torch.float32, device=device) if stream is None
+                 else _new_on(stream, (rows, rot), torch.float32, device))
         from . import _check, lib
         args = _SCALE.pack(base, factor, orig_len, low, high, magnitude, _SCALING[scaling], 0)
         on = _current(table.get_device()) if stream is None else stream.cuda_stream
         _check("q4k_rope_table", lib().q4k_rope_table(table.data_ptr(), rows, rot, args, on))
-        if stream is not None:
-            table.record_stream(stream)
     return table
 
 

@@ -18,12 +18,12 @@ typedef q4k_status (*rope_fn)(const q4k_rope_args *, void *);
 typedef q4k_status (*append_fn)(const q4k_paged_cache *, const q4k_append_args *, void *);
 typedef q4k_status (*attention_fn)(const q4k_paged_cache *, const q4k_attention_args *, void *);
 
-static PyObject *g_tensor, *g_dtype[3], *g_int32, *g_empty, *g_empty_like, *g_stream_of, *g_raise;
+static PyObject *g_tensor, *g_dtype[3], *g_int32, *g_empty, *g_empty_like, *g_new_on, *g_stream_of, *g_raise;
 static rope_fn g_rope;
 static append_fn g_append;
 static attention_fn g_attention;
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_device,
-    *s_cuda_stream, *s_record_stream, *k_dtype_device;
+    *s_cuda_stream, *k_dtype_device;
 
 /* ---- attributes */
 
@@ -274,7 +274,7 @@ static int stream_of(PyObject *stream, PyObject *t, void **s)
 }
 
 /* `out` checked against the wanted rows and dtype (None: any), or a new tensor like x of that dtype (None: x's)
- * that the call's stream may use.  A new reference, NULL on an error. */
+ * of the call's stream (the current one, or `stream`).  A new reference, NULL on an error. */
 static PyObject *output(PyObject *out, const char *name, PyObject *x, const Rows *like, PyObject *dtype, PyObject *stream, Rows *r)
 {
     if (out != Py_None) {
@@ -292,27 +292,24 @@ static PyObject *output(PyObject *out, const char *name, PyObject *x, const Rows
         return NULL;
     }
     PyObject *t = NULL;
-    if (code == like->code && like->sh == like->d && like->st == like->h * like->d) {
+    if (stream == Py_None && code == like->code && like->sh == like->d && like->st == like->h * like->d) {
         t = PyObject_CallOneArg(g_empty_like, x);
     } else {
         PyObject *device = PyObject_GetAttr(x, s_device);
         PyObject *shape = Py_BuildValue("(LLL)", (long long)like->n, (long long)like->h, (long long)like->d);
         if (device && shape) {
-            PyObject *args[3] = {shape, g_dtype[code], device};
-            t = PyObject_Vectorcall(g_empty, args, 1, k_dtype_device);
+            if (stream == Py_None) {
+                PyObject *args[3] = {shape, g_dtype[code], device};
+                t = PyObject_Vectorcall(g_empty, args, 1, k_dtype_device);
+            } else {
+                PyObject *args[4] = {stream, shape, g_dtype[code], device};
+                t = PyObject_Vectorcall(g_new_on, args, 4, NULL);
+            }
         }
         Py_XDECREF(shape);
         Py_XDECREF(device);
     }
     if (!t) return NULL;
-    if (stream != Py_None) {
-        PyObject *v = PyObject_CallMethodOneArg(t, s_record_stream, stream);
-        if (!v) {
-            Py_DECREF(t);
-            return NULL;
-        }
-        Py_DECREF(v);
-    }
     r->n = like->n, r->h = like->h, r->d = like->d, r->sh = like->d, r->st = like->h * like->d, r->code = code;
     if (!address_of(t, &r->p)) {
         Py_DECREF(t);
@@ -465,21 +462,22 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     Py_END_ALLOW_THREADS return result("q4k_paged_attention", st, out);
 }
 
-/* Tensor, float32, float16, bfloat16, int32, empty, empty_like, current stream's handle of a device, raise(fn, status),
+/* Tensor, float32, float16, bfloat16, int32, empty, empty_like, new_on(stream, shape, dtype, device), current stream's handle of a device, raise(fn, status),
  * and the addresses of q4k_rope, q4k_kv_append, q4k_paged_attention. */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
-    PyObject *o[9];
+    PyObject *o[10];
     unsigned long long f[3];
-    if (!PyArg_ParseTuple(args, "OOOOOOOOOKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &f[0], &f[1], &f[2]))
+    if (!PyArg_ParseTuple(args, "OOOOOOOOOOKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &o[9], &f[0],
+                          &f[1], &f[2]))
         return NULL;
     if (!PyType_Check(o[0])) {
         PyErr_SetString(PyExc_TypeError, "the Tensor class is wanted first");
         return NULL;
     }
-    for (int i = 0; i < 9; ++i) Py_INCREF(o[i]);   /* kept */
+    for (int i = 0; i < 10; ++i) Py_INCREF(o[i]);   /* kept */
     g_tensor = o[0], g_dtype[Q4K_F32] = o[1], g_dtype[Q4K_F16] = o[2], g_dtype[Q4K_BF16] = o[3], g_int32 = o[4];
-    g_empty = o[5], g_empty_like = o[6], g_stream_of = o[7], g_raise = o[8];
+    g_empty = o[5], g_empty_like = o[6], g_new_on = o[7], g_stream_of = o[8], g_raise = o[9];
     g_rope = (rope_fn)(uintptr_t)f[0], g_append = (append_fn)(uintptr_t)f[1], g_attention = (attention_fn)(uintptr_t)f[2];
     Py_RETURN_NONE;
 }
@@ -501,7 +499,7 @@ PyMODINIT_FUNC PyInit__marshal(void)
         const char *text;
     } names[] = {{&s_dtype, "dtype"}, {&s_is_cuda, "is_cuda"}, {&s_shape, "shape"}, {&s_stride, "stride"},
                  {&s_data_ptr, "data_ptr"}, {&s_is_contiguous, "is_contiguous"}, {&s_get_device, "get_device"},
-                 {&s_device, "device"}, {&s_cuda_stream, "cuda_stream"}, {&s_record_stream, "record_stream"}};
+                 {&s_device, "device"}, {&s_cuda_stream, "cuda_stream"}};
     for (size_t i = 0; i < sizeof names / sizeof *names; ++i)
         if (!(*names[i].to = PyUnicode_InternFromString(names[i].text))) return NULL;
     k_dtype_device = PyTuple_Pack(2, s_dtype, s_device);
