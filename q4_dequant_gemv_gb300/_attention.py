@@ -15,6 +15,8 @@ _SCALE = struct.Struct("@6d 2i")      # q4k_rope_scaling
 
 # The handle of a device's current stream, without building a Stream object around it (3 us a call).
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+# The current device, likewise.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _calls = None
 
 
@@ -43,7 +45,7 @@ def _load():
     except ImportError as e:
         raise RuntimeError("the _marshal module is not built; run __graft_entry__.build()") from e
     _marshal.setup(torch.Tensor, torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.empty, torch.empty_like,
-                   _new_on, _current, _raise, *(ctypes.cast(f, ctypes.c_void_p).value for f in
+                   _new_on, _device, _current, _raise, *(ctypes.cast(f, ctypes.c_void_p).value for f in
                                        (L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention)))
     _calls = _marshal
     return _marshal

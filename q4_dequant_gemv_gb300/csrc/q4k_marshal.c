@@ -18,11 +18,11 @@ typedef q4k_status (*rope_fn)(const q4k_rope_args *, void *);
 typedef q4k_status (*append_fn)(const q4k_paged_cache *, const q4k_append_args *, void *);
 typedef q4k_status (*attention_fn)(const q4k_paged_cache *, const q4k_attention_args *, void *);
 
-static PyObject *g_tensor, *g_dtype[3], *g_int32, *g_empty, *g_empty_like, *g_new_on, *g_stream_of, *g_raise;
+static PyObject *g_tensor, *g_dtype[3], *g_int32, *g_empty, *g_empty_like, *g_new_on, *g_device, *g_stream_of, *g_raise;
 static rope_fn g_rope;
 static append_fn g_append;
 static attention_fn g_attention;
-static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_device,
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_device,
     *s_cuda_stream, *k_dtype_device;
 
 /* ---- attributes */
@@ -49,14 +49,24 @@ static PyObject *dtype_of(PyObject *t) /* borrowed: dtypes live as long as torch
     return d;
 }
 
-static int on_gpu(PyObject *t, const char *name)
+/* Whether t is on the GPU *dev (-1: the first tensor of a call, which says). */
+static int on_gpu(PyObject *t, const char *name, int *dev)
 {
-    PyObject *v = PyObject_GetAttr(t, s_is_cuda);
+    PyObject *v = PyObject_CallMethodNoArgs(t, s_get_device);
     if (!v) return 0;
-    const int yes = v == Py_True;
+    const long d = PyLong_AsLong(v);
     Py_DECREF(v);
-    if (!yes) PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
-    return yes;
+    if (d == -1 && PyErr_Occurred()) return 0;
+    if (d < 0) {
+        PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
+        return 0;
+    }
+    if (*dev >= 0 && d != *dev) {
+        PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the tensors before it on cuda:%d", name, d, *dev);
+        return 0;
+    }
+    *dev = (int)d;
+    return 1;
 }
 
 static int contiguous(PyObject *t)
@@ -115,7 +125,7 @@ typedef struct {
 } Rows;
 
 /* A [tokens, heads, dim] tensor; heads, dim, tokens >= 0 are what it must have. */
-static int rows(PyObject *t, const char *name, int64_t tokens, int64_t heads, int64_t dim, Rows *r)
+static int rows(PyObject *t, const char *name, int64_t tokens, int64_t heads, int64_t dim, int *dev, Rows *r)
 {
     int64_t v[3];
     if (!is_tensor(t, name)) return 0;
@@ -125,7 +135,7 @@ static int rows(PyObject *t, const char *name, int64_t tokens, int64_t heads, in
         PyErr_Format(PyExc_TypeError, "%s must be float32, float16 or bfloat16, got %S", name, dtype);
         return 0;
     }
-    if (!on_gpu(t, name)) return 0;
+    if (!on_gpu(t, name, dev)) return 0;
     if (shape_of(t, v, 3) != 3 || (tokens >= 0 && v[0] != tokens) || (heads >= 0 && v[1] != heads) || (dim >= 0 && v[2] != dim)) {
         char want[96];
         if (tokens < 0 && heads < 0 && dim < 0) snprintf(want, sizeof want, "[tokens, heads, dim]");
@@ -144,7 +154,7 @@ static int rows(PyObject *t, const char *name, int64_t tokens, int64_t heads, in
 }
 
 /* A contiguous device array of n values of a dtype. */
-static int array(PyObject *t, const char *name, PyObject *want, int64_t n, void **p)
+static int array(PyObject *t, const char *name, PyObject *want, int64_t n, int *dev, void **p)
 {
     int64_t v[1];
     if (!is_tensor(t, name)) return 0;
@@ -154,7 +164,7 @@ static int array(PyObject *t, const char *name, PyObject *want, int64_t n, void 
         PyErr_Format(PyExc_TypeError, "%s must have dtype %S, got %S", name, want, dtype);
         return 0;
     }
-    if (!on_gpu(t, name)) return 0;
+    if (!on_gpu(t, name, dev)) return 0;
     if (shape_of(t, v, 1) != 1 || v[0] != n || contiguous(t) != 1) {
         char text[64];
         snprintf(text, sizeof text, "a contiguous array of %lld", (long long)n);
@@ -164,14 +174,14 @@ static int array(PyObject *t, const char *name, PyObject *want, int64_t n, void 
     return address_of(t, p);
 }
 
-static int array_or_none(PyObject *t, const char *name, PyObject *want, int64_t n, void **p)
+static int array_or_none(PyObject *t, const char *name, PyObject *want, int64_t n, int *dev, void **p)
 {
     *p = NULL;
-    return t == Py_None || array(t, name, want, n, p);
+    return t == Py_None || array(t, name, want, n, dev, p);
 }
 
 /* A rotary table or None. */
-static int turn(PyObject *t, int64_t dim, const float **p, int64_t *n, int64_t *rot)
+static int turn(PyObject *t, int64_t dim, int *dev, const float **p, int64_t *n, int64_t *rot)
 {
     int64_t v[2];
     *p = NULL, *n = 0, *rot = 0;
@@ -183,7 +193,7 @@ static int turn(PyObject *t, int64_t dim, const float **p, int64_t *n, int64_t *
         PyErr_Format(PyExc_TypeError, "table must have dtype %S, got %S", g_dtype[Q4K_F32], dtype);
         return 0;
     }
-    if (!on_gpu(t, "table")) return 0;
+    if (!on_gpu(t, "table", dev)) return 0;
     if (shape_of(t, v, 2) != 2 || contiguous(t) != 1) {
         bad_shape(t, "table", "a contiguous [positions, rot] tensor");
         return 0;
@@ -199,7 +209,7 @@ static int turn(PyObject *t, int64_t dim, const float **p, int64_t *n, int64_t *
 }
 
 /* k_cache, v_cache, page_table, seq_start, kv_len. */
-static int cache(PyObject *const *t, int64_t tokens, q4k_paged_cache *c)
+static int cache(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache *c)
 {
     int64_t v[4], w[4];
     static const char *names[2] = {"k_cache", "v_cache"};
@@ -214,7 +224,7 @@ static int cache(PyObject *const *t, int64_t tokens, q4k_paged_cache *c)
             PyErr_Format(PyExc_TypeError, "%s must be bfloat16 or float16, both caches the same, got %S", names[i], dtype);
             return 0;
         }
-        if (!on_gpu(t[i], names[i])) return 0;
+        if (!on_gpu(t[i], names[i], dev)) return 0;
     }
     if (shape_of(t[0], v, 4) != 4) {
         bad_shape(t[0], "k_cache", "[pages, page size, heads, dim]");
@@ -239,7 +249,7 @@ static int cache(PyObject *const *t, int64_t tokens, q4k_paged_cache *c)
         PyErr_Format(PyExc_TypeError, "page_table must have dtype %S, got %S", g_int32, dtype);
         return 0;
     }
-    if (!on_gpu(t[2], "page_table")) return 0;
+    if (!on_gpu(t[2], "page_table", dev)) return 0;
     if (shape_of(t[2], v, 2) != 2) {
         bad_shape(t[2], "page_table", "[sequences, pages]");
         return 0;
@@ -251,21 +261,30 @@ static int cache(PyObject *const *t, int64_t tokens, q4k_paged_cache *c)
     }
     c->batch = v[0], c->max_pages = v[1], c->page_table_stride = w[0], c->tokens = tokens;
     return address_of(t[0], &c->k) && address_of(t[1], &c->v) && address_of(t[2], (void **)&c->page_table) &&
-           array(t[3], "seq_start", g_int32, c->batch + 1, (void **)&c->seq_start) &&
-           array(t[4], "kv_len", g_int32, c->batch, (void **)&c->kv_len);
+           array(t[3], "seq_start", g_int32, c->batch + 1, dev, (void **)&c->seq_start) &&
+           array(t[4], "kv_len", g_int32, c->batch, dev, (void **)&c->kv_len);
 }
 
-/* The handle of the call's stream: the given one's, or the current one of t's device. */
-static int stream_of(PyObject *stream, PyObject *t, void **s)
+/* The handle of the call's stream: the given one's, or the current one of the tensors' device, which has to be
+ * the current device (the library launches there). */
+static int stream_of(PyObject *stream, int dev, void **s)
 {
-    PyObject *v = NULL;
+    PyObject *v = PyObject_CallNoArgs(g_device);
+    if (!v) return 0;
+    const long now = PyLong_AsLong(v);
+    Py_DECREF(v);
+    if (now == -1 && PyErr_Occurred()) return 0;
+    if (now != dev) {
+        PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%d, the current device is cuda:%ld", dev, now);
+        return 0;
+    }
     if (stream != Py_None) {
         v = PyObject_GetAttr(stream, s_cuda_stream);
     } else {
-        PyObject *dev = PyObject_CallMethodNoArgs(t, s_get_device);
-        if (!dev) return 0;
-        v = PyObject_CallOneArg(g_stream_of, dev);
-        Py_DECREF(dev);
+        PyObject *index = PyLong_FromLong(dev);
+        if (!index) return 0;
+        v = PyObject_CallOneArg(g_stream_of, index);
+        Py_DECREF(index);
     }
     if (!v) return 0;
     *s = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(v);
@@ -275,10 +294,11 @@ static int stream_of(PyObject *stream, PyObject *t, void **s)
 
 /* `out` checked against the wanted rows and dtype (None: any), or a new tensor like x of that dtype (None: x's)
  * of the call's stream (the current one, or `stream`).  A new reference, NULL on an error. */
-static PyObject *output(PyObject *out, const char *name, PyObject *x, const Rows *like, PyObject *dtype, PyObject *stream, Rows *r)
+static PyObject *output(PyObject *out, const char *name, PyObject *x, const Rows *like, PyObject *dtype, PyObject *stream, int *dev,
+                        Rows *r)
 {
     if (out != Py_None) {
-        if (!rows(out, name, like->n, like->h, like->d, r)) return NULL;
+        if (!rows(out, name, like->n, like->h, like->d, dev, r)) return NULL;
         if (dtype != Py_None && dtype_of(out) != dtype) {
             PyErr_Format(PyExc_TypeError, "%s must have dtype %S, got %S", name, dtype, dtype_of(out));
             return NULL;
@@ -344,16 +364,17 @@ static PyObject *rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     Rows x, y;
     q4k_rope_args r;
     void *stream;
+    int dev = -1;
     memset(&r, 0, sizeof r);
-    if (!wants(n, 8) || !rows(a[0], "x", -1, -1, -1, &x) || !turn(a[2], x.d, &r.table, &r.table_rows, &r.rot)) return NULL;
+    if (!wants(n, 8) || !rows(a[0], "x", -1, -1, -1, &dev, &x) || !turn(a[2], x.d, &dev, &r.table, &r.table_rows, &r.rot)) return NULL;
     if (r.rot && a[1] == Py_None) {
         PyErr_SetString(PyExc_ValueError, "pos is needed with a table");
         return NULL;
     }
-    if (!array_or_none(a[1], "pos", g_int32, x.n, (void **)&r.pos) || !stream_of(a[6], a[0], &stream)) return NULL;
+    if (!array_or_none(a[1], "pos", g_int32, x.n, &dev, (void **)&r.pos) || !stream_of(a[6], dev, &stream)) return NULL;
     const int inter = PyObject_IsTrue(a[4]), pdl = PyObject_IsTrue(a[7]);
     if (inter < 0 || pdl < 0) return NULL;
-    PyObject *out = output(a[3], "y", a[0], &x, a[5], a[6], &y);
+    PyObject *out = output(a[3], "y", a[0], &x, a[5], a[6], &dev, &y);
     if (!out) return NULL;
     r.x = x.p, r.y = y.p;
     r.tokens = x.n, r.heads = x.h, r.dim = x.d;
@@ -371,27 +392,28 @@ static PyObject *kv_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
     q4k_paged_cache c;
     q4k_append_args r;
     void *stream;
+    int dev = -1;
     memset(&r, 0, sizeof r);
-    if (!wants(n, 15) || !rows(a[0], "k", -1, -1, -1, &k) || !rows(a[1], "v", k.n, k.h, k.d, &v)) return NULL;
+    if (!wants(n, 15) || !rows(a[0], "k", -1, -1, -1, &dev, &k) || !rows(a[1], "v", k.n, k.h, k.d, &dev, &v)) return NULL;
     if (v.code != k.code) {
         PyErr_SetString(PyExc_TypeError, "k and v must have the same dtype");
         return NULL;
     }
-    if (!cache(a + 2, k.n, &c)) return NULL;
+    if (!cache(a + 2, k.n, &dev, &c)) return NULL;
     if (c.heads != k.h || c.dim != k.d) {
         PyErr_Format(PyExc_ValueError, "the cache holds %lld heads of %lld, k and v %lld of %lld", (long long)c.heads,
                      (long long)c.dim, (long long)k.h, (long long)k.d);
         return NULL;
     }
-    if (!turn(a[7], k.d, &r.table, &r.table_rows, &r.rot) || !array_or_none(a[9], "pos", g_int32, k.n, (void **)&r.pos) ||
-        !stream_of(a[13], a[0], &stream))
+    if (!turn(a[7], k.d, &dev, &r.table, &r.table_rows, &r.rot) || !array_or_none(a[9], "pos", g_int32, k.n, &dev, (void **)&r.pos) ||
+        !stream_of(a[13], dev, &stream))
         return NULL;
     const int inter = PyObject_IsTrue(a[8]), pdl = PyObject_IsTrue(a[14]);
     if (inter < 0 || pdl < 0) return NULL;
     PyObject *out = NULL;
     if (a[10] != Py_None) {
-        if (!rows(a[10], "q", k.n, -1, k.d, &q)) return NULL;
-        out = output(a[11], "q_out", a[10], &q, a[12], a[13], &o);
+        if (!rows(a[10], "q", k.n, -1, k.d, &dev, &q)) return NULL;
+        out = output(a[11], "q_out", a[10], &q, a[12], a[13], &dev, &o);
         if (!out) return NULL;
         r.q = q.p, r.q_out = o.p, r.q_heads = q.h;
         r.q_token_stride = q.st, r.q_head_stride = q.sh, r.q_out_token_stride = o.st, r.q_out_head_stride = o.sh;
@@ -420,8 +442,9 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     q4k_paged_cache c;
     q4k_attention_args r;
     void *stream;
+    int dev = -1;
     memset(&r, 0, sizeof r);
-    if (!wants(n, 19) || !rows(a[0], "q", -1, -1, -1, &q) || !cache(a + 1, q.n, &c)) return NULL;
+    if (!wants(n, 19) || !rows(a[0], "q", -1, -1, -1, &dev, &q) || !cache(a + 1, q.n, &dev, &c)) return NULL;
     if (c.dim != q.d || c.heads < 1 || q.h % c.heads) {
         PyErr_Format(PyExc_ValueError, "the cache holds %lld heads of %lld, q %lld of %lld", (long long)c.heads,
                      (long long)c.dim, (long long)q.h, (long long)q.d);
@@ -432,9 +455,9 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     const int causal = PyObject_IsTrue(a[12]);
     r.flags = (uint32_t)PyLong_AsUnsignedLong(a[17]), r.wait_limit_us = (uint32_t)PyLong_AsUnsignedLong(a[18]);
     if (PyErr_Occurred()) return NULL;
-    if (!array_or_none(a[10], "slopes", g_dtype[Q4K_F32], q.h, (void **)&r.slopes) ||
-        !array_or_none(a[13], "prefix_len", g_int32, c.batch, (void **)&r.prefix_len) ||
-        !array_or_none(a[14], "kv_start", g_int32, q.n, (void **)&r.kv_start))
+    if (!array_or_none(a[10], "slopes", g_dtype[Q4K_F32], q.h, &dev, (void **)&r.slopes) ||
+        !array_or_none(a[13], "prefix_len", g_int32, c.batch, &dev, (void **)&r.prefix_len) ||
+        !array_or_none(a[14], "kv_start", g_int32, q.n, &dev, (void **)&r.kv_start))
         return NULL;
     if (a[15] != Py_None) {
         int64_t v[2];
@@ -443,15 +466,15 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
             PyErr_SetString(PyExc_TypeError, "lse must be a float32 tensor");
             return NULL;
         }
-        if (!on_gpu(a[15], "lse")) return NULL;
+        if (!on_gpu(a[15], "lse", &dev)) return NULL;
         if (shape_of(a[15], v, 2) != 2 || v[0] != q.n || v[1] != q.h || contiguous(a[15]) != 1) {
             bad_shape(a[15], "lse", "a contiguous [tokens, q heads] tensor");
             return NULL;
         }
         if (!address_of(a[15], (void **)&r.lse)) return NULL;
     }
-    if (!stream_of(a[16], a[0], &stream)) return NULL;
-    PyObject *out = output(a[6], "out", a[0], &q, a[8], a[16], &o);
+    if (!stream_of(a[16], dev, &stream)) return NULL;
+    PyObject *out = output(a[6], "out", a[0], &q, a[8], a[16], &dev, &o);
     if (!out) return NULL;
     r.q = q.p, r.out = o.p;
     r.q_token_stride = q.st, r.q_head_stride = q.sh, r.out_token_stride = o.st, r.out_head_stride = o.sh;
@@ -462,22 +485,22 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     Py_END_ALLOW_THREADS return result("q4k_paged_attention", st, out);
 }
 
-/* Tensor, float32, float16, bfloat16, int32, empty, empty_like, new_on(stream, shape, dtype, device), current stream's handle of a device, raise(fn, status),
+/* Tensor, float32, float16, bfloat16, int32, empty, empty_like, new_on(stream, shape, dtype, device), current device, current stream's handle of a device, raise(fn, status),
  * and the addresses of q4k_rope, q4k_kv_append, q4k_paged_attention. */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
-    PyObject *o[10];
+    PyObject *o[11];
     unsigned long long f[3];
-    if (!PyArg_ParseTuple(args, "OOOOOOOOOOKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &o[9], &f[0],
+    if (!PyArg_ParseTuple(args, "OOOOOOOOOOOKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &o[9], &o[10], &f[0],
                           &f[1], &f[2]))
         return NULL;
     if (!PyType_Check(o[0])) {
         PyErr_SetString(PyExc_TypeError, "the Tensor class is wanted first");
         return NULL;
     }
-    for (int i = 0; i < 10; ++i) Py_INCREF(o[i]);   /* kept */
+    for (int i = 0; i < 11; ++i) Py_INCREF(o[i]);   /* kept */
     g_tensor = o[0], g_dtype[Q4K_F32] = o[1], g_dtype[Q4K_F16] = o[2], g_dtype[Q4K_BF16] = o[3], g_int32 = o[4];
-    g_empty = o[5], g_empty_like = o[6], g_new_on = o[7], g_stream_of = o[8], g_raise = o[9];
+    g_empty = o[5], g_empty_like = o[6], g_new_on = o[7], g_device = o[8], g_stream_of = o[9], g_raise = o[10];
     g_rope = (rope_fn)(uintptr_t)f[0], g_append = (append_fn)(uintptr_t)f[1], g_attention = (attention_fn)(uintptr_t)f[2];
     Py_RETURN_NONE;
 }
@@ -497,7 +520,7 @@ PyMODINIT_FUNC PyInit__marshal(void)
     struct {
         PyObject **to;
         const char *text;
-    } names[] = {{&s_dtype, "dtype"}, {&s_is_cuda, "is_cuda"}, {&s_shape, "shape"}, {&s_stride, "stride"},
+    } names[] = {{&s_dtype, "dtype"}, {&s_shape, "shape"}, {&s_stride, "stride"},
                  {&s_data_ptr, "data_ptr"}, {&s_is_contiguous, "is_contiguous"}, {&s_get_device, "get_device"},
                  {&s_device, "device"}, {&s_cuda_stream, "cuda_stream"}};
     for (size_t i = 0; i < sizeof names / sizeof *names; ++i)

@@ -19,8 +19,9 @@ class Tensor:
     """What the calls read of a CUDA tensor."""
 
     def __init__(self, shape, dtype=F32, device=0, stream=None, strides=None):
-        self.shape, self.dtype, self.device = tuple(shape), dtype, torch.device("cuda", device)
-        self.is_cuda, self.recorded, self.allocated_on = True, [], stream
+        self.shape, self.dtype = tuple(shape), dtype
+        self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
+        self.is_cuda, self.recorded, self.allocated_on = device >= 0, [], stream
         self._strides = strides
 
     def stride(self):
@@ -39,7 +40,7 @@ class Tensor:
         return self._strides is None
 
     def get_device(self):
-        return self.device.index
+        return self.device.index if self.is_cuda else -1
 
     def record_stream(self, stream):
         self.recorded.append(stream)
@@ -84,7 +85,7 @@ class World:
             Tensor=Tensor, float32=F32, float16=torch.float16, bfloat16=BF16, int32=I32, empty=empty, empty_like=empty_like,
             cuda=cuda, device=torch.device))
         monkeypatch.setattr(_attention, "_current", lambda d: self.now.cuda_stream)
-        monkeypatch.setattr(_attention, "_device", lambda: self.device, raising=False)
+        monkeypatch.setattr(_attention, "_device", lambda: self.device)
         _attention._calls = None
         proto = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
         proto3 = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
@@ -154,3 +155,58 @@ def test_outputs_of_the_current_stream(world):
             y = f()
             assert y.allocated_on is now and not y.recorded, name
             assert [c[1] for c in world.calls] == [now.cuda_stream], name
+
+
+def _swaps(world):
+    """(argument, call with that argument on another device) of every tensor argument."""
+    x, k = (lambda d=0: Tensor((4, 2, 64), device=d)), (lambda d=0: Tensor((4, 2, 64), device=d))
+    yield "pos", lambda: world.rope(pos=Tensor((4,), I32, 1))
+    yield "table", lambda: world.rope(table=Tensor((8, 64), device=1))
+    yield "y", lambda: world.rope(y=x(1))
+    cache, index = world.cache(), world.index()
+    base = [k(), k(), *cache, *index]
+    names = ["k", "v", "k_cache", "v_cache", "page_table", "seq_start", "kv_len"]
+    other = [k(1), k(1), *world.cache(1), *world.index(1)]
+    for i in range(1, 7):
+        yield "append " + names[i], lambda i=i: world.append(*base[:i], other[i], *base[i + 1:])
+    yield "append pos", lambda: world.append(*base, table=Tensor((8, 64)), pos=Tensor((4,), I32, 1))
+    yield "append table", lambda: world.append(*base, table=Tensor((8, 64), device=1))
+    yield "append q", lambda: world.append(*base, q=x(1))
+    yield "append q_out", lambda: world.append(*base, q=x(), q_out=x(1))
+    base, other = [x(), *cache, *index], [x(1), *world.cache(1), *world.index(1)]
+    names = ["q"] + names[2:]
+    for i in range(1, 6):
+        yield "attention " + names[i], lambda i=i: world.attention(*base[:i], other[i], *base[i + 1:])
+    for name, t in (("out", x(1)), ("slopes", Tensor((2,), device=1)), ("prefix_len", Tensor((1,), I32, 1)),
+                    ("kv_start", Tensor((4,), I32, 1)), ("lse", Tensor((4, 2), device=1))):
+        yield "attention " + name, lambda name=name, t=t: world.attention(*base, **{name: t})
+
+
+def test_tensors_of_several_devices_are_refused(world):
+    """Before anything is launched: one device's kernel would follow another one's addresses."""
+    for name, f in _swaps(world):
+        with pytest.raises(ValueError, match="cuda:1"):
+            f()
+        assert not world.calls, name
+
+
+def test_tensors_of_a_device_that_is_not_current_are_refused(world):
+    """The library launches on the current device."""
+    calls = [lambda: world.rope(Tensor((4, 2, 64), device=1), Tensor((4,), I32, 1), Tensor((8, 64), device=1)),
+             lambda: world.append(Tensor((4, 2, 64), device=1), Tensor((4, 2, 64), device=1), *world.cache(1), *world.index(1)),
+             lambda: world.attention(Tensor((4, 2, 64), device=1), *world.cache(1), *world.index(1))]
+    for f in calls:
+        with pytest.raises(ValueError, match="current device"):
+            f()
+        assert not world.calls
+    world.device = 1
+    for f in calls:
+        f()
+    assert [c[0] for c in world.calls] == ["rope", "append", "attention"]
+
+
+def test_host_tensors_are_refused(world):
+    for f in (lambda: world.rope(pos=torch.zeros(4, dtype=I32)), lambda: world.rope(x=Tensor((4, 2, 64), device=-1))):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+    assert not world.calls
