@@ -351,7 +351,9 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
         const attn::ChunkLaunch ch{p, l.device, sms, l.stream};
         e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {
-        e = c->type == Q4K_F16 ? attn::launch_rows_f16(l) : attn::launch_rows_bf16(l);
+        auto rows = c->type == Q4K_F16 ? (p.docs() ? attn::launch_rows_docs_f16 : attn::launch_rows_f16)
+                                       : (p.docs() ? attn::launch_rows_docs_bf16 : attn::launch_rows_bf16);
+        e = rows(l);
     }
     return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }

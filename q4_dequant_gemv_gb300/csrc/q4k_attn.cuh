@@ -70,6 +70,9 @@ struct Args {
     uint64_t wait_ns;      // bound of each wait
     int stall;             // (tests) the first copy of a CTA is awaited for 16 bytes too many
     bool pdl;              // launched as a programmatic dependent
+
+    // Tiles of the call may have keys that no row sees between some that one sees.
+    __host__ __device__ bool docs() const { return kv_start && causal; }
 };
 
 // A split tile: its rows, and the CTAs c0 .. c1 that hold its parts.  The first of
@@ -81,9 +84,12 @@ struct alignas(32) Joint {
 
 __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * static_cast<int64_t>(cta) + (begins ? 1 : 0); }
 
+constexpr int kHoles = 1 << 30;
+
 // One tile: the rows, their token range and the keys that any of them sees.
 struct Tile {
-    int seq, first, rows;      // first row in the sequence, number of rows (0: nothing to do)
+    int seq;                   // (+ kHoles: between `from` and `hi` there may be keys that no row sees)
+    int first, rows;           // first row in the sequence, number of rows (0: nothing to do)
     int tok0;                  // first token row of the sequence in the call
     int pos0;                  // position of the sequence's first new token
     int len;                   // cached positions (clamped to the page table)
@@ -113,18 +119,47 @@ __device__ __forceinline__ Range token_range(const Args &a, int seq, int pos, in
     return r;
 }
 
+// Bits [lo, hi) of a word, cut to it.
+__device__ __forceinline__ uint32_t span(int lo, int hi)
+{
+    lo = max(lo, 0), hi = min(hi, 32);
+    return hi > lo ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+}
+
+// The 32 WORDS keys from kb on that some row of a tile sees, a bit each; whole warps.
+template <int WORDS>
+__device__ __forceinline__ void seen_keys(const Args &a, const Tile &t, int kb, uint32_t (&seen)[WORDS])
+{
+    const int last = (t.first + t.rows - 1) / a.group;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) seen[w] = 0;
+#pragma unroll 1
+    for (int i = t.first / a.group + static_cast<int>(threadIdx.x & 31); i <= last; i += 32) {
+        const Range r = token_range(a, t.seq, t.pos0 + i, t.tok0 + i, t.len);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) seen[w] |= span(r.lo - kb - 32 * w, r.hi - kb - 32 * w);
+    }
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) seen[w] = __reduce_or_sync(0xffffffffu, seen[w]);
+}
+
 // The split of the call's work, one copy per CTA in shared memory.
-// R (rows of a tile) is given at run time; ALIGN: where units start (a power of two).
-template <int U, int THREADS, int ALIGN>
-struct Split {
+// R (rows of a tile) is given at run time; ALIGN: where units start (a power of two);
+// DOCS: tiles are marked where they may have holes (causal calls with kv_start).
+template <int THREADS>
+struct SplitShared {
     static constexpr int kSeqs = 512;        // sequence starts held in shared memory
-    struct Shared {
-        uint32_t prefix[THREADS];            // units up to the end of each stripe of tile slots
-        int start[kSeqs + 1], len[kSeqs];
-        uint32_t warp[THREADS / 32];
-        Tile first;                          // the tile of `hand_out`
-        int offset;
-    };
+    uint32_t prefix[THREADS];                // units up to the end of each stripe of tile slots
+    int start[kSeqs + 1], len[kSeqs];
+    uint32_t warp[THREADS / 32];
+    Tile first;                              // the tile of `hand_out`
+    int offset;
+};
+
+template <int U, int THREADS, int ALIGN, bool DOCS>
+struct Split {
+    using Shared = SplitShared<THREADS>;
+    static constexpr int kSeqs = Shared::kSeqs;
 
     const Args &a;
     Shared &sh;
@@ -178,12 +213,18 @@ struct Split {
         const Range last = token_range(a, b, t.pos0 + i1, s0 + i1, t.len);
         int lo = last.hi;
         if (WARP && a.kv_start) {
+            bool away = false;   // a token does not see its own position
 #pragma unroll 4
             for (int i = i0 + static_cast<int>(threadIdx.x & 31); i <= i1; i += 32) {
                 const Range r = token_range(a, b, t.pos0 + i, s0 + i, t.len);
                 if (r.hi > r.lo) lo = min(lo, r.lo);
+                if constexpr (DOCS) away |= r.lo > t.pos0 + i;
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
+            // Where every token sees its own position the ranges of consecutive ones meet,
+            // and where the mask is not causal all end together: no holes.
+            if constexpr (DOCS)
+                if (__any_sync(0xffffffffu, away)) t.seq |= kHoles;
         } else {
             lo = min(lo, token_range(a, b, t.pos0 + i0, s0 + i0, t.len).lo);
         }

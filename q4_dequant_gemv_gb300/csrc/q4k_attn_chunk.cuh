@@ -30,8 +30,8 @@
 // the rescaling waits for nothing.
 //
 // Slots that nothing of the tile sees may hold NaN: scores are replaced, not
-// added to, and the rows of V outside the tile's keys are zeroed in shared
-// memory before they meet P = 0.  Every wait is bounded in time: on a timeout the
+// added to, and the rows of V outside the tile's keys, or in a hole that a document
+// mask leaves between them, are zeroed in shared memory before they meet P = 0.  Every wait is bounded in time: on a timeout the
 // CTA sets bit 3 of the error word, stops, waits (bounded) for its copies in
 // flight, frees its tensor memory and returns.
 //
@@ -66,16 +66,16 @@ struct Work {
 
 template <int DP>
 struct ChunkShared {
-    using Plan = Split<kChunkKeys, kChunkThreads, kChunkKeys>;
     static constexpr int kHalf = 128 * 128;                    // bytes: 128 rows of 64 elements
     static constexpr int kTile = kHalf * (DP / 64);            // 128 rows of DP elements
     uint8_t q[2 * kTile];                                      // [dim / 64][256 rows][64]
     uint8_t kv[kStages * kTile];
     uint8_t out[8][32 * 64];                                   // a warp's rows on their way out, 32 columns at a time
-    typename Plan::Shared plan;
+    SplitShared<kChunkThreads> plan;
     unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2][2], o_done[2], q_full, q_empty, edge;
     unsigned long long work_full[2], work_empty[2];
     Work work[2];
+    alignas(16) uint32_t seen[2][kChunkKeys / 32];   // (tiles with holes) of the key and the value warp
     uint32_t tmem;
     int abort;
 };
@@ -256,13 +256,16 @@ constexpr float chunk_shift()
     return CT == Q4K_F16 ? 6.0f : 0.0f;
 }
 
-// MODE bit 0: capped scores, bit 1: distance bias.
+// MODE bit 0: capped scores, bit 1: distance bias, bit 2 (DOCS): a causal call with
+// kv_start, whose tiles may have holes (its code in every instance cost 2048 tokens
+// over 14336 positions 2 %).
 template <int CT, int DP, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ CacheMaps maps, const __grid_constant__ CUtensorMap qmap, const Args a, const int box)
 {
     using Sh = ChunkShared<DP>;
     constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
+    constexpr bool DOCS = MODE & 4;
     constexpr float kShift = chunk_shift<CT>();
     constexpr float kLazy = 8.0f;
     extern __shared__ uint8_t smem_raw[];
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tm_fence_before();
     pdl_launch_dependents();
     pdl_wait();   // (everything below may come from the kernel before)
-    typename Sh::Plan plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
+    Split<kChunkKeys, kChunkThreads, kChunkKeys, DOCS> plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
     plan.scan();
     tm_fence_after();
     const uint32_t tm = sh.tmem;
@@ -383,6 +386,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 __syncwarp();
                 if (item.todo == 0) break;
             }
+            const bool holes = DOCS && (item.t.seq & kHoles);
+            if (DOCS) item.t.seq &= ~kHoles;
             const Tile &t = item.t;
             const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
             if (!values && k == 0) queries(item);
@@ -392,6 +397,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // lane j: piece j of the tile
                 const int key = kb + lane * box;
                 bool live = lane < per && key + box > t.from && key < t.hi;
+                if (holes) {   // the keys that some row sees: no others are looked up, and their values are zeroed below
+                    uint32_t seen[kChunkKeys / 32];
+                    seen_keys(a, t, kb, seen);
+                    if (lane == 0) *reinterpret_cast<uint4 *>(sh.seen[values]) = make_uint4(seen[0], seen[1], seen[2], seen[3]);
+                    __syncwarp();
+                    live = false;
+                    for (int z = 0; z < box && lane < per; z += 16)
+                        live |= (sh.seen[values][(lane * box + z) >> 5] >> ((lane * box + z) & 31) & 0xFFFFu) != 0;
+                    __syncwarp();
+                }
                 int page = 0, slot = 0;
                 if (live) {
                     int e;
@@ -405,7 +420,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * static_cast<uint32_t>(box) * 128u * ND;
                 if (unit > 1 && !(ok = wait(sh.empty[stage], ((unit >> 1) - 1) & 1))) break;
                 uint8_t *dst = sh.kv + stage * kTile;
-                const bool clean = values && (kb < t.from || kb + kChunkKeys > t.hi);
+                const bool clean = values && (kb < t.from || kb + kChunkKeys > t.hi || holes);
                 unsigned long long &bar = clean ? sh.edge : sh.full[stage];
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar), bytes + (a.stall && !values && unit == 0 ? 16 : 0));
                 __syncwarp();
@@ -425,12 +440,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (!(ok = wait(sh.edge, edges & 1))) break;
                     ++edges;
                     const int r0 = max(0, t.from - kb), r1 = min(kChunkKeys, t.hi - kb);
-                    for (int r = 0; r < kChunkKeys; ++r) {
-                        if (r >= r0 && r < r1) continue;
+                    auto zero_row = [&](int r) {
                         if (lane < 8 * ND)
                             *reinterpret_cast<uint4 *>(dst + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
+                    };
+                    for (int r = 0; r < kChunkKeys; ++r) {
+                        if (r >= r0 && r < r1) continue;
+                        zero_row(r);
                     }
+                    if (holes)
+#pragma unroll 1
+                        for (int r = r0; r < r1; ++r)
+                            if (!(sh.seen[1][r >> 5] >> (r & 31) & 1)) zero_row(r);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.full[stage]));
@@ -526,6 +548,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             Work item;
             ok = next_work(k, item);
             if (!ok || item.todo == 0) break;
+            if (DOCS) item.t.seq &= ~kHoles;
             const Tile &t = item.t;
             const int head = item.head, off = item.off, todo = item.todo;
             if (t.rows <= 128 * h) continue;
@@ -585,7 +608,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         for (int z = 0; z < 4; ++z) x[z] = max3(x[z], v[j + 2 * z], v[j + 2 * z + 1]);
                     }
                 }
-                const float mul = MODE ? 1.0f : c;
+                const float mul = (MODE & 3) ? 1.0f : c;
                 const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * mul;
                 float f = 1.0f;
                 if (mx > m + kLazy || m == -INFINITY) {

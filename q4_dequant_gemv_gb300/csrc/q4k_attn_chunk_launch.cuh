@@ -45,9 +45,16 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
 template <int CT, int DP>
 static cudaError_t launch_chunk_mode(const ChunkLaunch &l)
 {
-    const bool cap = l.args.softcap > 0.0f, bias = l.args.slopes != nullptr;
-    if (cap) return bias ? launch_chunk_one<CT, DP, 3>(l) : launch_chunk_one<CT, DP, 1>(l);
-    return bias ? launch_chunk_one<CT, DP, 2>(l) : launch_chunk_one<CT, DP, 0>(l);
+    switch ((l.args.softcap > 0.0f ? 1 : 0) | (l.args.slopes ? 2 : 0) | (l.args.docs() ? 4 : 0)) {
+        case 0: return launch_chunk_one<CT, DP, 0>(l);
+        case 1: return launch_chunk_one<CT, DP, 1>(l);
+        case 2: return launch_chunk_one<CT, DP, 2>(l);
+        case 3: return launch_chunk_one<CT, DP, 3>(l);
+        case 4: return launch_chunk_one<CT, DP, 4>(l);
+        case 5: return launch_chunk_one<CT, DP, 5>(l);
+        case 6: return launch_chunk_one<CT, DP, 6>(l);
+        default: return launch_chunk_one<CT, DP, 7>(l);
+    }
 }
 
 template <int CT>

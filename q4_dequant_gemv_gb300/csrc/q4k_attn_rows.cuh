@@ -157,13 +157,12 @@ template <int CT, int PARTS, int NT, int RG, int DP>
 struct RowsShared {
     using Sp = RowsShape<NT, RG, DP>;
     static constexpr int R = Sp::R;
-    using Plan = Split<Sp::kUnit, Sp::kThreads, kBlock>;
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
     // a group's ring; when the warps join it holds the group's O instead
     static constexpr int kSlotBytes = Sp::kSlots * 2 * Sp::kSide, kOBytes = (R * kRed * 4 + 1023) / 1024 * 1024;
     static constexpr int kRing = kSlotBytes > kOBytes ? kSlotBytes : kOBytes;
     uint8_t ring[Sp::KG][kRing];
-    typename Plan::Shared plan;
+    SplitShared<Sp::kThreads> plan;
     uint4 q[PARTS][R / 8][DP / 32][32];    // B fragments of Q, lane-major
     float m[Sp::KG][R], l[Sp::KG][R];
     float scale[R], slope[R];
@@ -175,8 +174,10 @@ struct RowsShared {
     unsigned long long full[Sp::KG][Sp::kSlots], empty[Sp::KG][Sp::kSlots];
 };
 
-// TMA: slots filled by tensor copies (maps), else by cp.async.
-template <int CT, int PARTS, int NT, int RG, int DP, bool TMA>
+// TMA: slots filled by tensor copies (maps), else by cp.async.  DOCS: causal calls
+// with kv_start, whose tiles may have holes (an instance of its own: the code for
+// them, rarely run, cost calls without them 0.3 to 1 us where it was in one kernel).
+template <int CT, int PARTS, int NT, int RG, int DP, bool TMA, bool DOCS>
 __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
 {
     using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
     if (a.cluster > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
     pdl_launch_dependents();
     pdl_wait();                                    // (everything below may come from the kernel before)
-    typename Sh::Plan plan(a, sh.plan, R);         // synchronises the CTA
+    Split<Sp::kUnit, THREADS, kBlock, DOCS> plan(a, sh.plan, R);         // synchronises the CTA
     const int cta = blockIdx.x;
     int64_t total = 0, u = 0, u_end = 1;
     int n = 0;
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             todo = static_cast<int>(min(static_cast<int64_t>(t.units - off), u_end - u));
         }
 
+        const bool holes = DOCS && (t.seq & kHoles);
+        if (DOCS) t.seq &= ~kHoles;
         // ---- this group's blocks: key kb0 + i * kUnit, i < count
         const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
         const int kb0 = t.lo + off * Sp::kUnit + kBlock * kg;
@@ -264,8 +267,8 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         };
         auto check = [&]() {
             if (ids < 0 || ids >= a.pages) {
-                atomicOr(a.error, 4u);
-                ids = 0;
+                if (!holes) atomicOr(a.error, 4u);
+                ids = holes ? -1 : 0;   // (-1: `fill` looks whether any row sees the block)
             }
         };
         // block i into its slot, by the group's first warp
@@ -274,7 +277,14 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             const uint32_t dst = ring + s * 2 * Sp::kSide, bar = smem_u32(&sh.full[kg][s]);
             if constexpr (TMA) {
                 if (i > 0 && (i & 31) == 0) look(i), check();
-                const int page = __shfl_sync(0xffffffffu, ids, i & 31), slot = __shfl_sync(0xffffffffu, slots, i & 31);
+                int page = __shfl_sync(0xffffffffu, ids, i & 31);
+                const int slot = __shfl_sync(0xffffffffu, slots, i & 31);
+                if (DOCS && page < 0) {
+                    uint32_t some[1];
+                    seen_keys(a, t, kb0 + i * Sp::kUnit, some);
+                    if (lane == 0 && (some[0] & 0xFFFFu)) atomicOr(a.error, 4u);
+                    page = 0;
+                }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, 2 * Sp::kSide + (a.stall && f == 0 ? 16 : 0));
 #pragma unroll
@@ -286,7 +296,12 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
             } else {
                 // lane r < 16 finds row r
                 const int key = kb0 + i * Sp::kUnit + (lane & 15);
-                const bool seen = key >= t.from && key < t.hi;
+                bool seen = key >= t.from && key < t.hi;
+                if (holes) {
+                    uint32_t some[1];
+                    seen_keys(a, t, kb0 + i * Sp::kUnit, some);
+                    seen = some[0] >> (lane & 15) & 1;
+                }
                 int page = 0, slot = 0;
                 if (seen) {
                     int e;
@@ -428,12 +443,21 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 wind_down(i);
                 break;
             }
-            if (TMA && (kb < t.from || kb + kBlock > t.hi)) {
+            auto zero_row = [&](int r) {
+                if (lane < 8 * ND)
+                    *reinterpret_cast<uint4 *>(sh.ring[kg] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf + r * 128 +
+                                               (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            };
+            if (TMA && (kb < t.from || kb + kBlock > t.hi || holes)) {
                 // rows of V that nothing sees: zero (by every warp that reads them)
                 for (int r = 0; r < kBlock; ++r)
-                    if ((kb + r < t.from || kb + r >= t.hi) && lane < 8 * ND)
-                        *reinterpret_cast<uint4 *>(sh.ring[kg] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf +
-                                                   r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    if (kb + r < t.from || kb + r >= t.hi) zero_row(r);
+                if (holes) {
+                    uint32_t some[1];
+                    seen_keys(a, t, kb, some);
+                    for (int r = 0; r < kBlock; ++r)
+                        if (!(some[0] >> r & 1)) zero_row(r);
+                }
                 fence_proxy_async_smem();   // before a later copy into the slot
                 __syncwarp();
             }
@@ -711,6 +735,8 @@ struct RowsLaunch {
 cudaError_t clusters_at_once(int (&n)[kMaxCluster + 1]);
 cudaError_t launch_rows_f16(const RowsLaunch &l);
 cudaError_t launch_rows_bf16(const RowsLaunch &l);
+cudaError_t launch_rows_docs_f16(const RowsLaunch &l);
+cudaError_t launch_rows_docs_bf16(const RowsLaunch &l);
 
 }  // namespace attn
 }  // namespace q4k

@@ -4,6 +4,6 @@
 namespace q4k {
 namespace attn {
 cudaError_t clusters_at_once(int (&n)[kMaxCluster + 1]) { return rows_room<Q4K_BF16>(n); }
-cudaError_t launch_rows_bf16(const RowsLaunch &l) { return launch_rows_type<Q4K_BF16, 3>(l); }
+cudaError_t launch_rows_bf16(const RowsLaunch &l) { return launch_rows_type<Q4K_BF16, 3, false>(l); }
 }  // namespace attn
 }  // namespace q4k

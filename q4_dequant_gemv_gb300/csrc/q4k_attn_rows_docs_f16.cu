@@ -1,0 +1,8 @@
+// q4k_attn_rows_docs_f16.cu -- the few-rows attention kernel over an fp16 cache, causal calls with kv_start.
+#include "q4k_attn_rows_launch.cuh"
+
+namespace q4k {
+namespace attn {
+cudaError_t launch_rows_docs_f16(const RowsLaunch &l) { return launch_rows_type<Q4K_F16, 2, true>(l); }
+}  // namespace attn
+}  // namespace q4k

@@ -3,6 +3,6 @@
 
 namespace q4k {
 namespace attn {
-cudaError_t launch_rows_f16(const RowsLaunch &l) { return launch_rows_type<Q4K_F16, 2>(l); }
+cudaError_t launch_rows_f16(const RowsLaunch &l) { return launch_rows_type<Q4K_F16, 2, false>(l); }
 }  // namespace attn
 }  // namespace q4k

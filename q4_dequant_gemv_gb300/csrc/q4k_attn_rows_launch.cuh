@@ -8,12 +8,12 @@
 namespace q4k {
 namespace attn {
 
-template <int CT, int PARTS, int NT, int RG, int DP, bool TMA>
+template <int CT, int PARTS, int NT, int RG, int DP, bool TMA, bool DOCS>
 static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
     using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
     using Sp = RowsShape<NT, RG, DP>;
-    auto kern = rows_kernel<CT, PARTS, NT, RG, DP, TMA>;
+    auto kern = rows_kernel<CT, PARTS, NT, RG, DP, TMA, DOCS>;
     Args a = l.args;
     constexpr int R = Sh::R;
     constexpr int kSmem = static_cast<int>(sizeof(Sh)) + 1024;   // room to align the rings to 1024 bytes
@@ -48,19 +48,20 @@ static cudaError_t launch_rows_fill(const RowsLaunch &l)
                         [&](const Args &args) { return cudaLaunchKernelEx(&cfg, kern, maps, args); });
 }
 
-template <int CT, int PARTS, int NT, int RG, int DP>
+template <int CT, int PARTS, int NT, int RG, int DP, bool DOCS>
 static cudaError_t launch_rows_one(const RowsLaunch &l)
 {
-    return l.boxes ? launch_rows_fill<CT, PARTS, NT, RG, DP, true>(l) : launch_rows_fill<CT, PARTS, NT, RG, DP, false>(l);
+    return l.boxes ? launch_rows_fill<CT, PARTS, NT, RG, DP, true, DOCS>(l)
+                   : launch_rows_fill<CT, PARTS, NT, RG, DP, false, DOCS>(l);
 }
 
-template <int CT, int PARTS, int DP>
+template <int CT, int PARTS, int DP, bool DOCS>
 static cudaError_t launch_rows_tiles(const RowsLaunch &l)
 {
-    if (l.choice.rows == 8) return launch_rows_one<CT, PARTS, 1, 1, DP>(l);
+    if (l.choice.rows == 8) return launch_rows_one<CT, PARTS, 1, 1, DP, DOCS>(l);
     if constexpr (DP <= 128)
-        if (l.choice.rows == 32) return launch_rows_one<CT, PARTS, 2, 2, DP>(l);
-    return launch_rows_one<CT, PARTS, 2, 1, DP>(l);
+        if (l.choice.rows == 32) return launch_rows_one<CT, PARTS, 2, 2, DP, DOCS>(l);
+    return launch_rows_one<CT, PARTS, 2, 1, DP, DOCS>(l);
 }
 
 // How many clusters of 1 .. kMaxCluster CTAs the GPU holds at once.  Every instance
@@ -68,7 +69,7 @@ static cudaError_t launch_rows_tiles(const RowsLaunch &l)
 template <int CT>
 static cudaError_t rows_room(int (&n)[kMaxCluster + 1])
 {
-    auto kern = rows_kernel<CT, 1, 1, 1, 128, true>;
+    auto kern = rows_kernel<CT, 1, 1, 1, 128, true, false>;
     constexpr int kSmem = static_cast<int>(sizeof(RowsShared<CT, 1, 1, 1, 128>)) + 1024;
     static_assert(kSmem > 227 * 1024 / 2, "one CTA per SM");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -87,16 +88,16 @@ static cudaError_t rows_room(int (&n)[kMaxCluster + 1])
     return e;
 }
 
-template <int CT, int MANY>
+template <int CT, int MANY, bool DOCS>
 static cudaError_t launch_rows_type(const RowsLaunch &l)
 {
     const int dim = l.args.dim;
     if (l.parts_many) {
-        if (dim > 128) return launch_rows_tiles<CT, MANY, 256>(l);
-        return dim > 64 ? launch_rows_tiles<CT, MANY, 128>(l) : launch_rows_tiles<CT, MANY, 64>(l);
+        if (dim > 128) return launch_rows_tiles<CT, MANY, 256, DOCS>(l);
+        return dim > 64 ? launch_rows_tiles<CT, MANY, 128, DOCS>(l) : launch_rows_tiles<CT, MANY, 64, DOCS>(l);
     }
-    if (dim > 128) return launch_rows_tiles<CT, 1, 256>(l);
-    return dim > 64 ? launch_rows_tiles<CT, 1, 128>(l) : launch_rows_tiles<CT, 1, 64>(l);
+    if (dim > 128) return launch_rows_tiles<CT, 1, 256, DOCS>(l);
+    return dim > 64 ? launch_rows_tiles<CT, 1, 128, DOCS>(l) : launch_rows_tiles<CT, 1, 64, DOCS>(l);
 }
 
 }  // namespace attn
