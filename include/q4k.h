@@ -545,7 +545,8 @@ typedef struct {
     float scale, softcap;
     int32_t q_type, out_type, causal;
     uint32_t flags;         /* Q4K_FLAG_PDL, Q4K_FLAG_TEST_STALL (failure-path tests only), Q4K_FLAG_ATTN_FORM(n) or 0 */
-    uint32_t wait_limit_us; /* bound of each wait inside the kernel; 0 = 2 s */
+    uint32_t wait_limit_us; /* bound of each wait inside the kernel; 0 = 2 s (when one runs out, what is in flight
+                               is awaited, 20 ms at most each) */
     int32_t reserved;
 } q4k_attention_args;
 

@@ -86,6 +86,11 @@ __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * 
 
 constexpr int kHoles = 1 << 30;
 
+// How long a kernel that winds down waits for a copy or product in flight, whatever
+// limit the call gave its waits: they end in microseconds, and shared and tensor
+// memory are not given up before.
+constexpr uint64_t kLandNs = 20000000;
+
 // One tile: the rows, their token range and the keys that any of them sees.
 struct Tile {
     int seq;                   // (+ kHoles: between `from` and `hi` there may be keys that no row sees)

@@ -31,9 +31,10 @@
 //
 // Slots that nothing of the tile sees may hold NaN: scores are replaced, not
 // added to, and the rows of V outside the tile's keys, or in a hole that a document
-// mask leaves between them, are zeroed in shared memory before they meet P = 0.  Every wait is bounded in time: on a timeout the
-// CTA sets bit 3 of the error word, stops, waits (bounded) for its copies in
-// flight, frees its tensor memory and returns.
+// mask leaves between them, are zeroed in shared memory before they meet P = 0.
+// Every wait is bounded in time: on a timeout the CTA sets bit 3 of the error word,
+// stops, waits (bounded) for its copies and products in flight, frees its tensor
+// memory and returns.
 //
 // Measured (device): 2048 tokens of 32 / 8 bf16 heads over 14336 + 2048 positions 320
 // to 330 us, 1560 to 1610 TFLOP/s = 80 to 82 % of the measured matmul, tensor pipe
@@ -72,7 +73,7 @@ struct ChunkShared {
     uint8_t kv[kStages * kTile];
     uint8_t out[8][32 * 64];                                   // a warp's rows on their way out, 32 columns at a time
     SplitShared<kChunkThreads> plan;
-    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2][2], o_done[2], q_full, q_empty, edge;
+    unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2][2], o_done[2], q_full, q_empty, edge, drained;
     unsigned long long work_full[2], work_empty[2];
     Work work[2];
     alignas(16) uint32_t seen[2][kChunkKeys / 32];   // (tiles with holes) of the key and the value warp
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.edge), 1);
+        mbar_init(smem_u32(&sh.drained), 1);
         fence_barrier_init();
         sh.abort = 0;
     }
@@ -459,11 +461,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
             }
         }
-        // every copy issued lands before the CTA exits (at a wind-down, or its wait runs out): this
-        // warp's last two stages, the queries
+        // every copy issued lands before the CTA exits (another warp may wind down without having
+        // waited for it): this warp's last two stages, one that it has begun, the queries
         for (int i = max(0, unit - 2); i < unit + (ok ? 0 : 1); ++i)
-            (void)mbar_wait_bounded(smem_u32(&sh.full[2 * (i & 1) + (values ? 1 : 0)]), (i >> 1) & 1, a.wait_ns);
-        if (!ok && q_sent) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, a.wait_ns);
+            (void)mbar_wait_bounded(smem_u32(&sh.full[2 * (i & 1) + (values ? 1 : 0)]), (i >> 1) & 1, kLandNs);
+        if (!ok && values) (void)mbar_wait_bounded(smem_u32(&sh.edge), edges & 1, kLandNs);
+        if (q_sent) (void)mbar_wait_bounded(smem_u32(&sh.q_full), (k + 1) & 1, kLandNs);   // (of tile k - 1)
+        if (q_sent && !ok) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, kLandNs);
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
         regs_dec<kOtherRegs>();
@@ -717,6 +721,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tm_fence_before();
     __syncthreads();
     if (w == kMmaWarp) {
+        if (*abort) {   // (else the softmax warps have seen the last products done)
+            mma_commit(smem_u32(&sh.drained));
+            (void)mbar_wait_bounded(smem_u32(&sh.drained), 0, kLandNs);
+        }
         tm_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u) : "memory");
     }

@@ -425,12 +425,12 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
         }
 
-        // a wait has timed out: the copies in flight land (or time out) before the ring is used again
+        // a wait has timed out: the copies in flight land before the ring is used again
         auto wind_down = [&](int i) {
             if (lane == 0) atomicOr(a.error, 8u);
-            for (int k = i + 1; k < min(i + SLOTS, count); ++k)
+            for (int k = i; k < min(i + SLOTS, count); ++k)
                 (void)mbar_wait_bounded(smem_u32(&sh.full[kg][(first_fill + k) % SLOTS]), ((first_fill + k) / SLOTS) & 1,
-                                        a.wait_ns);
+                                        kLandNs);
         };
         for (int i = 0; i < count; ++i) {
             const int kb = kb0 + i * Sp::kUnit;
