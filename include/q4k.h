@@ -512,7 +512,9 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  * the cache's type and a 16-bit out, the weights exp(s_j - m) are rounded once to
  * the cache's type before they meet the values on the tensor cores (each by
  * at most 2^-8 of itself in bf16, 2^-11 in fp16, beside the output's own rounding).  With fp32 q or out, q and the weights enter as 2 (fp16) or 3
- * (bf16) parts, 22 and 24 bits.
+ * (bf16) parts, 22 and 24 bits; so they do with a softcap above 256, whose scores
+ * are formed to 2^-20 of themselves (2^-22 of the cap below that, in 16-bit calls).
+ * A softcap above 1e30 is taken as 1e30, one below 1e-30 as that.
  *
  *   q, out [tokens][q_heads][dim]: any type each; lse fp32 [tokens][q_heads] or NULL
  *   q_heads a positive multiple of the cache's heads, dim a multiple of 8,
@@ -531,7 +533,7 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  * of CTAs (Q4K_ATTN_CLUSTER8, 16, 32) or with the work split over the GPU
  * (Q4K_ATTN_SPLIT8, 16, 32; tiles of 32 for dim <= 128), or tiles of 256 rows on
  * tcgen05 (Q4K_ATTN_MANY: q of the cache's type, a 16-bit out, dim <= 128, pages of
- * a multiple of 16, scale >= 0); INVALID_ARG where the call cannot take it.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
+ * a multiple of 16, scale >= 0, softcap <= 256); INVALID_ARG where the call cannot take it.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, CUDA.
  */
 typedef struct {
     const void *q;

@@ -316,7 +316,10 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     const int64_t per = c->pages > 0 ? c->max_pages : 0;
     p.capacity = static_cast<int>(per > most / c->page_size ? most : per * c->page_size);
     // a window past every position is none
-    p.window = a->window > most ? 0 : static_cast<int>(a->window), p.scale = a->scale, p.softcap = a->softcap;
+    p.window = a->window > most ? 0 : static_cast<int>(a->window), p.scale = a->scale;
+    // beyond 1e30 a cap is none that fp32 scores could tell, below 1e-30 all scores are alike;
+    // the quotient and products with it stay normal numbers
+    p.softcap = a->softcap > 0.0f ? std::min(std::max(a->softcap, 1e-30f), 1e30f) : 0.0f;
     p.pages = static_cast<int>(c->pages), p.batch = static_cast<int>(c->batch);
     p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
     p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
@@ -329,7 +332,10 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
         return Q4K_ERR_CUDA;
     l.sms = sms;
     l.stream = static_cast<cudaStream_t>(stream);
-    l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32;
+    // 16-bit calls form cap tanh(s / cap) as cap (1 - 2 / (exp + 1)), off by 2^-22 of the cap:
+    // at 256 an eighth of what rounding a weight to fp16 may cost.  Larger caps take the
+    // kernels of fp32 calls, whose tanh is good to a few ulp of itself.
+    l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32 || p.softcap > 256.0f;
     // The tcgen05 kernel takes q of the cache's type, a 16-bit out and pages that split into
     // boxes of 16 slots or more.  Its TMA boxes also ask for positive strides and
     // groups of 256 heads at most, its maxima for a scale that is not negative.
