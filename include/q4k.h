@@ -376,7 +376,8 @@ q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, 
  * (page, slot, head, d) at page*page_stride + slot*slot_stride + head*head_stride
  * + d, for the keys and for the values with strides of their own: page-by-page
  * [slot][head] and [head][slot] orders and keys and values in one buffer are all
- * strides.  Cached position j of sequence b is slot j % page_size of page
+ * strides (one of an axis of a single element is not looked at).  Cached
+ * position j of sequence b is slot j % page_size of page
  * page_table[b*page_table_stride + j / page_size].  Sequence b of `batch` owns
  * the token rows seq_start[b] .. seq_start[b+1]-1 of the call (none is fine) and
  * kv_len[b] cached positions, these new tokens included: its token i is at
@@ -384,11 +385,11 @@ q4k_status q4k_stream_read(const void *buf, int64_t bytes, int64_t *bytes_read, 
  *
  * page_table, seq_start, kv_len and the other index arrays are device memory and
  * are read only by the kernels, so a call needs no host copy of them and can be
- * captured in a graph, a process's first one too.  The kernels check them: a position, page, row range or
- * length outside the buffers is not followed (nothing is read or written through
- * it), sets bit 2 of q4k_device_error_flags(), and leaves the outputs that
- * depend on it invalid.  Token rows that belong to no sequence are left as they
- * are.
+ * captured in a graph, a process's first one too.  The kernels check them: a
+ * position, page, row range or length outside the buffers is not followed (nothing
+ * is read or written through it), sets bit 2 of q4k_device_error_flags(), and
+ * leaves the outputs that depend on it invalid.  Token rows that belong to no
+ * sequence are left as they are.
  *
  * Q4K_FLAG_PDL in a call's flags launches its (first) kernel as a programmatic
  * dependent of the kernel before it on the stream: it may start while that one
@@ -511,7 +512,8 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  * Precision: softmax statistics, sums and outputs accumulate in fp32.  With q of
  * the cache's type and a 16-bit out, the weights exp(s_j - m) are rounded once to
  * the cache's type before they meet the values on the tensor cores (each by
- * at most 2^-8 of itself in bf16, 2^-11 in fp16, beside the output's own rounding).  With fp32 q or out, q and the weights enter as 2 (fp16) or 3
+ * at most 2^-8 of itself in bf16, 2^-11 in fp16, beside the output's own rounding).
+ * With fp32 q or out, q and the weights enter as 2 (fp16) or 3
  * (bf16) parts, 22 and 24 bits; so they do with a softcap above 256, whose scores
  * are formed to 2^-20 of themselves (2^-22 of the cap below that, in 16-bit calls).
  * A softcap above 1e30 is taken as 1e30, one below 1e-30 as that.

@@ -277,6 +277,8 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
 {
     q4k_status st = check_cache(c);
     if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
+    const q4k_paged_cache used = with_used_strides(*c);
+    c = &used;
     auto type_ok = [](int t) { return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16; };
     if (c->dim % 8 || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
         !type_ok(a->q_type) || !type_ok(a->out_type) || (a->causal & ~1) || a->window < 0 ||
@@ -289,10 +291,12 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     auto off16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; };
     auto off4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
     const int64_t qn = a->q_type == Q4K_F32 ? 4 : 8, on = a->out_type == Q4K_F32 ? 4 : 8;
+    const int64_t q_token = used_stride(a->q_token_stride, c->tokens), q_head = used_stride(a->q_head_stride, a->q_heads);
+    const int64_t out_token = used_stride(a->out_token_stride, c->tokens), out_head = used_stride(a->out_head_stride, a->q_heads);
     if (off16(c->k) || off16(c->v) || off16(a->q) || off16(a->out) || off4(a->lse) || off4(a->slopes) ||
         off4(a->prefix_len) || off4(a->kv_start) || c->k_page_stride % 8 || c->k_slot_stride % 8 ||
         c->k_head_stride % 8 || c->v_page_stride % 8 || c->v_slot_stride % 8 || c->v_head_stride % 8 ||
-        a->q_token_stride % qn || a->q_head_stride % qn || a->out_token_stride % on || a->out_head_stride % on)
+        q_token % qn || q_head % qn || out_token % on || out_head % on)
         return Q4K_ERR_MISALIGNED;
     int sms = 0;
     st = check_device(&sms);
@@ -301,8 +305,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     attn::RowsLaunch l{};
     attn::Args &p = l.args;
     p.q = a->q, p.k = c->k, p.v = c->v, p.out = a->out, p.lse = a->lse;
-    p.q_token = a->q_token_stride, p.q_head = a->q_head_stride;
-    p.out_token = a->out_token_stride, p.out_head = a->out_head_stride;
+    p.q_token = q_token, p.q_head = q_head, p.out_token = out_token, p.out_head = out_head;
     p.k_page = c->k_page_stride, p.k_slot = c->k_slot_stride, p.k_head = c->k_head_stride;
     p.v_page = c->v_page_stride, p.v_slot = c->v_slot_stride, p.v_head = c->v_head_stride;
     p.table_stride = c->page_table_stride, p.page_size = static_cast<int>(c->page_size);
@@ -345,7 +348,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
     l.boxes = boxes && p.capacity > 0;
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
-                         (c->tokens == 1 || stride_ok(a->q_token_stride)) && (a->q_heads == 1 || stride_ok(a->q_head_stride));
+                         (c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head));
     const int (*room)[attn::kMaxCluster + 1];
     if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
     const int parts = !l.parts_many ? 1 : c->type == Q4K_F16 ? 2 : 3;

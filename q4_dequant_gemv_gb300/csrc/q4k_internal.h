@@ -34,6 +34,9 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
 // Sizes, types and index pointers of a cache (no device call).
 q4k_status check_cache(const q4k_paged_cache *c);
+// A stride of an axis of one element is used by no index: whatever it is, it counts as 0.
+inline int64_t used_stride(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
+q4k_paged_cache with_used_strides(q4k_paged_cache c);
 unsigned int read_rope_error();
 unsigned int read_attn_error();
 bool clear_rope_error();

@@ -470,7 +470,8 @@ q4k_status rope_impl(const q4k_rope_args *a, void *stream)
     q4k_status st = check_device(&sms);
     if (st != Q4K_OK || a->tokens == 0) return st;
     TokenArgs p{};
-    p.part[0] = Part{a->x, a->y, a->x_token_stride, a->x_head_stride, a->y_token_stride, a->y_head_stride,
+    p.part[0] = Part{a->x, a->y, used_stride(a->x_token_stride, a->tokens), used_stride(a->x_head_stride, a->heads),
+                     used_stride(a->y_token_stride, a->tokens), used_stride(a->y_head_stride, a->heads),
                      static_cast<int>(a->heads), a->x_type, a->y_type, static_cast<int>(a->rot)};
     p.pos = a->pos, p.table = a->table, p.table_rows = a->table_rows;
     p.tokens = static_cast<int>(a->tokens), p.dim = static_cast<int>(a->dim), p.rot = static_cast<int>(a->rot);
@@ -496,11 +497,21 @@ q4k_status check_cache(const q4k_paged_cache *c)
     return Q4K_OK;
 }
 
+q4k_paged_cache with_used_strides(q4k_paged_cache c)
+{
+    c.k_page_stride = used_stride(c.k_page_stride, c.pages), c.v_page_stride = used_stride(c.v_page_stride, c.pages);
+    c.k_slot_stride = used_stride(c.k_slot_stride, c.page_size), c.v_slot_stride = used_stride(c.v_slot_stride, c.page_size);
+    c.k_head_stride = used_stride(c.k_head_stride, c.heads), c.v_head_stride = used_stride(c.v_head_stride, c.heads);
+    return c;
+}
+
 q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, void *stream)
 {
     using namespace rope;
     q4k_status st = check_cache(c);
     if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
+    const q4k_paged_cache used = with_used_strides(*c);
+    c = &used;
     const bool some = c->tokens > 0 && c->batch > 0;
     if (a->rot < 0 || a->rot % 2 || a->rot > c->dim || a->rot > kMaxRot || a->table_rows < 0 ||
         !good_type(a->kv_type) || (a->interleaved & ~1) || (a->flags & ~Q4K_FLAG_PDL) || (a->q == nullptr) != (a->q_out == nullptr))
@@ -517,11 +528,15 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
     if (st != Q4K_OK || !some) return st;
     TokenArgs p{};
     const int heads = static_cast<int>(c->heads), rot = static_cast<int>(a->rot);
-    p.part[0] = Part{a->k, c->k, a->k_token_stride, a->k_head_stride, 0, c->k_head_stride, heads, a->kv_type, c->type, rot};
-    p.part[1] = Part{a->v, c->v, a->v_token_stride, a->v_head_stride, 0, c->v_head_stride, heads, a->kv_type, c->type, 0};
+    const int64_t n = c->tokens;
+    p.part[0] = Part{a->k, c->k, used_stride(a->k_token_stride, n), used_stride(a->k_head_stride, heads), 0, c->k_head_stride,
+                     heads, a->kv_type, c->type, rot};
+    p.part[1] = Part{a->v, c->v, used_stride(a->v_token_stride, n), used_stride(a->v_head_stride, heads), 0, c->v_head_stride,
+                     heads, a->kv_type, c->type, 0};
     if (a->q)
-        p.part[2] = Part{a->q, a->q_out, a->q_token_stride, a->q_head_stride, a->q_out_token_stride,
-                         a->q_out_head_stride, static_cast<int>(a->q_heads), a->q_type, a->q_out_type, rot};
+        p.part[2] = Part{a->q, a->q_out, used_stride(a->q_token_stride, n), used_stride(a->q_head_stride, a->q_heads),
+                         used_stride(a->q_out_token_stride, n), used_stride(a->q_out_head_stride, a->q_heads),
+                         static_cast<int>(a->q_heads), a->q_type, a->q_out_type, rot};
     p.k_page = c->k_page_stride, p.k_slot = c->k_slot_stride, p.v_page = c->v_page_stride, p.v_slot = c->v_slot_stride;
     p.pages = c->pages, p.page_size = c->page_size, p.table_stride = c->page_table_stride, p.max_pages = c->max_pages;
     p.page_table = c->page_table, p.seq_start = c->seq_start, p.kv_len = c->kv_len, p.pos = a->pos;
