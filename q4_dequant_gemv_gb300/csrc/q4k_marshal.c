@@ -453,8 +453,13 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     const double scale = a[7] == Py_None ? 1.0 / sqrt((double)q.d) : PyFloat_AsDouble(a[7]), cap = PyFloat_AsDouble(a[9]);
     r.window = PyLong_AsLongLong(a[11]);
     const int causal = PyObject_IsTrue(a[12]);
-    r.flags = (uint32_t)PyLong_AsUnsignedLong(a[17]), r.wait_limit_us = (uint32_t)PyLong_AsUnsignedLong(a[18]);
+    const unsigned long limit = PyLong_AsUnsignedLong(a[18]);
+    r.flags = (uint32_t)PyLong_AsUnsignedLong(a[17]), r.wait_limit_us = (uint32_t)limit;
     if (PyErr_Occurred()) return NULL;
+    if (limit > UINT32_MAX) {
+        PyErr_SetString(PyExc_ValueError, "wait_limit_us must be less than 2^32");
+        return NULL;
+    }
     if (!array_or_none(a[10], "slopes", g_dtype[Q4K_F32], q.h, &dev, (void **)&r.slopes) ||
         !array_or_none(a[13], "prefix_len", g_int32, c.batch, &dev, (void **)&r.prefix_len) ||
         !array_or_none(a[14], "kv_start", g_int32, q.n, &dev, (void **)&r.kv_start))

@@ -210,3 +210,13 @@ def test_host_tensors_are_refused(world):
         with pytest.raises((TypeError, ValueError)):
             f()
     assert not world.calls
+
+
+def test_limits_past_32_bits_are_refused(world):
+    """wait_limit_us is 32 bits wide in the library; 2^32 would be 0, which stands for two seconds."""
+    for limit in (2 ** 32, 2 ** 40 + 5, -1):
+        with pytest.raises((ValueError, OverflowError)):
+            world.attention(wait_limit_us=limit)
+    assert not world.calls
+    world.attention(wait_limit_us=2 ** 32 - 1)
+    assert [c[0] for c in world.calls] == ["attention"]
