@@ -226,6 +226,7 @@ struct Split {
                 if constexpr (DOCS) away |= r.lo > t.pos0 + i;
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
+            if (lo >= last.hi) lo = (lo + ALIGN - 1) & ~(ALIGN - 1);   // sees nothing: no key is looked up
             // Where every token sees its own position the ranges of consecutive ones meet,
             // and where the mask is not causal all end together: no holes.
             if constexpr (DOCS)

@@ -31,6 +31,10 @@ CASES = [
          kv_start=_padded(200, 900, [(0, 1), (60, 61), (150, 200)], 400) + [0] + _padded(64, 64, [(0, 3), (50, 64)])),
     dict(new=[100], len=[400], prefix=[50], kv_start=_padded(100, 400, [(0, 1), (49, 50), (90, 100)])),
     dict(new=[90], len=[333], window=25, kv_start=_padded(90, 333, [(0, 20), (60, 90)])),
+    # tiles that see nothing at all
+    dict(new=[1, 2], len=[18, 100], causal=False, kv_start=[NOTHING, 100, NOTHING]),
+    dict(new=[40, 300], len=[57, 700], causal=False, kv_start=[NOTHING] * 40 + [650] * 20 + [700] * 280),
+    dict(new=[1, 40], len=[18, 77], kv_start=[18] + [NOTHING] * 40),
 ]
 
 
@@ -63,7 +67,7 @@ def test_holes(q4k, case, H, KH, D, page, types, fill, form):   # noqa: F811
     start = _dev([sum(case["new"][:i]) for i in range(len(case["new"]) + 1)])
     lse = torch.zeros(q.shape[0], H, device="cuda")
     out = q4k.paged_attention(q.cuda(), kc, vc, pt.cuda(), start, _dev(case["len"]), out_dtype=ot, lse=lse, form=form,
-                              window=case.get("window", 0), prefix_len=_dev(case.get("prefix")), kv_start=_dev(case["kv_start"]))
+                              causal=case.get("causal", True), window=case.get("window", 0), prefix_len=_dev(case.get("prefix")), kv_start=_dev(case["kv_start"]))
     torch.cuda.synchronize()
     flags = q4k.device_error_flags()
     q4k.device_error_clear()
