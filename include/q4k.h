@@ -525,11 +525,13 @@ q4k_status q4k_kv_append(const q4k_paged_cache *c, const q4k_append_args *a, voi
  *   causal 0 or 1; window >= 0; softcap >= 0 and finite.
  * Calls that split rows over the whole GPU (a few long sequences, prompt chunks)
  * take scratch on `stream` from a stream-ordered pool of the library's own, which
- * keeps it for later calls: two partial results per SM, 0.4 to 44 MB for each call
- * in flight.  Partial results are added in a fixed order: the same
- * inputs give the same bits.  Q4K_FLAG_TEST_STALL makes the first copy of each
- * CTA be awaited for 16 bytes more than it brings; the kernel then winds down as
- * after any wait that runs out (bit 3 of the error flags, outputs invalid).
+ * keeps it for later calls (to the end of the process): for each call in flight at
+ * most 8 R (W + 2) bytes an SM, R the rows of its tiles, W dim rounded up to 64,
+ * 128 or 256; on 152 SMs 0.6 MB (8 rows of 64) to 40.5 MB (256 rows of 128).
+ * Partial results are added in a fixed order: the same inputs give the same bits.
+ * Q4K_FLAG_TEST_STALL makes a CTA's first copies be awaited for 16 bytes more than
+ * they bring (where pages hold a multiple of 16 slots); the kernel then winds down
+ * as after any wait that runs out (bit 3 of the error flags, outputs invalid).
  * Q4K_FLAG_ATTN_FORM(n) has a call take one form of the kernels, normally chosen
  * by the library from the sizes: tiles of 8, 16 or 32 query rows, each by a cluster
  * of CTAs (Q4K_ATTN_CLUSTER8, 16, 32) or with the work split over the GPU

@@ -492,8 +492,6 @@ struct Attributes {
 bool encode_cache(CacheMaps *maps, const Args &a, int type, int box);
 // The queries as [token][head][d]: boxes of `tokens` tokens by a group's heads by 64 elements.
 bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens);
-// The queries as [token][head][d]: boxes of `tokens` tokens by a group's heads by 64 elements.
-bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens);
 
 }  // namespace attn
 }  // namespace q4k

@@ -36,9 +36,9 @@
 // stops, waits (bounded) for its copies and products in flight, frees its tensor
 // memory and returns.
 //
-// Measured (device): 2048 tokens of 32 / 8 bf16 heads over 14336 + 2048 positions 320
-// to 330 us, 1560 to 1610 TFLOP/s = 80 to 82 % of the measured matmul, tensor pipe
-// 75 % active (S read twice in pieces 451; eight query loads at a time 410; one
+// Measured (device): 2048 tokens of 32 / 8 bf16 heads over 14336 + 2048 positions 310
+// to 330 us, 1560 to 1660 TFLOP/s = 80 to 85 % of the measured matmul, tensor pipe
+// 76 % active (784 us with capped scores) (S read twice in pieces 451; eight query loads at a time 410; one
 // pipeline over tiles, a row of S in registers, P in two parts 340); three chunks of
 // 512 over 4096 81 us, of which 21 are start and join.
 #pragma once

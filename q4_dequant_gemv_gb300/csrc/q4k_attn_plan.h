@@ -10,15 +10,20 @@
 // Small tiles fill the GPU and read keys again (from L2), large ones read them
 // once.  The estimate below, in us, was fitted to 1317 measured calls (1 to 64
 // sequences of 1 to 8 tokens, 28/4, 32/8 and 16/2 heads of 128, 16/16 of 64, 200 to
-// 30000 positions, 16-bit and fp32 queries), each in every form: its choice is
-// within 1.2 % of the fastest on the geometric mean (1.4x at worst), where the
-// rule before it (the smallest tile that holds a sequence's rows, clusters by units,
-// the tcgen05 kernel above 16 rows) was 16 % off.  Both sides of it, in us:
+// 30000 positions, 16-bit and fp32 queries, page tables just wide enough), each in
+// every form: for those calls its choice is within 1.2 % of the fastest on the
+// geometric mean (1.4x at worst), where the rule before it (the smallest tile that
+// holds a sequence's rows, clusters by units, the tcgen05 kernel above 16 rows) was
+// 16 % off.  More than 8 tokens a sequence lie outside the fit.  Both sides, in us:
 //   4 sequences of 5 x 7 rows over 2000: clusters with tiles of 8 rows 15, of 16 22, of 32 24;
 //   64 of 8 x 7 over 200, fp32 queries: tiles of 8 70, of 16 51, of 32 44;
 //   1 of 1 x 7 over 1000: cluster 7.2, split 12.3; 1 of 1 x 4 over 131072: 109 and 92;
 //   2 x 4 rows over 14336, 16 bits: few-rows 20, many-rows 26; 8 x 4 rows 41 and 31.
-// It knows no lengths, only what a page table row can hold.
+// It knows no lengths, only what a page table row can hold.  A table much wider than
+// the sequences makes it take them for long ones: one token of 28 / 4 heads over
+// 1000 positions takes 7.1 us with a table of 1000, 11.2 (split, the cluster form
+// still 7.1) with one of 16384 or more; sixteen over 4096 28.2 and, in a table of
+// 32768, 36.1 (clusters 27.9).  Such a caller can ask for the form.
 #pragma once
 #include <algorithm>
 #include <cmath>

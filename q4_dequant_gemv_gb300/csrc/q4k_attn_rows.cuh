@@ -717,7 +717,6 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
     }
 }
 
-// Launches the kernel of one cache type (in a translation unit of its own).
 // What q4k_attn_plan.h chose for a call.
 struct Choice {
     bool chunk;    // the many-rows kernel
@@ -733,6 +732,7 @@ struct RowsLaunch {
     cudaStream_t stream;
 };
 cudaError_t clusters_at_once(int (&n)[kMaxCluster + 1]);
+// The kernel of one cache type, without and with holes (each in a translation unit of its own).
 cudaError_t launch_rows_f16(const RowsLaunch &l);
 cudaError_t launch_rows_bf16(const RowsLaunch &l);
 cudaError_t launch_rows_docs_f16(const RowsLaunch &l);
