@@ -1,7 +1,6 @@
 """The library's host code over a CUDA runtime that runs nothing (fake_cuda_runtime.cpp): what it launches, with which
 sizes, on which device, and what it does when a call fails.  CPU only."""
 import ctypes
-import glob
 import os
 import shutil
 import subprocess
@@ -53,10 +52,9 @@ class Library:
 def fake_path(tmp_path_factory):
     from q4_dequant_gemv_gb300 import _build
     _build.build()
-    objects = sorted(glob.glob(os.path.join(_build.BUILD_DIR, "q*.o")))
-    if len(objects) < len(_build._sources()):
+    objects = [os.path.join(_build.BUILD_DIR, os.path.basename(src)[:-3] + ".o") for src in _build._sources()]
+    if not all(os.path.exists(o) for o in objects):
         _build.build(force=True)
-        objects = sorted(glob.glob(os.path.join(_build.BUILD_DIR, "q*.o")))
     include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc()))), "include")
     out = str(tmp_path_factory.mktemp("fake") / "libq4k_fake.so")
     subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-O1", "-fPIC", "-shared", "-I", include, "-o", out,
