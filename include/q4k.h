@@ -567,6 +567,106 @@ typedef struct {
 
 q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The paged cache in 8 bits: codes with a scale for each block of tokens and
+ * head.  Half the memory of a 16-bit cache, half the bytes of a decode step.
+ * ---------------------------------------------------------------------------
+ * Codes lie in pages as in q4k_paged_cache (whose strides count elements, here
+ * bytes), of type Q4K_I8 (-127 .. 127) or Q4K_E4M3 (4 exponent and 3 fraction
+ * bits, up to 448).  The slots of a page are cut into blocks of `block`
+ * consecutive ones, and each block has one fp32 scale per head, for the keys and
+ * for the values: the value of (page, slot, head, d) is its code times the scale at
+ * page*page_stride + (slot / block)*block_stride + head*head_stride.  A block of one
+ * token costs 4 bytes a head and token and is never scaled anew; larger ones cost less
+ * and share their largest value.
+ */
+#define Q4K_I8 3
+#define Q4K_E4M3 4
+
+typedef struct {
+    q4k_paged_cache cache; /* type: Q4K_I8 or Q4K_E4M3 */
+    float *k_scale, *v_scale;
+    int64_t k_scale_page_stride, k_scale_block_stride, k_scale_head_stride;
+    int64_t v_scale_page_stride, v_scale_block_stride, v_scale_head_stride;
+    int64_t block; /* a power of two up to 128 that divides page_size */
+} q4k_paged_cache8;
+
+/*
+ * y = turn(x * weight / sqrt(mean(x^2) + eps)) for the heads of one or two tensors
+ * (queries and keys) in one launch: the mean over a head's dim elements, the rotation
+ * as q4k_rope's (row pos[t] of the table).  fp32 arithmetic, one rounding to y's type.
+ *   weight fp32 [dim], or [heads][dim] with weight_head_stride = dim; NULL: that
+ *   tensor is not normed.  k.x NULL: one tensor.  y may be x itself (same type and
+ *   strides); the tensors must not overlap otherwise.
+ *   tokens >= 0 (0: no-op), dim a multiple of 8 up to 256, rot even, 0 <= rot <= dim
+ *   (0: nothing is turned; pos and table may then be NULL), eps >= 0 and finite.
+ * Errors: as q4k_rope.
+ */
+typedef struct {
+    const void *x;
+    void *y;
+    const float *weight;
+    int64_t heads, x_token_stride, x_head_stride, y_token_stride, y_head_stride, weight_head_stride;
+    int32_t x_type, y_type;
+} q4k_heads;
+
+typedef struct {
+    q4k_heads q, k;
+    const int32_t *pos; /* [tokens] */
+    const float *table; /* [table_rows][rot] */
+    int64_t tokens, dim, rot, table_rows;
+    float eps;
+    int32_t interleaved;
+    uint32_t flags; /* Q4K_FLAG_PDL or 0 */
+    int32_t reserved;
+} q4k_norm_rope_args;
+
+q4k_status q4k_norm_rope(const q4k_norm_rope_args *a, void *stream);
+
+/*
+ * q4k_kv_append into an 8-bit cache: keys normed (k_weight, NULL: not) and turned,
+ * values as they come, both in fp32; queries, where given, normed (q_weight) and
+ * turned into q_out.  With top = 127 or 448, a block that new tokens fall into gets
+ *   scale = max(max|x| / top over its new tokens, its old scale where it holds older
+ *           tokens of the sequence (positions before the first new one), 2^-126),
+ *   code = x * (1 / scale) rounded to nearest even, at most top in size,
+ * and where that scale has grown the older tokens' codes become code * (old scale / scale),
+ * rounded again (by at most half a step of the new scale).  Slots behind the first new
+ * position count as empty: what an engine takes back is not asked.  Infinities do not
+ * count for the scale and are stored as +-top; a NaN is stored as 0 (Q4K_I8) or NaN
+ * (Q4K_E4M3).  Only the new tokens' slots, the older ones of their blocks and those
+ * blocks' scales are written; a block that new tokens fall into belongs to one sequence
+ * of the call.  dim a multiple of 8 up to 256; everything else as q4k_kv_append.
+ */
+typedef struct {
+    q4k_append_args a;
+    const float *q_weight, *k_weight; /* as in q4k_heads */
+    int64_t q_weight_head_stride, k_weight_head_stride;
+    float eps;
+    int32_t reserved;
+} q4k_append8_args;
+
+q4k_status q4k_kv_append8(const q4k_paged_cache8 *c, const q4k_append8_args *a, void *stream);
+
+/*
+ * Reads cached rows back: token row t of sequence b gets scale * code of its position
+ * (the positions that q4k_kv_append8 with the same arrays writes; for whole sequences
+ * seq_start counts up kv_len), formed in fp32 and rounded once to `type` (Q4K_F32,
+ * Q4K_F16 or Q4K_BF16).
+ *   k, v [tokens][heads][dim]; either may be NULL.  Rows of no sequence and rows whose
+ *   position or page is outside the buffers are left as they are (the latter set bit 2
+ *   of the error flags).  dim a multiple of 8 up to 256.  Errors: as q4k_rope.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int32_t type;
+    uint32_t flags; /* Q4K_FLAG_PDL or 0 */
+} q4k_read8_args;
+
+q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream);
+
 /* Launch plan the automatic heuristics pick for a shape (for tests and
  * reports): out[0] = split_k, out[1] = number of CTAs, out[2] = rows per CTA
  * tile, out[3] = K blocks per x chunk held in shared memory. */
@@ -576,8 +676,8 @@ q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4]);
  * from the current device: bit 0 = a bounded wait inside a GEMV/argmax
  * kernel (Q4_K or Q6_K) or the streaming probe timed out, bit 1 = the same in the prefill
  * kernel; the kernel then wound down early and its outputs are invalid;
- * bit 2 = an index array of q4k_rope, q4k_kv_append or q4k_paged_attention
- * points outside its buffers; bit 3 = a bounded wait in q4k_paged_attention.
+ * bit 2 = an index array of q4k_rope, q4k_norm_rope, q4k_kv_append(8), q4k_kv_read8
+ * or q4k_paged_attention points outside its buffers; bit 3 = a bounded wait in q4k_paged_attention.
  * 0 = no error.  The bits stay set until q4k_device_error_clear(). */
 unsigned int q4k_device_error_flags(void);
 

@@ -49,7 +49,8 @@ EXPORTS = ("q4k_status_string", "q4k_abi_version", "q4k_gemv", "q4k_gemv_argmax"
            "q4k_gemv_grouped", "q4k_gemv_plan",
            "q4k_device_error_flags", "q4k_device_error_clear", "q4k_stream_read", "q6k_gemv",
            "q6k_planar_bytes", "q6k_repack_planar", "q6k_gemv_planar",
-           "q4k_rope_table", "q4k_rope", "q4k_kv_append", "q4k_paged_attention")
+           "q4k_rope_table", "q4k_rope", "q4k_kv_append", "q4k_paged_attention",
+           "q4k_norm_rope", "q4k_kv_append8", "q4k_kv_read8")
 
 
 def lib():
@@ -95,12 +96,16 @@ def lib():
         L.q4k_device_error_clear.restype = I
         L.q4k_stream_read.argtypes = [P, I64, ctypes.POINTER(ctypes.c_int64), P]
         L.q4k_stream_read.restype = I
-        # the structures of these four are passed as packed bytes
+        # the structures of these are passed as packed bytes
         L.q4k_rope_table.argtypes = [P, I64, I64, ctypes.c_char_p, P]
         L.q4k_rope.argtypes = [ctypes.c_char_p, P]
         L.q4k_kv_append.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
         L.q4k_paged_attention.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
-        for f in (L.q4k_rope_table, L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention):
+        L.q4k_norm_rope.argtypes = [ctypes.c_char_p, P]
+        L.q4k_kv_append8.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
+        L.q4k_kv_read8.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
+        for f in (L.q4k_rope_table, L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention, L.q4k_norm_rope, L.q4k_kv_append8,
+                  L.q4k_kv_read8):
             f.restype = I
         _lib = L
         return L
@@ -327,10 +332,14 @@ def stream_read(buf, *, stream=None) -> int:
 
 
 def __getattr__(name):
-    # The attention module needs torch at import; the rest of the binding does not.
+    # The attention modules need torch at import; the rest of the binding does not.
     if name in ("rope_table", "rope", "kv_append", "paged_attention"):
         from . import _attention
         globals()[name] = f = getattr(_attention, name)
+        return f
+    if name in ("norm_rope", "kv_append8", "kv_read8"):
+        from . import _cache8
+        globals()[name] = f = getattr(_cache8, name)
         return f
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

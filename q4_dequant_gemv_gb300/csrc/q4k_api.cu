@@ -107,6 +107,18 @@ q4k_status q4k_paged_attention(const q4k_paged_cache *c, const q4k_attention_arg
     return q4k::paged_attention_impl(c, a, stream);
 }
 
+q4k_status q4k_norm_rope(const q4k_norm_rope_args *a, void *stream) { return q4k::norm_rope_impl(a, stream); }
+
+q4k_status q4k_kv_append8(const q4k_paged_cache8 *c, const q4k_append8_args *a, void *stream)
+{
+    return q4k::kv_append8_impl(c, a, stream);
+}
+
+q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream)
+{
+    return q4k::kv_read8_impl(c, a, stream);
+}
+
 q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4])
 {
     return q4k::gemv_plan_impl(N, K, batch, out);
@@ -117,14 +129,14 @@ q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4])
 unsigned int q4k_device_error_flags(void)
 {
     return q4k::read_device_error() | q4k::read_prefill_error() | q4k::read_q6k_error() | q4k::read_q6p_error() |
-           q4k::read_probe_error() | q4k::read_rope_error() | q4k::read_attn_error();
+           q4k::read_probe_error() | q4k::read_rope_error() | q4k::read_attn_error() | q4k::read_cache8_error();
 }
 
 q4k_status q4k_device_error_clear(void)
 {
     const bool ok = q4k::clear_device_error() & q4k::clear_prefill_error() & q4k::clear_q6k_error() &
                     q4k::clear_q6p_error() & q4k::clear_probe_error() & q4k::clear_rope_error() &
-                    q4k::clear_attn_error();
+                    q4k::clear_attn_error() & q4k::clear_cache8_error();
     return ok ? Q4K_OK : Q4K_ERR_CUDA;
 }
 

@@ -32,13 +32,20 @@ q4k_status rope_table_impl(float *table, int64_t rows, int64_t rot, const q4k_ro
 q4k_status rope_impl(const q4k_rope_args *a, void *stream);
 q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, void *stream);
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
+q4k_status norm_rope_impl(const q4k_norm_rope_args *a, void *stream);
+q4k_status kv_append8_impl(const q4k_paged_cache8 *c, const q4k_append8_args *a, void *stream);
+q4k_status kv_read8_impl(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream);
 // Sizes, types and index pointers of a cache (no device call).
 q4k_status check_cache(const q4k_paged_cache *c);
 // A stride of an axis of one element is used by no index: whatever it is, it counts as 0.
 inline int64_t used_stride(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
 q4k_paged_cache with_used_strides(q4k_paged_cache c);
+q4k_status check_cache8(const q4k_paged_cache8 *c);
+q4k_paged_cache8 with_used_strides(q4k_paged_cache8 c);   // (of a checked cache)
 unsigned int read_rope_error();
 unsigned int read_attn_error();
+unsigned int read_cache8_error();
+bool clear_cache8_error();
 bool clear_rope_error();
 bool clear_attn_error();
 unsigned int read_device_error();

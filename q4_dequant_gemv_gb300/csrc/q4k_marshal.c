@@ -1,5 +1,5 @@
-/* q4k_marshal.c -- the Python side of q4k_rope, q4k_kv_append and
- * q4k_paged_attention: checks tensors, fills the structures of include/q4k.h and
+/* q4k_marshal.c -- the Python side of q4k_rope, q4k_kv_append, q4k_paged_attention
+ * and their forms for an 8-bit cache: checks tensors, fills the structures of include/q4k.h and
  * calls the library.  These calls sit between the launches of a decode step, and
  * reading some forty tensor attributes from Python took 8 to 12 us a call, more
  * than the kernels; here they take a third of that.  Plain CPython API: torch's
@@ -22,6 +22,14 @@ static PyObject *g_tensor, *g_dtype[3], *g_int32, *g_empty, *g_empty_like, *g_ne
 static rope_fn g_rope;
 static append_fn g_append;
 static attention_fn g_attention;
+/* The calls of an 8-bit cache come in by themselves (setup8). */
+typedef q4k_status (*norm_rope_fn)(const q4k_norm_rope_args *, void *);
+typedef q4k_status (*append8_fn)(const q4k_paged_cache8 *, const q4k_append8_args *, void *);
+typedef q4k_status (*read8_fn)(const q4k_paged_cache8 *, const q4k_read8_args *, void *);
+static PyObject *g_int8, *g_e4m3;
+static norm_rope_fn g_norm_rope;
+static append8_fn g_append8;
+static read8_fn g_read8;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_device,
     *s_cuda_stream, *k_dtype_device;
 
@@ -208,8 +216,16 @@ static int turn(PyObject *t, int64_t dim, int *dev, const float **p, int64_t *n,
     return 1;
 }
 
-/* k_cache, v_cache, page_table, seq_start, kv_len. */
-static int cache(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache *c)
+/* Type code of a cache's dtype (16 bits, or 8), -1 for another one. */
+static int cache_code(PyObject *dtype, int bits8)
+{
+    if (bits8) return dtype == g_int8 ? Q4K_I8 : dtype == g_e4m3 ? Q4K_E4M3 : -1;
+    const int code = dtype_code(dtype);
+    return code < Q4K_F16 ? -1 : code;
+}
+
+/* k_cache, v_cache at t, page_table, seq_start, kv_len at x. */
+static int cache_parts(PyObject *const *t, PyObject *const *x, int64_t tokens, int bits8, int *dev, q4k_paged_cache *c)
 {
     int64_t v[4], w[4];
     static const char *names[2] = {"k_cache", "v_cache"};
@@ -219,9 +235,10 @@ static int cache(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache *
         if (!is_tensor(t[i], names[i])) return 0;
         PyObject *dtype = dtype_of(t[i]);
         if (!dtype) return 0;
-        code[i] = dtype_code(dtype);
-        if (code[i] < Q4K_F16 || code[i] != code[0]) {
-            PyErr_Format(PyExc_TypeError, "%s must be bfloat16 or float16, both caches the same, got %S", names[i], dtype);
+        code[i] = cache_code(dtype, bits8);
+        if (code[i] < 0 || code[i] != code[0]) {
+            PyErr_Format(PyExc_TypeError, "%s must be %s, both caches the same, got %S", names[i],
+                         bits8 ? "int8 or float8_e4m3fn" : "bfloat16 or float16", dtype);
             return 0;
         }
         if (!on_gpu(t[i], names[i], dev)) return 0;
@@ -242,27 +259,112 @@ static int cache(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache *
     }
     c->k_page_stride = v[0], c->k_slot_stride = v[1], c->k_head_stride = v[2];
     c->v_page_stride = w[0], c->v_slot_stride = w[1], c->v_head_stride = w[2];
-    if (!is_tensor(t[2], "page_table")) return 0;
-    PyObject *dtype = dtype_of(t[2]);
+    if (!is_tensor(x[0], "page_table")) return 0;
+    PyObject *dtype = dtype_of(x[0]);
     if (!dtype) return 0;
     if (dtype != g_int32) {
         PyErr_Format(PyExc_TypeError, "page_table must have dtype %S, got %S", g_int32, dtype);
         return 0;
     }
-    if (!on_gpu(t[2], "page_table", dev)) return 0;
-    if (shape_of(t[2], v, 2) != 2) {
-        bad_shape(t[2], "page_table", "[sequences, pages]");
+    if (!on_gpu(x[0], "page_table", dev)) return 0;
+    if (shape_of(x[0], v, 2) != 2) {
+        bad_shape(x[0], "page_table", "[sequences, pages]");
         return 0;
     }
-    if (stride_of(t[2], w, 2) != 2) return 0;
+    if (stride_of(x[0], w, 2) != 2) return 0;
     if (w[1] != 1 && v[1] > 1) {
         PyErr_SetString(PyExc_ValueError, "page_table must be contiguous in its last dimension");
         return 0;
     }
     c->batch = v[0], c->max_pages = v[1], c->page_table_stride = w[0], c->tokens = tokens;
-    return address_of(t[0], &c->k) && address_of(t[1], &c->v) && address_of(t[2], (void **)&c->page_table) &&
-           array(t[3], "seq_start", g_int32, c->batch + 1, dev, (void **)&c->seq_start) &&
-           array(t[4], "kv_len", g_int32, c->batch, dev, (void **)&c->kv_len);
+    return address_of(t[0], &c->k) && address_of(t[1], &c->v) && address_of(x[0], (void **)&c->page_table) &&
+           array(x[1], "seq_start", g_int32, c->batch + 1, dev, (void **)&c->seq_start) &&
+           array(x[2], "kv_len", g_int32, c->batch, dev, (void **)&c->kv_len);
+}
+
+static int cache(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache *c)
+{
+    return cache_parts(t, t + 2, tokens, 0, dev, c);
+}
+
+/* k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len. */
+static int cache8(PyObject *const *t, int64_t tokens, int *dev, q4k_paged_cache8 *c)
+{
+    static const char *names[2] = {"k_scale", "v_scale"};
+    int64_t v[3], w[2][3], blocks = 0;
+    memset(c, 0, sizeof *c);
+    if (!cache_parts(t, t + 4, tokens, 1, dev, &c->cache)) return 0;
+    for (int i = 0; i < 2; ++i) {
+        PyObject *s = t[2 + i];
+        if (!is_tensor(s, names[i])) return 0;
+        PyObject *dtype = dtype_of(s);
+        if (!dtype) return 0;
+        if (dtype != g_dtype[Q4K_F32]) {
+            PyErr_Format(PyExc_TypeError, "%s must have dtype %S, got %S", names[i], g_dtype[Q4K_F32], dtype);
+            return 0;
+        }
+        if (!on_gpu(s, names[i], dev)) return 0;
+        if (shape_of(s, v, 3) != 3 || v[0] != c->cache.pages || v[2] != c->cache.heads || v[1] < 1 || (i && v[1] != blocks) ||
+            c->cache.page_size % v[1]) {
+            bad_shape(s, names[i], "[pages, blocks of a page, heads], the same for keys and values");
+            return 0;
+        }
+        blocks = v[1];
+        if (stride_of(s, w[i], 3) != 3 || !address_of(s, i ? (void **)&c->v_scale : (void **)&c->k_scale)) return 0;
+    }
+    c->block = c->cache.page_size / blocks;
+    if (c->block < 1 || c->block > 128 || (c->block & (c->block - 1))) {
+        PyErr_Format(PyExc_ValueError, "a block of %lld tokens: a power of two up to 128 is wanted", (long long)c->block);
+        return 0;
+    }
+    c->k_scale_page_stride = w[0][0], c->k_scale_block_stride = w[0][1], c->k_scale_head_stride = w[0][2];
+    c->v_scale_page_stride = w[1][0], c->v_scale_block_stride = w[1][1], c->v_scale_head_stride = w[1][2];
+    return 1;
+}
+
+/* A head norm's weight, fp32 [dim] or [heads, dim], or None. */
+static int weight(PyObject *t, const char *name, int64_t heads, int64_t dim, int *dev, const float **p, int64_t *stride)
+{
+    int64_t v[2], w[2];
+    *p = NULL, *stride = 0;
+    if (t == Py_None) return 1;
+    if (!is_tensor(t, name)) return 0;
+    PyObject *dtype = dtype_of(t);
+    if (!dtype) return 0;
+    if (dtype != g_dtype[Q4K_F32]) {
+        PyErr_Format(PyExc_TypeError, "%s must have dtype %S, got %S", name, g_dtype[Q4K_F32], dtype);
+        return 0;
+    }
+    if (!on_gpu(t, name, dev)) return 0;
+    const Py_ssize_t n = shape_of(t, v, 2);
+    if (n < 1 || n > 2 || v[n - 1] != dim || (n == 2 && v[0] != heads)) {
+        char want[96];
+        snprintf(want, sizeof want, "[%lld] or [%lld, %lld]", (long long)dim, (long long)heads, (long long)dim);
+        bad_shape(t, name, want);
+        return 0;
+    }
+    if (stride_of(t, w, 2) != n) return 0;
+    if (w[n - 1] != 1 && dim > 1) {
+        PyErr_Format(PyExc_ValueError, "%s must be contiguous in its last dimension", name);
+        return 0;
+    }
+    *stride = n == 2 ? w[0] : 0;
+    void *a;
+    if (!address_of(t, &a)) return 0;
+    *p = (const float *)a;
+    return 1;
+}
+
+static int epsilon(PyObject *v, float *eps)
+{
+    const double e = PyFloat_AsDouble(v);
+    if (e == -1.0 && PyErr_Occurred()) return 0;
+    if (!(e >= 0.0 && e <= 3e38)) {
+        PyErr_SetString(PyExc_ValueError, "eps must be finite and not negative");
+        return 0;
+    }
+    *eps = (float)e;
+    return 1;
 }
 
 /* The handle of the call's stream: the given one's, or the current one of the tensors' device, which has to be
@@ -490,6 +592,165 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
     Py_END_ALLOW_THREADS return result("q4k_paged_attention", st, out);
 }
 
+/* q, k, pos, table, q_weight, k_weight, q_out, k_out, eps, interleaved, out_dtype, stream, pdl */
+static PyObject *norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Rows x, y;
+    q4k_norm_rope_args r;
+    void *stream;
+    int dev = -1;
+    memset(&r, 0, sizeof r);
+    if (!wants(n, 13) || !rows(a[0], "q", -1, -1, -1, &dev, &x) || !turn(a[3], x.d, &dev, &r.table, &r.table_rows, &r.rot)) return NULL;
+    if (r.rot && a[2] == Py_None) {
+        PyErr_SetString(PyExc_ValueError, "pos is needed with a table");
+        return NULL;
+    }
+    if (!array_or_none(a[2], "pos", g_int32, x.n, &dev, (void **)&r.pos) || !stream_of(a[11], dev, &stream) || !epsilon(a[8], &r.eps))
+        return NULL;
+    const int inter = PyObject_IsTrue(a[9]), pdl = PyObject_IsTrue(a[12]);
+    if (inter < 0 || pdl < 0) return NULL;
+    r.tokens = x.n, r.dim = x.d, r.interleaved = inter, r.flags = pdl ? Q4K_FLAG_PDL : 0;
+    PyObject *out[2] = {NULL, NULL};
+    q4k_heads *to[2] = {&r.q, &r.k};
+    const int two = a[1] != Py_None;
+    if (!two && (a[5] != Py_None || a[7] != Py_None)) {
+        PyErr_SetString(PyExc_ValueError, "k_weight or k_out without k");
+        return NULL;
+    }
+    for (int i = 0; i <= two; ++i) {
+        q4k_heads *h = to[i];
+        if ((i && !rows(a[1], "k", r.tokens, -1, r.dim, &dev, &x)) ||
+            !weight(a[4 + i], i ? "k_weight" : "q_weight", x.h, x.d, &dev, &h->weight, &h->weight_head_stride) ||
+            !(out[i] = output(a[6 + i], i ? "k_out" : "q_out", a[i], &x, a[10], a[11], &dev, &y))) {
+            Py_XDECREF(out[0]);
+            return NULL;
+        }
+        h->x = x.p, h->y = y.p, h->heads = x.h, h->x_type = x.code, h->y_type = y.code;
+        h->x_token_stride = x.st, h->x_head_stride = x.sh, h->y_token_stride = y.st, h->y_head_stride = y.sh;
+    }
+    q4k_status st;
+    Py_BEGIN_ALLOW_THREADS st = g_norm_rope(&r, stream);
+    Py_END_ALLOW_THREADS
+    if (!two) {
+        out[1] = Py_None;
+        Py_INCREF(out[1]);
+    }
+    PyObject *both = PyTuple_Pack(2, out[0], out[1]);
+    Py_DECREF(out[0]);
+    Py_DECREF(out[1]);
+    return both ? result("q4k_norm_rope", st, both) : NULL;
+}
+
+/* k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, table, interleaved, pos, q, q_out, q_dtype, q_weight,
+ * k_weight, eps, stream, pdl */
+static PyObject *kv_append8(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Rows k, v, q, o;
+    q4k_paged_cache8 c;
+    q4k_append8_args r8;
+    q4k_append_args *r = &r8.a;
+    void *stream;
+    int dev = -1;
+    memset(&r8, 0, sizeof r8);
+    if (!wants(n, 20) || !rows(a[0], "k", -1, -1, -1, &dev, &k) || !rows(a[1], "v", k.n, k.h, k.d, &dev, &v)) return NULL;
+    if (v.code != k.code) {
+        PyErr_SetString(PyExc_TypeError, "k and v must have the same dtype");
+        return NULL;
+    }
+    if (!cache8(a + 2, k.n, &dev, &c)) return NULL;
+    if (c.cache.heads != k.h || c.cache.dim != k.d) {
+        PyErr_Format(PyExc_ValueError, "the cache holds %lld heads of %lld, k and v %lld of %lld", (long long)c.cache.heads,
+                     (long long)c.cache.dim, (long long)k.h, (long long)k.d);
+        return NULL;
+    }
+    if (!turn(a[9], k.d, &dev, &r->table, &r->table_rows, &r->rot) || !array_or_none(a[11], "pos", g_int32, k.n, &dev, (void **)&r->pos) ||
+        !weight(a[16], "k_weight", k.h, k.d, &dev, &r8.k_weight, &r8.k_weight_head_stride) || !epsilon(a[17], &r8.eps) ||
+        !stream_of(a[18], dev, &stream))
+        return NULL;
+    const int inter = PyObject_IsTrue(a[10]), pdl = PyObject_IsTrue(a[19]);
+    if (inter < 0 || pdl < 0) return NULL;
+    PyObject *out = NULL;
+    if (a[12] != Py_None) {
+        if (!rows(a[12], "q", k.n, -1, k.d, &dev, &q) ||
+            !weight(a[15], "q_weight", q.h, q.d, &dev, &r8.q_weight, &r8.q_weight_head_stride))
+            return NULL;
+        out = output(a[13], "q_out", a[12], &q, a[14], a[18], &dev, &o);
+        if (!out) return NULL;
+        r->q = q.p, r->q_out = o.p, r->q_heads = q.h;
+        r->q_token_stride = q.st, r->q_head_stride = q.sh, r->q_out_token_stride = o.st, r->q_out_head_stride = o.sh;
+        r->q_type = q.code, r->q_out_type = o.code;
+    } else {
+        if (a[13] != Py_None || a[15] != Py_None) {
+            PyErr_SetString(PyExc_ValueError, "q_out or q_weight without q");
+            return NULL;
+        }
+        out = Py_None;
+        Py_INCREF(out);
+    }
+    r->k = k.p, r->v = v.p;
+    r->k_token_stride = k.st, r->k_head_stride = k.sh, r->v_token_stride = v.st, r->v_head_stride = v.sh;
+    r->kv_type = k.code, r->interleaved = inter, r->flags = pdl ? Q4K_FLAG_PDL : 0;
+    q4k_status st;
+    Py_BEGIN_ALLOW_THREADS st = g_append8(&c, &r8, stream);
+    Py_END_ALLOW_THREADS return result("q4k_kv_append8", st, out);
+}
+
+/* k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, tokens, k, v, dtype, stream, pdl */
+static PyObject *kv_read8(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Rows like, y[2];
+    q4k_paged_cache8 c;
+    q4k_read8_args r;
+    void *stream;
+    int dev = -1;
+    memset(&r, 0, sizeof r);
+    if (!wants(n, 13)) return NULL;
+    const int64_t tokens = PyLong_AsLongLong(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    if (tokens < 0) {
+        PyErr_SetString(PyExc_ValueError, "tokens must not be negative");
+        return NULL;
+    }
+    if (!cache8(a, tokens, &dev, &c) || !stream_of(a[11], dev, &stream)) return NULL;
+    const int pdl = PyObject_IsTrue(a[12]);
+    if (pdl < 0) return NULL;
+    /* (a code of no row type: a new output is made with its own) */
+    like.n = tokens, like.h = c.cache.heads, like.d = c.cache.dim, like.st = like.sh = 0, like.code = -1;
+    PyObject *out[2] = {NULL, NULL};
+    for (int i = 0; i < 2; ++i)
+        if (!(out[i] = output(a[8 + i], i ? "v" : "k", a[i], &like, a[10], a[11], &dev, &y[i]))) {
+            Py_XDECREF(out[0]);
+            return NULL;
+        }
+    if (y[0].code != y[1].code) {
+        PyErr_SetString(PyExc_TypeError, "k and v must have the same dtype");
+        Py_DECREF(out[0]);
+        Py_DECREF(out[1]);
+        return NULL;
+    }
+    r.k = y[0].p, r.v = y[1].p, r.type = y[0].code, r.flags = pdl ? Q4K_FLAG_PDL : 0;
+    r.k_token_stride = y[0].st, r.k_head_stride = y[0].sh, r.v_token_stride = y[1].st, r.v_head_stride = y[1].sh;
+    q4k_status st;
+    Py_BEGIN_ALLOW_THREADS st = g_read8(&c, &r, stream);
+    Py_END_ALLOW_THREADS
+    PyObject *both = PyTuple_Pack(2, out[0], out[1]);
+    Py_DECREF(out[0]);
+    Py_DECREF(out[1]);
+    return both ? result("q4k_kv_read8", st, both) : NULL;
+}
+
+/* int8, float8_e4m3fn, and the addresses of q4k_norm_rope, q4k_kv_append8, q4k_kv_read8 (after setup). */
+static PyObject *setup8(PyObject *self, PyObject *args)
+{
+    PyObject *o[2];
+    unsigned long long f[3];
+    if (!PyArg_ParseTuple(args, "OOKKK", &o[0], &o[1], &f[0], &f[1], &f[2])) return NULL;
+    for (int i = 0; i < 2; ++i) Py_INCREF(o[i]);   /* kept */
+    g_int8 = o[0], g_e4m3 = o[1];
+    g_norm_rope = (norm_rope_fn)(uintptr_t)f[0], g_append8 = (append8_fn)(uintptr_t)f[1], g_read8 = (read8_fn)(uintptr_t)f[2];
+    Py_RETURN_NONE;
+}
+
 /* Tensor, float32, float16, bfloat16, int32, empty, empty_like, new_on(stream, shape, dtype, device), current device, current stream's handle of a device, raise(fn, status),
  * and the addresses of q4k_rope, q4k_kv_append, q4k_paged_attention. */
 static PyObject *setup(PyObject *self, PyObject *args)
@@ -514,6 +775,10 @@ static PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, "What the calls need of torch and of the library."},
     {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, "q4k_rope"},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, "q4k_kv_append"},
+    {"setup8", setup8, METH_VARARGS, "The same of an 8-bit cache's calls."},
+    {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "q4k_norm_rope"},
+    {"kv_append8", (PyCFunction)(void (*)(void))kv_append8, METH_FASTCALL, "q4k_kv_append8"},
+    {"kv_read8", (PyCFunction)(void (*)(void))kv_read8, METH_FASTCALL, "q4k_kv_read8"},
     {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, "q4k_paged_attention"},
     {NULL, NULL, 0, NULL}};
 
