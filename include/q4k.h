@@ -667,6 +667,23 @@ typedef struct {
 
 q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream);
 
+/*
+ * q4k_paged_attention over an 8-bit cache: the same masks, scores and outputs, with
+ * scale * code for every key and value.  The codes are multiplied as they are (exact
+ * in fp16); keys' scales enter the scores, values' the softmax weights, in fp32.
+ * Precision: with 16-bit q and out, q enters as fp16 over a power of two per row (bf16
+ * values below 2^-38 of the row's largest lose bits) and the weights, with their
+ * values' scales, are rounded once to fp16 (2^-11 at most); with fp32 q or out, or a
+ * softcap above 256, both enter as two fp16 parts (22 bits).  A weight times its value's
+ * scale counts to 2^-38 of the largest scale of the values that its tile meets.  The
+ * rest is in fp32.
+ * Slots that no token of a sequence's query tile sees may hold anything, their scales
+ * too.  A block whose scale a token sees must have one that is finite.
+ *   dim a multiple of 16 up to 256; k and v 16-byte aligned, with strides that keep
+ *   every row 16-byte aligned; everything else, scratch among it, as q4k_paged_attention.
+ */
+q4k_status q4k_paged_attention8(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream);
+
 /* Launch plan the automatic heuristics pick for a shape (for tests and
  * reports): out[0] = split_k, out[1] = number of CTAs, out[2] = rows per CTA
  * tile, out[3] = K blocks per x chunk held in shared memory. */
@@ -677,7 +694,7 @@ q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4]);
  * kernel (Q4_K or Q6_K) or the streaming probe timed out, bit 1 = the same in the prefill
  * kernel; the kernel then wound down early and its outputs are invalid;
  * bit 2 = an index array of q4k_rope, q4k_norm_rope, q4k_kv_append(8), q4k_kv_read8
- * or q4k_paged_attention points outside its buffers; bit 3 = a bounded wait in q4k_paged_attention.
+ * or q4k_paged_attention(8) points outside its buffers; bit 3 = a bounded wait in q4k_paged_attention(8).
  * 0 = no error.  The bits stay set until q4k_device_error_clear(). */
 unsigned int q4k_device_error_flags(void);
 

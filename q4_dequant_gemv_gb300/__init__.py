@@ -50,7 +50,7 @@ EXPORTS = ("q4k_status_string", "q4k_abi_version", "q4k_gemv", "q4k_gemv_argmax"
            "q4k_device_error_flags", "q4k_device_error_clear", "q4k_stream_read", "q6k_gemv",
            "q6k_planar_bytes", "q6k_repack_planar", "q6k_gemv_planar",
            "q4k_rope_table", "q4k_rope", "q4k_kv_append", "q4k_paged_attention",
-           "q4k_norm_rope", "q4k_kv_append8", "q4k_kv_read8")
+           "q4k_norm_rope", "q4k_kv_append8", "q4k_kv_read8", "q4k_paged_attention8")
 
 
 def lib():
@@ -104,8 +104,9 @@ def lib():
         L.q4k_norm_rope.argtypes = [ctypes.c_char_p, P]
         L.q4k_kv_append8.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
         L.q4k_kv_read8.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
+        L.q4k_paged_attention8.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
         for f in (L.q4k_rope_table, L.q4k_rope, L.q4k_kv_append, L.q4k_paged_attention, L.q4k_norm_rope, L.q4k_kv_append8,
-                  L.q4k_kv_read8):
+                  L.q4k_kv_read8, L.q4k_paged_attention8):
             f.restype = I
         _lib = L
         return L
@@ -337,7 +338,7 @@ def __getattr__(name):
         from . import _attention
         globals()[name] = f = getattr(_attention, name)
         return f
-    if name in ("norm_rope", "kv_append8", "kv_read8"):
+    if name in ("norm_rope", "kv_append8", "kv_read8", "paged_attention8"):
         from . import _cache8
         globals()[name] = f = getattr(_cache8, name)
         return f

@@ -1,5 +1,5 @@
-"""The paged cache in 8 bits and what stands beside it: q4k_norm_rope, q4k_kv_append8, q4k_kv_read8 (include/q4k.h says
-what each computes; csrc/q4k_marshal.c checks their arguments and calls the library).
+"""The paged cache in 8 bits and what stands beside it: q4k_norm_rope, q4k_kv_append8, q4k_kv_read8 and
+q4k_paged_attention8 (include/q4k.h says what each computes; csrc/q4k_marshal.c checks their arguments and calls the library).
 
 An 8-bit cache is k_cache, v_cache [pages, page size, heads, dim] of codes, int8 or float8_e4m3fn (any strides), and
 k_scale, v_scale fp32 [pages, blocks of a page, heads] (any strides): a block is page size / blocks consecutive slots, a
@@ -23,7 +23,8 @@ def _load():
     m = _attention._calls or _attention._load()
     L = lib()
     m.setup8(torch.int8, torch.float8_e4m3fn, *(ctypes.cast(f, ctypes.c_void_p).value
-                                                for f in (L.q4k_norm_rope, L.q4k_kv_append8, L.q4k_kv_read8)))
+                                                for f in (L.q4k_norm_rope, L.q4k_kv_append8, L.q4k_kv_read8,
+                                                          L.q4k_paged_attention8)))
     _calls = m
     return m
 
@@ -56,3 +57,16 @@ def kv_read8(k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, 
         dtype = next((t.dtype for t in (k, v) if t is not None), torch.bfloat16)
     return (_calls or _load()).kv_read8(k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, tokens, k, v, dtype,
                                         stream, pdl)
+
+
+def paged_attention8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, out=None, *, scale=None,
+                     out_dtype=None, softcap: float = 0.0, slopes=None, window: int = 0, causal: bool = True, prefix_len=None,
+                     kv_start=None, lse=None, stream=None, pdl: bool = False, wait_limit_us: int = 0, test_stall: bool = False,
+                     form=None):
+    """paged_attention over an 8-bit cache (all options as there; dim a multiple of 16)."""
+    if form not in _attention._FORMS:
+        raise ValueError(f"form must be one of {list(_attention._FORMS)}")
+    return (_calls or _load()).paged_attention8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, out, scale,
+                                                out_dtype, softcap, slopes, window, causal, prefix_len, kv_start, lse, stream,
+                                                (1 if pdl else 0) | (8 if test_stall else 0) | _attention._FORMS[form] << 8,
+                                                wait_limit_us)

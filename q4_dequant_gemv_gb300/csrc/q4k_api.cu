@@ -114,6 +114,11 @@ q4k_status q4k_kv_append8(const q4k_paged_cache8 *c, const q4k_append8_args *a, 
     return q4k::kv_append8_impl(c, a, stream);
 }
 
+q4k_status q4k_paged_attention8(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream)
+{
+    return q4k::paged_attention8_impl(c, a, stream);
+}
+
 q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream)
 {
     return q4k::kv_read8_impl(c, a, stream);

@@ -84,23 +84,24 @@ static cudaError_t room_of(int dev, const int (**room)[kMaxCluster + 1])
     return once(dev, [&] { return clusters_at_once(n[dev]); });
 }
 
-bool encode_cache(CacheMaps *maps, const Args &a, int type, int box)
+bool encode_cache(CacheMaps *maps, const Args &a, int type, int box, int width)
 {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     auto one = [&](CUtensorMap *map, const void *base, int64_t page, int64_t slot, int64_t head) {
         // a stride that no index uses may be anything; the encoder wants a legal one
-        const int64_t row = (a.dim + 7) / 8 * 8;
+        const int64_t row = eight(type) ? (a.dim + 15) / 16 * 16 : (a.dim + 7) / 8 * 8, size = eight(type) ? 1 : 2;
         if (a.kv_heads == 1) head = row;
         if (a.pages == 1) page = row;
         cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.page_size),
                               static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.pages)};
-        cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot) * 2, static_cast<cuuint64_t>(head) * 2,
-                                 static_cast<cuuint64_t>(page) * 2};
-        cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
-        return enc(map, type == Q4K_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+        cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot * size), static_cast<cuuint64_t>(head * size),
+                                 static_cast<cuuint64_t>(page * size)};
+        cuuint32_t boxes[4] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+        return enc(map, eight(type) ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : type == Q4K_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                    const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   width * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     return one(&maps->k, a.k, a.k_page, a.k_slot, a.k_head) && one(&maps->v, a.v, a.v_page, a.v_slot, a.v_head);
@@ -273,14 +274,14 @@ cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, 
 
 }  // namespace attn
 
-q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)
+// The call over a cache of 16 bits, or (c8) of 8; its own checks have said `st` and both
+// hold the strides that count.
+static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache8 *c8, q4k_status st, const q4k_attention_args *a,
+                                 void *stream)
 {
-    q4k_status st = check_cache(c);
-    if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
-    const q4k_paged_cache used = with_used_strides(*c);
-    c = &used;
+    const int unit = c8 ? 16 : 8;   // elements of 16 bytes of the cache
     auto type_ok = [](int t) { return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16; };
-    if (c->dim % 8 || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
+    if (c->dim % unit || c->dim > 256 || a->q_heads < 1 || a->q_heads > 65536 || a->q_heads % c->heads ||
         !type_ok(a->q_type) || !type_ok(a->out_type) || (a->causal & ~1) || a->window < 0 ||
         !std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.0f ||
         c->tokens * a->q_heads > 0x7FFFFFFF || (a->flags & ~(Q4K_FLAG_PDL | Q4K_FLAG_TEST_STALL | Q4K_FLAG_ATTN_FORM(7))))
@@ -294,8 +295,8 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     const int64_t q_token = used_stride(a->q_token_stride, c->tokens), q_head = used_stride(a->q_head_stride, a->q_heads);
     const int64_t out_token = used_stride(a->out_token_stride, c->tokens), out_head = used_stride(a->out_head_stride, a->q_heads);
     if (off16(c->k) || off16(c->v) || off16(a->q) || off16(a->out) || off4(a->lse) || off4(a->slopes) ||
-        off4(a->prefix_len) || off4(a->kv_start) || c->k_page_stride % 8 || c->k_slot_stride % 8 ||
-        c->k_head_stride % 8 || c->v_page_stride % 8 || c->v_slot_stride % 8 || c->v_head_stride % 8 ||
+        off4(a->prefix_len) || off4(a->kv_start) || c->k_page_stride % unit || c->k_slot_stride % unit ||
+        c->k_head_stride % unit || c->v_page_stride % unit || c->v_slot_stride % unit || c->v_head_stride % unit ||
         q_token % qn || q_head % qn || out_token % on || out_head % on)
         return Q4K_ERR_MISALIGNED;
     int sms = 0;
@@ -327,6 +328,12 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
     p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
     p.dim = static_cast<int>(c->dim), p.q_type = a->q_type, p.out_type = a->out_type, p.causal = a->causal;
+    if (c8) {
+        p.ks = c8->k_scale, p.vs = c8->v_scale;
+        p.ks_page = c8->k_scale_page_stride, p.ks_block = c8->k_scale_block_stride, p.ks_head = c8->k_scale_head_stride;
+        p.vs_page = c8->v_scale_page_stride, p.vs_block = c8->v_scale_block_stride, p.vs_head = c8->v_scale_head_stride;
+        while ((int64_t{1} << p.block_shift) < c8->block) ++p.block_shift;
+    }
     p.wait_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 2000000000ull;
     p.stall = (a->flags & Q4K_FLAG_TEST_STALL) != 0;
     p.pdl = (a->flags & Q4K_FLAG_PDL) != 0;
@@ -338,7 +345,8 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
     // 16-bit calls form cap tanh(s / cap) as cap (1 - 2 / (exp + 1)), off by 2^-22 of the cap:
     // at 256 an eighth of what rounding a weight to fp16 may cost.  Larger caps take the
     // kernels of fp32 calls, whose tanh is good to a few ulp of itself.
-    l.parts_many = a->q_type != c->type || a->out_type == Q4K_F32 || p.softcap > 256.0f;
+    // (Codes meet the queries as fp16, whatever 16-bit type those have.)
+    l.parts_many = (c8 ? a->q_type == Q4K_F32 : a->q_type != c->type) || a->out_type == Q4K_F32 || p.softcap > 256.0f;
     // The tcgen05 kernel takes q of the cache's type, a 16-bit out and pages that split into
     // boxes of 16 slots or more.  Its TMA boxes also ask for positive strides and
     // groups of 256 heads at most, its maxima for a scale that is not negative.
@@ -351,8 +359,8 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
                          (c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head));
     const int (*room)[attn::kMaxCluster + 1];
     if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
-    const int parts = !l.parts_many ? 1 : c->type == Q4K_F16 ? 2 : 3;
-    l.choice = attn::choose(p, *room, sms, parts, !l.parts_many && c->dim <= 128 && l.boxes && queries,
+    const int parts = !l.parts_many ? 1 : c->type == Q4K_BF16 ? 3 : 2;
+    l.choice = attn::choose(p, *room, sms, parts, !c8 && !l.parts_many && c->dim <= 128 && l.boxes && queries,
                             static_cast<int>(a->flags >> 8 & 7));
     if (!l.choice.chunk && !l.choice.rows) return Q4K_ERR_INVALID_ARG;
     cudaError_t e;
@@ -360,11 +368,29 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
         const attn::ChunkLaunch ch{p, l.device, sms, l.stream};
         e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {
-        auto rows = c->type == Q4K_F16 ? (p.docs() ? attn::launch_rows_docs_f16 : attn::launch_rows_f16)
+        auto rows = c->type == Q4K_I8     ? (p.docs() ? attn::launch_rows_docs_i8 : attn::launch_rows_i8)
+                    : c->type == Q4K_E4M3 ? (p.docs() ? attn::launch_rows_docs_e4m3 : attn::launch_rows_e4m3)
+                    : c->type == Q4K_F16 ? (p.docs() ? attn::launch_rows_docs_f16 : attn::launch_rows_f16)
                                        : (p.docs() ? attn::launch_rows_docs_bf16 : attn::launch_rows_bf16);
         e = rows(l);
     }
     return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+}
+
+q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)
+{
+    const q4k_status st = check_cache(c);
+    if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
+    const q4k_paged_cache used = with_used_strides(*c);
+    return attention_over(&used, nullptr, st, a, stream);
+}
+
+q4k_status paged_attention8_impl(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream)
+{
+    const q4k_status st = check_cache8(c);
+    if (st == Q4K_ERR_INVALID_ARG || !a) return Q4K_ERR_INVALID_ARG;
+    const q4k_paged_cache8 used = with_used_strides(*c);
+    return attention_over(&used.cache, &used, st, a, stream);
 }
 
 }  // namespace q4k

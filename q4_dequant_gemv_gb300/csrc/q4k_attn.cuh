@@ -67,6 +67,9 @@ struct Args {
     float *part;           // partial results: two slots per CTA
     struct Joint *joint;   // the split tile that starts in each CTA's share
     unsigned int *error;   // the sticky error word
+    const float *ks, *vs;  // 8-bit caches: scales of keys and values, their strides in elements
+    int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
+    int block_shift;       // a scale's slots = 1 << block_shift
     uint64_t wait_ns;      // bound of each wait
     int stall;             // (tests) the first copy of a CTA is awaited for 16 bytes too many
     bool pdl;              // launched as a programmatic dependent
@@ -488,8 +491,12 @@ struct Attributes {
     }
 };
 
-// Host: the maps of a call's cache with boxes of `box` slots.
-bool encode_cache(CacheMaps *maps, const Args &a, int type, int box);
+// Whether a cache holds 8-bit codes.
+constexpr bool eight(int type) { return type == Q4K_I8 || type == Q4K_E4M3; }
+
+// Host: the maps of a call's cache with boxes of `box` slots by `width` elements (64
+// of 16 bits; 64 or 128 of 8: rows of as many bytes, swizzled as wide).
+bool encode_cache(CacheMaps *maps, const Args &a, int type, int box, int width = 64);
 // The queries as [token][head][d]: boxes of `tokens` tokens by a group's heads by 64 elements.
 bool encode_queries(CUtensorMap *map, const Args &a, int type, int tokens);
 

@@ -26,6 +26,16 @@
 // exact in fp32.  fp16: a power of two per query row brings max|q| to 2^14, and
 // P carries 2^14, so the low parts stay above fp16's subnormals.
 //
+// 8-bit caches (CT = Q4K_I8, Q4K_E4M3): codes go through shared memory as they are
+// and become fp16 (exactly) on their way into the fragments; a scale per key and value
+// comes with each slot by 4-byte copies.  Keys' scales multiply the scores.  Values'
+// join P before it is rounded, over a power of two E that no scale of the warp's exceeds
+// by more than 2 (O is rescaled when it grows), so fp16 holds them whatever their size.
+// The MMAs' k axes may run in any order that both operands share: a lane's 16 bytes of
+// a key are four k-steps of it, and 16 bytes of four values' rows are both halves of
+// eight O^T tiles; which key is which row of a block (`row_of`) is chosen so that both
+// reads meet every bank once.
+//
 // Measured (device): one token of 32 / 8 bf16 heads over 131072 positions 90 us,
 // 5.9 TB/s = 89 % of a copy's rate (keys straight into registers 142, rings 97, the
 // join in three trips 94); sixteen fp32 tokens of 28 / 4 heads over 4096 26.4 us (58
@@ -35,7 +45,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "q4k_attn.cuh"
+#include "q4k_cache8.cuh"
 #include "ptx.cuh"
 
 namespace q4k {
@@ -47,15 +60,23 @@ constexpr int kBlock = 16;                   // keys of a ring slot
 // A tile's shape: NT n8 tiles of query rows per warp, RG warps side by side on a
 // block of keys, KG such groups; slots of a group's ring (128 to 192 KB in all,
 // what the queries and the join leave).
-template <int NT, int RG, int DP>
+// 8-bit caches: twice the keys for the bytes, so twice the warps, or slots where the
+// registers are taken.
+template <int CT, int NT, int RG, int DP>
 struct RowsShape {
+    static constexpr bool kEight = eight(CT);
     static constexpr int R = 8 * NT * RG;
-    static constexpr int kWarps = DP == 256 ? 4 : 8;
+    static constexpr bool kTwice = kEight && (NT == 1 || DP == 256);   // twice the warps
+    static constexpr int kWarps = (DP == 256 ? 4 : 8) * (kTwice ? 2 : 1);
     static constexpr int kThreads = kWarps * 32;
     static constexpr int KG = kWarps / RG;
     static constexpr int kUnit = kBlock * KG;              // keys per unit
-    static constexpr int kSide = kBlock * DP * 2;          // bytes of K (or V) in a slot
-    static constexpr int kSlots = RG == 2 ? (DP == 64 ? 8 : 4) : DP == 64 ? 5 : NT * DP >= 512 ? 2 : 3;
+    static constexpr int kSlots16 = RG == 2 ? (DP == 64 ? 8 : 4) : DP == 64 ? 5 : NT * DP >= 512 ? 2 : 3;
+    static constexpr int kSide = kBlock * DP * (kEight ? 1 : 2);   // bytes of K (or V) in a slot
+    static constexpr int kScales = kEight ? 128 : 0;       // bytes of a slot's scales: 16 keys', 16 values'
+    static constexpr int kSlots = (kEight && !kTwice ? 2 : 1) * kSlots16;
+    static constexpr int kBox = !kEight ? 64 : DP == 64 ? 64 : 128;   // elements of a row of a box
+    static constexpr int kHalf = kBlock * kBox * (kEight ? 1 : 2), kBoxes = DP / kBox;   // bytes of a box, boxes of a side
 };
 
 template <int CT>
@@ -146,16 +167,84 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS])
     }
 }
 
+// Codes of both a block's keys and its values as fp16 pairs.  Keys: four consecutive
+// bytes of a row as two pairs.
+template <int CT>
+__device__ __forceinline__ void key_pairs(uint32_t w, uint32_t &p, uint32_t &q)
+{
+    if constexpr (CT == Q4K_I8) {   // 1024 + (code + 128) is 0x6400 | byte; minus 1152
+        const uint32_t u = w ^ 0x80808080u;
+        p = hsub2_u32(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+        q = hsub2_u32(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+    } else {
+        p = cache8::e4m3_pair(static_cast<uint16_t>(w)), q = cache8::e4m3_pair(static_cast<uint16_t>(w >> 16));
+    }
+}
+
+// Values: bytes 0, 1 (HIGH: 2, 3) of two rows, paired across the rows.
+template <int CT, bool HIGH>
+__device__ __forceinline__ void value_pairs(uint32_t w0, uint32_t w1, uint32_t &p, uint32_t &q)
+{
+    if constexpr (CT == Q4K_I8) {
+        const uint32_t x = __byte_perm(w0, w1, HIGH ? 0x7632 : 0x5410);
+        p = hsub2_u32((x & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+        q = hsub2_u32((x >> 8 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+    } else {
+        const uint32_t x = __byte_perm(w0, w1, HIGH ? 0x7362 : 0x5140);
+        p = cache8::e4m3_pair(static_cast<uint16_t>(x)), q = cache8::e4m3_pair(static_cast<uint16_t>(x >> 16));
+    }
+}
+
+// The row of a block that is row r < 8 of an MMA's keys (r + 8: 8 more): with rows of
+// 128 bytes swizzled by 16, eight lanes' reads of two rows' four chunks (keys) or of
+// four rows' two chunks (values) fall into eight different ones; so they do with 64.
+template <int DP>
+__device__ __forceinline__ constexpr int row_of(int r)
+{
+    if (DP == 64) return ((r >> 1 & 1) | (r >> 2 & 1) << 2) ^ (r & 1 ? 3 : 0);
+    return (r & 6) ^ (r & 1 ? 5 : 0);
+}
+
+// Byte of chunk c (16 bytes) of row r in a box.
+template <int BOX>
+__device__ __forceinline__ constexpr int chunk_at(int r, int c)
+{
+    return BOX == 64 ? r * 64 + ((c ^ (r >> 1 & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// 4 bytes global -> shared, or zeros.
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+
+// A power of two from its exponent (-126 .. 127).
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // P carries 2^shift (see above).
 template <int CT>
 constexpr float rows_shift()
 {
-    return CT == Q4K_F16 ? 14.0f : 0.0f;
+    return CT == Q4K_F16 ? 14.0f : 0.0f;   // (8 bits: within the values' scales, out of O again when the warps join)
 }
 
 template <int CT, int PARTS, int NT, int RG, int DP>
 struct RowsShared {
-    using Sp = RowsShape<NT, RG, DP>;
+    using Sp = RowsShape<CT, NT, RG, DP>;
     static constexpr int R = Sp::R;
     static constexpr int kRed = DP + 4;    // floats of a row of O when the warps join (no bank conflicts)
     // a group's ring; when the warps join it holds the group's O instead
@@ -172,19 +261,22 @@ struct RowsShared {
     float4 sent[R * (DP / 4 + kMaxCluster)];
     float2 stat[kMaxCluster][R];
     unsigned long long full[Sp::KG][Sp::kSlots], empty[Sp::KG][Sp::kSlots];
+    float scales[Sp::KG][Sp::kSlots][Sp::kEight ? 32 : 1];   // (8 bits) of the slots' keys and values
 };
 
 // TMA: slots filled by tensor copies (maps), else by cp.async.  DOCS: causal calls
 // with kv_start, whose tiles may have holes (an instance of its own: the code for
 // them, rarely run, cost calls without them 0.3 to 1 us where it was in one kernel).
 template <int CT, int PARTS, int NT, int RG, int DP, bool TMA, bool DOCS>
-__global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
+__global__ void __launch_bounds__(RowsShape<CT, NT, RG, DP>::kThreads, 1) rows_kernel(const __grid_constant__ CacheMaps maps, const Args a)
 {
     using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
-    using Sp = RowsShape<NT, RG, DP>;
-    constexpr int R = Sh::R, ND = DP / 64, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
+    using Sp = RowsShape<CT, NT, RG, DP>;
+    constexpr bool EIGHT = Sp::kEight;
+    constexpr int FT = EIGHT ? Q4K_F16 : CT;   // the type of the fragments
+    constexpr int R = Sh::R, ND = Sp::kBoxes, KS = DP / 16, WARPS = Sp::kWarps, THREADS = Sp::kThreads, SLOTS = Sp::kSlots;
     constexpr int KG = Sp::KG;
-    constexpr int kHalf = kBlock * 128;      // bytes of 16 rows of 64 elements
+    constexpr int kHalf = Sp::kHalf;         // bytes of 16 rows of a box
     constexpr float kShift = rows_shift<CT>();
     extern __shared__ uint8_t smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -192,7 +284,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
     const int kg = w % KG, rg = w / KG;      // group of keys, half of the rows
 
     if (tid < KG * SLOTS) {
-        mbar_init(smem_u32(&sh.full[0][0] + tid), TMA ? 1 : 32);
+        mbar_init(smem_u32(&sh.full[0][0] + tid), !TMA ? 32 : EIGHT ? 33 : 1);
         mbar_init(smem_u32(&sh.empty[0][0] + tid), RG);
         fence_barrier_init();
         if (TMA && tid == 0) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
@@ -275,6 +367,12 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         auto fill = [&](int i, uint32_t f) {
             const int s = static_cast<int>(f % SLOTS);
             const uint32_t dst = ring + s * 2 * Sp::kSide, bar = smem_u32(&sh.full[kg][s]);
+            // a lane per scale: of the slot's keys, then of its values
+            auto fill_scale = [&](int page, int slot, bool live) {
+                const float *p = lane < 16 ? a.ks + page * a.ks_page + (slot >> a.block_shift) * a.ks_block + head * a.ks_head
+                                           : a.vs + page * a.vs_page + (slot >> a.block_shift) * a.vs_block + head * a.vs_head;
+                copy4(smem_u32(&sh.scales[kg][s][EIGHT ? lane : 0]), p, live);
+            };
             if constexpr (TMA) {
                 if (i > 0 && (i & 31) == 0) look(i), check();
                 int page = __shfl_sync(0xffffffffu, ids, i & 31);
@@ -289,9 +387,14 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                     mbar_arrive_expect_tx(bar, 2 * Sp::kSide + (a.stall && f == 0 ? 16 : 0));
 #pragma unroll
                     for (int h = 0; h < ND; ++h) {
-                        load_box(dst + h * kHalf, &maps.k, 64 * h, slot, head, page, bar);
-                        load_box(dst + Sp::kSide + h * kHalf, &maps.v, 64 * h, slot, head, page, bar);
+                        load_box(dst + h * kHalf, &maps.k, Sp::kBox * h, slot, head, page, bar);
+                        load_box(dst + Sp::kSide + h * kHalf, &maps.v, Sp::kBox * h, slot, head, page, bar);
                     }
+                }
+                if constexpr (EIGHT) {
+                    const int r = lane & 15, key = kb0 + i * Sp::kUnit + r;
+                    fill_scale(page, slot + r, key >= t.from && key < t.hi);
+                    copies_arrive(bar);
                 }
             } else {
                 // lane r < 16 finds row r
@@ -313,19 +416,22 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                     }
                 }
                 const uint32_t some = __ballot_sync(0xffffffffu, seen);
-                constexpr int CPR = DP / 8;      // chunks of a row
+                constexpr int CPR = Sp::kSide / kBlock / 16, CPB = kHalf / kBlock / 16;   // chunks of a row, of a box's row
+                constexpr int EPC = EIGHT ? 16 : 8;                                       // elements of a chunk
 #pragma unroll
                 for (int j = 0; j < kBlock * CPR / 32; ++j) {
                     const int c = (lane + 32 * j) % CPR, r = (lane + 32 * j) / CPR;
                     const int64_t p = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
-                    const bool live = (some >> r & 1) && 8 * c < a.dim;
-                    const uint32_t o = (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    const bool live = (some >> r & 1) && EPC * c < a.dim;
+                    const uint32_t o = c / CPB * kHalf + chunk_at<kHalf / kBlock>(r, c % CPB);
                     // (a dead copy reads nothing; its address stays inside the cache)
-                    const int64_t d = live ? 8 * c : 0;
-                    copy16(dst + o, static_cast<const uint16_t *>(a.k) + p * a.k_page + sl * a.k_slot + head * a.k_head + d, live);
+                    const int64_t d = live ? EPC * c : 0;
+                    using Elem = typename std::conditional<EIGHT, uint8_t, uint16_t>::type;
+                    copy16(dst + o, static_cast<const Elem *>(a.k) + p * a.k_page + sl * a.k_slot + head * a.k_head + d, live);
                     copy16(dst + Sp::kSide + o,
-                           static_cast<const uint16_t *>(a.v) + p * a.v_page + sl * a.v_slot + head * a.v_head + d, live);
+                           static_cast<const Elem *>(a.v) + p * a.v_page + sl * a.v_slot + head * a.v_head + d, live);
                 }
+                if constexpr (EIGHT) fill_scale(page, slot, seen);
                 copies_arrive(bar);
             }
         };
@@ -340,8 +446,9 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
 
         // ---- loads on their way: pages, queries (a warp per row), then the first slots
         if constexpr (TMA) look(0);
-        constexpr int PER = R / WARPS;   // rows of a warp: w, w + WARPS, ..
-        static_assert(PER * WARPS == R, "whole rows per warp");
+        constexpr int PER = (R + WARPS - 1) / WARPS;   // rows of a warp: w, w + WARPS, ..
+        constexpr bool WHOLE = PER * WARPS == R;       // (else some warps have none)
+        static_assert(WHOLE || PER == 1, "whole rows per warp");
         float x[PER][DP / 32];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
@@ -372,6 +479,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int r = w + k * WARPS;
+            if (!WHOLE && r >= R) break;
             const bool live = r < t.rows;
             int hq;
             const int tok = token_of(r, hq);
@@ -379,7 +487,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) mx = fmaxf(mx, fabsf(x[k][c]));
             int e = 0;
-            if (PARTS > 1 && CT == Q4K_F16) {   // max|q| to [2^14, 2^15)
+            if ((PARTS > 1 && CT == Q4K_F16) || EIGHT) {   // max|q| to [2^14, 2^15)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const uint32_t b = __float_as_uint(mx);
@@ -393,10 +501,17 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 float v = x[k][c] * up;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
-                    const uint32_t h = pack2(v, 0.0f, CT);
-                    reinterpret_cast<uint16_t *>(&sh.q[p][r >> 3][c][4 * (r & 7) + ((lane >> 1) & 3)])
-                        [2 * (lane >> 3) + (lane & 1)] = static_cast<uint16_t>(h & 0xFFFFu);
-                    v -= unpack2(h, CT).x;
+                    const uint32_t h = pack2(v, 0.0f, FT);
+                    if constexpr (EIGHT) {
+                        // d = 64 s + 16 t + 4 i + 2 j + b: half b of word 2 (i % 2) + j of step pair 2 s + i / 2, lane 4 (r % 8) + t
+                        const int d = 32 * c + lane;
+                        reinterpret_cast<uint16_t *>(&sh.q[p][r >> 3][2 * (d >> 6) + (d >> 3 & 1)][4 * (r & 7) + (d >> 4 & 3)])[d & 7] =
+                            static_cast<uint16_t>(h & 0xFFFFu);
+                    } else {
+                        reinterpret_cast<uint16_t *>(&sh.q[p][r >> 3][c][4 * (r & 7) + ((lane >> 1) & 3)])
+                            [2 * (lane >> 3) + (lane & 1)] = static_cast<uint16_t>(h & 0xFFFFu);
+                    }
+                    v -= unpack2(h, FT).x;
                 }
             }
             if (lane == 0) {
@@ -414,7 +529,12 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
         int in_lo = 0, in_hi = 0x7FFFFFFF;   // keys that every live row sees
         for (int r = 0; r < t.rows; ++r) in_lo = max(in_lo, sh.lo[r]), in_hi = min(in_hi, sh.hi[r]);
 
-        float m[NT][2], l[NT][2], o[NT][KS][4];   // o[..][i]: d = 16 i + g (+8), queries 2 t4 (+1)
+        // o[..][i]: d = 16 i + g (+8), queries 2 t4 (+1); 8 bits: d = 128 (i / 8) + 16 g + 2 (i % 8) (+1), or 8 g + 2 i (+1)
+        float m[NT][2], l[NT][2], o[NT][KS][4];
+        // 8 bits: values' scales count over 2^top (at least 2^-112, so that 2^(14 - top) is a number), up to twice that
+        int top = -112;
+        float limit = two_to(-111);
+        const int row0 = row_of<DP>(g);   // the block's rows of this lane's scores: row0 and row0 + 8
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -444,9 +564,11 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 break;
             }
             auto zero_row = [&](int r) {
-                if (lane < 8 * ND)
-                    *reinterpret_cast<uint4 *>(sh.ring[kg] + slot * 2 * Sp::kSide + Sp::kSide + (lane >> 3) * kHalf + r * 128 +
-                                               (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                constexpr int CPB = kHalf / kBlock / 16;   // chunks of a box's row
+                if (lane < CPB * ND)
+                    *reinterpret_cast<uint4 *>(sh.ring[kg] + slot * 2 * Sp::kSide + Sp::kSide + lane / CPB * kHalf + r * (16 * CPB) +
+                                               lane % CPB * 16) = make_uint4(0, 0, 0, 0);
+                if (EIGHT && lane == 0) sh.scales[kg][slot][EIGHT ? 16 + r : 0] = 0.0f;
             };
             if (TMA && (kb < t.from || kb + kBlock > t.hi || holes)) {
                 // rows of V that nothing sees: zero (by every warp that reads them)
@@ -467,6 +589,28 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 // chains of their own: even and odd k-steps (one part), or the parts
                 constexpr int CHAINS = PARTS > 1 ? PARTS : 2;
                 float acc[NT][CHAINS][4] = {};
+                if constexpr (EIGHT) {
+#pragma unroll
+                    for (int b = 0; b < DP / 64; ++b) {
+                        const uint32_t box = kt + b * 64 / Sp::kBox * kHalf;
+                        const int c = 4 * b % (Sp::kBox / 16) + t4;
+                        const uint4 lo = ld_shared16(box + chunk_at<Sp::kBox>(row0, c)), hi = ld_shared16(box + chunk_at<Sp::kBox>(row0 + 8, c));
+                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t k0, k1, k2, k3;
+                            key_pairs<CT>(wl[i], k0, k2);
+                            key_pairs<CT>(wh[i], k1, k3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int p = 0; p < PARTS; ++p) {
+                                    const uint2 q = reinterpret_cast<const uint2 *>(&sh.q[p][rg * NT + nt][2 * b + (i >> 1)][lane])[i & 1];
+                                    mma_t<FT>(acc[nt][PARTS > 1 ? p : i & 1], k0, k1, k2, k3, q.x, q.y);
+                                }
+                        }
+                    }
+                } else
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
                     const int c = 2 * j + kch;
@@ -483,6 +627,11 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
 
                 // (each step over all n8 tiles before the next: their chains run side by side)
                 float s[NT][4];
+                float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};   // of rows row0 and row0 + 8
+                if constexpr (EIGHT) {
+                    const float *sc = sh.scales[kg][slot];
+                    ks[0] = sc[row0], ks[1] = sc[row0 + 8], vs[0] = sc[16 + row0], vs[1] = sc[24 + row0];
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int r0 = 8 * (rg * NT + nt) + 2 * t4;
@@ -499,9 +648,11 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                         } else {
                             x = acc[nt][0][j] + acc[nt][1][j];
                         }
+                        if constexpr (EIGHT) x *= ks[j >> 1];
                         s[nt][j] = x * (j & 1 ? scl.y : scl.x);
                     }
                 }
+                const int key0 = EIGHT ? row0 : g;   // keys of the scores: kb + key0 (+8)
                 if (a.softcap > 0.0f) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -517,7 +668,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + g + 8 * (j >> 1);
+                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + key0 + 8 * (j >> 1);
                             s[nt][j] -= sh.slope[r] * fabsf(static_cast<float>(t.pos0 + sh.pos[r] - key));
                         }
                 }
@@ -526,7 +677,7 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + g + 8 * (j >> 1);
+                            const int r = 8 * (rg * NT + nt) + 2 * t4 + (j & 1), key = kb + key0 + 8 * (j >> 1);
                             if (key < sh.lo[r] || key >= sh.hi[r]) s[nt][j] = -INFINITY;
                         }
                 }
@@ -562,6 +713,24 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                         }
                     }
                 }
+                if constexpr (EIGHT) {
+                    if (__any_sync(0xffffffffu, vs[0] > limit || vs[1] > limit)) {   // a larger scale: O over the new power of two
+                        float most = fmaxf(vs[0], vs[1]);
+#pragma unroll
+                        for (int hop = 4; hop < 32; hop <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, hop));
+                        const int to = min(static_cast<int>(__float_as_uint(most) >> 23) - 126, 122);   // most <= 2^to
+                        const float f = two_to(max(top - to, -126));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int q = 0; q < KS; ++q)
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) o[nt][q][z] *= f;
+                        top = to, limit = two_to(to + 1);
+                    }
+                    const float up = two_to(14 - top);
+                    vs[0] *= up, vs[1] *= up;
+                }
                 uint32_t pb[NT][PARTS][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -571,20 +740,17 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                         const float base = mx[nt][j & 1] == -INFINITY ? 0.0f : mx[nt][j & 1] - kShift;
                         e[j] = ex2(s[nt][j] - base);
                         l[nt][j & 1] += e[j];
+                        if constexpr (EIGHT) e[j] *= vs[j >> 1];
                     }
                     uint32_t p0[PARTS], p1[PARTS];
-                    split2<CT, PARTS>(e[0], e[1], p0);
-                    split2<CT, PARTS>(e[2], e[3], p1);
+                    split2<FT, PARTS>(e[0], e[1], p0);
+                    split2<FT, PARTS>(e[2], e[3], p1);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) pb[nt][p][0] = transpose8(p0[p]), pb[nt][p][1] = transpose8(p1[p]);
                 }
 
                 // ---- O^T
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    const int c = 2 * j + vch;
-                    uint32_t vf[4];
-                    ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
+                auto add_values = [&](int j, const uint32_t (&vf)[4]) {
                     if constexpr (PARTS > 1) {
                         // a block's sum by itself, added to O by an fp32 add: the MMA's own
                         // additions truncate, which over thousands of blocks is a bias
@@ -593,14 +759,52 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                         for (int p = PARTS - 1; p >= 0; --p)   // small parts first
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_t<CT>(sum[nt], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
+                                mma_t<FT>(sum[nt], vf[0], vf[1], vf[2], vf[3], pb[nt][p][0], pb[nt][p][1]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int z = 0; z < 4; ++z) o[nt][j][z] += sum[nt][z];
                     } else {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_t<CT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][0][0], pb[nt][0][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_t<FT>(o[nt][j], vf[0], vf[1], vf[2], vf[3], pb[nt][0][0], pb[nt][0][1]);
+                    }
+                };
+                if constexpr (EIGHT) {
+                    // a lane's rows: MMA keys 2 t4, 2 t4 + 1 and those 8 further
+                    const int v0 = row_of<DP>(2 * t4), v1 = row_of<DP>(2 * t4 + 1);
+#pragma unroll
+                    for (int b = 0; b < ND; ++b) {
+                        constexpr int WORDS = DP == 64 ? 2 : 4;
+                        uint32_t w[4][WORDS];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int row = (z & 1 ? v1 : v0) + 4 * (z & 2);
+                            if constexpr (DP == 64) {
+                                const uint2 v = ld_shared8(vt + chunk_at<64>(row, g >> 1) + 8 * (g & 1));
+                                w[z][0] = v.x, w[z][1] = v.y;
+                            } else {
+                                const uint4 v = ld_shared16(vt + b * kHalf + chunk_at<128>(row, g));
+                                w[z][0] = v.x, w[z][1] = v.y, w[z][WORDS - 2] = v.z, w[z][WORDS - 1] = v.w;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < WORDS; ++i) {
+                            uint32_t vf[4];
+                            value_pairs<CT, false>(w[0][i], w[1][i], vf[0], vf[1]);
+                            value_pairs<CT, false>(w[2][i], w[3][i], vf[2], vf[3]);
+                            add_values(2 * WORDS * b + 2 * i, vf);
+                            value_pairs<CT, true>(w[0][i], w[1][i], vf[0], vf[1]);
+                            value_pairs<CT, true>(w[2][i], w[3][i], vf[2], vf[3]);
+                            add_values(2 * WORDS * b + 2 * i + 1, vf);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        const int c = 2 * j + vch;
+                        uint32_t vf[4];
+                        ldmatrix4_t(vt + (c >> 3) * kHalf + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4), vf);
+                        add_values(j, vf);
                     }
                 }
             }
@@ -634,10 +838,19 @@ __global__ void __launch_bounds__(RowsShape<NT, RG, DP>::kThreads, 1) rows_kerne
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
                 const int q = 8 * (rg * NT + nt) + 2 * t4 + j;
                 if (g == 0) sh.m[kg][q] = m[nt][j], sh.l[kg][q] = l[nt][j];
+                if constexpr (EIGHT) {
+                    const float up = two_to(top - 14);
+                    constexpr int PER = DP == 64 ? 4 : 8;   // tiles of a lane's consecutive elements
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    red[q * Sh::kRed + 16 * i + g] = o[nt][i][j];
-                    red[q * Sh::kRed + 16 * i + 8 + g] = o[nt][i][j + 2];
+                    for (int i = 0; i < KS; i += 2)
+                        *reinterpret_cast<float4 *>(&red[q * Sh::kRed + i / PER * 128 + 2 * PER * g + 2 * (i % PER)]) =
+                            make_float4(o[nt][i][j] * up, o[nt][i][j + 2] * up, o[nt][i + 1][j] * up, o[nt][i + 1][j + 2] * up);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        red[q * Sh::kRed + 16 * i + g] = o[nt][i][j];
+                        red[q * Sh::kRed + 16 * i + 8 + g] = o[nt][i][j + 2];
+                    }
                 }
             }
         __syncthreads();
@@ -737,6 +950,10 @@ cudaError_t launch_rows_f16(const RowsLaunch &l);
 cudaError_t launch_rows_bf16(const RowsLaunch &l);
 cudaError_t launch_rows_docs_f16(const RowsLaunch &l);
 cudaError_t launch_rows_docs_bf16(const RowsLaunch &l);
+cudaError_t launch_rows_i8(const RowsLaunch &l);
+cudaError_t launch_rows_docs_i8(const RowsLaunch &l);
+cudaError_t launch_rows_e4m3(const RowsLaunch &l);
+cudaError_t launch_rows_docs_e4m3(const RowsLaunch &l);
 
 }  // namespace attn
 }  // namespace q4k

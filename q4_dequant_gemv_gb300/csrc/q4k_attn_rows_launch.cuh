@@ -12,14 +12,14 @@ template <int CT, int PARTS, int NT, int RG, int DP, bool TMA, bool DOCS>
 static cudaError_t launch_rows_fill(const RowsLaunch &l)
 {
     using Sh = RowsShared<CT, PARTS, NT, RG, DP>;
-    using Sp = RowsShape<NT, RG, DP>;
+    using Sp = RowsShape<CT, NT, RG, DP>;
     auto kern = rows_kernel<CT, PARTS, NT, RG, DP, TMA, DOCS>;
     Args a = l.args;
     constexpr int R = Sh::R;
     constexpr int kSmem = static_cast<int>(sizeof(Sh)) + 1024;   // room to align the rings to 1024 bytes
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     CacheMaps maps;
-    if (TMA && !encode_cache(&maps, a, CT, kBlock)) return cudaErrorInvalidValue;
+    if (TMA && !encode_cache(&maps, a, CT, kBlock, Sp::kBox)) return cudaErrorInvalidValue;
     a.slots = static_cast<int>(static_cast<int64_t>(a.tokens) * a.group / R) + a.batch;
     const int64_t units = (static_cast<int64_t>(a.capacity) + kBlock - 1) / Sp::kUnit + 1;   // of one tile at most
     static OncePerDevice once;
@@ -76,7 +76,7 @@ static cudaError_t rows_room(int (&n)[kMaxCluster + 1])
     for (int S = 1; S <= kMaxCluster && e == cudaSuccess; ++S) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = static_cast<unsigned>(1024 * S);
-        cfg.blockDim = RowsShape<1, 1, 128>::kThreads;
+        cfg.blockDim = RowsShape<CT, 1, 1, 128>::kThreads;
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;

@@ -34,6 +34,7 @@ q4k_status kv_append_impl(const q4k_paged_cache *c, const q4k_append_args *a, vo
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream);
 q4k_status norm_rope_impl(const q4k_norm_rope_args *a, void *stream);
 q4k_status kv_append8_impl(const q4k_paged_cache8 *c, const q4k_append8_args *a, void *stream);
+q4k_status paged_attention8_impl(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream);
 q4k_status kv_read8_impl(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream);
 // Sizes, types and index pointers of a cache (no device call).
 q4k_status check_cache(const q4k_paged_cache *c);

@@ -25,11 +25,13 @@ static attention_fn g_attention;
 /* The calls of an 8-bit cache come in by themselves (setup8). */
 typedef q4k_status (*norm_rope_fn)(const q4k_norm_rope_args *, void *);
 typedef q4k_status (*append8_fn)(const q4k_paged_cache8 *, const q4k_append8_args *, void *);
+typedef q4k_status (*attention8_fn)(const q4k_paged_cache8 *, const q4k_attention_args *, void *);
 typedef q4k_status (*read8_fn)(const q4k_paged_cache8 *, const q4k_read8_args *, void *);
 static PyObject *g_int8, *g_e4m3;
 static norm_rope_fn g_norm_rope;
 static append8_fn g_append8;
 static read8_fn g_read8;
+static attention8_fn g_attention8;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_device,
     *s_cuda_stream, *k_dtype_device;
 
@@ -538,15 +540,24 @@ static PyObject *kv_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
 
 /* q, k_cache, v_cache, page_table, seq_start, kv_len, out, scale, out_dtype, softcap, slopes, window, causal, prefix_len,
  * kv_start, lse, stream, flags, wait_limit_us */
-static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t n)
+static PyObject *attention(PyObject *const *a, Py_ssize_t n, int bits8)
 {
     Rows q, o;
+    q4k_paged_cache8 c8;
     q4k_paged_cache c;
     q4k_attention_args r;
     void *stream;
     int dev = -1;
     memset(&r, 0, sizeof r);
-    if (!wants(n, 19) || !rows(a[0], "q", -1, -1, -1, &dev, &q) || !cache(a + 1, q.n, &dev, &c)) return NULL;
+    if (!wants(n, 19 + 2 * bits8) || !rows(a[0], "q", -1, -1, -1, &dev, &q)) return NULL;
+    if (bits8) {
+        if (!cache8(a + 1, q.n, &dev, &c8)) return NULL;
+        c = c8.cache;
+    } else if (!cache(a + 1, q.n, &dev, &c)) {
+        return NULL;
+    }
+    PyObject *const q_tensor = a[0];
+    a += 2 * bits8;   /* (the scales' places) */
     if (c.dim != q.d || c.heads < 1 || q.h % c.heads) {
         PyErr_Format(PyExc_ValueError, "the cache holds %lld heads of %lld, q %lld of %lld", (long long)c.heads,
                      (long long)c.dim, (long long)q.h, (long long)q.d);
@@ -581,16 +592,21 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
         if (!address_of(a[15], (void **)&r.lse)) return NULL;
     }
     if (!stream_of(a[16], dev, &stream)) return NULL;
-    PyObject *out = output(a[6], "out", a[0], &q, a[8], a[16], &dev, &o);
+    PyObject *out = output(a[6], "out", q_tensor, &q, a[8], a[16], &dev, &o);
     if (!out) return NULL;
     r.q = q.p, r.out = o.p;
     r.q_token_stride = q.st, r.q_head_stride = q.sh, r.out_token_stride = o.st, r.out_head_stride = o.sh;
     r.q_heads = q.h, r.scale = (float)scale, r.softcap = (float)cap;
     r.q_type = q.code, r.out_type = o.code, r.causal = causal;
     q4k_status st;
-    Py_BEGIN_ALLOW_THREADS st = g_attention(&c, &r, stream);
-    Py_END_ALLOW_THREADS return result("q4k_paged_attention", st, out);
+    Py_BEGIN_ALLOW_THREADS st = bits8 ? g_attention8(&c8, &r, stream) : g_attention(&c, &r, stream);
+    Py_END_ALLOW_THREADS return result(bits8 ? "q4k_paged_attention8" : "q4k_paged_attention", st, out);
 }
+
+static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t n) { return attention(a, n, 0); }
+
+/* The same with k_scale, v_scale behind the caches. */
+static PyObject *paged_attention8(PyObject *self, PyObject *const *a, Py_ssize_t n) { return attention(a, n, 1); }
 
 /* q, k, pos, table, q_weight, k_weight, q_out, k_out, eps, interleaved, out_dtype, stream, pdl */
 static PyObject *norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -739,15 +755,16 @@ static PyObject *kv_read8(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return both ? result("q4k_kv_read8", st, both) : NULL;
 }
 
-/* int8, float8_e4m3fn, and the addresses of q4k_norm_rope, q4k_kv_append8, q4k_kv_read8 (after setup). */
+/* int8, float8_e4m3fn, and the addresses of q4k_norm_rope, q4k_kv_append8, q4k_kv_read8, q4k_paged_attention8 (after setup). */
 static PyObject *setup8(PyObject *self, PyObject *args)
 {
     PyObject *o[2];
-    unsigned long long f[3];
-    if (!PyArg_ParseTuple(args, "OOKKK", &o[0], &o[1], &f[0], &f[1], &f[2])) return NULL;
+    unsigned long long f[4];
+    if (!PyArg_ParseTuple(args, "OOKKKK", &o[0], &o[1], &f[0], &f[1], &f[2], &f[3])) return NULL;
     for (int i = 0; i < 2; ++i) Py_INCREF(o[i]);   /* kept */
     g_int8 = o[0], g_e4m3 = o[1];
     g_norm_rope = (norm_rope_fn)(uintptr_t)f[0], g_append8 = (append8_fn)(uintptr_t)f[1], g_read8 = (read8_fn)(uintptr_t)f[2];
+    g_attention8 = (attention8_fn)(uintptr_t)f[3];
     Py_RETURN_NONE;
 }
 
@@ -779,6 +796,7 @@ static PyMethodDef methods[] = {
     {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "q4k_norm_rope"},
     {"kv_append8", (PyCFunction)(void (*)(void))kv_append8, METH_FASTCALL, "q4k_kv_append8"},
     {"kv_read8", (PyCFunction)(void (*)(void))kv_read8, METH_FASTCALL, "q4k_kv_read8"},
+    {"paged_attention8", (PyCFunction)(void (*)(void))paged_attention8, METH_FASTCALL, "q4k_paged_attention8"},
     {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, "q4k_paged_attention"},
     {NULL, NULL, 0, NULL}};
 
