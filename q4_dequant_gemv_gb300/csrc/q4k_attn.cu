@@ -333,6 +333,7 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
         p.ks_page = c8->k_scale_page_stride, p.ks_block = c8->k_scale_block_stride, p.ks_head = c8->k_scale_head_stride;
         p.vs_page = c8->v_scale_page_stride, p.vs_block = c8->v_scale_block_stride, p.vs_head = c8->v_scale_head_stride;
         while ((int64_t{1} << p.block_shift) < c8->block) ++p.block_shift;
+        p.codes = c->type;
     }
     p.wait_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 2000000000ull;
     p.stall = (a->flags & Q4K_FLAG_TEST_STALL) != 0;
@@ -355,18 +356,20 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
                        (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
     l.boxes = boxes && p.capacity > 0;
+    // (Over 8-bit caches it loads everything itself, whatever the strides.)
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
-                         (c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head));
+                         (c8 || ((c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head))));
+    const bool pieces = c8 ? c->page_size % 16 == 0 && p.capacity > 0 : l.boxes;
     const int (*room)[attn::kMaxCluster + 1];
     if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
     const int parts = !l.parts_many ? 1 : c->type == Q4K_BF16 ? 3 : 2;
-    l.choice = attn::choose(p, *room, sms, parts, !c8 && !l.parts_many && c->dim <= 128 && l.boxes && queries,
+    l.choice = attn::choose(p, *room, sms, parts, !l.parts_many && c->dim <= 128 && pieces && queries,
                             static_cast<int>(a->flags >> 8 & 7));
     if (!l.choice.chunk && !l.choice.rows) return Q4K_ERR_INVALID_ARG;
     cudaError_t e;
     if (l.choice.chunk) {
         const attn::ChunkLaunch ch{p, l.device, sms, l.stream};
-        e = c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
+        e = c8 ? attn::launch_chunk_8(ch) : c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {
         auto rows = c->type == Q4K_I8     ? (p.docs() ? attn::launch_rows_docs_i8 : attn::launch_rows_i8)
                     : c->type == Q4K_E4M3 ? (p.docs() ? attn::launch_rows_docs_e4m3 : attn::launch_rows_e4m3)

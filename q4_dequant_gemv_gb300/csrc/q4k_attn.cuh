@@ -70,6 +70,7 @@ struct Args {
     const float *ks, *vs;  // 8-bit caches: scales of keys and values, their strides in elements
     int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int block_shift;       // a scale's slots = 1 << block_shift
+    int codes;             // Q4K_I8 or Q4K_E4M3
     uint64_t wait_ns;      // bound of each wait
     int stall;             // (tests) the first copy of a CTA is awaited for 16 bytes too many
     bool pdl;              // launched as a programmatic dependent

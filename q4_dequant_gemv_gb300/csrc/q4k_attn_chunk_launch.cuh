@@ -11,7 +11,7 @@ namespace attn {
 template <int CT, int DP, int MODE>
 static cudaError_t launch_chunk_one(const ChunkLaunch &l)
 {
-    using Sh = ChunkShared<DP>;
+    using Sh = ChunkShared<CT, DP>;
     auto kern = chunk_kernel<CT, DP, MODE>;
     Args a = l.args;
     constexpr int R = kChunkRows;
@@ -19,10 +19,10 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     int box = 128;
     while (a.page_size % box) box /= 2;
-    CacheMaps maps;
-    CUtensorMap qmap;
+    CacheMaps maps{};
+    CUtensorMap qmap{};
     const int tokens = R / a.group;   // of a tile
-    if (!encode_cache(&maps, a, CT, box) || !encode_queries(&qmap, a, CT, tokens)) return cudaErrorInvalidValue;
+    if (!eight(CT) && (!encode_cache(&maps, a, CT, box) || !encode_queries(&qmap, a, CT, tokens))) return cudaErrorInvalidValue;
     a.slots = a.tokens / tokens + a.batch;
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
@@ -34,7 +34,7 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     return launch_split(a, l.device, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = kChunkThreads;
+        cfg.blockDim = chunk_threads(CT);
         cfg.dynamicSmemBytes = kSmem;
         cfg.stream = l.stream;
         const Attributes at(&cfg, 0, args.pdl);

@@ -12,7 +12,7 @@ import plain_cache8 as plain8     # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F32, F16, BF16, I8, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
-FORMS = [None, "cluster8", "cluster16", "cluster32", "split8", "split16", "split32"]
+FORMS = [None, "cluster8", "cluster16", "cluster32", "split8", "split16", "split32", "many"]
 
 
 @pytest.fixture(scope="module")
@@ -66,13 +66,37 @@ def _cache(g, lens, page, block, KH, D, ct, first=False, spare=2, spread=1.0):
     return sides, pt
 
 
-def _floor(vs, vc, lens):
+def _floor(vs, vc, lens, many=False):
     """Softmax weights go to fp16 as e s 2^(14 - t), e the weight over the largest, s the value's scale, 2^t at most twice the
     largest scale: below fp16's normal numbers each (and the last part of one in parts) is off by half a step, 2^-25, so
     e s by 2^-39 2^t <= 2^-38 max s, and an output by that times the codes it sums, over a sum of weights of at least 1.
-    (It shows where the keys of large weight have codes of 0.)"""
+    (It shows where the keys of large weight have codes of 0.)  The many-rows form keeps e 2^6 or more, beside values over
+    the largest scale: 2^-31 of it, twice."""
     s = vs[torch.isfinite(vs)]
-    return 2.0 ** -38 * (float(s.max()) if s.numel() else 0.0) * plain8.TOP[vc.dtype] * max(lens)
+    return 2.0 ** (-30 if many else -38) * (float(s.max()) if s.numel() else 0.0) * plain8.TOP[vc.dtype] * max(lens)
+
+
+def _products(q, keys, vals, case, scale, slopes, softcap):
+    """What the many-rows form adds to the bound: keys and values over their units' powers of two are rounded to fp16, the
+    products with a key's scale once (2^-11 of itself), with a value's twice (its scale too), so a score is off by at most
+    2^-11 of its terms' sizes, as much as that the log-sum-exp (returned beside it), and a weight by twice that."""
+    T, H, D = q.shape
+    out, off = torch.zeros(T, H, D, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    for t, (b, p, lo, hi) in enumerate(plain.ranges(case)):
+        if hi <= lo:
+            continue
+        g = H // keys[b].shape[1]
+        k, v = (x[b][lo:hi].repeat_interleave(g, 1) for x in (keys, vals))
+        s = torch.einsum("hd,jhd->hj", q[t].double(), k) * scale
+        size = torch.einsum("hd,jhd->hj", q[t].double().abs(), k.abs()) * abs(scale)
+        if softcap:
+            s = softcap * torch.tanh(s / softcap)
+        if slopes is not None:
+            s = s - slopes.double()[:, None] * (p - torch.arange(lo, hi, dtype=torch.float64)).abs()
+        mag = torch.einsum("hj,jhd->hd", torch.softmax(s, 1), v.abs())
+        off[t] = 2.0 ** -11 * size.amax(1)
+        out[t] = (2 * off[t][:, None] + 2 * 2.0 ** -11) * mag
+    return out, off
 
 
 def _takes(form, qt, ot, D, page, scale, group, cap):
@@ -113,14 +137,16 @@ def _run(q4k, case, H, KH, D, page, block=16, qt=BF16, ct=I8, ot=None, softcap=0
     # the same sums as over a cache of fp16: weights rounded once to fp16, or both in parts of 22 bits
     many = qt == F32 or ot == F32 or softcap > 256
     ref, rl, bound = plain.attention(q, keys, vals, case, scale, softcap, sl, many, F16, ot)
-    bound = bound + _floor(vs, vc, case["len"])
+    chunk = not many and D <= 128 and page % 16 == 0 and form in (None, "many")   # (or may be)
+    bound = bound + _floor(vs, vc, case["len"], chunk) + (more := _products(q, keys, vals, case, scale, sl, softcap) if chunk else (0.0, 0.0))[0]
     err = (out.double().cpu() - ref).abs()
     assert (err <= bound).all(), f"out: worst {float((err / bound).max()):.3g} x the bound"
     dead = torch.isinf(rl)
     got = lse.double().cpu()
     assert torch.equal(dead, torch.isinf(got) & (got < 0))
     assert not out.cpu()[dead].any(), "a row that sees nothing is zero"
-    tol = 2.0 ** -12 + 2.0 ** -20 * rl[~dead].abs()
+    # the scores' own errors (bounded well inside 2^-12 here) and fp32's on the sum
+    tol = 2.0 ** -12 + 2.0 ** -20 * rl[~dead].abs() + (more[1][~dead] if chunk else 0.0)
     assert ((got[~dead] - rl[~dead]).abs() <= tol).all()
     return out, lambda **over: q4k.paged_attention8(*args, **{**kw, **over})
 
@@ -155,14 +181,14 @@ def test_heads_and_dims(q4k, H, KH, D, form):
 @pytest.mark.parametrize("types", [(BF16, I8, BF16), (F32, E4M3, F32)])
 def test_page_sizes(q4k, page, block, first, types):
     for D in (128, 64):
-        for form in (None,):
+        for form in (None, "many"):
             _run(q4k, dict(new=[1, 150, 2], len=[513, 277, 2]), 14, 2, D, page, block, *types, first=first, form=form)
 
 
 @pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 255, 257])
 @pytest.mark.parametrize("past", [0, 1, 100])
 def test_lengths(q4k, n, past):
-    for form in (None,):
+    for form in (None, "many"):
         _run(q4k, dict(new=[n], len=[n + past]), 4, 2, 64, 16, 1, seed=n, form=form)
 
 
@@ -225,7 +251,7 @@ def test_many_tiles(q4k, new, lens, form):
 @pytest.mark.parametrize("std", [1e-3, 40.0])
 @pytest.mark.parametrize("types", [(F32, I8, F32), (BF16, E4M3, BF16)])
 def test_flat_and_peaked_scores(q4k, std, types):
-    for form in (None,):
+    for form in (None, "many"):
         _run(q4k, dict(new=[1, 33], len=[150, 260]), 4, 2, 128, 16, 16, *types, std=std, form=form)
 
 
@@ -234,7 +260,7 @@ def test_flat_and_peaked_scores(q4k, std, types):
 def test_scales(q4k, scale, types):
     """Negative, zero and large scales of the scores, masked rows among them."""
     for new, lens in (([1], [70]), ([90, 3], [200, 40])):
-        for form in (None,):
+        for form in (None, "many"):
             _run(q4k, dict(new=new, len=lens, window=33), 4, 2, 64, 16, 16, *types, scale=scale, form=form)
 
 
@@ -270,7 +296,9 @@ def test_sizes_of_values(q4k, size, form):
         out = q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, pt.cuda(), _dev([0, n]), _dev([lens]), scale=0.1, form=form)
         # fp32's smallest numbers: a value's term below 2^-126 may be lost, at most one for each key and part
         err = (out.double().cpu() - ref).abs()
-        assert (err <= bound + _floor(vs, vc, [lens]) + lens * 2.0 ** -126).all(), f"{float((err / bound).max())} x the bound"
+        many = qt != F32
+        extra = _products(q, keys, vals, case, 0.1, None, 0.0)[0] if many else 0.0
+        assert (err <= bound + extra + _floor(vs, vc, [lens], many) + lens * 2.0 ** -126).all(), f"{float((err / bound).max())} x the bound"
     assert q4k.device_error_flags() == 0
 
 
@@ -305,7 +333,7 @@ def test_nan_codes_that_are_seen(q4k):
     n, lens = 15, 20
     g = torch.Generator().manual_seed(6)
     ((kc, ks, _), (vc, vs, _)), pt = _cache(g, [lens], 16, 1, 1, 64, E4M3)
-    for qt, forms in ((F32, (None,)), (BF16, (None,))):
+    for qt, forms in ((F32, (None,)), (BF16, (None, "many"))):
         q = torch.randn(n, 1, 64, generator=g).to(qt).cuda()
         args = (pt.cuda(), _dev([0, n]), _dev([lens]))
         for form in forms:
@@ -375,9 +403,11 @@ def test_offsets_past_32_bits(q4k, n, qt):
     step = float(torch.tensor(0.02))
     ref, _, bound = plain.attention(q, [k.double() * step], [v.double() * step], dict(new=[n], len=[length]), 0.125,
                                     parts=qt == F32, cache_dtype=F16, out_dtype=qt)
-    for form in (None,) if qt == BF16 else (None,):
+    for form in (None, "many") if qt == BF16 else (None,):
         out = q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, pt.cuda(), _dev([0, n]), _dev([length]), form=form)
-        assert ((out.double().cpu() - ref).abs() <= bound + 2.0 ** -38 * step * 127 * length).all()
+        k8, v8 = [k.double() * step], [v.double() * step]
+        extra = _products(q, k8, v8, dict(new=[n], len=[length]), 0.125, None, 0.0)[0] + 2.0 ** -30 * step * 127 * length
+        assert ((out.double().cpu() - ref).abs() <= bound + (extra if qt == BF16 else 2.0 ** -38 * step * 127 * length)).all()
     k2, v2 = q4k.kv_read8(kc, vc, ks, vs, pt.cuda(), _dev([0, length]), _dev([length]), length, dtype=F32)
     assert torch.equal(k2.cpu(), k.float() * step) and torch.equal(v2.cpu(), v.float() * step)
     assert q4k.device_error_flags() == 0
@@ -479,7 +509,10 @@ def test_chain(q4k, n, qt):
                                     out_dtype=qt)
     # the values read back are rounded to fp32 (2^-24 of themselves, as much in every score)
     size = torch.einsum("hd,jhd->hj", want[0].cpu().double().abs().amax(0), keys[0].double().abs().repeat_interleave(H // KH, 1)).amax() / 8
-    bound = bound + _floor(cache[3], cache[1], lens)
+    bound = bound + _floor(cache[3], cache[1], lens, qt == BF16)
+    if qt == BF16:
+        bound = bound + _products(want[0].cpu(), [t.double() for t in keys], [t.double() for t in vals], dict(new=[n, n], len=lens),
+                                  0.125, None, 0.0)[0]
     assert ((want[1].double().cpu() - ref).abs() <= bound + 2.0 ** -23 * (1 + 2 * size) * max(x.abs().max() for x in vals)).all()
     assert q4k.device_error_flags() == 0
 
