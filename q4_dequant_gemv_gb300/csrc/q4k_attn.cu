@@ -326,7 +326,7 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
     p.softcap = a->softcap > 0.0f ? std::min(std::max(a->softcap, 1e-30f), 1e30f) : 0.0f;
     p.pages = static_cast<int>(c->pages), p.batch = static_cast<int>(c->batch);
     p.tokens = static_cast<int>(c->tokens), p.heads = static_cast<int>(a->q_heads);
-    p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
+    p.lse_heads = p.heads, p.kv_heads = static_cast<int>(c->heads), p.group = static_cast<int>(a->q_heads / c->heads);
     p.dim = static_cast<int>(c->dim), p.q_type = a->q_type, p.out_type = a->out_type, p.causal = a->causal;
     if (c8) {
         p.ks = c8->k_scale, p.vs = c8->v_scale;
@@ -356,10 +356,12 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
                        (c->heads == 1 || (stride_ok(c->k_head_stride) && stride_ok(c->v_head_stride))) &&
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
     l.boxes = boxes && p.capacity > 0;
-    // (Over 8-bit caches it loads everything itself, whatever the strides.)
+    // (Over 8-bit caches the keys and values lie in scratch, and queries that are not fp16; one
+    // head's has to fit it.)
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
-                         (c8 || ((c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head))));
-    const bool pieces = c8 ? c->page_size % 16 == 0 && p.capacity > 0 : l.boxes;
+                         ((c8 && a->q_type != Q4K_F16) || ((c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head))));
+    const bool pieces = c8 ? c->page_size % 16 == 0 && p.capacity > 0 && p.batch < 65535 && attn::widened_bytes(p) <= attn::kWidenMost
+                            : l.boxes;
     const int (*room)[attn::kMaxCluster + 1];
     if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
     const int parts = !l.parts_many ? 1 : c->type == Q4K_BF16 ? 3 : 2;
@@ -369,7 +371,7 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
     cudaError_t e;
     if (l.choice.chunk) {
         const attn::ChunkLaunch ch{p, l.device, sms, l.stream};
-        e = c8 ? attn::launch_chunk_8(ch) : c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
+        e = c8 ? attn::launch_widened(ch) : c->type == Q4K_F16 ? attn::launch_chunk_f16(ch) : attn::launch_chunk_bf16(ch);
     } else {
         auto rows = c->type == Q4K_I8     ? (p.docs() ? attn::launch_rows_docs_i8 : attn::launch_rows_i8)
                     : c->type == Q4K_E4M3 ? (p.docs() ? attn::launch_rows_docs_e4m3 : attn::launch_rows_e4m3)

@@ -61,6 +61,7 @@ struct Args {
     int page_shift;        // page_size = 1 << page_shift, or -1
     float scale, softcap;
     int pages, batch, tokens, heads, kv_heads, group, dim;
+    int lse_heads;         // of a token of lse
     int q_type, out_type, causal;
     int slots;             // upper bound of the tiles per cache head
     int cluster;           // few-rows kernel: CTAs of a cluster that share a tile; 0: the split over all CTAs
@@ -71,6 +72,9 @@ struct Args {
     int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int block_shift;       // a scale's slots = 1 << block_shift
     int codes;             // Q4K_I8 or Q4K_E4M3
+    const float *row_scale;   // (a widened 8-bit cache) of the queries, [tokens][heads], or null
+    const float *factors;     // its factors: [page of 128][head][2][8]
+    int table_pages;          // its pages a sequence
     uint64_t wait_ns;      // bound of each wait
     int stall;             // (tests) the first copy of a CTA is awaited for 16 bytes too many
     bool pdl;              // launched as a programmatic dependent
@@ -403,7 +407,7 @@ __device__ __forceinline__ void finish_row(const Args &a, int64_t tok, int hq, i
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
     store4(a.out, a.out_type, tok * a.out_token + hq * a.out_head + d,
            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    if (a.lse && d == 0) a.lse[tok * a.heads + hq] = ls == 0.0f ? -INFINITY : (m + log2f(ls) - shift) * kLn2;
+    if (a.lse && d == 0) a.lse[tok * a.lse_heads + hq] = ls == 0.0f ? -INFINITY : (m + log2f(ls) - shift) * kLn2;
 }
 
 // Page (index into the sequence's table) and slot of a cached position.

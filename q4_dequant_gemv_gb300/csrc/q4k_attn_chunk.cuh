@@ -32,16 +32,13 @@
 // Slots that nothing of the tile sees may hold NaN: scores are replaced, not
 // added to, and the rows of V outside the tile's keys, or in a hole that a document
 // mask leaves between them, are zeroed in shared memory before they meet P = 0.
-// 8-bit caches (CT = Q4K_I8, for codes of either type): the MMA's operands are fp16
-// all the same, so codes become fp16 on their way into the stages.  Sixteen warps:
-// warp 9 plans, units too (pages, seen keys, scales), some units ahead; warps 10 to 15
-// take groups of 16 keys or values in turn, codes by 16-byte loads into registers one
-// group ahead, converted, scaled and stored where TMA would have put them; at the start
-// of a tile they turn the queries to fp16 over a power of two a row.  A unit's keys and
-// values are over a power of two of its largest scale (128 of it at most), so that fp16
-// holds them: the keys' joins the factor of the scores, the values' the exponents of P
-// (relative to the largest so far, by which O is rescaled).  Per-column factors in the
-// softmax instead would cost it 64 shared loads of 16 bytes a row and unit.
+// A widened 8-bit cache (MODE bit 3; q4k_attn_widen.cu): keys and values are codes, or
+// codes over a power of two, in fp16, in pages of 128 that follow each other; each piece of
+// 16 of them has a factor.  Warp 11 hands the factors of the units on, some ahead.  The
+// keys' multiply the scores, the values' join the exponents of P by their log2, over the
+// largest so far, by which O is rescaled as by a maximum; the sum of a piece loses it
+// again.  Nothing of it costs a score more than it did; the code of its own does not
+// touch the other instances.
 //
 // Every wait is bounded in time: on a timeout the CTA sets bit 3 of the error word,
 // stops, waits (bounded) for its copies and products in flight, frees its tensor
@@ -56,8 +53,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
 #include "q4k_attn.cuh"
 #include "q4k_codes.cuh"
 #include "ptx.cuh"
@@ -67,16 +62,11 @@ namespace attn {
 
 constexpr int kChunkRows = 256;              // query rows of a tile at most
 constexpr int kChunkKeys = 128;              // keys of a unit
-// two softmax warpgroups; MMA, key, value and idle warp, or MMA, planning and six converting warps
-constexpr int chunk_threads(int type) { return eight(type) ? 512 : 384; }
-constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
+constexpr int kChunkThreads = 384;           // two softmax warpgroups; MMA, key, value and idle warp
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kFactorWarp = 11;
 constexpr int kStages = 4;
-// 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch; 8 bits: 256 x 184 +
-// 256 x 72, the 512 x 128 of the launch
-constexpr int softmax_regs(int type) { return eight(type) ? 184 : 200; }
-constexpr int other_regs(int type) { return eight(type) ? 72 : 96; }
-constexpr int kPlanWarp = 9, kFirstConverter = 10, kConverters = 6;
-constexpr int kUnits = 4;                    // units planned ahead
+// 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 
 // A CTA's part of one tile, as the key warp found it.
 struct Work {
@@ -84,34 +74,27 @@ struct Work {
     int head, off, todo, last;   // units [off, off + todo) of the tile; the CTA that holds the tile's last unit
 };
 
-// (8 bits) A unit as the plan warp found it.
-struct alignas(16) UnitInfo {
-    float scale[2][kChunkKeys];              // of the keys and the values, over their powers of two; 0: not seen
-    int page[8], slot[8];                    // of each piece of 16 keys
-    uint32_t seen[kChunkKeys / 32];
-    int head, kind;                          // kind 1: the first of a tile, 2: no more
-    int exponent[2];                         // the powers of two
+// The factors of a unit: of the keys of each piece of 16, of the values as log2.
+struct UnitFactors {
+    float key[8], value[8];
+    int exponent;                            // the values' are at most 2^exponent
 };
-struct Planned {
-    UnitInfo unit[kUnits];
-    float row_scale[2][kChunkRows];          // of a tile's queries, two tiles
-    unsigned long long full[kUnits], empty[kUnits];
-};
-struct NotPlanned {};
+constexpr int kUnitsAhead = 4;
 
-template <int CT, int DP>
+template <int DP>
 struct ChunkShared {
     static constexpr int kHalf = 128 * 128;                    // bytes: 128 rows of 64 elements
     static constexpr int kTile = kHalf * (DP / 64);            // 128 rows of DP elements
     uint8_t q[2 * kTile];                                      // [dim / 64][256 rows][64]
     uint8_t kv[kStages * kTile];
     uint8_t out[8][32 * 64];                                   // a warp's rows on their way out, 32 columns at a time
-    SplitShared<chunk_threads(CT)> plan;
+    SplitShared<kChunkThreads> plan;
     unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2][2], o_done[2], q_full, q_empty, edge, drained;
     unsigned long long work_full[2], work_empty[2];
     Work work[2];
     alignas(16) uint32_t seen[2][kChunkKeys / 32];   // (tiles with holes) of the key and the value warp
-    typename std::conditional<eight(CT), Planned, NotPlanned>::type ahead;
+    unsigned long long factors_full[kUnitsAhead], factors_empty[kUnitsAhead];
+    UnitFactors factors[kUnitsAhead];
     uint32_t tmem;
     int abort;
 };
@@ -289,37 +272,19 @@ constexpr uint32_t chunk_idesc(int n, bool b_mn_major)
 template <int CT>
 constexpr float chunk_shift()
 {
-    return CT == Q4K_BF16 ? 0.0f : 6.0f;
-}
-
-// (8 bits) Sixteen codes as fp16, times hi + lo (KEYS) or hi.
-template <int CODES, bool KEYS>
-__device__ __forceinline__ void convert16(const uint4 &raw, uint32_t hi, uint32_t lo, uint4 &a, uint4 &b)
-{
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        key_pairs<CODES>(w[i], r[2 * i], r[2 * i + 1]);
-#pragma unroll
-        for (int j = 2 * i; j < 2 * i + 2; ++j)   // (the product with hi is rounded once, lo's part before it)
-            r[j] = KEYS ? hfma2_u32(r[j], hi, hmul2_u32(r[j], lo)) : hmul2_u32(r[j], hi);
-    }
-    a = make_uint4(r[0], r[1], r[2], r[3]), b = make_uint4(r[4], r[5], r[6], r[7]);
+    return CT == Q4K_F16 ? 6.0f : 0.0f;
 }
 
 // MODE bit 0: capped scores, bit 1: distance bias, bit 2 (DOCS): a causal call with
 // kv_start, whose tiles may have holes (its code in every instance cost 2048 tokens
-// over 14336 positions 2 %).
+// over 14336 positions 2 %), bit 3: a widened 8-bit cache.
 template <int CT, int DP, int MODE>
-__global__ void __launch_bounds__(chunk_threads(CT), 1)
+__global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ CacheMaps maps, const __grid_constant__ CUtensorMap qmap, const Args a, const int box)
 {
-    using Sh = ChunkShared<CT, DP>;
-    constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64, kOtherRegs = other_regs(CT);
-    constexpr bool EIGHT = eight(CT);
-    constexpr int FT = EIGHT ? Q4K_F16 : CT;   // the type of the products
-    constexpr bool DOCS = MODE & 4;
+    using Sh = ChunkShared<DP>;
+    constexpr int kHalf = Sh::kHalf, kTile = Sh::kTile, ND = DP / 64;
+    constexpr bool DOCS = MODE & 4, WIDE = MODE & 8;
     constexpr float kShift = chunk_shift<CT>();
     constexpr float kLazy = 8.0f;
     extern __shared__ uint8_t smem_raw[];
@@ -334,29 +299,29 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full[i]), EIGHT ? 8 : 1), mbar_init(smem_u32(&sh.empty[i]), 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
             mbar_init(smem_u32(&sh.p_ready[i][0]), 128);
             mbar_init(smem_u32(&sh.p_ready[i][1]), 128);
             mbar_init(smem_u32(&sh.o_done[i]), 1);
             mbar_init(smem_u32(&sh.work_full[i]), 1);
-            mbar_init(smem_u32(&sh.work_empty[i]), EIGHT ? 9 + kConverters : 10);   // the MMA, value (converting) and eight softmax warps
+            mbar_init(smem_u32(&sh.work_empty[i]), WIDE ? 11 : 10);   // the MMA, value (factor) and eight softmax warps
         }
-        mbar_init(smem_u32(&sh.q_full), EIGHT ? kConverters : 1);
-        if constexpr (EIGHT)
-            for (int i = 0; i < kUnits; ++i) mbar_init(smem_u32(&sh.ahead.full[i]), 1), mbar_init(smem_u32(&sh.ahead.empty[i]), kConverters + 8);
+        if constexpr (WIDE)
+            for (int i = 0; i < kUnitsAhead; ++i) mbar_init(smem_u32(&sh.factors_full[i]), 1), mbar_init(smem_u32(&sh.factors_empty[i]), 8);
+        mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.edge), 1);
         mbar_init(smem_u32(&sh.drained), 1);
         fence_barrier_init();
         sh.abort = 0;
     }
-    if (!EIGHT && tid == 32) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v), prefetch_tensormap(&qmap);
+    if (tid == 32) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v), prefetch_tensormap(&qmap);
     tm_fence_before();
     pdl_launch_dependents();
     pdl_wait();   // (everything below may come from the kernel before)
-    Split<kChunkKeys, chunk_threads(CT), kChunkKeys, DOCS> plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
+    Split<kChunkKeys, kChunkThreads, kChunkKeys, DOCS> plan(a, sh.plan, tokens * a.group);   // synchronises the CTA
     plan.scan();
     tm_fence_after();
     const uint32_t tm = sh.tmem;
@@ -400,267 +365,7 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
         return true;
     };
 
-    if (EIGHT && w == kPlanWarp) {
-        if constexpr (EIGHT) {
-        // ------------------------------------------------------------ tiles and units ahead
-        regs_dec<kOtherRegs>();
-        int unit = 0;
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            if (k > 1 && !(ok = wait(sh.work_empty[k & 1], ((k >> 1) - 1) & 1))) break;
-            Work item;
-            item.todo = 0;
-            if (u < u_end) {
-                item.head = static_cast<int>(quotient(u, plan.per_head));
-                if (k == 0 && known) item.t = sh.plan.first, item.off = sh.plan.offset;
-                else item.t = plan.locate(static_cast<uint32_t>(u - static_cast<int64_t>(item.head) * plan.per_head), item.off);
-                item.todo = static_cast<int>(min(static_cast<int64_t>(item.t.units - item.off), u_end - u));
-                item.last = share_owner(total, n, u - item.off + item.t.units - 1);
-                u += item.todo;
-            }
-            if (lane == 0) {
-                sh.work[k & 1] = item;
-                mbar_arrive(smem_u32(&sh.work_full[k & 1]));
-            }
-            __syncwarp();
-            const bool holes = DOCS && (item.t.seq & kHoles);
-            if (DOCS) item.t.seq &= ~kHoles;
-            const Tile &t = item.t;
-            const int32_t *pages = a.page_table + static_cast<int64_t>(t.seq) * a.table_stride;
-            const int kb0 = t.lo + item.off * kChunkKeys;
-            // lane 8 j + p: piece p of unit first + j
-            int ids = 0, slots = 0;
-            auto look = [&](int first) {
-                const int key = kb0 + first * kChunkKeys + 16 * lane;
-                ids = slots = 0;
-                if (first + (lane >> 3) < item.todo && key + 16 > t.from && key < t.hi) {
-                    int e;
-                    page_of(a, key, e, slots);
-                    ids = pages[e];
-                }
-            };
-            // lane: keys 4 lane .. of the unit, in piece lane / 4
-            float sc[2][4];
-            int page = 0, slot = 0;
-            uint32_t seen[kChunkKeys / 32];
-            auto fetch = [&](int i) {
-                if ((i & 3) == 0) look(i);
-                const int kb = kb0 + i * kChunkKeys;
-                page = __shfl_sync(0xffffffffu, ids, 8 * (i & 3) + (lane >> 2));
-                slot = __shfl_sync(0xffffffffu, slots, 8 * (i & 3) + (lane >> 2));
-                if (holes) {
-                    seen_keys(a, t, kb, seen);
-                } else {
-#pragma unroll
-                    for (int z = 0; z < kChunkKeys / 32; ++z) seen[z] = span(t.from - kb - 32 * z, t.hi - kb - 32 * z);
-                }
-                // a piece that some row sees must be in the cache
-                uint32_t mine = 0;   // the word of this lane's keys
-#pragma unroll
-                for (int z = 0; z < kChunkKeys / 32; ++z) mine = (lane >> 3) == z ? seen[z] : mine;
-                const bool bad = (mine >> (16 * (lane >> 2 & 1)) & 0xFFFFu) && (page < 0 || page >= a.pages);
-                const uint32_t lost = __ballot_sync(0xffffffffu, bad);
-                if (lost) {
-                    if (lane == 0) atomicOr(a.error, 4u);
-#pragma unroll
-                    for (int z = 0; z < kChunkKeys / 32; ++z)
-                        seen[z] &= ~((lost >> 8 * z & 1 ? 0xFFFFu : 0u) | (lost >> (8 * z + 4) & 1 ? 0xFFFF0000u : 0u));
-#pragma unroll
-                    for (int z = 0; z < kChunkKeys / 32; ++z) mine = (lane >> 3) == z ? seen[z] : mine;
-                }
-                const float *kp = a.ks + page * a.ks_page + item.head * a.ks_head, *vp = a.vs + page * a.vs_page + item.head * a.vs_head;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int s = slot + 4 * (lane & 3) + z;
-                    const bool live = mine >> (4 * (lane & 7) + z) & 1;
-                    sc[0][z] = live ? kp[(s >> a.block_shift) * a.ks_block] : 0.0f;
-                    sc[1][z] = live ? vp[(s >> a.block_shift) * a.vs_block] : 0.0f;
-                }
-            };
-            if (item.todo > 0) fetch(0);
-            for (int i = 0; i < item.todo + (item.todo == 0 ? 1 : 0); ++i, ++unit) {
-                UnitInfo &info = sh.ahead.unit[unit % kUnits];
-                if (unit >= kUnits && !(ok = wait(sh.ahead.empty[unit % kUnits], (unit / kUnits - 1) & 1))) break;
-                if (item.todo > 0) {
-#pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-                        const float most = fmaxf(fmaxf(fabsf(sc[side][0]), fabsf(sc[side][1])), fmaxf(fabsf(sc[side][2]), fabsf(sc[side][3])));
-                        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 133;
-                        const int x = max(-120, min(115, e));   // the largest to [64, 128)
-                        const float f = two_to(-x);
-                        *reinterpret_cast<float4 *>(&info.scale[side][4 * lane]) =
-                            make_float4(sc[side][0] * f, sc[side][1] * f, sc[side][2] * f, sc[side][3] * f);
-                        if (lane == 0) info.exponent[side] = x;
-                    }
-                    if ((lane & 3) == 0) info.page[lane >> 2] = page, info.slot[lane >> 2] = slot;
-                    if (lane == 0) {
-#pragma unroll
-                        for (int z = 0; z < kChunkKeys / 32; ++z) info.seen[z] = seen[z];
-                    }
-                }
-                if (lane == 0) info.head = item.head, info.kind = item.todo == 0 ? 2 : i == 0 ? 1 : 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.ahead.full[unit % kUnits]));
-                if (i + 1 < item.todo) fetch(i + 1);
-            }
-            if (item.todo == 0) break;
-        }
-        }
-    } else if (EIGHT && w >= kFirstConverter) {
-        if constexpr (EIGHT) {
-        // ------------------------------------------------------------ codes to fp16
-        regs_dec<kOtherRegs>();
-        const int cw = w - kFirstConverter;
-        // a group's loads: this lane's chunk of 16 codes of rows row0 + ROWS j; eight lanes store
-        // four chunks of two neighbouring rows, which the swizzle puts into eight places
-        constexpr int LOADS = DP / 32, ROWS = 16 / LOADS;
-        const int ch = DP == 128 ? (lane & 3) + (lane >> 1 & 4) : lane & 3;
-        const int row0 = DP == 128 ? (lane >> 2 & 1) + (lane >> 3 & 2) : lane >> 2;
-        const bool inside = 16 * ch < a.dim;
-        // a group's rows: where they are, which of them some row of the tile sees
-        const uint8_t *from = nullptr;
-        int64_t step = 0;
-        uint32_t seen = 0;
-        auto aim = [&](const UnitInfo &info, int part) {
-            const int piece = part & 7;
-            const bool values = part >= 8;
-            seen = inside ? info.seen[piece >> 1] >> (16 * (piece & 1) + row0) : 0u;
-            step = values ? a.v_slot : a.k_slot;
-            from = static_cast<const uint8_t *>(values ? a.v : a.k) + info.page[piece] * (values ? a.v_page : a.k_page) +
-                   info.head * (values ? a.v_head : a.k_head) + (info.slot[piece] + row0) * step + 16 * ch;
-            step *= ROWS;
-        };
-        auto load = [&](int j) {
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (seen >> (ROWS * j) & 1) r = __ldg(reinterpret_cast<const uint4 *>(from + j * step));
-            return r;
-        };
-        // the tile's queries: rows of 16 (8) lanes, in fp16 over a power of two
-        auto queries = [&](int k) -> bool {
-            if (!wait(sh.work_full[k & 1], (k >> 1) & 1)) return false;
-            const Work &item = sh.work[k & 1];
-            const int tok0 = item.t.tok0, first = item.t.first, rows = item.t.rows, hq0 = item.head * a.group;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.work_empty[k & 1]));
-            if (k > 0 && !wait(sh.q_empty, (k - 1) & 1)) return false;
-            constexpr int LANES = DP / 8, PER = 32 / LANES, DEEP = 4;
-            const int c = lane % LANES;
-            const uint16_t *q = static_cast<const uint16_t *>(a.q);
-#pragma unroll 1
-            for (int r0 = cw * PER; r0 < kChunkRows; r0 += DEEP * kConverters * PER) {
-                uint4 raw[DEEP];
-#pragma unroll
-                for (int j = 0; j < DEEP; ++j) {
-                    const int r = r0 + j * kConverters * PER + lane / LANES;
-                    raw[j] = make_uint4(0, 0, 0, 0);
-                    if (r < rows && 8 * c < a.dim) {
-                        const uint32_t x = first + r, tok = x / static_cast<uint32_t>(a.group);
-                        raw[j] = __ldg(reinterpret_cast<const uint4 *>(q + (tok0 + tok) * a.q_token + (hq0 + static_cast<int>(x - tok * a.group)) * a.q_head + 8 * c));
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < DEEP; ++j) {
-                    const int r = r0 + j * kConverters * PER + lane / LANES;
-                    const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-                    float mx = 0.0f;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float2 f = unpack2(w4[z], a.q_type);
-                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-#pragma unroll
-                    for (int o = LANES / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-                    const int e = ex != 0 && ex != 255 ? max(-126, min(126, 141 - ex)) : 0;   // max|q| to [2^14, 2^15)
-                    const float up = two_to(e);
-                    uint32_t h[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float2 f = unpack2(w4[z], a.q_type);
-                        h[z] = pack2(f.x * up, f.y * up, Q4K_F16);
-                    }
-                    if (r < kChunkRows) {
-                        *reinterpret_cast<uint4 *>(sh.q + (c >> 3) * 2 * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                        if (c == 0) sh.ahead.row_scale[k & 1][r] = two_to(-e);
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-            return true;
-        };
-        uint4 raw[LOADS];
-        int tile = 0;
-        bool ok = true, more = true;
-        // the first of this warp's groups of a unit: whether there is one, then whether its tile begins there
-        auto begin = [&](int un) -> bool {
-            if (!wait(sh.ahead.full[un % kUnits], (un / kUnits) & 1)) return ok = false;
-            return more = sh.ahead.unit[un % kUnits].kind != 2;
-        };
-        // group g: unit g / 16; its keys' pieces, then its values'
-        int g = cw;
-        (void)begin(0);
-        while (ok && more) {
-            const int un = g >> 4, part = g & 15;
-            const UnitInfo &info = sh.ahead.unit[un % kUnits];
-            if (part < kConverters && info.kind == 1) {   // a tile begins: its queries first
-                if (!(ok = queries(tile++))) break;
-                aim(info, part);
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j) raw[j] = load(j);
-            }
-            const bool values = part >= 8;
-            const int stage = 2 * (un & 1) + (values ? 1 : 0), piece = part & 7;
-            const int next = g + kConverters;
-            const bool last = (next >> 4) != un;   // of this unit's groups
-            // the next group's codes are on their way while this one's are converted (but for a new tile's)
-            bool ahead = !last;
-            if (last && begin(next >> 4)) ahead = sh.ahead.unit[(next >> 4) % kUnits].kind == 0;
-            if (!ok || (un > 1 && !(ok = wait(sh.empty[stage], ((un >> 1) - 1) & 1)))) break;
-            seen = 0;
-            if (ahead) aim(sh.ahead.unit[(next >> 4) % kUnits], next & 15);
-            uint8_t *dst = sh.kv + stage * kTile + (ch >> 2) * kHalf;
-            const float *scales = &info.scale[values][16 * piece + row0];
-            // (one straight line for each kind, so that the rows' chains run side by side)
-            auto convert = [&](auto codes, auto keys) {
-                uint32_t hi[LOADS], lo[LOADS];
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j) {
-                    const float s = scales[ROWS * j];
-                    const __half h = __float2half_rn(s);
-                    hi[j] = __half_as_ushort(h) * 0x10001u;
-                    lo[j] = decltype(keys)::value ? __half_as_ushort(__float2half_rn(s - __half2float(h))) * 0x10001u : 0u;
-                }
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j) {
-                    uint4 x, y;
-                    convert16<decltype(codes)::value, decltype(keys)::value>(raw[j], hi[j], lo[j], x, y);
-                    raw[j] = load(j);
-                    // (rows of a lane are 8 apart, or 4: the swizzle's place changes with bit 2)
-                    const int at = (16 * piece + row0 + ROWS * j) * 128 + ((2 * (ch & 3) ^ ((row0 + ROWS * j) & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(dst + at) = x;
-                    *reinterpret_cast<uint4 *>(dst + (at ^ 16)) = y;
-                }
-            };
-            if (a.codes == Q4K_I8) {
-                if (values) convert(std::integral_constant<int, Q4K_I8>{}, std::false_type{});
-                else convert(std::integral_constant<int, Q4K_I8>{}, std::true_type{});
-            } else {
-                if (values) convert(std::integral_constant<int, Q4K_E4M3>{}, std::false_type{});
-                else convert(std::integral_constant<int, Q4K_E4M3>{}, std::true_type{});
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (!(a.stall && g == 0)) mbar_arrive(smem_u32(&sh.full[stage]));
-                if (last) mbar_arrive(smem_u32(&sh.ahead.empty[un % kUnits]));
-            }
-            g = next;
-        }
-        }
-    } else if (!EIGHT && (w == kKeyWarp || w == kValueWarp)) {
+    if (w == kKeyWarp || w == kValueWarp) {
         // ------------------------------------------------------------ loads
         regs_dec<kOtherRegs>();
         const bool values = w == kValueWarp;
@@ -728,10 +433,14 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                 if (live) {
                     int e;
                     page_of(a, key, e, slot);
-                    page = pages[e];
-                    if (page < 0 || page >= a.pages) {
-                        atomicOr(a.error, 4u);
-                        live = false;
+                    if constexpr (WIDE) {
+                        page = t.seq * a.table_pages + e;
+                    } else {
+                        page = pages[e];
+                        if (page < 0 || page >= a.pages) {
+                            atomicOr(a.error, 4u);
+                            live = false;
+                        }
                     }
                 }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * static_cast<uint32_t>(box) * 128u * ND;
@@ -786,7 +495,7 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
         regs_dec<kOtherRegs>();
-        constexpr uint32_t id_s = chunk_idesc<FT>(kChunkKeys, false), id_o = chunk_idesc<FT>(DP, true);
+        constexpr uint32_t id_s = chunk_idesc<CT>(kChunkKeys, false), id_o = chunk_idesc<CT>(DP, true);
         const uint32_t q0 = smem_u32(sh.q), kv0 = smem_u32(sh.kv);
         int stage = 0;
         uint32_t round = 0, steps[2] = {0, 0};
@@ -855,12 +564,12 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
         }
     } else if (w < 8) {
         // ------------------------------------------------------------ softmax
-        regs_inc<softmax_regs(CT)>();
+        regs_inc<kSoftmaxRegs>();
         const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
         const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
         const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
         uint32_t steps = 0, done = 0;
-        int unit = 0;                   // (8 bits) units of this CTA so far
+        int unit = 0;                                   // (WIDE) units of this CTA so far
         bool ok = true;
         // masked scores are -inf: keep their product with the scale -inf when the scale is 0
         const float c = (MODE & 1) ? a.scale / a.softcap : fmaxf(a.scale * kLog2e, 1e-30f);
@@ -872,11 +581,10 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
             const Tile &t = item.t;
             const int head = item.head, off = item.off, todo = item.todo;
             if (t.rows <= 128 * h) {
-                if constexpr (EIGHT) {   // (the tile is not this warp's, but its phases are)
-                    ok = wait(sh.q_full, k & 1);
+                if constexpr (WIDE) {   // (the units are not this warp's, but it counts for their places)
                     for (int i = 0; i < todo && ok; ++i, ++unit) {
-                        ok = wait(sh.ahead.full[unit % kUnits], (unit / kUnits) & 1);
-                        if (ok && lane == 0) mbar_arrive(smem_u32(&sh.ahead.empty[unit % kUnits]));
+                        ok = wait(sh.factors_full[unit % kUnitsAhead], (unit / kUnitsAhead) & 1);
+                        if (ok && lane == 0) mbar_arrive(smem_u32(&sh.factors_empty[unit % kUnitsAhead]));
                     }
                 }
                 continue;
@@ -899,36 +607,15 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
             const int rel = live ? t.pos0 + static_cast<int>(tok) : 0;   // position, for the distance
 
             float m = -INFINITY, l = 0.0f;   // maximum in use (of c s, log2) and sum
-            float cq = c;                    // (8 bits) with the power of two of the row's queries
-            int top = 0;                     // (8 bits) O is over 2^top
-            if constexpr (EIGHT) {
-                ok = wait(sh.q_full, k & 1);
-                if (!ok) break;
-                cq = c * sh.ahead.row_scale[k & 1][row];
-            }
+            float cq = c;                    // (WIDE) with the power of two of the row's queries
+            int top = 0;                     // (WIDE) O is over 2^top
+            if (WIDE && live && a.row_scale) cq = c * a.row_scale[static_cast<int64_t>(t.tok0 + tok) * a.heads + hq];
             for (int i = 0; i < todo; ++i) {
                 const int kb = t.lo + (off + i) * kChunkKeys;
                 ok = wait(sh.s_full[h], steps & 1);
                 if (!ok) break;
                 ++steps;
                 tm_fence_after();
-                float cu = c;
-                int low = 0;       // (8 bits) the unit's values are over 2^(top + low), low <= 0
-                int grown = 0;     // (8 bits) by which the unit raises top
-                if constexpr (EIGHT) {
-                    const int un = unit++ % kUnits;
-                    ok = wait(sh.ahead.full[un], ((unit - 1) / kUnits) & 1);
-                    if (!ok) break;
-                    // (below 1e-30 a score is nothing, and one masked out has to stay -inf)
-                    cu = fminf(fmaxf(cq * two_to(sh.ahead.unit[un].exponent[0]), 1e-30f), 3e38f);
-                    const int x = sh.ahead.unit[un].exponent[1];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.ahead.empty[un]));
-                    if (i == 0) top = x;
-                    grown = max(x - top, 0);
-                    top += grown;
-                    low = max(x - top, -100);
-                }
                 float s[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tm_ld32(ts + 32 * q, s[q]);
@@ -936,42 +623,65 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
 #pragma unroll
                 for (int q = 1; q < 4; ++q) tm_here32(s[q]);
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                int grown = 0;               // (WIDE) by which the unit raises top
+                const UnitFactors *fac = &sh.factors[unit % kUnitsAhead];
+                if constexpr (WIDE) {
+                    ok = wait(sh.factors_full[unit % kUnitsAhead], (unit / kUnitsAhead) & 1);
+                    if (!ok) break;
+                    const int e = fac->exponent;
+                    grown = i == 0 ? 0 : max(e - top, 0);
+                    top = i == 0 ? e : top + grown;
+                }
+                // the factor of the scores of columns 32 q + 16 b and on
+                // (WIDE: below 1e-30 a score is nothing, and one masked out has to stay -inf)
+                auto score = [&](int q, int b) { return WIDE ? fminf(fmaxf(cq * fac->key[2 * q + b], 1e-30f), 3e38f) : c; };
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float *v = s[q];
+                    const float c0 = score(q, 0), c1 = WIDE ? score(q, 1) : c0;
                     if (MODE & 1) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j] = a.softcap * kLog2e * (1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * (v[j] * cu)) + 1.0f));
+                            v[j] = a.softcap * kLog2e * (1.0f - 2.0f * rcp(ex2(2.0f * kLog2e * (v[j] * (j < 16 ? c0 : c1))) + 1.0f));
                     }
                     if (MODE & 2) {
                         const float d0 = static_cast<float>(rel - kb - 32 * q);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), (MODE & 1) ? v[j] : v[j] * cu);
+                            v[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), (MODE & 1) ? v[j] : v[j] * (j < 16 ? c0 : c1));
                     }
                     if (kb < in_lo || kb + kChunkKeys > in_hi) {
                         const int a0 = lo - kb - 32 * q, a1 = hi - kb - 32 * q;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = j >= a0 && j < a1 ? v[j] : -INFINITY;
                     }
+                    if constexpr (WIDE && !(MODE & 3)) {   // a maximum for each factor
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                        for (int b = 0; b < 2; ++b) {
+                            const float *u = v + 16 * b;
+                            const float p0 = max3(u[0], u[1], u[2]), p1 = max3(u[3], u[4], u[5]), p2 = max3(u[6], u[7], u[8]),
+                                        p3 = max3(u[9], u[10], u[11]), p4 = max3(u[12], u[13], u[14]);
+                            x[q] = fmaxf(x[q], fmaxf(max3(p0, p1, p2), max3(p3, p4, u[15])) * (b ? c1 : c0));
+                        }
+                    } else {
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) x[z] = max3(x[z], v[j + 2 * z], v[j + 2 * z + 1]);
+                        for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) x[z] = max3(x[z], v[j + 2 * z], v[j + 2 * z + 1]);
+                        }
                     }
                 }
-                const float mul = (MODE & 3) ? 1.0f : cu;
-                const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * mul;
+                const float mul = (MODE & 3) ? 1.0f : c;
+                const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * (WIDE ? 1.0f : mul);
                 float f = 1.0f;
                 if (mx > m + kLazy || m == -INFINITY) {
                     // (m = mx = -inf: everything masked so far, l and O are zero)
                     f = mx == m ? 1.0f : ex2(m - mx);
                     m = mx;
                 }
-                if (i > 0 && (__any_sync(0xffffffffu, f != 1.0f) || (EIGHT && grown))) {
+                if (i > 0 && (__any_sync(0xffffffffu, f != 1.0f) || (WIDE && grown))) {
                     l *= f;
-                    if constexpr (EIGHT) f *= two_to(max(-grown, -126));
+                    if constexpr (WIDE) f *= two_to(max(-grown, -126));
 #pragma unroll
                     for (int j = 0; j < DP / 16; ++j) {
                         float o[16];
@@ -982,19 +692,41 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                         tm_st16(to + 16 * j, reinterpret_cast<const uint32_t *>(o));
                     }
                 }
-                const float base = (m == -INFINITY ? 0.0f : m - kShift) - static_cast<float>(low);
+                const float base = m == -INFINITY ? 0.0f : m - kShift;
                 const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t p[16];
+                    // (WIDE: P times the values' factor of its piece over 2^top, one of nothing counting as
+                    // 2^-30; the sum loses it again)
+                    float x0 = 0.0f, x1 = 0.0f;
+                    uint64_t mul_a = mul2, mul_b = mul2, base_a = base2, base_b = base2;
+                    if constexpr (WIDE) {
+                        x0 = fmaxf(fac->value[2 * q] - static_cast<float>(top), -30.0f);
+                        x1 = fmaxf(fac->value[2 * q + 1] - static_cast<float>(top), -30.0f);
+                        base_a = pair(x0 - base, x0 - base), base_b = pair(x1 - base, x1 - base);
+                        sum[0] = sum[1] = 0;
+                        if (!(MODE & 3)) {
+                            const float m0 = score(q, 0), m1 = score(q, 1);
+                            mul_a = pair(m0, m0), mul_b = pair(m1, m1);
+                        }
+                    }
 #pragma unroll
                     for (int z = 0; z < 16; ++z) {
                         float e0, e1;
-                        unpair(fma2(pair(s[q][2 * z], s[q][2 * z + 1]), mul2, base2), e0, e1);
+                        unpair(fma2(pair(s[q][2 * z], s[q][2 * z + 1]), z < 8 ? mul_a : mul_b, z < 8 ? base_a : base_b), e0, e1);
                         e0 = ex2(e0), e1 = ex2(e1);
-                        sum[z & 1] = add2(sum[z & 1], pair(e0, e1));
-                        p[z] = pack2(e0, e1, FT);
+                        uint64_t &add = sum[WIDE ? z >> 3 : z & 1];
+                        add = add2(add, pair(e0, e1));
+                        p[z] = pack2(e0, e1, CT);
+                    }
+                    if constexpr (WIDE) {
+                        float l0, l1;
+                        unpair(sum[0], l0, l1);
+                        l = fmaf(l0 + l1, ex2(-x0), l);
+                        unpair(sum[1], l0, l1);
+                        l = fmaf(l0 + l1, ex2(-x1), l);
                     }
                     tm_st16(ts + 16 * q, p);
                     if (q & 1) {   // 64 keys of P: the products can start on them
@@ -1003,12 +735,18 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                         mbar_arrive(smem_u32(&sh.p_ready[h][q >> 1]));
                     }
                 }
-                float l0, l1;
-                unpair(add2(sum[0], sum[1]), l0, l1);
-                l += EIGHT ? (l0 + l1) * two_to(-low) : l0 + l1;
+                if constexpr (WIDE) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.factors_empty[unit % kUnitsAhead]));
+                    ++unit;
+                } else {
+                    float l0, l1;
+                    unpair(add2(sum[0], sum[1]), l0, l1);
+                    l += l0 + l1;
+                }
             }
             if (!ok) break;
-            const float back = EIGHT ? two_to(top) : 1.0f;   // O's power of two
+            const float back = WIDE ? two_to(top) : 1.0f;   // O's power of two
 
             // ---- O: divide and store, or leave a partial result ([dim / 4][row] quads, maxima, sums)
             ok = wait(sh.o_done[h], done & 1);
@@ -1022,7 +760,7 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                     float o[32];
                     tm_ld32(to + 32 * j, o);
                     tm_wait_ld32(o);
-                    if constexpr (EIGHT)
+                    if constexpr (WIDE)
 #pragma unroll
                         for (int z = 0; z < 32; ++z) o[z] *= back;
                     if (live) {
@@ -1043,7 +781,7 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                     float o[32];
                     tm_ld32(to + 32 * j, o);
                     tm_wait_ld32(o);
-                    if constexpr (EIGHT)
+                    if constexpr (WIDE)
 #pragma unroll
                         for (int z = 0; z < 32; ++z) o[z] *= back;
 #pragma unroll
@@ -1066,13 +804,69 @@ __global__ void __launch_bounds__(chunk_threads(CT), 1)
                     __syncwarp();
                 }
                 if (live && a.lse)
-                    a.lse[static_cast<int64_t>(t.tok0 + tok) * a.heads + hq] =
+                    a.lse[static_cast<int64_t>(t.tok0 + tok) * a.lse_heads + hq] =
                         l == 0.0f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
             }
             tm_fence_before();
         }
     } else {
         regs_dec<kOtherRegs>();   // (a warpgroup changes its registers together)
+        if constexpr (WIDE) {
+            // -------------------------------------------------------- factors ahead
+            // two units at a time: lane 16 j + 8 s + p has piece p of unit i + j, its keys' (s = 0) or values'
+            int unit = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                Work item;
+                ok = next_work(k, item);
+                if (!ok || item.todo == 0) break;
+                const bool holes = DOCS && (item.t.seq & kHoles);
+                if (DOCS) item.t.seq &= ~kHoles;
+                const Tile &t = item.t;
+                const int first = t.lo / kChunkKeys + item.off;   // (tiles begin at pages)
+                for (int i = 0; i < item.todo; i += 2) {
+                    const bool mine = i + (lane >> 4) < item.todo;   // (the last may be alone)
+                    float f = 0.0f;
+                    if (mine)
+                        f = a.factors[((static_cast<int64_t>(t.seq) * a.table_pages + first + i + (lane >> 4)) * a.kv_heads + item.head) * 16 +
+                                      (lane & 15)];
+                    // a piece that is not in the cache: -inf.  Some row may see it, or none.
+                    if (__any_sync(0xffffffffu, f == -INFINITY)) {
+                        const int kb = (first + i + (lane >> 4)) * kChunkKeys + 16 * (lane & 7);
+                        bool seen = mine && kb + 16 > t.from && kb < t.hi;
+                        if (holes) {
+                            for (int j = 0; j < min(2, item.todo - i); ++j) {
+                                uint32_t all[kChunkKeys / 32];
+                                seen_keys(a, t, (first + i + j) * kChunkKeys, all);
+#pragma unroll
+                                for (int z = 0; z < kChunkKeys / 32; ++z)
+                                    if ((lane >> 4) == j && (lane >> 1 & 3) == z) seen = (all[z] >> (16 * (lane & 1)) & 0xFFFFu) != 0;
+                            }
+                        }
+                        if (f == -INFINITY) {
+                            if (seen) atomicOr(a.error, 4u);
+                            f = 0.0f;
+                        }
+                    }
+                    const int two = min(2, item.todo - i);
+                    for (int z = 0; z < two && ok; ++z)
+                        if (unit + z >= kUnitsAhead) ok = wait(sh.factors_empty[(unit + z) % kUnitsAhead], ((unit + z) / kUnitsAhead - 1) & 1);
+                    if (!ok) break;
+                    float most = (lane & 8) ? fabsf(f) : 0.0f;
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    UnitFactors &to = sh.factors[(unit + (lane >> 4)) % kUnitsAhead];
+                    if (mine) {
+                        if (lane & 8) to.value[lane & 7] = log2f(fabsf(f));
+                        else to.key[lane & 7] = f;
+                        if ((lane & 15) == 0) to.exponent = max(-112, min(122, static_cast<int>(__float_as_uint(most) >> 23) - 126));
+                    }
+                    __syncwarp();
+                    if (mine && (lane & 15) == 0) mbar_arrive(smem_u32(&sh.factors_full[(unit + (lane >> 4)) % kUnitsAhead]));
+                    unit += two;
+                }
+            }
+        }
     }
     __syncwarp();
     tm_fence_before();
@@ -1094,7 +888,12 @@ struct ChunkLaunch {
 };
 cudaError_t launch_chunk_f16(const ChunkLaunch &l);
 cudaError_t launch_chunk_bf16(const ChunkLaunch &l);
-cudaError_t launch_chunk_8(const ChunkLaunch &l);
+cudaError_t launch_chunk_wide(const ChunkLaunch &l);   // (a widened 8-bit cache)
+// A call over an 8-bit cache: widened, then the kernel, in passes of as many cache heads
+// as kWidenMost bytes of scratch hold.
+constexpr int64_t kWidenMost = int64_t{1} << 30;
+int64_t widened_bytes(const Args &a);   // of one cache head
+cudaError_t launch_widened(const ChunkLaunch &l);
 
 }  // namespace attn
 }  // namespace q4k

@@ -11,7 +11,7 @@ namespace attn {
 template <int CT, int DP, int MODE>
 static cudaError_t launch_chunk_one(const ChunkLaunch &l)
 {
-    using Sh = ChunkShared<CT, DP>;
+    using Sh = ChunkShared<DP>;
     auto kern = chunk_kernel<CT, DP, MODE>;
     Args a = l.args;
     constexpr int R = kChunkRows;
@@ -19,10 +19,10 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     int box = 128;
     while (a.page_size % box) box /= 2;
-    CacheMaps maps{};
-    CUtensorMap qmap{};
+    CacheMaps maps;
+    CUtensorMap qmap;
     const int tokens = R / a.group;   // of a tile
-    if (!eight(CT) && (!encode_cache(&maps, a, CT, box) || !encode_queries(&qmap, a, CT, tokens))) return cudaErrorInvalidValue;
+    if (!encode_cache(&maps, a, CT, box) || !encode_queries(&qmap, a, CT, tokens)) return cudaErrorInvalidValue;
     a.slots = a.tokens / tokens + a.batch;
     const int64_t units = a.capacity / kChunkKeys + 1;
     const int64_t most = static_cast<int64_t>(a.slots) * a.kv_heads * units;
@@ -34,7 +34,7 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     return launch_split(a, l.device, grid, R, DP, chunk_shift<CT>(), l.stream, [&](const Args &args) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = chunk_threads(CT);
+        cfg.blockDim = kChunkThreads;
         cfg.dynamicSmemBytes = kSmem;
         cfg.stream = l.stream;
         const Attributes at(&cfg, 0, args.pdl);
@@ -42,25 +42,26 @@ static cudaError_t launch_chunk_one(const ChunkLaunch &l)
     });
 }
 
-template <int CT, int DP>
+template <int CT, int DP, int WIDE>
 static cudaError_t launch_chunk_mode(const ChunkLaunch &l)
 {
     switch ((l.args.softcap > 0.0f ? 1 : 0) | (l.args.slopes ? 2 : 0) | (l.args.docs() ? 4 : 0)) {
-        case 0: return launch_chunk_one<CT, DP, 0>(l);
-        case 1: return launch_chunk_one<CT, DP, 1>(l);
-        case 2: return launch_chunk_one<CT, DP, 2>(l);
-        case 3: return launch_chunk_one<CT, DP, 3>(l);
-        case 4: return launch_chunk_one<CT, DP, 4>(l);
-        case 5: return launch_chunk_one<CT, DP, 5>(l);
-        case 6: return launch_chunk_one<CT, DP, 6>(l);
-        default: return launch_chunk_one<CT, DP, 7>(l);
+        case 0: return launch_chunk_one<CT, DP, 0 | WIDE>(l);
+        case 1: return launch_chunk_one<CT, DP, 1 | WIDE>(l);
+        case 2: return launch_chunk_one<CT, DP, 2 | WIDE>(l);
+        case 3: return launch_chunk_one<CT, DP, 3 | WIDE>(l);
+        case 4: return launch_chunk_one<CT, DP, 4 | WIDE>(l);
+        case 5: return launch_chunk_one<CT, DP, 5 | WIDE>(l);
+        case 6: return launch_chunk_one<CT, DP, 6 | WIDE>(l);
+        default: return launch_chunk_one<CT, DP, 7 | WIDE>(l);
     }
 }
 
-template <int CT>
+// WIDE: 8 for a widened 8-bit cache.
+template <int CT, int WIDE = 0>
 static cudaError_t launch_chunk_type(const ChunkLaunch &l)
 {
-    return l.args.dim > 64 ? launch_chunk_mode<CT, 128>(l) : launch_chunk_mode<CT, 64>(l);
+    return l.args.dim > 64 ? launch_chunk_mode<CT, 128, WIDE>(l) : launch_chunk_mode<CT, 64, WIDE>(l);
 }
 
 }  // namespace attn

@@ -126,12 +126,6 @@ __device__ __forceinline__ void st_shared_cluster_v2(uint32_t addr, float x, flo
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
-// 16 bytes global -> shared, or 16 zero bytes.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
 // One arrival on an mbarrier when this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint32_t bar)
 {
@@ -184,24 +178,11 @@ __device__ __forceinline__ constexpr int chunk_at(int r, int c)
     return BOX == 64 ? r * 64 + ((c ^ (r >> 1 & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint2 ld_shared8(uint32_t addr)
 {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
-}
-
-// 4 bytes global -> shared, or zeros.
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 
 // P carries 2^shift (see above).

@@ -1,0 +1,250 @@
+// q4k_attn_widen.cu -- prompt chunks over an 8-bit cache: the keys and values that the
+// call may see go to fp16 once, then the many-rows kernel runs over them.
+//
+// That kernel's products want fp16 operands.  Turned inside it, each of a tile's 256 rows
+// a code would cost as many instructions as its softmax does, again for every tile of a
+// sequence (issue slots bound it at half the speed of a 16-bit cache: 2048 tokens over
+// 14336 took 537 us at best); turned once they cost a read of the codes and a write and
+// re-reads, mostly from L2, of twice as many bytes.
+//
+// Layout: pages of 128 positions, table_pages a sequence, [page][head][128][dim], and
+// for each page and head the factors of its eight pieces of 16 keys, then of values.  A
+// block of 16 tokens or more covers whole pieces: the factor is its scale, and the fp16
+// values are the codes themselves, exactly.  Smaller blocks' scales multiply the codes over
+// a power of two of the piece, its factor, with one rounding to fp16 (2^-11 of a value).  A piece
+// that is not in the cache has factors of -inf; the kernel knows whether a row sees it.
+// bf16 queries become fp16 over a power of two a row here too.
+//
+// Bound by memory: 3 bytes a code (32 / 8 heads of 128, 16384 positions: 100 MB).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/q4k.h"
+#include "q4k_attn_chunk.cuh"
+#include "q4k_codes.cuh"
+
+namespace q4k {
+namespace attn {
+
+constexpr int kWidenThreads = 256, kWidenWarps = kWidenThreads / 32, kPage = 128;
+static_assert(kPage == kChunkKeys, "a unit of the many-rows kernel");
+
+struct WidenArgs {
+    Args a;                // of the call (k, v: codes; heads of this pass)
+    __half *k, *v, *q;     // to (q: null if the queries are fp16)
+    float *factors, *row_scale;
+};
+
+// Sixteen codes as fp16, times s (0: as they are).
+template <int CODES>
+__device__ __forceinline__ void widen16(const uint4 &raw, float s, uint4 &x, uint4 &y)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        key_pairs<CODES>(w[i], r[2 * i], r[2 * i + 1]);
+        if (s != 0.0f) {
+#pragma unroll
+            for (int j = 2 * i; j < 2 * i + 2; ++j) {   // (fp32 product, one rounding)
+                const float2 f = unpack2(r[j], Q4K_F16);
+                r[j] = pack2(f.x * s, f.y * s, Q4K_F16);
+            }
+        }
+    }
+    x = make_uint4(r[0], r[1], r[2], r[3]), y = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// A piece of 16 positions, head and side: a warp.  `live`: the piece's rows that count.
+__device__ __forceinline__ void widen_piece(const WidenArgs &w, int64_t to, int piece, int head, int side, int page, int slot, uint32_t live)
+{
+    const Args &a = w.a;
+    const int lane = threadIdx.x & 31;
+    const float *scales = side ? a.vs + page * a.vs_page + head * a.vs_head : a.ks + page * a.ks_page + head * a.ks_head;
+    const int64_t block = side ? a.vs_block : a.ks_block, slots = side ? a.v_slot : a.k_slot;
+    // the codes first: rows of CPR chunks
+    const int cpr = a.dim > 64 ? 8 : 4, rps = 32 / cpr, ch = lane & (cpr - 1), row0 = lane / cpr;
+    const uint8_t *from = static_cast<const uint8_t *>(side ? a.v : a.k) + page * (side ? a.v_page : a.k_page) +
+                          head * (side ? a.v_head : a.k_head) + (slot + row0) * slots + 16 * ch;
+    const bool inside = 16 * ch < a.dim;
+    uint4 raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (inside && rps * j < 16 && (live >> (row0 + rps * j) & 1)) raw[j] = __ldg(reinterpret_cast<const uint4 *>(from + j * rps * slots));
+    }
+    float s = 0.0f, factor;   // s: of row lane % 16, over the factor; 0 where the codes stay
+    if (a.block_shift >= 4) {
+        factor = scales[(slot >> a.block_shift) * block];
+    } else {
+        const int r = lane & 15;
+        s = live >> r & 1 ? scales[((slot + r) >> a.block_shift) * block] : 0.0f;
+        float most = fabsf(s);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const int x = max(-120, min(115, static_cast<int>(__float_as_uint(most) >> 23) - 133));   // the largest to [64, 128)
+        s *= two_to(-x);
+        factor = most > 0.0f ? two_to(x) : 0.0f;
+    }
+    if (lane == 0) w.factors[to * 16 + 8 * side + piece] = factor;
+    __half *out = (side ? w.v : w.k) + (to * kPage + 16 * piece) * a.dim + 16 * ch;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = row0 + rps * j;
+        const float f = __shfl_sync(0xffffffffu, s, r & 15);
+        if (!inside || rps * j >= 16 || !(live >> r & 1)) continue;
+        uint4 x, y;
+        if (a.codes == Q4K_I8) widen16<Q4K_I8>(raw[j], f, x, y);
+        else widen16<Q4K_E4M3>(raw[j], f, x, y);
+        // (a row of scale 0 among scaled ones: its codes count for nothing)
+        if (a.block_shift < 4 && f == 0.0f) x = y = make_uint4(0, 0, 0, 0);
+        uint4 *p = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(r) * a.dim);
+        p[0] = x, p[1] = y;
+    }
+}
+
+// blockIdx.y = the sequence, its pages of 128 in strides of the grid; one more: the queries.
+__global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ WidenArgs w)
+{
+    const Args &a = w.a;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+    if (b == a.batch) {
+        // rows of dim / 8 lanes in groups of 16 (8)
+        const int lanes = a.dim > 64 ? 16 : 8, per = 32 / lanes, c = lane & (lanes - 1);
+        const int64_t rows = static_cast<int64_t>(a.tokens) * a.heads;
+        for (int64_t r = (static_cast<int64_t>(blockIdx.x) * kWidenWarps + warp) * per; r < rows;
+             r += static_cast<int64_t>(gridDim.x) * kWidenWarps * per) {
+            const int64_t row = r + lane / lanes, tok = row / a.heads, h = row - tok * a.heads;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            const bool here = row < rows && 8 * c < a.dim;
+            if (here) raw = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_token + h * a.q_head + 8 * c);
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+            float mx = 0.0f;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float2 f = unpack2(u[z], a.q_type);
+                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            for (int o = lanes >> 1; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+            const int e = ex != 0 && ex != 255 ? max(-126, min(126, 141 - ex)) : 0;   // max|q| to [2^14, 2^15)
+            const float up = two_to(e);
+            if (here) {
+                uint32_t v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float2 f = unpack2(u[z], a.q_type);
+                    v[z] = pack2(f.x * up, f.y * up, Q4K_F16);
+                }
+                *reinterpret_cast<uint4 *>(w.q + row * a.dim + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                if (c == 0) w.row_scale[row] = two_to(-e);
+            }
+        }
+        return;
+    }
+    // what the sequence's tokens may see: from its first token's window on
+    const int s0 = a.seq_start[b], n = a.seq_start[b + 1] - s0, raw_len = a.kv_len[b];
+    if (n <= 0) return;
+    const int len = min(max(raw_len, 0), a.capacity), first = raw_len - n;
+    const int lo = a.window ? min(max(first + 1 - a.window, 0), len) : 0;
+    __shared__ int s_page[8], s_slot[8];
+    __shared__ uint32_t s_live[8];
+    for (int pg = lo / kPage + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
+        __syncthreads();
+        if (threadIdx.x < 8) {
+            const int key = pg * kPage + 16 * threadIdx.x;
+            const uint32_t live = span(lo - key, len - key) & 0xFFFFu;   // (positions)
+            int page = -1, slot = 0;
+            if (live) {
+                int e;
+                page_of(a, key, e, slot);
+                page = a.page_table[b * a.table_stride + e];
+                if (page >= a.pages) page = -1;
+            }
+            s_page[threadIdx.x] = page, s_slot[threadIdx.x] = slot, s_live[threadIdx.x] = live;
+        }
+        __syncthreads();
+        const int64_t base = (static_cast<int64_t>(b) * a.table_pages + pg) * a.kv_heads;
+        for (int i = warp; i < 16 * a.kv_heads; i += kWidenWarps) {
+            const int head = i % a.kv_heads, piece = i / a.kv_heads & 7, side = i / (8 * a.kv_heads);
+            if (s_live[piece] && s_page[piece] >= 0)
+                widen_piece(w, base + head, piece, head, side, s_page[piece], s_slot[piece], s_live[piece]);
+            else if (lane == 0)
+                w.factors[(base + head) * 16 + 8 * side + piece] = s_live[piece] ? -INFINITY : 0.0f;
+        }
+    }
+}
+
+// Bytes of the widened keys, values and factors of one cache head.
+int64_t widened_bytes(const Args &a)
+{
+    const int64_t pages = static_cast<int64_t>(a.batch) * ((a.capacity + kPage - 1) / kPage);
+    return pages * (2 * kPage * 2 * static_cast<int64_t>(a.dim) + 64);
+}
+
+// As many cache heads a pass as kWidenMost bytes hold, one at least.
+cudaError_t launch_widened(const ChunkLaunch &l)
+{
+    const Args &all = l.args;
+    const int64_t per_head = widened_bytes(all);
+    const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(all.kv_heads, kWidenMost / std::max<int64_t>(per_head, 1))));
+    const int passes = (all.kv_heads + most - 1) / most, per = (all.kv_heads + passes - 1) / passes;   // (about alike)
+    const int table_pages = (all.capacity + kPage - 1) / kPage;
+    const int64_t pages = static_cast<int64_t>(all.batch) * table_pages;
+    if (pages > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const bool turn = all.q_type != Q4K_F16;
+    auto room = [](int64_t n) { return (n + 255) / 256 * 256; };
+    const int64_t side = room(pages * per * kPage * all.dim * 2), fac = room(pages * per * 64);
+    const int64_t rows = static_cast<int64_t>(all.tokens) * per * all.group;
+    const int64_t q = turn ? room(rows * all.dim * 2) : 0, scale = turn ? room(rows * 4) : 0;
+    void *scratch = nullptr;
+    cudaError_t e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream);
+    if (e != cudaSuccess) return e;
+    uint8_t *at = static_cast<uint8_t *>(scratch);
+    for (int h0 = 0; h0 < all.kv_heads && e == cudaSuccess; h0 += per) {
+        WidenArgs w{};
+        Args &a = w.a;
+        a = all;
+        a.kv_heads = std::min(per, all.kv_heads - h0), a.heads = a.kv_heads * all.group, a.table_pages = table_pages;
+        a.k = static_cast<const uint8_t *>(all.k) + h0 * all.k_head, a.v = static_cast<const uint8_t *>(all.v) + h0 * all.v_head;
+        a.ks = all.ks + h0 * all.ks_head, a.vs = all.vs + h0 * all.vs_head;
+        const int64_t hq = static_cast<int64_t>(h0) * all.group;
+        a.q = static_cast<const uint16_t *>(all.q) + hq * all.q_head, a.out = static_cast<uint16_t *>(all.out) + hq * all.out_head;
+        if (all.lse) a.lse = all.lse + hq;
+        if (all.slopes) a.slopes = all.slopes + hq;
+        w.k = reinterpret_cast<__half *>(at), w.v = reinterpret_cast<__half *>(at + side);
+        w.factors = reinterpret_cast<float *>(at + 2 * side);
+        if (turn) w.q = reinterpret_cast<__half *>(at + 2 * side + fac), w.row_scale = reinterpret_cast<float *>(at + 2 * side + fac + q);
+        cudaLaunchConfig_t cfg = {};
+        // eight CTAs an SM in all, each sequence's pages dealt out over its share
+        const int64_t q_ctas = turn ? (static_cast<int64_t>(all.tokens) * a.heads + 15) / 16 : 1;
+        const int x = static_cast<int>(std::max<int64_t>(std::min<int64_t>(table_pages, (8 * l.sms + all.batch - 1) / all.batch),
+                                                         std::min<int64_t>(q_ctas, 4 * l.sms)));
+        cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(all.batch + (turn ? 1 : 0)));
+        cfg.blockDim = kWidenThreads;
+        cfg.stream = l.stream;
+        // (a later pass writes what the one before it reads)
+        const Attributes attributes(&cfg, 0, all.pdl && h0 == 0);
+        e = cudaLaunchKernelEx(&cfg, widen_kernel, w);
+        if (e != cudaSuccess) break;
+        ChunkLaunch ch = l;
+        Args &c = ch.args;
+        c = a;
+        c.k = w.k, c.v = w.v, c.factors = w.factors, c.row_scale = w.row_scale;
+        c.k_head = c.v_head = static_cast<int64_t>(kPage) * a.dim, c.k_slot = c.v_slot = a.dim;
+        c.k_page = c.v_page = a.kv_heads * c.k_head;
+        c.pages = static_cast<int>(pages), c.page_size = kPage, c.page_shift = 7;
+        c.q_type = Q4K_F16, c.pdl = true;
+        if (turn) c.q = w.q, c.q_head = a.dim, c.q_token = static_cast<int64_t>(a.heads) * a.dim;
+        e = launch_chunk_wide(ch);
+    }
+    const cudaError_t f = cudaFreeAsync(scratch, l.stream);
+    return e == cudaSuccess ? f : e;
+}
+
+}  // namespace attn
+}  // namespace q4k

@@ -70,10 +70,10 @@ def _floor(vs, vc, lens, many=False):
     """Softmax weights go to fp16 as e s 2^(14 - t), e the weight over the largest, s the value's scale, 2^t at most twice the
     largest scale: below fp16's normal numbers each (and the last part of one in parts) is off by half a step, 2^-25, so
     e s by 2^-39 2^t <= 2^-38 max s, and an output by that times the codes it sums, over a sum of weights of at least 1.
-    (It shows where the keys of large weight have codes of 0.)  The many-rows form keeps e 2^6 or more, beside values over
-    the largest scale: 2^-31 of it, twice."""
+    (It shows where the keys of large weight have codes of 0.)  The many-rows form has e 2^6 f / 2^t, f the factor of a piece of
+    values, 2^t at most twice the largest, and rows of up to 128 times their codes: 2^-25 2^-6 2^t 128 / 64 <= 2^-29 max s."""
     s = vs[torch.isfinite(vs)]
-    return 2.0 ** (-30 if many else -38) * (float(s.max()) if s.numel() else 0.0) * plain8.TOP[vc.dtype] * max(lens)
+    return 2.0 ** (-29 if many else -38) * (float(s.max()) if s.numel() else 0.0) * plain8.TOP[vc.dtype] * max(lens)
 
 
 def _products(q, keys, vals, case, scale, slopes, softcap):
@@ -406,7 +406,7 @@ def test_offsets_past_32_bits(q4k, n, qt):
     for form in (None, "many") if qt == BF16 else (None,):
         out = q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, pt.cuda(), _dev([0, n]), _dev([length]), form=form)
         k8, v8 = [k.double() * step], [v.double() * step]
-        extra = _products(q, k8, v8, dict(new=[n], len=[length]), 0.125, None, 0.0)[0] + 2.0 ** -30 * step * 127 * length
+        extra = _products(q, k8, v8, dict(new=[n], len=[length]), 0.125, None, 0.0)[0] + 2.0 ** -29 * step * 127 * length
         assert ((out.double().cpu() - ref).abs() <= bound + (extra if qt == BF16 else 2.0 ** -38 * step * 127 * length)).all()
     k2, v2 = q4k.kv_read8(kc, vc, ks, vs, pt.cuda(), _dev([0, length]), _dev([length]), length, dtype=F32)
     assert torch.equal(k2.cpu(), k.float() * step) and torch.equal(v2.cpu(), v.float() * step)
