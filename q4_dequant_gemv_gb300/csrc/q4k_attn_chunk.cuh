@@ -65,8 +65,10 @@ constexpr int kChunkKeys = 128;              // keys of a unit
 constexpr int kChunkThreads = 384;           // two softmax warpgroups; MMA, key, value and idle warp
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kFactorWarp = 11;
 constexpr int kStages = 4;
-// 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+// 256 x 200 + 128 x 96 registers, within the 384 x 168 of the launch; a widened cache's
+// factors take more beside a row of S: 256 x 208 + 128 x 88
+constexpr int softmax_regs(int mode) { return mode & 8 ? 208 : 200; }
+constexpr int other_regs(int mode) { return mode & 8 ? 88 : 96; }
 
 // A CTA's part of one tile, as the key warp found it.
 struct Work {
@@ -74,10 +76,11 @@ struct Work {
     int head, off, todo, last;   // units [off, off + todo) of the tile; the CTA that holds the tile's last unit
 };
 
-// The factors of a unit: of the keys of each piece of 16, of the values as log2.
+// The factors of a unit's pieces of 16: of the keys; of the values over 2^top as log2, and
+// one over that; by how much top has grown since the tile's (or this part's) unit before.
 struct UnitFactors {
-    float key[8], value[8];
-    int exponent;                            // the values' are at most 2^exponent
+    float key[8], value[8], undo[8];
+    int top, grown;
 };
 constexpr int kUnitsAhead = 4;
 
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
     if (w == kKeyWarp || w == kValueWarp) {
         // ------------------------------------------------------------ loads
-        regs_dec<kOtherRegs>();
+        regs_dec<other_regs(MODE)>();
         const bool values = w == kValueWarp;
         const CUtensorMap *map = values ? &maps.v : &maps.k;
         int unit = 0, edges = 0, k = 0;   // this warp's stage of unit i: 2 (i % 2), + 1 for values
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (q_sent && !ok) (void)mbar_wait_bounded(smem_u32(&sh.q_full), k & 1, kLandNs);
     } else if (w == kMmaWarp) {
         // ------------------------------------------------------------ products
-        regs_dec<kOtherRegs>();
+        regs_dec<other_regs(MODE)>();
         constexpr uint32_t id_s = chunk_idesc<CT>(kChunkKeys, false), id_o = chunk_idesc<CT>(DP, true);
         const uint32_t q0 = smem_u32(sh.q), kv0 = smem_u32(sh.kv);
         int stage = 0;
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (w < 8) {
         // ------------------------------------------------------------ softmax
-        regs_inc<kSoftmaxRegs>();
+        regs_inc<softmax_regs(MODE)>();
         const int h = w >> 2, row = tid;                // row of the tile: half h, TMEM lane tid % 128
         const uint32_t lane_base = static_cast<uint32_t>(w & 3) << 21;   // 32 (w % 4) lanes, in bits 16..
         const uint32_t ts = tm + lane_base + 128 * h, to = tm + lane_base + 256 + 128 * h;
@@ -628,13 +631,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if constexpr (WIDE) {
                     ok = wait(sh.factors_full[unit % kUnitsAhead], (unit / kUnitsAhead) & 1);
                     if (!ok) break;
-                    const int e = fac->exponent;
-                    grown = i == 0 ? 0 : max(e - top, 0);
-                    top = i == 0 ? e : top + grown;
+                    grown = fac->grown, top = fac->top;
                 }
                 // the factor of the scores of columns 32 q + 16 b and on
-                // (WIDE: below 1e-30 a score is nothing, and one masked out has to stay -inf)
-                auto score = [&](int q, int b) { return WIDE ? fminf(fmaxf(cq * fac->key[2 * q + b], 1e-30f), 3e38f) : c; };
+                // (WIDE: never 0, a score that is masked out has to stay -inf)
+                auto score = [&](int q, int b) { return WIDE ? fmaxf(cq * fac->key[2 * q + b], 1e-38f) : c; };
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float *v = s[q];
@@ -698,14 +699,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t p[16];
-                    // (WIDE: P times the values' factor of its piece over 2^top, one of nothing counting as
-                    // 2^-30; the sum loses it again)
-                    float x0 = 0.0f, x1 = 0.0f;
+                    // (WIDE: P times the values' factor of its piece over 2^top; the sum loses it again)
                     uint64_t mul_a = mul2, mul_b = mul2, base_a = base2, base_b = base2;
                     if constexpr (WIDE) {
-                        x0 = fmaxf(fac->value[2 * q] - static_cast<float>(top), -30.0f);
-                        x1 = fmaxf(fac->value[2 * q + 1] - static_cast<float>(top), -30.0f);
-                        base_a = pair(x0 - base, x0 - base), base_b = pair(x1 - base, x1 - base);
+                        const float x0 = fac->value[2 * q] - base, x1 = fac->value[2 * q + 1] - base;
+                        base_a = pair(x0, x0), base_b = pair(x1, x1);
                         sum[0] = sum[1] = 0;
                         if (!(MODE & 3)) {
                             const float m0 = score(q, 0), m1 = score(q, 1);
@@ -724,9 +722,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if constexpr (WIDE) {
                         float l0, l1;
                         unpair(sum[0], l0, l1);
-                        l = fmaf(l0 + l1, ex2(-x0), l);
+                        l = fmaf(l0 + l1, fac->undo[2 * q], l);
                         unpair(sum[1], l0, l1);
-                        l = fmaf(l0 + l1, ex2(-x1), l);
+                        l = fmaf(l0 + l1, fac->undo[2 * q + 1], l);
                     }
                     tm_st16(ts + 16 * q, p);
                     if (q & 1) {   // 64 keys of P: the products can start on them
@@ -810,7 +808,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tm_fence_before();
         }
     } else {
-        regs_dec<kOtherRegs>();   // (a warpgroup changes its registers together)
+        regs_dec<other_regs(MODE)>();   // (a warpgroup changes its registers together)
         if constexpr (WIDE) {
             // -------------------------------------------------------- factors ahead
             // two units at a time: lane 16 j + 8 s + p has piece p of unit i + j, its keys' (s = 0) or values'
@@ -824,6 +822,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (DOCS) item.t.seq &= ~kHoles;
                 const Tile &t = item.t;
                 const int first = t.lo / kChunkKeys + item.off;   // (tiles begin at pages)
+                int top = 0;
                 for (int i = 0; i < item.todo; i += 2) {
                     const bool mine = i + (lane >> 4) < item.todo;   // (the last may be alone)
                     float f = 0.0f;
@@ -855,11 +854,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     float most = (lane & 8) ? fabsf(f) : 0.0f;
 #pragma unroll
                     for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    // the units' exponents (factors are at most 2^e), one after the other
+                    const int e = max(-112, min(122, static_cast<int>(__float_as_uint(most) >> 23) - 126));
+                    const int e0 = __shfl_sync(0xffffffffu, e, 0), e1 = two > 1 ? __shfl_sync(0xffffffffu, e, 16) : e0;
+                    const int before = i == 0 ? e0 : top, top0 = max(before, e0);
+                    top = max(top0, e1);
+                    const int at = lane >> 4 ? top : top0, grown = lane >> 4 ? top - top0 : top0 - before;
                     UnitFactors &to = sh.factors[(unit + (lane >> 4)) % kUnitsAhead];
                     if (mine) {
-                        if (lane & 8) to.value[lane & 7] = log2f(fabsf(f));
-                        else to.key[lane & 7] = f;
-                        if ((lane & 15) == 0) to.exponent = max(-112, min(122, static_cast<int>(__float_as_uint(most) >> 23) - 126));
+                        if (lane & 8) {   // (one of nothing counts as 2^-30 of the largest)
+                            const float x = fmaxf(log2f(fabsf(f)) - static_cast<float>(at), -30.0f);
+                            to.value[lane & 7] = x, to.undo[lane & 7] = ex2(-x);
+                        } else {
+                            to.key[lane & 7] = f;
+                        }
+                        if ((lane & 15) == 0) to.top = at, to.grown = grown;
                     }
                     __syncwarp();
                     if (mine && (lane & 15) == 0) mbar_arrive(smem_u32(&sh.factors_full[(unit + (lane >> 4)) % kUnitsAhead]));

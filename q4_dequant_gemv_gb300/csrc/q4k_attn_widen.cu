@@ -105,7 +105,7 @@ __device__ __forceinline__ void widen_piece(const WidenArgs &w, int64_t to, int 
     }
 }
 
-// blockIdx.y = the sequence, its pages of 128 in strides of the grid; one more: the queries.
+// blockIdx.y = the sequence, its pieces in strides of the grid; one more: the queries.
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ WidenArgs w)
 {
     const Args &a = w.a;
@@ -151,31 +151,23 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
     if (n <= 0) return;
     const int len = min(max(raw_len, 0), a.capacity), first = raw_len - n;
     const int lo = a.window ? min(max(first + 1 - a.window, 0), len) : 0;
-    __shared__ int s_page[8], s_slot[8];
-    __shared__ uint32_t s_live[8];
-    for (int pg = lo / kPage + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
-        __syncthreads();
-        if (threadIdx.x < 8) {
-            const int key = pg * kPage + 16 * threadIdx.x;
-            const uint32_t live = span(lo - key, len - key) & 0xFFFFu;   // (positions)
-            int page = -1, slot = 0;
-            if (live) {
-                int e;
-                page_of(a, key, e, slot);
-                page = a.page_table[b * a.table_stride + e];
-                if (page >= a.pages) page = -1;
-            }
-            s_page[threadIdx.x] = page, s_slot[threadIdx.x] = slot, s_live[threadIdx.x] = live;
+    // a warp per piece, head and side, neighbouring warps on neighbouring heads
+    const int pg0 = lo / kPage, per_page = 16 * a.kv_heads;
+    const int64_t tasks = len > pg0 * kPage ? static_cast<int64_t>((len + kPage - 1) / kPage - pg0) * per_page : 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWidenWarps + warp; i < tasks; i += static_cast<int64_t>(gridDim.x) * kWidenWarps) {
+        const uint32_t x = static_cast<uint32_t>(quotient(i, a.kv_heads));   // (a position's fits 32 bits)
+        const int head = static_cast<int>(i - static_cast<int64_t>(x) * a.kv_heads), side = x & 1, piece = x >> 1 & 7, pg = pg0 + (x >> 4);
+        const int key = pg * kPage + 16 * piece;
+        const uint32_t live = span(lo - key, len - key) & 0xFFFFu;
+        int page = -1, slot = 0;
+        if (live) {
+            int e;
+            page_of(a, key, e, slot);
+            page = a.page_table[b * a.table_stride + e];
         }
-        __syncthreads();
-        const int64_t base = (static_cast<int64_t>(b) * a.table_pages + pg) * a.kv_heads;
-        for (int i = warp; i < 16 * a.kv_heads; i += kWidenWarps) {
-            const int head = i % a.kv_heads, piece = i / a.kv_heads & 7, side = i / (8 * a.kv_heads);
-            if (s_live[piece] && s_page[piece] >= 0)
-                widen_piece(w, base + head, piece, head, side, s_page[piece], s_slot[piece], s_live[piece]);
-            else if (lane == 0)
-                w.factors[(base + head) * 16 + 8 * side + piece] = s_live[piece] ? -INFINITY : 0.0f;
-        }
+        const int64_t to = (static_cast<int64_t>(b) * a.table_pages + pg) * a.kv_heads + head;
+        if (page >= 0 && page < a.pages) widen_piece(w, to, piece, head, side, page, slot, live);
+        else if (lane == 0) w.factors[to * 16 + 8 * side + piece] = live ? -INFINITY : 0.0f;
     }
 }
 
@@ -220,9 +212,10 @@ cudaError_t launch_widened(const ChunkLaunch &l)
         w.factors = reinterpret_cast<float *>(at + 2 * side);
         if (turn) w.q = reinterpret_cast<__half *>(at + 2 * side + fac), w.row_scale = reinterpret_cast<float *>(at + 2 * side + fac + q);
         cudaLaunchConfig_t cfg = {};
-        // eight CTAs an SM in all, each sequence's pages dealt out over its share
+        // up to eight CTAs an SM in all, each sequence's pieces dealt out over its share
         const int64_t q_ctas = turn ? (static_cast<int64_t>(all.tokens) * a.heads + 15) / 16 : 1;
-        const int x = static_cast<int>(std::max<int64_t>(std::min<int64_t>(table_pages, (8 * l.sms + all.batch - 1) / all.batch),
+        const int x = static_cast<int>(std::max<int64_t>(std::min<int64_t>(2 * static_cast<int64_t>(table_pages) * a.kv_heads,
+                                                                           (8 * l.sms + all.batch - 1) / all.batch),
                                                          std::min<int64_t>(q_ctas, 4 * l.sms)));
         cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(all.batch + (turn ? 1 : 0)));
         cfg.blockDim = kWidenThreads;
