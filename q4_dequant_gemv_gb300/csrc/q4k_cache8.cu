@@ -3,9 +3,18 @@
 // way back (q4k_kv_read8).
 //
 // Bound by memory, or for a few tokens by the chain of dependent index loads.  A
-// head of a token is 4 pairs a lane, 16 lanes (dim <= 128) or 32; a warp holds up to
-// 8 such rows a lane group in registers, all loaded before the index chain begins.
+// head of a token is E = 8 pairs a lane where dim and rot are multiples of 16 (8 lanes up
+// to a dim of 128, 16 above), else 4; a warp holds several such rows in registers, all
+// loaded before the index chain begins.  (4 pairs a lane throughout: 39 us for 4097
+// tokens of 40 heads, half of each turned.)
 // The norm is one sum over a lane group; pairs turn in the lane that holds them.
+//
+// Measured (device): norms of 4097 tokens of 40 bf16 heads, half of each turned, 27 us
+// (85 MB; the rotation alone moves as much in 18), bound by issue slots and latency alike
+// (6 CTAs of 128 threads an SM; 4: 35 us); three prompts of 2500 tokens, 32 / 8 bf16 heads,
+// appended 51 us (queries in a launch of their own: no less) and read back 13; 65536
+// positions of 8 heads read to bf16 76 us, 5.3 TB/s.  One token: 4 to 6 us of launch and
+// index loads.
 //
 // Quantising: a warp (several for blocks of more tokens than it holds) takes an
 // aligned run of positions of one head, so that every block lies in one warp, or in
@@ -20,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/q4k.h"
 #include "ptx.cuh"
@@ -47,10 +57,10 @@ bool clear_cache8_error()
 namespace cache8 {
 
 constexpr int kMaxRot = 512, kMaxDim = 256;
-constexpr int kRows = 8;         // rows of a lane group that a warp of the cache's side holds
+constexpr int rows_of(int e) { return 32 / e; }   // rows of a lane group that a warp of the cache's side holds
 constexpr int kWarps = 4;        // of a CTA where one warp holds a block
 constexpr int kMaxBlock = 128;   // tokens of a scale
-constexpr int kMaxWarps = kMaxBlock / kRows;
+constexpr int kMaxWarps = kMaxBlock / 8;
 
 // One tensor of heads.
 struct Heads {
@@ -79,7 +89,8 @@ struct Args {
     int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int dim, rot, inter, codes;
     int block, shift;       // tokens of a scale, its log2
-    int lanes;              // of a row: 16 or 32
+    int lanes;              // of a row: a power of two, dim / (2 E) of them at least
+    float over_dim;         // 1 / dim
     int run, warps;         // append: positions of an item, warps that hold them
     int slots;              // append: items of a head and tensor at most
     int kv_ctas;            // append: CTAs of the cache's side, the queries' follow
@@ -89,9 +100,10 @@ struct Args {
 
 // ---------------------------------------------------------------- a row's pairs
 
-// A lane's four pairs of a head: pair j is (a[j], b[j]).
+// A lane's pairs of a head: pair j is (a[j], b[j]).
+template <int E>
 struct Pairs {
-    float a[4], b[4];
+    float a[E], b[E];
 };
 
 __device__ __forceinline__ float load1(const void *p, int type, int64_t i)
@@ -108,21 +120,32 @@ __device__ __forceinline__ void store1(void *p, int type, int64_t i, float v)
     else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// Where a lane's pairs lie in a head: pair 4 u + j of unit u.  Turned pairs are
-// (p, p + rot/2), or (2p, 2p + 1) if interleaved; what is not turned goes in
-// neighbours.  Wide accesses (rot a multiple of 8) take two quads: `ia`, `ib`.
+// Where a lane's pairs lie in a head.  Turned pairs are (p, p + rot/2), or (2p, 2p + 1)
+// if INTER; what is not turned goes alike, in halves or in neighbours, so that every lane
+// does the same.  Wide accesses (rot and dim multiples of 2 E) take E elements at `ia`, E
+// at `ib`, each from neighbouring lanes without gaps (16 bytes of every 32 in two turns
+// took 33 us where this takes 31).  Pair j has the table's entry pa + j, for INTER from
+// the second half of the pairs on pb + j - E/2.  (Narrow accesses: pair E u + j.)
+template <int E, bool INTER>
 struct Lane {
     int u;                  // unit
-    bool live, turned, split;
-    int ia, ib;
+    bool live, turned, turned_b;   // (turned_b: INTER, of the pairs of ib)
+    int ia, ib, pa, pb;
 
-    __device__ __forceinline__ Lane(const Args &a, int rot, int lane) : u(lane % a.lanes)
+    __device__ __forceinline__ Lane(const Args &a, int rot, int lane) : u(lane & (a.lanes - 1))
     {
-        live = 8 * u < a.dim;
-        turned = 8 * u < rot;
-        split = turned && !a.inter;
-        ia = split ? 4 * u : 8 * u;
-        ib = split ? 4 * u + (rot >> 1) : 8 * u + 4;
+        live = 2 * E * u < a.dim;
+        if constexpr (INTER) {
+            ia = E * u, ib = E * u + (a.dim >> 1);
+            turned = ia < rot, turned_b = ib < rot;
+            pa = ia >> 1, pb = ib >> 1;
+        } else {
+            turned = turned_b = 2 * E * u < rot;
+            const int rest = rot + E * u - (rot >> 1);   // of the units behind the turned ones
+            ia = turned ? E * u : rest;
+            ib = turned ? E * u + (rot >> 1) : rest + ((a.dim - rot) >> 1);
+            pa = E * u, pb = pa + E / 2;
+        }
     }
 };
 
@@ -133,85 +156,107 @@ __device__ __forceinline__ void pair_at(int p, int rot, int inter, int &i, int &
     else i = 2 * p, j = i + 1;
 }
 
-// Two quads of fp32 as pairs.
-__device__ __forceinline__ void arrange(const float (&x)[4], const float (&y)[4], bool split, Pairs &r)
+// E elements at ia and E at ib as pairs, and back.
+template <int E, bool INTER>
+__device__ __forceinline__ void arrange(const float (&x)[E], const float (&y)[E], Pairs<E> &r)
 {
-    if (split) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r.a[j] = x[j], r.b[j] = y[j];
-    } else {
-        r.a[0] = x[0], r.b[0] = x[1], r.a[1] = x[2], r.b[1] = x[3];
-        r.a[2] = y[0], r.b[2] = y[1], r.a[3] = y[2], r.b[3] = y[3];
+    for (int j = 0; j < E; ++j) {
+        if constexpr (INTER) r.a[j] = j < E / 2 ? x[2 * j & (E - 1)] : y[2 * j & (E - 1)], r.b[j] = j < E / 2 ? x[(2 * j & (E - 1)) + 1] : y[(2 * j & (E - 1)) + 1];
+        else r.a[j] = x[j], r.b[j] = y[j];
     }
 }
 
-__device__ __forceinline__ void disarrange(const Pairs &r, bool split, float (&x)[4], float (&y)[4])
+template <int E, bool INTER>
+__device__ __forceinline__ void disarrange(const Pairs<E> &r, float (&x)[E], float (&y)[E])
 {
-    if (split) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = r.a[j], y[j] = r.b[j];
-    } else {
-        x[0] = r.a[0], x[1] = r.b[0], x[2] = r.a[1], x[3] = r.b[1];
-        y[0] = r.a[2], y[1] = r.b[2], y[2] = r.a[3], y[3] = r.b[3];
+    for (int j = 0; j < E; ++j) {
+        if constexpr (INTER) x[j] = j & 1 ? r.b[j / 2] : r.a[j / 2], y[j] = j & 1 ? r.b[E / 2 + j / 2] : r.a[E / 2 + j / 2];
+        else x[j] = r.a[j], y[j] = r.b[j];
     }
 }
 
-__device__ __forceinline__ void unpack4(uint2 r, int type, float (&f)[4])
+// E elements in one access (16 bits) or E / 4 (fp32).
+template <int E>
+struct Raw16 {
+    uint2 v[E / 4];
+};
+template <int E>
+__device__ __forceinline__ Raw16<E> load16(const uint16_t *p)
 {
-    const float2 a = attn::unpack2(r.x, type), b = attn::unpack2(r.y, type);
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+    Raw16<E> r;
+    if constexpr (E == 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        r.v[0] = make_uint2(x.x, x.y), r.v[1] = make_uint2(x.z, x.w);
+    } else {
+        r.v[0] = *reinterpret_cast<const uint2 *>(p);
+    }
+    return r;
+}
+
+template <int E>
+__device__ __forceinline__ void unpack(const Raw16<E> &r, int type, float (&f)[E])
+{
+#pragma unroll
+    for (int j = 0; j < E / 4; ++j) {
+        const float2 a = attn::unpack2(r.v[j].x, type), b = attn::unpack2(r.v[j].y, type);
+        f[4 * j] = a.x, f[4 * j + 1] = a.y, f[4 * j + 2] = b.x, f[4 * j + 3] = b.y;
+    }
 }
 
 // N rows of a lane group, the first at element `base`, `step` elements apart;
 // row k where `there` has bit k.  All loads first, conversions after.
-template <bool WIDE, int N>
-__device__ __forceinline__ void load_rows(const void *x, int type, int64_t base, int64_t step, const Lane &l, int rot, int inter,
-                                          uint32_t there, Pairs (&r)[N])
+template <bool WIDE, int N, int E, bool INTER>
+__device__ __forceinline__ void load_rows(const void *x, int type, int64_t base, int64_t step, const Lane<E, INTER> &l, int rot, int inter,
+                                          uint32_t there, Pairs<E> (&r)[N])
 {
     if constexpr (WIDE) {
         if (type == Q4K_F32) {
-            float4 p[N], q[N];
+            float p[N][E], q[N][E];
             const float *s = static_cast<const float *>(x) + base;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                p[k] = q[k] = make_float4(0, 0, 0, 0);
-                if (there >> k & 1) {
-                    p[k] = *reinterpret_cast<const float4 *>(s + k * step + l.ia);
-                    q[k] = *reinterpret_cast<const float4 *>(s + k * step + l.ib);
-                }
-            }
+            for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float a[4] = {p[k].x, p[k].y, p[k].z, p[k].w}, b[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-                arrange(a, b, l.split, r[k]);
-            }
+                for (int j = 0; j < E; j += 4) {
+                    float4 v = make_float4(0, 0, 0, 0), z = v;
+                    if (there >> k & 1) {
+                        v = *reinterpret_cast<const float4 *>(s + k * step + l.ia + j);
+                        z = *reinterpret_cast<const float4 *>(s + k * step + l.ib + j);
+                    }
+                    p[k][j] = v.x, p[k][j + 1] = v.y, p[k][j + 2] = v.z, p[k][j + 3] = v.w;
+                    q[k][j] = z.x, q[k][j + 1] = z.y, q[k][j + 2] = z.z, q[k][j + 3] = z.w;
+                }
+#pragma unroll
+            for (int k = 0; k < N; ++k) arrange<E, INTER>(p[k], q[k], r[k]);
         } else {
-            uint2 p[N], q[N];
+            Raw16<E> p[N], q[N];
             const uint16_t *s = static_cast<const uint16_t *>(x) + base;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                p[k] = q[k] = make_uint2(0, 0);
-                if (there >> k & 1) {
-                    p[k] = *reinterpret_cast<const uint2 *>(s + k * step + l.ia);
-                    q[k] = *reinterpret_cast<const uint2 *>(s + k * step + l.ib);
-                }
+                p[k] = q[k] = Raw16<E>{};
+                if (there >> k & 1) p[k] = load16<E>(s + k * step + l.ia), q[k] = load16<E>(s + k * step + l.ib);
             }
+            auto all = [&](auto t) {   // (the type outside the rows)
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                float a[4], b[4];
-                unpack4(p[k], type, a);
-                unpack4(q[k], type, b);
-                arrange(a, b, l.split, r[k]);
-            }
+                for (int k = 0; k < N; ++k) {
+                    float a[E], b[E];
+                    unpack<E>(p[k], decltype(t)::value, a);
+                    unpack<E>(q[k], decltype(t)::value, b);
+                    arrange<E, INTER>(a, b, r[k]);
+                }
+            };
+            if (type == Q4K_F16) all(std::integral_constant<int, Q4K_F16>{});
+            else all(std::integral_constant<int, Q4K_BF16>{});
         }
     } else {
 #pragma unroll 1
         for (int k = 0; k < N; ++k) {
-            Pairs one;
+            Pairs<E> one;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < E; ++j) {
                 int c, d;
-                pair_at(4 * l.u + j, rot, inter, c, d);
+                pair_at(E * l.u + j, rot, inter, c, d);
                 one.a[j] = one.b[j] = 0.0f;
                 if (there >> k & 1) one.a[j] = load1(x, type, base + k * step + c), one.b[j] = load1(x, type, base + k * step + d);
             }
@@ -222,26 +267,40 @@ __device__ __forceinline__ void load_rows(const void *x, int type, int64_t base,
     }
 }
 
-template <bool WIDE>
-__device__ __forceinline__ void store_row(void *y, int type, int64_t base, const Lane &l, int rot, int inter, const Pairs &r)
+template <bool WIDE, int E, bool INTER>
+__device__ __forceinline__ void store_row(void *y, int type, int64_t base, const Lane<E, INTER> &l, int rot, int inter, const Pairs<E> &r)
 {
     if constexpr (WIDE) {
-        float a[4], b[4];
-        disarrange(r, l.split, a, b);
+        float a[E], b[E];
+        disarrange<E, INTER>(r, a, b);
         if (type == Q4K_F32) {
             float *d = static_cast<float *>(y) + base;
-            *reinterpret_cast<float4 *>(d + l.ia) = make_float4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<float4 *>(d + l.ib) = make_float4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int j = 0; j < E; j += 4) {
+                *reinterpret_cast<float4 *>(d + l.ia + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+                *reinterpret_cast<float4 *>(d + l.ib + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+            }
         } else {
             uint16_t *d = static_cast<uint16_t *>(y) + base;
-            *reinterpret_cast<uint2 *>(d + l.ia) = make_uint2(attn::pack2(a[0], a[1], type), attn::pack2(a[2], a[3], type));
-            *reinterpret_cast<uint2 *>(d + l.ib) = make_uint2(attn::pack2(b[0], b[1], type), attn::pack2(b[2], b[3], type));
+            uint32_t p[E / 2], q[E / 2];
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                p[j] = attn::pack2(a[2 * j], a[2 * j + 1], type);
+                q[j] = attn::pack2(b[2 * j], b[2 * j + 1], type);
+            }
+            if constexpr (E == 8) {
+                *reinterpret_cast<uint4 *>(d + l.ia) = make_uint4(p[0], p[1], p[2], p[3]);
+                *reinterpret_cast<uint4 *>(d + l.ib) = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+                *reinterpret_cast<uint2 *>(d + l.ia) = make_uint2(p[0], p[1]);
+                *reinterpret_cast<uint2 *>(d + l.ib) = make_uint2(q[0], q[1]);
+            }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < E; ++j) {
             int c, d;
-            pair_at(4 * l.u + j, rot, inter, c, d);
+            pair_at(E * l.u + j, rot, inter, c, d);
             store1(y, type, base + c, r.a[j]);
             store1(y, type, base + d, r.b[j]);
         }
@@ -249,52 +308,80 @@ __device__ __forceinline__ void store_row(void *y, int type, int64_t base, const
 }
 
 // A lane's weights, ones where there are none.
-template <bool WIDE>
-__device__ __forceinline__ void load_weight(const Heads &h, int head, const Lane &l, int inter, Pairs &w)
+template <bool WIDE, int E, bool INTER>
+__device__ __forceinline__ void load_weight(const Heads &h, int head, const Lane<E, INTER> &l, int inter, Pairs<E> &w)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w.a[j] = w.b[j] = 1.0f;
+    for (int j = 0; j < E; ++j) w.a[j] = w.b[j] = 1.0f;
     if (!h.weight || !l.live) return;
-    Pairs one[1];
-    load_rows<WIDE, 1>(h.weight, Q4K_F32, head * h.wh, 0, l, h.rot, inter, 1u, one);
+    Pairs<E> one[1];
+    load_rows<WIDE, 1, E, INTER>(h.weight, Q4K_F32, head * h.wh, 0, l, h.rot, inter, 1u, one);
     w = one[0];
 }
 
-// Normed in place; whole warps.
-__device__ __forceinline__ void norm(Pairs &r, const Pairs &w, int lanes, int dim, float eps)
+// Sum and maximum over a row's lanes; whole warps.
+__device__ __forceinline__ float row_sum(float s, int lanes)
 {
-    float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s = fmaf(r.a[j], r.a[j], fmaf(r.b[j], r.b[j], s));
-    for (int o = lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float f = 1.0f / sqrtf(s / static_cast<float>(dim) + eps);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.a[j] *= f * w.a[j], r.b[j] *= f * w.b[j];
+    for (int o = 16; o; o >>= 1)
+        if (o < lanes) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
 }
 
-// Turned in place by a table row.
-template <bool WIDE>
-__device__ __forceinline__ void turn(Pairs &r, const float *row, const Lane &l, int rot, int inter)
+// Normed in place; whole warps.
+template <int E>
+__device__ __forceinline__ void norm(Pairs<E> &r, const Pairs<E> &w, int lanes, float over_dim, float eps)
 {
-    if constexpr (WIDE) {
-        if (!l.turned) return;
-        const float4 c = *reinterpret_cast<const float4 *>(row + 4 * l.u), s = *reinterpret_cast<const float4 *>(row + (rot >> 1) + 4 * l.u);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    float s = 0.0f, z = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = r.a[j], y = r.b[j];
-            r.a[j] = x * cc[j] - y * ss[j];
-            r.b[j] = x * ss[j] + y * cc[j];
+    for (int j = 0; j < E; ++j) s = fmaf(r.a[j], r.a[j], s), z = fmaf(r.b[j], r.b[j], z);
+    const float f = 1.0f / sqrtf(fmaf(row_sum(s + z, lanes), over_dim, eps));
+#pragma unroll
+    for (int j = 0; j < E; ++j) r.a[j] *= f * w.a[j], r.b[j] *= f * w.b[j];
+}
+
+// A lane's cosines and sines in a table row, and a turn by them.
+template <int E>
+struct Turn {
+    float c[E], s[E];
+};
+template <bool WIDE, int E, bool INTER>
+__device__ __forceinline__ void load_turn(Turn<E> &t, const float *row, const Lane<E, INTER> &l, int rot)
+{
+    if constexpr (WIDE && E == 8) {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+            if (!(j ? l.turned_b : l.turned)) continue;
+            const float *p = row + (j ? l.pb : l.pa);
+            const float4 c = *reinterpret_cast<const float4 *>(p), s = *reinterpret_cast<const float4 *>(p + (rot >> 1));
+            t.c[j] = c.x, t.c[j + 1] = c.y, t.c[j + 2] = c.z, t.c[j + 3] = c.w;
+            t.s[j] = s.x, t.s[j + 1] = s.y, t.s[j + 2] = s.z, t.s[j + 3] = s.w;
+        }
+    } else if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {   // (E = 4: two pairs of each part)
+            if (!(j ? l.turned_b : l.turned)) continue;
+            const float *p = row + (j ? l.pb : l.pa);
+            const float2 c = *reinterpret_cast<const float2 *>(p), s = *reinterpret_cast<const float2 *>(p + (rot >> 1));
+            t.c[j] = c.x, t.c[j + 1] = c.y, t.s[j] = s.x, t.s[j + 1] = s.y;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int p = 4 * l.u + j;
-            if (2 * p >= rot) continue;
-            const float c = row[p], s = row[(rot >> 1) + p], x = r.a[j], y = r.b[j];
-            r.a[j] = x * c - y * s;
-            r.b[j] = x * s + y * c;
+        for (int j = 0; j < E; ++j) {
+            const int p = E * l.u + j;
+            if (2 * p < rot) t.c[j] = row[p], t.s[j] = row[(rot >> 1) + p];
         }
+    }
+}
+template <bool WIDE, int E, bool INTER>
+__device__ __forceinline__ void turn(Pairs<E> &r, const Turn<E> &t, const Lane<E, INTER> &l, int rot)
+{
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        if (WIDE ? !(j < E / 2 ? l.turned : l.turned_b) : 2 * (E * l.u + j) >= rot) continue;
+        const float x = r.a[j], y = r.b[j];
+        r.a[j] = x * t.c[j] - y * t.s[j];
+        r.b[j] = x * t.s[j] + y * t.c[j];
     }
 }
 
@@ -339,122 +426,130 @@ __device__ __forceinline__ Place place_of(const Args &a, int t, int rot)
 
 // ---------------------------------------------------------------- queries (and norm_rope's keys)
 
-// N rows a lane group of one head: normed, turned, stored.  APPEND: rows are placed
-// by their sequences, else by pos.
-template <bool WIDE, int N, bool APPEND>
-__device__ __forceinline__ void turn_rows(const Args &a, const Heads &h, int head, int64_t t0)
+// Heads of a chunk: N rows a lane group of one token.
+__host__ __device__ __forceinline__ int chunk_heads(int n, int lanes) { return n * (32 / lanes); }
+
+// A chunk of a token's heads from head0 on: normed, turned, stored.  APPEND: the token is
+// placed by its sequence, else by pos.  (Heads of one token lie together and share its
+// table row; rows of one head of several tokens took 31 us where this takes 27.)
+template <bool WIDE, int N, int E, bool INTER, bool APPEND>
+__device__ __forceinline__ void turn_rows(const Args &a, const Heads &h, int head0, int64_t t)
 {
-    const int lane = threadIdx.x & 31, groups = 32 / a.lanes, g = lane / a.lanes;
-    const Lane l(a, h.rot, lane);
-    // row k of this group: token t0 + k groups + g
+    const int lane = threadIdx.x & 31, groups = 32 / a.lanes, first = head0 + lane / a.lanes;
+    const Lane<E, INTER> l(a, h.rot, lane);
+    // row k of this group: head first + k groups
     uint32_t there = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k)
-        if (l.live && t0 + k * groups + g < a.at.tokens) there |= 1u << k;
-    Pairs r[N], w;
-    load_rows<WIDE, N>(h.x, h.xtype, (t0 + g) * h.xt + head * h.xh, groups * h.xt, l, h.rot, a.inter, there, r);
-    load_weight<WIDE>(h, head, l, a.inter, w);
-    // lane i places token t0 + i
-    Place mine{0, 0, 0, 0};
-    if (lane < N * groups && t0 + lane < a.at.tokens) {
-        const int t = static_cast<int>(t0) + lane;
-        if (APPEND) {
-            mine = place_of(a, t, h.rot);
-        } else {
-            mine.state = 1;
-            if (h.rot) {
-                mine.row = a.at.pos[t];
-                if (mine.row < 0 || mine.row >= a.at.table_rows) mine.state = 2;
-            }
+        if (l.live && first + k * groups < h.heads) there |= 1u << k;
+    Pairs<E> r[N];
+    load_rows<WIDE, N, E, INTER>(h.x, h.xtype, t * h.xt + first * h.xh, groups * h.xh, l, h.rot, a.inter, there, r);
+    Place at{0, 0, 0, 1};
+    if (APPEND) {
+        at = place_of(a, static_cast<int>(t), h.rot);
+    } else if (h.rot) {
+        at.row = a.at.pos[t];
+        if (at.row < 0 || at.row >= a.at.table_rows) at.state = 2;
+    }
+    if (at.state == 2 && lane == 0) atomicOr(&g_cache8_error, 4u);
+    if (at.state != 1) return;   // (the whole warp)
+    Turn<E> by;
+    if (h.rot) load_turn<WIDE, E, INTER>(by, a.table + static_cast<int64_t>(at.row) * a.rot, l, h.rot);
+    if (h.weight) {
+        Pairs<E> w;
+        if (!h.wh) load_weight<WIDE, E, INTER>(h, 0, l, a.inter, w);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (h.wh) load_weight<WIDE, E, INTER>(h, min(first + k * groups, h.heads - 1), l, a.inter, w);
+            norm<E>(r[k], w, a.lanes, a.over_dim, a.eps);
         }
     }
-    if (mine.state == 2) atomicOr(&g_cache8_error, 4u);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int row = __shfl_sync(0xffffffffu, mine.row, k * groups + g);
-        const bool good = __shfl_sync(0xffffffffu, mine.state, k * groups + g) == 1 && (there >> k & 1);
-        if (h.weight) norm(r[k], w, a.lanes, a.dim, a.eps);
-        if (!good) continue;
-        if (h.rot) turn<WIDE>(r[k], a.table + static_cast<int64_t>(row) * a.rot, l, h.rot, a.inter);
-        store_row<WIDE>(h.y, h.ytype, (t0 + k * groups + g) * h.yt + head * h.yh, l, h.rot, a.inter, r[k]);
+        if (!(there >> k & 1)) continue;
+        if (h.rot) turn<WIDE, E, INTER>(r[k], by, l, h.rot);
+        store_row<WIDE, E, INTER>(h.y, h.ytype, t * h.yt + (first + k * groups) * h.yh, l, h.rot, a.inter, r[k]);
     }
 }
 
-template <bool WIDE, int N>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_constant__ Args a)
+template <bool WIDE, int N, int E, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, N * E == 16 ? 6 : 8) norm_rope_kernel(const __grid_constant__ Args a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int heads = a.q.heads + a.k.heads;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t group = item / heads, t0 = group * N * (32 / a.lanes);
-    int head = static_cast<int>(item - group * heads);
-    if (t0 >= a.at.tokens) return;
-    const bool keys = head >= a.q.heads;
-    if (keys) head -= a.q.heads;
-    turn_rows<WIDE, N, false>(a, keys ? a.k : a.q, head, t0);
+    const int per = chunk_heads(N, a.lanes), of_q = (a.q.heads + per - 1) / per, chunks = of_q + (a.k.heads + per - 1) / per;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), t = attn::quotient(item, chunks);
+    if (t >= a.at.tokens) return;
+    const int c = static_cast<int>(item - t * chunks);
+    const bool keys = c >= of_q;
+    turn_rows<WIDE, N, E, INTER, false>(a, keys ? a.k : a.q, (keys ? c - of_q : c) * per, t);
 }
 
 // ---------------------------------------------------------------- the cache's side of an append
 
 // Codes of a lane's pairs, times inv.
-template <bool WIDE>
-__device__ __forceinline__ void store_codes(uint8_t *to, int codes, const Lane &l, int rot, int inter, const Pairs &r, float inv)
+template <bool WIDE, int E, bool INTER>
+__device__ __forceinline__ void store_codes(uint8_t *to, int codes, const Lane<E, INTER> &l, int rot, int inter, const Pairs<E> &r, float inv)
 {
-    float x[4], y[4];
-    if constexpr (WIDE) disarrange(r, l.split, x, y);
+    float x[E], y[E];
+    if constexpr (WIDE) disarrange<E, INTER>(r, x, y);
     else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = r.a[j], y[j] = r.b[j];
+        for (int j = 0; j < E; ++j) x[j] = r.a[j], y[j] = r.b[j];
     }
+    uint32_t p[E / 4], q[E / 4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= inv, y[j] *= inv;
-    const uint32_t p = encode4(x, codes), q = encode4(y, codes);
-    if constexpr (WIDE) {
-        if (l.split) {
-            *reinterpret_cast<uint32_t *>(to + l.ia) = p;
-            *reinterpret_cast<uint32_t *>(to + l.ib) = q;
-        } else {
-            *reinterpret_cast<uint2 *>(to + l.ia) = make_uint2(p, q);
-        }
+    for (int j = 0; j < E; j += 4) {
+        const float f[4] = {x[j] * inv, x[j + 1] * inv, x[j + 2] * inv, x[j + 3] * inv};
+        const float z[4] = {y[j] * inv, y[j + 1] * inv, y[j + 2] * inv, y[j + 3] * inv};
+        p[j / 4] = encode4(f, codes), q[j / 4] = encode4(z, codes);
+    }
+    if constexpr (WIDE && E == 8) {
+        *reinterpret_cast<uint2 *>(to + l.ia) = make_uint2(p[0], p[1]);
+        *reinterpret_cast<uint2 *>(to + l.ib) = make_uint2(q[0], q[1]);
+    } else if constexpr (WIDE) {
+        *reinterpret_cast<uint32_t *>(to + l.ia) = p[0];
+        *reinterpret_cast<uint32_t *>(to + l.ib) = q[0];
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < E; ++j) {
             int c, d;
-            pair_at(4 * l.u + j, rot, inter, c, d);
-            to[c] = static_cast<uint8_t>(p >> 8 * j);
-            to[d] = static_cast<uint8_t>(q >> 8 * j);
+            pair_at(E * l.u + j, rot, inter, c, d);
+            to[c] = static_cast<uint8_t>(p[j / 4] >> 8 * (j & 3));
+            to[d] = static_cast<uint8_t>(q[j / 4] >> 8 * (j & 3));
         }
     }
 }
 
 // The older codes of a block, from one scale to another (ratio of the two).
-__device__ __forceinline__ void scale_codes(uint8_t *at, int codes, float ratio, const Lane &l)
+template <int E, bool INTER>
+__device__ __forceinline__ void scale_codes(uint8_t *at, int codes, float ratio, const Lane<E, INTER> &l)
 {
-#pragma unroll
-    for (int h = 0; h < 8; h += 4) {
+#pragma unroll 1
+    for (int h = 0; h < 2 * E; h += 4) {
         uint32_t w = 0;   // (bytes: rows may start anywhere)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(at[8 * l.u + h + j]) << 8 * j;
+        for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(at[2 * E * l.u + h + j]) << 8 * j;
         float f[4];
         decode4(w, codes, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] *= ratio;
         w = encode4(f, codes);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) at[8 * l.u + h + j] = static_cast<uint8_t>(w >> 8 * j);
+        for (int j = 0; j < 4; ++j) at[2 * E * l.u + h + j] = static_cast<uint8_t>(w >> 8 * j);
     }
 }
 
 // An aligned run of positions of one sequence, head and tensor.
-template <bool WIDE>
+template <bool WIDE, int E, bool INTER>
 __device__ __forceinline__ void append_run(const Args &a, float *s_max)
 {
+    constexpr int kRows = rows_of(E);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, groups = 32 / a.lanes, g = lane / a.lanes, hold = kRows * groups;
     const int per = static_cast<int>(blockDim.x >> 5) / a.warps;   // items of a CTA
     const int64_t item = static_cast<int64_t>(blockIdx.x) * per + w / a.warps;
     const int both = 2 * a.k.heads;
-    const int64_t slot = item / both;
+    const int64_t slot = attn::quotient(item, both);
     int head = static_cast<int>(item - slot * both);
     const bool values = head >= a.k.heads;
     if (values) head -= a.k.heads;
@@ -491,17 +586,17 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
     // this warp's positions
     const int64_t base = any ? (p0 / a.run + j) * a.run + (w % a.warps) * hold : 0;
     const bool here = any && base < len && ((base + hold - 1) >> a.shift) >= (p0 >> a.shift);   // (older tokens of its block count)
-    const Lane l(a, h.rot, lane);
+    const Lane<E, INTER> l(a, h.rot, lane);
     uint32_t there = 0;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         const int64_t p = base + k * groups + g;
         if (here && l.live && p >= p0 && p < len) there |= 1u << k;
     }
-    Pairs r[kRows], wt;
+    Pairs<E> r[kRows], wt;
     const int64_t first = s0 + (base - p0) + g;   // token row of this group's first position
-    load_rows<WIDE, kRows>(h.x, h.xtype, first * h.xt + head * h.xh, groups * h.xt, l, h.rot, a.inter, there, r);
-    load_weight<WIDE>(h, head, l, a.inter, wt);
+    load_rows<WIDE, kRows, E, INTER>(h.x, h.xtype, first * h.xt + head * h.xh, groups * h.xt, l, h.rot, a.inter, there, r);
+    load_weight<WIDE, E, INTER>(h, head, l, a.inter, wt);
     // lane i places position base + i, the block's older ones too
     Place mine{0, 0, 0, 0};
     const int64_t p = base + lane;
@@ -516,23 +611,27 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
     for (int k = 0; k < kRows; ++k) {
         const int from = k * groups + g;
         const int row = __shfl_sync(0xffffffffu, mine.row, from), state = __shfl_sync(0xffffffffu, mine.state, from);
-        if (h.weight) norm(r[k], wt, a.lanes, a.dim, a.eps);
+        if (h.weight) norm<E>(r[k], wt, a.lanes, a.over_dim, a.eps);
         most[k] = 0.0f;
         if (state == 1 && (there >> k & 1)) {
             good |= 1u << k;
-            if (h.rot) turn<WIDE>(r[k], a.table + static_cast<int64_t>(row) * a.rot, l, h.rot, a.inter);
+            if (h.rot) {
+                Turn<E> by;
+                load_turn<WIDE, E, INTER>(by, a.table + static_cast<int64_t>(row) * a.rot, l, h.rot);
+                turn<WIDE, E, INTER>(r[k], by, l, h.rot);
+            }
 #pragma unroll
-            for (int z = 0; z < 4; ++z) most[k] = fmaxf(most[k], fmaxf(finite_size(r[k].a[z]), finite_size(r[k].b[z])));
+            for (int z = 0; z < E; ++z) most[k] = fmaxf(most[k], fmaxf(finite_size(r[k].a[z]), finite_size(r[k].b[z])));
         }
     }
     // over a row's lanes, then over the rows of a block: lane groups, rows, warps
-    for (int o = a.lanes >> 1; o; o >>= 1) {
+    // (lane groups hold neighbouring positions: those of a block are the first of them that matter)
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
-    }
-    if (groups > 1 && a.block > 1) {
+    for (int o = 16; o; o >>= 1) {
+        if (o < a.lanes || (o < 32 && o / a.lanes < a.block)) {
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], 16));
+            for (int k = 0; k < kRows; ++k) most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+        }
     }
 #pragma unroll
     for (int step = 1; step < kRows; step <<= 1) {
@@ -579,28 +678,29 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
         const float inv = 1.0f / s;
         uint8_t *to = codes + page * c_page + sl * c_slot + head * c_head;
         if (good >> k & 1) {
-            store_codes<WIDE>(to, a.codes, l, h.rot, a.inter, r[k], inv);
+            store_codes<WIDE, E, INTER>(to, a.codes, l, h.rot, a.inter, r[k], inv);
             // the block's first new position writes its scale
             if (l.u == 0 && ((q & (a.block - 1)) == 0 || q == p0)) *scale_at(page, sl) = s;
         } else if (in_first && q < p0 && state == 1 && l.live && s != before) {
-            scale_codes(to, a.codes, before * inv, l);
+            scale_codes<E, INTER>(to, a.codes, before * inv, l);
         }
     }
 }
 
-template <bool WIDE, int N>
+template <bool WIDE, int N, int E, bool INTER>
 __global__ void __launch_bounds__(kMaxWarps * 32) append8_kernel(const __grid_constant__ Args a)
 {
     __shared__ float s_max[kMaxWarps];
     pdl_launch_dependents();
     pdl_wait();
     if (static_cast<int>(blockIdx.x) < a.kv_ctas) {
-        append_run<WIDE>(a, s_max);
+        append_run<WIDE, E, INTER>(a, s_max);
         return;
     }
     const int64_t item = static_cast<int64_t>(blockIdx.x - a.kv_ctas) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t group = item / a.q.heads, t0 = group * N * (32 / a.lanes);
-    if (t0 < a.at.tokens) turn_rows<WIDE, N, true>(a, a.q, static_cast<int>(item - group * a.q.heads), t0);
+    const int per = chunk_heads(N, a.lanes), chunks = (a.q.heads + per - 1) / per;
+    const int64_t t = attn::quotient(item, chunks);
+    if (t < a.at.tokens) turn_rows<WIDE, N, E, INTER, true>(a, a.q, static_cast<int>(item - t * chunks) * per, t);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -611,10 +711,11 @@ __global__ void __launch_bounds__(kWarps * 32) read8_kernel(const __grid_constan
 {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int kRows = 8;
     const int lane = threadIdx.x & 31, groups = 32 / a.lanes, g = lane / a.lanes, u = lane % a.lanes, hold = kRows * groups;
     const int heads = a.k.heads + a.v.heads;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t group = item / heads, t0 = group * hold;
+    const int64_t group = attn::quotient(item, heads), t0 = group * hold;
     int head = static_cast<int>(item - group * heads);
     if (t0 >= a.at.tokens) return;
     const bool values = head >= a.k.heads, live = 8 * u < a.dim;
@@ -712,6 +813,15 @@ static cudaError_t launch(void (*kern)(Args), const Args &a, int64_t ctas, int t
 
 // Rows a lane group of the queries' side: several where one each would make more
 // warps than the GPU holds.
+// Pairs of a lane, and lanes of a row.
+static int pairs_of(int64_t dim, int64_t rot, bool wide) { return wide && dim > 64 && dim % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+static int lanes_of(int64_t dim, int e)
+{
+    int n = 8;
+    while (2 * e * n < dim) n *= 2;
+    return n;
+}
+
 static bool many_rows(int64_t tokens, int heads, int lanes, int sms)
 {
     return tokens * heads * lanes / 32 >= 32LL * sms;
@@ -733,7 +843,7 @@ static void fill_cache(Args &p, const q4k_paged_cache8 *c8)
     p.vs_page = c8->v_scale_page_stride, p.vs_block = c8->v_scale_block_stride, p.vs_head = c8->v_scale_head_stride;
     p.dim = static_cast<int>(c.dim), p.codes = c.type, p.block = static_cast<int>(c8->block);
     for (p.shift = 0; (1 << p.shift) < p.block;) ++p.shift;
-    p.lanes = p.dim <= 128 ? 16 : 32;
+    p.over_dim = 1.0f / static_cast<float>(p.dim);
 }
 
 }  // namespace cache8
@@ -796,12 +906,19 @@ q4k_status norm_rope_impl(const q4k_norm_rope_args *a, void *stream)
     if (st != Q4K_OK || a->tokens == 0) return st;
     p.at.pos = a->pos, p.at.table_rows = a->table_rows, p.at.tokens = static_cast<int>(a->tokens);
     p.table = a->table, p.dim = static_cast<int>(a->dim), p.rot = static_cast<int>(a->rot), p.inter = a->interleaved;
-    p.lanes = p.dim <= 128 ? 16 : 32;
+    const int e = pairs_of(a->dim, a->rot, wide);
+    p.lanes = lanes_of(a->dim, e), p.over_dim = 1.0f / static_cast<float>(p.dim);
     p.eps = a->eps, p.pdl = a->flags & Q4K_FLAG_PDL;
     const int heads = p.q.heads + p.k.heads;
     const bool many = wide && many_rows(a->tokens, heads, p.lanes, sms);
-    const int64_t each = (many ? 4 : 1) * (32 / p.lanes), warps = (a->tokens + each - 1) / each * heads;
-    auto kern = !wide ? norm_rope_kernel<false, 1> : many ? norm_rope_kernel<true, 4> : norm_rope_kernel<true, 1>;
+    const int64_t each = chunk_heads(many ? 16 / e : 1, p.lanes);
+    const int64_t warps = a->tokens * ((p.q.heads + each - 1) / each + (p.k.heads + each - 1) / each);
+    auto pick = [&](auto inter) {
+        constexpr bool INTER = decltype(inter)::value;
+        return e == 8 ? (many ? norm_rope_kernel<true, 2, 8, INTER> : norm_rope_kernel<true, 1, 8, INTER>)
+                      : (many ? norm_rope_kernel<true, 4, 4, INTER> : norm_rope_kernel<true, 1, 4, INTER>);
+    };
+    auto kern = !wide ? norm_rope_kernel<false, 1, 4, false> : p.inter ? pick(std::true_type{}) : pick(std::false_type{});
     return launch(kern, p, (warps + kWarps - 1) / kWarps, kWarps * 32, stream) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
@@ -847,7 +964,9 @@ q4k_status kv_append8_impl(const q4k_paged_cache8 *c8, const q4k_append8_args *a
     }
     p.at.pos = a->pos, p.at.table_rows = a->table_rows;
     p.table = a->table, p.rot = rot, p.inter = a->interleaved, p.eps = a8->eps, p.pdl = a->flags & Q4K_FLAG_PDL;
-    const int groups = 32 / p.lanes, hold = kRows * groups;
+    const int e = pairs_of(c->dim, rot, wide);
+    p.lanes = lanes_of(c->dim, e);
+    const int groups = 32 / p.lanes, hold = rows_of(e) * groups;
     p.run = std::max(p.block, hold), p.warps = p.run / hold;
     const int64_t slots = 2 * static_cast<int64_t>(p.at.batch) + n / p.run + 1;
     if (slots > 0x7FFFFFFF) return Q4K_ERR_INVALID_ARG;
@@ -855,10 +974,15 @@ q4k_status kv_append8_impl(const q4k_paged_cache8 *c8, const q4k_append8_args *a
     const int warps = std::max(kWarps, p.warps), per = warps / p.warps;
     const int64_t kv_ctas = (slots * 2 * heads + per - 1) / per;
     const bool many = wide && many_rows(n, p.q.heads, p.lanes, sms);
-    const int64_t each = (many ? 4 : 1) * groups, q_warps = (n + each - 1) / each * p.q.heads;
+    const int64_t each = chunk_heads(many ? 16 / e : 1, p.lanes), q_warps = n * ((p.q.heads + each - 1) / each);
     if (kv_ctas + q_warps > 0x7FFFFFFF) return Q4K_ERR_INVALID_ARG;
     p.kv_ctas = static_cast<int>(kv_ctas);
-    auto kern = !wide ? append8_kernel<false, 1> : many ? append8_kernel<true, 4> : append8_kernel<true, 1>;
+    auto pick = [&](auto inter) {
+        constexpr bool INTER = decltype(inter)::value;
+        return e == 8 ? (many ? append8_kernel<true, 2, 8, INTER> : append8_kernel<true, 1, 8, INTER>)
+                      : (many ? append8_kernel<true, 4, 4, INTER> : append8_kernel<true, 1, 4, INTER>);
+    };
+    auto kern = !wide ? append8_kernel<false, 1, 4, false> : p.inter ? pick(std::true_type{}) : pick(std::false_type{});
     return launch(kern, p, kv_ctas + (q_warps + warps - 1) / warps, warps * 32, stream) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
@@ -883,7 +1007,8 @@ q4k_status kv_read8_impl(const q4k_paged_cache8 *c8, const q4k_read8_args *a, vo
     p.pdl = a->flags & Q4K_FLAG_PDL;
     const bool wide = wide_codes(c->k, p.k_page, p.k_slot, p.k_head) && wide_codes(c->v, p.v_page, p.v_slot, p.v_head) &&
                       wide_rows(a->k, a->type, p.k.yt, p.k.yh) && wide_rows(a->v, a->type, p.v.yt, p.v.yh);
-    const int hold = kRows * (32 / p.lanes);
+    p.lanes = lanes_of(c->dim, 4);   // 8 codes a lane
+    const int hold = 8 * (32 / p.lanes);
     const int64_t warps = (n + hold - 1) / hold * (p.k.heads + p.v.heads);
     auto kern = wide ? read8_kernel<true> : read8_kernel<false>;
     return launch(kern, p, (warps + kWarps - 1) / kWarps, kWarps * 32, stream) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
