@@ -313,15 +313,19 @@ __global__ void __launch_bounds__(RowsShape<CT, NT, RG, DP>::kThreads, 1) rows_k
                 ids = holes ? -1 : 0;   // (-1: `fill` looks whether any row sees the block)
             }
         };
+        // 8 bits: a lane per scale of a slot, of its keys, then of its values
+        const float *scale0 = nullptr;
+        int64_t scale_page = 0, scale_block = 0;
+        if constexpr (EIGHT) {
+            scale0 = lane < 16 ? a.ks + head * a.ks_head : a.vs + head * a.vs_head;
+            scale_page = lane < 16 ? a.ks_page : a.vs_page, scale_block = lane < 16 ? a.ks_block : a.vs_block;
+        }
         // block i into its slot, by the group's first warp
         auto fill = [&](int i, uint32_t f) {
             const int s = static_cast<int>(f % SLOTS);
             const uint32_t dst = ring + s * 2 * Sp::kSide, bar = smem_u32(&sh.full[kg][s]);
-            // a lane per scale: of the slot's keys, then of its values
             auto fill_scale = [&](int page, int slot, bool live) {
-                const float *p = lane < 16 ? a.ks + page * a.ks_page + (slot >> a.block_shift) * a.ks_block + head * a.ks_head
-                                           : a.vs + page * a.vs_page + (slot >> a.block_shift) * a.vs_block + head * a.vs_head;
-                copy4(smem_u32(&sh.scales[kg][s][EIGHT ? lane : 0]), p, live);
+                copy4(smem_u32(&sh.scales[kg][s][EIGHT ? lane : 0]), scale0 + page * scale_page + (slot >> a.block_shift) * scale_block, live);
             };
             if constexpr (TMA) {
                 if (i > 0 && (i & 31) == 0) look(i), check();
@@ -547,16 +551,19 @@ __global__ void __launch_bounds__(RowsShape<CT, NT, RG, DP>::kThreads, 1) rows_k
                         const uint4 lo = ld_shared16(box + chunk_at<Sp::kBox>(row0, c)), hi = ld_shared16(box + chunk_at<Sp::kBox>(row0 + 8, c));
                         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t k0, k1, k2, k3;
-                            key_pairs<CT>(wl[i], k0, k2);
-                            key_pairs<CT>(wh[i], k1, k3);
+                        for (int i = 0; i < 4; i += 2) {   // two k-steps, whose queries are one load
+                            uint32_t k[2][4];
+                            key_pairs<CT>(wl[i], k[0][0], k[0][2]);
+                            key_pairs<CT>(wh[i], k[0][1], k[0][3]);
+                            key_pairs<CT>(wl[i + 1], k[1][0], k[1][2]);
+                            key_pairs<CT>(wh[i + 1], k[1][1], k[1][3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int p = 0; p < PARTS; ++p) {
-                                    const uint2 q = reinterpret_cast<const uint2 *>(&sh.q[p][rg * NT + nt][2 * b + (i >> 1)][lane])[i & 1];
-                                    mma_t<FT>(acc[nt][PARTS > 1 ? p : i & 1], k0, k1, k2, k3, q.x, q.y);
+                                    const uint4 q = sh.q[p][rg * NT + nt][2 * b + (i >> 1)][lane];
+                                    mma_t<FT>(acc[nt][PARTS > 1 ? p : 0], k[0][0], k[0][1], k[0][2], k[0][3], q.x, q.y);
+                                    mma_t<FT>(acc[nt][PARTS > 1 ? p : 1], k[1][0], k[1][1], k[1][2], k[1][3], q.z, q.w);
                                 }
                         }
                     }
