@@ -675,12 +675,19 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
  * values below 2^-38 of the row's largest lose bits) and the weights, with their
  * values' scales, are rounded once to fp16 (2^-11 at most); with fp32 q or out, or a
  * softcap above 256, both enter as two fp16 parts (22 bits).  A weight times its value's
- * scale counts to 2^-38 of the largest scale of the values that its tile meets.  The
- * rest is in fp32.
+ * scale counts to 2^-38 of the largest scale of the values that its tile meets (2^-29 in
+ * the many-rows form).  The rest is in fp32.
+ * The many-rows form (prompt chunks; fp16 or bf16 q and out, dim up to 128, pages of a
+ * multiple of 16 slots) turns the codes into fp16 scratch first.  With blocks of 16 tokens
+ * or more they stay exact; with smaller ones scale * code, over a power of two for each 16
+ * tokens, is rounded once to fp16 (2^-11).  It takes 4 * dim bytes of stream-ordered scratch
+ * a table position of each sequence and cache head, up to 1 GiB; past that the cache heads
+ * go through in passes, and a call that has no room for one head takes another form
+ * (asked for by name it is refused), as does one of 65535 sequences or more.
  * Slots that no token of a sequence's query tile sees may hold anything, their scales
  * too.  A block whose scale a token sees must have one that is finite.
  *   dim a multiple of 16 up to 256; k and v 16-byte aligned, with strides that keep
- *   every row 16-byte aligned; everything else, scratch among it, as q4k_paged_attention.
+ *   every row 16-byte aligned; everything else as q4k_paged_attention.
  */
 q4k_status q4k_paged_attention8(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream);
 
