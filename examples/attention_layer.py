@@ -1,7 +1,7 @@
 """One attention layer of a Q4_K model on the GPU: the quantized products with the rotation, the paged cache and the
 attention between them, as an engine runs them.
 
-    python examples/attention_layer.py [--batch 4] [--prompt 1000] [--steps 16]
+    python examples/attention_layer.py [--batch 4] [--prompt 1000] [--steps 16] [--cache bf16|int8|e4m3] [--norms]
 
 A prompt goes through in chunks (bf16 activations, tensor-core products), then tokens are decoded one by one from a
 CUDA graph in which every launch is a programmatic dependent of the one before.  The shapes are those of a
@@ -35,9 +35,42 @@ class PagedCache:
     def args(self, start):
         return self.k, self.v, self.pages, start, self.lengths
 
+    def append(self, k, v, q, start, table, norms, q_out=None, q_dtype=None, pdl=False):
+        """New keys and values of as many tokens of each sequence into the cache, the keys and queries normed by `norms`
+        (two weights, or None) and turned -> the queries."""
+        if norms is None:
+            return q4k.kv_append(k, v, *self.args(start), table=table, q=q, q_out=q_out, q_dtype=q_dtype, pdl=pdl)
+        n = q.shape[0] // self.lengths.shape[0]
+        pos = (self.lengths[:, None] - n + torch.arange(n, dtype=torch.int32, device="cuda")).flatten()
+        q, k = q4k.norm_rope(q, k, pos, table, *norms, q_out, out_dtype=q_dtype, pdl=pdl)
+        q4k.kv_append(k, v.to(k.dtype), *self.args(start), pdl=pdl)     # (nothing left to turn)
+        return q
+
+    def attend(self, q, start, **kw):
+        return q4k.paged_attention(q, *self.args(start), **kw)
+
+
+class PagedCache8(PagedCache):
+    """The same in 8 bits: codes, and a scale for each block of tokens and head."""
+
+    def __init__(self, batch, capacity, heads, dim, page=16, dtype=torch.int8, block=None, seed=0):
+        super().__init__(batch, capacity, heads, dim, page, dtype, seed)
+        self.k_scale, self.v_scale = (torch.zeros(self.k.shape[0], page // (block or page), heads, device="cuda") for _ in range(2))
+
+    def args(self, start):
+        return self.k, self.v, self.k_scale, self.v_scale, self.pages, start, self.lengths
+
+    def append(self, k, v, q, start, table, norms, q_out=None, q_dtype=None, pdl=False):
+        q_weight, k_weight = norms or (None, None)          # (in the same launch here)
+        return q4k.kv_append8(k, v, *self.args(start), table=table, q=q, q_out=q_out, q_dtype=q_dtype, q_weight=q_weight,
+                              k_weight=k_weight, pdl=pdl)
+
+    def attend(self, q, start, **kw):
+        return q4k.paged_attention8(q, *self.args(start), **kw)
+
 
 class AttentionLayer:
-    def __init__(self, hidden=3584, heads=28, kv_heads=4, dim=128, context=32768, base=1000000.0, seed=1):
+    def __init__(self, hidden=3584, heads=28, kv_heads=4, dim=128, context=32768, base=1000000.0, seed=1, norms=False):
         self.hidden, self.heads, self.kv_heads, self.dim = hidden, heads, kv_heads, dim
         # synthetic weights with a mean near 0
         def weights(rows, cols, tag):
@@ -51,6 +84,10 @@ class AttentionLayer:
         self.wq, self.wk, self.wv = weights(heads * dim, hidden, 1), weights(kv_heads * dim, hidden, 2), weights(kv_heads * dim, hidden, 3)
         self.wo = weights(hidden, heads * dim, 4)
         self.table = q4k.rope_table(context, dim, base)
+        self.norms = None       # weights of the query and key heads' norms, where the model has them
+        if norms:
+            g = torch.Generator().manual_seed(seed)
+            self.norms = tuple((1 + 0.1 * torch.randn(dim, generator=g)).cuda() for _ in range(2))
 
     def _heads(self, y, n):
         return y.view(-1, n, self.dim)
@@ -58,18 +95,17 @@ class AttentionLayer:
     def prefill(self, x, cache, start):
         """x bf16 [tokens, hidden]: the sequences' next chunks, cache.lengths already counting them -> fp32."""
         q, k, v = (q4k.gemm_prefill(w, x) for w in (self.wq, self.wk, self.wv))
-        q = q4k.kv_append(self._heads(k, self.kv_heads), self._heads(v, self.kv_heads), *cache.args(start), table=self.table,
-                          q=self._heads(q, self.heads), q_dtype=torch.bfloat16)
-        y = q4k.paged_attention(q, *cache.args(start))
+        q = cache.append(self._heads(k, self.kv_heads), self._heads(v, self.kv_heads), self._heads(q, self.heads), start, self.table,
+                         self.norms, q_dtype=torch.bfloat16)
+        y = cache.attend(q, start)
         return q4k.gemm_prefill(self.wo, y.view(x.shape[0], -1))
 
     def decode(self, x, cache, start, pdl=True):
         """x fp32 [sequences, hidden]: a token each -> fp32."""
         q, k, v = q4k.gemv_grouped([self.wq, self.wk, self.wv], x, pdl=pdl)
         q = self._heads(q, self.heads)
-        q4k.kv_append(self._heads(k, self.kv_heads), self._heads(v, self.kv_heads), *cache.args(start), table=self.table, q=q,
-                      q_out=q, pdl=pdl)
-        y = q4k.paged_attention(q, *cache.args(start), pdl=pdl)
+        q = cache.append(self._heads(k, self.kv_heads), self._heads(v, self.kv_heads), q, start, self.table, self.norms, q_out=q, pdl=pdl)
+        y = cache.attend(q, start, pdl=pdl)
         return q4k.gemv(self.wo, y.view(x.shape[0], -1), pdl=pdl)
 
 
@@ -79,9 +115,12 @@ def main():
     ap.add_argument("--prompt", type=int, default=1000)
     ap.add_argument("--chunk", type=int, default=512)
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--cache", choices=("bf16", "int8", "e4m3"), default="bf16")
+    ap.add_argument("--norms", action="store_true", help="norms of the query and key heads")
     a = ap.parse_args()
-    layer = AttentionLayer()
-    cache = PagedCache(a.batch, a.prompt + a.steps + 1, layer.kv_heads, layer.dim)
+    layer = AttentionLayer(norms=a.norms)
+    kind, dtype = {"bf16": (PagedCache, torch.bfloat16), "int8": (PagedCache8, torch.int8), "e4m3": (PagedCache8, torch.float8_e4m3fn)}[a.cache]
+    cache = kind(a.batch, a.prompt + a.steps + 1, layer.kv_heads, layer.dim, dtype=dtype)
     g = torch.Generator(device="cuda").manual_seed(7)
     x = torch.randn(a.batch, a.prompt, layer.hidden, generator=g, device="cuda").bfloat16()
     torch.cuda.synchronize()
