@@ -357,11 +357,10 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
                        (c->pages == 1 || (stride_ok(c->k_page_stride) && stride_ok(c->v_page_stride)));
     l.boxes = boxes && p.capacity > 0;
     // (Over 8-bit caches the keys and values lie in scratch, and queries that are not fp16; one
-    // head's has to fit it.)
+    // head of a sequence has to fit it.)
     const bool queries = p.group <= attn::kChunkRows && a->scale >= 0.0f &&
                          ((c8 && a->q_type != Q4K_F16) || ((c->tokens == 1 || stride_ok(q_token)) && (a->q_heads == 1 || stride_ok(q_head))));
-    const bool pieces = c8 ? c->page_size % 16 == 0 && p.capacity > 0 && p.batch < 65535 && attn::widened_bytes(p) <= attn::kWidenMost
-                            : l.boxes;
+    const bool pieces = c8 ? c->page_size % 16 == 0 && p.capacity > 0 && attn::widened_bytes(p) <= attn::kWidenMost : l.boxes;
     const int (*room)[attn::kMaxCluster + 1];
     if (attn::room_of(l.device, &room) != cudaSuccess) return Q4K_ERR_CUDA;
     const int parts = !l.parts_many ? 1 : c->type == Q4K_BF16 ? 3 : 2;

@@ -210,6 +210,7 @@ struct Split {
                 if (extra(m) <= x) b = m; else e = m - 1;
             }
             j = x - extra(b) + 1;
+            if (j < 1) j = -1;   // (the first sequence does not begin with the call's first row)
         }
         const int s0 = start_of(b), n = start_of(b + 1) - s0, all = n * a.group;
         const int raw = a.batch <= kSeqs ? sh.len[b] : a.kv_len[b];

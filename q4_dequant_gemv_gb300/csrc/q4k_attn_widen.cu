@@ -171,59 +171,65 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
     }
 }
 
-// Bytes of the widened keys, values and factors of one cache head.
+// Bytes of the widened keys, values and factors of one cache head of one sequence.
 int64_t widened_bytes(const Args &a)
 {
-    const int64_t pages = static_cast<int64_t>(a.batch) * ((a.capacity + kPage - 1) / kPage);
-    return pages * (2 * kPage * 2 * static_cast<int64_t>(a.dim) + 64);
+    return (a.capacity + static_cast<int64_t>(kPage) - 1) / kPage * (2 * kPage * 2 * static_cast<int64_t>(a.dim) + 64);
 }
 
-// As many cache heads a pass as kWidenMost bytes hold, one at least.
+// As many cache heads of all sequences a pass as kWidenMost bytes hold, or of one head as many sequences.
 cudaError_t launch_widened(const ChunkLaunch &l)
 {
     const Args &all = l.args;
-    const int64_t per_head = widened_bytes(all);
-    const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(all.kv_heads, kWidenMost / std::max<int64_t>(per_head, 1))));
-    const int passes = (all.kv_heads + most - 1) / most, per = (all.kv_heads + passes - 1) / passes;   // (about alike)
+    const int64_t fit = std::max<int64_t>(1, kWidenMost / widened_bytes(all));
+    auto alike = [](int n, int64_t most) {   // passes of about as many
+        const int passes = static_cast<int>((n + most - 1) / most);
+        return (n + passes - 1) / passes;
+    };
+    const int heads = alike(all.kv_heads, std::max<int64_t>(1, fit / all.batch));
+    const int seqs = alike(all.batch, std::min<int64_t>({fit, all.batch, 65534}));   // (a grid's y)
     const int table_pages = (all.capacity + kPage - 1) / kPage;
-    const int64_t pages = static_cast<int64_t>(all.batch) * table_pages;
-    if (pages > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const int64_t pages = static_cast<int64_t>(seqs) * table_pages;
     const bool turn = all.q_type != Q4K_F16;
     auto room = [](int64_t n) { return (n + 255) / 256 * 256; };
-    const int64_t side = room(pages * per * kPage * all.dim * 2), fac = room(pages * per * 64);
-    const int64_t rows = static_cast<int64_t>(all.tokens) * per * all.group;
+    const int64_t side = room(pages * heads * kPage * all.dim * 2), fac = room(pages * heads * 64);
+    const int64_t rows = static_cast<int64_t>(all.tokens) * heads * all.group;
     const int64_t q = turn ? room(rows * all.dim * 2) : 0, scale = turn ? room(rows * 4) : 0;
     void *scratch = nullptr;
     cudaError_t e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream);
     if (e != cudaSuccess) return e;
     uint8_t *at = static_cast<uint8_t *>(scratch);
-    for (int h0 = 0; h0 < all.kv_heads && e == cudaSuccess; h0 += per) {
+    auto pass = [&](int h0, int b0) {
         WidenArgs w{};
         Args &a = w.a;
         a = all;
-        a.kv_heads = std::min(per, all.kv_heads - h0), a.heads = a.kv_heads * all.group, a.table_pages = table_pages;
+        a.kv_heads = std::min(heads, all.kv_heads - h0), a.heads = a.kv_heads * all.group, a.table_pages = table_pages;
+        a.batch = std::min(seqs, all.batch - b0);
+        a.seq_start += b0, a.kv_len += b0, a.page_table += b0 * all.table_stride;
+        if (all.prefix_len) a.prefix_len += b0;
         a.k = static_cast<const uint8_t *>(all.k) + h0 * all.k_head, a.v = static_cast<const uint8_t *>(all.v) + h0 * all.v_head;
-        a.ks = all.ks + h0 * all.ks_head, a.vs = all.vs + h0 * all.vs_head;
+        a.ks += h0 * all.ks_head, a.vs += h0 * all.vs_head;
         const int64_t hq = static_cast<int64_t>(h0) * all.group;
         a.q = static_cast<const uint16_t *>(all.q) + hq * all.q_head, a.out = static_cast<uint16_t *>(all.out) + hq * all.out_head;
-        if (all.lse) a.lse = all.lse + hq;
-        if (all.slopes) a.slopes = all.slopes + hq;
+        if (all.lse) a.lse += hq;
+        if (all.slopes) a.slopes += hq;
         w.k = reinterpret_cast<__half *>(at), w.v = reinterpret_cast<__half *>(at + side);
         w.factors = reinterpret_cast<float *>(at + 2 * side);
         if (turn) w.q = reinterpret_cast<__half *>(at + 2 * side + fac), w.row_scale = reinterpret_cast<float *>(at + 2 * side + fac + q);
         cudaLaunchConfig_t cfg = {};
-        // up to eight CTAs an SM in all, each sequence's pieces dealt out over its share
-        const int64_t q_ctas = turn ? (static_cast<int64_t>(all.tokens) * a.heads + 15) / 16 : 1;
+        // up to eight CTAs an SM in all, each sequence's pieces dealt out over its share; the heads' queries once
+        const bool queries = turn && b0 == 0;
+        const int64_t q_ctas = queries ? (static_cast<int64_t>(all.tokens) * a.heads + 15) / 16 : 1;
         const int x = static_cast<int>(std::max<int64_t>(std::min<int64_t>(2 * static_cast<int64_t>(table_pages) * a.kv_heads,
-                                                                           (8 * l.sms + all.batch - 1) / all.batch),
+                                                                           (8 * l.sms + a.batch - 1) / a.batch),
                                                          std::min<int64_t>(q_ctas, 4 * l.sms)));
-        cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(all.batch + (turn ? 1 : 0)));
+        cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(a.batch + (queries ? 1 : 0)));
         cfg.blockDim = kWidenThreads;
         cfg.stream = l.stream;
         // (a later pass writes what the one before it reads)
-        const Attributes attributes(&cfg, 0, all.pdl && h0 == 0);
-        e = cudaLaunchKernelEx(&cfg, widen_kernel, w);
-        if (e != cudaSuccess) break;
+        const Attributes attributes(&cfg, 0, all.pdl && h0 == 0 && b0 == 0);
+        const cudaError_t err = cudaLaunchKernelEx(&cfg, widen_kernel, w);
+        if (err != cudaSuccess) return err;
         ChunkLaunch ch = l;
         Args &c = ch.args;
         c = a;
@@ -233,8 +239,10 @@ cudaError_t launch_widened(const ChunkLaunch &l)
         c.pages = static_cast<int>(pages), c.page_size = kPage, c.page_shift = 7;
         c.q_type = Q4K_F16, c.pdl = true;
         if (turn) c.q = w.q, c.q_head = a.dim, c.q_token = static_cast<int64_t>(a.heads) * a.dim;
-        e = launch_chunk_wide(ch);
-    }
+        return launch_chunk_wide(ch);
+    };
+    for (int h0 = 0; h0 < all.kv_heads && e == cudaSuccess; h0 += heads)
+        for (int b0 = 0; b0 < all.batch && e == cudaSuccess; b0 += seqs) e = pass(h0, b0);
     const cudaError_t f = cudaFreeAsync(scratch, l.stream);
     return e == cudaSuccess ? f : e;
 }

@@ -183,19 +183,24 @@ def test_a_failure_is_not_kept(fake, form, name, skip):   # noqa: F811
 
 
 def test_passes_of_heads(fake):   # noqa: F811
-    """A widened cache past a gigabyte goes through in passes of as many heads as fit, one past it for a head not at all."""
+    """A widened cache past 4 GiB goes through in passes of as many heads as fit, then of sequences, one past it for a head of
+    a sequence not at all."""
     L = _bind(fake)
     def call(heads, most, form=7, batch=1, tokens=2):
         c = _cache8(size=128, heads=heads, dim=128, block=16, kh=128, ks=128 * heads, kp=128 * 128 * heads, vh=128, vs=128 * heads,
                     vp=128 * 128 * heads, pages=1 << 20, row=most, most=most, batch=batch, tokens=tokens)
         return L.q4k_paged_attention8(c, _attention(heads=heads, qt=128 * heads, qh=128, ot=128 * heads, oh=128, flags=form << 8), 0)
-    assert call(8, 1024) == 0          # 131072 positions of 8 heads: 0.5 GB
-    assert [b"widen" in x.kernel for x in fake.launches()].count(True) == 1
-    assert call(8, 4096) == 0          # four times as many: 2 GB
-    got = [x for x in fake.launches() if b"widen" in x.kernel]
-    assert len(got) == 3 and fake.blocks(0) == 0
-    assert call(1, 1 << 15) == 1       # 4 million positions of a head: 2 GB
-    assert call(1, 1 << 15, form=0) == 0 and not any(b"widen" in x.kernel for x in fake.launches())
+    for heads, most, batch, passes in ((8, 1024, 1, 1),       # 131072 positions of 8 heads: 0.5 GiB
+                                       (8, 1024, 16, 3),      # 8 GiB and a little more
+                                       (3, 16384, 1, 1), (3, 16384, 2, 3),      # a head 2 GiB
+                                       (2, 30000, 5, 6),      # a sequence 1.8: two a pass
+                                       (1, 8, 70000, 9)):     # 512 KiB a sequence
+        assert call(heads, most, batch=batch) == 0
+        got = fake.launches()
+        assert [b"widen" in x.kernel for x in got].count(True) == passes and len(got) == 3 * passes, (heads, most, batch)
+        assert fake.blocks(0) == 0
+    assert call(1, 1 << 16) == 1       # 8 million positions of a head: 4 GiB and the factors
+    assert call(1, 1 << 16, form=0) == 0 and not any(b"widen" in x.kernel for x in fake.launches())
 
 
 def test_wide_and_narrow_rows(fake):   # noqa: F811

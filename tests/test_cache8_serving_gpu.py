@@ -171,11 +171,11 @@ def test_old_contents_of_pages(q4k, form):
 
 @pytest.mark.parametrize("qt,block,first", [(BF16, 16, False), (F16, 4, True)])
 def test_passes_of_heads(q4k, qt, block, first):
-    """A page table of half a million positions: the widened keys and values of 6 heads take 1.6 GB, so they go in passes."""
+    """A page table of a million positions: the widened keys and values of 6 heads take 6.6 GB, so they go in passes."""
     g = torch.Generator().manual_seed(61)
     H, KH, D, page, lens, new = 12, 6, 128, 128, [700, 90], [150, 33]
     ((kc, ks, keys), (vc, vs, vals)), pt = _cache(g, lens, page, block, KH, D, I8, first)
-    wide = torch.full((2, 2100), -1, dtype=torch.int32)
+    wide = torch.full((2, 8500), -1, dtype=torch.int32)
     wide[:, :pt.shape[1]] = pt
     q = torch.randn(sum(new), H, D, generator=g).to(qt)
     slopes = torch.tensor([2.0 ** (-0.5 * i - 1) for i in range(H)])
@@ -200,12 +200,41 @@ def test_passes_of_heads(q4k, qt, block, first):
     assert q4k.device_error_flags() == 0
 
 
+@pytest.mark.parametrize("ct,qt,mask", [(I8, BF16, {}), (E4M3, F16, dict(window=60)), (I8, BF16, dict(prefix=[30, 200, 0, 90, 5])),
+                                        (E4M3, BF16, dict(kv_start=True))])
+def test_passes_of_sequences(q4k, ct, qt, mask):
+    """A page table of three million positions: two sequences of a head a pass, five sequences, three of them with no new tokens
+    at an end or between."""
+    g = torch.Generator().manual_seed(63)
+    H, KH, D, page, lens, new = 4, 2, 128, 64, [300, 40, 129, 700, 90], [0, 40, 0, 133, 260]
+    lens[4] = 260
+    ((kc, ks, keys), (vc, vs, vals)), pt = _cache(g, lens, page, 4, KH, D, ct)
+    wide = torch.full((5, 3 * 2 ** 20 // page), -1, dtype=torch.int32)
+    wide[:, :pt.shape[1]] = pt
+    case = dict(new=new, len=lens, **mask)
+    if mask.get("kv_start"):
+        case["kv_start"] = [(n - m + i) // 50 * 50 for n, m in zip(lens, new) for i in range(m)]
+    q = torch.randn(sum(new), H, D, generator=g).to(qt)
+    lse = torch.zeros(sum(new), H, device="cuda")
+    kw = dict(window=mask.get("window", 0), prefix_len=None if "prefix" not in mask else _dev(mask["prefix"]),
+              kv_start=None if "kv_start" not in mask else _dev(case["kv_start"]))
+    call = lambda **more: q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, wide.cuda(), _dev(_starts(new)), _dev(lens), lse=lse,
+                                               form="many", **kw, **more)
+    y = call()
+    ref, rl, bound, off = _bound(q, keys, vals, case, 1 / math.sqrt(D), qt, True, vs, vc)
+    assert ((y.double().cpu() - ref).abs() <= bound).all()
+    assert ((lse.double().cpu() - rl).abs() <= 2.0 ** -12 + 2.0 ** -20 * rl.abs() + off).all()
+    for _ in range(3):
+        assert torch.equal(call(pdl=True), y)
+    assert q4k.device_error_flags() == 0
+
+
 def test_no_room_for_a_head(q4k):
-    """Past a gigabyte for one head the widened form is refused by name and not chosen by itself."""
+    """Past 4 GiB for one head of a sequence the widened form is refused by name and not chosen by itself."""
     g = torch.Generator().manual_seed(71)
     H, KH, D, page, lens, new = 4, 2, 64, 16, [400], [300]
     ((kc, ks, keys), (vc, vs, vals)), pt = _cache(g, lens, page, 16, KH, D, I8)
-    wide = torch.full((1, 2 ** 22 // page + 1), -1, dtype=torch.int32)
+    wide = torch.full((1, 2 ** 24 // page + 1), -1, dtype=torch.int32)
     wide[:, :pt.shape[1]] = pt
     q = torch.randn(300, H, D, generator=g).bfloat16()
     args = (q.cuda(), kc, vc, ks, vs, wide.cuda(), _dev([0, 300]), _dev(lens))
