@@ -37,8 +37,9 @@
 // 16 of them has a factor.  Warp 11 hands the factors of the units on, some ahead.  The
 // keys' multiply the scores, the values' join the exponents of P by their log2, over the
 // largest so far, by which O is rescaled as by a maximum; the sum of a piece loses it
-// again.  Nothing of it costs a score more than it did; the code of its own does not
-// touch the other instances.
+// again.  That is a multiplication a piece and row, and no instruction a score more; three
+// chunks of 512 over 4096 take 79 us where the 16-bit kernel takes 69, 2048 tokens over
+// 14336 345 where it takes 300 (each launch by itself).
 //
 // Every wait is bounded in time: on a timeout the CTA sets bit 3 of the error word,
 // stops, waits (bounded) for its copies and products in flight, frees its tensor

@@ -24,6 +24,8 @@
 // 1000 positions takes 7.1 us with a table of 1000, 11.2 (split, the cluster form
 // still 7.1) with one of 16384 or more; sixteen over 4096 28.2 and, in a table of
 // 32768, 36.1 (clusters 27.9).  Such a caller can ask for the form.
+// 8-bit caches take the same estimate: over 14 calls of theirs (1 to 64 sequences of 1 to
+// 128 tokens, 500 to 131072 positions) its choice was the fastest form or within 13 % of it.
 #pragma once
 #include <algorithm>
 #include <cmath>

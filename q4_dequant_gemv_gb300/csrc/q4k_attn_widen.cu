@@ -15,7 +15,11 @@
 // that is not in the cache has factors of -inf; the kernel knows whether a row sees it.
 // bf16 queries become fp16 over a power of two a row here too.
 //
-// Bound by memory: 3 bytes a code (32 / 8 heads of 128, 16384 positions: 100 MB).
+// Bound by memory: 3 bytes a code and 4 an element of the queries.  Three chunks of 512 over
+// 4096, 32 / 8 heads of 128 (28 M codes, 110 MB): 15.7 us of the call's 111 (the kernel 79,
+// its join 21, each by itself), 2048 over 14336 (34 M codes, 134 MB) 26 of 395 (345, 20); with
+// the conversion inside the kernel they took 142 and 537, the mma.sync kernel takes 753 for
+// the first.
 #include <cuda_runtime.h>
 
 #include <algorithm>
