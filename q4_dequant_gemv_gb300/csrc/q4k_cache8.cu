@@ -612,9 +612,10 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
         const int from = k * groups + g;
         const int row = __shfl_sync(0xffffffffu, mine.row, from), state = __shfl_sync(0xffffffffu, mine.state, from);
         if (h.weight) norm<E>(r[k], wt, a.lanes, a.over_dim, a.eps);
-        most[k] = 0.0f;
+        most[k] = -1.0f;   // (a block without a token that has a place stays as it is)
         if (state == 1 && (there >> k & 1)) {
             good |= 1u << k;
+            most[k] = 0.0f;
             if (h.rot) {
                 Turn<E> by;
                 load_turn<WIDE, E, INTER>(by, a.table + static_cast<int64_t>(row) * a.rot, l, h.rot);
@@ -644,7 +645,7 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
     if (a.warps > 1) {
         if (lane == 0) s_max[w] = most[0];
         __syncthreads();
-        float m = 0.0f;
+        float m = -1.0f;
         for (int z = 0; z < a.warps; ++z) m = fmaxf(m, s_max[w - w % a.warps + z]);
 #pragma unroll
         for (int k = 0; k < kRows; ++k) most[k] = m;
@@ -679,9 +680,9 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
         uint8_t *to = codes + page * c_page + sl * c_slot + head * c_head;
         if (good >> k & 1) {
             store_codes<WIDE, E, INTER>(to, a.codes, l, h.rot, a.inter, r[k], inv);
-            // the block's first new position writes its scale
-            if (l.u == 0 && ((q & (a.block - 1)) == 0 || q == p0)) *scale_at(page, sl) = s;
-        } else if (in_first && q < p0 && state == 1 && l.live && s != before) {
+            // (every token of a block writes the same scale: which of them have a place differs)
+            if (l.u == 0) *scale_at(page, sl) = s;
+        } else if (in_first && q < p0 && state == 1 && l.live && most[k] >= 0.0f && s != before) {
             scale_codes<E, INTER>(to, a.codes, before * inv, l);
         }
     }

@@ -87,6 +87,53 @@ def test_a_sequence_step_by_step(q4k, ct, page, block, qt):
     assert q4k.device_error_flags() == 0
 
 
+@pytest.mark.parametrize("ct", [I8, E4M3])
+@pytest.mark.parametrize("block,bad", [(4, [0, 4, 9]), (4, [1, 2, 3]), (16, [0]), (16, [3, 4]), (64, [0, 1, 2, 3]), (64, range(40)),
+                                       (1, [0, 5])])
+def test_tokens_without_a_place_in_a_block(q4k, ct, block, bad):
+    """Keys whose rotation row lies outside the table are left out and flagged, wherever in a block they are: the others of it
+    get a scale of their own, and a block that gets none keeps its codes and its scale, even one below the least."""
+    n, past, KH, D, page = 40, 3, 2, 64, 64
+    g = torch.Generator().manual_seed(33)
+    cache = plain8.Cache([past + n], past + n, page, block, KH, D, ct, seed=7)
+    for s in cache.scales:
+        s[cache.table[0, 0].long(), 0] = 1e-39 if len(bad) == n else 1e-3
+    dev = cache.device()
+    k, v = (torch.randn(n, KH, D, generator=g) for _ in range(2))
+    tab = plain.table(64, D)
+    pos = torch.arange(past, past + n)
+    pos[list(bad)] = 10 ** 6
+    q4k.kv_append8(k.cuda(), v.cuda(), *dev[:4], dev[4], _dev([0, n]), _dev([past + n]), table=tab.cuda(), pos=_dev(pos))
+    torch.cuda.synchronize()
+    assert q4k.device_error_flags() == 4
+    q4k.device_error_clear()
+    after = copy.copy(cache)
+    after.codes, after.scales = [t.cpu() for t in dev[:2]], [t.cpu() for t in dev[2:4]]
+    after.touched, after.blocks = [set(), set()], [set(), set()]
+    plain8.check_append(cache, after, 1, 0, v.double(), torch.zeros(n, KH, D, dtype=torch.float64), past)
+    good = [i for i in range(n) if i not in bad]
+    x, err = plain8.heads(k[good], None, EPS, tab[torch.tensor(good, dtype=torch.long) + past], False)
+    for first in range(0, past + n, block):
+        here = [j for j, i in enumerate(good) if first <= past + i < first + block]
+        at = [past + good[j] for j in here]
+        old = list(range(first, min(first + block, past)))
+        pg, slot = cache.where(0, [first])
+        was, got = (c.scales[0][int(pg), int(slot) // block].double() for c in (cache, after))
+        every = torch.arange(first, min(first + block, past + n))
+        if not here:
+            assert torch.equal(was, got)
+            where = cache.where(0, every)
+            assert torch.equal(*(c.codes[0].view(torch.uint8)[where] for c in (cache, after)))
+            continue
+        want = (x[here].abs().amax((0, 2)) / plain8.TOP[ct]).clamp(min=plain8.LEAST)
+        want = torch.maximum(want, was) if old else want
+        assert ((got - want).abs() <= err[here].amax((0, 2)) / plain8.TOP[ct] + 2.0 ** -23 * want).all()
+        y = x[here] / got[:, None]
+        off = (after.values(0, 0, at) / got[:, None] - y).abs()
+        near = plain8.half_step(y * (1 + 2.0 ** -20), ct) * (1 + 2.0 ** -20) + err[here] / got[:, None] + y.abs() * 2.0 ** -22
+        assert (off <= near).all()
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_graphs_share_scratch(q4k, form):
     """Two captured graphs and eager calls in turn, all on the library's one pool of scratch, each with lengths and values
