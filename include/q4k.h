@@ -683,7 +683,8 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
  * tokens, is rounded once to fp16 (2^-11).  It takes 4 * dim bytes of stream-ordered scratch
  * a table position of each sequence and cache head, up to 4 GiB; past that heads, then
  * sequences go through in passes, and where one head of one sequence has no room the call
- * takes another form (asked for by name it is refused).
+ * takes another form (asked for by name it is refused).  (Where the device has less to
+ * give the passes get smaller.)
  * Slots that no token of a sequence's query tile sees may hold anything, their scales
  * too.  A block whose scale a token sees must have one that is finite.
  *   dim a multiple of 16 up to 256; k and v 16-byte aligned, with strides that keep

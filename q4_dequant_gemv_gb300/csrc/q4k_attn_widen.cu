@@ -32,6 +32,7 @@
 namespace q4k {
 namespace attn {
 
+constexpr int64_t kWidenLeast = int64_t{64} << 20;   // (a pass of no more than this many bytes is not divided)
 constexpr int kWidenThreads = 256, kWidenWarps = kWidenThreads / 32, kPage = 128;
 static_assert(kPage == kChunkKeys, "a unit of the many-rows kernel");
 
@@ -181,26 +182,34 @@ int64_t widened_bytes(const Args &a)
     return (a.capacity + static_cast<int64_t>(kPage) - 1) / kPage * (2 * kPage * 2 * static_cast<int64_t>(a.dim) + 64);
 }
 
-// As many cache heads of all sequences a pass as kWidenMost bytes hold, or of one head as many sequences.
+// As many cache heads of all sequences a pass as kWidenMost bytes hold, or of one head as many sequences; fewer
+// where the device has no room for that.
 cudaError_t launch_widened(const ChunkLaunch &l)
 {
     const Args &all = l.args;
-    const int64_t fit = std::max<int64_t>(1, kWidenMost / widened_bytes(all));
+    const int table_pages = (all.capacity + kPage - 1) / kPage;
+    const bool turn = all.q_type != Q4K_F16;
+    auto room = [](int64_t n) { return (n + 255) / 256 * 256; };
     auto alike = [](int n, int64_t most) {   // passes of about as many
         const int passes = static_cast<int>((n + most - 1) / most);
         return (n + passes - 1) / passes;
     };
-    const int heads = alike(all.kv_heads, std::max<int64_t>(1, fit / all.batch));
-    const int seqs = alike(all.batch, std::min<int64_t>({fit, all.batch, 65534}));   // (a grid's y)
-    const int table_pages = (all.capacity + kPage - 1) / kPage;
-    const int64_t pages = static_cast<int64_t>(seqs) * table_pages;
-    const bool turn = all.q_type != Q4K_F16;
-    auto room = [](int64_t n) { return (n + 255) / 256 * 256; };
-    const int64_t side = room(pages * heads * kPage * all.dim * 2), fac = room(pages * heads * 64);
-    const int64_t rows = static_cast<int64_t>(all.tokens) * heads * all.group;
-    const int64_t q = turn ? room(rows * all.dim * 2) : 0, scale = turn ? room(rows * 4) : 0;
+    int heads, seqs;
+    int64_t pages, side, fac, q, scale;
     void *scratch = nullptr;
-    cudaError_t e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream);
+    cudaError_t e;
+    for (int64_t fit = std::max<int64_t>(1, kWidenMost / widened_bytes(all));;) {
+        heads = alike(all.kv_heads, std::max<int64_t>(1, fit / all.batch));
+        seqs = alike(all.batch, std::min<int64_t>({fit, all.batch, 65534}));   // (a grid's y)
+        pages = static_cast<int64_t>(seqs) * table_pages;
+        side = room(pages * heads * kPage * all.dim * 2), fac = room(pages * heads * 64);
+        const int64_t rows = static_cast<int64_t>(all.tokens) * heads * all.group;
+        q = turn ? room(rows * all.dim * 2) : 0, scale = turn ? room(rows * 4) : 0;
+        e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream);
+        if (e != cudaErrorMemoryAllocation || 2 * side <= kWidenLeast || static_cast<int64_t>(heads) * seqs == 1) break;
+        (void)cudaGetLastError();
+        fit = std::max<int64_t>(1, static_cast<int64_t>(heads) * seqs / 2);
+    }
     if (e != cudaSuccess) return e;
     uint8_t *at = static_cast<uint8_t *>(scratch);
     auto pass = [&](int h0, int b0) {

@@ -203,6 +203,25 @@ def test_passes_of_heads(fake):   # noqa: F811
     assert call(1, 1 << 16, form=0) == 0 and not any(b"widen" in x.kernel for x in fake.launches())
 
 
+def test_less_memory_makes_smaller_passes(fake):   # noqa: F811
+    """An allocation that fails is tried again with half the heads, then half the sequences; small ones are not."""
+    L = _bind(fake)
+    def call(heads, most, batch):
+        c = _cache8(size=128, heads=heads, dim=128, block=16, kh=128, ks=128 * heads, kp=128 * 128 * heads, vh=128, vs=128 * heads,
+                    vp=128 * 128 * heads, pages=1 << 20, row=most, most=most, batch=batch)
+        return L.q4k_paged_attention8(c, _attention(heads=heads, qt=128 * heads, qh=128, ot=128 * heads, oh=128, flags=7 << 8), 0)
+    passes = lambda: [b"widen" in x.kernel for x in fake.launches()].count(True)
+    for times, want in ((0, 1), (1, 2), (2, 4), (3, 8), (4, 16)):   # 8 heads of 2 sequences, 64 MiB each
+        fake.fail("cudaMallocFromPoolAsync", times)
+        assert call(8, 1024, 2) == 0 and passes() == want and fake.blocks(0) == 0, times
+    fake.fail("cudaMallocFromPoolAsync", 5)
+    assert call(8, 1024, 2) == 4 and passes() == 0 and fake.blocks(0) == 0
+    fake.fail("cudaMallocFromPoolAsync", 1)
+    assert call(8, 8, 2) == 4 and passes() == 0
+    fake.fail("cudaMallocFromPoolAsync", 0)
+    assert call(8, 8, 2) == 0 and passes() == 1
+
+
 def test_wide_and_narrow_rows(fake):   # noqa: F811
     """Aligned rows of sizes that fit take the wide kernels; strides that no index uses make no difference."""
     L = _bind(fake)
