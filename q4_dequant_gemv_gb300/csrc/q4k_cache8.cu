@@ -9,10 +9,10 @@
 // tokens of 40 heads, half of each turned.)
 // The norm is one sum over a lane group; pairs turn in the lane that holds them.
 //
-// Measured (device): norms of 4097 tokens of 40 bf16 heads, half of each turned, 27 us
+// Measured (device): norms of 4097 tokens of 40 bf16 heads, half of each turned, 26.9 us
 // (85 MB; the rotation alone moves as much in 18), bound by issue slots and latency alike
-// (6 CTAs of 128 threads an SM; 4: 35 us); three prompts of 2500 tokens, 32 / 8 bf16 heads,
-// appended 51 us (queries in a launch of their own: no less) and read back 13; 65536
+// (6 CTAs of 128 threads an SM; 5: 31 us, 8: 29); three prompts of 2500 tokens, 32 / 8 bf16
+// heads, appended 47 us (queries in a launch of their own: no less) and read back 13; 65536
 // positions of 8 heads read to bf16 76 us, 5.3 TB/s.  One token: 4 to 6 us of launch and
 // index loads.
 //
@@ -443,14 +443,13 @@ __device__ __forceinline__ void turn_rows(const Args &a, const Heads &h, int hea
     for (int k = 0; k < N; ++k)
         if (l.live && first + k * groups < h.heads) there |= 1u << k;
     Pairs<E> r[N];
-    load_rows<WIDE, N, E, INTER>(h.x, h.xtype, t * h.xt + first * h.xh, groups * h.xh, l, h.rot, a.inter, there, r);
     Place at{0, 0, 0, 1};
-    if (APPEND) {
-        at = place_of(a, static_cast<int>(t), h.rot);
-    } else if (h.rot) {
+    if (!APPEND && h.rot) {   // (one load: ahead of the data; the append's chain of them behind it)
         at.row = a.at.pos[t];
         if (at.row < 0 || at.row >= a.at.table_rows) at.state = 2;
     }
+    load_rows<WIDE, N, E, INTER>(h.x, h.xtype, t * h.xt + first * h.xh, groups * h.xh, l, h.rot, a.inter, there, r);
+    if (APPEND) at = place_of(a, static_cast<int>(t), h.rot);
     if (at.state == 2 && lane == 0) atomicOr(&g_cache8_error, 4u);
     if (at.state != 1) return;   // (the whole warp)
     Turn<E> by;
@@ -688,8 +687,9 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
     }
 }
 
-template <bool WIDE, int N, int E, bool INTER>
-__global__ void __launch_bounds__(kMaxWarps * 32) append8_kernel(const __grid_constant__ Args a)
+// FIVE: 96 registers instead of 128, five CTAs of 128 threads an SM instead of four.
+template <bool WIDE, int N, int E, bool INTER, bool FIVE>
+__global__ void __launch_bounds__(FIVE ? 640 : kMaxWarps * 32) append8_kernel(const __grid_constant__ Args a)
 {
     __shared__ float s_max[kMaxWarps];
     pdl_launch_dependents();
@@ -812,8 +812,6 @@ static cudaError_t launch(void (*kern)(Args), const Args &a, int64_t ctas, int t
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Rows a lane group of the queries' side: several where one each would make more
-// warps than the GPU holds.
 // Pairs of a lane, and lanes of a row.
 static int pairs_of(int64_t dim, int64_t rot, bool wide) { return wide && dim > 64 && dim % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
 static int lanes_of(int64_t dim, int e)
@@ -823,6 +821,8 @@ static int lanes_of(int64_t dim, int e)
     return n;
 }
 
+// Rows a lane group of the queries' side: several where one each would make more
+// warps than the GPU holds.
 static bool many_rows(int64_t tokens, int heads, int lanes, int sms)
 {
     return tokens * heads * lanes / 32 >= 32LL * sms;
@@ -978,13 +978,20 @@ q4k_status kv_append8_impl(const q4k_paged_cache8 *c8, const q4k_append8_args *a
     const int64_t each = chunk_heads(many ? 16 / e : 1, p.lanes), q_warps = n * ((p.q.heads + each - 1) / each);
     if (kv_ctas + q_warps > 0x7FFFFFFF) return Q4K_ERR_INVALID_ARG;
     p.kv_ctas = static_cast<int>(kv_ctas);
+    // Many waves of CTAs gain by a fifth on each SM what the spilled registers cost: 7000 tokens of 32 / 8 bf16 heads,
+    // normed, 59.3 us (four CTAs 63.2), of 28 / 4 fp32 heads 54.9 (57.0); 2048 tokens 18.5 (18.6); 1500 fp32 tokens,
+    // three waves, 17.7 (14.5).
+    const int64_t ctas = kv_ctas + (q_warps + warps - 1) / warps;
+    const bool five = ctas * warps >= 24LL * kWarps * sms;
     auto pick = [&](auto inter) {
         constexpr bool INTER = decltype(inter)::value;
-        return e == 8 ? (many ? append8_kernel<true, 2, 8, INTER> : append8_kernel<true, 1, 8, INTER>)
-                      : (many ? append8_kernel<true, 4, 4, INTER> : append8_kernel<true, 1, 4, INTER>);
+        return e == 8 ? (!many  ? append8_kernel<true, 1, 8, INTER, false>
+                         : five ? append8_kernel<true, 2, 8, INTER, true>
+                                : append8_kernel<true, 2, 8, INTER, false>)
+                      : (many ? append8_kernel<true, 4, 4, INTER, false> : append8_kernel<true, 1, 4, INTER, false>);
     };
-    auto kern = !wide ? append8_kernel<false, 1, 4, false> : p.inter ? pick(std::true_type{}) : pick(std::false_type{});
-    return launch(kern, p, kv_ctas + (q_warps + warps - 1) / warps, warps * 32, stream) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+    auto kern = !wide ? append8_kernel<false, 1, 4, false, false> : p.inter ? pick(std::true_type{}) : pick(std::false_type{});
+    return launch(kern, p, ctas, warps * 32, stream) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
 q4k_status kv_read8_impl(const q4k_paged_cache8 *c8, const q4k_read8_args *a, void *stream)

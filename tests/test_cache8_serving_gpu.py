@@ -10,6 +10,7 @@ torch = pytest.importorskip("torch")
 import plain_attention as plain   # noqa: E402
 import plain_cache8 as plain8     # noqa: E402
 from test_attention8_gpu import FORMS, _cache, _floor, _products, _takes   # noqa: E402
+from test_cache8_gpu import _append   # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F32, F16, BF16, I8, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
@@ -132,6 +133,14 @@ def test_tokens_without_a_place_in_a_block(q4k, ct, block, bad):
         off = (after.values(0, 0, at) / got[:, None] - y).abs()
         near = plain8.half_step(y * (1 + 2.0 ** -20), ct) * (1 + 2.0 ** -20) + err[here] / got[:, None] + y.abs() * 2.0 ** -22
         assert (off <= near).all()
+
+
+@pytest.mark.parametrize("dtype,block", [(I8, 64), (E4M3, 128)])
+@pytest.mark.parametrize("xt,inter,rot", [(BF16, False, 128), (F32, True, 64)])
+def test_appends_of_many_waves(q4k, dtype, block, xt, inter, rot):
+    """Thousands of tokens of many heads, enough for the kernel of five CTAs an SM."""
+    cache = plain8.Cache([2500, 400], 2600, 128, block, 2, 128, dtype, seed=12)
+    _append(q4k, cache, [2500, 310], [0, 90], H=48, rot=rot, xt=xt, interleaved=inter, seed=13)
 
 
 @pytest.mark.parametrize("form", FORMS)
