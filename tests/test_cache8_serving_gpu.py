@@ -209,6 +209,45 @@ def test_padded_batches(q4k, form):
 
 
 @pytest.mark.parametrize("form", FORMS)
+def test_rows_before_the_first_sequence(q4k, form):
+    """A call whose first sequence does not begin with its first row: the rows before it stay as they are."""
+    g = torch.Generator().manual_seed(43)
+    H, KH, D, page, lens, new, skip = 8, 2, 64, 16, [200, 77], [150, 9], 301
+    ((kc, ks, _), (vc, vs, _)), pt = _cache(g, lens, page, 16, KH, D, I8)
+    q = torch.randn(skip + sum(new), H, D, generator=g).bfloat16().cuda()
+    start = torch.tensor(_starts(new), dtype=torch.int32).cuda()
+    want = q4k.paged_attention8(q[skip:], kc, vc, ks, vs, pt.cuda(), start, _dev(lens), form=form)
+    out = torch.full_like(q, 7.0)
+    q4k.paged_attention8(q, kc, vc, ks, vs, pt.cuda(), start + skip, _dev(lens), out, form=form)
+    # (the same tiles; which CTA holds which part of them may differ)
+    assert bool((out[:skip] == 7).all())
+    assert (out[skip:].double() - want.double()).abs().max() <= 2.0 ** -7 * want.double().abs().max()
+    assert q4k.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("qt", [F32, BF16])
+def test_heads_of_one_memory(q4k, form, qt):
+    """Cache heads that are one (a stride of 0, which TMA boxes do not take), a table row shared by two sequences."""
+    H, KH, D, page, lens, new = 8, 4, 128, 32, [100, 90], [40, 3]
+    if not _takes(form, qt, qt, D, page, 1.0, H // KH, 0.0):
+        pytest.skip("not a form of fp32 calls")
+    g = torch.Generator().manual_seed(47)
+    ((kc, ks, _), (vc, vs, _)), pt = _cache(g, lens[:1], page, 4, 1, D, E4M3)
+    pt = pt.expand(2, -1)
+    q = torch.randn(sum(new), H, D, generator=g).to(qt).cuda()
+    index = (_dev(_starts(new)), _dev(lens))
+    one = [t.expand(*t.shape[:2], KH, *t.shape[3:]) for t in (kc, vc, ks, vs)]
+    full = [t.contiguous() for t in one]
+    want = q4k.paged_attention8(q, *full, pt.contiguous().cuda(), *index, form=form)
+    got = q4k.paged_attention8(q, *one, pt.cuda(), *index, form=form)
+    assert torch.equal(got, want)
+    r = q4k.kv_read8(*one, pt.cuda(), *index, sum(new))
+    assert all(torch.equal(x, y) for x, y in zip(r, q4k.kv_read8(*full, pt.cuda(), *index, sum(new))))
+    assert q4k.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("form", FORMS)
 def test_old_contents_of_pages(q4k, form):
     """What earlier sequences left in a page's later slots, large scales among it, changes nothing."""
     g = torch.Generator().manual_seed(51)
