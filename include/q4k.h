@@ -628,10 +628,10 @@ q4k_status q4k_norm_rope(const q4k_norm_rope_args *a, void *stream);
  * q4k_kv_append into an 8-bit cache: keys normed (k_weight, NULL: not) and turned,
  * values as they come, both in fp32; queries, where given, normed (q_weight) and
  * turned into q_out.  With top = 127 or 448, a block that new tokens fall into gets
- *   scale = max(max|x| / top over its new tokens, its old scale where it holds older
+ *   scale = max(max|x| / top over its new tokens, its old |scale| where it holds older
  *           tokens of the sequence (positions before the first new one), 2^-126),
  *   code = x * (1 / scale) rounded to nearest even, at most top in size,
- * and where that scale has grown the older tokens' codes become code * (old scale / scale),
+ * and where that scale has changed the older tokens' codes become code * (old scale / scale),
  * rounded again (by at most half a step of the new scale).  Slots behind the first new
  * position count as empty: what an engine takes back is not asked.  Infinities do not
  * count for the scale and are stored as +-top; a NaN is stored as 0 (Q4K_I8) or NaN

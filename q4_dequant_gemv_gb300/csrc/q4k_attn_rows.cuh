@@ -41,12 +41,13 @@
 // join in three trips 94); sixteen fp32 tokens of 28 / 4 heads over 4096 26.4 us (58
 // without rings, 37 without clusters); one over 1000 7.4 us, five dependent trips to
 // memory; four times five tokens over 2000, scores capped, 15.4 us.
-// Over int8 codes: one token over 131072 66 us, 4.1 TB/s (272 MB; 8 warps 83, 12 70), of
+// Over int8 codes: one token over 131072 66 us, 4.1 TB/s (272 MB; 8 warps 83, 12 70, which
+// over 1000 take 8.1 and 8.6 where these take 9.2), of
 // which the join is 7: 525 instructions a block of 16 keys, a third of them conversions,
 // keep the issue slots 55 % and the ALU 50 % busy where a copy would take 40 us; sixteen
 // fp32 tokens over 4096 27 us, twice the instructions a byte in two parts and latency
-// (issue slots 40 %); one over 1000 12.0; four times five e4m3 16.7.  K's half of the loop
-// rolled up (fewer misses of the instruction cache): 28.2 and 66.9.
+// (issue slots 40 %); four times five e4m3 16.7.  K's half of the loop rolled up (fewer
+// misses of the instruction cache): 66.9 and 28.2.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -677,8 +678,8 @@ __global__ void __launch_bounds__(RowsShape<CT, NT, RG, DP>::kThreads, 1) rows_k
                     }
                 }
                 if constexpr (EIGHT) {
-                    if (__any_sync(0xffffffffu, vs[0] > limit || vs[1] > limit)) {   // a larger scale: O over the new power of two
-                        float most = fmaxf(vs[0], vs[1]);
+                    if (__any_sync(0xffffffffu, fabsf(vs[0]) > limit || fabsf(vs[1]) > limit)) {   // a larger scale: O over the new power of two
+                        float most = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
 #pragma unroll
                         for (int hop = 4; hop < 32; hop <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, hop));
                         const int to = min(static_cast<int>(__float_as_uint(most) >> 23) - 126, 122);   // most <= 2^to

@@ -83,6 +83,7 @@ __device__ __forceinline__ void widen_piece(const WidenArgs &w, int64_t to, int 
     float s = 0.0f, factor;   // s: of row lane % 16, over the factor; 0 where the codes stay
     if (a.block_shift >= 4) {
         factor = scales[(slot >> a.block_shift) * block];
+        if (factor < 0.0f) s = -1.0f, factor = -factor;   // (factors have no sign: the codes take it)
     } else {
         const int r = lane & 15;
         s = live >> r & 1 ? scales[((slot + r) >> a.block_shift) * block] : 0.0f;

@@ -674,7 +674,7 @@ __device__ __forceinline__ void append_run(const Args &a, float *s_max)
         const int64_t q = base + from;
         const bool in_first = mixed && (q >> a.shift) == (p0 >> a.shift);
         float s = fmaxf(most[k] / top, kLeastScale);
-        if (in_first) s = fmaxf(s, before);
+        if (in_first) s = fmaxf(s, fabsf(before));   // (a negative one: the older codes take its sign)
         const float inv = 1.0f / s;
         uint8_t *to = codes + page * c_page + sl * c_slot + head * c_head;
         if (good >> k & 1) {

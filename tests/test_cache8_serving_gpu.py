@@ -248,6 +248,61 @@ def test_heads_of_one_memory(q4k, form, qt):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("block", [4, 16, 64])
+def test_scales_of_both_signs(q4k, form, block):
+    """A cache filled by someone else may have negative scales, the largest among them."""
+    H, KH, D, page, lens, new = 4, 2, 128, 64, [300, 90], [40, 3]
+    for qt, ct in ((F32, I8), (BF16, E4M3), (F16, I8)):
+        if not _takes(form, qt, qt, D, page, 1.0, H // KH, 0.0):
+            continue
+        g = torch.Generator().manual_seed(53)
+        sides, pt = _cache(g, lens, page, block, KH, D, ct)
+        moved = []
+        for c, s, vals in sides:
+            sign = torch.where(torch.rand(s.shape, generator=g) < 0.5, -1.0, 1.0)
+            sign = torch.where(s.cpu() > s.cpu().nan_to_num().median(), sign * 16, sign) if s is sides[1][1] else sign
+            out = []
+            for b, n in enumerate(lens):
+                at = torch.arange(n)
+                out.append(vals[b] * sign[pt[b].long()[at // page], at % page // block].double()[..., None])
+            moved.append((c, s * sign.cuda(), out))
+        (kc, ks, keys), (vc, vs, vals) = moved
+        q = torch.randn(sum(new), H, D, generator=g).to(qt)
+        y = q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, pt.cuda(), _dev(_starts(new)), _dev(lens), form=form)
+        ref, _, bound, _ = _bound(q, keys, vals, dict(new=new, len=lens), 1 / math.sqrt(D), qt, qt != F32 and form in (None, "many"),
+                                  vs.abs(), vc)
+        assert ((y.double().cpu() - ref).abs() <= bound).all()
+    assert q4k.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("ct", [I8, E4M3])
+def test_append_to_a_negative_scale(q4k, ct):
+    """The older tokens of a block keep their values under the new, positive scale."""
+    past, n, KH, D, page, block = 5, 3, 2, 64, 16, 16
+    g = torch.Generator().manual_seed(57)
+    for old in (-0.5, -1e-4):
+        cache = plain8.Cache([past + n], past + n, page, block, KH, D, ct, seed=8)
+        for s in cache.scales:
+            s[:] = old
+        dev = cache.device()
+        v = torch.randn(n, KH, D, generator=g)
+        q4k.kv_append8(v.cuda(), v.cuda(), *dev[:4], dev[4], _dev([0, n]), _dev([past + n]))
+        after = copy.copy(cache)
+        after.codes, after.scales = [t.cpu() for t in dev[:2]], [t.cpu() for t in dev[2:4]]
+        for side in (0, 1):
+            got = after.scales[side][cache.table[0, 0].long(), 0].double()
+            want = torch.maximum(v.double().abs().amax((0, 2)) / plain8.TOP[ct], torch.tensor(-old).double())
+            assert ((got - want).abs() <= 2.0 ** -23 * want).all()
+            y = cache.values(side, 0, torch.arange(past)) / got[:, None]
+            near = plain8.half_step(y * (1 + 2.0 ** -20), ct) * (1 + 2.0 ** -20) + y.abs() * 2.0 ** -22
+            assert ((after.values(side, 0, torch.arange(past)) / got[:, None] - y).abs() <= near).all()
+            y = v.double() / got[:, None]
+            near = plain8.half_step(y * (1 + 2.0 ** -20), ct) * (1 + 2.0 ** -20) + y.abs() * 2.0 ** -22
+            assert ((after.values(side, 0, torch.arange(past, past + n)) / got[:, None] - y).abs() <= near).all()
+    assert q4k.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("form", FORMS)
 def test_old_contents_of_pages(q4k, form):
     """What earlier sequences left in a page's later slots, large scales among it, changes nothing."""
     g = torch.Generator().manual_seed(51)
