@@ -826,14 +826,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 int top = 0;
                 for (int i = 0; i < item.todo; i += 2) {
                     const bool mine = i + (lane >> 4) < item.todo;   // (the last may be alone)
+                    const int kb = (first + i + (lane >> 4)) * kChunkKeys + 16 * (lane & 7);
+                    // Only the pieces of the tile's keys count: those around them may hold any scale, and a tile that
+                    // sees nothing has its unit behind the sequence's last page.
+                    bool seen = mine && kb + 16 > t.from && kb < t.hi;
                     float f = 0.0f;
-                    if (mine)
+                    if (seen)
                         f = a.factors[((static_cast<int64_t>(t.seq) * a.table_pages + first + i + (lane >> 4)) * a.kv_heads + item.head) * 16 +
                                       (lane & 15)];
                     // a piece that is not in the cache: -inf.  Some row may see it, or none.
                     if (__any_sync(0xffffffffu, f == -INFINITY)) {
-                        const int kb = (first + i + (lane >> 4)) * kChunkKeys + 16 * (lane & 7);
-                        bool seen = mine && kb + 16 > t.from && kb < t.hi;
                         if (holes) {
                             for (int j = 0; j < min(2, item.todo - i); ++j) {
                                 uint32_t all[kChunkKeys / 32];
