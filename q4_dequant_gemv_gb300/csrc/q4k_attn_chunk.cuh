@@ -827,28 +827,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int i = 0; i < item.todo; i += 2) {
                     const bool mine = i + (lane >> 4) < item.todo;   // (the last may be alone)
                     const int kb = (first + i + (lane >> 4)) * kChunkKeys + 16 * (lane & 7);
-                    // Only the pieces of the tile's keys count: those around them may hold any scale, and a tile that
-                    // sees nothing has its unit behind the sequence's last page.
+                    // Only pieces that some row sees count: the others may hold any scale, and a tile that sees
+                    // nothing has its unit behind the sequence's last page.
                     bool seen = mine && kb + 16 > t.from && kb < t.hi;
+                    if (holes) {
+                        for (int j = 0; j < min(2, item.todo - i); ++j) {
+                            uint32_t all[kChunkKeys / 32];
+                            seen_keys(a, t, (first + i + j) * kChunkKeys, all);
+#pragma unroll
+                            for (int z = 0; z < kChunkKeys / 32; ++z)
+                                if ((lane >> 4) == j && (lane >> 1 & 3) == z) seen = (all[z] >> (16 * (lane & 1)) & 0xFFFFu) != 0;
+                        }
+                    }
                     float f = 0.0f;
                     if (seen)
                         f = a.factors[((static_cast<int64_t>(t.seq) * a.table_pages + first + i + (lane >> 4)) * a.kv_heads + item.head) * 16 +
                                       (lane & 15)];
-                    // a piece that is not in the cache: -inf.  Some row may see it, or none.
-                    if (__any_sync(0xffffffffu, f == -INFINITY)) {
-                        if (holes) {
-                            for (int j = 0; j < min(2, item.todo - i); ++j) {
-                                uint32_t all[kChunkKeys / 32];
-                                seen_keys(a, t, (first + i + j) * kChunkKeys, all);
-#pragma unroll
-                                for (int z = 0; z < kChunkKeys / 32; ++z)
-                                    if ((lane >> 4) == j && (lane >> 1 & 3) == z) seen = (all[z] >> (16 * (lane & 1)) & 0xFFFFu) != 0;
-                            }
-                        }
-                        if (f == -INFINITY) {
-                            if (seen) atomicOr(a.error, 4u);
-                            f = 0.0f;
-                        }
+                    if (f == -INFINITY) {   // a piece that is not in the cache
+                        atomicOr(a.error, 4u);
+                        f = 0.0f;
                     }
                     const int two = min(2, item.todo - i);
                     for (int z = 0; z < two && ok; ++z)

@@ -1,5 +1,5 @@
 """Attention over an 8-bit paged cache where much of the cache is seen by nobody: tiles that see nothing at all, scales
-of slots that no token sees.  All forms of the kernels."""
+of slots that no token sees, before its keys or between them.  All forms of the kernels."""
 import math
 
 import pytest
@@ -90,14 +90,27 @@ def _seen(case):
     return seen
 
 
+def _padded(n, length, seen, first=0):
+    """kv_start of n new tokens: the ranges `seen` of them see the keys from `first` on (the first range) or from their range's
+    own start on, the tokens between see nothing."""
+    out, past = [NOTHING] * n, length - n
+    for k, (a, b) in enumerate(seen):
+        for i in range(a, b):
+            out[i] = first if k == 0 else past + a
+    return out
+
+
 UNSEEN = {
     # keys that a sequence's every token starts behind: padding, what an engine has given up
     "padding": dict(new=[300, 3], len=[400, 90], kv_start=[40] * 300 + [70] * 3),
     "padding, no causal mask": dict(new=[20, 40], len=[300, 90], causal=False, kv_start=[150] * 20 + [33] * 40),
+    # between documents, after tokens that see nothing
+    "holes": dict(new=[200, 1, 64], len=[900, 20, 64],
+                  kv_start=_padded(200, 900, [(0, 1), (60, 61), (150, 200)], 400) + [0] + _padded(64, 64, [(0, 3), (50, 64)])),
+    "holes and a prefix": dict(new=[100], len=[400], prefix=[50], kv_start=_padded(100, 400, [(0, 1), (49, 50), (90, 100)])),
+    "late": dict(new=[150], len=[400], kv_start=[250 + i + (1 if i % 50 > 16 else -(i % 50)) for i in range(150)]),
 }
-
-
-CASES = ["padding", "padding, no causal mask"]
+CASES = list(UNSEEN)
 BLOCKS = [16, 64]
 
 
