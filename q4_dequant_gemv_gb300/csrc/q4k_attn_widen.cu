@@ -153,10 +153,38 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
         return;
     }
     // what the sequence's tokens may see: from its first token's window on
-    const int s0 = a.seq_start[b], n = a.seq_start[b + 1] - s0, raw_len = a.kv_len[b];
+    auto start_of = [&](int i) { return min(max(a.seq_start[i], 0), a.tokens); };
+    const int s0 = start_of(b), n = start_of(b + 1) - s0, raw_len = a.kv_len[b];
     if (n <= 0) return;
-    const int len = min(max(raw_len, 0), a.capacity), first = raw_len - n;
-    const int lo = a.window ? min(max(first + 1 - a.window, 0), len) : 0;
+    const int len = min(max(raw_len, 0), a.capacity), first = max(raw_len, -1) - n;
+    int lo = a.window ? min(max(first + 1 - a.window, 0), len) : 0;
+    // Blocks below 16: the scales of a piece meet over one power of two, so those that no token sees, which may be
+    // anything, have to stay out.  What is seen has no holes unless a token does not see its own position.
+    const bool starts = a.kv_start && a.block_shift < 4;
+    bool holes = false;
+    if (starts) {
+        __shared__ int s_lo, s_holes;
+        if (threadIdx.x == 0) s_lo = len, s_holes = 0;
+        __syncthreads();
+        int least = len;
+        for (int i = threadIdx.x; i < n; i += kWidenThreads) {
+            const Range r = token_range(a, b, first + i, s0 + i, len);
+            if (r.hi > r.lo) least = min(least, r.lo);
+            holes |= a.causal && r.lo > first + i;
+        }
+        atomicMin(&s_lo, least);
+        if (holes) s_holes = 1;
+        __syncthreads();
+        lo = s_lo, holes = s_holes != 0;
+    }
+    auto seen16 = [&](int key) {   // which of 16 keys some token sees, whole warps
+        uint32_t seen = 0;
+        for (int i = lane; i < n; i += 32) {
+            const Range r = token_range(a, b, first + i, s0 + i, len);
+            seen |= span(r.lo - key, r.hi - key);
+        }
+        return __reduce_or_sync(0xffffffffu, seen);
+    };
     // a warp per piece, head and side, neighbouring warps on neighbouring heads
     const int pg0 = lo / kPage, per_page = 16 * a.kv_heads;
     const int64_t tasks = len > pg0 * kPage ? static_cast<int64_t>((len + kPage - 1) / kPage - pg0) * per_page : 0;
@@ -164,7 +192,8 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
         const uint32_t x = static_cast<uint32_t>(quotient(i, a.kv_heads));   // (a position's fits 32 bits)
         const int head = static_cast<int>(i - static_cast<int64_t>(x) * a.kv_heads), side = x & 1, piece = x >> 1 & 7, pg = pg0 + (x >> 4);
         const int key = pg * kPage + 16 * piece;
-        const uint32_t live = span(lo - key, len - key) & 0xFFFFu;
+        uint32_t live = span(lo - key, len - key) & 0xFFFFu;
+        if (holes && live) live &= seen16(key);
         int page = -1, slot = 0;
         if (live) {
             int e;

@@ -111,7 +111,7 @@ UNSEEN = {
     "late": dict(new=[150], len=[400], kv_start=[250 + i + (1 if i % 50 > 16 else -(i % 50)) for i in range(150)]),
 }
 CASES = list(UNSEEN)
-BLOCKS = [16, 64]
+BLOCKS = [1, 4, 8, 16, 64]
 
 
 @pytest.mark.parametrize("form", FORMS)
