@@ -862,8 +862,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const int at = lane >> 4 ? top : top0, grown = lane >> 4 ? top - top0 : top0 - before;
                     UnitFactors &to = sh.factors[(unit + (lane >> 4)) % kUnitsAhead];
                     if (mine) {
-                        if (lane & 8) {   // (one of nothing counts as 2^-30 of the largest)
-                            const float x = fmaxf(log2f(fabsf(f)) - static_cast<float>(at), -30.0f);
+                        if (lane & 8) {   // (below 2^-38 of the largest P is 0 in fp16; the sums, in fp32, still count)
+                            const float x = fmaxf(log2f(fabsf(f)) - static_cast<float>(at), -60.0f);
                             to.value[lane & 7] = x, to.undo[lane & 7] = ex2(-x);
                         } else {
                             to.key[lane & 7] = f;

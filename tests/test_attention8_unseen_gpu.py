@@ -149,3 +149,29 @@ def test_scales_that_nobody_sees(q4k, name, block, qt, ct, form):   # noqa: F811
             want = out, lse
             _check(out, lse, q, keys, vals, vs, vc, case, form, page)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), f"scales of {fill}: {float((out - want[0]).abs().max())} off"
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("qt,ct", [(BF16, I8), (F16, E4M3), (F32, I8)])
+@pytest.mark.parametrize("ratio", [0.0, 2.0 ** -45, 2.0 ** -33, 2.0 ** -25])
+def test_small_values_beside_large_ones(q4k, ratio, qt, ct, form):   # noqa: F811
+    """Rows that see only values whose scale is a small part, or none, of one beside them: at most their own size.  (A weight
+    times a scale may be lost in fp16 or rounded up to its smallest number, at most to twice itself.)"""
+    case, H, KH, D, page, block = dict(new=[40], len=[200], window=16), 4, 2, 64, 64, 16
+    if not _takes(form, qt, qt, D, page, 1.0, 2, 0.0):
+        return
+    g = torch.Generator().manual_seed(12)
+    ((kc, ks, keys), (vc, _, vals)), pt = _cache(g, case["len"], page, block, KH, D, ct)
+    s = torch.where(torch.arange(200) < 192, ratio * 4.0, 4.0)
+    vs = torch.full_like(ks, math.nan)
+    at = torch.arange(0, 200, block)
+    vs[pt[0].long()[at // page].cuda(), (at % page // block).cuda()] = s[at].cuda()[:, None]
+    codes = vc.float().cpu()[pt[0].long()].flatten(0, 1)[:200]
+    vals = [codes.double() * s.double()[:, None, None]]
+    q = torch.randn(40, H, D, generator=g).to(qt)
+    lse = torch.zeros(40, H, device="cuda")
+    out = q4k.paged_attention8(q.cuda(), kc, vc, ks, vs, pt.cuda(), _starts([40]), _dev([200]), window=16, lse=lse, form=form).double().cpu()
+    assert q4k.device_error_flags() == 0
+    _check(out.to(qt).cuda(), lse, q, keys, vals, vs, vc, case, form, page)
+    mag, _, _ = plain.attention(q, keys, [v.abs() for v in vals], case, 0.125, 0.0, None, qt == F32, F16, qt)
+    assert (out.abs() <= 2 * (1 + 2.0 ** -6) * mag)[:32].all()   # (2^-8 of it the output's rounding)
