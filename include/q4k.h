@@ -680,13 +680,15 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
  * The many-rows form (prompt chunks; fp16 or bf16 q and out, dim up to 128, pages of a
  * multiple of 16 slots) turns the codes into fp16 scratch first.  With blocks of 16 tokens
  * or more they stay exact; with smaller ones scale * code, over a power of two for each 16
- * tokens, is rounded once to fp16 (2^-11).  It takes 4 * dim bytes of stream-ordered scratch
+ * tokens, is rounded once to fp16 (2^-11, or 2^-31 of the largest scale of those of the 16
+ * that the sequence's tokens see).  It takes 4 * dim bytes of stream-ordered scratch
  * a table position of each sequence and cache head, up to 4 GiB; past that heads, then
  * sequences go through in passes, and where one head of one sequence has no room the call
  * takes another form (asked for by name it is refused).  (Where the device has less to
  * give the passes get smaller.)
  * Slots that no token of a sequence's query tile sees may hold anything, their scales
- * too.  A block whose scale a token sees must have one that is finite.
+ * too.  A block whose scale a token sees must have one that is finite: NaN makes the
+ * token's rows NaN, and may those of nearby tokens.
  *   dim a multiple of 16 up to 256; k and v 16-byte aligned, with strides that keep
  *   every row 16-byte aligned; everything else as q4k_paged_attention.
  */

@@ -860,10 +860,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const int before = i == 0 ? e0 : top, top0 = max(before, e0);
                     top = max(top0, e1);
                     const int at = lane >> 4 ? top : top0, grown = lane >> 4 ? top - top0 : top0 - before;
+                    const float keys = __shfl_xor_sync(0xffffffffu, f, 8);   // (to values: their keys')
                     UnitFactors &to = sh.factors[(unit + (lane >> 4)) % kUnitsAhead];
                     if (mine) {
                         if (lane & 8) {   // (below 2^-38 of the largest P is 0 in fp16; the sums, in fp32, still count)
-                            const float x = fmaxf(log2f(fabsf(f)) - static_cast<float>(at), -60.0f);
+                            float x = log2f(fabsf(f)) - static_cast<float>(at);
+                            if (x < -60.0f) x = -60.0f;
+                            if (keys != keys) x = keys;   // (a NaN among the factors of what is seen shows)
                             to.value[lane & 7] = x, to.undo[lane & 7] = ex2(-x);
                         } else {
                             to.key[lane & 7] = f;

@@ -175,3 +175,30 @@ def test_small_values_beside_large_ones(q4k, ratio, qt, ct, form):   # noqa: F81
     _check(out.to(qt).cuda(), lse, q, keys, vals, vs, vc, case, form, page)
     mag, _, _ = plain.attention(q, keys, [v.abs() for v in vals], case, 0.125, 0.0, None, qt == F32, F16, qt)
     assert (out.abs() <= 2 * (1 + 2.0 ** -6) * mag)[:32].all()   # (2^-8 of it the output's rounding)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("qt,ct,block", [(BF16, I8, 16), (F16, E4M3, 64), (BF16, E4M3, 4), (F32, I8, 16)])
+@pytest.mark.parametrize("side", [0, 1])
+def test_nan_scales_that_are_seen(q4k, side, qt, ct, block, form):   # noqa: F811
+    """A scale of NaN that a row sees makes that row NaN; tokens far from those that see it do not change."""
+    n, length, H, KH, D, page = 600, 700, 4, 2, 64, 64
+    if not _takes(form, qt, qt, D, page, 1.0, 2, 0.0):
+        return
+    g = torch.Generator().manual_seed(23)
+    ((kc, ks, _), (vc, vs, _)), pt = _cache(g, [length], page, block, KH, D, ct)
+    q = torch.randn(n, H, D, generator=g).to(qt).cuda()
+    args = (pt.cuda(), _starts([n]), _dev([length]))
+    want = q4k.paged_attention8(q, kc, vc, ks, vs, *args, window=40, form=form)
+    p = 448   # the block that holds this position, of cache head 1
+    (vs if side else ks)[int(pt[0, p // page]), p % page // block, 1] = math.nan
+    lse = torch.zeros(n, H, device="cuda")
+    out = q4k.paged_attention8(q, kc, vc, ks, vs, *args, window=40, lse=lse, form=form)
+    torch.cuda.synchronize()
+    assert q4k.device_error_flags() == 0
+    rows = torch.arange(n) + length - n
+    sees = (rows >= p) & (rows - 39 < p // block * block + block)
+    assert torch.isnan(out[sees.cuda()][:, 2:]).all()
+    assert side or torch.isnan(lse[sees.cuda()][:, 2:]).all()
+    far = ((rows < p - 256) | (rows >= p + block + 40 + 256)).cuda()
+    assert int(far.sum()) > 20 and torch.equal(out[far], want[far]) and torch.equal(out[:, :2], want[:, :2])
