@@ -685,7 +685,9 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
  * a table position of each sequence and cache head, up to 4 GiB; past that heads, then
  * sequences go through in passes, and where one head of one sequence has no room the call
  * takes another form (asked for by name it is refused).  (Where the device has less to
- * give the passes get smaller.)
+ * give the passes get smaller.)  bf16 queries come on top: 2 * dim + 4 bytes a token and
+ * query head of a pass.  That scratch is a call's in flight and the page table's width
+ * sets it, not the lengths; its memory stays with the library as q4k_scratch_keep says.
  * Slots that no token of a sequence's query tile sees may hold anything, their scales
  * too.  A block whose scale a token sees must have one that is finite: NaN makes the
  * token's rows NaN, and may those of nearby tokens.
@@ -693,6 +695,15 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
  *   every row 16-byte aligned; everything else as q4k_paged_attention.
  */
 q4k_status q4k_paged_attention8(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream);
+
+/*
+ * How much free memory the current device's pool of that scratch may hold when the program
+ * synchronises (a stream, an event or the device); the rest goes back to the system.  It
+ * has a pool of its own beside q4k_paged_attention's, with 5 GiB to begin with.  0: all of
+ * it goes back each time, and the first call after that waits for it (0.7 ms a GiB).  A
+ * captured call's scratch belongs to its graph.  bytes >= 0, else INVALID_ARG.
+ */
+q4k_status q4k_scratch_keep(int64_t bytes);
 
 /* Launch plan the automatic heuristics pick for a shape (for tests and
  * reports): out[0] = split_k, out[1] = number of CTAs, out[2] = rows per CTA

@@ -50,7 +50,8 @@ EXPORTS = ("q4k_status_string", "q4k_abi_version", "q4k_gemv", "q4k_gemv_argmax"
            "q4k_device_error_flags", "q4k_device_error_clear", "q4k_stream_read", "q6k_gemv",
            "q6k_planar_bytes", "q6k_repack_planar", "q6k_gemv_planar",
            "q4k_rope_table", "q4k_rope", "q4k_kv_append", "q4k_paged_attention",
-           "q4k_norm_rope", "q4k_kv_append8", "q4k_kv_read8", "q4k_paged_attention8")
+           "q4k_norm_rope", "q4k_kv_append8", "q4k_kv_read8", "q4k_paged_attention8",
+           "q4k_scratch_keep")
 
 
 def lib():
@@ -92,6 +93,8 @@ def lib():
         L.q4k_gemm_prefill.restype = I
         L.q4k_gemv_plan.argtypes = [I64, I64, I, ctypes.POINTER(ctypes.c_int * 4)]
         L.q4k_gemv_plan.restype = I
+        L.q4k_scratch_keep.argtypes = [I64]
+        L.q4k_scratch_keep.restype = I
         L.q4k_device_error_flags.restype = ctypes.c_uint
         L.q4k_device_error_clear.restype = I
         L.q4k_stream_read.argtypes = [P, I64, ctypes.POINTER(ctypes.c_int64), P]
@@ -343,6 +346,14 @@ def __getattr__(name):
         globals()[name] = f = getattr(_cache8, name)
         return f
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def scratch_keep(nbytes: int) -> None:
+    """How much of the scratch of prompt chunks over 8-bit caches (as wide as their page tables, up to 4 GiB a call) the library
+    may keep on the current device when the program synchronises; 5 GiB unless it is told otherwise."""
+    if not 0 <= nbytes < 2 ** 63:
+        raise ValueError(f"nbytes must be a size in bytes, got {nbytes}")
+    _check("q4k_scratch_keep", lib().q4k_scratch_keep(nbytes))
 
 
 def device_error_flags() -> int:

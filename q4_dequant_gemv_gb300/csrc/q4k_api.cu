@@ -124,6 +124,8 @@ q4k_status q4k_kv_read8(const q4k_paged_cache8 *c, const q4k_read8_args *a, void
     return q4k::kv_read8_impl(c, a, stream);
 }
 
+q4k_status q4k_scratch_keep(int64_t bytes) { return q4k::scratch_keep_impl(bytes); }
+
 q4k_status q4k_gemv_plan(int64_t N, int64_t K, int batch, int out[4])
 {
     return q4k::gemv_plan_impl(N, K, batch, out);

@@ -50,14 +50,15 @@ struct BesideCaptures {
     ~BesideCaptures() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
 };
 
-// Scratch comes from a pool of the library's own, one per device, that keeps its
-// memory: the default pool gives it back to the system whenever the program
-// synchronises, and the next call then waits 250 us for it.
-cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream)
+// Scratch comes from pools of the library's own that keep their memory: the default pool
+// gives it back to the system whenever the program synchronises, and the next call then
+// waits 250 us for it.  Two per device: partial results, some tens of MB, stay for good;
+// widened caches, as wide as page tables are, up to kWidenKept or what the caller says.
+static cudaError_t pool_of(int dev, bool widened, cudaMemPool_t *pool)
 {
-    static cudaMemPool_t pools[kDevices];
-    static OncePerDevice once;
-    const cudaError_t e = once(dev, [&] {
+    static cudaMemPool_t pools[2][kDevices];
+    static OncePerDevice once[2];
+    const cudaError_t e = once[widened](dev, [&] {
         const BesideCaptures beside;   // (a first call may be a captured one)
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
@@ -66,13 +67,21 @@ cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream)
         cudaMemPool_t made = nullptr;
         cudaError_t bad = cudaMemPoolCreate(&made, &props);
         if (bad != cudaSuccess) return bad;
-        cuuint64_t keep = UINT64_MAX;
+        cuuint64_t keep = widened ? static_cast<cuuint64_t>(kWidenKept) : UINT64_MAX;
         bad = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
         if (bad != cudaSuccess) (void)cudaMemPoolDestroy(made);
-        else pools[dev] = made;
+        else pools[widened][dev] = made;
         return bad;
     });
-    return e == cudaSuccess ? cudaMallocFromPoolAsync(p, bytes, pools[dev], stream) : e;
+    *pool = pools[widened][dev];
+    return e;
+}
+
+cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream, bool widened)
+{
+    cudaMemPool_t pool;
+    const cudaError_t e = pool_of(dev, widened, &pool);
+    return e == cudaSuccess ? cudaMallocFromPoolAsync(p, bytes, pool, stream) : e;
 }
 
 // Clusters of each size that a device holds at once.
@@ -379,6 +388,18 @@ static q4k_status attention_over(const q4k_paged_cache *c, const q4k_paged_cache
         e = rows(l);
     }
     return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
+}
+
+q4k_status scratch_keep_impl(int64_t bytes)
+{
+    if (bytes < 0) return Q4K_ERR_INVALID_ARG;
+    const q4k_status st = check_device(nullptr);
+    if (st != Q4K_OK) return st;
+    int dev = 0;
+    cudaMemPool_t pool;
+    if (cudaGetDevice(&dev) != cudaSuccess || attn::pool_of(dev, true, &pool) != cudaSuccess) return Q4K_ERR_CUDA;
+    cuuint64_t keep = static_cast<cuuint64_t>(bytes);
+    return cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA;
 }
 
 q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_args *a, void *stream)

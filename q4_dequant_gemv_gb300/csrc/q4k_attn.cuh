@@ -458,7 +458,7 @@ struct OncePerDevice {
 // tiles that it left split; R rows and `width` columns a slot.
 constexpr int kJoinThreads = 256, kJoinRows = 32;   // of a CTA of the join at most
 constexpr int kMaxParts = 184;   // CTAs of a split call at most (the join's statistics: 47 KB)
-cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream);   // freed with cudaFreeAsync
+cudaError_t take_scratch(int dev, void **p, size_t bytes, cudaStream_t stream, bool widened = false);   // freed with cudaFreeAsync
 cudaError_t launch_join(const Args &a, int grid, int R, int width, float shift, cudaStream_t stream);
 
 template <class Launch>

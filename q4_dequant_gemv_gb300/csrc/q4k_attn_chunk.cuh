@@ -907,6 +907,11 @@ cudaError_t launch_chunk_wide(const ChunkLaunch &l);   // (a widened 8-bit cache
 // 128, take 328 us in one pass, in 2 (a table of 65536 positions) 377, in 4 421; with 1 GiB
 // they took 375 to 618, and the mma.sync kernel takes 2316.
 constexpr int64_t kWidenMost = int64_t{4} << 30;
+// What the library holds of it from call to call unless it is told otherwise: one such call's
+// and its queries.  What is past that goes back to the system when the program synchronises,
+// which costs 1.2 ms a GiB, and the next call 0.7 to take it again: with 1 GiB the above, its
+// table of 32768, takes 2.8 ms between two synchronisations instead of 0.37.
+constexpr int64_t kWidenKept = int64_t{5} << 30;
 int64_t widened_bytes(const Args &a);   // of one cache head of one sequence
 cudaError_t launch_widened(const ChunkLaunch &l);
 

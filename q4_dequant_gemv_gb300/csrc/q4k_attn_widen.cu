@@ -235,7 +235,7 @@ cudaError_t launch_widened(const ChunkLaunch &l)
         side = room(pages * heads * kPage * all.dim * 2), fac = room(pages * heads * 64);
         const int64_t rows = static_cast<int64_t>(all.tokens) * heads * all.group;
         q = turn ? room(rows * all.dim * 2) : 0, scale = turn ? room(rows * 4) : 0;
-        e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream);
+        e = take_scratch(l.device, &scratch, 2 * side + fac + q + scale, l.stream, true);
         if (e != cudaErrorMemoryAllocation || 2 * side <= kWidenLeast || static_cast<int64_t>(heads) * seqs == 1) break;
         (void)cudaGetLastError();
         fit = std::max<int64_t>(1, static_cast<int64_t>(heads) * seqs / 2);

@@ -35,6 +35,7 @@ q4k_status paged_attention_impl(const q4k_paged_cache *c, const q4k_attention_ar
 q4k_status norm_rope_impl(const q4k_norm_rope_args *a, void *stream);
 q4k_status kv_append8_impl(const q4k_paged_cache8 *c, const q4k_append8_args *a, void *stream);
 q4k_status paged_attention8_impl(const q4k_paged_cache8 *c, const q4k_attention_args *a, void *stream);
+q4k_status scratch_keep_impl(int64_t bytes);
 q4k_status kv_read8_impl(const q4k_paged_cache8 *c, const q4k_read8_args *a, void *stream);
 // Sizes, types and index pointers of a cache (no device call).
 q4k_status check_cache(const q4k_paged_cache *c);
