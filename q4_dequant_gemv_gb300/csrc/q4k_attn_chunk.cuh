@@ -913,6 +913,7 @@ constexpr int64_t kWidenMost = int64_t{4} << 30;
 // table of 32768, takes 2.8 ms between two synchronisations instead of 0.37.
 constexpr int64_t kWidenKept = int64_t{5} << 30;
 int64_t widened_bytes(const Args &a);   // of one cache head of one sequence
+double widened_us(const Args &a, int64_t keys);
 cudaError_t launch_widened(const ChunkLaunch &l);
 
 }  // namespace attn

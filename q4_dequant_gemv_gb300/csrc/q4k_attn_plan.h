@@ -24,8 +24,15 @@
 // 1000 positions takes 7.1 us with a table of 1000, 11.2 (split, the cluster form
 // still 7.1) with one of 16384 or more; sixteen over 4096 28.2 and, in a table of
 // 32768, 36.1 (clusters 27.9).  Such a caller can ask for the form.
-// 8-bit caches take the same estimate: over 14 calls of theirs (1 to 64 sequences of 1 to
-// 128 tokens, 500 to 131072 positions) its choice was the fastest form or within 13 % of it.
+// 8-bit caches take the same estimate, with their widening added to the many-rows form
+// (`widened_us`).  Over 216 bf16 calls of theirs (1 to 64 sequences of 2 to 128 tokens, 32/8
+// and 28/4 heads of 128, 500 to 32000 positions, tables just wide enough, int8 in blocks of 16
+// and e4m3 of 1) its choice is within 1.4 % of the fastest form on the geometric mean, 1.29x at
+// worst (without that term 6.5 % and 2.1x); over 56 in tables eight times as wide 8 % and 1.9x
+// (21 % and 2.1x).  Both sides, in us:
+//   64 sequences of 4 tokens over 500, 28/4 heads: clusters of tiles of 32 rows 38, many-rows 82;
+//   4 of 8 over 8000, 32/8: 50 and 80; 4 of 32 over 8000, 28/4: 146 and 59.
+// (Their tiles of 8 rows have units of twice the keys that is counted here.)
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -88,7 +95,7 @@ inline Choice choose(const Args &a, const int (&room)[kMaxCluster + 1], int sms,
     }
     if (may_chunk && (!form || form == Q4K_ATTN_MANY)) {
         const int64_t tiles = int64_t{a.kv_heads} * a.batch * up(a.tokens, int64_t{kChunkRows / a.group} * a.batch);
-        const double us = kChunkCall + join(tiles, keys / kChunkKeys + 1) +
+        const double us = kChunkCall + (a.ks ? widened_us(a, keys) : 0.0) + join(tiles, keys / kChunkKeys + 1) +
                           static_cast<double>(tiles) / sms * (a.dim <= 64 ? 0.8 : 1.0) *
                               (kChunkTile + kChunkUnit * static_cast<double>(keys / kChunkKeys + 1));
         if (us < least) best = {true, 0, 0};

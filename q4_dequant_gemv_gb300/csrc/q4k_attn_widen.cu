@@ -212,25 +212,47 @@ int64_t widened_bytes(const Args &a)
     return (a.capacity + static_cast<int64_t>(kPage) - 1) / kPage * (2 * kPage * 2 * static_cast<int64_t>(a.dim) + 64);
 }
 
-// As many cache heads of all sequences a pass as kWidenMost bytes hold, or of one head as many sequences; fewer
-// where the device has no room for that.
+// Cache heads and sequences of a pass that holds `fit` heads of one sequence: heads of all sequences, or one head of
+// as many as fit.  Passes of about the same size.
+struct Pass {
+    int heads, seqs;
+};
+static Pass pass_of(const Args &a, int64_t fit)
+{
+    auto alike = [](int n, int64_t most) {
+        const int passes = static_cast<int>((n + most - 1) / most);
+        return (n + passes - 1) / passes;
+    };
+    return {alike(a.kv_heads, std::max<int64_t>(1, fit / a.batch)), alike(a.batch, std::min<int64_t>({fit, a.batch, 65534}))};   // (a grid's y)
+}
+
+static int64_t fitting(const Args &a) { return std::max<int64_t>(1, kWidenMost / widened_bytes(a)); }
+
+// What widening adds to a call that sees `keys` positions a sequence, about, in us: a launch, bytes (three a code, four an
+// element of queries that are turned) and the start and end of each further pass.  Fitted with the estimate of the forms.
+double widened_us(const Args &a, int64_t keys)
+{
+    const double codes = 2.0 * static_cast<double>(keys) * a.batch * a.kv_heads * a.dim;
+    const double q = a.q_type == Q4K_F16 ? 0.0 : static_cast<double>(a.tokens) * a.heads * a.dim;
+    const Pass p = pass_of(a, fitting(a));
+    const double passes = static_cast<double>((a.kv_heads + p.heads - 1) / p.heads) * ((a.batch + p.seqs - 1) / p.seqs);
+    return 6.0 + (3.0 * codes + 4.0 * q) / 7e6 + 45.0 * (passes - 1.0);
+}
+
+// In passes of what kWidenMost bytes hold; of less where the device has no room for that.
 cudaError_t launch_widened(const ChunkLaunch &l)
 {
     const Args &all = l.args;
     const int table_pages = (all.capacity + kPage - 1) / kPage;
     const bool turn = all.q_type != Q4K_F16;
     auto room = [](int64_t n) { return (n + 255) / 256 * 256; };
-    auto alike = [](int n, int64_t most) {   // passes of about as many
-        const int passes = static_cast<int>((n + most - 1) / most);
-        return (n + passes - 1) / passes;
-    };
     int heads, seqs;
     int64_t pages, side, fac, q, scale;
     void *scratch = nullptr;
     cudaError_t e;
-    for (int64_t fit = std::max<int64_t>(1, kWidenMost / widened_bytes(all));;) {
-        heads = alike(all.kv_heads, std::max<int64_t>(1, fit / all.batch));
-        seqs = alike(all.batch, std::min<int64_t>({fit, all.batch, 65534}));   // (a grid's y)
+    for (int64_t fit = fitting(all);;) {
+        const Pass p = pass_of(all, fit);
+        heads = p.heads, seqs = p.seqs;
         pages = static_cast<int64_t>(seqs) * table_pages;
         side = room(pages * heads * kPage * all.dim * 2), fac = room(pages * heads * 64);
         const int64_t rows = static_cast<int64_t>(all.tokens) * heads * all.group;
