@@ -69,7 +69,8 @@ __device__ __forceinline__ void widen_piece(const WidenArgs &w, int64_t to, int 
     const int lane = threadIdx.x & 31;
     const float *scales = side ? a.vs + page * a.vs_page + head * a.vs_head : a.ks + page * a.ks_page + head * a.ks_head;
     const int64_t block = side ? a.vs_block : a.ks_block, slots = side ? a.v_slot : a.k_slot;
-    // the codes first: rows of CPR chunks
+    // the codes first: rows of CPR chunks (plain loads: as a programmatic dependent this kernel starts while the append
+    // before it still writes them)
     const int cpr = a.dim > 64 ? 8 : 4, rps = 32 / cpr, ch = lane & (cpr - 1), row0 = lane / cpr;
     const uint8_t *from = static_cast<const uint8_t *>(side ? a.v : a.k) + page * (side ? a.v_page : a.k_page) +
                           head * (side ? a.v_head : a.k_head) + (slot + row0) * slots + 16 * ch;
@@ -78,7 +79,7 @@ __device__ __forceinline__ void widen_piece(const WidenArgs &w, int64_t to, int 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         raw[j] = make_uint4(0, 0, 0, 0);
-        if (inside && rps * j < 16 && (live >> (row0 + rps * j) & 1)) raw[j] = __ldg(reinterpret_cast<const uint4 *>(from + j * rps * slots));
+        if (inside && rps * j < 16 && (live >> (row0 + rps * j) & 1)) raw[j] = *reinterpret_cast<const uint4 *>(from + j * rps * slots);
     }
     float s = 0.0f, factor;   // s: of row lane % 16, over the factor; 0 where the codes stay
     if (a.block_shift >= 4) {
