@@ -843,9 +843,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (seen)
                         f = a.factors[((static_cast<int64_t>(t.seq) * a.table_pages + first + i + (lane >> 4)) * a.kv_heads + item.head) * 16 +
                                       (lane & 15)];
-                    if (f == -INFINITY) {   // a piece that is not in the cache
-                        atomicOr(a.error, 4u);
-                        f = 0.0f;
+                    if (__any_sync(0xffffffffu, f == -INFINITY)) {   // a piece that is not in the cache (whole warps: 1 % of the call)
+                        if (f == -INFINITY) {
+                            atomicOr(a.error, 4u);
+                            f = 0.0f;
+                        }
                     }
                     const int two = min(2, item.todo - i);
                     for (int z = 0; z < two && ok; ++z)
