@@ -637,7 +637,8 @@ q4k_status q4k_norm_rope(const q4k_norm_rope_args *a, void *stream);
  * count for the scale and are stored as +-top; a NaN is stored as 0 (Q4K_I8) or NaN
  * (Q4K_E4M3).  Only the new tokens' slots, the older ones of their blocks and those
  * blocks' scales are written; a block that new tokens fall into belongs to one sequence
- * of the call.  dim a multiple of 8 up to 256; everything else as q4k_kv_append.
+ * of the call.  dim a multiple of 8 up to 256; no stride of the cache or its scales is 0
+ * along an axis of more than one (INVALID_ARG); everything else as q4k_kv_append.
  */
 typedef struct {
     q4k_append_args a;

@@ -937,6 +937,14 @@ q4k_status kv_append8_impl(const q4k_paged_cache8 *c8, const q4k_append8_args *a
         return Q4K_ERR_INVALID_ARG;
     if (a->q && (a->q_heads < 1 || a->q_heads > 65536 || !good_type(a->q_type) || !good_type(a->q_out_type))) return Q4K_ERR_INVALID_ARG;
     if (some && (!a->k || !a->v || (a->rot && !a->table))) return Q4K_ERR_INVALID_ARG;
+    // slots or scales that are one and the same would take what was written last
+    auto same = [](int64_t stride, int64_t n) { return n > 1 && stride == 0; };
+    const int64_t blocks = c->page_size / used.block;
+    if (same(c->k_page_stride, c->pages) || same(c->k_slot_stride, c->page_size) || same(c->k_head_stride, c->heads) ||
+        same(c->v_page_stride, c->pages) || same(c->v_slot_stride, c->page_size) || same(c->v_head_stride, c->heads) ||
+        same(used.k_scale_page_stride, c->pages) || same(used.k_scale_block_stride, blocks) || same(used.k_scale_head_stride, c->heads) ||
+        same(used.v_scale_page_stride, c->pages) || same(used.v_scale_block_stride, blocks) || same(used.v_scale_head_stride, c->heads))
+        return Q4K_ERR_INVALID_ARG;
     if (st != Q4K_OK) return st;
     if (off(a->k, size_of(a->kv_type)) || off(a->v, size_of(a->kv_type)) || off(a->pos, 4) || off(a->table, 4) ||
         off(a8->q_weight, 4) || off(a8->k_weight, 4) ||
