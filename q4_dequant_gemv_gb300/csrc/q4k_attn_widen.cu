@@ -15,10 +15,15 @@
 // that is not in the cache has factors of -inf; the kernel knows whether a row sees it.
 // bf16 queries become fp16 over a power of two a row here too.
 //
-// Bound by memory: 3 bytes a code and 4 an element of the queries.  Three chunks of 512 over
-// 4096, 32 / 8 heads of 128 (28 M codes, 110 MB): 15.7 us of the call's 111 (the kernel 79,
-// its join 21, each by itself), 2048 over 14336 (34 M codes, 134 MB) 26 of 395 (345, 20); with
-// the conversion inside the kernel they took 142 and 537, the mma.sync kernel takes 753 for
+// What no token sees may hold any scale: it is not read where a window or (blocks below 16,
+// whose scales share a power of two) kv_start leaves it out, else the attention kernel's
+// factor warp lets it count as 0.
+//
+// 3 bytes a code and 4 an element of the queries.  Three chunks of 512 (1327 tokens) over up
+// to 4608, 28 / 4 heads of 128 (12.4 M codes, 56 MB): 16 us of the call's 110 (the kernel 79,
+// its join 22, each by itself), 3.5 TB/s: latency and issue slots (49 %), DRAM is at 17 %;
+// 2048 over 14336, 32 / 8 heads (34 M codes, 134 MB) 27 of 395 (347, 20), 5 TB/s; with the
+// conversion inside the kernel they took 142 and 537, the mma.sync kernel takes 753 for
 // the first.
 #include <cuda_runtime.h>
 
