@@ -43,7 +43,8 @@ def kv_append8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, 
                pdl: bool = False):
     """kv_append into an 8-bit cache: keys normed (k_weight) and turned, values as they are, quantised with a scale for each
     block and head.  A block that already holds older tokens of its sequence keeps its scale, or takes a larger one and
-    has the older codes rounded again.  Queries, where given, are normed (q_weight) and turned into q_out."""
+    has the older codes rounded again.  Queries, where given, are normed (q_weight) and turned into q_out.  Caches or scales
+    that repeat themselves (a stride of 0) are refused."""
     return (_calls or _load()).kv_append8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, table,
                                           interleaved, pos, q, q_out, q_dtype, q_weight, k_weight, eps, stream, pdl)
 
@@ -63,7 +64,8 @@ def paged_attention8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_star
                      out_dtype=None, softcap: float = 0.0, slopes=None, window: int = 0, causal: bool = True, prefix_len=None,
                      kv_start=None, lse=None, stream=None, pdl: bool = False, wait_limit_us: int = 0, test_stall: bool = False,
                      form=None):
-    """paged_attention over an 8-bit cache (all options as there; dim a multiple of 16)."""
+    """paged_attention over an 8-bit cache (all options as there; dim a multiple of 16).  Prompt chunks take scratch as wide as
+    the page table (scratch_keep says how much of it stays)."""
     if form not in _attention._FORMS:
         raise ValueError(f"form must be one of {list(_attention._FORMS)}")
     return (_calls or _load()).paged_attention8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_start, kv_len, out, scale,
